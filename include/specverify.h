@@ -66,6 +66,8 @@ extern "C" {
                                      SPEC_STATIC_SCRATCH_BYTES of scratch */
 #define SPEC_ERR_HINT (-6)        /* spec_verify_khint_*: k_min < 0, k_max > 255, k_min > k_max,
                                      a NaN threshold or h_lo > h_hi */
+#define SPEC_ERR_OVERLAP (-7)     /* spec_process_logits_*: out_logits overlaps logits without being it;
+                                     spec_kv_commit: out_lengths overlaps lengths */
 
 /* Size of the fixed per-device scratch buffer of spec_verify_bf16_static_scratch. */
 #define SPEC_STATIC_SCRATCH_BYTES ((size_t)8 << 20)
@@ -409,6 +411,173 @@ int spec_acceptance_stats(const int32_t *n_accepted, int B, int K, uint64_t *out
 int spec_ngram_draft(const int32_t *tokens, const int32_t *lengths, int B, int stride, int n_min,
                      int n_max, int K, int32_t *out_drafts, int32_t *out_n_drafts,
                      int32_t *out_match_len, cudaStream_t stream);
+
+/*
+ * Token counts, the state behind the penalties of spec_process_logits_*.
+ *
+ * The state is an int32 device array [B, words], words =
+ * spec_token_state_words(V), that the caller owns and zeroes (all zeros: no
+ * tokens yet).  Row b holds, with P = V rounded up to a multiple of 32:
+ *   words 0 .. P - 1          token v: bits 0..30 its occurrences among the
+ *                             output tokens, bit 31 set when it is in the prompt
+ *   words P .. P + P / 32 - 1 bit v % 32 of word P + v / 32: word v is not zero
+ * (then padding to a multiple of 4 words).  A row's memory can be passed as a
+ * state of its own (B = 1), so that one sequence of a batch is replaced.
+ * spec_token_state_words returns the words of a row, or SPEC_ERR_SHAPE for V
+ * outside [1, 2^30].
+ */
+int spec_token_state_words(int V);
+
+/*
+ * Adds tokens to the counts.
+ *   tokens         [B, stride] int32: row b's first lengths[b] entries are counted.
+ *   lengths        [B] int32 or NULL (all `stride` entries of every row).
+ *   prompt_lengths [B] int32 or NULL (0): the first prompt_lengths[b] entries
+ *                  are of the prompt, the rest are output tokens.
+ *   V              vocabulary, 1 <= V <= 2^30.  Tokens outside [0, V) count for
+ *                  nothing, so that a verify's out_tokens [B, K+1] or out_path
+ *                  [B, N+1] with its -1 padding can be passed as it is (stride
+ *                  K + 1 or N + 1, lengths and prompt_lengths NULL).
+ *   reset          not 0: the rows are zeroed first.
+ * Bad data: a length outside [0, stride] or a prompt length outside [0,
+ * length] adds nothing to that row and sets SPEC_FLAG_BAD_DATA.  Counts are
+ * exact.  Returns SPEC_OK, SPEC_ERR_NULL, SPEC_ERR_SHAPE (B < 0, stride < 0, V)
+ * or SPEC_ERR_CUDA.  Asynchronous on `stream`; no scratch.
+ */
+int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32_t *prompt_lengths, int B,
+                      int stride, int V, int reset, int32_t *state, cudaStream_t stream);
+
+/*
+ * Penalties for repeated tokens, additive biases and grammar masks on the rows
+ * that a verify reads (the target's; a drafter's rows likewise).
+ *
+ *   logits        [B, R, V].  For a chain verify R = K + 1, for a tree N + 1;
+ *                 R = 1 is a single step's row.
+ *   draft_tokens  [B, R-1] int32 or NULL.  Row r's penalties also count the
+ *                 drafts above it: x_0 .. x_{r-1} of a chain; node r - 1 and
+ *                 its ancestors of a tree.  Tokens outside [0, V) count for
+ *                 nothing (the verify judges them).
+ *   parent_idx    [B, R-1] int32 as for spec_tree_verify_*, or NULL: a chain.
+ *   token_state   [B, spec_token_state_words(V)] int32 or NULL (no history).
+ *   repetition, frequency, presence  [B] float each or NULL (1, 0, 0).
+ *   bias_tokens, bias_values  [B, n_bias]; tokens outside [0, V) are skipped
+ *                 (padding), a token given twice gets the sum, added in order.
+ *                 Both may be NULL when n_bias == 0.
+ *   allowed_mask  [B, mask_rows, ceil(V/32)] uint32 or NULL: bit v % 32 of word
+ *                 v / 32 set = token v allowed.  mask_rows is R, or 1 for one
+ *                 mask per sequence.  Bits at V and above are not read as tokens.
+ *   out_logits    [B, R, V]: `logits` itself (in place: only what changes is
+ *                 read and written), or memory apart from it.
+ * With c the occurrences of v among the output tokens and the drafts above the
+ * row, and seen = (v in the prompt or c > 0):
+ *   z1 = seen ? (z > 0 ? z / repetition : z * repetition) : z
+ *   z2 = z1 - frequency * c - presence * (c > 0) + bias
+ *   out = allowed ? z2 : -inf
+ * in fp32 and rounded once.  A masked token is -inf whatever its logit was
+ * (NaN included); a row with nothing allowed is all -inf, which a verify
+ * reports as bad data, as it does a NaN that is allowed.
+ * Bad data: a parent index outside [-1, i), a repetition that is not positive
+ * and finite, or a frequency or presence that is not finite makes every row of
+ * that sequence NaN and sets SPEC_FLAG_BAD_DATA.
+ * 1 <= R <= 1025, 1 <= V <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,
+ * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`;
+ * no scratch.
+ */
+int spec_process_logits_f32(const float *logits, const int32_t *draft_tokens, const int32_t *parent_idx,
+                            const int32_t *token_state, const float *repetition, const float *frequency,
+                            const float *presence, int n_bias, const int32_t *bias_tokens,
+                            const float *bias_values, const uint32_t *allowed_mask, int mask_rows, int B,
+                            int R, int V, float *out_logits, cudaStream_t stream);
+int spec_process_logits_bf16(const uint16_t *logits, const int32_t *draft_tokens, const int32_t *parent_idx,
+                             const int32_t *token_state, const float *repetition, const float *frequency,
+                             const float *presence, int n_bias, const int32_t *bias_tokens,
+                             const float *bias_values, const uint32_t *allowed_mask, int mask_rows, int B,
+                             int R, int V, uint16_t *out_logits, cudaStream_t stream);
+
+/*
+ * Appends a step's keys and values to a paged cache, turned to their positions
+ * on the way, and turns its queries.
+ *
+ * The forward pass that a verify needs takes T tokens of each sequence: for a
+ * chain the last committed token and the K drafts (T = K + 1), for a tree that
+ * token and the N nodes (T = N + 1, node j is token j + 1), or a prompt.
+ * Token i goes to slot lengths[b] + i of its sequence; its position is
+ * lengths[b] + depth, where depth is i without parent_idx and, with it, 0 for
+ * token 0 and the node's level for the others (a child of the root: 1).
+ *
+ *   k, v          token t = b T + i at element t * kv_stride, its Hkv x D
+ *                 values contiguous (a slice of a joint projection fits).
+ *   q, out_q      the same with Hq heads and q_stride; out_q is [B, T, Hq, D],
+ *                 or q itself when q_stride == Hq * D.  NULL when Hq == 0.
+ *   parent_idx    [B, T-1] int32 as for spec_tree_verify_*, or NULL.
+ *   n_new         [B] int32 or NULL (T): tokens i >= n_new[b] are padding;
+ *                 nothing is written for them.
+ *   lengths       [B] int32: entries of the sequence already in the cache.
+ *   page_table    [B, max_pages] int32: slot s lies in page page_table[b, s /
+ *                 page_size] at s % page_size.
+ *   rot_dim       even, 0 <= rot_dim <= D: the first rot_dim values of a head
+ *                 are turned, pair i by 2 pi * position * turns[i] / 2^64.
+ *                 interleaved == 0: pair i is (i, i + rot_dim / 2), else
+ *                 (2 i, 2 i + 1).
+ *   turns         [rot_dim / 2] uint64 (device): frequency i in 2^-64 turns a
+ *                 position, that is radians / (2 pi) * 2^64.  The fraction of
+ *                 a turn is exact for every position.
+ *   key_cache, value_cache  [pages, page_size, Hkv, D].
+ * Values are copied as they are; keys and queries are turned in fp32 and
+ * rounded once.  Two tokens of a call that share a slot (sequences that share
+ * a page they write to) are the caller's mistake: either may stay.
+ * Bad data (SPEC_FLAG_BAD_DATA): a length or n_new out of range, tokens past
+ * max_pages * page_size or a parent index outside [-1, i): nothing of that
+ * sequence is written to the caches and its out_q rows are NaN.  A page index
+ * outside [0, pages): the tokens of that page are not written to the caches.
+ * T >= 0 (<= 1025 with parent_idx), 1 <= D <= 1024.  Returns SPEC_OK,
+ * SPEC_ERR_NULL, SPEC_ERR_SHAPE or SPEC_ERR_CUDA.  One launch on `stream`; no
+ * scratch.
+ */
+int spec_kv_append_f32(const float *k, const float *v, int64_t kv_stride, const float *q, int64_t q_stride,
+                       float *out_q, const int32_t *parent_idx, const int32_t *n_new, const int32_t *lengths,
+                       const int32_t *page_table, int B, int T, int Hq, int Hkv, int D, int rot_dim,
+                       int interleaved, const uint64_t *turns, float *key_cache, float *value_cache, int pages,
+                       int page_size, int max_pages, cudaStream_t stream);
+int spec_kv_append_bf16(const uint16_t *k, const uint16_t *v, int64_t kv_stride, const uint16_t *q,
+                        int64_t q_stride, uint16_t *out_q, const int32_t *parent_idx, const int32_t *n_new,
+                        const int32_t *lengths, const int32_t *page_table, int B, int T, int Hq, int Hkv, int D,
+                        int rot_dim, int interleaved, const uint64_t *turns, uint16_t *key_cache,
+                        uint16_t *value_cache, int pages, int page_size, int max_pages, cudaStream_t stream);
+
+/*
+ * Keeps the accepted path of a tree verify in the paged cache: the entries of
+ * the path's nodes move to the slots behind the root's, in every layer.
+ *
+ *   key_cache, value_cache  layer l at byte l * layer_bytes: [pages,
+ *                 page_size] entries of entry_bytes each (any type: bytes are
+ *                 moved).
+ *   page_table, lengths  as given to spec_kv_append_* for this step.
+ *   tree_tokens, parent_idx  [B, N], out_path [B, N+1], out_len [B]: the tree
+ *                 and what spec_tree_verify_* answered.
+ *   out_nodes     [B, N+1] int32: the path's nodes by level, then -1.  (Of
+ *                 nodes that carry the same tokens down from the root the last
+ *                 level's lowest index counts; their entries are alike.)
+ *   out_lengths   [B] int32: lengths[b] + out_len[b], the entries that the
+ *                 cache then holds (the token that the verify added is not
+ *                 among them: it is the next step's root).
+ * With n = out_len[b] - 1 accepted nodes, the entry of the node on level d
+ * (slot lengths[b] + 1 + node) moves to slot lengths[b] + d, d = 1 .. n.
+ * A sequence with out_len -1 (bad data of the verify) is left as it is:
+ * out_nodes -1, out_lengths = lengths.  So is one whose own data are bad
+ * (SPEC_FLAG_BAD_DATA): an out_len outside [1, N + 1], tokens that no path of
+ * the tree carries, a parent outside [-1, i), slots past the page table or a
+ * page outside [0, pages).
+ * out_lengths may not share memory with lengths (SPEC_ERR_OVERLAP).
+ * 0 <= N <= 1024, 1 <= layers <= 32767.  Returns SPEC_OK, SPEC_ERR_NULL,
+ * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`;
+ * no scratch.
+ */
+int spec_kv_commit(void *key_cache, void *value_cache, int layers, int64_t layer_bytes, int pages,
+                   int page_size, int entry_bytes, const int32_t *page_table, int max_pages,
+                   const int32_t *lengths, const int32_t *tree_tokens, const int32_t *parent_idx,
+                   const int32_t *out_path, const int32_t *out_len, int B, int N, int32_t *out_nodes,
+                   int32_t *out_lengths, cudaStream_t stream);
 
 /*
  * Test hook, for fault-injection tests: the next n scratch allocations from

@@ -16,6 +16,10 @@ library's CUDA kernels.  There is no CPU fallback.
     spec_tree_verify_sampling(target_logits, draft_logits, tree_tokens, parent_idx, T, seed)
     spec_acceptance_stats(n_accepted, K)  # histogram, alpha, mean tokens
     spec_ngram_draft(tokens, lengths, n_min, n_max, K)  # prompt-lookup drafts
+    spec_token_state(B, V, device)    # zeroed token counts; spec_count_tokens(state, tokens, V) adds to them
+    spec_process_logits(logits, draft_tokens, ...)  # penalties, biases and grammar masks on a verify's rows
+    spec_kv_append(k, v, key_cache, value_cache, page_table, lengths, ...)  # rotated, into a paged cache
+    spec_kv_commit(key_cache, value_cache, page_table, lengths, ...)  # a tree's accepted path stays
     spec_get_status()                 # device status word (bad data, timeouts)
 """
 from __future__ import annotations
@@ -29,6 +33,8 @@ __all__ = [
     "spec_verify", "spec_verify_early_exit", "spec_verify_static_scratch", "spec_verify_stats", "spec_verify_khint",
     "spec_verify_greedy_argmax",
     "spec_tree_verify_greedy", "spec_tree_verify_sampling", "spec_acceptance_stats", "spec_ngram_draft",
+    "spec_token_state", "spec_count_tokens", "spec_process_logits", "spec_rope_turns", "spec_kv_append",
+    "spec_kv_commit",
     "spec_get_status", "spec_test_spin_limit", "spec_test_wait_probe", "SpecError",
     "SPEC_FLAG_BAD_DATA", "SPEC_FLAG_TIMEOUT",
 ]
@@ -345,6 +351,238 @@ def spec_ngram_draft(tokens, lengths, n_min: int, n_max: int, K: int, out_drafts
         _lib.check(lib.spec_ngram_draft(_ptr(tokens), _ptr(lengths), B, Lmax, int(n_min), int(n_max), int(K),
                                         _ptr(drafts), _ptr(n_drafts), _ptr(match_len), _stream(stream)))
     return drafts, n_drafts, match_len
+
+
+def spec_token_state(B: int, V: int, device) -> torch.Tensor:
+    """An empty token-count state: int32 [B, words] zeros (spec_count_tokens
+    fills it, spec_process_logits reads it; the layout is in specverify.h).
+    One row of it, state[b:b+1], is a state too."""
+    words = _lib.load().spec_token_state_words(int(V))
+    if words < 0:
+        _lib.check(words)
+    return torch.zeros((B, words), dtype=torch.int32, device=device)
+
+
+def _state(t, B, V, device):
+    words = _lib.load().spec_token_state_words(int(V))
+    if words < 0:
+        _lib.check(words)
+    return _i32(t, (B, words), "token_state", device)
+
+
+def spec_count_tokens(state, tokens, V: int, lengths=None, prompt_lengths=None, reset: bool = False, stream=None):
+    """Adds tokens [B, S] int32 to the counts in `state` and returns it.
+
+    Row b's first lengths[b] entries count (None: all S); the first
+    prompt_lengths[b] of them as prompt (None: none), the rest as output.
+    Tokens outside [0, V) are skipped: a verify's padded out_tokens or
+    out_path can be passed.  reset=True empties the state first."""
+    if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
+        raise ValueError("tokens must be [B, S]")
+    B, S = tokens.shape
+    _i32(tokens, (B, S), "tokens")
+    dev = tokens.device
+    _state(state, B, V, dev)
+    if lengths is not None:
+        _i32(lengths, (B,), "lengths", dev)
+    if prompt_lengths is not None:
+        _i32(prompt_lengths, (B,), "prompt_lengths", dev)
+    with torch.cuda.device(dev):
+        _lib.check(_lib.load().spec_count_tokens(_ptr(tokens), _ptr(lengths), _ptr(prompt_lengths), B, S, int(V),
+                                                 1 if reset else 0, _ptr(state), _stream(stream)))
+    return state
+
+
+def _f32(t, shape, name, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _same_device(t, device, name)
+    return t
+
+
+def spec_process_logits(logits, draft_tokens=None, parent_idx=None, token_state=None, repetition=None,
+                        frequency=None, presence=None, bias_tokens=None, bias_values=None, allowed_mask=None,
+                        out=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on the rows a
+    verify reads: logits [B, R, V] (R = K + 1 of a chain, N + 1 of a tree).
+
+    draft_tokens [B, R-1] int32 (with parent_idx [B, R-1] for a tree): row r's
+    penalties count the drafts above it too.  token_state: spec_token_state's,
+    filled by spec_count_tokens.  repetition, frequency, presence: float32 [B].
+    bias_tokens int32 / bias_values float32 [B, n]; tokens outside [0, V) are
+    padding.  allowed_mask int32 [B, R, ceil(V/32)], or [B, ceil(V/32)] for
+    all rows: a set bit allows the token.  out=logits works in place and
+    touches only what changes; out=None allocates.  Returns out."""
+    bf16 = _is_bf16(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, R, V]")
+    B, R, V = logits.shape
+    dev = logits.device
+    if draft_tokens is not None:
+        _i32(draft_tokens, (B, R - 1), "draft_tokens", dev)
+    if parent_idx is not None:
+        if draft_tokens is None:
+            raise ValueError("parent_idx needs draft_tokens")
+        _i32(parent_idx, (B, R - 1), "parent_idx", dev)
+    if token_state is not None:
+        _state(token_state, B, V, dev)
+    for t, name in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence")):
+        if t is not None:
+            _f32(t, (B,), name, dev)
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values go together")
+    n_bias = 0
+    if bias_tokens is not None:
+        if bias_tokens.dim() != 2:
+            raise ValueError("bias_tokens must be [B, n]")
+        n_bias = bias_tokens.shape[1]
+        _i32(bias_tokens, (B, n_bias), "bias_tokens", dev)
+        _f32(bias_values, (B, n_bias), "bias_values", dev)
+    mask_rows = 0
+    if allowed_mask is not None:
+        W = (V + 31) // 32
+        mask_rows = 1 if allowed_mask.dim() == 2 else R
+        _i32(allowed_mask, (B, W) if allowed_mask.dim() == 2 else (B, R, W), "allowed_mask", dev)
+    out = _out(out, (B, R, V), logits.dtype, dev, "out")
+    lib = _lib.load()
+    fn = lib.spec_process_logits_bf16 if bf16 else lib.spec_process_logits_f32
+    with torch.cuda.device(dev):
+        _lib.check(fn(_ptr(logits), _ptr(draft_tokens), _ptr(parent_idx), _ptr(token_state), _ptr(repetition),
+                      _ptr(frequency), _ptr(presence), n_bias, _ptr(bias_tokens), _ptr(bias_values),
+                      _ptr(allowed_mask), mask_rows, B, R, V, _ptr(out), _stream(stream)))
+    return out
+
+
+def spec_rope_turns(inv_freq, device) -> torch.Tensor:
+    """Rotary frequencies (radians a position, float64-able: theta ** (-2 i /
+    rot_dim) or any scaled set) as spec_kv_append takes them: int64 [rot_dim /
+    2] holding 2^-64 fractions of a turn (the bits are unsigned)."""
+    import math
+    vals = [int(round(float(f) / (2 * math.pi) * 2.0 ** 64)) % 2 ** 64 for f in inv_freq]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in vals], dtype=torch.int64, device=device)
+
+
+def _tokens_view(t, name, dtype, B, T, D, device):
+    """(heads, token stride) of a [B, T, H, D] tensor whose tokens lie at equal
+    distances and whose heads are contiguous (a slice of a joint projection)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    _same_device(t, device, name)
+    if t.dim() != 4 or tuple(t.shape[:2]) != (B, T) or t.shape[3] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, T, 'H', D)}")
+    H = t.shape[2]
+    sb, st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if T == 1:
+        st = sb if B > 1 else max(H * D, 1)
+    elif B > 1 and sb != T * st:
+        raise ValueError(f"{name}'s tokens must lie at equal distances")
+    return H, st
+
+
+def spec_kv_append(k, v, key_cache, value_cache, page_table, lengths, turns=None, q=None, parent_idx=None,
+                   n_new=None, interleaved: bool = False, out_q=None, stream=None):
+    """Appends a step's keys and values [B, T, Hkv, D] to a paged cache
+    [pages, page_size, Hkv, D], the keys rotated to their positions, and
+    rotates the queries q [B, T, Hq, D].
+
+    Token i goes to slot lengths[b] + i; its position is lengths[b] + i, or,
+    with parent_idx [B, T-1] (token 0 the root, token j + 1 node j),
+    lengths[b] + its depth.  turns (spec_rope_turns): None rotates nothing.
+    n_new [B]: tokens from there on are padding.  k, v and q may be slices of
+    a joint projection.  Returns out_q (None without q)."""
+    bf16 = isinstance(k, torch.Tensor) and k.dtype == torch.bfloat16
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 4:
+        raise ValueError("k must be a CUDA tensor [B, T, Hkv, D]")
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"k must be float32 or bfloat16, got {k.dtype}")
+    B, T, _, D = k.shape
+    dev = k.device
+    Hkv, ks = _tokens_view(k, "k", k.dtype, B, T, D, dev)
+    Hv, vs = _tokens_view(v, "v", k.dtype, B, T, D, dev)
+    if Hv != Hkv or vs != ks:
+        raise ValueError("k and v must share heads and token stride")
+    for c, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        if (not isinstance(c, torch.Tensor) or c.dtype != k.dtype or c.dim() != 4 or not c.is_contiguous()
+                or tuple(c.shape[2:]) != (Hkv, D)):
+            raise ValueError(f"{name} must be a contiguous {k.dtype} tensor [pages, page_size, {Hkv}, {D}]")
+        _same_device(c, dev, name)
+    if key_cache.shape != value_cache.shape:
+        raise ValueError("key_cache and value_cache must have the same shape")
+    pages, page_size = key_cache.shape[:2]
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    max_pages = page_table.shape[1]
+    _i32(page_table, (B, max_pages), "page_table", dev)
+    _i32(lengths, (B,), "lengths", dev)
+    if parent_idx is not None:
+        _i32(parent_idx, (B, T - 1), "parent_idx", dev)
+    if n_new is not None:
+        _i32(n_new, (B,), "n_new", dev)
+    rot = 0
+    if turns is not None:
+        if not isinstance(turns, torch.Tensor) or turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+            raise ValueError("turns must be a contiguous int64 tensor [rot_dim / 2]")
+        _same_device(turns, dev, "turns")
+        rot = 2 * turns.shape[0]
+    Hq = qs = 0
+    if q is not None:
+        Hq, qs = _tokens_view(q, "q", k.dtype, B, T, D, dev)
+        out_q = _out(out_q, (B, T, Hq, D), k.dtype, dev, "out_q")
+    elif out_q is not None:
+        raise ValueError("out_q needs q")
+    lib = _lib.load()
+    fn = lib.spec_kv_append_bf16 if bf16 else lib.spec_kv_append_f32
+    with torch.cuda.device(dev):
+        _lib.check(fn(_ptr(k), _ptr(v), ks, _ptr(q), qs, _ptr(out_q), _ptr(parent_idx), _ptr(n_new), _ptr(lengths),
+                      _ptr(page_table), B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, _ptr(turns),
+                      _ptr(key_cache), _ptr(value_cache), pages, page_size, max_pages, _stream(stream)))
+    return out_q
+
+
+def spec_kv_commit(key_cache, value_cache, page_table, lengths, tree_tokens, parent_idx, out_path, out_len,
+                   out_nodes=None, out_lengths=None, stream=None):
+    """Keeps a tree verify's accepted path in the paged cache: its nodes'
+    entries move to the slots behind the root's.
+
+    key_cache, value_cache: [pages, page_size, ...] or, with all layers in one
+    tensor, [layers, pages, page_size, ...] (five dimensions), any type.
+    lengths as given to spec_kv_append for the step; out_path, out_len: the
+    verify's.  Returns (nodes [B, N+1] int32, -1 padded; new lengths [B])."""
+    if not isinstance(key_cache, torch.Tensor) or not key_cache.is_cuda or key_cache.dim() not in (4, 5):
+        raise ValueError("key_cache must be a CUDA tensor [(layers,) pages, page_size, H, D]")
+    dev = key_cache.device
+    if (not isinstance(value_cache, torch.Tensor) or value_cache.shape != key_cache.shape
+            or value_cache.dtype != key_cache.dtype):
+        raise ValueError("value_cache must be like key_cache")
+    _same_device(value_cache, dev, "value_cache")
+    if not key_cache.is_contiguous() or not value_cache.is_contiguous():
+        raise ValueError("the caches must be contiguous")
+    shape = tuple(key_cache.shape)
+    layers, (pages, page_size, H, D) = (shape[0], shape[1:]) if len(shape) == 5 else (1, shape)
+    entry = H * D * key_cache.element_size()
+    if not isinstance(tree_tokens, torch.Tensor) or tree_tokens.dim() != 2:
+        raise ValueError("tree_tokens must be [B, N]")
+    B, N = tree_tokens.shape
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    max_pages = page_table.shape[1]
+    _i32(page_table, (B, max_pages), "page_table", dev)
+    for t, s, name in ((lengths, (B,), "lengths"), (tree_tokens, (B, N), "tree_tokens"),
+                       (parent_idx, (B, N), "parent_idx"), (out_path, (B, N + 1), "out_path"),
+                       (out_len, (B,), "out_len")):
+        _i32(t, s, name, dev)
+    out_nodes = _out(out_nodes, (B, N + 1), torch.int32, dev, "out_nodes")
+    out_lengths = _out(out_lengths, (B,), torch.int32, dev, "out_lengths")
+    with torch.cuda.device(dev):
+        _lib.check(_lib.load().spec_kv_commit(
+            _ptr(key_cache), _ptr(value_cache), layers, pages * page_size * entry, pages, page_size, entry,
+            _ptr(page_table), max_pages, _ptr(lengths), _ptr(tree_tokens), _ptr(parent_idx), _ptr(out_path),
+            _ptr(out_len), B, N, _ptr(out_nodes), _ptr(out_lengths), _stream(stream)))
+    return out_nodes, out_lengths
 
 
 def spec_get_status(stream=None, device=None) -> int:

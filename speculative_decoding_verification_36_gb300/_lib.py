@@ -22,6 +22,7 @@ SPEC_ERR_TEMPERATURE = -3
 SPEC_ERR_CUDA = -4
 SPEC_ERR_SCRATCH = -5
 SPEC_ERR_HINT = -6
+SPEC_ERR_OVERLAP = -7
 SPEC_STATIC_SCRATCH_BYTES = 8 << 20
 SPEC_FLAG_BAD_DATA = 1
 SPEC_FLAG_TIMEOUT = 2
@@ -34,6 +35,7 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _U64 = ctypes.c_uint64
 _D = ctypes.c_double
+_I64 = ctypes.c_int64
 
 # name -> argtypes (restype is int for all but spec_status_string)
 SIGNATURES = {
@@ -56,6 +58,15 @@ SIGNATURES = {
     "spec_tree_verify_sampling_bf16": [_P, _P, _P, _P, _I, _I, _I, _F, _U64, _P, _P, _P],
     "spec_acceptance_stats": [_P, _I, _I, _P, _P, _P, _P],
     "spec_ngram_draft": [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P],
+    "spec_token_state_words": [_I],
+    "spec_count_tokens": [_P, _P, _P, _I, _I, _I, _I, _P, _P],
+    "spec_process_logits_f32": [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P],
+    "spec_process_logits_bf16": [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P],
+    "spec_kv_append_f32": [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P,
+                           _I, _I, _I, _P],
+    "spec_kv_append_bf16": [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P,
+                            _I, _I, _I, _P],
+    "spec_kv_commit": [_P, _P, _I, _I64, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P],
     "spec_test_fail_allocations": [_I],
     "spec_test_spin_limit": [ctypes.c_uint32],
     "spec_test_wait_probe": [ctypes.c_void_p],

@@ -528,6 +528,124 @@ int tree_sample_impl(bool bf16, const void* target, const void* draft, const int
   return SPEC_OK;
 }
 
+// Token counts: words of a sequence's state row and the counts in it.
+long long state_counts(int V) { return ((long long)V + 31) / 32 * 32; }
+long long state_words(int V) { return state_counts(V) + (state_counts(V) / 32 + 3) / 4 * 4; }
+constexpr int kMaxStateVocab = 1 << 30;
+
+// Do [p, p + n) and [q, q + m) share a byte?
+bool overlaps(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + m && b < a + n;
+}
+
+int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int32_t* parents,
+                 const int32_t* state, const float* rep, const float* freq, const float* pres,
+                 int n_bias, const int32_t* bias_tokens, const float* bias_values,
+                 const uint32_t* mask, int mask_rows, int B, int R, int V, void* out,
+                 cudaStream_t stream) {
+  if (B < 0 || R < 1 || R > sv::kMaxTreeNodes + 1 || V < 1 || V > kMaxStateVocab || n_bias < 0 ||
+      !sizes_ok(B, R, V) || (mask && mask_rows != 1 && mask_rows != R))
+    return SPEC_ERR_SHAPE;
+  if (B == 0) return SPEC_OK;
+  if (!logits || !out || (parents && !drafts) || (n_bias > 0 && (!bias_tokens || !bias_values)))
+    return SPEC_ERR_NULL;
+  const size_t esz = bf16 ? 2 : 4;
+  const size_t bytes = (size_t)B * R * V * esz;
+  if (logits != out && overlaps(logits, bytes, out, bytes)) return SPEC_ERR_OVERLAP;
+  sv::ProcessArgs a;
+  memset(&a, 0, sizeof a);
+  a.in = logits;
+  a.out = out;
+  a.drafts = R > 1 ? drafts : nullptr;
+  a.parents = R > 1 ? parents : nullptr;
+  a.state = state;
+  a.P = state_counts(V);
+  a.words = state_words(V);
+  a.rep = rep;
+  a.freq = freq;
+  a.pres = pres;
+  a.n_bias = n_bias;
+  a.bias_tokens = bias_tokens;
+  a.bias_values = bias_values;
+  a.mask = mask;
+  a.mask_rows = mask_rows;
+  a.W = (int)(((long long)V + 31) / 32);
+  a.B = B;
+  a.R = R;
+  a.V = V;
+  DeviceState* d = nullptr;
+  const int rc = get_device_state(&d);
+  if (rc) return rc;
+  a.status = d->status;
+  a.chunks = (V + sv::process_chunk() - 1) / sv::process_chunk();
+  // a few CTAs per SM: few sequences are split by rows as well
+  const long long units = (long long)B * a.chunks, want = 8LL * d->sms;
+  long long groups = units < want ? (want + units - 1) / units : 1;
+  if (groups > R) groups = R;
+  a.rows_per = (int)((R + groups - 1) / groups);
+  if (a.parents && a.rows_per > sv::process_tree_rows()) a.rows_per = sv::process_tree_rows();
+  a.groups = (R + a.rows_per - 1) / a.rows_per;
+  if (units * a.groups > INT_MAX) return SPEC_ERR_SHAPE;
+  const bool vec = aligned16(logits) && aligned16(out) && ((size_t)V * esz) % 16 == 0;
+  const cudaError_t e = sv::launch_process(a, bf16, vec, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "logit processing launch");
+  return SPEC_OK;
+}
+
+int kv_append_impl(bool bf16, const void* k, const void* v, int64_t kv_stride, const void* q,
+                   int64_t q_stride, void* out_q, const int32_t* parents, const int32_t* n_new,
+                   const int32_t* lengths, const int32_t* page_table, int B, int T, int Hq, int Hkv,
+                   int D, int rot, int interleaved, const uint64_t* turns, void* k_cache,
+                   void* v_cache, int pages, int page_size, int max_pages, cudaStream_t stream) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 1 || D < 1 || D > sv::kv_max_rot() || rot < 0 || rot > D ||
+      rot % 2 || pages < 1 || page_size < 1 || max_pages < 1 ||
+      (parents && T > sv::kMaxTreeNodes + 1) || (long long)Hkv * D > INT_MAX / 8 ||
+      (long long)Hq * D > INT_MAX / 8 || kv_stride < (long long)Hkv * D ||
+      (Hq > 0 && q_stride < (long long)Hq * D) || (long long)B * T > INT_MAX)
+    return SPEC_ERR_SHAPE;
+  if (B == 0 || T == 0) return SPEC_OK;
+  if (!k || !v || !lengths || !page_table || !k_cache || !v_cache || (rot > 0 && !turns) ||
+      (Hq > 0 && (!q || !out_q)))
+    return SPEC_ERR_NULL;
+  sv::KvAppendArgs a;
+  memset(&a, 0, sizeof a);
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.out_q = out_q;
+  a.kv_stride = kv_stride;
+  a.q_stride = q_stride;
+  a.parents = T > 1 ? parents : nullptr;
+  a.n_new = n_new;
+  a.lengths = lengths;
+  a.page_table = page_table;
+  a.turns = (const unsigned long long*)turns;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.rot = rot;
+  a.interleaved = interleaved ? 1 : 0;
+  a.pages = pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  DeviceState* d = nullptr;
+  const int rc = get_device_state(&d);
+  if (rc) return rc;
+  a.status = d->status;
+  const int ve = bf16 ? 8 : 4;
+  const bool vec = aligned16(k) && aligned16(v) && aligned16(k_cache) && aligned16(v_cache) &&
+                   kv_stride % ve == 0 && D % ve == 0 && rot % (interleaved ? ve : 2 * ve) == 0 &&
+                   (Hq == 0 || (aligned16(q) && aligned16(out_q) && q_stride % ve == 0));
+  const cudaError_t e = sv::launch_kv_append(a, bf16, vec, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+  return SPEC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -751,6 +869,123 @@ int spec_ngram_draft(const int32_t* tokens, const int32_t* lengths, int B, int s
   return SPEC_OK;
 }
 
+int spec_token_state_words(int V) {
+  return V < 1 || V > kMaxStateVocab ? SPEC_ERR_SHAPE : (int)state_words(V);
+}
+
+int spec_count_tokens(const int32_t* tokens, const int32_t* lengths, const int32_t* prompt_lengths, int B,
+                      int stride, int V, int reset, int32_t* state, cudaStream_t stream) {
+  if (B < 0 || stride < 0 || V < 1 || V > kMaxStateVocab) return SPEC_ERR_SHAPE;
+  if (B == 0) return SPEC_OK;
+  if (!state || (stride > 0 && !tokens)) return SPEC_ERR_NULL;
+  DeviceState* d = nullptr;
+  const int rc = get_device_state(&d);
+  if (rc) return rc;
+  sv::CountArgs a;
+  memset(&a, 0, sizeof a);
+  a.tokens = tokens;
+  a.stride = stride;
+  a.lengths = lengths;
+  a.prompt_lengths = prompt_lengths;
+  a.B = B;
+  a.V = V;
+  a.reset = reset ? 1 : 0;
+  a.P = state_counts(V);
+  a.words = state_words(V);
+  a.state = state;
+  a.status = d->status;
+  const cudaError_t e = sv::launch_count(a, d->sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "token count launch");
+  return SPEC_OK;
+}
+
+int spec_process_logits_f32(const float* logits, const int32_t* draft_tokens, const int32_t* parent_idx,
+                            const int32_t* token_state, const float* repetition, const float* frequency,
+                            const float* presence, int n_bias, const int32_t* bias_tokens,
+                            const float* bias_values, const uint32_t* allowed_mask, int mask_rows, int B,
+                            int R, int V, float* out_logits, cudaStream_t stream) {
+  return process_impl(false, logits, draft_tokens, parent_idx, token_state, repetition, frequency, presence,
+                      n_bias, bias_tokens, bias_values, allowed_mask, mask_rows, B, R, V, out_logits, stream);
+}
+
+int spec_process_logits_bf16(const uint16_t* logits, const int32_t* draft_tokens, const int32_t* parent_idx,
+                             const int32_t* token_state, const float* repetition, const float* frequency,
+                             const float* presence, int n_bias, const int32_t* bias_tokens,
+                             const float* bias_values, const uint32_t* allowed_mask, int mask_rows, int B,
+                             int R, int V, uint16_t* out_logits, cudaStream_t stream) {
+  return process_impl(true, logits, draft_tokens, parent_idx, token_state, repetition, frequency, presence,
+                      n_bias, bias_tokens, bias_values, allowed_mask, mask_rows, B, R, V, out_logits, stream);
+}
+
+int spec_kv_append_f32(const float* k, const float* v, int64_t kv_stride, const float* q, int64_t q_stride,
+                       float* out_q, const int32_t* parent_idx, const int32_t* n_new, const int32_t* lengths,
+                       const int32_t* page_table, int B, int T, int Hq, int Hkv, int D, int rot_dim,
+                       int interleaved, const uint64_t* turns, float* key_cache, float* value_cache, int pages,
+                       int page_size, int max_pages, cudaStream_t stream) {
+  return kv_append_impl(false, k, v, kv_stride, q, q_stride, out_q, parent_idx, n_new, lengths, page_table, B, T,
+                        Hq, Hkv, D, rot_dim, interleaved, turns, key_cache, value_cache, pages, page_size,
+                        max_pages, stream);
+}
+
+int spec_kv_append_bf16(const uint16_t* k, const uint16_t* v, int64_t kv_stride, const uint16_t* q,
+                        int64_t q_stride, uint16_t* out_q, const int32_t* parent_idx, const int32_t* n_new,
+                        const int32_t* lengths, const int32_t* page_table, int B, int T, int Hq, int Hkv, int D,
+                        int rot_dim, int interleaved, const uint64_t* turns, uint16_t* key_cache,
+                        uint16_t* value_cache, int pages, int page_size, int max_pages, cudaStream_t stream) {
+  return kv_append_impl(true, k, v, kv_stride, q, q_stride, out_q, parent_idx, n_new, lengths, page_table, B, T,
+                        Hq, Hkv, D, rot_dim, interleaved, turns, key_cache, value_cache, pages, page_size,
+                        max_pages, stream);
+}
+
+int spec_kv_commit(void* key_cache, void* value_cache, int layers, int64_t layer_bytes, int pages,
+                   int page_size, int entry_bytes, const int32_t* page_table, int max_pages,
+                   const int32_t* lengths, const int32_t* tree_tokens, const int32_t* parent_idx,
+                   const int32_t* out_path, const int32_t* out_len, int B, int N, int32_t* out_nodes,
+                   int32_t* out_lengths, cudaStream_t stream) {
+  if (B < 0 || N < 0 || N > sv::kMaxTreeNodes || layers < 1 || layers > 32767 || pages < 1 || page_size < 1 ||
+      entry_bytes < 1 || max_pages < 1 ||
+      layer_bytes / page_size / entry_bytes < pages)
+    return SPEC_ERR_SHAPE;
+  if (B == 0) return SPEC_OK;
+  if (!key_cache || !value_cache || !page_table || !lengths || !out_path || !out_len || !out_nodes ||
+      !out_lengths || (N > 0 && (!tree_tokens || !parent_idx)))
+    return SPEC_ERR_NULL;
+  // every CTA of a sequence reads its length: the new one goes elsewhere
+  if (overlaps(lengths, (size_t)B * 4, out_lengths, (size_t)B * 4)) return SPEC_ERR_OVERLAP;
+  sv::KvCommitArgs a;
+  memset(&a, 0, sizeof a);
+  a.k_cache = key_cache;
+  a.v_cache = value_cache;
+  a.layer_bytes = layer_bytes;
+  a.layers = layers;
+  a.pages = pages;
+  a.page_size = page_size;
+  a.entry_bytes = entry_bytes;
+  a.max_pages = max_pages;
+  a.page_table = page_table;
+  a.lengths = lengths;
+  a.tokens = tree_tokens;
+  a.parents = parent_idx;
+  a.path = out_path;
+  a.path_len = out_len;
+  a.B = B;
+  a.N = N;
+  a.out_nodes = out_nodes;
+  a.out_lengths = out_lengths;
+  DeviceState* d = nullptr;
+  const int rc = get_device_state(&d);
+  if (rc) return rc;
+  a.status = d->status;
+  int vb = 16;
+  if (entry_bytes % 16 || layer_bytes % 16 || !aligned16(key_cache) || !aligned16(value_cache)) {
+    const bool word = entry_bytes % 4 == 0 && layer_bytes % 4 == 0 && (((uintptr_t)key_cache | (uintptr_t)value_cache) & 3) == 0;
+    vb = word ? 4 : 1;
+  }
+  const cudaError_t e = sv::launch_kv_commit(a, vb, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache commit launch");
+  return SPEC_OK;
+}
+
 int spec_test_fail_allocations(int n) { return g_fail_allocs.exchange(n < 0 ? 0 : n); }
 
 int spec_test_spin_limit(uint32_t iterations) {
@@ -799,13 +1034,16 @@ const char* spec_status_string(int code) {
     case SPEC_ERR_NULL:
       return "a required pointer is NULL";
     case SPEC_ERR_SHAPE:
-      return "bad shape: B < 0, K outside [0, 255], N outside [0, 1024], V < 1, or size overflow";
+      return "bad shape: B < 0, K outside [0, 255], N outside [0, 1024], V < 1, a size outside its "
+             "documented range, or size overflow";
     case SPEC_ERR_TEMPERATURE:
       return "bad temperature: NaN, negative, or in (0, 1e-30)";
     case SPEC_ERR_CUDA:
       return g_cuda_msg;
     case SPEC_ERR_HINT:
       return "bad draft-length parameters: need 0 <= k_min <= k_max <= 255 and h_lo <= h_hi (no NaN)";
+    case SPEC_ERR_OVERLAP:
+      return "an output shares memory with an input that it may not share memory with";
     case SPEC_ERR_SCRATCH:
       return "the problem needs more scratch than the static buffer holds "
              "(SPEC_STATIC_SCRATCH_BYTES)";

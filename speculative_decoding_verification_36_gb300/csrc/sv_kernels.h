@@ -260,6 +260,71 @@ cudaError_t launch_ngram(const NgramArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_acceptance(const int32_t* n, int B, int K, unsigned long long* hist, double* alpha,
                               double* mean_tokens, int sms, cudaStream_t s);
 
+// Token counts and logit processing (process_kernel.cu).
+struct CountArgs {
+  const int32_t* tokens;          // [B, stride]
+  long long stride;
+  const int32_t* lengths;         // [B] or NULL: every entry
+  const int32_t* prompt_lengths;  // [B] or NULL: none is of the prompt
+  int B, V, reset;
+  long long P, words;             // counts of a row, words of a row (spec_token_state_words)
+  int32_t* state;                 // [B, words]
+  unsigned* status;
+};
+cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s);
+
+struct ProcessArgs {
+  const void* in;         // [B, R, V]
+  void* out;              // [B, R, V], == in: in place
+  const int32_t* drafts;  // [B, R - 1] or NULL
+  const int32_t* parents; // [B, R - 1] or NULL: a chain
+  const int32_t* state;   // [B, words] or NULL
+  long long P, words;
+  const float *rep, *freq, *pres;  // [B] or NULL
+  int n_bias;
+  const int32_t* bias_tokens;  // [B, n_bias]
+  const float* bias_values;    // [B, n_bias]
+  const uint32_t* mask;        // [B, mask_rows, W] or NULL
+  int mask_rows, W;
+  int B, R, V;
+  int chunks, groups, rows_per;  // the launch: vocabulary chunks, row groups and rows of a group
+  unsigned* status;
+};
+int process_chunk();      // tokens of one CTA's chunk
+int process_tree_rows();  // most rows of a group when the drafts form a tree
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, bool vec, cudaStream_t s);
+
+// The paged key/value cache's append and commit (kv_kernel.cu).
+struct KvAppendArgs {
+  const void *k, *v;    // token stride kv_stride, heads contiguous
+  const void* q;        // token stride q_stride, or NULL
+  void* out_q;          // [B, T, Hq, D]
+  long long kv_stride, q_stride;  // elements
+  const int32_t* parents;     // [B, T - 1] or NULL: a chain
+  const int32_t* n_new;       // [B] or NULL: T
+  const int32_t* lengths;     // [B]
+  const int32_t* page_table;  // [B, max_pages]
+  const unsigned long long* turns;  // [rot / 2]
+  int B, T, Hq, Hkv, D, rot, interleaved;
+  int pages, page_size, max_pages;
+  void *k_cache, *v_cache;    // [pages, page_size, Hkv, D]
+  unsigned* status;
+};
+int kv_max_rot();
+cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, bool vec, cudaStream_t s);
+
+struct KvCommitArgs {
+  void *k_cache, *v_cache;  // [layers] of [pages, page_size, entry_bytes]
+  long long layer_bytes;
+  int layers, pages, page_size, entry_bytes, max_pages;
+  const int32_t *page_table, *lengths, *tokens, *parents, *path, *path_len;
+  int B, N;
+  int32_t* out_nodes;    // [B, N + 1]
+  int32_t* out_lengths;  // [B]
+  unsigned* status;
+};
+cudaError_t launch_kv_commit(const KvCommitArgs& a, int vec_bytes, cudaStream_t s);
+
 // Resident CTAs per SM for each kernel (occupancy calculator).
 int sample_blocks_per_sm(bool bf16, bool vec);
 int greedy_blocks_per_sm(bool bf16, bool vec);

@@ -1,0 +1,428 @@
+"""Token counts and logit processing on the GPU against a plain 64-bit
+implementation.
+
+Tolerance: z * rep, f * c + p and the additions are at most eight fp32
+operations (the reciprocal of rep, its product, f * c, two penalties joined,
+the drafts' share, the biases' sum of up to 3 terms, the last addition), each
+off by at most 2^-24 of the magnitudes it adds: 8 * 2^-24 of their sum.  A bf16
+output adds half a step of the result, 2^-8 of it."""
+import numpy as np
+import pytest
+import torch
+
+import plain_ops
+import speculative_decoding_verification_36_gb300 as sv
+from speculative_decoding_verification_36_gb300 import workloads as wl
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+
+
+def dev(x):
+    return None if x is None else torch.as_tensor(np.ascontiguousarray(x)).to(DEV)
+
+
+def random_parents(rng, B, N, kind):
+    if kind == "chain":
+        return np.tile(np.arange(-1, N - 1, dtype=np.int32), (B, 1))
+    if kind == "star":
+        return np.full((B, N), -1, np.int32)
+    return np.stack([[int(rng.integers(-1, j)) if j else -1 for j in range(N)] for _ in range(B)]).astype(np.int32)
+
+
+def make(rng, B, R, V, dtype, tree=None, hist=40, bias=6, mask="rows", dups=True, alphabet=None):
+    """Inputs as numpy arrays (logits: exactly representable in dtype)."""
+    hi = min(V, alphabet or V)
+    z = torch.from_numpy(rng.normal(0, 4, (B, R, V)).astype(np.float32)).to(dtype)
+    x = dict(logits=z, drafts=None, parents=None, state=None, rep=None, freq=None, pres=None, bias_tokens=None,
+             bias_values=None, mask=None)
+    if R > 1:
+        x["drafts"] = rng.integers(0, hi, (B, R - 1)).astype(np.int32)
+        if tree:
+            x["parents"] = random_parents(rng, B, R - 1, tree)
+    if hist:
+        tok = rng.integers(0, hi, (B, hist)).astype(np.int32)
+        ln = rng.integers(0, hist + 1, B).astype(np.int32)
+        x["state"] = plain_ops.count(tok, ln, (ln * 0.6).astype(np.int32), V)
+    x["rep"] = rng.uniform(0.8, 1.6, B).astype(np.float32)
+    x["freq"] = rng.uniform(-0.5, 1, B).astype(np.float32)
+    x["pres"] = rng.uniform(-0.5, 1, B).astype(np.float32)
+    if bias:
+        x["bias_tokens"] = rng.integers(-1, V, (B, bias)).astype(np.int32)
+        if dups and bias > 2:
+            x["bias_tokens"][:, 1:3] = x["bias_tokens"][:, :1]  # the same token three times
+        x["bias_values"] = rng.normal(0, 3, (B, bias)).astype(np.float32)
+    if mask:
+        W = (V + 31) // 32
+        shape = (B, R, W) if mask == "rows" else (B, W)
+        m = rng.integers(0, 2 ** 32, shape, dtype=np.uint32)
+        if mask == "rows":
+            m[:, ::2] |= rng.integers(0, 2 ** 32, m[:, ::2].shape, dtype=np.uint32)
+            m[0, 0] = 0xffffffff
+            m[-1, -1] = 0  # nothing allowed
+        x["mask"] = m.view(np.int32)
+    return x
+
+
+def call(x, out=None, logits=None, stream=None):
+    return sv.spec_process_logits(
+        x["logits"].to(DEV) if logits is None else logits, draft_tokens=dev(x["drafts"]), parent_idx=dev(x["parents"]),
+        token_state=dev(x["state"]), repetition=dev(x["rep"]), frequency=dev(x["freq"]), presence=dev(x["pres"]),
+        bias_tokens=dev(x["bias_tokens"]), bias_values=dev(x["bias_values"]), allowed_mask=dev(x["mask"]), out=out,
+        stream=stream)
+
+
+def check(x, got):
+    kw = {k: v for k, v in x.items() if k != "logits"}
+    ref, mag = plain_ops.process(x["logits"].double().numpy(), **kw)
+    g = got.cpu().double().numpy()
+    np.testing.assert_array_equal(np.isnan(g), np.isnan(ref))
+    inf = np.isinf(ref)
+    np.testing.assert_array_equal(g[inf], ref[inf])
+    ok = np.isfinite(ref)
+    tol = 8 * 2.0 ** -24 * mag[ok]
+    if x["logits"].dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (np.abs(ref[ok]) + tol)
+    err = np.abs(g[ok] - ref[ok])
+    assert (err <= tol).all(), (err - tol).max()
+
+
+SHAPES = [
+    # B, R, V, dtype, tree, hist
+    (1, 1, 1, torch.float32, None, 3),
+    (2, 3, 7, torch.bfloat16, None, 5),
+    (3, 5, 1000, torch.bfloat16, None, 40),
+    (3, 5, 1000, torch.float32, None, 400),
+    (2, 4, 4096, torch.bfloat16, None, 100),
+    (2, 4, 4097, torch.float32, None, 100),
+    (2, 3, 8200, torch.bfloat16, None, 1000),
+    (1, 9, 32000, torch.float32, None, 512),
+    (5, 2, 12345, torch.bfloat16, None, 300),
+    (2, 7, 1003, torch.float32, "tree", 30),
+    (2, 31, 5000, torch.bfloat16, "tree", 200),
+    (1, 70, 600, torch.bfloat16, "tree", 20),      # more rows than one group of a tree holds
+    (1, 90, 96, torch.float32, "chain", 20),       # a tree that is one long path
+    (2, 40, 50, torch.float32, "star", 20),
+    (1, 256, 200, torch.bfloat16, None, 10),       # the longest chain
+    (70, 2, 40, torch.float32, None, 10),
+]
+
+
+@pytest.mark.parametrize("B,R,V,dtype,tree,hist", SHAPES)
+@pytest.mark.parametrize("mask", [None, "rows", "shared"])
+def test_process_matches_plain(B, R, V, dtype, tree, hist, mask):
+    rng = np.random.default_rng(B * 1000 + R * 10 + V)
+    x = make(rng, B, R, V, dtype, tree, hist, mask=mask)
+    got = call(x)
+    check(x, got)
+    # in place: the same bits
+    z = x["logits"].to(DEV).clone()
+    assert call(x, out=z, logits=z) is z
+    assert torch.equal(z.view(torch.int16 if dtype == torch.bfloat16 else torch.int32),
+                       got.view(torch.int16 if dtype == torch.bfloat16 else torch.int32))
+    assert sv.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("keep", [(), ("state", "rep"), ("state", "freq"), ("state", "pres"), ("drafts", "rep", "pres"),
+                                  ("bias_tokens", "bias_values"), ("mask",), ("state", "drafts", "parents", "rep")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_each_part_alone(keep, dtype):
+    rng = np.random.default_rng(3)
+    x = make(rng, 3, 6, 2056, dtype, "tree", 60)
+    x = {k: v if k in keep or k == "logits" else None for k, v in x.items()}
+    got = call(x)
+    check(x, got)
+    if not keep:
+        assert torch.equal(got.cpu().view(torch.uint8), x["logits"].view(torch.uint8))
+    assert sv.spec_get_status() == 0
+
+
+def test_largest_tree_many_equal_tokens():
+    rng = np.random.default_rng(8)
+    x = make(rng, 1, 1025, 50, torch.float32, "tree", 30, mask=None, alphabet=7)
+    check(x, call(x))
+
+
+def test_extreme_values_and_masks():
+    rng = np.random.default_rng(5)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = make(rng, 2, 4, 300, dtype, None, 50)
+        low = torch.finfo(dtype).min
+        x["logits"][0, :, ::7] = float("-inf")
+        x["logits"][0, :, 1::11] = low
+        x["logits"][1, :, 2::13] = torch.finfo(dtype).max / 4
+        x["mask"][1] = 0  # a sequence whose mask leaves nothing, and NaN and infinities under it
+        x["logits"][1, 0, ::3] = float("nan")
+        x["logits"][1, 1, ::3] = float("inf")
+        x["bias_values"][0, 3] = float("-inf")
+        x["rep"][0] = 1.0  # the lowest value times a factor would overflow
+        x["freq"][:] = np.abs(x["freq"])
+        got = call(x)
+        check(x, got)
+        assert bool((got[1] == float("-inf")).all())
+        # what a verify says of rows with nothing left
+        tok, n = sv.spec_verify(got.float().contiguous(), got[:, :3].float().contiguous(), dev(x["drafts"]), 1.0, 0)
+        assert int(n[1]) == -1
+        assert sv.spec_get_status() == sv.SPEC_FLAG_BAD_DATA
+
+
+def test_nan_allowed_reaches_the_verify():
+    z = torch.zeros((2, 2, 64), device=DEV)
+    z[0, 1, 5] = float("nan")
+    out = sv.spec_process_logits(z)
+    assert bool(torch.isnan(out[0, 1, 5])) and int(torch.isnan(out).sum()) == 1
+    _, n = sv.spec_verify(out, None, torch.zeros((2, 1), dtype=torch.int32, device=DEV), 0.0, 0)
+    assert n.tolist()[0] == -1 and n.tolist()[1] >= 0
+    sv.spec_get_status()
+
+
+@pytest.mark.parametrize("what,value", [("rep", 0.0), ("rep", -1.0), ("rep", np.nan), ("rep", np.inf), ("freq", np.nan),
+                                        ("pres", np.inf), ("parent", 5), ("parent", -2)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_bad_data_makes_the_sequence_nan(what, value, in_place):
+    rng = np.random.default_rng(9)
+    x = make(rng, 3, 6, 5000, torch.bfloat16, "tree", 30)
+    if what == "parent":
+        x["parents"][1, 2] = value
+    else:
+        x[what][1] = value
+    z = x["logits"].to(DEV)
+    got = call(x, logits=z, out=z if in_place else None)
+    check(x, got)
+    assert bool(torch.isnan(got[1].float()).all())
+    assert sv.spec_get_status() == sv.SPEC_FLAG_BAD_DATA
+
+
+def test_drafts_outside_the_vocabulary_count_for_nothing():
+    rng = np.random.default_rng(10)
+    x = make(rng, 2, 6, 100, torch.float32, None, 20)
+    x["drafts"][0, 1:] = -1
+    x["drafts"][1, 2] = 100
+    x["drafts"][1, 3] = 2 ** 31 - 1
+    check(x, call(x))
+    assert sv.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift_in,shift_out", [(0, 1), (1, 0), (1, 1), (3, 5), (4, 4), (2, 6)])
+@pytest.mark.parametrize("V", [777, 4104])
+def test_unaligned_buffers_and_guards(dtype, shift_in, shift_out, V):
+    rng = np.random.default_rng(11)
+    x = make(rng, 2, 3, V, dtype, None, 50)
+    n = 2 * 3 * V
+    src = torch.zeros(n + 16, dtype=dtype, device=DEV)
+    z = src[shift_in:shift_in + n].view(2, 3, V)
+    z.copy_(x["logits"])
+    buf = torch.full((n + 16,), 77.0, dtype=dtype, device=DEV)
+    out = buf[shift_out:shift_out + n].view(2, 3, V)
+    check(x, call(x, logits=z, out=out))
+    assert bool((buf[:shift_out] == 77).all()) and bool((buf[shift_out + n:] == 77).all())
+    keep = (src[:shift_in].clone(), src[shift_in + n:].clone())
+    call(x, logits=z, out=z)
+    assert torch.equal(z, out)
+    assert torch.equal(src[:shift_in], keep[0]) and torch.equal(src[shift_in + n:], keep[1])
+
+
+def test_overlapping_output_is_refused():
+    buf = torch.zeros(2 * 64 + 8, device=DEV)
+    with pytest.raises(sv.SpecError):
+        sv.spec_process_logits(buf[:128].view(1, 2, 64), out=buf[8:].view(1, 2, 64))
+
+
+def test_binding_refuses():
+    z = torch.zeros((2, 3, 64), device=DEV)
+    i = torch.zeros((2, 2), dtype=torch.int32, device=DEV)
+    for kw in (dict(draft_tokens=i[:, :1].contiguous()), dict(parent_idx=i), dict(draft_tokens=i.long()),
+               dict(token_state=i), dict(repetition=torch.ones(3, device=DEV)), dict(frequency=torch.ones(2)),
+               dict(bias_tokens=i), dict(bias_tokens=i, bias_values=torch.zeros((2, 3), device=DEV)),
+               dict(allowed_mask=torch.zeros((2, 3, 1), dtype=torch.int32, device=DEV)),
+               dict(out=z[:, :2]), dict(out=z.to(torch.bfloat16))):
+        with pytest.raises((ValueError, TypeError)):
+            sv.spec_process_logits(z, **kw)
+    with pytest.raises(ValueError):
+        sv.spec_process_logits(z.transpose(0, 1))
+    with pytest.raises(TypeError):
+        sv.spec_process_logits(z.half())
+
+
+# ---------------------------------------------------------------------------
+# counts
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("B,S,V", [(1, 1, 1), (3, 17, 5), (4, 300, 33), (2, 5000, 1000), (7, 64, 128256), (1, 70000, 40),
+                                   (1, 20000, 100001), (2, 0, 9)])
+def test_counts_match_plain(B, S, V):
+    rng = np.random.default_rng(B + S + V)
+    tok = rng.integers(-1, V + 1, (B, S)).astype(np.int32)  # some just outside
+    ln = rng.integers(0, S + 1, B).astype(np.int32)
+    pl = (ln * rng.uniform(0, 1, B)).astype(np.int32)
+    state = sv.spec_token_state(B, V, DEV)
+    state.fill_(-1)
+    got = sv.spec_count_tokens(state, dev(tok).reshape(B, S), V, lengths=dev(ln), prompt_lengths=dev(pl), reset=True)
+    assert got is state
+    ref = plain_ops.count(tok, ln, pl, V)
+    np.testing.assert_array_equal(state.cpu().numpy(), ref)
+    # added to, as a verify's padded output is
+    more = rng.integers(-1, V, (B, 6)).astype(np.int32)
+    sv.spec_count_tokens(state, dev(more), V)
+    np.testing.assert_array_equal(state.cpu().numpy(), plain_ops.count(more, None, None, V, start=ref))
+    assert sv.spec_get_status() == 0
+
+
+def test_counts_bad_lengths_leave_the_row():
+    V = 50
+    tok = np.arange(24, dtype=np.int32).reshape(4, 6)
+    ln, pl = np.array([6, 7, -1, 3], np.int32), np.array([2, 0, 0, 4], np.int32)
+    state = sv.spec_token_state(4, V, DEV)
+    sv.spec_count_tokens(state, dev(tok), V, lengths=dev(ln), prompt_lengths=dev(pl))
+    np.testing.assert_array_equal(state.cpu().numpy(), plain_ops.count(tok, ln, pl, V))
+    assert bool((state[1:] == 0).all())
+    assert sv.spec_get_status() == sv.SPEC_FLAG_BAD_DATA
+
+
+def test_one_row_of_a_state_is_replaced():
+    rng = np.random.default_rng(12)
+    V, tok = 777, rng.integers(0, 777, (3, 50)).astype(np.int32)
+    state = sv.spec_token_state(3, V, DEV)
+    sv.spec_count_tokens(state, dev(tok), V)
+    new = rng.integers(0, V, (1, 20)).astype(np.int32)
+    sv.spec_count_tokens(state[1:2], dev(new), V, prompt_lengths=dev(np.array([20], np.int32)), reset=True)
+    ref = plain_ops.count(tok, None, None, V)
+    ref[1:2] = plain_ops.count(new, None, np.array([20]), V)
+    np.testing.assert_array_equal(state.cpu().numpy(), ref)
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, the loop
+# ---------------------------------------------------------------------------
+def test_two_streams_at_once_match_the_calls_alone():
+    rng = np.random.default_rng(13)
+    xs = [make(rng, 8, 5, 32000, torch.bfloat16, None, 500), make(rng, 4, 9, 20001, torch.float32, "tree", 300)]
+    alone = [call(x) for x in xs]
+    ins = [x["logits"].to(DEV) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        outs = []
+        for x, z, s in zip(xs, ins, streams):
+            with torch.cuda.stream(s):
+                outs.append(call(x, logits=z))
+        torch.cuda.synchronize()
+        for o, a in zip(outs, alone):
+            assert torch.equal(o.nan_to_num(7.0), a.nan_to_num(7.0))
+
+
+def test_captured_step_replays_on_new_data():
+    """Processing, a greedy verify and the counting of its answer in one graph."""
+    rng = np.random.default_rng(14)
+    B, K, V = 4, 3, 5000
+    x = make(rng, B, K + 1, V, torch.bfloat16, None, 100, mask="rows")
+    x["mask"] |= 1  # every row keeps a token
+    z, d = x["logits"].to(DEV), dev(x["drafts"])
+    start = dev(x["state"])
+    state = start.clone()
+    pen = [dev(x[k]) for k in ("rep", "freq", "pres")]
+    bt, bv, mask = dev(x["bias_tokens"]), dev(x["bias_values"]), dev(x["mask"])
+    out = torch.empty_like(z)
+    tok = torch.empty((B, K + 1), dtype=torch.int32, device=DEV)
+    n = torch.empty((B,), dtype=torch.int32, device=DEV)
+
+    def step():
+        sv.spec_process_logits(z, d, None, state, *pen, bias_tokens=bt, bias_values=bv, allowed_mask=mask, out=out)
+        sv.spec_verify(out, None, d, 0.0, 0, out_tokens=tok, out_n_accepted=n)
+        sv.spec_count_tokens(state, tok, V)
+
+    step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step()
+    state.copy_(start)
+    for rep in range(3):
+        z.copy_(torch.randn(z.shape, device=DEV) * 4)
+        before = state.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        got = (out.clone(), tok.clone(), n.clone(), state.clone())
+        state.copy_(before)
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (out, tok, n, state)):
+            assert torch.equal(a, b)
+        assert not torch.equal(before, state)
+    assert sv.spec_get_status() == 0
+
+
+def test_decode_loop_follows_a_plain_one():
+    """N-gram drafts, processed rows, a greedy verify and the counts over
+    several steps, against the same loop in numpy: tokens have to agree."""
+    rng = np.random.default_rng(15)
+    B, K, V, steps, room = 3, 4, 600, 6, 200
+    hist = np.full((B, room), -7, np.int32)
+    length = np.array([30, 41, 25])
+    for b in range(B):
+        hist[b, :length[b]] = np.tile(rng.integers(0, 40, 9), 6)[:length[b]]
+    prompt = length.copy()
+    rep, freq, pres = (np.array(v, np.float32) for v in ([1.2, 1.0, 1.5], [0.1, 0.3, 0.0], [0.2, 0.0, 0.4]))
+    state = sv.spec_token_state(B, V, DEV)
+    sv.spec_count_tokens(state, dev(hist), V, lengths=dev(length.astype(np.int32)), prompt_lengths=dev(prompt.astype(np.int32)),
+                         reset=True)
+    for step in range(steps):
+        drafts, nd, _ = sv.spec_ngram_draft(dev(hist), dev(length.astype(np.int32)), 1, 4, K)
+        d = drafts.clamp(min=0)  # a padded draft is some token: the verify judges it
+        z = torch.randn((B, K + 1, V), generator=torch.Generator().manual_seed(step)) * 3
+        for b in range(B):  # the model tends to go on with the drafts
+            for i in range(K):
+                z[b, i, int(d[b, i])] += 14
+        mask = torch.from_numpy(rng.integers(0, 2 ** 32, (B, K + 1, (V + 31) // 32), dtype=np.uint32).view(np.int32)) | 0x55555555
+        kw = dict(drafts=d.cpu().numpy(), state=state.cpu().numpy(), rep=rep, freq=freq, pres=pres, mask=mask.numpy())
+        ref, _ = plain_ops.process(z.double().numpy(), **kw)
+        out = sv.spec_process_logits(z.to(DEV), d, None, state, dev(rep), dev(freq), dev(pres), allowed_mask=mask.to(DEV))
+        tok, n = sv.spec_verify(out, None, d, 0.0, 0)
+        sv.spec_count_tokens(state, tok, V)
+        tok, n = tok.cpu().numpy(), n.cpu().numpy()
+        for b in range(B):
+            want = []
+            for i in range(K + 1):
+                want.append(int(ref[b, i].argmax()))
+                if i == K or want[-1] != int(d[b, i]):
+                    break
+            assert tok[b, :n[b] + 1].tolist() == want, (step, b)
+            hist[b, length[b]:length[b] + len(want)] = want
+            length[b] += len(want)
+    ref = plain_ops.count(hist, length, prompt, V)
+    np.testing.assert_array_equal(state.cpu().numpy(), ref)
+    assert (length - prompt).sum() > steps * B  # drafts were accepted
+
+
+def test_other_stream_argument():
+    rng = np.random.default_rng(16)
+    x = make(rng, 2, 3, 4000, torch.float32)
+    s = torch.cuda.Stream()
+    z = x["logits"].to(DEV)
+    torch.cuda.synchronize()
+    got = call(x, logits=z, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    check(x, got)
+
+
+def test_workload_shapes_sampled():
+    """The largest batch's shape, rows drawn at random against the plain form."""
+    p = wl.preset("c3", B=24)
+    rng = np.random.default_rng(17)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    z = (torch.randn((p.B, p.K + 1, p.V), generator=g, device=DEV) * 4).to(torch.bfloat16)
+    x = make(rng, p.B, p.K + 1, 64, torch.bfloat16, None, 0, bias=0, mask=None)  # the scalars
+    tok = rng.integers(0, p.V, (p.B, 4000)).astype(np.int32)
+    tok[:, ::2] //= 200
+    ln = rng.integers(2000, 4001, p.B).astype(np.int32)
+    x["state"] = plain_ops.count(tok, ln, (ln // 2).astype(np.int32), p.V)
+    x["drafts"] = tok[:, :p.K].copy()
+    x["mask"] = rng.integers(0, 2 ** 32, (p.B, p.K + 1, p.V // 32), dtype=np.uint32).view(np.int32)
+    got = call(x, logits=z)
+    for b in (0, 7, p.B - 1):
+        sub = {k: v[b:b + 1] if v is not None else None for k, v in x.items()}
+        sub["logits"] = z[b:b + 1].cpu()
+        check(sub, got[b:b + 1])

@@ -1,0 +1,118 @@
+"""Refusals of the logit-processing, token-count and paged-cache entry points
+that need no GPU: bad arguments are turned down on the host before any CUDA
+call."""
+import pytest
+import torch
+
+import speculative_decoding_verification_36_gb300 as sv
+from speculative_decoding_verification_36_gb300 import _lib, build
+import plain_ops
+
+FAKE = 0x100000  # never dereferenced
+FAR = 0x900000000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def test_state_words(lib):
+    for V in (1, 31, 32, 33, 127, 128, 129, 32000, 128256, 152064, 96001):
+        assert lib.spec_token_state_words(V) == plain_ops.state_words(V)[1]
+        assert lib.spec_token_state_words(V) % 4 == 0
+    for V in (0, -1, 2 ** 30 + 1):
+        assert lib.spec_token_state_words(V) == _lib.SPEC_ERR_SHAPE
+    assert lib.spec_token_state_words(2 ** 30) > 0
+
+
+def test_count_checks(lib):
+    def call(tok=FAKE, ln=None, pl=None, B=2, S=4, V=10, st=FAKE):
+        return lib.spec_count_tokens(tok, ln, pl, B, S, V, 0, st, None)
+
+    assert call(tok=None) == _lib.SPEC_ERR_NULL
+    assert call(st=None) == _lib.SPEC_ERR_NULL
+    for bad in (dict(B=-1), dict(S=-1), dict(V=0), dict(V=2 ** 30 + 1)):
+        assert call(**bad) == _lib.SPEC_ERR_SHAPE
+    assert call(B=0, tok=None, st=None) == _lib.SPEC_OK
+
+
+@pytest.mark.parametrize("fn", ["spec_process_logits_f32", "spec_process_logits_bf16"])
+def test_process_checks(lib, fn):
+    f = getattr(lib, fn)
+
+    def call(z=FAKE, d=FAKE, p=None, n_bias=0, bt=None, bv=None, mask=None, rows=0, B=2, R=3, V=16, out=FAKE):
+        return f(z, d, p, None, None, None, None, n_bias, bt, bv, mask, rows, B, R, V, out, None)
+
+    assert call(z=None) == _lib.SPEC_ERR_NULL
+    assert call(out=None) == _lib.SPEC_ERR_NULL
+    assert call(d=None, p=FAKE) == _lib.SPEC_ERR_NULL
+    assert call(n_bias=1, bt=FAKE) == _lib.SPEC_ERR_NULL
+    assert call(n_bias=1, bv=FAKE) == _lib.SPEC_ERR_NULL
+    for bad in (dict(B=-1), dict(R=0), dict(R=1026), dict(V=0), dict(V=2 ** 30 + 1), dict(n_bias=-1),
+                dict(mask=FAKE, rows=0), dict(mask=FAKE, rows=2), dict(B=2 ** 30, R=1025, V=2 ** 30)):
+        assert call(**bad) == _lib.SPEC_ERR_SHAPE, bad
+    assert call(B=0, z=None, out=None) == _lib.SPEC_OK
+    # 2 * 3 * 16 values: an output that starts inside the input, or ends in it
+    size = 2 * 3 * 16 * (4 if fn.endswith("f32") else 2)
+    assert call(out=FAKE + 16) == _lib.SPEC_ERR_OVERLAP
+    assert call(out=FAKE + size - 1) == _lib.SPEC_ERR_OVERLAP
+    assert call(out=FAKE - 16) == _lib.SPEC_ERR_OVERLAP
+
+
+@pytest.mark.parametrize("fn", ["spec_kv_append_f32", "spec_kv_append_bf16"])
+def test_append_checks(lib, fn):
+    f = getattr(lib, fn)
+
+    def call(k=FAKE, v=FAKE, ks=32, q=None, qs=0, oq=None, par=None, ln=FAKE, tab=FAKE, B=2, T=3, Hq=0, Hkv=2, D=16,
+             rot=16, turns=FAKE, kc=FAR, vc=FAR, pages=4, ps=16, mp=2):
+        return f(k, v, ks, q, qs, oq, par, None, ln, tab, B, T, Hq, Hkv, D, rot, 0, turns, kc, vc, pages, ps, mp, None)
+
+    for name in ("k", "v", "ln", "tab", "kc", "vc", "turns"):
+        assert call(**{name: None}) == _lib.SPEC_ERR_NULL, name
+    assert call(Hq=2, qs=32, q=FAKE) == _lib.SPEC_ERR_NULL
+    assert call(Hq=2, qs=32, oq=FAKE) == _lib.SPEC_ERR_NULL
+    for bad in (dict(B=-1), dict(T=-1), dict(Hq=-1), dict(Hkv=0), dict(D=0), dict(D=1025), dict(rot=-2), dict(rot=3),
+                dict(rot=18), dict(pages=0), dict(ps=0), dict(mp=0), dict(ks=31), dict(Hq=2, qs=31, q=FAKE, oq=FAKE),
+                dict(par=FAKE, T=1026), dict(B=2 ** 20, T=2 ** 20)):
+        assert call(**bad) == _lib.SPEC_ERR_SHAPE, bad
+    assert call(B=0) == _lib.SPEC_OK
+    assert call(T=0) == _lib.SPEC_OK
+
+
+def test_commit_checks(lib):
+    def call(kc=FAKE, vc=FAKE, layers=1, lb=4 * 16 * 64, pages=4, ps=16, eb=64, tab=FAR, mp=2, ln=FAR, tok=FAR, par=FAR,
+             path=FAR, plen=FAR, B=2, N=3, nodes=FAR, oln=FAR + 4096):
+        return lib.spec_kv_commit(kc, vc, layers, lb, pages, ps, eb, tab, mp, ln, tok, par, path, plen, B, N, nodes, oln,
+                                  None)
+
+    for name in ("kc", "vc", "tab", "ln", "tok", "par", "path", "plen", "nodes", "oln"):
+        assert call(**{name: None}) == _lib.SPEC_ERR_NULL, name
+    for bad in (dict(B=-1), dict(N=-1), dict(N=1025), dict(layers=0), dict(layers=32768), dict(pages=0), dict(ps=0),
+                dict(eb=0), dict(mp=0), dict(lb=4 * 16 * 64 - 1)):
+        assert call(**bad) == _lib.SPEC_ERR_SHAPE, bad
+    assert call(oln=FAR) == _lib.SPEC_ERR_OVERLAP
+    assert call(oln=FAR + 4) == _lib.SPEC_ERR_OVERLAP
+    assert call(B=0) == _lib.SPEC_OK
+
+
+def test_binding_refuses_host_tensors(lib):
+    i = torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        sv.spec_count_tokens(i, i, 10)
+    with pytest.raises(ValueError):
+        sv.spec_process_logits(torch.zeros(2, 3, 8))
+    with pytest.raises(ValueError):
+        sv.spec_kv_append(torch.zeros(1, 2, 1, 4), torch.zeros(1, 2, 1, 4), None, None, i, i)
+    with pytest.raises(ValueError):
+        sv.spec_kv_commit(torch.zeros(1, 2, 1, 4), torch.zeros(1, 2, 1, 4), i, i, i, i, i, i)
+    with pytest.raises(sv.SpecError):
+        sv.spec_token_state(1, 0, "cpu")
+
+
+def test_rope_turns():
+    import math
+    t = sv.spec_rope_turns([2 * math.pi / 4, 2 * math.pi * 0.75, 0.0, 2 * math.pi], "cpu")
+    assert t.dtype == torch.int64
+    assert [int(x) % 2 ** 64 for x in t] == [2 ** 62, 3 * 2 ** 62, 0, 0]
