@@ -24,6 +24,8 @@ library's CUDA kernels.  There is no CPU fallback.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _lib
@@ -353,21 +355,46 @@ def spec_ngram_draft(tokens, lengths, n_min: int, n_max: int, K: int, out_drafts
     return drafts, n_drafts, match_len
 
 
+# The entry points below are called once or more a layer, where a few
+# microseconds of checking are a large part of the call: one pass over each
+# tensor's properties, and a message only once something is wrong.
+def _arg(t, dtype, shape, device, name):
+    """The address of a contiguous CUDA tensor of this type, shape and device
+    (None for None and for an empty one)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr() or None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _same_device(t, device, name)
+    raise ValueError(f"{name} cannot be used")
+
+
+def _invoke(fn, device, stream, *args):
+    """Calls a C entry point on `device`, its current stream by default."""
+    if torch.cuda.current_device() == device.index:
+        _lib.check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _lib.check(fn(*args, _stream(stream)))
+
+
+def _words(V: int) -> int:
+    """spec_token_state_words(V), worked out here (the layout is the header's)."""
+    if not 1 <= V <= 2 ** 30:
+        _lib.check(_lib.SPEC_ERR_SHAPE)
+    P = (V + 31) // 32
+    return 32 * P + (P + 3) // 4 * 4
+
+
 def spec_token_state(B: int, V: int, device) -> torch.Tensor:
     """An empty token-count state: int32 [B, words] zeros (spec_count_tokens
     fills it, spec_process_logits reads it; the layout is in specverify.h).
     One row of it, state[b:b+1], is a state too."""
-    words = _lib.load().spec_token_state_words(int(V))
-    if words < 0:
-        _lib.check(words)
-    return torch.zeros((B, words), dtype=torch.int32, device=device)
-
-
-def _state(t, B, V, device):
-    words = _lib.load().spec_token_state_words(int(V))
-    if words < 0:
-        _lib.check(words)
-    return _i32(t, (B, words), "token_state", device)
+    return torch.zeros((B, _words(int(V))), dtype=torch.int32, device=device)
 
 
 def spec_count_tokens(state, tokens, V: int, lengths=None, prompt_lengths=None, reset: bool = False, stream=None):
@@ -377,29 +404,14 @@ def spec_count_tokens(state, tokens, V: int, lengths=None, prompt_lengths=None, 
     prompt_lengths[b] of them as prompt (None: none), the rest as output.
     Tokens outside [0, V) are skipped: a verify's padded out_tokens or
     out_path can be passed.  reset=True empties the state first."""
-    if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
-        raise ValueError("tokens must be [B, S]")
+    if not isinstance(tokens, torch.Tensor) or not tokens.is_cuda or tokens.dim() != 2:
+        raise ValueError("tokens must be a CUDA tensor [B, S]")
     B, S = tokens.shape
-    _i32(tokens, (B, S), "tokens")
-    dev = tokens.device
-    _state(state, B, V, dev)
-    if lengths is not None:
-        _i32(lengths, (B,), "lengths", dev)
-    if prompt_lengths is not None:
-        _i32(prompt_lengths, (B,), "prompt_lengths", dev)
-    with torch.cuda.device(dev):
-        _lib.check(_lib.load().spec_count_tokens(_ptr(tokens), _ptr(lengths), _ptr(prompt_lengths), B, S, int(V),
-                                                 1 if reset else 0, _ptr(state), _stream(stream)))
+    dev, i32, V = tokens.device, torch.int32, int(V)
+    _invoke(_lib.load().spec_count_tokens, dev, stream, _arg(tokens, i32, (B, S), dev, "tokens"),
+            _arg(lengths, i32, (B,), dev, "lengths"), _arg(prompt_lengths, i32, (B,), dev, "prompt_lengths"), B, S, V,
+            1 if reset else 0, _arg(state, i32, (B, _words(V)), dev, "state"))
     return state
-
-
-def _f32(t, shape, name, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    _same_device(t, device, name)
-    return t
 
 
 def spec_process_logits(logits, draft_tokens=None, parent_idx=None, token_state=None, repetition=None,
@@ -419,39 +431,31 @@ def spec_process_logits(logits, draft_tokens=None, parent_idx=None, token_state=
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")
     B, R, V = logits.shape
-    dev = logits.device
-    if draft_tokens is not None:
-        _i32(draft_tokens, (B, R - 1), "draft_tokens", dev)
-    if parent_idx is not None:
-        if draft_tokens is None:
-            raise ValueError("parent_idx needs draft_tokens")
-        _i32(parent_idx, (B, R - 1), "parent_idx", dev)
-    if token_state is not None:
-        _state(token_state, B, V, dev)
-    for t, name in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence")):
-        if t is not None:
-            _f32(t, (B,), name, dev)
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    if parent_idx is not None and draft_tokens is None:
+        raise ValueError("parent_idx needs draft_tokens")
     if (bias_tokens is None) != (bias_values is None):
         raise ValueError("bias_tokens and bias_values go together")
-    n_bias = 0
+    n_bias = mask_rows = 0
     if bias_tokens is not None:
         if bias_tokens.dim() != 2:
             raise ValueError("bias_tokens must be [B, n]")
         n_bias = bias_tokens.shape[1]
-        _i32(bias_tokens, (B, n_bias), "bias_tokens", dev)
-        _f32(bias_values, (B, n_bias), "bias_values", dev)
-    mask_rows = 0
+    mask = None
     if allowed_mask is not None:
         W = (V + 31) // 32
         mask_rows = 1 if allowed_mask.dim() == 2 else R
-        _i32(allowed_mask, (B, W) if allowed_mask.dim() == 2 else (B, R, W), "allowed_mask", dev)
-    out = _out(out, (B, R, V), logits.dtype, dev, "out")
+        mask = _arg(allowed_mask, i32, (B, W) if allowed_mask.dim() == 2 else (B, R, W), dev, "allowed_mask")
+    state = None if token_state is None else _arg(token_state, i32, (B, _words(V)), dev, "token_state")
+    if out is None:
+        out = torch.empty_like(logits)
     lib = _lib.load()
-    fn = lib.spec_process_logits_bf16 if bf16 else lib.spec_process_logits_f32
-    with torch.cuda.device(dev):
-        _lib.check(fn(_ptr(logits), _ptr(draft_tokens), _ptr(parent_idx), _ptr(token_state), _ptr(repetition),
-                      _ptr(frequency), _ptr(presence), n_bias, _ptr(bias_tokens), _ptr(bias_values),
-                      _ptr(allowed_mask), mask_rows, B, R, V, _ptr(out), _stream(stream)))
+    _invoke(lib.spec_process_logits_bf16 if bf16 else lib.spec_process_logits_f32, dev, stream, _ptr(logits),
+            _arg(draft_tokens, i32, (B, R - 1), dev, "draft_tokens"), _arg(parent_idx, i32, (B, R - 1), dev, "parent_idx"),
+            state, _arg(repetition, f32, (B,), dev, "repetition"), _arg(frequency, f32, (B,), dev, "frequency"),
+            _arg(presence, f32, (B,), dev, "presence"), n_bias, _arg(bias_tokens, i32, (B, n_bias), dev, "bias_tokens"),
+            _arg(bias_values, f32, (B, n_bias), dev, "bias_values"), mask, mask_rows, B, R, V,
+            _arg(out, logits.dtype, (B, R, V), dev, "out"))
     return out
 
 
@@ -459,28 +463,29 @@ def spec_rope_turns(inv_freq, device) -> torch.Tensor:
     """Rotary frequencies (radians a position, float64-able: theta ** (-2 i /
     rot_dim) or any scaled set) as spec_kv_append takes them: int64 [rot_dim /
     2] holding 2^-64 fractions of a turn (the bits are unsigned)."""
-    import math
     vals = [int(round(float(f) / (2 * math.pi) * 2.0 ** 64)) % 2 ** 64 for f in inv_freq]
     return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in vals], dtype=torch.int64, device=device)
 
 
-def _tokens_view(t, name, dtype, B, T, D, device):
-    """(heads, token stride) of a [B, T, H, D] tensor whose tokens lie at equal
-    distances and whose heads are contiguous (a slice of a joint projection)."""
+def _token_stride(t, name, dtype, shape, device):
+    """Elements between successive tokens of a [B, T, H, D] tensor whose tokens
+    lie at equal distances and whose heads are contiguous (such as a slice of a
+    joint projection)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
         raise ValueError(f"{name} must be a {dtype} CUDA tensor")
-    _same_device(t, device, name)
-    if t.dim() != 4 or tuple(t.shape[:2]) != (B, T) or t.shape[3] != D:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, T, 'H', D)}")
-    H = t.shape[2]
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        _same_device(t, device, name)
+    B, T, H, D = shape
     sb, st, sh, sd = t.stride()
-    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}'s heads must be contiguous")
     if T == 1:
-        st = sb if B > 1 else max(H * D, 1)
-    elif B > 1 and sb != T * st:
+        return sb if B > 1 else max(H * D, 1)
+    if sb != T * st and B > 1:
         raise ValueError(f"{name}'s tokens must lie at equal distances")
-    return H, st
+    return st
 
 
 def spec_kv_append(k, v, key_cache, value_cache, page_table, lengths, turns=None, q=None, parent_idx=None,
@@ -494,52 +499,45 @@ def spec_kv_append(k, v, key_cache, value_cache, page_table, lengths, turns=None
     lengths[b] + its depth.  turns (spec_rope_turns): None rotates nothing.
     n_new [B]: tokens from there on are padding.  k, v and q may be slices of
     a joint projection.  Returns out_q (None without q)."""
-    bf16 = isinstance(k, torch.Tensor) and k.dtype == torch.bfloat16
     if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 4:
         raise ValueError("k must be a CUDA tensor [B, T, Hkv, D]")
-    if k.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"k must be float32 or bfloat16, got {k.dtype}")
-    B, T, _, D = k.shape
-    dev = k.device
-    Hkv, ks = _tokens_view(k, "k", k.dtype, B, T, D, dev)
-    Hv, vs = _tokens_view(v, "v", k.dtype, B, T, D, dev)
-    if Hv != Hkv or vs != ks:
-        raise ValueError("k and v must share heads and token stride")
-    for c, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
-        if (not isinstance(c, torch.Tensor) or c.dtype != k.dtype or c.dim() != 4 or not c.is_contiguous()
-                or tuple(c.shape[2:]) != (Hkv, D)):
-            raise ValueError(f"{name} must be a contiguous {k.dtype} tensor [pages, page_size, {Hkv}, {D}]")
-        _same_device(c, dev, name)
-    if key_cache.shape != value_cache.shape:
-        raise ValueError("key_cache and value_cache must have the same shape")
+    dt, dev, i32 = k.dtype, k.device, torch.int32
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError(f"k must be float32 or bfloat16, got {dt}")
+    shape = k.shape
+    B, T, Hkv, D = shape
+    ks = _token_stride(k, "k", dt, shape, dev)
+    if _token_stride(v, "v", dt, shape, dev) != ks:
+        raise ValueError("k and v must share a token stride")
+    if not isinstance(key_cache, torch.Tensor) or key_cache.dim() != 4:
+        raise ValueError("key_cache must be [pages, page_size, Hkv, D]")
     pages, page_size = key_cache.shape[:2]
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     max_pages = page_table.shape[1]
-    _i32(page_table, (B, max_pages), "page_table", dev)
-    _i32(lengths, (B,), "lengths", dev)
-    if parent_idx is not None:
-        _i32(parent_idx, (B, T - 1), "parent_idx", dev)
-    if n_new is not None:
-        _i32(n_new, (B,), "n_new", dev)
     rot = 0
     if turns is not None:
-        if not isinstance(turns, torch.Tensor) or turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
-            raise ValueError("turns must be a contiguous int64 tensor [rot_dim / 2]")
-        _same_device(turns, dev, "turns")
-        rot = 2 * turns.shape[0]
+        rot = 2 * turns.numel()
+    qp = oq = None
     Hq = qs = 0
     if q is not None:
-        Hq, qs = _tokens_view(q, "q", k.dtype, B, T, D, dev)
-        out_q = _out(out_q, (B, T, Hq, D), k.dtype, dev, "out_q")
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be a CUDA tensor [B, T, Hq, D]")
+        Hq = q.shape[2]
+        qs = _token_stride(q, "q", dt, (B, T, Hq, D), dev)
+        if out_q is None:
+            out_q = torch.empty((B, T, Hq, D), dtype=dt, device=dev)
+        qp, oq = q.data_ptr(), _arg(out_q, dt, (B, T, Hq, D), dev, "out_q")
     elif out_q is not None:
         raise ValueError("out_q needs q")
+    cache = (pages, page_size, Hkv, D)
     lib = _lib.load()
-    fn = lib.spec_kv_append_bf16 if bf16 else lib.spec_kv_append_f32
-    with torch.cuda.device(dev):
-        _lib.check(fn(_ptr(k), _ptr(v), ks, _ptr(q), qs, _ptr(out_q), _ptr(parent_idx), _ptr(n_new), _ptr(lengths),
-                      _ptr(page_table), B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, _ptr(turns),
-                      _ptr(key_cache), _ptr(value_cache), pages, page_size, max_pages, _stream(stream)))
+    _invoke(lib.spec_kv_append_bf16 if dt is torch.bfloat16 else lib.spec_kv_append_f32, dev, stream, k.data_ptr(),
+            v.data_ptr(), ks, qp, qs, oq, _arg(parent_idx, i32, (B, T - 1), dev, "parent_idx"),
+            _arg(n_new, i32, (B,), dev, "n_new"), _arg(lengths, i32, (B,), dev, "lengths"),
+            _arg(page_table, i32, (B, max_pages), dev, "page_table"), B, T, Hq, Hkv, D, rot, 1 if interleaved else 0,
+            _arg(turns, torch.int64, (rot // 2,), dev, "turns"), _arg(key_cache, dt, cache, dev, "key_cache"),
+            _arg(value_cache, dt, cache, dev, "value_cache"), pages, page_size, max_pages)
     return out_q
 
 
@@ -548,21 +546,16 @@ def spec_kv_commit(key_cache, value_cache, page_table, lengths, tree_tokens, par
     """Keeps a tree verify's accepted path in the paged cache: its nodes'
     entries move to the slots behind the root's.
 
-    key_cache, value_cache: [pages, page_size, ...] or, with all layers in one
-    tensor, [layers, pages, page_size, ...] (five dimensions), any type.
-    lengths as given to spec_kv_append for the step; out_path, out_len: the
-    verify's.  Returns (nodes [B, N+1] int32, -1 padded; new lengths [B])."""
+    key_cache, value_cache: [pages, page_size, H, D] or, with all layers in one
+    tensor, [layers, pages, page_size, H, D], any type.  lengths as given to
+    spec_kv_append for the step; out_path, out_len: the verify's.  Returns
+    (nodes [B, N+1] int32, -1 padded; new lengths [B])."""
     if not isinstance(key_cache, torch.Tensor) or not key_cache.is_cuda or key_cache.dim() not in (4, 5):
         raise ValueError("key_cache must be a CUDA tensor [(layers,) pages, page_size, H, D]")
-    dev = key_cache.device
-    if (not isinstance(value_cache, torch.Tensor) or value_cache.shape != key_cache.shape
-            or value_cache.dtype != key_cache.dtype):
-        raise ValueError("value_cache must be like key_cache")
-    _same_device(value_cache, dev, "value_cache")
-    if not key_cache.is_contiguous() or not value_cache.is_contiguous():
-        raise ValueError("the caches must be contiguous")
-    shape = tuple(key_cache.shape)
-    layers, (pages, page_size, H, D) = (shape[0], shape[1:]) if len(shape) == 5 else (1, shape)
+    dev, dt, i32 = key_cache.device, key_cache.dtype, torch.int32
+    shape = key_cache.shape
+    pages, page_size, H, D = shape[-4:]
+    layers = shape[0] if len(shape) == 5 else 1
     entry = H * D * key_cache.element_size()
     if not isinstance(tree_tokens, torch.Tensor) or tree_tokens.dim() != 2:
         raise ValueError("tree_tokens must be [B, N]")
@@ -570,18 +563,17 @@ def spec_kv_commit(key_cache, value_cache, page_table, lengths, tree_tokens, par
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     max_pages = page_table.shape[1]
-    _i32(page_table, (B, max_pages), "page_table", dev)
-    for t, s, name in ((lengths, (B,), "lengths"), (tree_tokens, (B, N), "tree_tokens"),
-                       (parent_idx, (B, N), "parent_idx"), (out_path, (B, N + 1), "out_path"),
-                       (out_len, (B,), "out_len")):
-        _i32(t, s, name, dev)
-    out_nodes = _out(out_nodes, (B, N + 1), torch.int32, dev, "out_nodes")
-    out_lengths = _out(out_lengths, (B,), torch.int32, dev, "out_lengths")
-    with torch.cuda.device(dev):
-        _lib.check(_lib.load().spec_kv_commit(
-            _ptr(key_cache), _ptr(value_cache), layers, pages * page_size * entry, pages, page_size, entry,
-            _ptr(page_table), max_pages, _ptr(lengths), _ptr(tree_tokens), _ptr(parent_idx), _ptr(out_path),
-            _ptr(out_len), B, N, _ptr(out_nodes), _ptr(out_lengths), _stream(stream)))
+    if out_nodes is None:
+        out_nodes = torch.empty((B, N + 1), dtype=i32, device=dev)
+    if out_lengths is None:
+        out_lengths = torch.empty((B,), dtype=i32, device=dev)
+    _invoke(_lib.load().spec_kv_commit, dev, stream, _arg(key_cache, dt, shape, dev, "key_cache"),
+            _arg(value_cache, dt, shape, dev, "value_cache"), layers, pages * page_size * entry, pages, page_size, entry,
+            _arg(page_table, i32, (B, max_pages), dev, "page_table"), max_pages,
+            _arg(lengths, i32, (B,), dev, "lengths"), _arg(tree_tokens, i32, (B, N), dev, "tree_tokens"),
+            _arg(parent_idx, i32, (B, N), dev, "parent_idx"), _arg(out_path, i32, (B, N + 1), dev, "out_path"),
+            _arg(out_len, i32, (B,), dev, "out_len"), B, N, _arg(out_nodes, i32, (B, N + 1), dev, "out_nodes"),
+            _arg(out_lengths, i32, (B,), dev, "out_lengths"))
     return out_nodes, out_lengths
 
 

@@ -93,6 +93,8 @@ def header_symbols(path: str = HEADER):
 def load():
     """Load libspecverify.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

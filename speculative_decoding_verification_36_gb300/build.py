@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["api.cu", "sample_kernel.cu", "greedy_kernel.cu", "acceptance_kernel.cu",
            "tree_sample_kernel.cu", "ngram_kernel.cu", "process_kernel.cu", "kv_kernel.cu"]
-HEADERS = ["sv_common.cuh", "sv_kernels.h"]
+HEADERS = ["sv_common.cuh", "sv_bulk.cuh", "sv_kernels.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

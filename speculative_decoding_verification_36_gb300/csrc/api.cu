@@ -587,8 +587,7 @@ int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int
   if (a.parents && a.rows_per > sv::process_tree_rows()) a.rows_per = sv::process_tree_rows();
   a.groups = (R + a.rows_per - 1) / a.rows_per;
   if (units * a.groups > INT_MAX) return SPEC_ERR_SHAPE;
-  const bool vec = aligned16(logits) && aligned16(out) && ((size_t)V * esz) % 16 == 0;
-  const cudaError_t e = sv::launch_process(a, bf16, vec, stream);
+  const cudaError_t e = sv::launch_process(a, bf16, stream);
   if (e != cudaSuccess) return cuda_fail(e, "logit processing launch");
   return SPEC_OK;
 }

@@ -48,6 +48,7 @@
 // launch adds no launch gap.
 //
 // Every history token is read from HBM once.
+#include "sv_bulk.cuh"
 #include "sv_common.cuh"
 #include "sv_kernels.h"
 
@@ -71,57 +72,6 @@ constexpr int kNgramFinishWarps = 8;
 static_assert(kNgramPerThread % 4 == 0, "ends are compared four at a time");
 static_assert((kNgramHalo * 4) % 16 == 0 && (kNgramWinOff * 4) % 16 == 0 && (kNgramStageInts * 4) % 16 == 0,
               "stage layout must keep 16-byte alignment");
-
-// ---------------------------------------------------------------------------
-// mbarrier and bulk-copy primitives (shared memory of this CTA)
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ unsigned smem_addr(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void mbar_init(unsigned long long* bar, unsigned count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-// arrive and add `bytes` to the transaction count the phase waits for
-__device__ __forceinline__ void mbar_arrive_tx(unsigned long long* bar, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
-               : "memory");
-}
-// Has the phase with this parity completed?  The thread may be suspended up
-// to about kNgramSuspendNs while the phase is still open (no instructions
-// issue meanwhile).  Acquire: the completing arrivals and copies are visible
-// afterwards.
-constexpr unsigned kNgramSuspendNs = 128;
-__device__ __forceinline__ bool mbar_try(unsigned long long* bar, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(kNgramSuspendNs)
-      : "memory");
-  return ok != 0;
-}
-// One bulk copy global -> shared, completing `bytes` on the mbarrier.  Both
-// addresses and the size are multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes, unsigned long long* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
-      : "memory");
-}
-// Warp-uniform bounded wait: every lane tries, and the warp leaves together
-// once all lanes have seen the phase; false after `limit` further tries
-// (each suspends for at most about kNgramSuspendNs).
-__device__ __forceinline__ bool warp_wait(unsigned long long* bar, unsigned parity, unsigned limit) {
-  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-  for (unsigned it = 0; it < limit; ++it)
-    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-  return false;
-}
 
 // First token of the window staged over h[L - kNgramMaxN .. L - 1]: a
 // multiple of 4, so that the window's copy starts on a 16-byte boundary.

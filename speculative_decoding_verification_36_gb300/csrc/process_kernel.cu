@@ -72,77 +72,116 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
 // logits
 // ---------------------------------------------------------------------------
 // A CTA takes one chunk of the vocabulary of one sequence and all rows of a
-// row group.  What the rows share is laid out once in shared memory: per token
-// of the chunk the additive term of the history and the biases, and bitmaps of
-// the tokens that something touches, that were seen, that occurred in the
-// output and that a draft carries.  Then the chunk's logits stream through
-// registers row by row; a vector that nothing touches is only masked.
+// row group, in two passes.  The dense one copies the rows through registers
+// and puts -inf where the mask forbids; it needs nothing but the masks, so it
+// runs while the history's counts come in.  The sparse one visits only the
+// tokens that the history, a bias or a draft touches (a few percent of the
+// vocabulary under a long history), which the CTA lists once for all its rows:
+// it reads each one's logit again (from L2: the dense pass has just been
+// there), and writes the result over the copy.  In place the dense pass reads
+// and writes only vectors that hold a forbidden token.
 constexpr int kProcThreads = 256;
 constexpr int kProcWarps = kProcThreads / 32;
 constexpr int kProcChunk = 4096;                     // tokens of a CTA's chunk
 constexpr int kProcWords = kProcChunk / 32;          // ... in bitmap words
-constexpr int kProcWarpToks = kProcChunk / kProcWarps;  // tokens whose biases one warp sums
+constexpr int kProcWarpToks = kProcChunk / kProcWarps;  // tokens of one warp's threads
+constexpr int kProcBatch = 4;                        // vectors in flight per thread
+constexpr int kProcItems = 4;                        // listed logits in flight per thread
 constexpr int kProcMaxDrafts = 1024;
+constexpr int kProcDrafts = 256;   // drafts in a chunk that are listed; more are looked up in the input
 constexpr int kProcTreeRows = 32;  // rows of a group whose paths are kept as bit sets
-static_assert(kProcThreads >= kProcWords, "one thread per bitmap word");
-static_assert(kProcChunk % (2 * kProcThreads) == 0, "a half-word of the bitmap per thread");
+static_assert(kProcChunk == 16 * kProcThreads, "16 tokens per thread");
+// list entries: offset, then
+constexpr unsigned kProcSeen = 1u << 12;     // in the history
+constexpr unsigned kProcCounted = 1u << 13;  // c > 0 without the drafts
+constexpr unsigned kProcDraft = 1u << 14;    // some draft carries it
+constexpr unsigned kProcOffset = kProcSeen - 1u;
+static_assert(kProcChunk <= (int)kProcSeen, "an offset leaves the flags free");
 
 struct ProcShared {
-  float adj[kProcChunk];        // -f c - p [c > 0] + biases, without the drafts
-  unsigned touch[kProcWords];   // history, draft or bias
-  unsigned seen[kProcWords];    // history
-  unsigned out[kProcWords];     // c > 0 without the drafts
-  unsigned draft[kProcWords];   // some draft carries it
-  unsigned list[kProcMaxDrafts];  // drafts in the chunk: (offset << 16) | node
+  float adj[kProcChunk];             // listed tokens: -f c - p [c > 0] + biases, without the drafts
+  unsigned short list[kProcChunk];   // in no particular order
+  unsigned bias[kProcWords];         // tokens with a bias
+  unsigned draft[kProcWords];        // tokens that some draft carries
+  unsigned drafts[kProcDrafts];      // drafts in the chunk: (offset << 16) | node
   unsigned path[kProcTreeRows][kProcMaxDrafts / 32];  // tree: the nodes above each row of the group
-  int n_list;
+  int n_list, n_draft;
+  int twice;  // a token with several biases
   int bad;
 };
 
+struct Bf16Tag {};
 template <class T>
 struct ProcType;
 template <>
 struct ProcType<float> {
-  static constexpr int kVec = 4;
   using storage = uint32_t;
+  static constexpr int kVec = 4;
+  static constexpr uint32_t kNegInf = 0xff800000u, kNan = 0x7fc00000u;
   static __device__ __forceinline__ float widen(uint32_t w) { return __uint_as_float(w); }
   static __device__ __forceinline__ uint32_t round(float f) { return __float_as_uint(f); }
-  static constexpr uint32_t kNegInf = 0xff800000u, kNan = 0x7fc00000u;
 };
-struct Bf16Tag {};
 template <>
 struct ProcType<Bf16Tag> {
-  static constexpr int kVec = 8;
   using storage = uint16_t;
+  static constexpr int kVec = 8;
+  static constexpr uint16_t kNegInf = 0xff80u, kNan = 0x7fc0u;
   static __device__ __forceinline__ float widen(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
   static __device__ __forceinline__ uint16_t round(float f) {
     uint16_t r;
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(f));
     return r;
   }
-  static constexpr uint16_t kNegInf = 0xff80u, kNan = 0x7fc0u;
 };
 
-template <class S, int VEC>
-union ProcVec {
-  S e[VEC];
-  uint4 q;
-};
-
-// n bits (n a power of two <= 8) of a bitmap in shared memory from bit v on;
-// v is a multiple of n
-template <int N>
-__device__ __forceinline__ unsigned bits_at(const unsigned* words, int v) {
-  return (words[v >> 5] >> (v & 31)) & ((1u << N) - 1u);
+// A vector with -inf where the element's bit is clear.
+template <class T>
+__device__ __forceinline__ uint4 proc_keep(uint4 x, unsigned bits) {
+  if constexpr (sizeof(typename ProcType<T>::storage) == 4) {
+    x.x = bits & 1u ? x.x : ProcType<T>::kNegInf;
+    x.y = bits & 2u ? x.y : ProcType<T>::kNegInf;
+    x.z = bits & 4u ? x.z : ProcType<T>::kNegInf;
+    x.w = bits & 8u ? x.w : ProcType<T>::kNegInf;
+  } else {
+    constexpr uint32_t fill = ProcType<T>::kNegInf * 0x10001u;
+    auto one = [](uint32_t w, uint32_t b) {
+      const uint32_t keep = (b & 1u) * 0xffffu + (b & 2u) * 0x7fff8000u;  // each bit widened to 16
+      return (w & keep) | (fill & ~keep);
+    };
+    x.x = one(x.x, bits), x.y = one(x.y, bits >> 2), x.z = one(x.z, bits >> 4), x.w = one(x.w, bits >> 6);
+  }
+  return x;
 }
 
-template <class T, bool kVecPath, bool kInPlace>
+// The occurrences of the chunk's token `off` among the drafts above row r.
+__device__ __forceinline__ int proc_extra(const ProcessArgs& a, const ProcShared& sh, int b, int base, int off, int r,
+                                          int r0) {
+  int extra = 0;
+  const unsigned* path = a.parents ? sh.path[r - r0] : nullptr;
+  if (sh.n_draft <= kProcDrafts) {
+    for (int i = 0; i < sh.n_draft; ++i) {
+      const unsigned d = sh.drafts[i];
+      const int j = d & 0xffffu;
+      extra += (int)(d >> 16) == off && (path ? (path[j >> 5] >> (j & 31) & 1u) : j < r);
+    }
+  } else {
+    const int32_t* tok = a.drafts + (long long)b * (a.R - 1);
+    for (int j = 0; j < r; ++j)  // the nodes above a row have lower indexes than it
+      extra += __ldg(tok + j) == base + off && (!path || (path[j >> 5] >> (j & 31) & 1u));
+  }
+  return extra;
+}
+
+template <class T, bool kShifted, bool kInPlace>
 __global__ void __launch_bounds__(kProcThreads) process_kernel(const __grid_constant__ ProcessArgs a) {
   using Ty = ProcType<T>;
   using S = typename Ty::storage;
-  constexpr int VEC = kVecPath ? Ty::kVec : 1;
-  constexpr int U = 4;  // vectors in flight per thread
-  __shared__ ProcShared sh;
+  constexpr int VEC = Ty::kVec;
+  constexpr unsigned kAll = (1u << VEC) - 1u;
+  constexpr int kPer = kProcChunk / (kProcThreads * VEC);  // vectors per thread and row
+  constexpr int RU = kProcBatch / kPer;                    // rows of a batch
+  static_assert(kProcBatch % kPer == 0, "whole rows in flight");
+  __shared__ __align__(16) ProcShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int unit = blockIdx.x;
   const int chunk = unit % a.chunks;
@@ -152,78 +191,167 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const __grid_cons
   const int base = chunk * kProcChunk;
   const int n_tok = min(kProcChunk, a.V - base);
   const int r0 = group * a.rows_per, r1 = min(a.R, r0 + a.rows_per);
-  const float rep = a.rep ? __ldg(a.rep + b) : 1.f;
-  const float freq = a.freq ? __ldg(a.freq + b) : 0.f;
-  const float pres = a.pres ? __ldg(a.pres + b) : 0.f;
-  const float inv = 1.f / rep;
   const int N = a.drafts ? a.R - 1 : 0;
+  const S* in = (const S*)a.in;
+  S* out = (S*)a.out;
 
-  // ---- what the rows share ----
+  // ---- what the history, the drafts and the biases hold of the chunk ----
   const int32_t* state = a.state ? a.state + (long long)b * a.words : nullptr;
-  if (tid == 0) {
-    sh.n_list = 0;
-    // a penalty that is no number, or a factor that is not positive
-    sh.bad = !(rep > 0.f && rep < INFINITY) || !(fabsf(freq) < INFINITY) || !(fabsf(pres) < INFINITY);
-  }
+  unsigned mine = 0;  // the bitmap of the thread's 16 tokens
+  if (state && base + 16 * tid < a.P) mine = __ldg((const unsigned short*)(state + a.P) + (base >> 4) + tid);
   if (tid < kProcWords) {
-    const unsigned w = state && base + 32 * tid < a.P ? __ldg((const unsigned*)state + a.P + (base >> 5) + tid) : 0u;
-    sh.touch[tid] = w;
-    sh.seen[tid] = w;
+    sh.bias[tid] = 0u;
     sh.draft[tid] = 0u;
-    sh.out[tid] = 0u;
   }
-  for (int i = tid; i < kProcChunk / 4; i += kProcThreads) ((float4*)sh.adj)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (tid == 0) sh.n_list = sh.n_draft = sh.twice = sh.bad = 0;
+  int count[16];  // all at once: one trip to memory
+#pragma unroll
+  for (int i = 0; i < 16; ++i) count[i] = mine >> i & 1u ? __ldg(state + base + 16 * tid + i) : 0;
   __syncthreads();
-  {  // history: 16 tokens of the bitmap per thread
-    unsigned w = (sh.seen[tid >> 1] >> (16 * (tid & 1))) & 0xffffu;
-    unsigned counted = 0;
-    while (w) {
-      const int i = __ffs(w) - 1;
-      w &= w - 1;
-      const int off = 16 * tid + i;
-      const int c = __ldg(state + base + off) & 0x7fffffff;
-      if (c > 0) {
-        sh.adj[off] = -freq * (float)c - pres;
-        counted |= 1u << i;
-      }
-    }
-    ((unsigned short*)sh.out)[tid] = (unsigned short)counted;
-  }
   for (int j = tid; j < N; j += kProcThreads) {
     const int t = __ldg(a.drafts + (long long)b * N + j) - base;
     if (t >= 0 && t < n_tok) {
-      sh.list[atomicAdd(&sh.n_list, 1)] = ((unsigned)t << 16) | (unsigned)j;
+      const int at = atomicAdd(&sh.n_draft, 1);
+      if (at < kProcDrafts) sh.drafts[at] = ((unsigned)t << 16) | (unsigned)j;
       atomicOr(&sh.draft[t >> 5], 1u << (t & 31));
-      atomicOr(&sh.touch[t >> 5], 1u << (t & 31));
     }
     if (a.parents) {
       const int p = __ldg(a.parents + (long long)b * N + j);
       if (p < -1 || p >= j) sh.bad = 1;
     }
   }
-  __syncthreads();
-  if (a.n_bias > 0) {
-    // each warp sums the biases of its own tokens, in the list's order
-    const int lo = warp * kProcWarpToks;
-    const long long at = (long long)b * a.n_bias;
-    for (int i0 = 0; i0 < a.n_bias; i0 += 32) {
-      const int i = i0 + lane;
-      const int t = i < a.n_bias ? __ldg(a.bias_tokens + at + i) - base - lo : -1;
-      const bool mine = t >= 0 && t < kProcWarpToks && lo + t < n_tok;
-      const float v = mine ? __ldg(a.bias_values + at + i) : 0.f;
-      for (unsigned m = __ballot_sync(0xffffffffu, mine); m; m &= m - 1) {
-        const int l = __ffs(m) - 1;
-        const int off = lo + __shfl_sync(0xffffffffu, t, l);
-        const float x = __shfl_sync(0xffffffffu, v, l);
-        if (lane == 0) {
-          sh.adj[off] += x;
-          sh.touch[off >> 5] |= 1u << (off & 31);
+  for (int i = tid; i < a.n_bias; i += kProcThreads) {
+    const int t = __ldg(a.bias_tokens + (long long)b * a.n_bias + i) - base;
+    if (t >= 0 && t < n_tok) {
+      if (atomicOr(&sh.bias[t >> 5], 1u << (t & 31)) >> (t & 31) & 1u)
+        sh.twice = 1;
+      else
+        sh.adj[t] = __ldg(a.bias_values + (long long)b * a.n_bias + i);
+    }
+  }
+
+  // ---- dense pass: copy and mask ----
+  auto row_at = [&](int r) { return ((long long)b * a.R + r) * a.V + base; };
+  const uint32_t* mask0 = a.mask ? a.mask + (long long)b * a.mask_rows * a.W + (base >> 5) : nullptr;
+  const int mask_step = a.mask_rows > 1 ? a.W : 0;
+  const int mask_end = 4 * (a.W - (base >> 5));  // bytes of a mask row from the chunk on
+  auto mask_row = [&](int r) { return (const uint8_t*)(mask0 + (long long)r * mask_step); };
+  auto allowed_at = [&](int r, int t) { return !mask0 || (__ldg(mask_row(r) + (t >> 3)) >> (t & 7) & 1u); };
+  // elements of a row's part of the chunk before its first 16-byte boundary
+  auto head_of = [&](int r) {
+    if constexpr (!kShifted) return 0;
+    const int off = (int)((row_at(r) + a.phase) & (VEC - 1));
+    return min(off ? VEC - off : 0, n_tok);
+  };
+  if (a.split) {
+    // the output's vectors lie at another phase than the input's: single elements
+    for (int r = r0; r < r1; ++r)
+#pragma unroll 4
+      for (int t = tid; t < n_tok; t += kProcThreads) {
+        const S x = in[row_at(r) + t];
+        out[row_at(r) + t] = allowed_at(r, t) ? x : Ty::kNegInf;
+      }
+  } else if (!kInPlace || mask0) {
+    for (int rb = r0; rb < r1; rb += RU) {
+      uint4 x[RU][kPer];
+      unsigned allowed[RU][kPer];
+      int at[RU][kPer];  // -1: no work here
+#pragma unroll
+      for (int i = 0; i < RU; ++i)
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+          const int r = rb + i, v = (p * kProcThreads + tid) * VEC + (r < r1 ? head_of(r) : 0);
+          at[i][p] = r < r1 && v + VEC <= n_tok ? v : -1;
+          allowed[i][p] = kAll;
+          if (mask0 && at[i][p] >= 0) {
+            const uint8_t* m = mask_row(r) + (v >> 3);
+            unsigned w = __ldg(m);
+            if (kShifted && (v & 7) > 8 - VEC) w |= (unsigned)__ldg(m + ((v >> 3) + 1 < mask_end ? 1 : 0)) << 8;
+            allowed[i][p] = w >> (v & 7) & kAll;
+          }
         }
+#pragma unroll
+      for (int i = 0; i < RU; ++i)
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+          if (kInPlace && allowed[i][p] == kAll) at[i][p] = -1;
+          if (at[i][p] >= 0 && !(kInPlace && allowed[i][p] == 0u)) x[i][p] = *(const uint4*)(in + row_at(rb + i) + at[i][p]);
+        }
+#pragma unroll
+      for (int i = 0; i < RU; ++i)
+#pragma unroll
+        for (int p = 0; p < kPer; ++p)
+          if (at[i][p] >= 0) {
+            if (allowed[i][p] != kAll) x[i][p] = proc_keep<T>(x[i][p], allowed[i][p]);
+            *(uint4*)(out + row_at(rb + i) + at[i][p]) = x[i][p];
+          }
+    }
+    if constexpr (kShifted) {
+      // the elements before the first and after the last whole vector of each row
+      for (int r = r0 + warp; r < r1; r += kProcWarps) {
+        const int head = head_of(r), tail = head + (n_tok - head) / VEC * VEC;
+        const int t = lane < 16 ? lane : tail + lane - 16;
+        if (lane < 16 ? t >= head : t >= n_tok) continue;
+        out[row_at(r) + t] = allowed_at(r, t) ? in[row_at(r) + t] : Ty::kNegInf;
       }
     }
   }
-  const int n_list = sh.n_list;
-  if (a.parents && n_list > 0 && !sh.bad) {
+
+  // ---- the list ----
+  const float rep = a.rep ? __ldg(a.rep + b) : 1.f;
+  const float freq = a.freq ? __ldg(a.freq + b) : 0.f;
+  const float pres = a.pres ? __ldg(a.pres + b) : 0.f;
+  const float inv = 1.f / rep;
+  // a penalty that is no number, or a factor that is not positive
+  if (!(rep > 0.f && rep < INFINITY) || !(fabsf(freq) < INFINITY) || !(fabsf(pres) < INFINITY)) sh.bad = 1;
+  __syncthreads();
+  if (sh.bad) {
+    if (tid == 0) atomicOr(a.status, kStatusBadData);
+    for (int r = r0; r < r1; ++r)
+      for (int t = tid; t < n_tok; t += kProcThreads) out[row_at(r) + t] = Ty::kNan;
+    return;
+  }
+  if (sh.twice) {
+    // some token has several biases: each warp sums those of its own tokens,
+    // in the list's order
+    const int lo = warp * kProcWarpToks;
+    const long long first = (long long)b * a.n_bias;
+    for (int i = lane; i < kProcWarpToks; i += 32) sh.adj[lo + i] = 0.f;
+    __syncwarp();
+    for (int i0 = 0; i0 < a.n_bias; i0 += 32) {
+      const int i = i0 + lane;
+      const int t = i < a.n_bias ? __ldg(a.bias_tokens + first + i) - base - lo : -1;
+      const bool own = t >= 0 && t < kProcWarpToks && lo + t < n_tok;
+      const float v = own ? __ldg(a.bias_values + first + i) : 0.f;
+      for (unsigned m = __ballot_sync(0xffffffffu, own); m; m &= m - 1) {
+        const int l = __ffs(m) - 1;
+        const int off = lo + __shfl_sync(0xffffffffu, t, l);
+        const float x = __shfl_sync(0xffffffffu, v, l);
+        if (lane == 0) sh.adj[off] += x;
+      }
+    }
+    __syncwarp();
+  }
+  {
+    static_assert(kProcWarpToks == 16 * 32, "a warp's threads hold the warp's tokens");
+    const unsigned bias = (sh.bias[tid >> 1] >> (16 * (tid & 1))) & 0xffffu;
+    const unsigned draft = (sh.draft[tid >> 1] >> (16 * (tid & 1))) & 0xffffu;
+    const unsigned touch = mine | bias | draft;
+    if (touch) {
+      int at = atomicAdd(&sh.n_list, __popc(touch));
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (touch >> i & 1u) {
+          const int off = 16 * tid + i, n = count[i] & 0x7fffffff;
+          float adj = bias >> i & 1u ? sh.adj[off] : 0.f;
+          if (n > 0) adj += -freq * (float)n - pres;
+          sh.adj[off] = adj;
+          sh.list[at++] = (unsigned short)(off | (mine >> i & 1u ? kProcSeen : 0u) | (n > 0 ? kProcCounted : 0u) |
+                                           (draft >> i & 1u ? kProcDraft : 0u));
+        }
+    }
+  }
+  if (a.parents && sh.n_draft > 0) {
     // the nodes above each row of the group; a parent precedes its child
     const int W = (N + 31) >> 5;
     for (int r = r0 + tid; r < r1; r += kProcThreads) {
@@ -233,87 +361,43 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const __grid_cons
     }
   }
   __syncthreads();
-  const bool bad = sh.bad != 0;
-  if (bad && tid == 0) atomicOr(a.status, kStatusBadData);
 
-  // ---- the rows ----
-  const S* in = (const S*)a.in;
-  S* out = (S*)a.out;
-  constexpr unsigned kAll = (1u << VEC) - 1u;
-  for (int r = r0; r < r1; ++r) {
-    const long long row = ((long long)b * a.R + r) * a.V + base;
-    const uint8_t* mask =
-        a.mask ? (const uint8_t*)(a.mask + ((long long)b * a.mask_rows + (a.mask_rows > 1 ? r : 0)) * a.W + (base >> 5))
-               : nullptr;
-    for (int v0 = tid * VEC; v0 < n_tok; v0 += U * kProcThreads * VEC) {
-      ProcVec<S, VEC> x[U];
-      unsigned allowed[U], touch[U];
+  // ---- sparse pass: 32 entries of one row per step of a warp ----
+  const int n_list = sh.n_list, blocks = (n_list + 31) >> 5, steps = blocks * (r1 - r0);
+  for (int k0 = warp; k0 < steps; k0 += kProcItems * kProcWarps) {
+    unsigned entry[kProcItems];
+    int row[kProcItems];  // -1: nothing to do
+    S z[kProcItems];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * kProcThreads * VEC;
-        allowed[u] = kAll;
-        touch[u] = 0;
-        if (v < n_tok) {
-          if (mask) allowed[u] = ((unsigned)__ldg(mask + (v >> 3)) >> (v & 7)) & kAll;
-          touch[u] = bits_at<VEC>(sh.touch, v);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * kProcThreads * VEC;
-        if (v < n_tok && !(kInPlace && (allowed[u] == 0u || (allowed[u] == kAll && touch[u] == 0u)))) {
-          if constexpr (kVecPath)
-            x[u].q = *(const uint4*)(in + row + v);
-          else
-            x[u].e[0] = in[row + v];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * kProcThreads * VEC;
-        if (v >= n_tok) continue;
-        if (kInPlace && !bad && allowed[u] == kAll && touch[u] == 0u) continue;
-        if (touch[u] & allowed[u]) {
-          const unsigned seen = bits_at<VEC>(sh.seen, v), counted = bits_at<VEC>(sh.out, v);
-          const unsigned draft = bits_at<VEC>(sh.draft, v);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            if (!(touch[u] >> e & 1u)) continue;
-            float adj = sh.adj[v + e];
-            bool hit = seen >> e & 1u;
-            if (draft >> e & 1u) {
-              int extra = 0;
-              for (int i = 0; i < n_list; ++i) {
-                const unsigned entry = sh.list[i];
-                const int j = entry & 0xffffu;
-                const bool on = a.parents ? (sh.path[r - r0][j >> 5] >> (j & 31) & 1u) : j < r;
-                extra += (int)(entry >> 16) == v + e && on;
-              }
-              if (extra) {
-                hit = true;
-                adj -= freq * (float)extra;
-                if (!(counted >> e & 1u)) adj -= pres;
-              }
-            }
-            const float z = Ty::widen(x[u].e[e]);
-            x[u].e[e] = Ty::round((hit ? (z > 0.f ? z * inv : z * rep) : z) + adj);
-          }
-        }
-        if (allowed[u] != kAll) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (!(allowed[u] >> e & 1u)) x[u].e[e] = Ty::kNegInf;
-        }
-        if (bad) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) x[u].e[e] = Ty::kNan;
-        }
-        if constexpr (kVecPath)
-          *(uint4*)(out + row + v) = x[u].q;
-        else
-          out[row + v] = x[u].e[0];
+    for (int i = 0; i < kProcItems; ++i) {
+      const int k = k0 + i * kProcWarps;
+      const int r = (int)((unsigned)k / (unsigned)blocks), e = (k - r * blocks) * 32 + lane;
+      row[i] = -1;
+      if (k < steps && e < n_list) {
+        entry[i] = sh.list[e];
+        if (allowed_at(r0 + r, entry[i] & kProcOffset)) row[i] = r0 + r;
       }
     }
+#pragma unroll
+    for (int i = 0; i < kProcItems; ++i)
+      if (row[i] >= 0) z[i] = in[row_at(row[i]) + (entry[i] & kProcOffset)];
+#pragma unroll
+    for (int i = 0; i < kProcItems; ++i)
+      if (row[i] >= 0) {
+        const int off = entry[i] & kProcOffset;
+        float adj = sh.adj[off];
+        bool seen = entry[i] & kProcSeen;
+        if (entry[i] & kProcDraft) {
+          const int extra = proc_extra(a, sh, b, base, off, row[i], r0);
+          if (extra) {
+            seen = true;
+            adj -= freq * (float)extra;
+            if (!(entry[i] & kProcCounted)) adj -= pres;
+          }
+        }
+        const float x = Ty::widen(z[i]);
+        out[row_at(row[i]) + off] = Ty::round((seen ? (x > 0.f ? x * inv : x * rep) : x) + adj);
+      }
   }
 }
 
@@ -321,11 +405,11 @@ int process_chunk() { return kProcChunk; }
 int process_tree_rows() { return kProcTreeRows; }
 
 template <class T>
-static void launch_one(const ProcessArgs& a, bool vec, unsigned grid, cudaStream_t s) {
+static void launch_one(const ProcessArgs& a, bool shifted, unsigned grid, cudaStream_t s) {
   const bool in_place = a.in == a.out;
-  if (vec && in_place)
+  if (shifted && in_place)
     process_kernel<T, true, true><<<grid, kProcThreads, 0, s>>>(a);
-  else if (vec)
+  else if (shifted)
     process_kernel<T, true, false><<<grid, kProcThreads, 0, s>>>(a);
   else if (in_place)
     process_kernel<T, false, true><<<grid, kProcThreads, 0, s>>>(a);
@@ -333,12 +417,18 @@ static void launch_one(const ProcessArgs& a, bool vec, unsigned grid, cudaStream
     process_kernel<T, false, false><<<grid, kProcThreads, 0, s>>>(a);
 }
 
-cudaError_t launch_process(const ProcessArgs& a, bool bf16, bool vec, cudaStream_t s) {
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s) {
   const unsigned grid = (unsigned)((long long)a.B * a.groups * a.chunks);
+  const int esz = bf16 ? 2 : 4;
+  const unsigned in_off = (unsigned)((uintptr_t)a.in & 15), out_off = (unsigned)((uintptr_t)a.out & 15);
+  ProcessArgs k = a;
+  k.phase = (int)in_off / esz;
+  k.split = in_off != out_off;
+  const bool shifted = in_off || (long long)a.V * esz % 16;
   if (bf16)
-    launch_one<Bf16Tag>(a, vec, grid, s);
+    launch_one<Bf16Tag>(k, shifted, grid, s);
   else
-    launch_one<float>(a, vec, grid, s);
+    launch_one<float>(k, shifted, grid, s);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,76 @@
+// sv_bulk.cuh -- mbarriers and one-dimensional bulk asynchronous copies (TMA)
+// between global memory and the shared memory of a CTA.
+#pragma once
+
+#include <stdint.h>
+
+namespace sv {
+
+// ---------------------------------------------------------------------------
+// mbarrier and bulk-copy primitives (shared memory of this CTA)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ unsigned smem_addr(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(unsigned long long* bar, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// arrive and add `bytes` to the transaction count the phase waits for
+__device__ __forceinline__ void mbar_arrive_tx(unsigned long long* bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
+               : "memory");
+}
+// Has the phase with this parity completed?  The thread may be suspended up
+// to about kSuspendNs while the phase is still open (no instructions
+// issue meanwhile).  Acquire: the completing arrivals and copies are visible
+// afterwards.
+constexpr unsigned kSuspendNs = 128;
+__device__ __forceinline__ bool mbar_try(unsigned long long* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+// One bulk copy global -> shared, completing `bytes` on the mbarrier.  Both
+// addresses and the size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes, unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+// Warp-uniform bounded wait: every lane tries, and the warp leaves together
+// once all lanes have seen the phase; false after `limit` further tries
+// (each suspends for at most about kSuspendNs).
+__device__ __forceinline__ bool warp_wait(unsigned long long* bar, unsigned parity, unsigned limit) {
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  for (unsigned it = 0; it < limit; ++it)
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  return false;
+}
+
+// One bulk copy shared -> global, in the calling thread's current bulk group.
+// Both addresses and the size are multiples of 16 bytes; generic writes to the
+// source are made visible by fence_async() before it.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, unsigned bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the thread's latest kPending groups have read their sources.
+template <int kPending>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+// This thread's generic writes to shared memory come before later bulk copies.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+}  // namespace sv

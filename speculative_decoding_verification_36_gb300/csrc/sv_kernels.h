@@ -287,12 +287,16 @@ struct ProcessArgs {
   const uint32_t* mask;        // [B, mask_rows, W] or NULL
   int mask_rows, W;
   int B, R, V;
-  int chunks, groups, rows_per;  // the launch: vocabulary chunks, row groups and rows of a group
+  // the launch: vocabulary chunks, row groups and rows of a group
+  int chunks, groups, rows_per;
+  // ... and, set by it: elements from the 16-byte boundary below the input to
+  // its start, and whether the output starts at another offset from one
+  int phase, split;
   unsigned* status;
 };
 int process_chunk();      // tokens of one CTA's chunk
 int process_tree_rows();  // most rows of a group when the drafts form a tree
-cudaError_t launch_process(const ProcessArgs& a, bool bf16, bool vec, cudaStream_t s);
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s);
 
 // The paged key/value cache's append and commit (kv_kernel.cu).
 struct KvAppendArgs {

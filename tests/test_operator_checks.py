@@ -109,6 +109,8 @@ def test_binding_refuses_host_tensors(lib):
         sv.spec_kv_commit(torch.zeros(1, 2, 1, 4), torch.zeros(1, 2, 1, 4), i, i, i, i, i, i)
     with pytest.raises(sv.SpecError):
         sv.spec_token_state(1, 0, "cpu")
+    for V in (1, 32, 33, 4095, 152064):
+        assert sv.spec_token_state(2, V, "cpu").shape == (2, lib.spec_token_state_words(V))
 
 
 def test_rope_turns():
