@@ -86,6 +86,8 @@ int get_device_state(DeviceState** out) {
         for (int c = 0; c < 5; ++c) d.walk_clusters[bf][v][c] = sv::tree_walk_clusters(bf, v, 1 << c);
       }
     d.occ_ngram = sv::ngram_blocks_per_sm();
+    e = sv::process_configure();
+    if (e != cudaSuccess) return cuda_fail(e, "logit processing shared memory");
     d.init = true;
   }
   *out = &d;
@@ -579,15 +581,16 @@ int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int
   if (rc) return rc;
   a.status = d->status;
   a.chunks = (V + sv::process_chunk() - 1) / sv::process_chunk();
-  // a few CTAs per SM: few sequences are split by rows as well
-  const long long units = (long long)B * a.chunks, want = 8LL * d->sms;
+  // few sequences are split by rows as well, until every CTA has a unit
+  const int capacity = d->sms * sv::process_blocks_per_sm();
+  const long long units = (long long)B * a.chunks, want = capacity;
   long long groups = units < want ? (want + units - 1) / units : 1;
   if (groups > R) groups = R;
   a.rows_per = (int)((R + groups - 1) / groups);
   if (a.parents && a.rows_per > sv::process_tree_rows()) a.rows_per = sv::process_tree_rows();
   a.groups = (R + a.rows_per - 1) / a.rows_per;
-  if (units * a.groups > INT_MAX) return SPEC_ERR_SHAPE;
-  const cudaError_t e = sv::launch_process(a, bf16, stream);
+  if (units * a.groups > (1 << 30)) return SPEC_ERR_SHAPE;  // rounds of the grid past the last unit count on
+  const cudaError_t e = sv::launch_process(a, bf16, capacity, stream);
   if (e != cudaSuccess) return cuda_fail(e, "logit processing launch");
   return SPEC_OK;
 }
@@ -997,6 +1000,7 @@ int spec_test_spin_limit(uint32_t iterations) {
   if (e == cudaSuccess) e = sv::greedy_set_spin_limit(n);
   if (e == cudaSuccess) e = sv::tree_sample_set_spin_limit(n);
   if (e == cudaSuccess) e = sv::ngram_set_spin_limit(n);
+  if (e == cudaSuccess) e = sv::process_set_spin_limit(n);
   if (e != cudaSuccess) return cuda_fail(e, "spin limit");
   return SPEC_OK;
 }

@@ -10,6 +10,7 @@
 //   z' = v allowed in row r ? z2 : -inf
 // in fp32, rounded once to the logits' type.  A verify under these settings
 // needs them per row: row r of a chain already counts the r drafts before it.
+#include "sv_bulk.cuh"
 #include "sv_common.cuh"
 #include "sv_kernels.h"
 
@@ -72,26 +73,30 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
 // logits
 // ---------------------------------------------------------------------------
 // A CTA takes one chunk of the vocabulary of one sequence and all rows of a
-// row group, in two passes.  The dense one copies the rows through registers
-// and puts -inf where the mask forbids; it needs nothing but the masks, so it
-// runs while the history's counts come in.  The sparse one visits only the
-// tokens that the history, a bias or a draft touches (a few percent of the
-// vocabulary under a long history), which the CTA lists once for all its rows:
-// it reads each one's logit again (from L2: the dense pass has just been
-// there), and writes the result over the copy.  In place the dense pass reads
-// and writes only vectors that hold a forbidden token.
+// row group; each of its warps has 512 of the chunk's tokens.  What the rows
+// share is worked out once: few tokens are touched by the history, a bias or a
+// draft (a few percent of the vocabulary under a long history), so each warp
+// lists its own, with the additive term -f c - p [c > 0] + biases.  After the
+// lists no barrier joins the warps.
+//
+// Apart from its input (process_kernel): a warp's part of a row travels global
+// -> shared -> global by bulk copies, kBatch rows at a time and the next batch
+// in flight, and the list and the mask are applied to it in shared memory.  Per row a warp visits its list
+// and, with a mask, its vectors; without one no instruction sees the rest.
+// In place (process_in_place_kernel): only the listed tokens and the vectors
+// that hold a forbidden one are read and written, where they lie.
 constexpr int kProcThreads = 256;
 constexpr int kProcWarps = kProcThreads / 32;
-constexpr int kProcChunk = 4096;                     // tokens of a CTA's chunk
-constexpr int kProcWords = kProcChunk / 32;          // ... in bitmap words
-constexpr int kProcWarpToks = kProcChunk / kProcWarps;  // tokens of one warp's threads
-constexpr int kProcBatch = 4;                        // vectors in flight per thread
-constexpr int kProcItems = 4;                        // listed logits in flight per thread
+constexpr int kProcPiece = 512;                        // tokens of a warp
+constexpr int kProcChunk = kProcPiece * kProcWarps;    // ... of a CTA
+constexpr int kProcWords = kProcChunk / 32;            // ... in bitmap words
+constexpr int kProcRows = 4;       // rows at once when in place
 constexpr int kProcMaxDrafts = 1024;
 constexpr int kProcDrafts = 256;   // drafts in a chunk that are listed; more are looked up in the input
 constexpr int kProcTreeRows = 32;  // rows of a group whose paths are kept as bit sets
-static_assert(kProcChunk == 16 * kProcThreads, "16 tokens per thread");
-// list entries: offset, then
+static_assert(kProcPiece == 16 * 32, "a lane holds 16 of its warp's tokens");
+static_assert(kProcWords <= kProcThreads, "a thread clears a word");
+// list entries: offset in the chunk, then
 constexpr unsigned kProcSeen = 1u << 12;     // in the history
 constexpr unsigned kProcCounted = 1u << 13;  // c > 0 without the drafts
 constexpr unsigned kProcDraft = 1u << 14;    // some draft carries it
@@ -99,15 +104,18 @@ constexpr unsigned kProcOffset = kProcSeen - 1u;
 static_assert(kProcChunk <= (int)kProcSeen, "an offset leaves the flags free");
 
 struct ProcShared {
-  float adj[kProcChunk];             // listed tokens: -f c - p [c > 0] + biases, without the drafts
-  unsigned short list[kProcChunk];   // in no particular order
-  unsigned bias[kProcWords];         // tokens with a bias
-  unsigned draft[kProcWords];        // tokens that some draft carries
-  unsigned drafts[kProcDrafts];      // drafts in the chunk: (offset << 16) | node
-  unsigned path[kProcTreeRows][kProcMaxDrafts / 32];  // tree: the nodes above each row of the group
-  int n_list, n_draft;
+  float adj[kProcChunk];            // of the listed tokens, without the drafts
+  unsigned short list[kProcChunk];  // each warp's in its own part
+  unsigned bias[kProcWords];        // tokens with a bias
+  unsigned draft[kProcWords];       // tokens that some draft carries
+  unsigned drafts[kProcDrafts];     // drafts in the chunk: (offset << 16) | node
+  int n_draft;
   int twice;  // a token with several biases
-  int bad;
+  int bad, pad;
+};
+// tree: the nodes above each row of the group
+struct ProcPaths {
+  unsigned row[kProcTreeRows][kProcMaxDrafts / 32];
 };
 
 struct Bf16Tag {};
@@ -116,7 +124,7 @@ struct ProcType;
 template <>
 struct ProcType<float> {
   using storage = uint32_t;
-  static constexpr int kVec = 4;
+  static constexpr int kVec = 4, kBatch = 2, kBatches = 2;
   static constexpr uint32_t kNegInf = 0xff800000u, kNan = 0x7fc00000u;
   static __device__ __forceinline__ float widen(uint32_t w) { return __uint_as_float(w); }
   static __device__ __forceinline__ uint32_t round(float f) { return __float_as_uint(f); }
@@ -124,7 +132,7 @@ struct ProcType<float> {
 template <>
 struct ProcType<Bf16Tag> {
   using storage = uint16_t;
-  static constexpr int kVec = 8;
+  static constexpr int kVec = 8, kBatch = 3, kBatches = 3;
   static constexpr uint16_t kNegInf = 0xff80u, kNan = 0x7fc0u;
   static __device__ __forceinline__ float widen(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
   static __device__ __forceinline__ uint16_t round(float f) {
@@ -132,6 +140,19 @@ struct ProcType<Bf16Tag> {
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(f));
     return r;
   }
+};
+
+// A warp's rows in flight: a piece each, and its phase.
+template <class T>
+struct alignas(16) ProcStages {
+  static constexpr int kStage = kProcPiece + 2 * ProcType<T>::kVec;
+  typename ProcType<T>::storage row[ProcType<T>::kBatches][ProcType<T>::kBatch][kStage];
+};
+template <class T>
+struct ProcCopyShared : ProcShared {
+  ProcStages<T> stages[kProcWarps];
+  unsigned long long full[kProcWarps][ProcType<T>::kBatches];
+  // then, for a tree, ProcPaths
 };
 
 // A vector with -inf where the element's bit is clear.
@@ -144,184 +165,154 @@ __device__ __forceinline__ uint4 proc_keep(uint4 x, unsigned bits) {
     x.w = bits & 8u ? x.w : ProcType<T>::kNegInf;
   } else {
     constexpr uint32_t fill = ProcType<T>::kNegInf * 0x10001u;
-    auto one = [](uint32_t w, uint32_t b) {
-      const uint32_t keep = (b & 1u) * 0xffffu + (b & 2u) * 0x7fff8000u;  // each bit widened to 16
+    // four bits to the tops of four bytes, then each top over two bytes
+    const uint32_t lo = (bits & 15u) * 0x10204080u, hi = (bits >> 4) * 0x10204080u;
+    auto one = [](uint32_t w, uint32_t tops, unsigned which) {
+      uint32_t keep;  // a selector digit of 8 and up spreads the byte's top bit
+      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(keep) : "r"(tops), "r"(which));
       return (w & keep) | (fill & ~keep);
     };
-    x.x = one(x.x, bits), x.y = one(x.y, bits >> 2), x.z = one(x.z, bits >> 4), x.w = one(x.w, bits >> 6);
+    x.x = one(x.x, lo, 0x9988u), x.y = one(x.y, lo, 0xbbaau), x.z = one(x.z, hi, 0x9988u), x.w = one(x.w, hi, 0xbbaau);
   }
   return x;
 }
 
-// The occurrences of the chunk's token `off` among the drafts above row r.
-__device__ __forceinline__ int proc_extra(const ProcessArgs& a, const ProcShared& sh, int b, int base, int off, int r,
-                                          int r0) {
-  int extra = 0;
-  const unsigned* path = a.parents ? sh.path[r - r0] : nullptr;
-  if (sh.n_draft <= kProcDrafts) {
-    for (int i = 0; i < sh.n_draft; ++i) {
-      const unsigned d = sh.drafts[i];
-      const int j = d & 0xffffu;
-      extra += (int)(d >> 16) == off && (path ? (path[j >> 5] >> (j & 31) & 1u) : j < r);
-    }
-  } else {
-    const int32_t* tok = a.drafts + (long long)b * (a.R - 1);
-    for (int j = 0; j < r; ++j)  // the nodes above a row have lower indexes than it
-      extra += __ldg(tok + j) == base + off && (!path || (path[j >> 5] >> (j & 31) & 1u));
-  }
-  return extra;
+// Where a unit lies: a chunk of a sequence's vocabulary in a group of its rows.
+struct ProcUnit {
+  int b, base;        // sequence, first token of the chunk
+  int r0, rows;       // first row, rows
+  int start, n_tok;   // first token and tokens of this warp's piece
+  long long row0;     // elements before the piece in row r0
+};
+__device__ __forceinline__ ProcUnit proc_unit(const ProcessArgs& a, unsigned unit) {
+  ProcUnit u;
+  const unsigned q = unit / (unsigned)a.chunks, b = q / (unsigned)a.groups;
+  u.base = (int)(unit - q * (unsigned)a.chunks) * kProcChunk;
+  u.b = (int)b;
+  u.r0 = (int)(q - b * (unsigned)a.groups) * a.rows_per;
+  u.rows = min(a.rows_per, a.R - u.r0);
+  u.start = u.base + (int)(threadIdx.x >> 5) * kProcPiece;
+  u.n_tok = max(0, min(kProcPiece, a.V - u.start));
+  u.row0 = ((long long)u.b * a.R + u.r0) * a.V + u.start;
+  return u;
 }
 
-template <class T, bool kShifted, bool kInPlace>
-__global__ void __launch_bounds__(kProcThreads) process_kernel(const __grid_constant__ ProcessArgs a) {
-  using Ty = ProcType<T>;
-  using S = typename Ty::storage;
-  constexpr int VEC = Ty::kVec;
-  constexpr unsigned kAll = (1u << VEC) - 1u;
-  constexpr int kPer = kProcChunk / (kProcThreads * VEC);  // vectors per thread and row
-  constexpr int RU = kProcBatch / kPer;                    // rows of a batch
-  static_assert(kProcBatch % kPer == 0, "whole rows in flight");
-  __shared__ __align__(16) ProcShared sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int unit = blockIdx.x;
-  const int chunk = unit % a.chunks;
-  unit /= a.chunks;
-  const int group = unit % a.groups;
-  const int b = unit / a.groups;
-  const int base = chunk * kProcChunk;
-  const int n_tok = min(kProcChunk, a.V - base);
-  const int r0 = group * a.rows_per, r1 = min(a.R, r0 + a.rows_per);
-  const int N = a.drafts ? a.R - 1 : 0;
-  const S* in = (const S*)a.in;
-  S* out = (S*)a.out;
+// What the rows of a unit share, for one warp.
+struct ProcShare {
+  int n_list;
+  float rep, inv, freq, pres;
+  bool bad;
+  ProcPaths* paths;
+};
 
-  // ---- what the history, the drafts and the biases hold of the chunk ----
-  const int32_t* state = a.state ? a.state + (long long)b * a.words : nullptr;
-  unsigned mine = 0;  // the bitmap of the thread's 16 tokens
-  if (state && base + 16 * tid < a.P) mine = __ldg((const unsigned short*)(state + a.P) + (base >> 4) + tid);
+// What a unit's lists are made from, on its way into a thread's registers: the
+// bitmap of the thread's 16 tokens, the penalties, and of the drafts and biases
+// as many as fit (longer lists are read to the end later).
+constexpr int kProcBiasRegs = 2;
+struct ProcAhead {
+  unsigned mine;
+  int draft, parent;
+  int bias_t[kProcBiasRegs];
+  float bias_v[kProcBiasRegs];
+  float rep, freq, pres;
+};
+__device__ __forceinline__ ProcAhead proc_ahead(const ProcessArgs& a, const ProcUnit& u) {
+  const int tid = threadIdx.x;
+  ProcAhead h;
+  h.mine = a.state && u.base + 16 * tid < a.P
+               ? __ldg((const unsigned short*)(a.state + (long long)u.b * a.words + a.P) + (u.base >> 4) + tid)
+               : 0u;
+  const int N = a.drafts ? a.R - 1 : 0;
+  h.draft = tid < N ? __ldg(a.drafts + (long long)u.b * N + tid) : -1;
+  h.parent = a.parents && tid < N ? __ldg(a.parents + (long long)u.b * N + tid) : -1;
+#pragma unroll
+  for (int q = 0; q < kProcBiasRegs; ++q) {
+    const int i = q * kProcThreads + tid;
+    const long long at = (long long)u.b * a.n_bias + i;
+    h.bias_t[q] = i < a.n_bias ? __ldg(a.bias_tokens + at) : -1;
+    h.bias_v[q] = i < a.n_bias ? __ldg(a.bias_values + at) : 0.f;
+  }
+  h.rep = a.rep ? __ldg(a.rep + u.b) : 1.f;
+  h.freq = a.freq ? __ldg(a.freq + u.b) : 0.f;
+  h.pres = a.pres ? __ldg(a.pres + u.b) : 0.f;
+  return h;
+}
+
+// The lists of a unit from what came ahead; the counts of the listed tokens are
+// one more trip to memory.  Every thread of the CTA takes part (the lists
+// before are done with); on return each warp may go on.
+__device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh, const ProcUnit& u, const ProcAhead& h,
+                                           ProcShare& c) {
+  const int tid = threadIdx.x, lane = tid & 31, lo = tid >> 5 << 9;  // the warp's first token in the chunk
+  const int32_t* state = a.state + (long long)u.b * a.words;
+  const int N = a.drafts ? a.R - 1 : 0;
+  const int32_t* draft_row = a.drafts + (long long)u.b * N;
+  const int32_t* parent_row = a.parents + (long long)u.b * N;
+  const long long first = (long long)u.b * a.n_bias;
+  const int left = min(kProcChunk, a.V - u.base);
+  const unsigned mine = h.mine;
+  c.rep = h.rep;
+  c.freq = h.freq;
+  c.pres = h.pres;
+  c.inv = 1.f / c.rep;
+  __syncthreads();
   if (tid < kProcWords) {
     sh.bias[tid] = 0u;
     sh.draft[tid] = 0u;
   }
-  if (tid == 0) sh.n_list = sh.n_draft = sh.twice = sh.bad = 0;
-  int count[16];  // all at once: one trip to memory
-#pragma unroll
-  for (int i = 0; i < 16; ++i) count[i] = mine >> i & 1u ? __ldg(state + base + 16 * tid + i) : 0;
+  if (tid == 0) sh.n_draft = sh.twice = sh.bad = 0;
   __syncthreads();
-  for (int j = tid; j < N; j += kProcThreads) {
-    const int t = __ldg(a.drafts + (long long)b * N + j) - base;
-    if (t >= 0 && t < n_tok) {
+  auto put_draft = [&](int j, int t, int parent) {
+    if (t >= 0 && t < left) {
       const int at = atomicAdd(&sh.n_draft, 1);
       if (at < kProcDrafts) sh.drafts[at] = ((unsigned)t << 16) | (unsigned)j;
       atomicOr(&sh.draft[t >> 5], 1u << (t & 31));
     }
-    if (a.parents) {
-      const int p = __ldg(a.parents + (long long)b * N + j);
-      if (p < -1 || p >= j) sh.bad = 1;
-    }
-  }
-  for (int i = tid; i < a.n_bias; i += kProcThreads) {
-    const int t = __ldg(a.bias_tokens + (long long)b * a.n_bias + i) - base;
-    if (t >= 0 && t < n_tok) {
-      if (atomicOr(&sh.bias[t >> 5], 1u << (t & 31)) >> (t & 31) & 1u)
-        sh.twice = 1;
-      else
-        sh.adj[t] = __ldg(a.bias_values + (long long)b * a.n_bias + i);
-    }
-  }
-
-  // ---- dense pass: copy and mask ----
-  auto row_at = [&](int r) { return ((long long)b * a.R + r) * a.V + base; };
-  const uint32_t* mask0 = a.mask ? a.mask + (long long)b * a.mask_rows * a.W + (base >> 5) : nullptr;
-  const int mask_step = a.mask_rows > 1 ? a.W : 0;
-  const int mask_end = 4 * (a.W - (base >> 5));  // bytes of a mask row from the chunk on
-  auto mask_row = [&](int r) { return (const uint8_t*)(mask0 + (long long)r * mask_step); };
-  auto allowed_at = [&](int r, int t) { return !mask0 || (__ldg(mask_row(r) + (t >> 3)) >> (t & 7) & 1u); };
-  // elements of a row's part of the chunk before its first 16-byte boundary
-  auto head_of = [&](int r) {
-    if constexpr (!kShifted) return 0;
-    const int off = (int)((row_at(r) + a.phase) & (VEC - 1));
-    return min(off ? VEC - off : 0, n_tok);
+    if (parent < -1 || parent >= j) sh.bad = 1;
   };
-  if (a.split) {
-    // the output's vectors lie at another phase than the input's: single elements
-    for (int r = r0; r < r1; ++r)
-#pragma unroll 4
-      for (int t = tid; t < n_tok; t += kProcThreads) {
-        const S x = in[row_at(r) + t];
-        out[row_at(r) + t] = allowed_at(r, t) ? x : Ty::kNegInf;
-      }
-  } else if (!kInPlace || mask0) {
-    for (int rb = r0; rb < r1; rb += RU) {
-      uint4 x[RU][kPer];
-      unsigned allowed[RU][kPer];
-      int at[RU][kPer];  // -1: no work here
+  if (tid < N) put_draft(tid, h.draft - u.base, h.parent);
+  for (int j = kProcThreads + tid; j < N; j += kProcThreads)
+    put_draft(j, __ldg(draft_row + j) - u.base, a.parents ? __ldg(parent_row + j) : -1);
+  auto put_bias = [&](int t, float v) {
+    if (t < 0 || t >= left) return;
+    if (atomicOr(&sh.bias[t >> 5], 1u << (t & 31)) >> (t & 31) & 1u)
+      sh.twice = 1;
+    else
+      sh.adj[t] = v;
+  };
 #pragma unroll
-      for (int i = 0; i < RU; ++i)
-#pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-          const int r = rb + i, v = (p * kProcThreads + tid) * VEC + (r < r1 ? head_of(r) : 0);
-          at[i][p] = r < r1 && v + VEC <= n_tok ? v : -1;
-          allowed[i][p] = kAll;
-          if (mask0 && at[i][p] >= 0) {
-            const uint8_t* m = mask_row(r) + (v >> 3);
-            unsigned w = __ldg(m);
-            if (kShifted && (v & 7) > 8 - VEC) w |= (unsigned)__ldg(m + ((v >> 3) + 1 < mask_end ? 1 : 0)) << 8;
-            allowed[i][p] = w >> (v & 7) & kAll;
-          }
-        }
-#pragma unroll
-      for (int i = 0; i < RU; ++i)
-#pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-          if (kInPlace && allowed[i][p] == kAll) at[i][p] = -1;
-          if (at[i][p] >= 0 && !(kInPlace && allowed[i][p] == 0u)) x[i][p] = *(const uint4*)(in + row_at(rb + i) + at[i][p]);
-        }
-#pragma unroll
-      for (int i = 0; i < RU; ++i)
-#pragma unroll
-        for (int p = 0; p < kPer; ++p)
-          if (at[i][p] >= 0) {
-            if (allowed[i][p] != kAll) x[i][p] = proc_keep<T>(x[i][p], allowed[i][p]);
-            *(uint4*)(out + row_at(rb + i) + at[i][p]) = x[i][p];
-          }
-    }
-    if constexpr (kShifted) {
-      // the elements before the first and after the last whole vector of each row
-      for (int r = r0 + warp; r < r1; r += kProcWarps) {
-        const int head = head_of(r), tail = head + (n_tok - head) / VEC * VEC;
-        const int t = lane < 16 ? lane : tail + lane - 16;
-        if (lane < 16 ? t >= head : t >= n_tok) continue;
-        out[row_at(r) + t] = allowed_at(r, t) ? in[row_at(r) + t] : Ty::kNegInf;
-      }
-    }
-  }
-
-  // ---- the list ----
-  const float rep = a.rep ? __ldg(a.rep + b) : 1.f;
-  const float freq = a.freq ? __ldg(a.freq + b) : 0.f;
-  const float pres = a.pres ? __ldg(a.pres + b) : 0.f;
-  const float inv = 1.f / rep;
-  // a penalty that is no number, or a factor that is not positive
-  if (!(rep > 0.f && rep < INFINITY) || !(fabsf(freq) < INFINITY) || !(fabsf(pres) < INFINITY)) sh.bad = 1;
+  for (int q = 0; q < kProcBiasRegs; ++q)
+    if (q * kProcThreads + tid < a.n_bias) put_bias(h.bias_t[q] - u.base, h.bias_v[q]);
+  for (int i = kProcBiasRegs * kProcThreads + tid; i < a.n_bias; i += kProcThreads)
+    put_bias(__ldg(a.bias_tokens + first + i) - u.base, __ldg(a.bias_values + first + i));
   __syncthreads();
-  if (sh.bad) {
-    if (tid == 0) atomicOr(a.status, kStatusBadData);
-    for (int r = r0; r < r1; ++r)
-      for (int t = tid; t < n_tok; t += kProcThreads) out[row_at(r) + t] = Ty::kNan;
-    return;
+  // a penalty that is no number, or a factor that is not positive
+  c.bad = sh.bad || !(c.rep > 0.f && c.rep < INFINITY) || !(fabsf(c.freq) < INFINITY) || !(fabsf(c.pres) < INFINITY);
+  if (c.bad && tid == 0) atomicOr(a.status, kStatusBadData);
+
+  const unsigned draft = (sh.draft[tid >> 1] >> (16 * (tid & 1))) & 0xffffu;
+  unsigned touch = mine | draft | ((sh.bias[tid >> 1] >> (16 * (tid & 1))) & 0xffffu);
+  int at = __popc(touch);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, at, d);
+    if (lane >= d) at += o;
+  }
+  c.n_list = __shfl_sync(0xffffffffu, at, 31);
+  at += lo - __popc(touch);
+  for (; touch; touch &= touch - 1) {
+    const int i = __ffs(touch) - 1;
+    sh.list[at++] = (unsigned short)((16 * tid + i) | (mine >> i & 1u ? kProcSeen : 0u) | (draft >> i & 1u ? kProcDraft : 0u));
   }
   if (sh.twice) {
     // some token has several biases: each warp sums those of its own tokens,
-    // in the list's order
-    const int lo = warp * kProcWarpToks;
-    const long long first = (long long)b * a.n_bias;
-    for (int i = lane; i < kProcWarpToks; i += 32) sh.adj[lo + i] = 0.f;
+    // in the order given
+    for (int i = lane; i < kProcPiece; i += 32) sh.adj[lo + i] = 0.f;
     __syncwarp();
     for (int i0 = 0; i0 < a.n_bias; i0 += 32) {
       const int i = i0 + lane;
-      const int t = i < a.n_bias ? __ldg(a.bias_tokens + first + i) - base - lo : -1;
-      const bool own = t >= 0 && t < kProcWarpToks && lo + t < n_tok;
+      const int t = i < a.n_bias ? __ldg(a.bias_tokens + first + i) - u.base - lo : -1;
+      const bool own = t >= 0 && t < u.n_tok;
       const float v = own ? __ldg(a.bias_values + first + i) : 0.f;
       for (unsigned m = __ballot_sync(0xffffffffu, own); m; m &= m - 1) {
         const int l = __ffs(m) - 1;
@@ -330,106 +321,464 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const __grid_cons
         if (lane == 0) sh.adj[off] += x;
       }
     }
-    __syncwarp();
   }
-  {
-    static_assert(kProcWarpToks == 16 * 32, "a warp's threads hold the warp's tokens");
-    const unsigned bias = (sh.bias[tid >> 1] >> (16 * (tid & 1))) & 0xffffu;
-    const unsigned draft = (sh.draft[tid >> 1] >> (16 * (tid & 1))) & 0xffffu;
-    const unsigned touch = mine | bias | draft;
-    if (touch) {
-      int at = atomicAdd(&sh.n_list, __popc(touch));
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (touch >> i & 1u) {
-          const int off = 16 * tid + i, n = count[i] & 0x7fffffff;
-          float adj = bias >> i & 1u ? sh.adj[off] : 0.f;
-          if (n > 0) adj += -freq * (float)n - pres;
-          sh.adj[off] = adj;
-          sh.list[at++] = (unsigned short)(off | (mine >> i & 1u ? kProcSeen : 0u) | (n > 0 ? kProcCounted : 0u) |
-                                           (draft >> i & 1u ? kProcDraft : 0u));
-        }
+  __syncwarp();
+  for (int e = lane; e < c.n_list; e += 32) {
+    const unsigned entry = sh.list[lo + e];
+    const int off = entry & kProcOffset, n = entry & kProcSeen ? __ldg(state + u.base + off) & 0x7fffffff : 0;
+    float adj = sh.bias[off >> 5] >> (off & 31) & 1u ? sh.adj[off] : 0.f;
+    if (n > 0) {
+      adj += -c.freq * (float)n - c.pres;
+      sh.list[lo + e] = (unsigned short)(entry | kProcCounted);
     }
+    sh.adj[off] = adj;
   }
   if (a.parents && sh.n_draft > 0) {
     // the nodes above each row of the group; a parent precedes its child
     const int W = (N + 31) >> 5;
-    for (int r = r0 + tid; r < r1; r += kProcThreads) {
-      unsigned* path = sh.path[r - r0];
-      for (int w = 0; w < W; ++w) path[w] = 0u;
-      for (int j = r - 1; j >= 0; j = __ldg(a.parents + (long long)b * N + j)) path[j >> 5] |= 1u << (j & 31);
-    }
+    if (!c.bad)
+      for (int r = u.r0 + tid; r < u.r0 + u.rows; r += kProcThreads) {
+        unsigned* path = c.paths->row[r - u.r0];
+        for (int w = 0; w < W; ++w) path[w] = 0u;
+        for (int j = r - 1; j >= 0; j = __ldg(a.parents + (long long)u.b * N + j)) path[j >> 5] |= 1u << (j & 31);
+      }
+    __syncthreads();
   }
-  __syncthreads();
+  __syncwarp();
+}
 
-  // ---- sparse pass: 32 entries of one row per step of a warp ----
-  const int n_list = sh.n_list, blocks = (n_list + 31) >> 5, steps = blocks * (r1 - r0);
-  for (int k0 = warp; k0 < steps; k0 += kProcItems * kProcWarps) {
-    unsigned entry[kProcItems];
-    int row[kProcItems];  // -1: nothing to do
-    S z[kProcItems];
+// The occurrences of the chunk's token `off` among the drafts above row r.
+__device__ __forceinline__ int proc_extra(const ProcessArgs& a, const ProcShared& sh, const ProcUnit& u,
+                                          const ProcShare& c, int off, int r) {
+  int extra = 0;
+  const unsigned* path = a.parents ? c.paths->row[r - u.r0] : nullptr;
+  if (sh.n_draft <= kProcDrafts) {
+    for (int i = 0; i < sh.n_draft; ++i) {
+      const unsigned d = sh.drafts[i];
+      const int j = d & 0xffffu;
+      extra += (int)(d >> 16) == off && (path ? (path[j >> 5] >> (j & 31) & 1u) : j < r);
+    }
+  } else {
+    const int32_t* tok = a.drafts + (long long)u.b * (a.R - 1);
+    for (int j = 0; j < r; ++j)  // the nodes above a row have lower indexes than it
+      extra += __ldg(tok + j) == u.base + off && (!path || (path[j >> 5] >> (j & 31) & 1u));
+  }
+  return extra;
+}
+
+// What a listed token's logit z becomes: z up + add where z > 0, z down + add
+// elsewhere.  -inf stays -inf, whatever is added: a masked vocabulary stays masked.
+struct ProcTerm {
+  float up, down, add;
+  __device__ __forceinline__ float operator()(float z) const {
+    return z == neg_inf() ? z : fmaf(z, z > 0.f ? up : down, add);
+  }
+};
+__device__ __forceinline__ ProcTerm proc_term(const ProcShare& c, bool seen, float add) {
+  return {seen ? c.inv : 1.f, seen ? c.rep : 1.f, add};
+}
+// ... of a token that some draft carries, in row r
+__device__ __forceinline__ ProcTerm proc_draft_term(const ProcessArgs& a, const ProcShared& sh, const ProcUnit& u,
+                                                    const ProcShare& c, unsigned entry, float add, int r) {
+  const int extra = proc_extra(a, sh, u, c, entry & kProcOffset, r);
+  if (extra) {
+    add -= c.freq * (float)extra;
+    if (!(entry & kProcCounted)) add -= c.pres;
+  }
+  return proc_term(c, (entry & kProcSeen) || extra, add);
+}
+
+// kShifted: rows start off 16-byte boundaries (the vocabulary's size, or the
+// buffers).  A row keeps its phase in shared memory: element t of the piece
+// lies at phase + t, whole 16-byte vectors move by bulk copies, and the few
+// elements before the first and after the last one are moved by lanes.
+//
+// The grid stays: a CTA goes from unit to unit, and each warp's ring of batches
+// runs on across them, so that the rows of the next unit are under way while
+// the lists of this one wait for their counts.  (One CTA per unit, with the
+// same passes: 343 us for B = 256, R = 9, V = 152064 in bf16, everything on.)
+template <class T, bool kShifted, bool kMask>
+__global__ void __launch_bounds__(kProcThreads, 2) process_kernel(const __grid_constant__ ProcessArgs a) {
+  using Ty = ProcType<T>;
+  using S = typename Ty::storage;
+  constexpr int VEC = Ty::kVec, RB = Ty::kBatch, NB = Ty::kBatches;
+  constexpr unsigned kAll = (1u << VEC) - 1u;
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  ProcCopyShared<T>& sh = *(ProcCopyShared<T>*)s_raw;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned total = (unsigned)a.B * (unsigned)a.groups * (unsigned)a.chunks, G = gridDim.x;
+  // round i's unit: each round hands out G units in another order, so that no
+  // CTA always meets the chunk of the frequent tokens, whose lists are long
+  auto unit_of = [&](unsigned i) { return i * G + (blockIdx.x + i * 7919u) % G; };
+  const S* in = (const S*)a.in;
+  S* out = (S*)a.out;
+  auto phase_of = [&](const ProcUnit& u, int i) { return kShifted ? (int)((u.row0 + (long long)i * a.V + a.phase) & (VEC - 1)) : 0; };
+  auto head_of = [&](const ProcUnit& u, int ph) { return kShifted && ph ? min(VEC - ph, u.n_tok) : 0; };
+  auto stage = [&](int g, int j) { return sh.stages[warp].row[g % NB][j]; };
+
+  if (lane == 0) {
+    for (int k = 0; k < NB; ++k) mbar_init(&sh.full[warp][k], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+
+  // ---- the ring: batch g sets out, lane j with row j's copy ----
+  unsigned load_round = 0;
+  ProcUnit lu = proc_unit(a, unit_of(0));  // the unit, the batch of it and the batch of the ring that set out next
+  int load_batch = 0, load_g = 0;
+  auto load_next = [&]() {
+    if (load_batch * RB >= lu.rows) {
+      const unsigned next = unit_of(++load_round);
+      if (next >= total) {
+        lu.rows = 0;  // and stays so
+        load_batch = 0;
+        return;
+      }
+      lu = proc_unit(a, next);
+      load_batch = 0;
+    }
+    const int i = load_batch * RB + lane;
+    int bytes = 0, ph = 0, head = 0;
+    if (lane < RB && i < lu.rows) {
+      ph = phase_of(lu, i);
+      head = head_of(lu, ph);
+      bytes = (lu.n_tok - head) / VEC * 16;
+    }
+    const int sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)bytes);
+    unsigned long long* bar = &sh.full[warp][load_g % NB];
+    if (lane == 0) {
+      if (sum)
+        mbar_arrive_tx(bar, (unsigned)sum);
+      else
+        mbar_arrive(bar);
+    }
+    __syncwarp();
+    if (bytes) bulk_load(stage(load_g, lane) + (ph ? VEC : 0), in + lu.row0 + (long long)i * a.V + head, (unsigned)bytes, bar);
+    ++load_batch;
+    ++load_g;
+  };
+  for (int k = 0; k < NB; ++k)
+    if (lu.rows) load_next();
+
+  // ---- masks and edge elements of the next batch, one batch ahead ----
+  // A lane holds the mask bits of 16 tokens, of the rows of a batch.
+  auto mask_row = [&](const ProcUnit& u, int i) {
+    return a.mask + ((long long)u.b * a.mask_rows + (a.mask_rows > 1 ? u.r0 + i : 0)) * a.W + (u.start >> 5);
+  };
+  unsigned next_word[RB];
+  // Eight lanes a row: first its elements before its first vector, then those after its last.
+  S edge[2] = {0, 0};
+  auto edge_at = [&](const ProcUnit& u, int i, int side) {  // the lane's token, -1 for none
+    if (i >= u.rows || (lane >> 3) >= RB) return -1;
+    const int head = head_of(u, phase_of(u, i)), e = lane & 7;
+    const int t = side ? head + (u.n_tok - head) / VEC * VEC + e : e;
+    return (side ? t < u.n_tok : t < head) ? t : -1;
+  };
+  auto look = [&](const ProcUnit& u, int batch) {
+    if constexpr (kMask) {
 #pragma unroll
-    for (int i = 0; i < kProcItems; ++i) {
-      const int k = k0 + i * kProcWarps;
-      const int r = (int)((unsigned)k / (unsigned)blocks), e = (k - r * blocks) * 32 + lane;
-      row[i] = -1;
-      if (k < steps && e < n_list) {
-        entry[i] = sh.list[e];
-        if (allowed_at(r0 + r, entry[i] & kProcOffset)) row[i] = r0 + r;
+      for (int j = 0; j < RB; ++j) {
+        const int i = batch * RB + j;
+        next_word[j] = i < u.rows && 16 * lane < u.n_tok ? __ldg((const unsigned short*)mask_row(u, i) + lane) : 0xffffu;
       }
     }
+    if constexpr (kShifted) {
+      const int i = batch * RB + (lane >> 3);
 #pragma unroll
-    for (int i = 0; i < kProcItems; ++i)
-      if (row[i] >= 0) z[i] = in[row_at(row[i]) + (entry[i] & kProcOffset)];
+      for (int side = 0; side < 2; ++side) {
+        const int t = edge_at(u, i, side);
+        if (t >= 0) edge[side] = in[u.row0 + (long long)i * a.V + t];
+      }
+    }
+  };
+
+  ProcUnit u = proc_unit(a, unit_of(0));
+  look(u, 0);
+  ProcAhead ahead = proc_ahead(a, u);
+  ProcShare c;
+  c.paths = (ProcPaths*)(s_raw + sizeof(ProcCopyShared<T>));
+  const unsigned short* list = sh.list + warp * kProcPiece;
+  const unsigned limit = spin_limit();
+  bool dead = false;
+  int g = 0;
+  for (unsigned round = 0;; ++round) {
+    proc_lists(a, sh, u, ahead, c);
+    const unsigned next = unit_of(round + 1);
+    ProcUnit nu = u;
+    if (next < total) {
+      nu = proc_unit(a, next);
+      ahead = proc_ahead(a, nu);
+    }
+    for (int i0 = 0; i0 < u.rows; i0 += RB, ++g) {
+      const int n = min(RB, u.rows - i0);
+      unsigned word[RB];
 #pragma unroll
-    for (int i = 0; i < kProcItems; ++i)
-      if (row[i] >= 0) {
-        const int off = entry[i] & kProcOffset;
-        float adj = sh.adj[off];
-        bool seen = entry[i] & kProcSeen;
-        if (entry[i] & kProcDraft) {
-          const int extra = proc_extra(a, sh, b, base, off, row[i], r0);
-          if (extra) {
-            seen = true;
-            adj -= freq * (float)extra;
-            if (!(entry[i] & kProcCounted)) adj -= pres;
+      for (int j = 0; j < RB; ++j) word[j] = kMask ? next_word[j] : 0xffffu;
+      const S mine[2] = {edge[0], edge[1]};
+      if (i0 + RB < u.rows)
+        look(u, i0 / RB + 1);
+      else if (next < total)
+        look(nu, 0);
+      if (!dead && !warp_wait(&sh.full[warp][g % NB], (g / NB) & 1, limit)) {
+        // a copy that never came: this warp hands out nothing more, and waits
+        // for what is in flight, so that no copy outlives the CTA's memory
+        if (lane == 0) atomicOr(a.status, kStatusTimeout);
+        bulk_wait_read<0>();
+        for (int q = g; q < load_g; ++q) warp_wait(&sh.full[warp][q % NB], (q / NB) & 1, kSpinLimit);
+        dead = true;
+      }
+      if (dead) continue;
+      int te[2] = {-1, -1};
+      if constexpr (kShifted) {
+        const int i = i0 + (lane >> 3);
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          te[side] = edge_at(u, i, side);
+          if (te[side] >= 0) stage(g, lane >> 3)[phase_of(u, i) + te[side]] = mine[side];
+        }
+        __syncwarp();
+      }
+      // the listed tokens, each for all rows of the batch
+      for (int e = lane; e < c.n_list; e += 32) {
+        const unsigned entry = list[e];
+        const int off = entry & kProcOffset;
+        const float add = sh.adj[off];
+        S* x = stage(g, 0) + off - warp * kProcPiece;
+        ProcTerm term = proc_term(c, entry & kProcSeen, add);
+#pragma unroll
+        for (int j = 0; j < RB; ++j)
+          if (j < n) {
+            if (entry & kProcDraft) term = proc_draft_term(a, sh, u, c, entry, add, u.r0 + i0 + j);
+            S* at = x + j * ProcStages<T>::kStage + phase_of(u, i0 + j);
+            *at = Ty::round(term(Ty::widen(*at)));
+          }
+      }
+      if constexpr (kMask) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+          unsigned w = word[j];
+          if constexpr (kShifted) {
+            // the bits of the 16-byte lattice: of the elements 16 lane .. from
+            // the boundary below the piece
+            const unsigned below = __shfl_up_sync(0xffffffffu, w, 1);
+            w = ((lane ? below : 0xffffu) | w << 16) >> (16 - phase_of(u, i0 + j)) & 0xffffu;
+          }
+          if (w == 0xffffu) continue;
+          uint4* x = (uint4*)stage(g, j) + lane * (16 / VEC);
+#pragma unroll
+          for (int q = 0; q < 16 / VEC; ++q) {
+            // lanes take their vectors in orders that spread over the banks
+            const int v = q ^ (lane * (16 / VEC) >> 3 & (16 / VEC - 1));
+            const unsigned bits = w >> (v * VEC) & kAll;
+            if (bits != kAll) x[v] = proc_keep<T>(x[v], bits);
           }
         }
-        const float x = Ty::widen(z[i]);
-        out[row_at(row[i]) + off] = Ty::round((seen ? (x > 0.f ? x * inv : x * rep) : x) + adj);
+        if constexpr (kShifted) {
+          // the edges, also those in no vector of the loop's
+          __syncwarp();
+          const int i = i0 + (lane >> 3);
+#pragma unroll
+          for (int side = 0; side < 2; ++side)
+            if (te[side] >= 0 && !(__ldg((const uint8_t*)mask_row(u, i) + (te[side] >> 3)) >> (te[side] & 7) & 1u))
+              stage(g, lane >> 3)[phase_of(u, i) + te[side]] = Ty::kNegInf;
+        }
       }
+      if (c.bad) {
+        __syncwarp();
+        for (int j = 0; j < n; ++j)
+          for (int t = lane; t < u.n_tok; t += 32) stage(g, j)[phase_of(u, i0 + j) + t] = Ty::kNan;
+      }
+      fence_async();
+      __syncwarp();
+      if (kShifted && a.split) {
+        // the output's vectors lie at another phase: element by element
+        for (int j = 0; j < n; ++j)
+          for (int t = lane; t < u.n_tok; t += 32)
+            out[u.row0 + (long long)(i0 + j) * a.V + t] = stage(g, j)[phase_of(u, i0 + j) + t];
+      } else {
+        if constexpr (kShifted) {
+          const int i = i0 + (lane >> 3);
+#pragma unroll
+          for (int side = 0; side < 2; ++side)
+            if (te[side] >= 0) out[u.row0 + (long long)i * a.V + te[side]] = stage(g, lane >> 3)[phase_of(u, i) + te[side]];
+        }
+        if (lane < n) {
+          const int i = i0 + lane, ph = phase_of(u, i), head = head_of(u, ph), bytes = (u.n_tok - head) / VEC * 16;
+          if (bytes) bulk_store(out + u.row0 + (long long)i * a.V + head, stage(g, lane) + (ph ? VEC : 0), (unsigned)bytes);
+        }
+      }
+      bulk_commit();
+      // the batch before this one has left its stages: the next one goes there
+      if (g > 0 && lu.rows) {
+        bulk_wait_read<1>();
+        __syncwarp();
+        load_next();
+      }
+    }
+    if (next >= total) break;
+    u = nu;
   }
+  bulk_wait_read<0>();
+}
+
+template <class T, bool kShifted, bool kMask>
+__global__ void __launch_bounds__(kProcThreads, 4) process_in_place_kernel(const __grid_constant__ ProcessArgs a) {
+  using Ty = ProcType<T>;
+  using S = typename Ty::storage;
+  constexpr int VEC = Ty::kVec;
+  constexpr int kVecs = kProcPiece / VEC / 32;  // vectors of a piece per lane
+  constexpr int RU = 8 / kVecs;                 // rows whose vectors are in flight
+  constexpr unsigned kAll = (1u << VEC) - 1u;
+  __shared__ __align__(16) ProcShared sh;
+  __shared__ ProcPaths s_paths;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const ProcUnit u = proc_unit(a, blockIdx.x);
+  ProcShare c;
+  c.paths = &s_paths;
+  const ProcAhead ahead = proc_ahead(a, u);
+  S* z = (S*)a.out + u.row0;
+  const int rows = u.n_tok > 0 ? u.rows : 0;
+  auto phase_of = [&](int i) { return kShifted ? (int)((u.row0 + (long long)i * a.V + a.phase) & (VEC - 1)) : 0; };
+  const uint32_t* mask0 = kMask ? a.mask + ((long long)u.b * a.mask_rows + (a.mask_rows > 1 ? u.r0 : 0)) * a.W + (u.start >> 5) : nullptr;
+  const int mask_step = a.mask_rows > 1 ? a.W : 0;
+  const int mask_words = min(kProcPiece / 32, a.W - (u.start >> 5));
+  auto mask_word = [&](int i) {
+    const unsigned hi = lane < mask_words && i < rows ? __ldg(mask0 + (long long)i * mask_step + lane) : 0xffffffffu;
+    if constexpr (!kShifted) return hi;
+    const unsigned lo = __shfl_up_sync(0xffffffffu, hi, 1);
+    return __funnelshift_l(lane ? lo : 0xffffffffu, hi, phase_of(i));
+  };
+  auto allowed_at = [&](int i, int t) {
+    return !kMask || (__ldg((const uint8_t*)(mask0 + (long long)i * mask_step) + (t >> 3)) >> (t & 7) & 1u);
+  };
+
+  // ---- forbidden tokens ----
+  if constexpr (kMask) {
+    for (int rb = 0; rb < rows; rb += RU) {
+      unsigned word[RU], bits[RU][kVecs];
+      uint4 x[RU][kVecs];
+#pragma unroll
+      for (int i = 0; i < RU; ++i) word[i] = mask_word(rb + i);
+#pragma unroll
+      for (int i = 0; i < RU; ++i) {
+        const int ph = phase_of(rb + i), v0 = ph ? 1 : 0;
+        const int v1 = (u.n_tok + ph) / VEC;  // the lattice's whole vectors of the piece: v0 .. v1 - 1
+        const S* row = z + (long long)(rb + i) * a.V - ph;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+          const int v = 32 * k + lane;
+          bits[i][k] = __shfl_sync(0xffffffffu, word[i], v * VEC >> 5) >> (v * VEC & 31) & kAll;
+          if (v < v0 || v >= v1) bits[i][k] = kAll;
+          if (bits[i][k] != kAll && bits[i][k]) x[i][k] = *(const uint4*)(row + v * VEC);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RU; ++i) {
+        const int ph = phase_of(rb + i);
+        S* row = z + (long long)(rb + i) * a.V - ph;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+          if (bits[i][k] != kAll) *(uint4*)(row + (32 * k + lane) * VEC) = proc_keep<T>(x[i][k], bits[i][k]);
+        if (kShifted && rb + i < rows) {
+          // the elements before the first and after the last whole vector
+          const int head = ph ? min(VEC - ph, u.n_tok) : 0, tail = max(head, (u.n_tok + ph) / VEC * VEC - ph);
+          const int t = lane < 16 ? lane : tail + lane - 16;
+          if ((lane < 16 ? t < head : t < u.n_tok) && !allowed_at(rb + i, t)) row[ph + t] = Ty::kNegInf;
+        }
+      }
+    }
+  }
+
+  proc_lists(a, sh, u, ahead, c);
+  if (c.bad) {
+    for (int i = 0; i < rows; ++i)
+      for (int t = lane; t < u.n_tok; t += 32) z[(long long)i * a.V + t] = Ty::kNan;
+    return;
+  }
+  // ---- listed tokens ----
+  for (int rb = 0; rb < rows; rb += kProcRows)
+    for (int e = lane; e < c.n_list; e += 32) {
+      const unsigned entry = sh.list[warp * kProcPiece + e];
+      const int t = (int)(entry & kProcOffset) - warp * kProcPiece;
+      const float add = sh.adj[entry & kProcOffset];
+      S* at = z + (long long)rb * a.V + t;
+      bool on[kProcRows];
+      S v[kProcRows];
+#pragma unroll
+      for (int i = 0; i < kProcRows; ++i) on[i] = rb + i < rows && allowed_at(rb + i, t);
+#pragma unroll
+      for (int i = 0; i < kProcRows; ++i)
+        if (on[i]) v[i] = at[(long long)i * a.V];
+      ProcTerm term = proc_term(c, entry & kProcSeen, add);
+#pragma unroll
+      for (int i = 0; i < kProcRows; ++i)
+        if (on[i]) {
+          if (entry & kProcDraft) term = proc_draft_term(a, sh, u, c, entry, add, u.r0 + rb + i);
+          at[(long long)i * a.V] = Ty::round(term(Ty::widen(v[i])));
+        }
+    }
 }
 
 int process_chunk() { return kProcChunk; }
 int process_tree_rows() { return kProcTreeRows; }
+int process_blocks_per_sm() { return 2; }
 
 template <class T>
-static void launch_one(const ProcessArgs& a, bool shifted, unsigned grid, cudaStream_t s) {
-  const bool in_place = a.in == a.out;
-  if (shifted && in_place)
-    process_kernel<T, true, true><<<grid, kProcThreads, 0, s>>>(a);
-  else if (shifted)
-    process_kernel<T, true, false><<<grid, kProcThreads, 0, s>>>(a);
-  else if (in_place)
-    process_kernel<T, false, true><<<grid, kProcThreads, 0, s>>>(a);
-  else
-    process_kernel<T, false, false><<<grid, kProcThreads, 0, s>>>(a);
+static int copy_smem(bool tree) { return (int)(sizeof(ProcCopyShared<T>) + (tree ? sizeof(ProcPaths) : 0)); }
+
+template <class T>
+static cudaError_t allow_smem() {
+  cudaError_t e = cudaSuccess;
+  auto one = [&](const void* f) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, copy_smem<T>(true));
+  };
+  one((const void*)process_kernel<T, false, false>);
+  one((const void*)process_kernel<T, false, true>);
+  one((const void*)process_kernel<T, true, false>);
+  one((const void*)process_kernel<T, true, true>);
+  return e;
+}
+cudaError_t process_configure() {
+  const cudaError_t e = allow_smem<float>();
+  return e != cudaSuccess ? e : allow_smem<Bf16Tag>();
 }
 
-cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s) {
-  const unsigned grid = (unsigned)((long long)a.B * a.groups * a.chunks);
+template <class T, bool kShifted, bool kMask>
+static void launch_one(const ProcessArgs& a, int capacity, cudaStream_t s) {
+  const unsigned units = (unsigned)a.B * (unsigned)a.groups * (unsigned)a.chunks;
+  if (a.in == a.out)
+    process_in_place_kernel<T, kShifted, kMask><<<units, kProcThreads, 0, s>>>(a);
+  else
+    process_kernel<T, kShifted, kMask>
+        <<<units < (unsigned)capacity ? units : (unsigned)capacity, kProcThreads, copy_smem<T>(a.parents != nullptr), s>>>(a);
+}
+template <class T>
+static void launch_type(const ProcessArgs& a, bool shifted, int capacity, cudaStream_t s) {
+  if (shifted && a.mask)
+    launch_one<T, true, true>(a, capacity, s);
+  else if (shifted)
+    launch_one<T, true, false>(a, capacity, s);
+  else if (a.mask)
+    launch_one<T, false, true>(a, capacity, s);
+  else
+    launch_one<T, false, false>(a, capacity, s);
+}
+
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, int capacity, cudaStream_t s) {
   const int esz = bf16 ? 2 : 4;
   const unsigned in_off = (unsigned)((uintptr_t)a.in & 15), out_off = (unsigned)((uintptr_t)a.out & 15);
   ProcessArgs k = a;
   k.phase = (int)in_off / esz;
   k.split = in_off != out_off;
-  const bool shifted = in_off || (long long)a.V * esz % 16;
+  const bool shifted = in_off || out_off || (long long)a.V * esz % 16;
   if (bf16)
-    launch_one<Bf16Tag>(k, shifted, grid, s);
+    launch_type<Bf16Tag>(k, shifted, capacity, s);
   else
-    launch_one<float>(k, shifted, grid, s);
+    launch_type<float>(k, shifted, capacity, s);
   return cudaGetLastError();
 }
+
+cudaError_t process_set_spin_limit(unsigned n) { return set_spin_limit_here(n); }
 
 }  // namespace sv

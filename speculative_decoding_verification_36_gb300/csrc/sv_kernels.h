@@ -295,8 +295,12 @@ struct ProcessArgs {
   unsigned* status;
 };
 int process_chunk();      // tokens of one CTA's chunk
+cudaError_t process_configure();  // once per device, before the first launch
+cudaError_t process_set_spin_limit(unsigned n);
 int process_tree_rows();  // most rows of a group when the drafts form a tree
-cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s);
+int process_blocks_per_sm();  // CTAs at once per SM (not in place)
+// capacity: CTAs of the persistent grid at most
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, int capacity, cudaStream_t s);
 
 // The paged key/value cache's append and commit (kv_kernel.cu).
 struct KvAppendArgs {
