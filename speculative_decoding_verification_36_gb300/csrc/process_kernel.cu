@@ -79,10 +79,9 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
 // lists its own, with the additive term -f c - p [c > 0] + biases.  After the
 // lists no barrier joins the warps.
 //
-// Apart from its input (process_kernel): a warp's part of a row travels global
-// -> shared -> global by bulk copies, kBatch rows at a time and the next batch
-// in flight, and the list and the mask are applied to it in shared memory.  Per row a warp visits its list
-// and, with a mask, its vectors; without one no instruction sees the rest.
+// Apart from its input (process_kernel): a warp's parts of kBatch rows at a time
+// come to shared memory by bulk copies, with further batches behind them; the
+// list is applied to them there, and they go out through registers, masked.
 // In place (process_in_place_kernel): only the listed tokens and the vectors
 // that hold a forbidden one are read and written, where they lie.
 constexpr int kProcThreads = 256;
@@ -109,6 +108,7 @@ struct ProcShared {
   unsigned bias[kProcWords];        // tokens with a bias
   unsigned draft[kProcWords];       // tokens that some draft carries
   unsigned drafts[kProcDrafts];     // drafts in the chunk: (offset << 16) | node
+  int4 own[kProcThreads];           // per lane: offset and flags (-1: no terms), node (-1: none), lanes with the token, terms
   int n_draft;
   int twice;  // a token with several biases
   int bad, pad;
@@ -124,7 +124,7 @@ struct ProcType;
 template <>
 struct ProcType<float> {
   using storage = uint32_t;
-  static constexpr int kVec = 4, kBatch = 2, kBatches = 2;
+  static constexpr int kVec = 4, kBatch = 1, kBatches = 2;
   static constexpr uint32_t kNegInf = 0xff800000u, kNan = 0x7fc00000u;
   static __device__ __forceinline__ float widen(uint32_t w) { return __uint_as_float(w); }
   static __device__ __forceinline__ uint32_t round(float f) { return __float_as_uint(f); }
@@ -132,7 +132,7 @@ struct ProcType<float> {
 template <>
 struct ProcType<Bf16Tag> {
   using storage = uint16_t;
-  static constexpr int kVec = 8, kBatch = 3, kBatches = 3;
+  static constexpr int kVec = 8, kBatch = 2, kBatches = 2;
   static constexpr uint16_t kNegInf = 0xff80u, kNan = 0x7fc0u;
   static __device__ __forceinline__ float widen(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
   static __device__ __forceinline__ uint16_t round(float f) {
@@ -145,7 +145,7 @@ struct ProcType<Bf16Tag> {
 // A warp's rows in flight: a piece each, and its phase.
 template <class T>
 struct alignas(16) ProcStages {
-  static constexpr int kStage = kProcPiece + 2 * ProcType<T>::kVec;
+  static constexpr int kStage = kProcPiece + ProcType<T>::kVec;
   typename ProcType<T>::storage row[ProcType<T>::kBatches][ProcType<T>::kBatch][kStage];
 };
 template <class T>
@@ -203,6 +203,10 @@ struct ProcShare {
   float rep, inv, freq, pres;
   bool bad;
   ProcPaths* paths;
+  // Up to 32 drafts in the chunk: their tokens are not in the list, but lane i
+  // has draft i (ProcShared::own), and its token's terms where it is the lowest
+  // lane that carries the token and the token is the warp's.
+  bool few, here;  // ... so; some lane of the warp has terms
 };
 
 // What a unit's lists are made from, on its way into a thread's registers: the
@@ -255,6 +259,13 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   c.freq = h.freq;
   c.pres = h.pres;
   c.inv = 1.f / c.rep;
+  if (!a.state && !N && !a.n_bias) {
+    c.n_list = 0;
+    c.here = false;
+    c.bad = !(c.rep > 0.f && c.rep < INFINITY) || !(fabsf(c.freq) < INFINITY) || !(fabsf(c.pres) < INFINITY);
+    if (c.bad && tid == 0) atomicOr(a.status, kStatusBadData);
+    return;
+  }
   __syncthreads();
   if (tid < kProcWords) {
     sh.bias[tid] = 0u;
@@ -290,8 +301,11 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   c.bad = sh.bad || !(c.rep > 0.f && c.rep < INFINITY) || !(fabsf(c.freq) < INFINITY) || !(fabsf(c.pres) < INFINITY);
   if (c.bad && tid == 0) atomicOr(a.status, kStatusBadData);
 
+  const int n_draft = sh.n_draft;
+  c.few = n_draft <= 32;
   const unsigned draft = (sh.draft[tid >> 1] >> (16 * (tid & 1))) & 0xffffu;
-  unsigned touch = mine | draft | ((sh.bias[tid >> 1] >> (16 * (tid & 1))) & 0xffffu);
+  unsigned touch = mine | ((sh.bias[tid >> 1] >> (16 * (tid & 1))) & 0xffffu);
+  touch = c.few ? touch & ~draft : touch | draft;
   int at = __popc(touch);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -323,6 +337,23 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
     }
   }
   __syncwarp();
+  c.here = false;
+  if (c.few && n_draft > 0) {
+    const unsigned d = lane < n_draft ? sh.drafts[lane] : 0xffffffffu;
+    int off = lane < n_draft ? (int)(d >> 16) : -1 - lane;
+    const unsigned same = __match_any_sync(0xffffffffu, off);
+    const unsigned bits = __shfl_sync(0xffffffffu, mine, off >> 4 & 31);
+    if (off < 0 || off >> 9 != tid >> 5 || lane != __ffs(same) - 1) off = -1;
+    c.here = __any_sync(0xffffffffu, off >= 0);
+    if (c.here) {
+      const bool seen = off >= 0 && (bits >> (off & 15) & 1u);
+      const int n = seen ? __ldg(state + u.base + off) & 0x7fffffff : 0;
+      float add = off >= 0 && (sh.bias[off >> 5] >> (off & 31) & 1u) ? sh.adj[off] : 0.f;
+      if (n > 0) add += -c.freq * (float)n - c.pres;
+      if (off >= 0) off |= (seen ? kProcSeen : 0u) | (n > 0 ? kProcCounted : 0u);
+      sh.own[tid] = make_int4(off, lane < n_draft ? (int)(d & 0xffffu) : -1, (int)same, __float_as_int(add));
+    }
+  }
   for (int e = lane; e < c.n_list; e += 32) {
     const unsigned entry = sh.list[lo + e];
     const int off = entry & kProcOffset, n = entry & kProcSeen ? __ldg(state + u.base + off) & 0x7fffffff : 0;
@@ -333,7 +364,7 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
     }
     sh.adj[off] = adj;
   }
-  if (a.parents && sh.n_draft > 0) {
+  if (a.parents && n_draft > 0) {
     // the nodes above each row of the group; a parent precedes its child
     const int W = (N + 31) >> 5;
     if (!c.bad)
@@ -388,6 +419,19 @@ __device__ __forceinline__ ProcTerm proc_draft_term(const ProcessArgs& a, const 
   return proc_term(c, (entry & kProcSeen) || extra, add);
 }
 
+// The terms that a lane has of its own (ProcShared::own) in row r.
+__device__ __forceinline__ ProcTerm proc_own_term(const ProcessArgs& a, const ProcUnit& u, const ProcShare& c, int4 own, int r) {
+  const int j = own.y;
+  const bool on = j >= 0 && (a.parents ? (c.paths->row[r - u.r0][j >> 5] >> (j & 31) & 1u) : j < r);
+  const int extra = __popc(__ballot_sync(0xffffffffu, on) & (unsigned)own.z);
+  float add = __int_as_float(own.w);
+  if (extra) {
+    add -= c.freq * (float)extra;
+    if (!(own.x & kProcCounted)) add -= c.pres;
+  }
+  return proc_term(c, (own.x & kProcSeen) || extra, add);
+}
+
 // kShifted: rows start off 16-byte boundaries (the vocabulary's size, or the
 // buffers).  A row keeps its phase in shared memory: element t of the piece
 // lies at phase + t, whole 16-byte vectors move by bulk copies, and the few
@@ -398,10 +442,11 @@ __device__ __forceinline__ ProcTerm proc_draft_term(const ProcessArgs& a, const 
 // the lists of this one wait for their counts.  (One CTA per unit, with the
 // same passes: 343 us for B = 256, R = 9, V = 152064 in bf16, everything on.)
 template <class T, bool kShifted, bool kMask>
-__global__ void __launch_bounds__(kProcThreads, 2) process_kernel(const __grid_constant__ ProcessArgs a) {
+__global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_constant__ ProcessArgs a) {
   using Ty = ProcType<T>;
   using S = typename Ty::storage;
   constexpr int VEC = Ty::kVec, RB = Ty::kBatch, NB = Ty::kBatches;
+  constexpr int kVecs = kProcPiece / VEC / 32;  // vectors of a piece per lane
   constexpr unsigned kAll = (1u << VEC) - 1u;
   extern __shared__ __align__(16) unsigned char s_raw[];
   ProcCopyShared<T>& sh = *(ProcCopyShared<T>*)s_raw;
@@ -417,12 +462,12 @@ __global__ void __launch_bounds__(kProcThreads, 2) process_kernel(const __grid_c
   auto stage = [&](int g, int j) { return sh.stages[warp].row[g % NB][j]; };
 
   if (lane == 0) {
-    for (int k = 0; k < NB; ++k) mbar_init(&sh.full[warp][k], 1);
+    for (int k = 0; k < NB; ++k) mbar_init(&sh.full[warp][k], RB);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
 
-  // ---- the ring: batch g sets out, lane j with row j's copy ----
+  // ---- the ring: a batch sets out, lane j with row j's copy ----
   unsigned load_round = 0;
   ProcUnit lu = proc_unit(a, unit_of(0));  // the unit, the batch of it and the batch of the ring that set out next
   int load_batch = 0, load_g = 0;
@@ -438,22 +483,17 @@ __global__ void __launch_bounds__(kProcThreads, 2) process_kernel(const __grid_c
       load_batch = 0;
     }
     const int i = load_batch * RB + lane;
-    int bytes = 0, ph = 0, head = 0;
-    if (lane < RB && i < lu.rows) {
-      ph = phase_of(lu, i);
-      head = head_of(lu, ph);
-      bytes = (lu.n_tok - head) / VEC * 16;
-    }
-    const int sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)bytes);
-    unsigned long long* bar = &sh.full[warp][load_g % NB];
-    if (lane == 0) {
-      if (sum)
-        mbar_arrive_tx(bar, (unsigned)sum);
-      else
+    if (lane < RB) {
+      // each of the batch's lanes arrives, with its row's bytes
+      const int ph = phase_of(lu, i), head = head_of(lu, ph), bytes = i < lu.rows ? (lu.n_tok - head) / VEC * 16 : 0;
+      unsigned long long* bar = &sh.full[warp][load_g % NB];
+      if (bytes) {
+        mbar_arrive_tx(bar, (unsigned)bytes);
+        bulk_load(stage(load_g, lane) + (ph ? VEC : 0), in + lu.row0 + (long long)i * a.V + head, (unsigned)bytes, bar);
+      } else {
         mbar_arrive(bar);
+      }
     }
-    __syncwarp();
-    if (bytes) bulk_load(stage(load_g, lane) + (ph ? VEC : 0), in + lu.row0 + (long long)i * a.V + head, (unsigned)bytes, bar);
     ++load_batch;
     ++load_g;
   };
@@ -461,9 +501,12 @@ __global__ void __launch_bounds__(kProcThreads, 2) process_kernel(const __grid_c
     if (lu.rows) load_next();
 
   // ---- masks and edge elements of the next batch, one batch ahead ----
-  // A lane holds the mask bits of 16 tokens, of the rows of a batch.
+  // Lane w holds word w of the piece's mask, of the rows of a batch.
   auto mask_row = [&](const ProcUnit& u, int i) {
     return a.mask + ((long long)u.b * a.mask_rows + (a.mask_rows > 1 ? u.r0 + i : 0)) * a.W + (u.start >> 5);
+  };
+  auto allowed_at = [&](const ProcUnit& u, int i, int t) {
+    return !kMask || (__ldg((const uint8_t*)mask_row(u, i) + (t >> 3)) >> (t & 7) & 1u);
   };
   unsigned next_word[RB];
   // Eight lanes a row: first its elements before its first vector, then those after its last.
@@ -479,7 +522,7 @@ __global__ void __launch_bounds__(kProcThreads, 2) process_kernel(const __grid_c
 #pragma unroll
       for (int j = 0; j < RB; ++j) {
         const int i = batch * RB + j;
-        next_word[j] = i < u.rows && 16 * lane < u.n_tok ? __ldg((const unsigned short*)mask_row(u, i) + lane) : 0xffffu;
+        next_word[j] = i < u.rows && 32 * lane < u.n_tok ? __ldg(mask_row(u, i) + lane) : 0xffffffffu;
       }
     }
     if constexpr (kShifted) {
@@ -504,26 +547,21 @@ __global__ void __launch_bounds__(kProcThreads, 2) process_kernel(const __grid_c
   for (unsigned round = 0;; ++round) {
     proc_lists(a, sh, u, ahead, c);
     const unsigned next = unit_of(round + 1);
-    ProcUnit nu = u;
-    if (next < total) {
-      nu = proc_unit(a, next);
-      ahead = proc_ahead(a, nu);
-    }
+    if (next < total) ahead = proc_ahead(a, proc_unit(a, next));
     for (int i0 = 0; i0 < u.rows; i0 += RB, ++g) {
       const int n = min(RB, u.rows - i0);
       unsigned word[RB];
 #pragma unroll
-      for (int j = 0; j < RB; ++j) word[j] = kMask ? next_word[j] : 0xffffu;
+      for (int j = 0; j < RB; ++j) word[j] = kMask ? next_word[j] : 0xffffffffu;
       const S mine[2] = {edge[0], edge[1]};
       if (i0 + RB < u.rows)
         look(u, i0 / RB + 1);
       else if (next < total)
-        look(nu, 0);
+        look(proc_unit(a, next), 0);
       if (!dead && !warp_wait(&sh.full[warp][g % NB], (g / NB) & 1, limit)) {
         // a copy that never came: this warp hands out nothing more, and waits
         // for what is in flight, so that no copy outlives the CTA's memory
         if (lane == 0) atomicOr(a.status, kStatusTimeout);
-        bulk_wait_read<0>();
         for (int q = g; q < load_g; ++q) warp_wait(&sh.full[warp][q % NB], (q / NB) & 1, kSpinLimit);
         dead = true;
       }
@@ -553,73 +591,69 @@ __global__ void __launch_bounds__(kProcThreads, 2) process_kernel(const __grid_c
             *at = Ty::round(term(Ty::widen(*at)));
           }
       }
-      if constexpr (kMask) {
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < RB; ++j) {
-          unsigned w = word[j];
-          if constexpr (kShifted) {
-            // the bits of the 16-byte lattice: of the elements 16 lane .. from
-            // the boundary below the piece
-            const unsigned below = __shfl_up_sync(0xffffffffu, w, 1);
-            w = ((lane ? below : 0xffffu) | w << 16) >> (16 - phase_of(u, i0 + j)) & 0xffffu;
-          }
-          if (w == 0xffffu) continue;
-          uint4* x = (uint4*)stage(g, j) + lane * (16 / VEC);
-#pragma unroll
-          for (int q = 0; q < 16 / VEC; ++q) {
-            // lanes take their vectors in orders that spread over the banks
-            const int v = q ^ (lane * (16 / VEC) >> 3 & (16 / VEC - 1));
-            const unsigned bits = w >> (v * VEC) & kAll;
-            if (bits != kAll) x[v] = proc_keep<T>(x[v], bits);
+      if (c.here && !c.bad) {
+        const int4 own = sh.own[threadIdx.x];
+        for (int j = 0; j < n; ++j) {
+          const ProcTerm term = proc_own_term(a, u, c, own, u.r0 + i0 + j);
+          if (own.x >= 0) {
+            S* at = stage(g, j) + phase_of(u, i0 + j) + (own.x & kProcOffset) - warp * kProcPiece;
+            *at = Ty::round(term(Ty::widen(*at)));
           }
         }
-        if constexpr (kShifted) {
-          // the edges, also those in no vector of the loop's
-          __syncwarp();
-          const int i = i0 + (lane >> 3);
-#pragma unroll
-          for (int side = 0; side < 2; ++side)
-            if (te[side] >= 0 && !(__ldg((const uint8_t*)mask_row(u, i) + (te[side] >> 3)) >> (te[side] & 7) & 1u))
-              stage(g, lane >> 3)[phase_of(u, i) + te[side]] = Ty::kNegInf;
-        }
       }
-      if (c.bad) {
-        __syncwarp();
-        for (int j = 0; j < n; ++j)
-          for (int t = lane; t < u.n_tok; t += 32) stage(g, j)[phase_of(u, i0 + j) + t] = Ty::kNan;
-      }
-      fence_async();
+      // the rows go out: shared -> registers, masked, -> global
       __syncwarp();
-      if (kShifted && a.split) {
+      if (c.bad) {
+        for (int j = 0; j < n; ++j)
+          for (int t = lane; t < u.n_tok; t += 32) out[u.row0 + (long long)(i0 + j) * a.V + t] = Ty::kNan;
+      } else if (kShifted && a.split) {
         // the output's vectors lie at another phase: element by element
         for (int j = 0; j < n; ++j)
           for (int t = lane; t < u.n_tok; t += 32)
-            out[u.row0 + (long long)(i0 + j) * a.V + t] = stage(g, j)[phase_of(u, i0 + j) + t];
+            out[u.row0 + (long long)(i0 + j) * a.V + t] =
+                allowed_at(u, i0 + j, t) ? stage(g, j)[phase_of(u, i0 + j) + t] : Ty::kNegInf;
       } else {
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+          if (j >= n) break;
+          const int ph = phase_of(u, i0 + j);
+          unsigned w = word[j];
+          if constexpr (kShifted && kMask) {
+            // the bits of the 16-byte lattice
+            const unsigned below = __shfl_up_sync(0xffffffffu, w, 1);
+            w = __funnelshift_l(lane ? below : 0xffffffffu, w, ph);
+          }
+          const uint4* x = (const uint4*)stage(g, j);
+          S* to = out + u.row0 + (long long)(i0 + j) * a.V - ph;
+          const int v0 = kShifted && ph ? 1 : 0, v1 = (u.n_tok + ph) / VEC;  // whole vectors of the piece
+#pragma unroll
+          for (int q = 0; q < kVecs; ++q) {
+            const int v = 32 * q + lane;  // of the lattice
+            const unsigned bits = kMask ? __shfl_sync(0xffffffffu, w, v * VEC >> 5) >> (v * VEC & 31) & kAll : kAll;
+            if (v >= v0 && v < v1) {
+              uint4 y = x[v];
+              if (kMask && bits != kAll) y = proc_keep<T>(y, bits);
+              *(uint4*)(to + v * VEC) = y;
+            }
+          }
+        }
         if constexpr (kShifted) {
           const int i = i0 + (lane >> 3);
 #pragma unroll
           for (int side = 0; side < 2; ++side)
-            if (te[side] >= 0) out[u.row0 + (long long)i * a.V + te[side]] = stage(g, lane >> 3)[phase_of(u, i) + te[side]];
-        }
-        if (lane < n) {
-          const int i = i0 + lane, ph = phase_of(u, i), head = head_of(u, ph), bytes = (u.n_tok - head) / VEC * 16;
-          if (bytes) bulk_store(out + u.row0 + (long long)i * a.V + head, stage(g, lane) + (ph ? VEC : 0), (unsigned)bytes);
+            if (te[side] >= 0)
+              out[u.row0 + (long long)i * a.V + te[side]] =
+                  allowed_at(u, i, te[side]) ? stage(g, lane >> 3)[phase_of(u, i) + te[side]] : Ty::kNegInf;
         }
       }
-      bulk_commit();
-      // the batch before this one has left its stages: the next one goes there
-      if (g > 0 && lu.rows) {
-        bulk_wait_read<1>();
-        __syncwarp();
-        load_next();
-      }
+      // the stages are free: the next batch goes there
+      fence_async();
+      __syncwarp();
+      if (lu.rows) load_next();
     }
     if (next >= total) break;
-    u = nu;
+    u = proc_unit(a, next);
   }
-  bulk_wait_read<0>();
 }
 
 template <class T, bool kShifted, bool kMask>
@@ -718,11 +752,22 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_in_place_kernel(const
           at[(long long)i * a.V] = Ty::round(term(Ty::widen(v[i])));
         }
     }
+  if (c.here) {
+    const int4 own = sh.own[threadIdx.x];
+    const int t = (own.x & kProcOffset) - warp * kProcPiece;
+    for (int i = 0; i < rows; ++i) {
+      const ProcTerm term = proc_own_term(a, u, c, own, u.r0 + i);
+      if (own.x >= 0 && allowed_at(i, t)) {
+        S* at = z + (long long)i * a.V + t;
+        *at = Ty::round(term(Ty::widen(*at)));
+      }
+    }
+  }
 }
 
 int process_chunk() { return kProcChunk; }
 int process_tree_rows() { return kProcTreeRows; }
-int process_blocks_per_sm() { return 2; }
+int process_blocks_per_sm() { return 3; }
 
 template <class T>
 static int copy_smem(bool tree) { return (int)(sizeof(ProcCopyShared<T>) + (tree ? sizeof(ProcPaths) : 0)); }
