@@ -416,8 +416,8 @@ int spec_ngram_draft(const int32_t *tokens, const int32_t *lengths, int B, int s
  * Token counts, the state behind the penalties of spec_process_logits_*.
  *
  * The state is an int32 device array [B, words], words =
- * spec_token_state_words(V), that the caller owns and zeroes (all zeros: no
- * tokens yet).  Row b holds, with P = V rounded up to a multiple of 32:
+ * spec_token_state_words(V), on a 16-byte boundary, that the caller owns and
+ * zeroes (all zeros: no tokens yet).  Row b holds, with P = V rounded up to a multiple of 32:
  *   words 0 .. P - 1          token v: bits 0..30 its occurrences among the
  *                             output tokens, bit 31 set when it is in the prompt
  *   words P .. P + P / 32 - 1 bit v % 32 of word P + v / 32: word v is not zero
@@ -441,8 +441,8 @@ int spec_token_state_words(int V);
  *   reset          not 0: the rows are zeroed first.
  * Bad data: a length outside [0, stride] or a prompt length outside [0,
  * length] adds nothing to that row and sets SPEC_FLAG_BAD_DATA.  Counts are
- * exact.  Returns SPEC_OK, SPEC_ERR_NULL, SPEC_ERR_SHAPE (B < 0, stride < 0, V)
- * or SPEC_ERR_CUDA.  Asynchronous on `stream`; no scratch.
+ * exact.  Returns SPEC_OK, SPEC_ERR_NULL, SPEC_ERR_SHAPE (B < 0, stride < 0, V,
+ * a state off a 16-byte boundary) or SPEC_ERR_CUDA.  Asynchronous on `stream`; no scratch.
  */
 int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32_t *prompt_lengths, int B,
                       int stride, int V, int reset, int32_t *state, cudaStream_t stream);
@@ -474,7 +474,7 @@ int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32
  *   z2 = z1 - frequency * c - presence * (c > 0) + bias
  *   out = allowed ? z2 : -inf
  * in fp32 and rounded once.  A masked token is -inf whatever its logit was
- * (NaN included); a row with nothing allowed is all -inf, which a verify
+ * (NaN included), and a logit of -inf stays -inf whatever is added; a row with nothing allowed is all -inf, which a verify
  * reports as bad data, as it does a NaN that is allowed.
  * Bad data: a parent index outside [-1, i), a repetition that is not positive
  * and finite, or a frequency or presence that is not finite makes every row of
@@ -530,7 +530,8 @@ int spec_process_logits_bf16(const uint16_t *logits, const int32_t *draft_tokens
  * max_pages * page_size or a parent index outside [-1, i): nothing of that
  * sequence is written to the caches and its out_q rows are NaN.  A page index
  * outside [0, pages): the tokens of that page are not written to the caches.
- * T >= 0 (<= 1025 with parent_idx), 1 <= D <= 1024.  Returns SPEC_OK,
+ * T >= 0 (<= 1025 with parent_idx), 1 <= D <= 1024, Hkv * D and Hq * D up to
+ * 2^24.  Returns SPEC_OK,
  * SPEC_ERR_NULL, SPEC_ERR_SHAPE or SPEC_ERR_CUDA.  One launch on `stream`; no
  * scratch.
  */

@@ -373,13 +373,22 @@ def _arg(t, dtype, shape, device, name):
     raise ValueError(f"{name} cannot be used")
 
 
+# the handle of a device's current stream without a Stream object around it
+# (0.1 us, where torch.cuda.current_stream().cuda_stream takes 2.8)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _invoke(fn, device, stream, *args):
     """Calls a C entry point on `device`, its current stream by default."""
-    if torch.cuda.current_device() == device.index:
-        _lib.check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)))
+    index = device.index
+    if torch.cuda.current_device() == index:
+        code = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(device):
-            _lib.check(fn(*args, _stream(stream)))
+            code = fn(*args, _stream(stream))
+    if code:
+        _lib.check(code)
 
 
 def _words(V: int) -> int:
@@ -471,13 +480,16 @@ def _token_stride(t, name, dtype, shape, device):
     """Elements between successive tokens of a [B, T, H, D] tensor whose tokens
     lie at equal distances and whose heads are contiguous (such as a slice of a
     joint projection)."""
+    B, T, H, D = shape
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        sb, st, sh, sd = t.stride()
+        if sd == 1 and sh == D and sb == T * st:
+            return st
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
         raise ValueError(f"{name} must be a {dtype} CUDA tensor")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        _same_device(t, device, name)
-    B, T, H, D = shape
+    _same_device(t, device, name)
     sb, st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}'s heads must be contiguous")

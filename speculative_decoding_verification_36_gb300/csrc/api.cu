@@ -552,6 +552,7 @@ int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int
   if (B == 0) return SPEC_OK;
   if (!logits || !out || (parents && !drafts) || (n_bias > 0 && (!bias_tokens || !bias_values)))
     return SPEC_ERR_NULL;
+  if (!aligned16(state)) return SPEC_ERR_SHAPE;
   const size_t esz = bf16 ? 2 : 4;
   const size_t bytes = (size_t)B * R * V * esz;
   if (logits != out && overlaps(logits, bytes, out, bytes)) return SPEC_ERR_OVERLAP;
@@ -602,8 +603,8 @@ int kv_append_impl(bool bf16, const void* k, const void* v, int64_t kv_stride, c
                    void* v_cache, int pages, int page_size, int max_pages, cudaStream_t stream) {
   if (B < 0 || T < 0 || Hq < 0 || Hkv < 1 || D < 1 || D > sv::kv_max_rot() || rot < 0 || rot > D ||
       rot % 2 || pages < 1 || page_size < 1 || max_pages < 1 ||
-      (parents && T > sv::kMaxTreeNodes + 1) || (long long)Hkv * D > INT_MAX / 8 ||
-      (long long)Hq * D > INT_MAX / 8 || kv_stride < (long long)Hkv * D ||
+      (parents && T > sv::kMaxTreeNodes + 1) || (long long)Hkv * D > (1 << 24) ||
+      (long long)Hq * D > (1 << 24) || kv_stride < (long long)Hkv * D ||
       (Hq > 0 && q_stride < (long long)Hq * D) || (long long)B * T > INT_MAX)
     return SPEC_ERR_SHAPE;
   if (B == 0 || T == 0) return SPEC_OK;
@@ -639,6 +640,7 @@ int kv_append_impl(bool bf16, const void* k, const void* v, int64_t kv_stride, c
   const int rc = get_device_state(&d);
   if (rc) return rc;
   a.status = d->status;
+  a.sms = d->sms;
   const int ve = bf16 ? 8 : 4;
   const bool vec = aligned16(k) && aligned16(v) && aligned16(k_cache) && aligned16(v_cache) &&
                    kv_stride % ve == 0 && D % ve == 0 && rot % (interleaved ? ve : 2 * ve) == 0 &&
@@ -880,6 +882,7 @@ int spec_count_tokens(const int32_t* tokens, const int32_t* lengths, const int32
   if (B < 0 || stride < 0 || V < 1 || V > kMaxStateVocab) return SPEC_ERR_SHAPE;
   if (B == 0) return SPEC_OK;
   if (!state || (stride > 0 && !tokens)) return SPEC_ERR_NULL;
+  if (!aligned16(state)) return SPEC_ERR_SHAPE;
   DeviceState* d = nullptr;
   const int rc = get_device_state(&d);
   if (rc) return rc;

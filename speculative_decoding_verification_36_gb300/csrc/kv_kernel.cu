@@ -18,233 +18,341 @@
 
 namespace sv {
 
-constexpr int kKvThreads = 256;
-constexpr int kKvTokens = 4;  // tokens of a CTA
+constexpr int kKvThreads = 128;
+constexpr int kKvWarps = kKvThreads / 32;
 
-template <class S>
-__device__ __forceinline__ float kv_widen(S w);
-template <>
-__device__ __forceinline__ float kv_widen<uint32_t>(uint32_t w) { return __uint_as_float(w); }
-template <>
-__device__ __forceinline__ float kv_widen<uint16_t>(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
-template <class S>
-__device__ __forceinline__ S kv_round(float f);
-template <>
-__device__ __forceinline__ uint32_t kv_round<uint32_t>(float f) { return __float_as_uint(f); }
-template <>
-__device__ __forceinline__ uint16_t kv_round<uint16_t>(float f) {
-  uint16_t r;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(f));
-  return r;
-}
-
+// VEC values of a type (S: its bits) as they lie in memory, in whole words:
+// 16 bytes, or a single value.
 template <class S, int VEC>
-struct alignas(sizeof(S) * VEC) KvVec {
-  S e[VEC];
+struct KvVec;
+template <>
+struct KvVec<uint32_t, 4> {
+  uint4 q;
+  __device__ __forceinline__ void load(const uint32_t* p) { q = *(const uint4*)p; }
+  __device__ __forceinline__ void store(uint32_t* p) const { *(uint4*)p = q; }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = __uint_as_float(q.x), f[1] = __uint_as_float(q.y), f[2] = __uint_as_float(q.z), f[3] = __uint_as_float(q.w);
+  }
+  __device__ __forceinline__ void set(const float (&f)[4]) {
+    q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <>
+struct KvVec<uint16_t, 8> {
+  uint4 q;
+  __device__ __forceinline__ void load(const uint16_t* p) { q = *(const uint4*)p; }
+  __device__ __forceinline__ void store(uint16_t* p) const { *(uint4*)p = q; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = bf16_lo(q.x), f[1] = bf16_hi(q.x), f[2] = bf16_lo(q.y), f[3] = bf16_hi(q.y);
+    f[4] = bf16_lo(q.z), f[5] = bf16_hi(q.z), f[6] = bf16_lo(q.w), f[7] = bf16_hi(q.w);
+  }
+  static __device__ __forceinline__ uint32_t two(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    q = make_uint4(two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7]));
+  }
+};
+template <>
+struct KvVec<uint32_t, 1> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const uint32_t* p) { v = *p; }
+  __device__ __forceinline__ void store(uint32_t* p) const { *p = v; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = __uint_as_float(v); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { v = __float_as_uint(f[0]); }
+};
+template <>
+struct KvVec<uint16_t, 1> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
+  __device__ __forceinline__ void store(uint16_t* p) const { *p = (uint16_t)v; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = bf16_lo(v); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { v = KvVec<uint16_t, 8>::two(f[0], 0.f); }
 };
 
-// One token's place, as a CTA works it out for its tokens.
-struct KvToken {
-  long long dst;  // element offset of its entry in the caches, -1: not written
-  int state;      // 0: behind the sequence's new tokens, 1: valid, 2: bad sequence
-};
+constexpr int kKvHeads = 2;  // rounds of heads in flight per warp
+constexpr int kKvVals = 2;   // ... of V's vectors
 
-// Shared memory: the tokens, then cos and sin [kKvTokens][rot / 2].
-template <class S, int VEC>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
-  extern __shared__ __align__(16) float2 s_cs[];
-  __shared__ KvToken s_tok[kKvTokens];
-  __shared__ unsigned long long s_pos[kKvTokens];
+// A warp takes a token, or one of `parts` shares of its heads where there are
+// few tokens, and works by itself.  A lane keeps its place within the head from
+// head to head, and with it its cosines and sines in registers (kRegs; heads
+// of more vectors than a warp has lanes read them from shared memory).  A
+// token's values are read once and written once; the reads of the first heads
+// need only the token's index and set out before the two trips to memory that
+// its slot takes.
+//
+// Shared memory, per warp: cos and sin [rot / 2], then for a tree the parents [T - 1].
+template <class S, int VEC, bool kInterleaved, bool kRegs>
+__global__ void __launch_bounds__(kKvThreads, 8) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
+  extern __shared__ __align__(16) unsigned char s_kv[];
   using V = KvVec<S, VEC>;
-  const int tid = threadIdx.x;
-  const long long first = (long long)blockIdx.x * kKvTokens;
-  const int n = (int)min((long long)kKvTokens, (long long)a.B * a.T - first);
-  if (tid < n) {
-    const long long g = first + tid;
-    const int b = (int)(g / a.T), i = (int)(g - (long long)b * a.T);
-    const long long len = __ldg(a.lengths + b);
-    const int n_new = a.n_new ? __ldg(a.n_new + b) : a.T;
-    KvToken t = {-1, 1};
-    int depth = i;
-    if (len < 0 || n_new < 0 || n_new > a.T || len + n_new > (long long)a.max_pages * a.page_size) t.state = 2;
-    if (a.parents) {
-      // every parent of the sequence has to precede its node
-      const int32_t* par = a.parents + (long long)b * (a.T - 1);
-      for (int j = 0; j < a.T - 1; ++j) {
-        const int p = __ldg(par + j);
-        if (p < -1 || p >= j) t.state = 2;
-      }
-      depth = 0;
-      if (t.state != 2)
-        for (int j = i - 1; j >= 0; j = __ldg(par + j)) ++depth;
-    }
-    if (t.state == 1 && i >= n_new) t.state = 0;
-    if (t.state == 1) {
-      const long long slot = len + i;
-      const int page = __ldg(a.page_table + (long long)b * a.max_pages + slot / a.page_size);
-      if (page < 0 || page >= a.pages)
-        atomicOr(a.status, kStatusBadData);
-      else
-        t.dst = ((long long)page * a.page_size + slot % a.page_size) * a.Hkv * a.D;
-    }
-    if (t.state == 2) atomicOr(a.status, kStatusBadData);
-    s_tok[tid] = t;
-    s_pos[tid] = (unsigned long long)(len + depth);
-  }
-  __syncthreads();
+  constexpr int kFreqs = kInterleaved ? (VEC > 1 ? VEC / 2 : 1) : VEC;  // frequencies of an item
+  constexpr int kPair = kInterleaved && VEC == 1 ? 1 : 0;              // interleaved single values go by two
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int half = a.rot / 2;
-  for (int x = tid; x < n * half; x += kKvThreads) {
-    const int t = x / half, f = x - t * half;
-    const unsigned long long turn = s_pos[t] * __ldg(a.turns + f);
-    float s, c;
-    // the fraction of a turn in [-1/2, 1/2); half turns in, radians / pi
-    sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
-    s_cs[x] = make_float2(c, s);
-  }
-  __syncthreads();
+  const int N = a.parents ? a.T - 1 : 0;
+  float2* cs = (float2*)(s_kv + (size_t)warp * a.warp_bytes);
+  int* par = (int*)(cs + half);
+  const long long unit = (long long)blockIdx.x * kKvWarps + warp;
+  if (unit >= (long long)a.B * a.T * a.parts) return;
+  const int g = (int)(unit / a.parts), part = (int)(unit - (long long)g * a.parts);
+  const int b = fdiv(g, a.div_t), i = g - b * a.T;
 
-  // items of a token: per head of K and Q the rotated vectors (pairs of
-  // vectors when the halves rotate against each other) and the plain ones,
-  // per head of V the plain ones
-  const int rot_items = a.interleaved ? a.rot / (VEC > 1 ? VEC : 2) : half / VEC;
-  const int head_items = rot_items + (a.D - a.rot) / VEC;
-  const int k_items = a.Hkv * head_items, q_items = a.Hq * head_items, v_items = a.Hkv * (a.D / VEC);
-  const int items = k_items + q_items + v_items;
-  for (int x = tid; x < n * items; x += kKvThreads) {
-    const int t = x / items;
-    int it = x - t * items;
-    const KvToken tok = s_tok[t];
-    if (tok.state == 0) continue;
-    const long long g = first + t;
-    if (it >= k_items + q_items) {
-      it -= k_items + q_items;
-      if (tok.dst >= 0) *(V*)((S*)a.v_cache + tok.dst + it * VEC) = *(const V*)((const S*)a.v + g * a.kv_stride + it * VEC);
-      continue;
+  // its heads: K's, then Q's; items of a head: rotated vectors (pairs of
+  // vectors where the halves rotate against each other)
+  const int H = a.Hkv + a.Hq, h0 = (int)((long long)H * part / a.parts), h1 = (int)((long long)H * (part + 1) / a.parts);
+  const int per = half / kFreqs;
+  auto src_of = [&](int h) {
+    return h < a.Hkv ? (const S*)a.k + (long long)g * a.kv_stride + h * a.D
+                     : (const S*)a.q + (long long)g * a.q_stride + (h - a.Hkv) * a.D;
+  };
+  V lo[kKvHeads], hi[kKvHeads];
+  auto load = [&](int x, int h, int j) {  // item j of head h
+    const S* src = src_of(h) + j * (kInterleaved ? VEC + kPair : VEC);
+    lo[x].load(src);
+    if (!kInterleaved) hi[x].load(src + half);
+    if (kPair) hi[x].load(src + 1);
+  };
+  // kRegs: lanes by place in the head, then by head
+  const int at_once = kRegs ? 32 / max(per, 1) : 0;  // heads at once
+  const int jr = kRegs ? lane % max(per, 1) : 0, hr = kRegs && lane < at_once * per ? lane / max(per, 1) : 1 << 28;
+  const int all = a.Hkv * (a.D / VEC);  // V's vectors
+  const int v0 = (int)((long long)all * part / a.parts), v1 = (int)((long long)all * (part + 1) / a.parts);
+  const S* v_from = (const S*)a.v + (long long)g * a.kv_stride;
+  V val[kKvVals];
+  // its first values set out as soon as it is known that it is no padding
+  auto first = [&]() {
+    if constexpr (kRegs) {
+#pragma unroll
+      for (int x = 0; x < kKvHeads; ++x)
+        if (h0 + hr + x * at_once < h1 && per) load(x, h0 + hr + x * at_once, jr);
     }
-    const bool is_q = it >= k_items;
-    if (is_q) it -= k_items;
-    const int head = it / head_items, j = it - head * head_items;
-    const S* src = is_q ? (const S*)a.q + g * a.q_stride + head * a.D : (const S*)a.k + g * a.kv_stride + head * a.D;
-    S* dst = is_q ? (S*)a.out_q + (g * a.Hq + head) * a.D : (S*)a.k_cache + tok.dst + head * a.D;
-    if (!is_q && tok.dst < 0) continue;
-    const bool nan = tok.state == 2;  // a bad sequence's queries
-    const float2* cs = s_cs + t * half;
-    if (j >= rot_items) {
-      const int e = a.rot + (j - rot_items) * VEC;
-      V v = *(const V*)(src + e);
-      if (nan)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v.e[i] = kv_round<S>(NAN);
-      *(V*)(dst + e) = v;
-    } else if (a.interleaved) {
-      if constexpr (VEC > 1) {
-        V v = *(const V*)(src + j * VEC);
+    for (int q = 0; q < kKvVals; ++q)
+      if (v0 + lane + 32 * q < v1) val[q].load(v_from + (v0 + lane + 32 * q) * VEC);
+  };
+  if (!a.n_new) first();
+
+  // ---- its place ----
+  const long long len = __ldg(a.lengths + b);
+  const int n_new = a.n_new ? __ldg(a.n_new + b) : a.T;
+  bool bad = len < 0 || n_new < 0 || n_new > a.T || len + n_new > (long long)a.max_pages * a.page_size;
+  int depth = i;
+  if (a.parents) {
+    // every parent of the sequence has to precede its node
+    for (int j = lane; j < N; j += 32) {
+      const int p = __ldg(a.parents + (long long)b * N + j);
+      par[j] = p;
+      bad |= p < -1 || p >= j;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    __syncwarp();
+    depth = 0;
+    if (!bad)
+      for (int j = i - 1; j >= 0; j = par[j]) ++depth;
+  }
+  if (!bad && i >= n_new) return;  // behind the sequence's new tokens
+  if (a.n_new) first();
+  long long dst = -1;  // element offset of its entry in the caches, -1: not written
+  bool lost = bad;
+  if (!bad) {
+    const long long slot = len + i, in_table = slot / a.page_size;
+    const int page = __ldg(a.page_table + (long long)b * a.max_pages + in_table);
+    lost = page < 0 || page >= a.pages;
+    if (!lost) dst = ((long long)page * a.page_size + (slot - in_table * a.page_size)) * a.Hkv * a.D;
+  }
+  if (lost && lane == 0) atomicOr(a.status, kStatusBadData);
+  if (dst >= 0) {
+    S* v_to = (S*)a.v_cache + dst;
+    for (int x = v0 + lane; x < v1; x += kKvVals * 32) {
+      if (x != v0 + lane)
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-          const float2 w = cs[j * (VEC / 2) + i];
-          const float p = kv_widen<S>(v.e[2 * i]), q = kv_widen<S>(v.e[2 * i + 1]);
-          v.e[2 * i] = kv_round<S>(nan ? NAN : p * w.x - q * w.y);
-          v.e[2 * i + 1] = kv_round<S>(nan ? NAN : p * w.y + q * w.x);
-        }
-        *(V*)(dst + j * VEC) = v;
-      } else {
-        const float2 w = cs[j];
-        const float p = kv_widen<S>(src[2 * j]), q = kv_widen<S>(src[2 * j + 1]);
-        dst[2 * j] = kv_round<S>(nan ? NAN : p * w.x - q * w.y);
-        dst[2 * j + 1] = kv_round<S>(nan ? NAN : p * w.y + q * w.x);
+        for (int q = 0; q < kKvVals; ++q)
+          if (x + 32 * q < v1) val[q].load(v_from + (x + 32 * q) * VEC);
+#pragma unroll
+      for (int q = 0; q < kKvVals; ++q)
+        if (x + 32 * q < v1) val[q].store(v_to + (x + 32 * q) * VEC);
+    }
+  }
+  const unsigned long long pos = (unsigned long long)(len + depth);
+  for (int f = lane; f < half; f += 32) {
+    const unsigned long long turn = pos * __ldg(a.turns + f);
+    float s, c;
+    // the fraction of a turn in [-1/2, 1/2): half turns in, radians / pi
+    sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
+    if (bad) s = c = NAN;  // a bad sequence's queries
+    cs[f] = make_float2(c, s);
+  }
+  __syncwarp();
+
+  auto dst_of = [&](int h) -> S* {
+    if (h >= a.Hkv) return (S*)a.out_q + ((long long)g * a.Hq + h - a.Hkv) * a.D;
+    return dst < 0 ? nullptr : (S*)a.k_cache + dst + h * a.D;
+  };
+  auto store = [&](int x, int h, int j, const float2 (&w)[kFreqs]) {
+    S* to = dst_of(h);
+    if (!to) return;
+    to += j * (kInterleaved ? VEC + kPair : VEC);
+    float p[VEC], q[VEC];
+    lo[x].get(p);
+    if constexpr (kInterleaved && VEC > 1) {
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        q[e] = p[e] * w[e / 2].x - p[e + 1] * w[e / 2].y;
+        q[e + 1] = p[e] * w[e / 2].y + p[e + 1] * w[e / 2].x;
+      }
+      lo[x].set(q);
+      lo[x].store(to);
+    } else {
+      hi[x].get(q);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float r = p[e] * w[e].x - q[e] * w[e].y;
+        q[e] = p[e] * w[e].y + q[e] * w[e].x;
+        p[e] = r;
+      }
+      lo[x].set(p);
+      hi[x].set(q);
+      lo[x].store(to);
+      hi[x].store(to + (kInterleaved ? 1 : half));
+    }
+  };
+  if (per > 0) {
+    if constexpr (kRegs) {
+      float2 w[kFreqs];
+#pragma unroll
+      for (int e = 0; e < kFreqs; ++e) w[e] = cs[jr * kFreqs + e];
+      for (int h = h0 + hr; h < h1; h += kKvHeads * at_once) {
+        if (h != h0 + hr)
+#pragma unroll
+          for (int x = 0; x < kKvHeads; ++x)
+            if (h + x * at_once < h1) load(x, h + x * at_once, jr);
+#pragma unroll
+        for (int x = 0; x < kKvHeads; ++x)
+          if (h + x * at_once < h1) store(x, h + x * at_once, jr, w);
       }
     } else {
-      V lo = *(const V*)(src + j * VEC), hi = *(const V*)(src + half + j * VEC);
+      for (int h = h0; h < h1; ++h)
+        for (int j = lane; j < per; j += 32) {
+          float2 w[kFreqs];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float2 w = cs[j * VEC + i];
-        const float p = kv_widen<S>(lo.e[i]), q = kv_widen<S>(hi.e[i]);
-        lo.e[i] = kv_round<S>(nan ? NAN : p * w.x - q * w.y);
-        hi.e[i] = kv_round<S>(nan ? NAN : p * w.y + q * w.x);
-      }
-      *(V*)(dst + j * VEC) = lo;
-      *(V*)(dst + half + j * VEC) = hi;
+          for (int e = 0; e < kFreqs; ++e) w[e] = cs[j * kFreqs + e];
+          load(0, h, j);
+          store(0, h, j, w);
+        }
     }
+  }
+  // what is not turned: the rest of the heads, and V
+  const int rest = (a.D - a.rot) / VEC;
+  for (int x = lane; x < rest * (h1 - h0); x += 32) {
+    const int h = h0 + x / rest, e = a.rot + x % rest * VEC;
+    S* to = dst_of(h);
+    if (!to) continue;
+    V v;
+    v.load(src_of(h) + e);
+    if (bad) {
+      float f[VEC];
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) f[q] = NAN;
+      v.set(f);
+    }
+    v.store(to + e);
   }
 }
 
 int kv_max_rot() { return 1024; }
 
-cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, bool vec, cudaStream_t s) {
-  const unsigned grid = (unsigned)(((long long)a.B * a.T + kKvTokens - 1) / kKvTokens);
-  const size_t smem = (size_t)kKvTokens * (a.rot / 2) * sizeof(float2);
-  if (bf16 && vec)
-    kv_append_kernel<uint16_t, 8><<<grid, kKvThreads, smem, s>>>(a);
-  else if (bf16)
-    kv_append_kernel<uint16_t, 1><<<grid, kKvThreads, smem, s>>>(a);
-  else if (vec)
-    kv_append_kernel<uint32_t, 4><<<grid, kKvThreads, smem, s>>>(a);
+template <class S, int VEC, bool kInterleaved>
+static void launch_append(const KvAppendArgs& a, cudaStream_t s) {
+  KvAppendArgs k = a;
+  const long long all = (long long)a.B * a.T;
+  // few tokens: a token's heads go to several warps, until every SM has some
+  k.parts = 1;
+  while (k.parts < 8 && all * k.parts < 8LL * a.sms) k.parts *= 2;
+  k.div_t = make_fastdiv((uint32_t)a.T);
+  k.warp_bytes = (int)(((a.rot / 2) * sizeof(float2) + (a.parents ? (a.T - 1) * sizeof(int) : 0) + 15) / 16 * 16);
+  const unsigned grid = (unsigned)((all * k.parts + kKvWarps - 1) / kKvWarps);
+  const size_t smem = (size_t)kKvWarps * k.warp_bytes;
+  const int per = a.rot / 2 / (kInterleaved ? (VEC > 1 ? VEC / 2 : 1) : VEC);
+  if (per <= 32)
+    kv_append_kernel<S, VEC, kInterleaved, true><<<grid, kKvThreads, smem, s>>>(k);
   else
-    kv_append_kernel<uint32_t, 1><<<grid, kKvThreads, smem, s>>>(a);
+    kv_append_kernel<S, VEC, kInterleaved, false><<<grid, kKvThreads, smem, s>>>(k);
+}
+template <class S, int VEC>
+static void launch_append(const KvAppendArgs& a, cudaStream_t s) {
+  if (a.interleaved)
+    launch_append<S, VEC, true>(a, s);
+  else
+    launch_append<S, VEC, false>(a, s);
+}
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, bool vec, cudaStream_t s) {
+  if (bf16 && vec)
+    launch_append<uint16_t, 8>(a, s);
+  else if (bf16)
+    launch_append<uint16_t, 1>(a, s);
+  else if (vec)
+    launch_append<uint32_t, 4>(a, s);
+  else
+    launch_append<uint32_t, 1>(a, s);
   return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // commit
 // ---------------------------------------------------------------------------
-// One CTA per (sequence, layer, cache).  It finds the path's nodes level by
-// level (a node is on level d when its parent is on level d - 1 and it carries
-// the path's d-th token), takes the lowest node of the last level and its
-// ancestors, and moves the entries: slot len + 1 + node_d to slot len + d.
-// node_d >= d - 1, so moving in ascending order never overwrites an entry that
-// is still to be read; each thread keeps that order for its own bytes.
-constexpr int kCommitThreads = 256;
+// One CTA per (sequence, layer, cache).  Every thread takes nodes that carry the
+// path's last token and follows them up, token by token; the lowest node whose
+// way to the root spells the path is the path's last.  Then the entries move:
+// slot len + 1 + node_d to slot len + d.  node_d >= d - 1, so moving in
+// ascending order never overwrites an entry that is still to be read; each
+// thread keeps that order for its own bytes.
+constexpr int kCommitThreads = 128;
 constexpr int kCommitBatch = 4;  // entries in flight per thread
 
 template <class V>
 __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const __grid_constant__ KvCommitArgs a) {
-  __shared__ short s_level[kMaxTreeNodes];     // 1-based level, 0: not on the path
-  __shared__ int s_node[kMaxTreeNodes];        // the path's nodes, by level
+  __shared__ int s_par[kMaxTreeNodes], s_tok[kMaxTreeNodes], s_path[kMaxTreeNodes];
+  __shared__ int s_node[kMaxTreeNodes];           // the path's nodes, by level
   __shared__ long long s_slot[2][kMaxTreeNodes];  // byte offsets: to, from
   __shared__ int s_last;
   const int tid = threadIdx.x;
   const int b = blockIdx.x;
   const int layer = blockIdx.y >> 1, which = blockIdx.y & 1;
   const int N = a.N;
-  const int32_t* tok = a.tokens + (long long)b * N;
-  const int32_t* par = a.parents + (long long)b * N;
-  const int32_t* path = a.path + (long long)b * (N + 1);
   const int size = __ldg(a.path_len + b);
   const long long len = __ldg(a.lengths + b);
   const int n = size > 0 ? size - 1 : 0;
   const long long most = min((long long)a.max_pages * a.page_size, 2147483647LL);
-  // every verdict below is the whole CTA's: the barriers stay uniform
-  bool bad = size != -1 && (size < 1 || n > N || len < 0 || len + N + 1 > most);
-  const bool go = size != -1 && !bad;
-  if (go) {
-    if (tid == 0) s_last = N;
-    bool wrong = false;
-    for (int j = tid; j < N; j += kCommitThreads) {
-      s_level[j] = 0;
-      const int p = __ldg(par + j);
-      wrong |= p < -1 || p >= j;
-    }
-    bad = __syncthreads_or(wrong);
+  bool wrong = false;
+  for (int j = tid; j < N; j += kCommitThreads) {
+    const int p = __ldg(a.parents + (long long)b * N + j);
+    s_par[j] = p;
+    s_tok[j] = __ldg(a.tokens + (long long)b * N + j);
+    s_path[j] = __ldg(a.path + (long long)b * (N + 1) + j);
+    wrong |= p < -1 || p >= j;
   }
-  if (go && !bad) {
-    for (int d = 1; d <= n; ++d) {
-      const int want = __ldg(path + d - 1);
-      for (int j = tid; j < N; j += kCommitThreads) {
-        const int p = __ldg(par + j);
-        if ((d == 1 ? p == -1 : p >= 0 && s_level[p] == d - 1) && __ldg(tok + j) == want) {
-          s_level[j] = (short)d;
-          if (d == n) atomicMin(&s_last, j);
-        }
-      }
-      __syncthreads();
+  if (tid == 0) s_last = N;
+  // every verdict below is the whole CTA's: the barriers stay uniform
+  bool bad = __syncthreads_or(wrong) || size < 1 || n > N || len < 0 || len + N + 1 > most;
+  const bool go = size != -1;  // a verify's bad sequence is left as it is
+  if (go && !bad && n > 0) {
+    for (int j = tid; j < N; j += kCommitThreads) {
+      int at = j, d = n;
+      while (d > 0 && at >= 0 && s_tok[at] == s_path[d - 1]) at = s_par[at], --d;
+      if (d == 0 && at < 0) atomicMin(&s_last, j);
     }
-    bad = n > 0 && s_last >= N;  // no path of the tree carries these tokens
+    __syncthreads();
+    bad = s_last >= N;  // no path of the tree carries these tokens
   }
   if (go && !bad) {
     if (tid == 0 && n > 0)
-      for (int j = s_last, d = n; d >= 1; --d, j = __ldg(par + j)) s_node[d - 1] = j;
+      for (int j = s_last, d = n; d >= 1; --d, j = s_par[j]) s_node[d - 1] = j;
     __syncthreads();
-    bool wrong = false;
+    wrong = false;
     for (int d = tid; d < n; d += kCommitThreads) {
       const long long to = len + 1 + d, from = len + 1 + s_node[d];
       const int32_t* table = a.page_table + (long long)b * a.max_pages;
@@ -259,7 +367,7 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const __grid_
     for (int d = tid; d <= N; d += kCommitThreads) a.out_nodes[(long long)b * (N + 1) + d] = go && !bad && d < n ? s_node[d] : -1;
     if (tid == 0) {
       a.out_lengths[b] = (int)(go && !bad ? len + size : len);
-      if (bad) atomicOr(a.status, kStatusBadData);
+      if (go && bad) atomicOr(a.status, kStatusBadData);
     }
   }
   if (!go || bad) return;

@@ -270,6 +270,7 @@ struct CountArgs {
   long long P, words;             // counts of a row, words of a row (spec_token_state_words)
   int32_t* state;                 // [B, words]
   unsigned* status;
+  int range, ranges, vec;         // set by the launch: the vocabulary's ranges; 16-byte rows
 };
 cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s);
 
@@ -317,6 +318,9 @@ struct KvAppendArgs {
   int pages, page_size, max_pages;
   void *k_cache, *v_cache;    // [pages, page_size, Hkv, D]
   unsigned* status;
+  int sms;
+  int parts, warp_bytes;      // set by the launch: warps of a token, shared memory of a warp
+  FastDiv div_t;
 };
 int kv_max_rot();
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, bool vec, cudaStream_t s);

@@ -36,6 +36,7 @@ def test_count_checks(lib):
     for bad in (dict(B=-1), dict(S=-1), dict(V=0), dict(V=2 ** 30 + 1)):
         assert call(**bad) == _lib.SPEC_ERR_SHAPE
     assert call(B=0, tok=None, st=None) == _lib.SPEC_OK
+    assert call(st=FAKE + 8) == _lib.SPEC_ERR_SHAPE  # off a 16-byte boundary
 
 
 @pytest.mark.parametrize("fn", ["spec_process_logits_f32", "spec_process_logits_bf16"])
@@ -75,7 +76,8 @@ def test_append_checks(lib, fn):
     assert call(Hq=2, qs=32, oq=FAKE) == _lib.SPEC_ERR_NULL
     for bad in (dict(B=-1), dict(T=-1), dict(Hq=-1), dict(Hkv=0), dict(D=0), dict(D=1025), dict(rot=-2), dict(rot=3),
                 dict(rot=18), dict(pages=0), dict(ps=0), dict(mp=0), dict(ks=31), dict(Hq=2, qs=31, q=FAKE, oq=FAKE),
-                dict(par=FAKE, T=1026), dict(B=2 ** 20, T=2 ** 20)):
+                dict(par=FAKE, T=1026), dict(B=2 ** 20, T=2 ** 20), dict(Hq=2 ** 14 + 1, D=1024, ks=2 ** 12, qs=2 ** 25, q=FAKE, oq=FAKE, rot=0),
+                dict(Hkv=2 ** 14 + 1, D=1024, ks=2 ** 25, rot=0)):
         assert call(**bad) == _lib.SPEC_ERR_SHAPE, bad
     assert call(B=0) == _lib.SPEC_OK
     assert call(T=0) == _lib.SPEC_OK
