@@ -441,8 +441,8 @@ int spec_token_state_words(int V);
  *   reset          not 0: the rows are zeroed first.
  * Bad data: a length outside [0, stride] or a prompt length outside [0,
  * length] adds nothing to that row and sets SPEC_FLAG_BAD_DATA.  Counts are
- * exact.  Returns SPEC_OK, SPEC_ERR_NULL, SPEC_ERR_SHAPE (B < 0, stride < 0, V,
- * a state off a 16-byte boundary) or SPEC_ERR_CUDA.  Asynchronous on `stream`; no scratch.
+ * exact.  Returns SPEC_OK, SPEC_ERR_NULL, SPEC_ERR_SHAPE (B < 0, a stride
+ * outside [0, 2^30], V, a state off a 16-byte boundary) or SPEC_ERR_CUDA.  Asynchronous on `stream`; no scratch.
  */
 int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32_t *prompt_lengths, int B,
                       int stride, int V, int reset, int32_t *state, cudaStream_t stream);
@@ -480,8 +480,8 @@ int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32
  * and finite, or a frequency or presence that is not finite makes every row of
  * that sequence NaN and sets SPEC_FLAG_BAD_DATA.
  * 1 <= R <= 1025, 1 <= V <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,
- * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`;
- * no scratch.
+ * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`
+ * (two in place, with a mask and with penalties or biases); no scratch.
  */
 int spec_process_logits_f32(const float *logits, const int32_t *draft_tokens, const int32_t *parent_idx,
                             const int32_t *token_state, const float *repetition, const float *frequency,

@@ -879,7 +879,7 @@ int spec_token_state_words(int V) {
 
 int spec_count_tokens(const int32_t* tokens, const int32_t* lengths, const int32_t* prompt_lengths, int B,
                       int stride, int V, int reset, int32_t* state, cudaStream_t stream) {
-  if (B < 0 || stride < 0 || V < 1 || V > kMaxStateVocab) return SPEC_ERR_SHAPE;
+  if (B < 0 || stride < 0 || stride > (1 << 30) || V < 1 || V > kMaxStateVocab) return SPEC_ERR_SHAPE;
   if (B == 0) return SPEC_OK;
   if (!state || (stride > 0 && !tokens)) return SPEC_ERR_NULL;
   if (!aligned16(state)) return SPEC_ERR_SHAPE;

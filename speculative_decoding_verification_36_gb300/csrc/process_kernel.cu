@@ -68,7 +68,12 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const __grid_const
 // Few sequences with long histories: a cluster of CTAs shares a range, each
 // counts a part of the history, and then each adds up a part of the range over
 // the cluster's shared memory.
+// kPacked: no history has over 32767 tokens, so that a count and the prompt's
+// bit fit 16 bits, and a range of twice the tokens the same memory: half the
+// readings of the history.
 constexpr int kCountNewThreads = 512;
+constexpr int kCountPackedMost = 32767;
+template <bool kPacked>
 __global__ void __launch_bounds__(kCountNewThreads) count_new_kernel(const __grid_constant__ CountArgs a) {
   extern __shared__ __align__(16) unsigned s_count[];
   namespace cg = cooperative_groups;
@@ -80,36 +85,35 @@ __global__ void __launch_bounds__(kCountNewThreads) count_new_kernel(const __gri
   const int tid = threadIdx.x;
   int L, Lp;
   const bool ok = count_lengths(a, b, L, Lp);
-  for (int i = tid; i < n / 4; i += kCountNewThreads) ((uint4*)s_count)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < n / (kPacked ? 8 : 4); i += kCountNewThreads) ((uint4*)s_count)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (!ok && c0 == 0 && rank == 0 && tid == 0) atomicOr(a.status, kStatusBadData);
   __syncthreads();
   if (ok) {
     const int32_t* h = a.tokens + (long long)b * a.stride;
     const unsigned end = (unsigned)min(n, a.V - c0);
-    // a token's offset in the range; a negative token's is above every range's end
-    auto off_of = [&](int t) { return (unsigned)t - (unsigned)c0; };
-    auto add = [&](unsigned off, int i) {
-      if (off < end) {
-        if (i < Lp)
-          atomicOr(&s_count[off], 0x80000000u);
-        else
-          atomicAdd(&s_count[off], 1u);
-      }
-    };
+    // tokens [from, to) of the history: the prompt's set a bit, the others count.
+    // A negative token's offset is above every range's end.
     const int step = C * kCountNewThreads, me = rank * kCountNewThreads + tid;
-    int i0 = 0;
-    if (a.vec) {
-      const int quads = L / 4;
+    auto scan = [&](int from, int to, auto&& put) {
+      auto one = [&](int t) {
+        const unsigned off = (unsigned)t - (unsigned)c0;
+        if (off < end) put(kPacked ? s_count + (off >> 1) : s_count + off, kPacked ? 16 * (off & 1) : 0);
+      };
+      int q0 = from, q1 = from;  // whole 16-byte loads
+      if (a.vec && to - from >= 8) {
+        q0 = (from + 3) & ~3;
+        q1 = to & ~3;
 #pragma unroll 4
-      for (int q = me; q < quads; q += step) {
-        const int4 v = __ldg((const int4*)h + q);
-        const unsigned x = off_of(v.x), y = off_of(v.y), z = off_of(v.z), w = off_of(v.w);
-        if (min(min(x, y), min(z, w)) < end) add(x, 4 * q), add(y, 4 * q + 1), add(z, 4 * q + 2), add(w, 4 * q + 3);
+        for (int q = q0 + 4 * me; q < q1; q += 4 * step) {
+          const int4 v = __ldg((const int4*)(h + q));
+          one(v.x), one(v.y), one(v.z), one(v.w);
+        }
+        if (me < q0 - from) one(__ldg(h + from + me));
       }
-      i0 = 4 * quads;
-    }
-#pragma unroll 4
-    for (int i = i0 + me; i < L; i += step) add(off_of(__ldg(h + i)), i);
+      for (int i = q1 + me; i < to; i += step) one(__ldg(h + i));
+    };
+    scan(0, Lp, [](unsigned* p, int at) { atomicOr(p, (kPacked ? 0x8000u : 0x80000000u) << at); });
+    scan(Lp, L, [](unsigned* p, int at) { atomicAdd(p, 1u << at); });
   }
   if (C > 1)
     cluster.sync();
@@ -123,8 +127,14 @@ __global__ void __launch_bounds__(kCountNewThreads) count_new_kernel(const __gri
     const int off = o + 4 * lane;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (off < o1) {
-      v = *(const uint4*)(s_count + off);
-      if (C > 1) {
+      if constexpr (kPacked) {
+        const uint2 w = *(const uint2*)(s_count + off / 2);
+        auto wide = [](unsigned x) { return (x & 0x7fffu) | (x & 0x8000u) << 16; };
+        v = make_uint4(wide(w.x), wide(w.x >> 16), wide(w.y), wide(w.y >> 16));
+      } else {
+        v = *(const uint4*)(s_count + off);
+      }
+      if (!kPacked && C > 1) {
         uint4 sum = make_uint4(0u, 0u, 0u, 0u), top = sum;
         for (int r = 0; r < C; ++r) {
           const uint4 x = *cluster.map_shared_rank((const uint4*)(s_count + off), r);
@@ -146,11 +156,14 @@ __global__ void __launch_bounds__(kCountNewThreads) count_new_kernel(const __gri
   if (C > 1) cluster.sync();  // the others read this CTA's shared memory until here
 }
 
-constexpr int kCountRange = 16384;     // most tokens of a range: 64 KB, three CTAs per SM
+constexpr int kCountRange = 16384;     // most counts of a range: 64 KB, three CTAs per SM (packed: twice as many)
 constexpr int kCountMinRange = 1024;
 
 cudaError_t count_configure() {
-  return cudaFuncSetAttribute(count_new_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCountRange * 4);
+  const cudaError_t e =
+      cudaFuncSetAttribute(count_new_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCountRange * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(count_new_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCountRange * 4);
 }
 
 cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
@@ -161,10 +174,13 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
     // enough history to share out.
     int C = 1;
     while (C < 8 && (long long)a.B * ((a.P + kCountRange - 1) / kCountRange) * C < sms && a.stride >= 4096LL * C) C *= 2;
+    const bool packed = C == 1 && a.stride <= kCountPackedMost;
+    const int most = packed ? 2 * kCountRange : kCountRange;
     const long long want = ((long long)a.B * a.P * C + 2LL * sms - 1) / (2LL * sms);
-    c.range = (int)((want + 31) / 32 * 32);
+    c.range = want > most ? most : (int)((want + 31) / 32 * 32);
     if (c.range < kCountMinRange) c.range = kCountMinRange;
-    if (c.range > kCountRange) c.range = kCountRange;
+    c.ranges = (int)((a.P + c.range - 1) / c.range);
+    c.range = (int)(((a.P + c.ranges - 1) / c.ranges + 127) / 128 * 128);  // of equal lengths
     c.ranges = (int)((a.P + c.range - 1) / c.range);
     c.vec = ((uintptr_t)a.tokens & 15) == 0 && a.stride % 4 == 0;
     const long long per = (1LL << 27) / c.ranges;  // sequences of one launch
@@ -178,7 +194,7 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
       memset(&cfg, 0, sizeof cfg);
       cfg.gridDim = dim3((unsigned)(c.B * c.ranges * C));
       cfg.blockDim = dim3(kCountNewThreads);
-      cfg.dynamicSmemBytes = (size_t)c.range * 4;
+      cfg.dynamicSmemBytes = (size_t)c.range * (packed ? 2 : 4);
       cfg.stream = s;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
@@ -186,7 +202,8 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
       at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
       cfg.attrs = at;
       cfg.numAttrs = 1;
-      const cudaError_t e = cudaLaunchKernelEx(&cfg, count_new_kernel, c);
+      const cudaError_t e =
+          packed ? cudaLaunchKernelEx(&cfg, count_new_kernel<true>, c) : cudaLaunchKernelEx(&cfg, count_new_kernel<false>, c);
       if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -220,14 +237,14 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
 // Apart from its input (process_kernel): a warp's parts of kBatch rows at a time
 // come to shared memory by bulk copies, with further batches behind them; the
 // list is applied to them there, and they go out through registers, masked.
-// In place (process_in_place_kernel): only the listed tokens and the vectors
-// that hold a forbidden one are read and written, where they lie.
+// In place (process_mask_kernel, process_in_place_kernel): only the vectors that
+// hold a forbidden token and the listed tokens are read and written, where they lie.
 constexpr int kProcThreads = 256;
 constexpr int kProcWarps = kProcThreads / 32;
 constexpr int kProcPiece = 512;                        // tokens of a warp
 constexpr int kProcChunk = kProcPiece * kProcWarps;    // ... of a CTA
 constexpr int kProcWords = kProcChunk / 32;            // ... in bitmap words
-constexpr int kProcRows = 4;       // rows at once when in place
+constexpr int kProcRows = 4;       // rows of an entry at once when in place
 constexpr int kProcMaxDrafts = 1024;
 constexpr int kProcDrafts = 256;   // drafts in a chunk that are listed; more are looked up in the input
 constexpr int kProcTreeRows = 32;  // rows of a group whose paths are kept as bit sets
@@ -794,102 +811,106 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   }
 }
 
-template <class T, bool kShifted, bool kMask>
-__global__ void __launch_bounds__(kProcThreads, 4) process_in_place_kernel(const __grid_constant__ ProcessArgs a) {
+// In place, the forbidden tokens: a warp takes 1024 tokens of one row, a lane
+// their mask word; a vector that holds a forbidden token is read (unless all
+// of it is forbidden) and written, no other is touched.
+constexpr int kMaskThreads = 128;
+constexpr int kMaskPiece = 1024;
+template <class T, bool kShifted>
+__global__ void __launch_bounds__(kMaskThreads) process_mask_kernel(const __grid_constant__ ProcessArgs a) {
   using Ty = ProcType<T>;
   using S = typename Ty::storage;
   constexpr int VEC = Ty::kVec;
-  constexpr int kVecs = kProcPiece / VEC / 32;  // vectors of a piece per lane
-  constexpr int RU = 8 / kVecs;                 // rows whose vectors are in flight
+  constexpr int kVecs = kMaskPiece / VEC / 32;  // vectors of a piece per lane
   constexpr unsigned kAll = (1u << VEC) - 1u;
+  const int lane = threadIdx.x & 31;
+  const unsigned pieces = ((unsigned)a.V + kMaskPiece - 1) / kMaskPiece;
+  const unsigned long long unit = (unsigned long long)blockIdx.x * (kMaskThreads / 32) + (threadIdx.x >> 5);
+  const long long row = (long long)(unit / pieces);  // b R + r
+  if (row >= (long long)a.B * a.R) return;
+  const int start = (int)(unit - (unsigned long long)row * pieces) * kMaskPiece, n = min(kMaskPiece, a.V - start);
+  const long long mrow = a.mask_rows > 1 ? row : row / a.R;
+  const uint32_t* mask = a.mask + mrow * a.W + (start >> 5);
+  unsigned w = 32 * lane < n ? __ldg(mask + lane) : 0xffffffffu;
+  S* z = (S*)a.out + row * a.V + start;
+  const int ph = kShifted ? (int)((row * a.V + start + a.phase) & (VEC - 1)) : 0;
+  if (!__any_sync(0xffffffffu, w != 0xffffffffu)) return;
+  if constexpr (kShifted) {
+    // the elements before the first and after the last whole vector
+    const int head = ph ? min(VEC - ph, n) : 0, tail = max(head, (n + ph) / VEC * VEC - ph);
+    const int t = lane < 16 ? lane : tail + lane - 16;
+    if ((lane < 16 ? t < head : t < n) && !(__ldg((const uint8_t*)mask + (t >> 3)) >> (t & 7) & 1u)) z[t] = Ty::kNegInf;
+    // the bits of the 16-byte lattice
+    const unsigned below = __shfl_up_sync(0xffffffffu, w, 1);
+    w = __funnelshift_l(lane ? below : 0xffffffffu, w, ph);
+  }
+  const int v0 = ph ? 1 : 0, v1 = (n + ph) / VEC;
+  uint4 x[kVecs];
+  unsigned bits[kVecs];
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    const int v = 32 * k + lane;
+    bits[k] = __shfl_sync(0xffffffffu, w, v * VEC >> 5) >> (v * VEC & 31) & kAll;
+    if (v < v0 || v >= v1) bits[k] = kAll;
+    if (bits[k] != kAll && bits[k]) x[k] = *(const uint4*)(z - ph + v * VEC);
+  }
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k)
+    if (bits[k] != kAll) *(uint4*)(z - ph + (32 * k + lane) * VEC) = proc_keep<T>(x[k], bits[k]);
+}
+
+// In place, the listed tokens (after the forbidden ones: what is not allowed is
+// left alone).  A lane has an entry, for kProcRows rows at a time.
+template <class T>
+__global__ void __launch_bounds__(kProcThreads, 5) process_in_place_kernel(const __grid_constant__ ProcessArgs a) {
+  using Ty = ProcType<T>;
+  using S = typename Ty::storage;
   __shared__ __align__(16) ProcShared sh;
   __shared__ ProcPaths s_paths;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const ProcUnit u = proc_unit(a, blockIdx.x);
   ProcShare c;
   c.paths = &s_paths;
-  const ProcAhead ahead = proc_ahead(a, u);
+  {
+    const ProcAhead ahead = proc_ahead(a, u);
+    proc_lists(a, sh, u, ahead, c);
+  }
   S* z = (S*)a.out + u.row0;
   const int rows = u.n_tok > 0 ? u.rows : 0;
-  auto phase_of = [&](int i) { return kShifted ? (int)((u.row0 + (long long)i * a.V + a.phase) & (VEC - 1)) : 0; };
-  const uint32_t* mask0 = kMask ? a.mask + ((long long)u.b * a.mask_rows + (a.mask_rows > 1 ? u.r0 : 0)) * a.W + (u.start >> 5) : nullptr;
-  const int mask_step = a.mask_rows > 1 ? a.W : 0;
-  const int mask_words = min(kProcPiece / 32, a.W - (u.start >> 5));
-  auto mask_word = [&](int i) {
-    const unsigned hi = lane < mask_words && i < rows ? __ldg(mask0 + (long long)i * mask_step + lane) : 0xffffffffu;
-    if constexpr (!kShifted) return hi;
-    const unsigned lo = __shfl_up_sync(0xffffffffu, hi, 1);
-    return __funnelshift_l(lane ? lo : 0xffffffffu, hi, phase_of(i));
-  };
-  auto allowed_at = [&](int i, int t) {
-    return !kMask || (__ldg((const uint8_t*)(mask0 + (long long)i * mask_step) + (t >> 3)) >> (t & 7) & 1u);
-  };
-
-  // ---- forbidden tokens ----
-  if constexpr (kMask) {
-    for (int rb = 0; rb < rows; rb += RU) {
-      unsigned word[RU], bits[RU][kVecs];
-      uint4 x[RU][kVecs];
-#pragma unroll
-      for (int i = 0; i < RU; ++i) word[i] = mask_word(rb + i);
-#pragma unroll
-      for (int i = 0; i < RU; ++i) {
-        const int ph = phase_of(rb + i), v0 = ph ? 1 : 0;
-        const int v1 = (u.n_tok + ph) / VEC;  // the lattice's whole vectors of the piece: v0 .. v1 - 1
-        const S* row = z + (long long)(rb + i) * a.V - ph;
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-          const int v = 32 * k + lane;
-          bits[i][k] = __shfl_sync(0xffffffffu, word[i], v * VEC >> 5) >> (v * VEC & 31) & kAll;
-          if (v < v0 || v >= v1) bits[i][k] = kAll;
-          if (bits[i][k] != kAll && bits[i][k]) x[i][k] = *(const uint4*)(row + v * VEC);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < RU; ++i) {
-        const int ph = phase_of(rb + i);
-        S* row = z + (long long)(rb + i) * a.V - ph;
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k)
-          if (bits[i][k] != kAll) *(uint4*)(row + (32 * k + lane) * VEC) = proc_keep<T>(x[i][k], bits[i][k]);
-        if (kShifted && rb + i < rows) {
-          // the elements before the first and after the last whole vector
-          const int head = ph ? min(VEC - ph, u.n_tok) : 0, tail = max(head, (u.n_tok + ph) / VEC * VEC - ph);
-          const int t = lane < 16 ? lane : tail + lane - 16;
-          if ((lane < 16 ? t < head : t < u.n_tok) && !allowed_at(rb + i, t)) row[ph + t] = Ty::kNegInf;
-        }
-      }
-    }
-  }
-
-  proc_lists(a, sh, u, ahead, c);
   if (c.bad) {
     for (int i = 0; i < rows; ++i)
       for (int t = lane; t < u.n_tok; t += 32) z[(long long)i * a.V + t] = Ty::kNan;
     return;
   }
-  // ---- listed tokens ----
-  for (int rb = 0; rb < rows; rb += kProcRows)
-    for (int e = lane; e < c.n_list; e += 32) {
-      const unsigned entry = sh.list[warp * kProcPiece + e];
-      const int t = (int)(entry & kProcOffset) - warp * kProcPiece;
-      const float add = sh.adj[entry & kProcOffset];
+  const uint32_t* mask0 =
+      a.mask ? a.mask + ((long long)u.b * a.mask_rows + (a.mask_rows > 1 ? u.r0 : 0)) * a.W + (u.start >> 5) : nullptr;
+  const int mask_step = a.mask_rows > 1 ? a.W : 0;
+  auto allowed_at = [&](int i, int t) {
+    return !mask0 || (__ldg((const uint8_t*)(mask0 + (long long)i * mask_step) + (t >> 3)) >> (t & 7) & 1u);
+  };
+  for (int e = lane; e < c.n_list; e += 32) {
+    const unsigned entry = sh.list[warp * kProcPiece + e];
+    const int t = (int)(entry & kProcOffset) - warp * kProcPiece;
+    const float add = sh.adj[entry & kProcOffset];
+    ProcTerm term = proc_term(c, entry & kProcSeen, add);
+    for (int rb = 0; rb < rows; rb += kProcRows) {
       S* at = z + (long long)rb * a.V + t;
-      bool on[kProcRows];
+      unsigned on = 0;
       S v[kProcRows];
 #pragma unroll
-      for (int i = 0; i < kProcRows; ++i) on[i] = rb + i < rows && allowed_at(rb + i, t);
+      for (int i = 0; i < kProcRows; ++i)
+        if (rb + i < rows && allowed_at(rb + i, t)) {
+          on |= 1u << i;
+          v[i] = at[(long long)i * a.V];
+        }
 #pragma unroll
       for (int i = 0; i < kProcRows; ++i)
-        if (on[i]) v[i] = at[(long long)i * a.V];
-      ProcTerm term = proc_term(c, entry & kProcSeen, add);
-#pragma unroll
-      for (int i = 0; i < kProcRows; ++i)
-        if (on[i]) {
+        if (on >> i & 1u) {
           if (entry & kProcDraft) term = proc_draft_term(a, sh, u, c, entry, add, u.r0 + rb + i);
           at[(long long)i * a.V] = Ty::round(term(Ty::widen(v[i])));
         }
     }
+  }
   if (c.here) {
     const int4 own = sh.own[threadIdx.x];
     const int t = (own.x & kProcOffset) - warp * kProcPiece;
@@ -932,11 +953,16 @@ cudaError_t process_configure() {
 template <class T, bool kShifted, bool kMask>
 static void launch_one(const ProcessArgs& a, int capacity, cudaStream_t s) {
   const unsigned units = (unsigned)a.B * (unsigned)a.groups * (unsigned)a.chunks;
-  if (a.in == a.out)
-    process_in_place_kernel<T, kShifted, kMask><<<units, kProcThreads, 0, s>>>(a);
-  else
+  if (a.in != a.out) {
     process_kernel<T, kShifted, kMask>
         <<<units < (unsigned)capacity ? units : (unsigned)capacity, kProcThreads, copy_smem<T>(a.parents != nullptr), s>>>(a);
+    return;
+  }
+  if (kMask) {
+    const long long warps = (long long)a.B * a.R * ((a.V + kMaskPiece - 1) / kMaskPiece);
+    process_mask_kernel<T, kShifted><<<(unsigned)((warps + kMaskThreads / 32 - 1) / (kMaskThreads / 32)), kMaskThreads, 0, s>>>(a);
+  }
+  if (a.state || a.drafts || a.n_bias || a.rep || a.freq || a.pres) process_in_place_kernel<T><<<units, kProcThreads, 0, s>>>(a);
 }
 template <class T>
 static void launch_type(const ProcessArgs& a, bool shifted, int capacity, cudaStream_t s) {

@@ -33,7 +33,7 @@ def test_count_checks(lib):
 
     assert call(tok=None) == _lib.SPEC_ERR_NULL
     assert call(st=None) == _lib.SPEC_ERR_NULL
-    for bad in (dict(B=-1), dict(S=-1), dict(V=0), dict(V=2 ** 30 + 1)):
+    for bad in (dict(B=-1), dict(S=-1), dict(S=2 ** 30 + 1), dict(V=0), dict(V=2 ** 30 + 1)):
         assert call(**bad) == _lib.SPEC_ERR_SHAPE
     assert call(B=0, tok=None, st=None) == _lib.SPEC_OK
     assert call(st=FAKE + 8) == _lib.SPEC_ERR_SHAPE  # off a 16-byte boundary
