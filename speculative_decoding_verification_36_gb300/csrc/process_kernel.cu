@@ -257,17 +257,26 @@ constexpr unsigned kProcDraft = 1u << 14;    // some draft carries it
 constexpr unsigned kProcOffset = kProcSeen - 1u;
 static_assert(kProcChunk <= (int)kProcSeen, "an offset leaves the flags free");
 
-struct ProcShared {
-  float adj[kProcChunk];            // of the listed tokens, without the drafts
-  unsigned short list[kProcChunk];  // each warp's in its own part
-  unsigned bias[kProcWords];        // tokens with a bias
-  unsigned draft[kProcWords];       // tokens that some draft carries
-  unsigned drafts[kProcDrafts];     // drafts in the chunk: (offset << 16) | node
-  int4 own[kProcThreads];           // per lane: offset and flags (-1: no terms), node (-1: none), lanes with the token, terms
+// What the CTA's threads gather for their unit's lists; two, by turns, so that
+// the next unit's is cleared while this one's is in use.
+struct ProcGather {
+  unsigned bias[kProcWords];     // tokens with a bias
+  unsigned draft[kProcWords];    // tokens that some draft carries
+  unsigned drafts[kProcDrafts];  // drafts in the chunk: (offset << 16) | node
   int n_draft;
   int twice;  // a token with several biases
   int bad, pad;
 };
+struct ProcShared {
+  float adj[kProcChunk];            // of the listed tokens, without the drafts
+  unsigned short list[kProcChunk];  // each warp's in its own part
+  int4 own[kProcThreads];           // per lane: offset and flags (-1: no terms), node (-1: none), lanes with the token, terms
+  ProcGather gather[2];
+};
+__device__ __forceinline__ void proc_clear(ProcGather& g) {
+  if (threadIdx.x < kProcWords) g.bias[threadIdx.x] = g.draft[threadIdx.x] = 0u;
+  if (threadIdx.x == 0) g.n_draft = g.twice = g.bad = 0;
+}
 // tree: the nodes above each row of the group
 struct ProcPaths {
   unsigned row[kProcTreeRows][kProcMaxDrafts / 32];
@@ -362,14 +371,17 @@ struct ProcShare {
   // has draft i (ProcShared::own), and its token's terms where it is the lowest
   // lane that carries the token and the token is the warp's.
   bool few, here;  // ... so; some lane of the warp has terms
+  const ProcGather* gather;
 };
 
 // What a unit's lists are made from, on its way into a thread's registers: the
 // bitmap of the thread's 16 tokens, the penalties, and of the drafts and biases
 // as many as fit (longer lists are read to the end later).
 constexpr int kProcBiasRegs = 2;
+constexpr int kProcCountRegs = 3;  // counts of the thread's tokens that occurred, the first of them
 struct ProcAhead {
   unsigned mine;
+  int count[kProcCountRegs];
   int draft, parent;
   int bias_t[kProcBiasRegs];
   float bias_v[kProcBiasRegs];
@@ -396,12 +408,21 @@ __device__ __forceinline__ ProcAhead proc_ahead(const ProcessArgs& a, const Proc
   h.pres = a.pres ? __ldg(a.pres + u.b) : 0.f;
   return h;
 }
+// ... and, once the bitmap is there, the counts.
+__device__ __forceinline__ void proc_counts(const ProcessArgs& a, const ProcUnit& u, ProcAhead& h) {
+  unsigned left = h.mine;
+#pragma unroll
+  for (int q = 0; q < kProcCountRegs; ++q) {
+    h.count[q] = left ? __ldg(a.state + (long long)u.b * a.words + u.base + 16 * (int)threadIdx.x + __ffs(left) - 1) : 0;
+    left &= left - 1;
+  }
+}
 
-// The lists of a unit from what came ahead; the counts of the listed tokens are
-// one more trip to memory.  Every thread of the CTA takes part (the lists
-// before are done with); on return each warp may go on.
-__device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh, const ProcUnit& u, const ProcAhead& h,
-                                           ProcShare& c) {
+// The lists of a unit from what came ahead.  Every thread of the CTA takes part
+// (the lists before are done with); on return each warp may go on.  g: the
+// unit's gathering, empty; idle: the other, which is emptied for the next unit.
+__device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh, ProcGather& g, ProcGather& idle,
+                                           const ProcUnit& u, const ProcAhead& h, ProcShare& c) {
   const int tid = threadIdx.x, lane = tid & 31, lo = tid >> 5 << 9;  // the warp's first token in the chunk
   const int32_t* state = a.state + (long long)u.b * a.words;
   const int N = a.drafts ? a.R - 1 : 0;
@@ -414,35 +435,28 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   c.freq = h.freq;
   c.pres = h.pres;
   c.inv = 1.f / c.rep;
-  if (!a.state && !N && !a.n_bias) {
-    c.n_list = 0;
-    c.here = false;
-    c.bad = !(c.rep > 0.f && c.rep < INFINITY) || !(fabsf(c.freq) < INFINITY) || !(fabsf(c.pres) < INFINITY);
-    if (c.bad && tid == 0) atomicOr(a.status, kStatusBadData);
-    return;
+  c.gather = &g;
+  // drafts and biases may be any warp's; without them no barrier is needed
+  const bool shared = N > 0 || a.n_bias > 0;
+  if (shared) {
+    __syncthreads();
+    proc_clear(idle);
   }
-  __syncthreads();
-  if (tid < kProcWords) {
-    sh.bias[tid] = 0u;
-    sh.draft[tid] = 0u;
-  }
-  if (tid == 0) sh.n_draft = sh.twice = sh.bad = 0;
-  __syncthreads();
   auto put_draft = [&](int j, int t, int parent) {
     if (t >= 0 && t < left) {
-      const int at = atomicAdd(&sh.n_draft, 1);
-      if (at < kProcDrafts) sh.drafts[at] = ((unsigned)t << 16) | (unsigned)j;
-      atomicOr(&sh.draft[t >> 5], 1u << (t & 31));
+      const int at = atomicAdd(&g.n_draft, 1);
+      if (at < kProcDrafts) g.drafts[at] = ((unsigned)t << 16) | (unsigned)j;
+      atomicOr(&g.draft[t >> 5], 1u << (t & 31));
     }
-    if (parent < -1 || parent >= j) sh.bad = 1;
+    if (parent < -1 || parent >= j) g.bad = 1;
   };
   if (tid < N) put_draft(tid, h.draft - u.base, h.parent);
   for (int j = kProcThreads + tid; j < N; j += kProcThreads)
     put_draft(j, __ldg(draft_row + j) - u.base, a.parents ? __ldg(parent_row + j) : -1);
   auto put_bias = [&](int t, float v) {
     if (t < 0 || t >= left) return;
-    if (atomicOr(&sh.bias[t >> 5], 1u << (t & 31)) >> (t & 31) & 1u)
-      sh.twice = 1;
+    if (atomicOr(&g.bias[t >> 5], 1u << (t & 31)) >> (t & 31) & 1u)
+      g.twice = 1;
     else
       sh.adj[t] = v;
   };
@@ -451,15 +465,16 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
     if (q * kProcThreads + tid < a.n_bias) put_bias(h.bias_t[q] - u.base, h.bias_v[q]);
   for (int i = kProcBiasRegs * kProcThreads + tid; i < a.n_bias; i += kProcThreads)
     put_bias(__ldg(a.bias_tokens + first + i) - u.base, __ldg(a.bias_values + first + i));
-  __syncthreads();
+  if (shared) __syncthreads();
   // a penalty that is no number, or a factor that is not positive
-  c.bad = sh.bad || !(c.rep > 0.f && c.rep < INFINITY) || !(fabsf(c.freq) < INFINITY) || !(fabsf(c.pres) < INFINITY);
+  c.bad = (shared && g.bad) || !(c.rep > 0.f && c.rep < INFINITY) || !(fabsf(c.freq) < INFINITY) || !(fabsf(c.pres) < INFINITY);
   if (c.bad && tid == 0) atomicOr(a.status, kStatusBadData);
 
-  const int n_draft = sh.n_draft;
+  const int n_draft = shared ? g.n_draft : 0;
   c.few = n_draft <= 32;
-  const unsigned draft = (sh.draft[tid >> 1] >> (16 * (tid & 1))) & 0xffffu;
-  unsigned touch = mine | ((sh.bias[tid >> 1] >> (16 * (tid & 1))) & 0xffffu);
+  const unsigned draft = shared ? (g.draft[tid >> 1] >> (16 * (tid & 1))) & 0xffffu : 0u;
+  const unsigned bias = shared ? (g.bias[tid >> 1] >> (16 * (tid & 1))) & 0xffffu : 0u;
+  unsigned touch = mine | bias;
   touch = c.few ? touch & ~draft : touch | draft;
   int at = __popc(touch);
 #pragma unroll
@@ -469,11 +484,7 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   }
   c.n_list = __shfl_sync(0xffffffffu, at, 31);
   at += lo - __popc(touch);
-  for (; touch; touch &= touch - 1) {
-    const int i = __ffs(touch) - 1;
-    sh.list[at++] = (unsigned short)((16 * tid + i) | (mine >> i & 1u ? kProcSeen : 0u) | (draft >> i & 1u ? kProcDraft : 0u));
-  }
-  if (sh.twice) {
+  if (shared && g.twice) {
     // some token has several biases: each warp sums those of its own tokens,
     // in the order given
     for (int i = lane; i < kProcPiece; i += 32) sh.adj[lo + i] = 0.f;
@@ -494,7 +505,7 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   __syncwarp();
   c.here = false;
   if (c.few && n_draft > 0) {
-    const unsigned d = lane < n_draft ? sh.drafts[lane] : 0xffffffffu;
+    const unsigned d = lane < n_draft ? g.drafts[lane] : 0xffffffffu;
     int off = lane < n_draft ? (int)(d >> 16) : -1 - lane;
     const unsigned same = __match_any_sync(0xffffffffu, off);
     const unsigned bits = __shfl_sync(0xffffffffu, mine, off >> 4 & 31);
@@ -503,21 +514,48 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
     if (c.here) {
       const bool seen = off >= 0 && (bits >> (off & 15) & 1u);
       const int n = seen ? __ldg(state + u.base + off) & 0x7fffffff : 0;
-      float add = off >= 0 && (sh.bias[off >> 5] >> (off & 31) & 1u) ? sh.adj[off] : 0.f;
+      float add = off >= 0 && (g.bias[off >> 5] >> (off & 31) & 1u) ? sh.adj[off] : 0.f;
       if (n > 0) add += -c.freq * (float)n - c.pres;
       if (off >= 0) off |= (seen ? kProcSeen : 0u) | (n > 0 ? kProcCounted : 0u);
       sh.own[tid] = make_int4(off, lane < n_draft ? (int)(d & 0xffffu) : -1, (int)same, __float_as_int(add));
     }
   }
-  for (int e = lane; e < c.n_list; e += 32) {
-    const unsigned entry = sh.list[lo + e];
-    const int off = entry & kProcOffset, n = entry & kProcSeen ? __ldg(state + u.base + off) & 0x7fffffff : 0;
-    float adj = sh.bias[off >> 5] >> (off & 31) & 1u ? sh.adj[off] : 0.f;
-    if (n > 0) {
-      adj += -c.freq * (float)n - c.pres;
-      sh.list[lo + e] = (unsigned short)(entry | kProcCounted);
-    }
+  // the entries and their terms
+  auto put_entry = [&](int i, int n, float adj) {
+    const int off = 16 * tid + i;
+    if (n > 0) adj += -c.freq * (float)n - c.pres;
     sh.adj[off] = adj;
+    sh.list[at++] = (unsigned short)(off | (mine >> i & 1u ? kProcSeen : 0u) | (n > 0 ? kProcCounted : 0u) |
+                                     (draft >> i & 1u ? kProcDraft : 0u));
+  };
+  if (!__any_sync(0xffffffffu, __popc(mine) > kProcCountRegs)) {
+    int rank = 0;
+    for (unsigned all = mine | touch; all; all &= all - 1) {
+      const int i = __ffs(all) - 1;
+      int n = 0;
+      if (mine >> i & 1u) {
+        static_assert(kProcCountRegs == 3, "named one by one");
+        n = (rank == 0 ? h.count[0] : rank == 1 ? h.count[1] : h.count[2]) & 0x7fffffff;
+        ++rank;
+      }
+      if (touch >> i & 1u) put_entry(i, n, bias >> i & 1u ? sh.adj[16 * tid + i] : 0.f);
+    }
+  } else {
+    // more counts than came ahead: entries first, then their counts all at once
+    for (unsigned all = touch; all; all &= all - 1) {
+      const int i = __ffs(all) - 1;
+      put_entry(i, 0, bias >> i & 1u ? sh.adj[16 * tid + i] : 0.f);
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int e = lane; e < c.n_list; e += 32) {
+      const unsigned entry = sh.list[lo + e];
+      const int off = entry & kProcOffset, n = entry & kProcSeen ? __ldg(state + u.base + off) & 0x7fffffff : 0;
+      if (n > 0) {
+        sh.adj[off] += -c.freq * (float)n - c.pres;
+        sh.list[lo + e] = (unsigned short)(entry | kProcCounted);
+      }
+    }
   }
   if (a.parents && n_draft > 0) {
     // the nodes above each row of the group; a parent precedes its child
@@ -534,13 +572,12 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
 }
 
 // The occurrences of the chunk's token `off` among the drafts above row r.
-__device__ __forceinline__ int proc_extra(const ProcessArgs& a, const ProcShared& sh, const ProcUnit& u,
-                                          const ProcShare& c, int off, int r) {
+__device__ __forceinline__ int proc_extra(const ProcessArgs& a, const ProcUnit& u, const ProcShare& c, int off, int r) {
   int extra = 0;
   const unsigned* path = a.parents ? c.paths->row[r - u.r0] : nullptr;
-  if (sh.n_draft <= kProcDrafts) {
-    for (int i = 0; i < sh.n_draft; ++i) {
-      const unsigned d = sh.drafts[i];
+  if (c.gather->n_draft <= kProcDrafts) {
+    for (int i = 0; i < c.gather->n_draft; ++i) {
+      const unsigned d = c.gather->drafts[i];
       const int j = d & 0xffffu;
       extra += (int)(d >> 16) == off && (path ? (path[j >> 5] >> (j & 31) & 1u) : j < r);
     }
@@ -564,9 +601,9 @@ __device__ __forceinline__ ProcTerm proc_term(const ProcShare& c, bool seen, flo
   return {seen ? c.inv : 1.f, seen ? c.rep : 1.f, add};
 }
 // ... of a token that some draft carries, in row r
-__device__ __forceinline__ ProcTerm proc_draft_term(const ProcessArgs& a, const ProcShared& sh, const ProcUnit& u,
-                                                    const ProcShare& c, unsigned entry, float add, int r) {
-  const int extra = proc_extra(a, sh, u, c, entry & kProcOffset, r);
+__device__ __forceinline__ ProcTerm proc_draft_term(const ProcessArgs& a, const ProcUnit& u, const ProcShare& c,
+                                                    unsigned entry, float add, int r) {
+  const int extra = proc_extra(a, u, c, entry & kProcOffset, r);
   if (extra) {
     add -= c.freq * (float)extra;
     if (!(entry & kProcCounted)) add -= c.pres;
@@ -693,6 +730,8 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   ProcUnit u = proc_unit(a, unit_of(0));
   look(u, 0);
   ProcAhead ahead = proc_ahead(a, u);
+  proc_clear(sh.gather[0]);
+  proc_counts(a, u, ahead);
   ProcShare c;
   c.paths = (ProcPaths*)(s_raw + sizeof(ProcCopyShared<T>));
   const unsigned short* list = sh.list + warp * kProcPiece;
@@ -700,10 +739,11 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   bool dead = false;
   int g = 0;
   for (unsigned round = 0;; ++round) {
-    proc_lists(a, sh, u, ahead, c);
+    proc_lists(a, sh, sh.gather[round & 1], sh.gather[~round & 1], u, ahead, c);
     const unsigned next = unit_of(round + 1);
     if (next < total) ahead = proc_ahead(a, proc_unit(a, next));
     for (int i0 = 0; i0 < u.rows; i0 += RB, ++g) {
+      if (i0 + RB >= u.rows && next < total) proc_counts(a, proc_unit(a, next), ahead);
       const int n = min(RB, u.rows - i0);
       unsigned word[RB];
 #pragma unroll
@@ -741,7 +781,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < RB; ++j)
           if (j < n) {
-            if (entry & kProcDraft) term = proc_draft_term(a, sh, u, c, entry, add, u.r0 + i0 + j);
+            if (entry & kProcDraft) term = proc_draft_term(a, u, c, entry, add, u.r0 + i0 + j);
             S* at = x + j * ProcStages<T>::kStage + phase_of(u, i0 + j);
             *at = Ty::round(term(Ty::widen(*at)));
           }
@@ -872,8 +912,10 @@ __global__ void __launch_bounds__(kProcThreads, 5) process_in_place_kernel(const
   ProcShare c;
   c.paths = &s_paths;
   {
-    const ProcAhead ahead = proc_ahead(a, u);
-    proc_lists(a, sh, u, ahead, c);
+    ProcAhead ahead = proc_ahead(a, u);
+    proc_clear(sh.gather[0]);
+    proc_counts(a, u, ahead);
+    proc_lists(a, sh, sh.gather[0], sh.gather[1], u, ahead, c);
   }
   S* z = (S*)a.out + u.row0;
   const int rows = u.n_tok > 0 ? u.rows : 0;
@@ -906,7 +948,7 @@ __global__ void __launch_bounds__(kProcThreads, 5) process_in_place_kernel(const
 #pragma unroll
       for (int i = 0; i < kProcRows; ++i)
         if (on >> i & 1u) {
-          if (entry & kProcDraft) term = proc_draft_term(a, sh, u, c, entry, add, u.r0 + rb + i);
+          if (entry & kProcDraft) term = proc_draft_term(a, u, c, entry, add, u.r0 + rb + i);
           at[(long long)i * a.V] = Ty::round(term(Ty::widen(v[i])));
         }
     }
