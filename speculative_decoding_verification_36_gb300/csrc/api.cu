@@ -583,15 +583,16 @@ int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int
   a.status = d->status;
   a.chunks = (V + sv::process_chunk() - 1) / sv::process_chunk();
   // few sequences are split by rows as well, until every CTA has a unit
-  const int capacity = d->sms * sv::process_blocks_per_sm();
-  const long long units = (long long)B * a.chunks, want = capacity;
+  const long long units = (long long)B * a.chunks, want = (long long)d->sms * sv::process_blocks_per_sm();
   long long groups = units < want ? (want + units - 1) / units : 1;
+  // and many rows, so that the units that end last are not long
+  const long long least = (R + sv::process_most_rows() - 1) / sv::process_most_rows();
+  if (groups < least) groups = least;
   if (groups > R) groups = R;
   a.rows_per = (int)((R + groups - 1) / groups);
-  if (a.parents && a.rows_per > sv::process_tree_rows()) a.rows_per = sv::process_tree_rows();
   a.groups = (R + a.rows_per - 1) / a.rows_per;
-  if (units * a.groups > (1 << 30)) return SPEC_ERR_SHAPE;  // rounds of the grid past the last unit count on
-  const cudaError_t e = sv::launch_process(a, bf16, capacity, stream);
+  if (units * a.groups > INT_MAX) return SPEC_ERR_SHAPE;
+  const cudaError_t e = sv::launch_process(a, bf16, stream);
   if (e != cudaSuccess) return cuda_fail(e, "logit processing launch");
   return SPEC_OK;
 }

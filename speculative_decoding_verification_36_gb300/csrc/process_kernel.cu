@@ -247,7 +247,7 @@ constexpr int kProcWords = kProcChunk / 32;            // ... in bitmap words
 constexpr int kProcRows = 4;       // rows of an entry at once when in place
 constexpr int kProcMaxDrafts = 1024;
 constexpr int kProcDrafts = 256;   // drafts in a chunk that are listed; more are looked up in the input
-constexpr int kProcTreeRows = 32;  // rows of a group whose paths are kept as bit sets
+constexpr int kProcMostRows = 12;  // rows of a group (in a tree, their paths are kept as bit sets)
 static_assert(kProcPiece == 16 * 32, "a lane holds 16 of its warp's tokens");
 static_assert(kProcWords <= kProcThreads, "a thread clears a word");
 // list entries: offset in the chunk, then
@@ -279,7 +279,7 @@ __device__ __forceinline__ void proc_clear(ProcGather& g) {
 }
 // tree: the nodes above each row of the group
 struct ProcPaths {
-  unsigned row[kProcTreeRows][kProcMaxDrafts / 32];
+  unsigned row[kProcMostRows][kProcMaxDrafts / 32];
 };
 
 struct Bf16Tag {};
@@ -316,6 +316,9 @@ template <class T>
 struct ProcCopyShared : ProcShared {
   ProcStages<T> stages[kProcWarps];
   unsigned long long full[kProcWarps][ProcType<T>::kBatches];
+  uint4 claim[2];                // answers to the requests for further units
+  unsigned long long claimed[2];
+  int unit[2];                   // the unit of each round, by turns
   // then, for a tree, ProcPaths
 };
 
@@ -348,12 +351,30 @@ struct ProcUnit {
   int start, n_tok;   // first token and tokens of this warp's piece
   long long row0;     // elements before the piece in row r0
 };
+// The order of the units: by sequence and row group, then by chunk; but the
+// first chunks, where a tokenizer puts what is frequent and the lists are long,
+// are dealt out evenly over the first half, so that none of them is still under
+// way when the others end.  (B = 256, R = 9, V = 152064, everything on: 266 us
+// without this, 242 with it.)
 __device__ __forceinline__ ProcUnit proc_unit(const ProcessArgs& a, unsigned unit) {
   ProcUnit u;
-  const unsigned q = unit / (unsigned)a.chunks, b = q / (unsigned)a.groups;
-  u.base = (int)(unit - q * (unsigned)a.chunks) * kProcChunk;
-  u.b = (int)b;
-  u.r0 = (int)(q - b * (unsigned)a.groups) * a.rows_per;
+  int pair = 0, chunk = 0, x = (int)unit;
+  const int pairs = a.B * a.groups;
+  if (a.chunks > 1) {
+    const int turn = fdiv(x, a.div_turn);  // one first chunk, then turn_length - 1 others
+    if (turn < pairs && x == turn * a.turn_length) {
+      pair = turn;
+    } else {
+      x -= min(turn + 1, pairs);
+      pair = fdiv(x, a.div_rest);
+      chunk = 1 + x - pair * (a.chunks - 1);
+    }
+  } else {
+    pair = x;
+  }
+  u.base = chunk * kProcChunk;
+  u.b = fdiv(pair, a.div_groups);
+  u.r0 = (pair - u.b * a.groups) * a.rows_per;
   u.rows = min(a.rows_per, a.R - u.r0);
   u.start = u.base + (int)(threadIdx.x >> 5) * kProcPiece;
   u.n_tok = max(0, min(kProcPiece, a.V - u.start));
@@ -378,7 +399,7 @@ struct ProcShare {
 // bitmap of the thread's 16 tokens, the penalties, and of the drafts and biases
 // as many as fit (longer lists are read to the end later).
 constexpr int kProcBiasRegs = 2;
-constexpr int kProcCountRegs = 3;  // counts of the thread's tokens that occurred, the first of them
+constexpr int kProcCountRegs = 2;  // counts of the thread's tokens that occurred, the first of them
 struct ProcAhead {
   unsigned mine;
   int count[kProcCountRegs];
@@ -418,9 +439,31 @@ __device__ __forceinline__ void proc_counts(const ProcessArgs& a, const ProcUnit
   }
 }
 
-// The lists of a unit from what came ahead.  Every thread of the CTA takes part
-// (the lists before are done with); on return each warp may go on.  g: the
-// unit's gathering, empty; idle: the other, which is emptied for the next unit.
+// Some token has several biases: each warp sums those of its own tokens, in the
+// order given.
+__device__ __forceinline__ void proc_twice(const ProcessArgs& a, float* adj, int b, int base, int n_tok) {
+  const int lane = threadIdx.x & 31, lo = (int)(threadIdx.x >> 5) * kProcPiece;
+  const long long first = (long long)b * a.n_bias;
+  for (int i = lane; i < kProcPiece; i += 32) adj[lo + i] = 0.f;
+  __syncwarp();
+  for (int i0 = 0; i0 < a.n_bias; i0 += 32) {
+    const int i = i0 + lane;
+    const int t = i < a.n_bias ? __ldg(a.bias_tokens + first + i) - base - lo : -1;
+    const bool own = t >= 0 && t < n_tok;
+    const float v = own ? __ldg(a.bias_values + first + i) : 0.f;
+    for (unsigned m = __ballot_sync(0xffffffffu, own); m; m &= m - 1) {
+      const int l = __ffs(m) - 1;
+      const int off = lo + __shfl_sync(0xffffffffu, t, l);
+      const float x = __shfl_sync(0xffffffffu, v, l);
+      if (lane == 0) adj[off] += x;
+    }
+  }
+}
+
+// The lists of a unit from what came ahead.  Every thread of the CTA takes part,
+// behind a barrier that says that the lists before are done with and `g`, the
+// unit's gathering, is empty; on return each warp may go on.  idle: the other
+// gathering, which is emptied for the next unit.
 __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh, ProcGather& g, ProcGather& idle,
                                            const ProcUnit& u, const ProcAhead& h, ProcShare& c) {
   const int tid = threadIdx.x, lane = tid & 31, lo = tid >> 5 << 9;  // the warp's first token in the chunk
@@ -438,10 +481,7 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   c.gather = &g;
   // drafts and biases may be any warp's; without them no barrier is needed
   const bool shared = N > 0 || a.n_bias > 0;
-  if (shared) {
-    __syncthreads();
-    proc_clear(idle);
-  }
+  if (shared) proc_clear(idle);
   auto put_draft = [&](int j, int t, int parent) {
     if (t >= 0 && t < left) {
       const int at = atomicAdd(&g.n_draft, 1);
@@ -451,6 +491,7 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
     if (parent < -1 || parent >= j) g.bad = 1;
   };
   if (tid < N) put_draft(tid, h.draft - u.base, h.parent);
+#pragma unroll 1
   for (int j = kProcThreads + tid; j < N; j += kProcThreads)
     put_draft(j, __ldg(draft_row + j) - u.base, a.parents ? __ldg(parent_row + j) : -1);
   auto put_bias = [&](int t, float v) {
@@ -463,6 +504,7 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
 #pragma unroll
   for (int q = 0; q < kProcBiasRegs; ++q)
     if (q * kProcThreads + tid < a.n_bias) put_bias(h.bias_t[q] - u.base, h.bias_v[q]);
+#pragma unroll 1
   for (int i = kProcBiasRegs * kProcThreads + tid; i < a.n_bias; i += kProcThreads)
     put_bias(__ldg(a.bias_tokens + first + i) - u.base, __ldg(a.bias_values + first + i));
   if (shared) __syncthreads();
@@ -484,24 +526,7 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   }
   c.n_list = __shfl_sync(0xffffffffu, at, 31);
   at += lo - __popc(touch);
-  if (shared && g.twice) {
-    // some token has several biases: each warp sums those of its own tokens,
-    // in the order given
-    for (int i = lane; i < kProcPiece; i += 32) sh.adj[lo + i] = 0.f;
-    __syncwarp();
-    for (int i0 = 0; i0 < a.n_bias; i0 += 32) {
-      const int i = i0 + lane;
-      const int t = i < a.n_bias ? __ldg(a.bias_tokens + first + i) - u.base - lo : -1;
-      const bool own = t >= 0 && t < u.n_tok;
-      const float v = own ? __ldg(a.bias_values + first + i) : 0.f;
-      for (unsigned m = __ballot_sync(0xffffffffu, own); m; m &= m - 1) {
-        const int l = __ffs(m) - 1;
-        const int off = lo + __shfl_sync(0xffffffffu, t, l);
-        const float x = __shfl_sync(0xffffffffu, v, l);
-        if (lane == 0) sh.adj[off] += x;
-      }
-    }
-  }
+  if (shared && g.twice) proc_twice(a, sh.adj, u.b, u.base, u.n_tok);
   __syncwarp();
   c.here = false;
   if (c.few && n_draft > 0) {
@@ -530,18 +555,20 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   };
   if (!__any_sync(0xffffffffu, __popc(mine) > kProcCountRegs)) {
     int rank = 0;
+#pragma unroll 1
     for (unsigned all = mine | touch; all; all &= all - 1) {
       const int i = __ffs(all) - 1;
       int n = 0;
       if (mine >> i & 1u) {
-        static_assert(kProcCountRegs == 3, "named one by one");
-        n = (rank == 0 ? h.count[0] : rank == 1 ? h.count[1] : h.count[2]) & 0x7fffffff;
+        static_assert(kProcCountRegs == 2, "named one by one");
+        n = (rank == 0 ? h.count[0] : h.count[1]) & 0x7fffffff;
         ++rank;
       }
       if (touch >> i & 1u) put_entry(i, n, bias >> i & 1u ? sh.adj[16 * tid + i] : 0.f);
     }
   } else {
     // more counts than came ahead: entries first, then their counts all at once
+#pragma unroll 1
     for (unsigned all = touch; all; all &= all - 1) {
       const int i = __ffs(all) - 1;
       put_entry(i, 0, bias >> i & 1u ? sh.adj[16 * tid + i] : 0.f);
@@ -561,9 +588,12 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
     // the nodes above each row of the group; a parent precedes its child
     const int W = (N + 31) >> 5;
     if (!c.bad)
+#pragma unroll 1
       for (int r = u.r0 + tid; r < u.r0 + u.rows; r += kProcThreads) {
         unsigned* path = c.paths->row[r - u.r0];
+#pragma unroll 1
         for (int w = 0; w < W; ++w) path[w] = 0u;
+#pragma unroll 1
         for (int j = r - 1; j >= 0; j = __ldg(a.parents + (long long)u.b * N + j)) path[j >> 5] |= 1u << (j & 31);
       }
     __syncthreads();
@@ -572,19 +602,20 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
 }
 
 // The occurrences of the chunk's token `off` among the drafts above row r.
-__device__ __forceinline__ int proc_extra(const ProcessArgs& a, const ProcUnit& u, const ProcShare& c, int off, int r) {
+__device__ __forceinline__ int proc_extra(const ProcessArgs& a, const ProcGather* g, const ProcPaths* paths, int b, int base,
+                                       int r0, int off, int r) {
   int extra = 0;
-  const unsigned* path = a.parents ? c.paths->row[r - u.r0] : nullptr;
-  if (c.gather->n_draft <= kProcDrafts) {
-    for (int i = 0; i < c.gather->n_draft; ++i) {
-      const unsigned d = c.gather->drafts[i];
+  const unsigned* path = a.parents ? paths->row[r - r0] : nullptr;
+  if (g->n_draft <= kProcDrafts) {
+    for (int i = 0; i < g->n_draft; ++i) {
+      const unsigned d = g->drafts[i];
       const int j = d & 0xffffu;
       extra += (int)(d >> 16) == off && (path ? (path[j >> 5] >> (j & 31) & 1u) : j < r);
     }
   } else {
-    const int32_t* tok = a.drafts + (long long)u.b * (a.R - 1);
+    const int32_t* tok = a.drafts + (long long)b * (a.R - 1);
     for (int j = 0; j < r; ++j)  // the nodes above a row have lower indexes than it
-      extra += __ldg(tok + j) == u.base + off && (!path || (path[j >> 5] >> (j & 31) & 1u));
+      extra += __ldg(tok + j) == base + off && (!path || (path[j >> 5] >> (j & 31) & 1u));
   }
   return extra;
 }
@@ -603,7 +634,7 @@ __device__ __forceinline__ ProcTerm proc_term(const ProcShare& c, bool seen, flo
 // ... of a token that some draft carries, in row r
 __device__ __forceinline__ ProcTerm proc_draft_term(const ProcessArgs& a, const ProcUnit& u, const ProcShare& c,
                                                     unsigned entry, float add, int r) {
-  const int extra = proc_extra(a, u, c, entry & kProcOffset, r);
+  const int extra = proc_extra(a, c.gather, c.paths, u.b, u.base, u.r0, entry & kProcOffset, r);
   if (extra) {
     add -= c.freq * (float)extra;
     if (!(entry & kProcCounted)) add -= c.pres;
@@ -629,10 +660,12 @@ __device__ __forceinline__ ProcTerm proc_own_term(const ProcessArgs& a, const Pr
 // lies at phase + t, whole 16-byte vectors move by bulk copies, and the few
 // elements before the first and after the last one are moved by lanes.
 //
-// The grid stays: a CTA goes from unit to unit, and each warp's ring of batches
+// The grid has a CTA for every unit, but those that start take over the ones
+// that have not: a CTA goes from unit to unit, and each warp's ring of batches
 // runs on across them, so that the rows of the next unit are under way while
-// the lists of this one wait for their counts.  (One CTA per unit, with the
-// same passes: 343 us for B = 256, R = 9, V = 152064 in bf16, everything on.)
+// the lists of this one are made.  (One CTA per unit with the same passes: 343
+// us for B = 256, R = 9, V = 152064 in bf16, everything on; equal shares for
+// the CTAs of a persistent grid: 258 us, with SMs that are done early.)
 template <class T, bool kShifted, bool kMask>
 __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_constant__ ProcessArgs a) {
   using Ty = ProcType<T>;
@@ -643,10 +676,6 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   extern __shared__ __align__(16) unsigned char s_raw[];
   ProcCopyShared<T>& sh = *(ProcCopyShared<T>*)s_raw;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned total = (unsigned)a.B * (unsigned)a.groups * (unsigned)a.chunks, G = gridDim.x;
-  // round i's unit: each round hands out G units in another order, so that no
-  // CTA always meets the chunk of the frequent tokens, whose lists are long
-  auto unit_of = [&](unsigned i) { return i * G + (blockIdx.x + i * 7919u) % G; };
   const S* in = (const S*)a.in;
   S* out = (S*)a.out;
   auto phase_of = [&](const ProcUnit& u, int i) { return kShifted ? (int)((u.row0 + (long long)i * a.V + a.phase) & (VEC - 1)) : 0; };
@@ -655,42 +684,49 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
 
   if (lane == 0) {
     for (int k = 0; k < NB; ++k) mbar_init(&sh.full[warp][k], RB);
+    if (warp == 0) {
+      mbar_init(&sh.claimed[0], 1);
+      mbar_init(&sh.claimed[1], 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (warp == 0) cta_request(&sh.claim[0], &sh.claimed[0]);
   }
   __syncwarp();
 
-  // ---- the ring: a batch sets out, lane j with row j's copy ----
-  unsigned load_round = 0;
-  ProcUnit lu = proc_unit(a, unit_of(0));  // the unit, the batch of it and the batch of the ring that set out next
-  int load_batch = 0, load_g = 0;
-  auto load_next = [&]() {
-    if (load_batch * RB >= lu.rows) {
-      const unsigned next = unit_of(++load_round);
-      if (next >= total) {
-        lu.rows = 0;  // and stays so
-        load_batch = 0;
-        return;
-      }
-      lu = proc_unit(a, next);
-      load_batch = 0;
+  ProcUnit u = proc_unit(a, blockIdx.x);
+  int next = -1;  // the unit after it, once known
+
+  // ---- the ring: the batches of a unit up to `most` set out, a lane with each row's copy ----
+  long long load_row0 = u.row0;  // of the unit whose batch sets out next
+  int load_rows = u.rows, load_tok = u.n_tok;
+  bool load_ahead = false;  // ... which is the one after u
+  int load_i = 0, load_g = 0;
+  auto refill = [&](int most) {
+    if (load_i >= load_rows) {
+      if (load_ahead || next < 0) return;
+      const ProcUnit v = proc_unit(a, (unsigned)next);
+      load_row0 = v.row0, load_rows = v.rows, load_tok = v.n_tok;
+      load_ahead = true;
+      load_i = 0;
     }
-    const int i = load_batch * RB + lane;
-    if (lane < RB) {
-      // each of the batch's lanes arrives, with its row's bytes
-      const int ph = phase_of(lu, i), head = head_of(lu, ph), bytes = i < lu.rows ? (lu.n_tok - head) / VEC * 16 : 0;
-      unsigned long long* bar = &sh.full[warp][load_g % NB];
+    const int batches = min(most - load_g, (load_rows - load_i + RB - 1) / RB);
+    if (lane < batches * RB) {
+      // each of a batch's lanes arrives, with its row's bytes
+      const int i = load_i + lane, s = (load_g + lane / RB) % NB;
+      const long long row = load_row0 + (long long)i * a.V;
+      const int ph = kShifted ? (int)((row + a.phase) & (VEC - 1)) : 0, head = kShifted && ph ? min(VEC - ph, load_tok) : 0;
+      const int bytes = i < load_rows ? (load_tok - head) / VEC * 16 : 0;
       if (bytes) {
-        mbar_arrive_tx(bar, (unsigned)bytes);
-        bulk_load(stage(load_g, lane) + (ph ? VEC : 0), in + lu.row0 + (long long)i * a.V + head, (unsigned)bytes, bar);
+        mbar_arrive_tx(&sh.full[warp][s], (unsigned)bytes);
+        bulk_load(sh.stages[warp].row[s][lane % RB] + (ph ? VEC : 0), in + row + head, (unsigned)bytes, &sh.full[warp][s]);
       } else {
-        mbar_arrive(bar);
+        mbar_arrive(&sh.full[warp][s]);
       }
     }
-    ++load_batch;
-    ++load_g;
+    load_i += batches * RB;
+    load_g += batches;
   };
-  for (int k = 0; k < NB; ++k)
-    if (lu.rows) load_next();
+  refill(NB);
 
   // ---- masks and edge elements of the next batch, one batch ahead ----
   // Lane w holds word w of the piece's mask, of the rows of a batch.
@@ -727,7 +763,6 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
     }
   };
 
-  ProcUnit u = proc_unit(a, unit_of(0));
   look(u, 0);
   ProcAhead ahead = proc_ahead(a, u);
   proc_clear(sh.gather[0]);
@@ -739,11 +774,32 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   bool dead = false;
   int g = 0;
   for (unsigned round = 0;; ++round) {
+    if (threadIdx.x == 0) {
+      // the unit after this one, asked for a round ago; and the one after that
+      const unsigned k = round & 1;
+      int answer = -1;
+      bool came = false;
+#pragma unroll 1
+      for (unsigned it = 0; !came && it <= limit; ++it) came = mbar_try(&sh.claimed[k], (round >> 1) & 1);
+      if (!came) {
+        // out of time; but the answer has to have come before the CTA leaves
+        atomicOr(a.status, kStatusTimeout);
+#pragma unroll 1
+        for (unsigned it = 0; !came && it <= kSpinLimit; ++it) came = mbar_try(&sh.claimed[k], (round >> 1) & 1);
+      }
+      if (came) answer = cta_answer(&sh.claim[k]);
+      sh.unit[k] = answer;
+      if (answer >= 0) {
+        fence_async();
+        cta_request(&sh.claim[~round & 1], &sh.claimed[~round & 1]);
+      }
+    }
+    __syncthreads();  // and every warp is done with the lists before
+    next = sh.unit[round & 1];
     proc_lists(a, sh, sh.gather[round & 1], sh.gather[~round & 1], u, ahead, c);
-    const unsigned next = unit_of(round + 1);
-    if (next < total) ahead = proc_ahead(a, proc_unit(a, next));
+    if (next >= 0) ahead = proc_ahead(a, proc_unit(a, (unsigned)next));
     for (int i0 = 0; i0 < u.rows; i0 += RB, ++g) {
-      if (i0 + RB >= u.rows && next < total) proc_counts(a, proc_unit(a, next), ahead);
+      if (i0 + RB >= u.rows && next >= 0) proc_counts(a, proc_unit(a, (unsigned)next), ahead);
       const int n = min(RB, u.rows - i0);
       unsigned word[RB];
 #pragma unroll
@@ -751,12 +807,13 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       const S mine[2] = {edge[0], edge[1]};
       if (i0 + RB < u.rows)
         look(u, i0 / RB + 1);
-      else if (next < total)
-        look(proc_unit(a, next), 0);
+      else if (next >= 0)
+        look(proc_unit(a, (unsigned)next), 0);
       if (!dead && !warp_wait(&sh.full[warp][g % NB], (g / NB) & 1, limit)) {
         // a copy that never came: this warp hands out nothing more, and waits
         // for what is in flight, so that no copy outlives the CTA's memory
         if (lane == 0) atomicOr(a.status, kStatusTimeout);
+#pragma unroll 1
         for (int q = g; q < load_g; ++q) warp_wait(&sh.full[warp][q % NB], (q / NB) & 1, kSpinLimit);
         dead = true;
       }
@@ -772,6 +829,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
         __syncwarp();
       }
       // the listed tokens, each for all rows of the batch
+#pragma unroll 1
       for (int e = lane; e < c.n_list; e += 32) {
         const unsigned entry = list[e];
         const int off = entry & kProcOffset;
@@ -788,6 +846,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       }
       if (c.here && !c.bad) {
         const int4 own = sh.own[threadIdx.x];
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const ProcTerm term = proc_own_term(a, u, c, own, u.r0 + i0 + j);
           if (own.x >= 0) {
@@ -799,11 +858,15 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       // the rows go out: shared -> registers, masked, -> global
       __syncwarp();
       if (c.bad) {
+#pragma unroll 1
         for (int j = 0; j < n; ++j)
+#pragma unroll 1
           for (int t = lane; t < u.n_tok; t += 32) out[u.row0 + (long long)(i0 + j) * a.V + t] = Ty::kNan;
       } else if (kShifted && a.split) {
         // the output's vectors lie at another phase: element by element
+#pragma unroll 1
         for (int j = 0; j < n; ++j)
+#pragma unroll 1
           for (int t = lane; t < u.n_tok; t += 32)
             out[u.row0 + (long long)(i0 + j) * a.V + t] =
                 allowed_at(u, i0 + j, t) ? stage(g, j)[phase_of(u, i0 + j) + t] : Ty::kNegInf;
@@ -844,10 +907,17 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       // the stages are free: the next batch goes there
       fence_async();
       __syncwarp();
-      if (lu.rows) load_next();
+      // (the next unit is known by then: its first batch sets out here at the latest)
+      refill(g + 1 + NB);
     }
-    if (next >= total) break;
-    u = proc_unit(a, next);
+    if (next < 0) break;
+    u = proc_unit(a, (unsigned)next);
+    if (!load_ahead) {  // all of the unit before had set out
+      load_row0 = u.row0, load_rows = u.rows, load_tok = u.n_tok;
+      load_i = 0;
+    }
+    load_ahead = false;
+    next = -1;
   }
 }
 
@@ -915,6 +985,7 @@ __global__ void __launch_bounds__(kProcThreads, 5) process_in_place_kernel(const
     ProcAhead ahead = proc_ahead(a, u);
     proc_clear(sh.gather[0]);
     proc_counts(a, u, ahead);
+    __syncthreads();
     proc_lists(a, sh, sh.gather[0], sh.gather[1], u, ahead, c);
   }
   S* z = (S*)a.out + u.row0;
@@ -967,7 +1038,7 @@ __global__ void __launch_bounds__(kProcThreads, 5) process_in_place_kernel(const
 }
 
 int process_chunk() { return kProcChunk; }
-int process_tree_rows() { return kProcTreeRows; }
+int process_most_rows() { return kProcMostRows; }
 int process_blocks_per_sm() { return 3; }
 
 template <class T>
@@ -993,11 +1064,10 @@ cudaError_t process_configure() {
 }
 
 template <class T, bool kShifted, bool kMask>
-static void launch_one(const ProcessArgs& a, int capacity, cudaStream_t s) {
+static void launch_one(const ProcessArgs& a, cudaStream_t s) {
   const unsigned units = (unsigned)a.B * (unsigned)a.groups * (unsigned)a.chunks;
   if (a.in != a.out) {
-    process_kernel<T, kShifted, kMask>
-        <<<units < (unsigned)capacity ? units : (unsigned)capacity, kProcThreads, copy_smem<T>(a.parents != nullptr), s>>>(a);
+    process_kernel<T, kShifted, kMask><<<units, kProcThreads, copy_smem<T>(a.parents != nullptr), s>>>(a);
     return;
   }
   if (kMask) {
@@ -1007,28 +1077,32 @@ static void launch_one(const ProcessArgs& a, int capacity, cudaStream_t s) {
   if (a.state || a.drafts || a.n_bias || a.rep || a.freq || a.pres) process_in_place_kernel<T><<<units, kProcThreads, 0, s>>>(a);
 }
 template <class T>
-static void launch_type(const ProcessArgs& a, bool shifted, int capacity, cudaStream_t s) {
+static void launch_type(const ProcessArgs& a, bool shifted, cudaStream_t s) {
   if (shifted && a.mask)
-    launch_one<T, true, true>(a, capacity, s);
+    launch_one<T, true, true>(a, s);
   else if (shifted)
-    launch_one<T, true, false>(a, capacity, s);
+    launch_one<T, true, false>(a, s);
   else if (a.mask)
-    launch_one<T, false, true>(a, capacity, s);
+    launch_one<T, false, true>(a, s);
   else
-    launch_one<T, false, false>(a, capacity, s);
+    launch_one<T, false, false>(a, s);
 }
 
-cudaError_t launch_process(const ProcessArgs& a, bool bf16, int capacity, cudaStream_t s) {
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s) {
   const int esz = bf16 ? 2 : 4;
   const unsigned in_off = (unsigned)((uintptr_t)a.in & 15), out_off = (unsigned)((uintptr_t)a.out & 15);
   ProcessArgs k = a;
+  k.turn_length = a.chunks > 3 ? a.chunks / 2 : 1;
+  k.div_turn = make_fastdiv((uint32_t)k.turn_length);
+  k.div_rest = make_fastdiv((uint32_t)(a.chunks > 1 ? a.chunks - 1 : 1));
+  k.div_groups = make_fastdiv((uint32_t)a.groups);
   k.phase = (int)in_off / esz;
   k.split = in_off != out_off;
   const bool shifted = in_off || out_off || (long long)a.V * esz % 16;
   if (bf16)
-    launch_type<Bf16Tag>(k, shifted, capacity, s);
+    launch_type<Bf16Tag>(k, shifted, s);
   else
-    launch_type<float>(k, shifted, capacity, s);
+    launch_type<float>(k, shifted, s);
   return cudaGetLastError();
 }
 

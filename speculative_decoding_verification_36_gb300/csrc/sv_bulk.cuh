@@ -73,4 +73,30 @@ __device__ __forceinline__ void bulk_wait_read() {
 // This thread's generic writes to shared memory come before later bulk copies.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Asks the hardware for a CTA of this grid that has not started: it then never
+// starts, and its index comes to `slot` (16 bytes on a 16-byte boundary of
+// shared memory), completing 16 bytes on the mbarrier.
+__device__ __forceinline__ void cta_request(void* slot, unsigned long long* bar) {
+  mbar_arrive_tx(bar, 16u);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_addr(slot)),
+               "r"(smem_addr(bar))
+               : "memory");
+}
+// The answer once it has come: blockIdx.x of that CTA, -1 when none is left
+// (after which none may be asked for).
+__device__ __forceinline__ int cta_answer(const void* slot) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
+      : "=r"(x)
+      : "r"(smem_addr(slot))
+      : "memory");
+  return x;
+}
+
 }  // namespace sv

@@ -293,15 +293,16 @@ struct ProcessArgs {
   // ... and, set by it: elements from the 16-byte boundary below the input to
   // its start, and whether the output starts at another offset from one
   int phase, split;
+  int turn_length;  // the order of the units (process_kernel.cu)
+  FastDiv div_turn, div_rest, div_groups;
   unsigned* status;
 };
 int process_chunk();      // tokens of one CTA's chunk
 cudaError_t process_configure();  // once per device, before the first launch
 cudaError_t process_set_spin_limit(unsigned n);
-int process_tree_rows();  // most rows of a group when the drafts form a tree
+int process_most_rows();  // most rows of a group
 int process_blocks_per_sm();  // CTAs at once per SM (not in place)
-// capacity: CTAs of the persistent grid at most
-cudaError_t launch_process(const ProcessArgs& a, bool bf16, int capacity, cudaStream_t s);
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s);
 
 // The paged key/value cache's append and commit (kv_kernel.cu).
 struct KvAppendArgs {
