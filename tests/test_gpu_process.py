@@ -105,6 +105,10 @@ SHAPES = [
     (2, 40, 50, torch.float32, "star", 20),
     (1, 256, 200, torch.bfloat16, None, 10),       # the longest chain
     (70, 2, 40, torch.float32, None, 10),
+    (2, 41, 9000, torch.bfloat16, "tree", 100),    # several chunks of the vocabulary and row groups
+    (3, 3, 1000, torch.bfloat16, None, 9000),      # a history in which nearly every token occurs
+    (2, 14, 16390, torch.float32, "tree", 4000),
+    (5, 1, 20000, torch.bfloat16, None, 700),      # single rows
 ]
 
 
@@ -141,6 +145,59 @@ def test_largest_tree_many_equal_tokens():
     rng = np.random.default_rng(8)
     x = make(rng, 1, 1025, 50, torch.float32, "tree", 30, mask=None, alphabet=7)
     check(x, call(x))
+
+
+def test_many_drafts_that_share_tokens():
+    """More drafts in a chunk than a warp has lanes, and fewer, with repeats."""
+    for R, V, alphabet in ((33, 5000, 5), (34, 5000, 5), (60, 9000, 9), (20, 300, 3)):
+        for tree in (None, "tree", "star", "chain"):
+            rng = np.random.default_rng(R)
+            x = make(rng, 2, R, V, torch.bfloat16, tree, 60, alphabet=alphabet)
+            got = call(x)
+            check(x, got)
+            z = x["logits"].to(DEV).clone()
+            call(x, out=z, logits=z)
+            assert torch.equal(z.view(torch.int16), got.view(torch.int16))
+    assert sv.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("dups", [False, True])
+def test_long_bias_lists(dups):
+    """More biases than a CTA has ahead, up to one for every token."""
+    rng = np.random.default_rng(21)
+    for V, n in ((6000, 1500), (700, 700), (5000, 5000)):
+        x = make(rng, 2, 3, V, torch.float32, None, 40, bias=n, dups=False)
+        x["bias_tokens"] = np.stack([rng.permutation(V)[:n] for _ in range(2)]).astype(np.int32)
+        if dups:
+            x["bias_tokens"][:, 1:3] = x["bias_tokens"][:, :1]
+            x["bias_tokens"][:, -1] = x["bias_tokens"][:, 0]  # four times one token
+        check(x, call(x))
+    assert sv.spec_get_status() == 0
+
+
+def test_a_lowered_wait_limit_ends_and_the_next_call_is_right():
+    """Waits that give up after one poll: the launch ends, says so, and writes
+    nothing next to its output; with the limit restored all is as before."""
+    rng = np.random.default_rng(22)
+    x = make(rng, 16, 7, 50000, torch.bfloat16, None, 500)
+    n = 16 * 7 * 50000
+    buf = torch.full((n + 128,), 77.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[64:64 + n].view(16, 7, 50000)
+    z = x["logits"].to(DEV)
+    before = call(x, logits=z)
+    torch.cuda.synchronize()
+    sv.spec_get_status()
+    sv.spec_test_spin_limit(1)
+    try:
+        call(x, logits=z, out=out)
+        torch.cuda.synchronize()
+    finally:
+        sv.spec_test_spin_limit(0)
+    assert sv.spec_get_status() in (0, sv.SPEC_FLAG_TIMEOUT)
+    assert bool((buf[:64] == 77).all()) and bool((buf[64 + n:] == 77).all())
+    call(x, logits=z, out=out)
+    assert torch.equal(out.view(torch.int16), before.view(torch.int16))
+    assert sv.spec_get_status() == 0
 
 
 def test_extreme_values_and_masks():
@@ -266,6 +323,38 @@ def test_counts_match_plain(B, S, V):
     sv.spec_count_tokens(state, dev(more), V)
     np.testing.assert_array_equal(state.cpu().numpy(), plain_ops.count(more, None, None, V, start=ref))
     assert sv.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("B,S", [(200, 32767), (200, 32768), (1, 32767), (1, 40000), (3, 32768)])
+def test_counts_of_one_token_over_and_over(B, S):
+    """The largest counts that 16 bits hold beside the prompt's bit, and the
+    next, in a large batch, in a small one and with a cluster's shares."""
+    V = 100
+    tok = torch.full((B, S), 7, dtype=torch.int32, device=DEV)
+    tok[:, 0] = 8
+    prompts = torch.full((B,), 1, dtype=torch.int32, device=DEV)
+    prompts[-1] = 3
+    state = sv.spec_token_state(B, V, DEV)
+    sv.spec_count_tokens(state, tok, V, prompt_lengths=prompts, reset=True)
+    got = state.cpu().numpy()
+    want = np.zeros_like(got)
+    want[:, 7], want[:, 8] = S - 1, -2 ** 31
+    want[-1, 7] = (S - 3) - 2 ** 31
+    want[:, plain_ops.state_words(V)[0]] = 1 << 7 | 1 << 8
+    np.testing.assert_array_equal(got, want)
+    assert sv.spec_get_status() == 0
+
+
+def test_counts_at_unaligned_rows():
+    rng = np.random.default_rng(23)
+    for B, S, V in ((3, 4099, 5000), (1, 20001, 3000), (5, 63, 40000)):
+        buf = torch.from_numpy(rng.integers(0, V, B * S + 3).astype(np.int32)).to(DEV)
+        for shift in (0, 1, 3):
+            tok = buf[shift:shift + B * S].view(B, S)
+            ln = rng.integers(0, S + 1, B).astype(np.int32)
+            pl = (ln * rng.uniform(0, 1, B)).astype(np.int32)
+            state = sv.spec_count_tokens(sv.spec_token_state(B, V, DEV), tok, V, lengths=dev(ln), prompt_lengths=dev(pl), reset=True)
+            np.testing.assert_array_equal(state.cpu().numpy(), plain_ops.count(tok.cpu().numpy(), ln, pl, V))
 
 
 def test_counts_bad_lengths_leave_the_row():
