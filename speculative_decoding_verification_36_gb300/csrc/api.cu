@@ -592,7 +592,7 @@ int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int
   a.rows_per = (int)((R + groups - 1) / groups);
   a.groups = (R + a.rows_per - 1) / a.rows_per;
   if (units * a.groups > INT_MAX) return SPEC_ERR_SHAPE;
-  const cudaError_t e = sv::launch_process(a, bf16, stream);
+  const cudaError_t e = sv::launch_process(a, bf16, d->sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "logit processing launch");
   return SPEC_OK;
 }

@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       mbar_init(&sh.claimed[1], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (warp == 0) cta_request(&sh.claim[0], &sh.claimed[0]);
+    if (warp == 0 && a.take_over) cta_request(&sh.claim[0], &sh.claimed[0]);
   }
   __syncwarp();
 
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   bool dead = false;
   int g = 0;
   for (unsigned round = 0;; ++round) {
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && a.take_over) {
       // the unit after this one, asked for a round ago; and the one after that
       const unsigned k = round & 1;
       int answer = -1;
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       }
     }
     __syncthreads();  // and every warp is done with the lists before
-    next = sh.unit[round & 1];
+    if (a.take_over) next = sh.unit[round & 1];
     proc_lists(a, sh, sh.gather[round & 1], sh.gather[~round & 1], u, ahead, c);
     if (next >= 0) ahead = proc_ahead(a, proc_unit(a, (unsigned)next));
     for (int i0 = 0; i0 < u.rows; i0 += RB, ++g) {
@@ -1064,10 +1064,12 @@ cudaError_t process_configure() {
 }
 
 template <class T, bool kShifted, bool kMask>
-static void launch_one(const ProcessArgs& a, cudaStream_t s) {
+static void launch_one(const ProcessArgs& a, int sms, cudaStream_t s) {
   const unsigned units = (unsigned)a.B * (unsigned)a.groups * (unsigned)a.chunks;
   if (a.in != a.out) {
-    process_kernel<T, kShifted, kMask><<<units, kProcThreads, copy_smem<T>(a.parents != nullptr), s>>>(a);
+    ProcessArgs k = a;
+    k.take_over = units > (unsigned)(sms * process_blocks_per_sm());  // else all start at once
+    process_kernel<T, kShifted, kMask><<<units, kProcThreads, copy_smem<T>(a.parents != nullptr), s>>>(k);
     return;
   }
   if (kMask) {
@@ -1077,18 +1079,18 @@ static void launch_one(const ProcessArgs& a, cudaStream_t s) {
   if (a.state || a.drafts || a.n_bias || a.rep || a.freq || a.pres) process_in_place_kernel<T><<<units, kProcThreads, 0, s>>>(a);
 }
 template <class T>
-static void launch_type(const ProcessArgs& a, bool shifted, cudaStream_t s) {
+static void launch_type(const ProcessArgs& a, bool shifted, int sms, cudaStream_t s) {
   if (shifted && a.mask)
-    launch_one<T, true, true>(a, s);
+    launch_one<T, true, true>(a, sms, s);
   else if (shifted)
-    launch_one<T, true, false>(a, s);
+    launch_one<T, true, false>(a, sms, s);
   else if (a.mask)
-    launch_one<T, false, true>(a, s);
+    launch_one<T, false, true>(a, sms, s);
   else
-    launch_one<T, false, false>(a, s);
+    launch_one<T, false, false>(a, sms, s);
 }
 
-cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s) {
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, int sms, cudaStream_t s) {
   const int esz = bf16 ? 2 : 4;
   const unsigned in_off = (unsigned)((uintptr_t)a.in & 15), out_off = (unsigned)((uintptr_t)a.out & 15);
   ProcessArgs k = a;
@@ -1100,9 +1102,9 @@ cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s) {
   k.split = in_off != out_off;
   const bool shifted = in_off || out_off || (long long)a.V * esz % 16;
   if (bf16)
-    launch_type<Bf16Tag>(k, shifted, s);
+    launch_type<Bf16Tag>(k, shifted, sms, s);
   else
-    launch_type<float>(k, shifted, s);
+    launch_type<float>(k, shifted, sms, s);
   return cudaGetLastError();
 }
 

@@ -294,6 +294,7 @@ struct ProcessArgs {
   // its start, and whether the output starts at another offset from one
   int phase, split;
   int turn_length;  // the order of the units (process_kernel.cu)
+  int take_over;    // CTAs take over units that have not started
   FastDiv div_turn, div_rest, div_groups;
   unsigned* status;
 };
@@ -302,7 +303,7 @@ cudaError_t process_configure();  // once per device, before the first launch
 cudaError_t process_set_spin_limit(unsigned n);
 int process_most_rows();  // most rows of a group
 int process_blocks_per_sm();  // CTAs at once per SM (not in place)
-cudaError_t launch_process(const ProcessArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_process(const ProcessArgs& a, bool bf16, int sms, cudaStream_t s);
 
 // The paged key/value cache's append and commit (kv_kernel.cu).
 struct KvAppendArgs {
