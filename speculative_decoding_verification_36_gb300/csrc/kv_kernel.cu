@@ -136,9 +136,14 @@ __global__ void __launch_bounds__(kKvThreads, 8) kv_append_kernel(const __grid_c
   if (!a.n_new) first();
 
   // ---- its place ----
-  const long long len = __ldg(a.lengths + b);
+  unsigned long long turn[2];  // the lane's first frequencies
+#pragma unroll
+  for (int q = 0; q < 2; ++q) turn[q] = lane + 32 * q < half ? __ldg(a.turns + lane + 32 * q) : 0ull;
+  const int len = __ldg(a.lengths + b);
   const int n_new = a.n_new ? __ldg(a.n_new + b) : a.T;
-  bool bad = len < 0 || n_new < 0 || n_new > a.T || len + n_new > (long long)a.max_pages * a.page_size;
+  bool bad = len < 0 || n_new < 0 || n_new > a.T || (long long)len + n_new > (long long)a.max_pages * a.page_size;
+  const unsigned slot = (unsigned)len + (unsigned)i, in_table = slot / (unsigned)a.page_size;
+  const int page = !bad && i < n_new ? __ldg(a.page_table + (long long)b * a.max_pages + in_table) : -1;
   int depth = i;
   if (a.parents) {
     // every parent of the sequence has to precede its node
@@ -155,15 +160,21 @@ __global__ void __launch_bounds__(kKvThreads, 8) kv_append_kernel(const __grid_c
   }
   if (!bad && i >= n_new) return;  // behind the sequence's new tokens
   if (a.n_new) first();
-  long long dst = -1;  // element offset of its entry in the caches, -1: not written
-  bool lost = bad;
-  if (!bad) {
-    const long long slot = len + i, in_table = slot / a.page_size;
-    const int page = __ldg(a.page_table + (long long)b * a.max_pages + in_table);
-    lost = page < 0 || page >= a.pages;
-    if (!lost) dst = ((long long)page * a.page_size + (slot - in_table * a.page_size)) * a.Hkv * a.D;
+  const unsigned long long pos = (unsigned long long)((long long)len + depth);
+  for (int f = lane, q = 0; f < half; f += 32, ++q) {
+    const unsigned long long angle = pos * (q == 0 ? turn[0] : q == 1 ? turn[1] : __ldg(a.turns + f));
+    float s, c;
+    // the fraction of a turn in [-1/2, 1/2): half turns in, radians / pi
+    sincospif((float)(int)(angle >> 32) * 4.656612873077393e-10f, &s, &c);
+    if (bad) s = c = NAN;  // a bad sequence's queries
+    cs[f] = make_float2(c, s);
   }
+  __syncwarp();
+  const bool lost = bad || page < 0 || page >= a.pages;
   if (lost && lane == 0) atomicOr(a.status, kStatusBadData);
+  // element offset of its entry in the caches, -1: not written
+  const long long dst =
+      lost ? -1 : ((long long)page * a.page_size + (slot - in_table * (unsigned)a.page_size)) * a.Hkv * a.D;
   if (dst >= 0) {
     S* v_to = (S*)a.v_cache + dst;
     for (int x = v0 + lane; x < v1; x += kKvVals * 32) {
@@ -176,16 +187,6 @@ __global__ void __launch_bounds__(kKvThreads, 8) kv_append_kernel(const __grid_c
         if (x + 32 * q < v1) val[q].store(v_to + (x + 32 * q) * VEC);
     }
   }
-  const unsigned long long pos = (unsigned long long)(len + depth);
-  for (int f = lane; f < half; f += 32) {
-    const unsigned long long turn = pos * __ldg(a.turns + f);
-    float s, c;
-    // the fraction of a turn in [-1/2, 1/2): half turns in, radians / pi
-    sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
-    if (bad) s = c = NAN;  // a bad sequence's queries
-    cs[f] = make_float2(c, s);
-  }
-  __syncwarp();
 
   auto dst_of = [&](int h) -> S* {
     if (h >= a.Hkv) return (S*)a.out_q + ((long long)g * a.Hq + h - a.Hkv) * a.D;
@@ -315,14 +316,15 @@ constexpr int kCommitBatch = 4;  // entries in flight per thread
 
 template <class V>
 __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const __grid_constant__ KvCommitArgs a) {
-  __shared__ int s_par[kMaxTreeNodes], s_tok[kMaxTreeNodes], s_path[kMaxTreeNodes];
-  __shared__ int s_node[kMaxTreeNodes];           // the path's nodes, by level
-  __shared__ long long s_slot[2][kMaxTreeNodes];  // byte offsets: to, from
+  extern __shared__ __align__(16) long long s_commit[];
+  const int N = a.N;
+  long long *s_to = s_commit, *s_from = s_to + N;  // the path's byte offsets, by level
+  int *s_par = (int*)(s_from + N), *s_tok = s_par + N, *s_path = s_tok + N;
+  int* s_node = s_path + N;  // the path's nodes, by level
   __shared__ int s_last;
   const int tid = threadIdx.x;
   const int b = blockIdx.x;
   const int layer = blockIdx.y >> 1, which = blockIdx.y & 1;
-  const int N = a.N;
   const int size = __ldg(a.path_len + b);
   const long long len = __ldg(a.lengths + b);
   const int n = size > 0 ? size - 1 : 0;
@@ -358,8 +360,8 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const __grid_
       const int32_t* table = a.page_table + (long long)b * a.max_pages;
       const int p0 = __ldg(table + to / a.page_size), p1 = __ldg(table + from / a.page_size);
       wrong |= p0 < 0 || p0 >= a.pages || p1 < 0 || p1 >= a.pages;
-      s_slot[0][d] = ((long long)p0 * a.page_size + to % a.page_size) * a.entry_bytes;
-      s_slot[1][d] = ((long long)p1 * a.page_size + from % a.page_size) * a.entry_bytes;
+      s_to[d] = ((long long)p0 * a.page_size + to % a.page_size) * a.entry_bytes;
+      s_from[d] = ((long long)p1 * a.page_size + from % a.page_size) * a.entry_bytes;
     }
     bad = __syncthreads_or(wrong);
   }
@@ -378,22 +380,23 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const __grid_
       V v[kCommitBatch];
 #pragma unroll
       for (int i = 0; i < kCommitBatch; ++i)
-        if (d0 + i < n) v[i] = ((const V*)(cache + s_slot[1][d0 + i]))[x];
+        if (d0 + i < n) v[i] = ((const V*)(cache + s_from[d0 + i]))[x];
 #pragma unroll
       for (int i = 0; i < kCommitBatch; ++i)
-        if (d0 + i < n) ((V*)(cache + s_slot[0][d0 + i]))[x] = v[i];
+        if (d0 + i < n) ((V*)(cache + s_to[d0 + i]))[x] = v[i];
     }
   }
 }
 
 cudaError_t launch_kv_commit(const KvCommitArgs& a, int vec_bytes, cudaStream_t s) {
   const dim3 grid((unsigned)a.B, (unsigned)(2 * a.layers));
+  const size_t smem = (size_t)a.N * (2 * sizeof(long long) + 4 * sizeof(int));
   if (vec_bytes == 16)
-    kv_commit_kernel<uint4><<<grid, kCommitThreads, 0, s>>>(a);
+    kv_commit_kernel<uint4><<<grid, kCommitThreads, smem, s>>>(a);
   else if (vec_bytes == 4)
-    kv_commit_kernel<uint32_t><<<grid, kCommitThreads, 0, s>>>(a);
+    kv_commit_kernel<uint32_t><<<grid, kCommitThreads, smem, s>>>(a);
   else
-    kv_commit_kernel<uint8_t><<<grid, kCommitThreads, 0, s>>>(a);
+    kv_commit_kernel<uint8_t><<<grid, kCommitThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
