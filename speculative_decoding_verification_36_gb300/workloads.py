@@ -73,7 +73,7 @@ PRESETS = {
     "c5": TreePreset("c5", 32, 4, 128256, torch.bfloat16, 0),
 }
 
-_PRESET_INDEX = {"c1": 1, "c2": 2, "c3": 3, "c4": 4, "c5": 5}
+_PRESET_INDEX = {"c1": 1, "c2": 2, "c3": 3, "c4": 4, "c5": 5, "settings": 11, "cache": 12}
 
 
 def preset(name: str, **overrides):
@@ -232,3 +232,53 @@ def make_ngram_histories(B: int, Lmax: int, V: int = 128256, seed: int = 0, copy
             row.extend(seg)
         tokens[b, :L] = torch.tensor(row[:L], dtype=torch.int32)
     return dict(tokens=tokens.to(device), lengths=lengths.to(device))
+
+
+def make_settings(B: int, R: int, V: int, hist: int = 4096, n_bias: int = 64, mask: bool = True, seed: int = 0,
+                  device="cpu"):
+    """What a serving batch's users set, for spec_process_logits on [B, R, V]
+    rows: dict(tokens [B, hist], lengths, prompt_lengths [B] int32;
+    repetition, frequency, presence [B]; bias_tokens, bias_values [B, n_bias];
+    allowed_mask [B, R, ceil(V/32)] int32 or None).
+
+    Half of a history's tokens repeat the vocabulary's first ids (a law that is
+    uniform in the id's logarithm), half are uniform; 70 % of it is the prompt.
+    A mask's rows allow 0.2 %, 10 % or 95 % of the vocabulary, as the states of
+    a grammar do, and a quarter of the sequences has no grammar."""
+    g = _gen(device, "settings", seed)
+    u = torch.rand((B, hist), generator=g, device=device, dtype=torch.float64)
+    often = torch.rand((B, hist), generator=g, device=device) < 0.5
+    tokens = torch.where(often, torch.exp(u * torch.log(torch.tensor(float(V), dtype=torch.float64))) - 1, u * V)
+    tokens = tokens.to(torch.int64).clamp_(0, V - 1).to(torch.int32)
+    lengths = torch.randint((hist + 1) // 2, hist + 1, (B,), generator=g, device=device, dtype=torch.int32)
+    out = dict(tokens=tokens, lengths=lengths, prompt_lengths=(lengths * 0.7).to(torch.int32),
+               repetition=1.0 + 0.3 * torch.rand((B,), generator=g, device=device),
+               frequency=0.5 * torch.rand((B,), generator=g, device=device),
+               presence=0.5 * torch.rand((B,), generator=g, device=device),
+               bias_tokens=torch.randint(0, V, (B, n_bias), generator=g, device=device, dtype=torch.int32),
+               bias_values=5.0 * _randn((B, n_bias), g, device), allowed_mask=None)
+    if mask:
+        W = (V + 31) // 32
+        share = torch.tensor([0.002, 0.1, 0.95], device=device)[torch.randint(0, 3, (B, R, 1), generator=g, device=device)]
+        share = torch.where(torch.rand((B, 1, 1), generator=g, device=device) < 0.25, 2.0, share)
+        bits = torch.rand((B, R, 32 * W), generator=g, device=device) < share
+        bits[..., 0] = True
+        weight = torch.tensor([1 << i for i in range(31)] + [-2 ** 31], dtype=torch.int64, device=device)
+        out["allowed_mask"] = (bits.reshape(B, R, W, 32) * weight).sum(-1).to(torch.int32)
+    return out
+
+
+def make_cache_step(B: int, T: int, Hq: int, Hkv: int, D: int, page: int = 16, ctx: int = 1024, layers: int = 1,
+                    dtype=torch.bfloat16, seed: int = 0, device="cpu"):
+    """A step's queries, keys and values and a paged cache: dict(q [layers, B,
+    T, Hq, D], k, v [layers, B, T, Hkv, D], key_cache, value_cache [layers,
+    pages, page, Hkv, D], page_table, lengths, inv_freq).  Each sequence holds
+    up to ctx entries; its pages lie anywhere in the pool."""
+    g = _gen(device, "cache", seed)
+    lengths = torch.randint(0, ctx + 1, (B,), generator=g, device=device, dtype=torch.int32)
+    most = (ctx + T + page - 1) // page + 1
+    table = torch.randperm(B * most, generator=g, device=device).to(torch.int32).reshape(B, most)
+    one = lambda *s: _randn(s, g, device).to(dtype)  # noqa: E731
+    return dict(q=one(layers, B, T, Hq, D), k=one(layers, B, T, Hkv, D), v=one(layers, B, T, Hkv, D),
+                key_cache=one(layers, B * most, page, Hkv, D), value_cache=one(layers, B * most, page, Hkv, D),
+                page_table=table, lengths=lengths, inv_freq=[10000.0 ** (-2 * i / D) for i in range(D // 2)])
