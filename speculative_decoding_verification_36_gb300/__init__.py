@@ -490,6 +490,8 @@ def _token_stride(t, name, dtype, shape, device):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     _same_device(t, device, name)
+    if t.numel() == 0:
+        return H * D
     sb, st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}'s heads must be contiguous")

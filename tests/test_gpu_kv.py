@@ -184,6 +184,40 @@ def test_append_bad_data_is_left_out():
         assert sv.spec_get_status() == sv.SPEC_FLAG_BAD_DATA, what
 
 
+def test_empty_steps():
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)  # noqa: E731
+    kc = torch.full((3, 4, 2, 16), 5.0, device=DEV)
+    for B, T in ((0, 3), (2, 0), (0, 0)):
+        k = torch.zeros((B, T, 2, 16), device=DEV)
+        q = sv.spec_kv_append(k, k, kc, kc.clone(), i(B, 2), i(B), turns=sv.spec_rope_turns([0.5] * 8, DEV), q=k)
+        assert q.shape == (B, T, 2, 16)
+    assert bool((kc == 5).all())
+    nodes, new = sv.spec_kv_commit(kc, kc.clone(), i(0, 2), i(0), i(0, 3), i(0, 3), i(0, 4), i(0))
+    assert nodes.shape == (0, 4) and new.shape == (0,)
+    assert sv.spec_get_status() == 0
+
+
+def test_products_depend_on_the_distance():
+    """The rotation preserves lengths and angles between equal positions: the
+    product of a turned query and key depends on their distance alone."""
+    D, far = 64, 1000003
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q, k = (torch.randn((1, 1, 1, D), generator=g, device=DEV) for _ in range(2))
+    turns = sv.spec_rope_turns([10000.0 ** (-2 * i / D) for i in range(D // 2)], DEV)
+    kc, vc = (torch.zeros((1, 16, 1, D), device=DEV) for _ in range(2))
+    table = torch.zeros((1, 1 << 17), dtype=torch.int32, device=DEV)
+
+    def turned(x, pos):
+        at = torch.tensor([pos], dtype=torch.int32, device=DEV)
+        return sv.spec_kv_append(k, k, kc, vc, table, at, turns=turns, q=x)[0, 0, 0].double()
+
+    for gap in (0, 1, 37):
+        near, away = (float(turned(q, p + gap) @ turned(k, p)) for p in (5, far))
+        # 2 D products of values off by ANGLE of |x0| + |x1| each
+        bound = 4 * ANGLE * float(q.abs().sum() * k.abs().max() + k.abs().sum() * q.abs().max())
+        assert abs(near - away) <= bound
+
+
 def test_append_refusals():
     rng = np.random.default_rng(6)
     x = make(rng, 2, 3, 2, 2, 16, 16, torch.float32, 4, 8, joint=False)

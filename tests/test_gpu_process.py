@@ -443,6 +443,89 @@ def test_captured_step_replays_on_new_data():
     assert sv.spec_get_status() == 0
 
 
+def test_captured_large_launches_replay():
+    """Launches of more units than start at once, and a history shared out over
+    a cluster, in one graph; two graphs of the same buffers, replayed by turns."""
+    B, R, V = 40, 5, 128256
+    o = wl.make_settings(B, R, V, hist=600, n_bias=40, seed=3, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    z = (torch.randn((B, R, V), generator=g, device=DEV) * 4).to(torch.bfloat16)
+    d = torch.randint(0, V, (B, R - 1), generator=g, device=DEV, dtype=torch.int32)
+    state, out = sv.spec_token_state(B, V, DEV), torch.empty_like(z)
+    long = torch.randint(0, V, (1, 60000), generator=g, device=DEV, dtype=torch.int32)
+    long_state = sv.spec_token_state(1, V, DEV)
+
+    def step():
+        sv.spec_count_tokens(state, o["tokens"], V, o["lengths"], o["prompt_lengths"], reset=True)
+        sv.spec_count_tokens(long_state, long, V, reset=True)
+        sv.spec_process_logits(z, d, None, state, o["repetition"], o["frequency"], o["presence"], o["bias_tokens"],
+                               o["bias_values"], o["allowed_mask"], out=out)
+
+    step()
+    torch.cuda.synchronize()
+    side, graphs = torch.cuda.Stream(), []
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=side):
+                step()
+    for k in range(4):
+        z.copy_((torch.randn((B, R, V), generator=g, device=DEV) * 4).to(torch.bfloat16))
+        long.random_(0, V, generator=g)
+        o["tokens"].random_(0, V, generator=g)
+        out.zero_(), state.fill_(7), long_state.fill_(7)
+        graphs[k % 2].replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (out, state, long_state)]
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (out, state, long_state)):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert sv.spec_get_status() == 0
+
+
+def test_two_large_launches_side_by_side():
+    """Two launches that each fill the device, at once: only CTAs that have
+    started hold work, and neither takes the other's."""
+    B, R, V = 24, 6, 152064
+    o = wl.make_settings(B, R, V, hist=2000, n_bias=40, seed=5, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    zs = [(torch.randn((B, R, V), generator=g, device=DEV) * 4).to(torch.bfloat16) for _ in range(2)]
+    state = sv.spec_count_tokens(sv.spec_token_state(B, V, DEV), o["tokens"], V, o["lengths"], o["prompt_lengths"], reset=True)
+    outs = [torch.empty_like(z) for z in zs]
+
+    def one(i, stream=None):
+        sv.spec_process_logits(zs[i], None, None, state, o["repetition"], o["frequency"], o["presence"], o["bias_tokens"],
+                               o["bias_values"], o["allowed_mask"], out=outs[i], stream=stream)
+
+    alone = []
+    for i in range(2):
+        one(i)
+        alone.append(outs[i].clone())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for x in outs:
+            x.zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            one(i, streams[i])
+        torch.cuda.synchronize()
+        for x, y in zip(outs, alone):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    assert sv.spec_get_status() == 0
+
+
+def test_empty_batches_and_rows():
+    V = 100
+    state = sv.spec_token_state(0, V, DEV)
+    none = torch.empty((0, 4), dtype=torch.int32, device=DEV)
+    sv.spec_count_tokens(state, none, V, reset=True)
+    z = torch.empty((0, 5, V), device=DEV)
+    assert sv.spec_process_logits(z, none, None, state).shape == (0, 5, V)
+    one = torch.zeros((1, 1, V), device=DEV)
+    assert torch.equal(sv.spec_process_logits(one, torch.empty((1, 0), dtype=torch.int32, device=DEV)), one)
+
+
 def test_decode_loop_follows_a_plain_one():
     """N-gram drafts, processed rows, a greedy verify and the counts over
     several steps, against the same loop in numpy: tokens have to agree."""
