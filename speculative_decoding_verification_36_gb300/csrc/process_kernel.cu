@@ -657,8 +657,8 @@ __device__ __forceinline__ ProcTerm proc_own_term(const ProcessArgs& a, const Pr
 
 // kShifted: rows start off 16-byte boundaries (the vocabulary's size, or the
 // buffers).  A row keeps its phase in shared memory: element t of the piece
-// lies at phase + t, whole 16-byte vectors move by bulk copies, and the few
-// elements before the first and after the last one are moved by lanes.
+// lies at phase + t.  The copies take the 16-byte vectors that hold the piece,
+// the output is written in whole vectors and, at its ends, by single elements.
 //
 // The grid has a CTA for every unit, but those that start take over the ones
 // that have not: a CTA goes from unit to unit, and each warp's ring of batches
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   const S* in = (const S*)a.in;
   S* out = (S*)a.out;
   auto phase_of = [&](const ProcUnit& u, int i) { return kShifted ? (int)((u.row0 + (long long)i * a.V + a.phase) & (VEC - 1)) : 0; };
-  auto head_of = [&](const ProcUnit& u, int ph) { return kShifted && ph ? min(VEC - ph, u.n_tok) : 0; };
+  const long long elements = (long long)a.B * a.R * a.V;
   auto stage = [&](int g, int j) { return sh.stages[warp].row[g % NB][j]; };
 
   if (lane == 0) {
@@ -714,11 +714,18 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       // each of a batch's lanes arrives, with its row's bytes
       const int i = load_i + lane, s = (load_g + lane / RB) % NB;
       const long long row = load_row0 + (long long)i * a.V;
-      const int ph = kShifted ? (int)((row + a.phase) & (VEC - 1)) : 0, head = kShifted && ph ? min(VEC - ph, load_tok) : 0;
-      const int bytes = i < load_rows ? (load_tok - head) / VEC * 16 : 0;
+      int lo = 0, bytes = i < load_rows ? load_tok / VEC * 16 : 0, ph = 0;
+      if constexpr (kShifted) {
+        // the 16-byte vectors that hold the piece, but none past the input's ends
+        ph = (int)((row + a.phase) & (VEC - 1));
+        const int nv = (ph + load_tok + VEC - 1) / VEC;
+        lo = row < ph;
+        const int hi = row - ph + nv * VEC > elements;
+        bytes = i < load_rows && load_tok > 0 ? max(nv - lo - hi, 0) * 16 : 0;
+      }
       if (bytes) {
         mbar_arrive_tx(&sh.full[warp][s], (unsigned)bytes);
-        bulk_load(sh.stages[warp].row[s][lane % RB] + (ph ? VEC : 0), in + row + head, (unsigned)bytes, &sh.full[warp][s]);
+        bulk_load(sh.stages[warp].row[s][lane % RB] + lo * VEC, in + row - ph + lo * VEC, (unsigned)bytes, &sh.full[warp][s]);
       } else {
         mbar_arrive(&sh.full[warp][s]);
       }
@@ -728,7 +735,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   };
   refill(NB);
 
-  // ---- masks and edge elements of the next batch, one batch ahead ----
+  // ---- masks of the next batch, one batch ahead ----
   // Lane w holds word w of the piece's mask, of the rows of a batch.
   auto mask_row = [&](const ProcUnit& u, int i) {
     return a.mask + ((long long)u.b * a.mask_rows + (a.mask_rows > 1 ? u.r0 + i : 0)) * a.W + (u.start >> 5);
@@ -737,13 +744,14 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
     return !kMask || (__ldg((const uint8_t*)mask_row(u, i) + (t >> 3)) >> (t & 7) & 1u);
   };
   unsigned next_word[RB];
-  // Eight lanes a row: first its elements before its first vector, then those after its last.
-  S edge[2] = {0, 0};
-  auto edge_at = [&](const ProcUnit& u, int i, int side) {  // the lane's token, -1 for none
-    if (i >= u.rows || (lane >> 3) >= RB) return -1;
-    const int head = head_of(u, phase_of(u, i)), e = lane & 7;
-    const int t = side ? head + (u.n_tok - head) / VEC * VEC + e : e;
-    return (side ? t < u.n_tok : t < head) ? t : -1;
+  // A lane's element at the ends of a row's piece, in no whole vector of it: of
+  // row lane / 16 of a batch, eight lanes those before the first vector, eight
+  // those after the last.  From the boundary below the piece; -1 for none.
+  const int edge_row = lane >> 4, edge_side = lane >> 3 & 1;
+  auto edge_at = [&](const ProcUnit& u, int ph) {
+    const int end = u.n_tok + ph, v1 = end / VEC;
+    if (edge_side) return v1 * VEC + (lane & 7) < end && (v1 > 0 || ph == 0) ? v1 * VEC + (lane & 7) : -1;
+    return (lane & 7) >= ph && ph > 0 && (lane & 7) < min(VEC, end) ? lane & 7 : -1;
   };
   auto look = [&](const ProcUnit& u, int batch) {
     if constexpr (kMask) {
@@ -751,14 +759,6 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       for (int j = 0; j < RB; ++j) {
         const int i = batch * RB + j;
         next_word[j] = i < u.rows && 32 * lane < u.n_tok ? __ldg(mask_row(u, i) + lane) : 0xffffffffu;
-      }
-    }
-    if constexpr (kShifted) {
-      const int i = batch * RB + (lane >> 3);
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        const int t = edge_at(u, i, side);
-        if (t >= 0) edge[side] = in[u.row0 + (long long)i * a.V + t];
       }
     }
   };
@@ -804,7 +804,6 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       unsigned word[RB];
 #pragma unroll
       for (int j = 0; j < RB; ++j) word[j] = kMask ? next_word[j] : 0xffffffffu;
-      const S mine[2] = {edge[0], edge[1]};
       if (i0 + RB < u.rows)
         look(u, i0 / RB + 1);
       else if (next >= 0)
@@ -818,13 +817,15 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
         dead = true;
       }
       if (dead) continue;
-      int te[2] = {-1, -1};
+      int edge = -1, edge_ph = 0;
       if constexpr (kShifted) {
-        const int i = i0 + (lane >> 3);
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          te[side] = edge_at(u, i, side);
-          if (te[side] >= 0) stage(g, lane >> 3)[phase_of(u, i) + te[side]] = mine[side];
+        if (edge_row < n) {
+          edge_ph = phase_of(u, i0 + edge_row);
+          edge = edge_at(u, edge_ph);
+          // the very first and last vectors of the input were not copied whole
+          const long long from = u.row0 + (long long)(i0 + edge_row) * a.V - edge_ph;
+          if (edge >= 0 && (edge_side ? from + (edge / VEC + 1) * VEC > elements : from < 0))
+            stage(g, edge_row)[edge] = in[from + edge];
         }
         __syncwarp();
       }
@@ -875,7 +876,7 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
         for (int j = 0; j < RB; ++j) {
           if (j >= n) break;
           const int ph = phase_of(u, i0 + j);
-          unsigned w = word[j];
+          unsigned& w = word[j];
           if constexpr (kShifted && kMask) {
             // the bits of the 16-byte lattice
             const unsigned below = __shfl_up_sync(0xffffffffu, w, 1);
@@ -896,12 +897,16 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
           }
         }
         if constexpr (kShifted) {
-          const int i = i0 + (lane >> 3);
+          bool on = true;
+          if constexpr (kMask) {
 #pragma unroll
-          for (int side = 0; side < 2; ++side)
-            if (te[side] >= 0)
-              out[u.row0 + (long long)i * a.V + te[side]] =
-                  allowed_at(u, i, te[side]) ? stage(g, lane >> 3)[phase_of(u, i) + te[side]] : Ty::kNegInf;
+            for (int j = 0; j < RB; ++j) {
+              const unsigned w = __shfl_sync(0xffffffffu, word[j], max(edge, 0) >> 5);
+              if (j == edge_row) on = w >> (edge & 31) & 1u;
+            }
+          }
+          if (edge >= 0)
+            out[u.row0 + (long long)(i0 + edge_row) * a.V - edge_ph + edge] = on ? stage(g, edge_row)[edge] : Ty::kNegInf;
         }
       }
       // the stages are free: the next batch goes there
