@@ -62,12 +62,15 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const __grid_const
 // A state made anew: a CTA counts one range of the vocabulary of one sequence
 // in shared memory, from the whole history (4 bytes a token, from L2 for every
 // range but the first), and writes the range's counts and bitmap once.  The
-// bound is the state's 4 1/8 bytes a token of the vocabulary; zeroing it and
-// adding with atomics, which fetch and write a sector each, took 74 us for
-// B = 256, V = 152064 and histories of up to 8192 tokens.
+// bound is the state's 4 1/8 bytes a token of the vocabulary: 40 us for B = 256,
+// V = 152064 and histories of up to 8192 tokens (0.17 GB, 4.2 TB/s; a range is
+// cleared, counted and written by turns, and the history read once per range).
+// Zeroing the state and adding with atomics,
+// which fetch and write a sector each, took 74 us.
 // Few sequences with long histories: a cluster of CTAs shares a range, each
 // counts a part of the history, and then each adds up a part of the range over
-// the cluster's shared memory.
+// the cluster's shared memory.  (One history of 131072 tokens, V = 128256: 9 us,
+// and 26 us with one CTA per range.)
 // kPacked: no history has over 32767 tokens, so that a count and the prompt's
 // bit fit 16 bits, and a range of twice the tokens the same memory: half the
 // readings of the history.
@@ -232,13 +235,24 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
 // share is worked out once: few tokens are touched by the history, a bias or a
 // draft (a few percent of the vocabulary under a long history), so each warp
 // lists its own, with the additive term -f c - p [c > 0] + biases.  After the
-// lists no barrier joins the warps.
+// lists no barrier joins the warps until the next unit.
 //
 // Apart from its input (process_kernel): a warp's parts of kBatch rows at a time
 // come to shared memory by bulk copies, with further batches behind them; the
 // list is applied to them there, and they go out through registers, masked.
+// The bound is one reading and one writing of the logits: 241 us for B = 256,
+// R = 9, V = 152064 in bf16 with histories of up to 8192 tokens, 300 biases and
+// a mask for every row (1.46 GB, 6.0 TB/s; without any of them 206 us, as fast
+// as a plain copy).  What else was measured on that workload: the terms worked
+// into every vector that holds a touched token, from a dense table, 333 us
+// (nearly every warp-wide vector holds one); a copying pass and then single
+// touched tokens read and written over it, 292 us (32 sectors a step).
+// A small call is bound by its chain of two trips to memory, the barrier and
+// the launch: 6.8 us for B = 1, R = 5, V = 32000.
+//
 // In place (process_mask_kernel, process_in_place_kernel): only the vectors that
-// hold a forbidden token and the listed tokens are read and written, where they lie.
+// hold a forbidden token and the listed tokens are read and written, where they
+// lie.
 constexpr int kProcThreads = 256;
 constexpr int kProcWarps = kProcThreads / 32;
 constexpr int kProcPiece = 512;                        // tokens of a warp
@@ -928,7 +942,10 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
 
 // In place, the forbidden tokens: a warp takes 1024 tokens of one row, a lane
 // their mask word; a vector that holds a forbidden token is read (unless all
-// of it is forbidden) and written, no other is touched.
+// of it is forbidden) and written, no other is touched.  The bound is the
+// traffic of the sectors that hold one: 61 us for B = 256, R = 5, V = 128256
+// in bf16 where a quarter of the rows is free and the others allow 0.2, 10 or
+// 95 % (about 0.35 GB by that count; 104 us as a part of process_kernel).
 constexpr int kMaskThreads = 128;
 constexpr int kMaskPiece = 1024;
 template <class T, bool kShifted>
@@ -975,7 +992,10 @@ __global__ void __launch_bounds__(kMaskThreads) process_mask_kernel(const __grid
 }
 
 // In place, the listed tokens (after the forbidden ones: what is not allowed is
-// left alone).  A lane has an entry, for kProcRows rows at a time.
+// left alone).  A lane has an entry, for kProcRows rows at a time.  Each token
+// costs the reading and writing of a sector, whatever else is in it: 178 us
+// for B = 256, R = 9, V = 152064 in bf16 and histories of up to 8192 tokens
+// (3 % of the tokens in 37 % of the sectors), 92 us with up to 512 tokens.
 template <class T>
 __global__ void __launch_bounds__(kProcThreads, 5) process_in_place_kernel(const __grid_constant__ ProcessArgs a) {
   using Ty = ProcType<T>;

@@ -57,19 +57,6 @@ __device__ __forceinline__ bool warp_wait(unsigned long long* bar, unsigned pari
   return false;
 }
 
-// One bulk copy shared -> global, in the calling thread's current bulk group.
-// Both addresses and the size are multiples of 16 bytes; generic writes to the
-// source are made visible by fence_async() before it.
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, unsigned bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// All but the thread's latest kPending groups have read their sources.
-template <int kPending>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
-}
 // This thread's generic writes to shared memory come before later bulk copies.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
