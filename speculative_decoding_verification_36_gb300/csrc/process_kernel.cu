@@ -836,10 +836,11 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
         if (edge_row < n) {
           edge_ph = phase_of(u, i0 + edge_row);
           edge = edge_at(u, edge_ph);
-          // the very first and last vectors of the input were not copied whole
-          const long long from = u.row0 + (long long)(i0 + edge_row) * a.V - edge_ph;
-          if (edge >= 0 && (edge_side ? from + (edge / VEC + 1) * VEC > elements : from < 0))
-            stage(g, edge_row)[edge] = in[from + edge];
+          // vectors that reach over the input's ends were not copied (a piece's
+          // first vector may be the input's last)
+          const long long from = u.row0 + (long long)(i0 + edge_row) * a.V - edge_ph + (edge & -VEC);
+          if (edge >= 0 && (from < 0 || from + VEC > elements))
+            stage(g, edge_row)[edge] = in[from + (edge & (VEC - 1))];
         }
         __syncwarp();
       }

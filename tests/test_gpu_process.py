@@ -598,3 +598,19 @@ def test_workload_shapes_sampled():
         sub = {k: v[b:b + 1] if v is not None else None for k, v in x.items()}
         sub["logits"] = z[b:b + 1].cpu()
         check(sub, got[b:b + 1])
+
+
+# The last piece of the last row then ends inside the 16-byte vector that it
+# starts in, or lies across the input's end.
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 9, 511, 513, 515, 1027, 4097, 4099])
+def test_last_elements_of_rows_off_16_bytes(V, dtype):
+    rng = np.random.default_rng(V)
+    for B, R in ((1, 1), (1, 2), (1, 3), (2, 3), (1, 5), (3, 3), (7, 1), (2, 7)):
+        for mask in (None, "rows"):
+            x = make(rng, B, R, V, dtype, mask=mask)
+            x["logits"] += 100 * torch.sign(x["logits"])  # far from what other rows or calls left behind
+            check(x, call(x))
+            plain = {k: None for k in x} | {"logits": x["logits"]}
+            assert torch.equal(call(plain).cpu(), x["logits"])
+            check(x, call(x, out=(z := x["logits"].to(DEV)), logits=z))
