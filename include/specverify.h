@@ -458,7 +458,8 @@ int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32
  *                 its ancestors of a tree.  Tokens outside [0, V) count for
  *                 nothing (the verify judges them).
  *   parent_idx    [B, R-1] int32 as for spec_tree_verify_*, or NULL: a chain.
- *   token_state   [B, spec_token_state_words(V)] int32 or NULL (no history).
+ *   token_state   [B, spec_token_state_words(V)] int32 or NULL (no history);
+ *                 what it holds of tokens at V and above is not read.
  *   repetition, frequency, presence  [B] float each or NULL (1, 0, 0).
  *   bias_tokens, bias_values  [B, n_bias]; tokens outside [0, V) are skipped
  *                 (padding), a token given twice gets the sum, added in order.

@@ -428,6 +428,9 @@ __device__ __forceinline__ ProcAhead proc_ahead(const ProcessArgs& a, const Proc
   h.mine = a.state && u.base + 16 * tid < a.P
                ? __ldg((const unsigned short*)(a.state + (long long)u.b * a.words + a.P) + (u.base >> 4) + tid)
                : 0u;
+  // a state counted for a larger vocabulary may hold tokens that these rows do not have
+  const int own = a.V - u.base - 16 * tid;
+  if (own < 16) h.mine &= (1u << max(own, 0)) - 1u;
   const int N = a.drafts ? a.R - 1 : 0;
   h.draft = tid < N ? __ldg(a.drafts + (long long)u.b * N + tid) : -1;
   h.parent = a.parents && tid < N ? __ldg(a.parents + (long long)u.b * N + tid) : -1;

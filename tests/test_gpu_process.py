@@ -614,3 +614,30 @@ def test_last_elements_of_rows_off_16_bytes(V, dtype):
             plain = {k: None for k in x} | {"logits": x["logits"]}
             assert torch.equal(call(plain).cpu(), x["logits"])
             check(x, call(x, out=(z := x["logits"].to(DEV)), logits=z))
+
+
+# A padded vocabulary's state has the same size as the rows' own: tokens that
+# the rows do not have change nothing, beside the rows least of all.
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,counted", [(33, 64), (40, 64), (4097, 4128), (5000, 5024)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_state_of_a_padded_vocabulary(V, counted, dtype, in_place):
+    rng = np.random.default_rng(V)
+    B, R, guard = 3, 4, 64
+    x = make(rng, B, R, V, dtype, None, 200)
+    tok = np.concatenate([rng.integers(0, V, (B, 50)), np.tile(np.arange(V, counted), (B, 1))], 1).astype(np.int32)
+    state = sv.spec_token_state(B, counted, DEV)
+    assert state.shape == sv.spec_token_state(B, V, DEV).shape
+    sv.spec_count_tokens(state, dev(tok), counted, reset=True)
+    x["state"] = plain_ops.count(np.where(tok < V, tok, -1), np.full(B, tok.shape[1], np.int32), np.zeros(B, np.int32), V)
+    n = B * R * V
+    buf = torch.full((n + guard,), 77.0, dtype=dtype, device=DEV)
+    z = buf[:n].view(B, R, V)
+    z.copy_(x["logits"])
+    got = sv.spec_process_logits(
+        z, draft_tokens=dev(x["drafts"]), token_state=state, repetition=dev(x["rep"]), frequency=dev(x["freq"]),
+        presence=dev(x["pres"]), bias_tokens=dev(x["bias_tokens"]), bias_values=dev(x["bias_values"]),
+        allowed_mask=dev(x["mask"]), out=z if in_place else None)
+    check(x, got)
+    assert bool((buf[n:] == 77).all())
+    assert sv.spec_get_status() == 0
