@@ -67,7 +67,8 @@ extern "C" {
 #define SPEC_ERR_HINT (-6)        /* spec_verify_khint_*: k_min < 0, k_max > 255, k_min > k_max,
                                      a NaN threshold or h_lo > h_hi */
 #define SPEC_ERR_OVERLAP (-7)     /* spec_process_logits_*: out_logits overlaps logits without being it;
-                                     spec_kv_commit: out_lengths overlaps lengths */
+                                     spec_kv_append_*: the two caches overlap;
+                                     spec_kv_commit: so, or an output overlaps an input */
 
 /* Size of the fixed per-device scratch buffer of spec_verify_bf16_static_scratch. */
 #define SPEC_STATIC_SCRATCH_BYTES ((size_t)8 << 20)
@@ -523,7 +524,8 @@ int spec_process_logits_bf16(const uint16_t *logits, const int32_t *draft_tokens
  *   turns         [rot_dim / 2] uint64 (device): frequency i in 2^-64 turns a
  *                 position, that is radians / (2 pi) * 2^64.  The fraction of
  *                 a turn is exact for every position.
- *   key_cache, value_cache  [pages, page_size, Hkv, D].
+ *   key_cache, value_cache  [pages, page_size, Hkv, D], apart from each other
+ *                 (SPEC_ERR_OVERLAP).
  * Values are copied as they are; keys and queries are turned in fp32 and
  * rounded once.  Two tokens of a call that share a slot (sequences that share
  * a page they write to) are the caller's mistake: either may stay.
@@ -533,8 +535,8 @@ int spec_process_logits_bf16(const uint16_t *logits, const int32_t *draft_tokens
  * outside [0, pages): the tokens of that page are not written to the caches.
  * T >= 0 (<= 1025 with parent_idx), 1 <= D <= 1024, Hkv * D and Hq * D up to
  * 2^24.  Returns SPEC_OK,
- * SPEC_ERR_NULL, SPEC_ERR_SHAPE or SPEC_ERR_CUDA.  One launch on `stream`; no
- * scratch.
+ * SPEC_ERR_NULL, SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One
+ * launch on `stream`; no scratch.
  */
 int spec_kv_append_f32(const float *k, const float *v, int64_t kv_stride, const float *q, int64_t q_stride,
                        float *out_q, const int32_t *parent_idx, const int32_t *n_new, const int32_t *lengths,
@@ -570,7 +572,9 @@ int spec_kv_append_bf16(const uint16_t *k, const uint16_t *v, int64_t kv_stride,
  * (SPEC_FLAG_BAD_DATA): an out_len outside [1, N + 1], tokens that no path of
  * the tree carries, a parent outside [-1, i), slots past the page table or a
  * page outside [0, pages).
- * out_lengths may not share memory with lengths (SPEC_ERR_OVERLAP).
+ * The two caches may not share memory (their layers may lie by turns), nor
+ * out_nodes and out_lengths with each other or with lengths, out_len,
+ * out_path, tree_tokens or parent_idx (SPEC_ERR_OVERLAP).
  * 0 <= N <= 1024, 1 <= layers <= 32767.  Returns SPEC_OK, SPEC_ERR_NULL,
  * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`;
  * no scratch.

@@ -541,6 +541,14 @@ bool overlaps(const void* p, size_t n, const void* q, size_t m) {
   return a < b + m && b < a + n;
 }
 
+// Does a cache of `layers` parts of `size` bytes, `step` bytes apart, share memory
+// with another of the same shape?  (Layers of the two may lie by turns.)
+bool caches_overlap(const void* p, const void* q, uint64_t size, uint64_t step, int layers) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  const uint64_t apart = a < b ? b - a : a - b, k = apart / step, rest = apart % step;
+  return (k < (uint64_t)layers && rest < size) || (k + 1 < (uint64_t)layers && step - rest < size);
+}
+
 int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int32_t* parents,
                  const int32_t* state, const float* rep, const float* freq, const float* pres,
                  int n_bias, const int32_t* bias_tokens, const float* bias_values,
@@ -612,6 +620,10 @@ int kv_append_impl(bool bf16, const void* k, const void* v, int64_t kv_stride, c
   if (!k || !v || !lengths || !page_table || !k_cache || !v_cache || (rot > 0 && !turns) ||
       (Hq > 0 && (!q || !out_q)))
     return SPEC_ERR_NULL;
+  uint64_t size;
+  if (__builtin_mul_overflow((uint64_t)pages * page_size, (uint64_t)Hkv * D * (bf16 ? 2 : 4), &size))
+    return SPEC_ERR_SHAPE;
+  if (caches_overlap(k_cache, v_cache, size, size, 1)) return SPEC_ERR_OVERLAP;
   sv::KvAppendArgs a;
   memset(&a, 0, sizeof a);
   a.k = k;
@@ -956,8 +968,16 @@ int spec_kv_commit(void* key_cache, void* value_cache, int layers, int64_t layer
   if (!key_cache || !value_cache || !page_table || !lengths || !out_path || !out_len || !out_nodes ||
       !out_lengths || (N > 0 && (!tree_tokens || !parent_idx)))
     return SPEC_ERR_NULL;
-  // every CTA of a sequence reads its length: the new one goes elsewhere
-  if (overlaps(lengths, (size_t)B * 4, out_lengths, (size_t)B * 4)) return SPEC_ERR_OVERLAP;
+  // every CTA of a sequence reads its data while one writes the answers, and the
+  // two caches move side by side: what is written lies elsewhere
+  const size_t row = (size_t)B * 4, tree = row * N, path = row * (N + 1);
+  const struct { const void* p; size_t n; } read[] = {{lengths, row}, {out_len, row}, {out_path, path},
+                                                      {tree_tokens, tree}, {parent_idx, tree}};
+  for (const auto& r : read)
+    if (overlaps(r.p, r.n, out_lengths, row) || overlaps(r.p, r.n, out_nodes, path)) return SPEC_ERR_OVERLAP;
+  if (overlaps(out_lengths, row, out_nodes, path)) return SPEC_ERR_OVERLAP;
+  if (caches_overlap(key_cache, value_cache, (uint64_t)pages * page_size * entry_bytes, layer_bytes, layers))
+    return SPEC_ERR_OVERLAP;
   sv::KvCommitArgs a;
   memset(&a, 0, sizeof a);
   a.k_cache = key_cache;

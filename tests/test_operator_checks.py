@@ -120,3 +120,36 @@ def test_rope_turns():
     t = sv.spec_rope_turns([2 * math.pi / 4, 2 * math.pi * 0.75, 0.0, 2 * math.pi], "cpu")
     assert t.dtype == torch.int64
     assert [int(x) % 2 ** 64 for x in t] == [2 ** 62, 3 * 2 ** 62, 0, 0]
+
+
+def test_caches_that_share_memory_are_refused(lib):
+    def append(fn, kc, vc, pages=4):
+        return getattr(lib, fn)(FAKE, FAKE, 32, None, 0, None, None, None, FAKE, FAKE, 2, 3, 0, 2, 16, 16, 0, FAKE, kc, vc,
+                                pages, 16, 2, None)
+
+    for fn, size in (("spec_kv_append_f32", 4 * 16 * 32 * 4), ("spec_kv_append_bf16", 4 * 16 * 32 * 2)):
+        for d in (0, 16, size - 16):
+            assert append(fn, FAR, FAR + d) == _lib.SPEC_ERR_OVERLAP
+            assert append(fn, FAR + d, FAR) == _lib.SPEC_ERR_OVERLAP
+
+    def commit(kc, vc, layers=1, lb=4 * 16 * 64, nodes=FAR + 8192, oln=FAR + 4096, **at):
+        p = dict(ln=FAR, plen=FAR + 64, path=FAR + 128, tok=FAR + 256, par=FAR + 384) | at
+        return lib.spec_kv_commit(kc, vc, layers, lb, 4, 16, 64, FAR + 512, 2, p["ln"], p["tok"], p["par"], p["path"],
+                                  p["plen"], 2, 3, nodes, oln, None)
+
+    size, base = 4 * 16 * 64, FAR + (1 << 30)
+    for d in (0, 64, size - 64):
+        assert commit(base, base + d) == _lib.SPEC_ERR_OVERLAP
+        assert commit(base + d, base) == _lib.SPEC_ERR_OVERLAP
+    # three layers, twice their size apart: by turns they fit, half a layer on they do not
+    for d in (0, 2 * size, 4 * size, size // 2, size + size // 2, 3 * size + 64, 5 * size - 64 - size):
+        assert commit(base, base + d, 3, 2 * size) == _lib.SPEC_ERR_OVERLAP, d
+    for name in ("ln", "plen", "path", "tok", "par"):
+        assert commit(base, base + size, **{name: FAR + 4096}) == _lib.SPEC_ERR_OVERLAP, name
+        assert commit(base, base + size, **{name: FAR + 8192 + 4}) == _lib.SPEC_ERR_OVERLAP, name
+    assert commit(base, base + size, nodes=FAR + 4096) == _lib.SPEC_ERR_OVERLAP
+    # what is apart goes past these checks: to the device, which is not there
+    if not torch.cuda.is_available():
+        for d, layers, lb in ((size, 1, size), (3 * size, 3, size), (size, 3, 2 * size), (5 * size, 3, 2 * size)):
+            assert commit(base, base + d, layers, lb) == _lib.SPEC_ERR_CUDA
+            assert commit(base + d, base, layers, lb) == _lib.SPEC_ERR_CUDA
