@@ -481,7 +481,7 @@ int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32
  * Bad data: a parent index outside [-1, i), a repetition that is not positive
  * and finite, or a frequency or presence that is not finite makes every row of
  * that sequence NaN and sets SPEC_FLAG_BAD_DATA.
- * 1 <= R <= 1025, 1 <= V <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,
+ * 1 <= R <= 1025, 1 <= V <= 2^30, B * R < 2^31, n_bias <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,
  * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`
  * (two in place, with a mask and with penalties or biases); no scratch.
  */
@@ -575,7 +575,7 @@ int spec_kv_append_bf16(const uint16_t *k, const uint16_t *v, int64_t kv_stride,
  * The two caches may not share memory (their layers may lie by turns), nor
  * out_nodes and out_lengths with each other or with lengths, out_len,
  * out_path, tree_tokens or parent_idx (SPEC_ERR_OVERLAP).
- * 0 <= N <= 1024, 1 <= layers <= 32767.  Returns SPEC_OK, SPEC_ERR_NULL,
+ * 0 <= N <= 1024, 1 <= layers <= 32767, entry_bytes <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,
  * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`;
  * no scratch.
  */

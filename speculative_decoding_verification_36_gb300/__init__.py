@@ -481,7 +481,7 @@ def _token_stride(t, name, dtype, shape, device):
     lie at equal distances and whose heads are contiguous (such as a slice of a
     joint projection)."""
     B, T, H, D = shape
-    if t.dtype is dtype and t.shape == shape and t.device == device:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device:
         sb, st, sh, sd = t.stride()
         if sd == 1 and sh == D and sb == T * st:
             return st
@@ -571,6 +571,8 @@ def spec_kv_commit(key_cache, value_cache, page_table, lengths, tree_tokens, par
     pages, page_size, H, D = shape[-4:]
     layers = shape[0] if len(shape) == 5 else 1
     entry = H * D * key_cache.element_size()
+    if max(shape) >= 2 ** 31 or entry > 2 ** 30:  # more than the C entry point's ints carry
+        _lib.check(_lib.SPEC_ERR_SHAPE)
     if not isinstance(tree_tokens, torch.Tensor) or tree_tokens.dim() != 2:
         raise ValueError("tree_tokens must be [B, N]")
     B, N = tree_tokens.shape

@@ -534,6 +534,7 @@ int tree_sample_impl(bool bf16, const void* target, const void* draft, const int
 long long state_counts(int V) { return ((long long)V + 31) / 32 * 32; }
 long long state_words(int V) { return state_counts(V) + (state_counts(V) / 32 + 3) / 4 * 4; }
 constexpr int kMaxStateVocab = 1 << 30;
+constexpr int kMaxListed = 1 << 30;  // of a kernel's loop: its counter steps past the end
 
 // Do [p, p + n) and [q, q + m) share a byte?
 bool overlaps(const void* p, size_t n, const void* q, size_t m) {
@@ -555,7 +556,7 @@ int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int
                  const uint32_t* mask, int mask_rows, int B, int R, int V, void* out,
                  cudaStream_t stream) {
   if (B < 0 || R < 1 || R > sv::kMaxTreeNodes + 1 || V < 1 || V > kMaxStateVocab || n_bias < 0 ||
-      !sizes_ok(B, R, V) || (mask && mask_rows != 1 && mask_rows != R))
+      n_bias > kMaxListed || (long long)B * R > INT_MAX || !sizes_ok(B, R, V) || (mask && mask_rows != 1 && mask_rows != R))
     return SPEC_ERR_SHAPE;
   if (B == 0) return SPEC_OK;
   if (!logits || !out || (parents && !drafts) || (n_bias > 0 && (!bias_tokens || !bias_values)))
@@ -961,7 +962,7 @@ int spec_kv_commit(void* key_cache, void* value_cache, int layers, int64_t layer
                    const int32_t* out_path, const int32_t* out_len, int B, int N, int32_t* out_nodes,
                    int32_t* out_lengths, cudaStream_t stream) {
   if (B < 0 || N < 0 || N > sv::kMaxTreeNodes || layers < 1 || layers > 32767 || pages < 1 || page_size < 1 ||
-      entry_bytes < 1 || max_pages < 1 ||
+      entry_bytes < 1 || entry_bytes > kMaxListed || max_pages < 1 ||
       layer_bytes / page_size / entry_bytes < pages)
     return SPEC_ERR_SHAPE;
   if (B == 0) return SPEC_OK;

@@ -153,3 +153,22 @@ def test_caches_that_share_memory_are_refused(lib):
         for d, layers, lb in ((size, 1, size), (3 * size, 3, size), (size, 3, 2 * size), (5 * size, 3, 2 * size)):
             assert commit(base, base + d, layers, lb) == _lib.SPEC_ERR_CUDA
             assert commit(base + d, base, layers, lb) == _lib.SPEC_ERR_CUDA
+
+
+@pytest.mark.parametrize("fn", ["spec_process_logits_f32", "spec_process_logits_bf16"])
+def test_sizes_past_a_kernels_counters_are_refused(lib, fn):
+    def call(B=1, R=1, V=8, n_bias=0):
+        return getattr(lib, fn)(FAKE, None, None, None, None, None, None, n_bias, FAKE, FAKE, None, 0, B, R, V, FAKE, None)
+
+    assert call(n_bias=2 ** 30 + 1) == _lib.SPEC_ERR_SHAPE
+    assert call(n_bias=2 ** 31 - 1) == _lib.SPEC_ERR_SHAPE
+    assert call(B=2 ** 21, R=1024, V=1) == _lib.SPEC_ERR_SHAPE
+    assert lib.spec_kv_commit(FAKE, FAR, 1, 2 ** 40, 1, 1, 2 ** 30 + 1, FAR, 2, FAR, FAR, FAR, FAR, FAR, 2, 3, FAR, FAR,
+                              None) == _lib.SPEC_ERR_SHAPE
+
+
+def test_append_refuses_what_is_no_tensor():
+    k = torch.empty(1, 2, 1, 4)
+    for v in (None, 3, [1.0]):
+        with pytest.raises(ValueError, match="v must be"):
+            sv._token_stride(v, "v", torch.float32, k.shape, k.device)
