@@ -478,8 +478,8 @@ int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32
  * in fp32 and rounded once.  A masked token is -inf whatever its logit was
  * (NaN included), and a logit of -inf stays -inf whatever is added; a row with nothing allowed is all -inf, which a verify
  * reports as bad data, as it does a NaN that is allowed.
- * Bad data: a parent index outside [-1, i), a repetition that is not positive
- * and finite, or a frequency or presence that is not finite makes every row of
+ * Bad data: a parent index outside [-1, i), a repetition outside [2^-126,
+ * 2^126] (zero, negative, infinite or NaN among them), or a frequency or presence that is not finite makes every row of
  * that sequence NaN and sets SPEC_FLAG_BAD_DATA.
  * 1 <= R <= 1025, 1 <= V <= 2^30, B * R < 2^31, n_bias <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,
  * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`

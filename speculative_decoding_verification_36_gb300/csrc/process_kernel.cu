@@ -525,8 +525,9 @@ __device__ __forceinline__ void proc_lists(const ProcessArgs& a, ProcShared& sh,
   for (int i = kProcBiasRegs * kProcThreads + tid; i < a.n_bias; i += kProcThreads)
     put_bias(__ldg(a.bias_tokens + first + i) - u.base, __ldg(a.bias_values + first + i));
   if (shared) __syncthreads();
-  // a penalty that is no number, or a factor that is not positive
-  c.bad = (shared && g.bad) || !(c.rep > 0.f && c.rep < INFINITY) || !(fabsf(c.freq) < INFINITY) || !(fabsf(c.pres) < INFINITY);
+  // a penalty that is no number, or a factor that it is not possible to divide by:
+  // within these limits its reciprocal is a normal number too
+  c.bad = (shared && g.bad) || !(c.rep >= 0x1p-126f && c.rep <= 0x1p126f) || !(fabsf(c.freq) < INFINITY) || !(fabsf(c.pres) < INFINITY);
   if (c.bad && tid == 0) atomicOr(a.status, kStatusBadData);
 
   const int n_draft = shared ? g.n_draft : 0;

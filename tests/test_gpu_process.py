@@ -641,3 +641,28 @@ def test_state_of_a_padded_vocabulary(V, counted, dtype, in_place):
     check(x, got)
     assert bool((buf[n:] == 77).all())
     assert sv.spec_get_status() == 0
+
+
+# z / repetition is worked out with the reciprocal, which has to be a normal
+# number: outside these limits the call reports bad data instead of a wrong value.
+@pytest.mark.parametrize("value,good", [(2.0 ** -126, True), (2.0 ** 126, True), (2.0 ** -127, False),
+                                        (2.0 ** -149, False), (1.5 * 2.0 ** 126, False), (3e38, False)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_smallest_and_largest_repetitions(value, good, in_place):
+    rng = np.random.default_rng(21)
+    B, R, V = 2, 2, 64
+    z = torch.from_numpy((rng.uniform(0.5, 1, (B, R, V)) * 2.0 ** -4).astype(np.float32))
+    if value > 1:
+        z = z * 2.0 ** 100  # the quotient stays a normal number
+    rep = np.array([1.0, value], np.float32)
+    tok = np.tile(np.arange(V, dtype=np.int32), (B, 1))
+    st = dev(plain_ops.count(tok, np.full(B, V, np.int32), np.full(B, V, np.int32), V))
+    g = z.to(DEV)
+    got = sv.spec_process_logits(g, token_state=st, repetition=dev(rep), out=g if in_place else None).cpu()
+    assert torch.equal(got[0], z[0])
+    if good:
+        ref = z[1].double() / value
+        assert bool(((got[1].double() - ref).abs() <= 8 * 2.0 ** -24 * ref.abs()).all())
+    else:
+        assert bool(torch.isnan(got[1]).all())
+    assert sv.spec_get_status() == (0 if good else sv.SPEC_FLAG_BAD_DATA)
