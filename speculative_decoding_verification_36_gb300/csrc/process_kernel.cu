@@ -240,15 +240,15 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
 // Apart from its input (process_kernel): a warp's parts of kBatch rows at a time
 // come to shared memory by bulk copies, with further batches behind them; the
 // list is applied to them there, and they go out through registers, masked.
-// The bound is one reading and one writing of the logits: 241 us for B = 256,
+// The bound is one reading and one writing of the logits: 242 us for B = 256,
 // R = 9, V = 152064 in bf16 with histories of up to 8192 tokens, 300 biases and
-// a mask for every row (1.46 GB, 6.0 TB/s; without any of them 206 us, as fast
+// a mask for every row (1.46 GB, 6.0 TB/s; without any of them 207 us, as fast
 // as a plain copy).  What else was measured on that workload: the terms worked
 // into every vector that holds a touched token, from a dense table, 333 us
 // (nearly every warp-wide vector holds one); a copying pass and then single
 // touched tokens read and written over it, 292 us (32 sectors a step).
 // A small call is bound by its chain of two trips to memory, the barrier and
-// the launch: 6.8 us for B = 1, R = 5, V = 32000.
+// the launch: 6.9 us for B = 1, R = 5, V = 32000.
 //
 // In place (process_mask_kernel, process_in_place_kernel): only the vectors that
 // hold a forbidden token and the listed tokens are read and written, where they
