@@ -67,7 +67,8 @@ extern "C" {
 #define SPEC_ERR_HINT (-6)        /* spec_verify_khint_*: k_min < 0, k_max > 255, k_min > k_max,
                                      a NaN threshold or h_lo > h_hi */
 #define SPEC_ERR_OVERLAP (-7)     /* spec_process_logits_*: out_logits overlaps logits without being it;
-                                     spec_kv_append_*: the two caches overlap;
+                                     spec_kv_append_*: the two caches overlap, or out_q overlaps k, v,
+                                     a cache, or q without being it;
                                      spec_kv_commit: so, or an output overlaps an input */
 
 /* Size of the fixed per-device scratch buffer of spec_verify_bf16_static_scratch. */
@@ -510,7 +511,9 @@ int spec_process_logits_bf16(const uint16_t *logits, const int32_t *draft_tokens
  *   k, v          token t = b T + i at element t * kv_stride, its Hkv x D
  *                 values contiguous (a slice of a joint projection fits).
  *   q, out_q      the same with Hq heads and q_stride; out_q is [B, T, Hq, D],
- *                 or q itself when q_stride == Hq * D.  NULL when Hq == 0.
+ *                 or q itself when q_stride == Hq * D (or there is one token);
+ *                 it lies apart from the rest of q, from k, v and the caches
+ *                 (SPEC_ERR_OVERLAP).  NULL when Hq == 0.
  *   parent_idx    [B, T-1] int32 as for spec_tree_verify_*, or NULL.
  *   n_new         [B] int32 or NULL (T): tokens i >= n_new[b] are padding;
  *                 nothing is written for them.

@@ -550,6 +550,14 @@ bool caches_overlap(const void* p, const void* q, uint64_t size, uint64_t step, 
   return (k < (uint64_t)layers && rest < size) || (k + 1 < (uint64_t)layers && step - rest < size);
 }
 
+// Does one of `rows` parts of n bytes, `step` bytes apart, share a byte with [q, q + m)?
+bool rows_overlap(const void* p, uint64_t n, uint64_t step, uint64_t rows, const void* q, uint64_t m) {
+  if (n == 0 || m == 0) return false;
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  const uint64_t k = a + n > b ? 0 : (b - a - n) / step + 1;  // the first part that ends behind q
+  return k < rows && a + (unsigned __int128)step * k < (unsigned __int128)b + m;
+}
+
 int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int32_t* parents,
                  const int32_t* state, const float* rep, const float* freq, const float* pres,
                  int n_bias, const int32_t* bias_tokens, const float* bias_values,
@@ -625,6 +633,17 @@ int kv_append_impl(bool bf16, const void* k, const void* v, int64_t kv_stride, c
   if (__builtin_mul_overflow((uint64_t)pages * page_size, (uint64_t)Hkv * D * (bf16 ? 2 : 4), &size))
     return SPEC_ERR_SHAPE;
   if (caches_overlap(k_cache, v_cache, size, size, 1)) return SPEC_ERR_OVERLAP;
+  if (Hq > 0) {
+    // the warps of other tokens still read: turned queries go onto the same
+    // token's queries or where nothing of the call lies
+    const uint64_t esz = bf16 ? 2 : 4, rows = (uint64_t)B * T, kv = (uint64_t)Hkv * D * esz;
+    const uint64_t qn = (uint64_t)Hq * D * esz, n = rows * qn;
+    const bool own = out_q == q && (q_stride == (long long)Hq * D || rows == 1);
+    if ((!own && rows_overlap(q, qn, q_stride * esz, rows, out_q, n)) ||
+        rows_overlap(k, kv, kv_stride * esz, rows, out_q, n) || rows_overlap(v, kv, kv_stride * esz, rows, out_q, n) ||
+        overlaps(out_q, n, k_cache, size) || overlaps(out_q, n, v_cache, size))
+      return SPEC_ERR_OVERLAP;
+  }
   sv::KvAppendArgs a;
   memset(&a, 0, sizeof a);
   a.k = k;

@@ -172,3 +172,43 @@ def test_append_refuses_what_is_no_tensor():
     for v in (None, 3, [1.0]):
         with pytest.raises(ValueError, match="v must be"):
             sv._token_stride(v, "v", torch.float32, k.shape, k.device)
+
+
+# Every token's warps read their own queries, keys and values: turned queries go
+# where no other token still reads, or onto the same token's queries.
+@pytest.mark.parametrize("fn,e", [("spec_kv_append_f32", 4), ("spec_kv_append_bf16", 2)])
+def test_turned_queries_over_memory_in_use_are_refused(lib, fn, e):
+    base, Hq, Hkv, D, B, T = FAR + (1 << 32), 4, 2, 16, 2, 3
+    row, n = (Hq + 2 * Hkv) * D, B * T * Hq * D * e
+    size = 4 * 16 * Hkv * D * e
+    kc, vc = FAR, FAR + size
+
+    def call(q, out_q, k=base + Hq * D * e, v=base + (Hq + Hkv) * D * e, ks=row, qs=row, B=B, T=T):
+        return getattr(lib, fn)(k, v, ks, q, qs, out_q, None, None, FAKE, FAKE, B, T, Hq, Hkv, D, D, 0, FAKE, kc, vc, 4, 16,
+                                2, None)
+
+    # a joint projection's queries, in place: token 1's answer lies over token 0's keys
+    assert call(base, base) == _lib.SPEC_ERR_OVERLAP
+    dense = dict(k=base + (1 << 20), v=base + (2 << 20), ks=Hkv * D, qs=Hq * D)
+    for d in (-n + 16, -16, 16, n - 16):  # its own buffer, shifted
+        assert call(base, base + d, **dense) == _lib.SPEC_ERR_OVERLAP, d
+    far = base + (1 << 28)
+    assert call(base, base - n + e) == _lib.SPEC_ERR_OVERLAP  # the projection's rows
+    for at in (base + Hq * D * e, base + 5 * row * e + (Hq + Hkv) * D * e):
+        assert call(far, at, qs=Hq * D) == _lib.SPEC_ERR_OVERLAP
+        assert call(base, at) == _lib.SPEC_ERR_OVERLAP
+    kv = B * T * Hkv * D * e
+    for first in (dense["k"], dense["v"]):
+        for at in (first, first - n + 16, first + kv - 16):
+            assert call(base, at, **dense) == _lib.SPEC_ERR_OVERLAP
+    for at in (kc, kc - n + 16, kc + size - 16, vc, vc + size - 16):
+        assert call(base, at) == _lib.SPEC_ERR_OVERLAP
+    if not torch.cuda.is_available():  # what is apart goes on to the device, which is not there
+        assert call(base, base, **dense) == _lib.SPEC_ERR_CUDA
+        assert call(base, base, B=1, T=1) == _lib.SPEC_ERR_CUDA  # one token has no stride
+        assert call(base, base - n, **dense) == _lib.SPEC_ERR_CUDA
+        assert call(base, base + n, **dense) == _lib.SPEC_ERR_CUDA
+        assert call(base, base + 6 * row * e) == _lib.SPEC_ERR_CUDA
+        assert call(base, vc + size) == _lib.SPEC_ERR_CUDA
+        wide = n // e + row  # between two rows that lie this far apart there is room
+        assert call(base, base + row * e, ks=wide, qs=wide) == _lib.SPEC_ERR_CUDA
