@@ -577,7 +577,7 @@ int spec_kv_append_bf16(const uint16_t *k, const uint16_t *v, int64_t kv_stride,
  * page outside [0, pages).
  * The two caches may not share memory (their layers may lie by turns), nor
  * out_nodes and out_lengths with each other or with lengths, out_len,
- * out_path, tree_tokens or parent_idx (SPEC_ERR_OVERLAP).
+ * out_path, tree_tokens, parent_idx or page_table (SPEC_ERR_OVERLAP).
  * 0 <= N <= 1024, 1 <= layers <= 32767, entry_bytes <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,
  * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`;
  * no scratch.

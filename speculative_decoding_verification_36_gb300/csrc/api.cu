@@ -992,7 +992,7 @@ int spec_kv_commit(void* key_cache, void* value_cache, int layers, int64_t layer
   // two caches move side by side: what is written lies elsewhere
   const size_t row = (size_t)B * 4, tree = row * N, path = row * (N + 1);
   const struct { const void* p; size_t n; } read[] = {{lengths, row}, {out_len, row}, {out_path, path},
-                                                      {tree_tokens, tree}, {parent_idx, tree}};
+                                                      {tree_tokens, tree}, {parent_idx, tree}, {page_table, row * max_pages}};
   for (const auto& r : read)
     if (overlaps(r.p, r.n, out_lengths, row) || overlaps(r.p, r.n, out_nodes, path)) return SPEC_ERR_OVERLAP;
   if (overlaps(out_lengths, row, out_nodes, path)) return SPEC_ERR_OVERLAP;

@@ -212,3 +212,20 @@ def test_turned_queries_over_memory_in_use_are_refused(lib, fn, e):
         assert call(base, vc + size) == _lib.SPEC_ERR_CUDA
         wide = n // e + row  # between two rows that lie this far apart there is room
         assert call(base, base + row * e, ks=wide, qs=wide) == _lib.SPEC_ERR_CUDA
+
+
+# Every CTA of a sequence looks up its pages while one writes the answers.
+def test_commit_answers_over_the_page_table_are_refused(lib):
+    base = FAR + (1 << 32)
+
+    def commit(tab, nodes=FAR + 8192, oln=FAR + 4096, B=2, N=3, mp=5):
+        return lib.spec_kv_commit(base, base + (1 << 20), 1, 4 * 16 * 64, 4, 16, 64, tab, mp, FAR, FAR + 256, FAR + 384,
+                                  FAR + 128, FAR + 64, B, N, nodes, oln, None)
+
+    for at, n in ((FAR + 8192, 2 * 4 * 4), (FAR + 4096, 2 * 4)):
+        for d in (0, 4 - 2 * 5 * 4, n - 4):  # the table's last word, or its first
+            assert commit(at + d) == _lib.SPEC_ERR_OVERLAP
+    if not torch.cuda.is_available():
+        for at, n in ((FAR + 8192, 2 * 4 * 4), (FAR + 4096, 2 * 4)):
+            for d in (-2 * 5 * 4, n):
+                assert commit(at + d) == _lib.SPEC_ERR_CUDA
