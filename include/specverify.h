@@ -66,10 +66,9 @@ extern "C" {
                                      SPEC_STATIC_SCRATCH_BYTES of scratch */
 #define SPEC_ERR_HINT (-6)        /* spec_verify_khint_*: k_min < 0, k_max > 255, k_min > k_max,
                                      a NaN threshold or h_lo > h_hi */
-#define SPEC_ERR_OVERLAP (-7)     /* spec_process_logits_*: out_logits overlaps logits without being it;
-                                     spec_kv_append_*: the two caches overlap, or out_q overlaps k, v,
-                                     a cache, or q without being it;
-                                     spec_kv_commit: so, or an output overlaps an input */
+#define SPEC_ERR_OVERLAP (-7)     /* spec_count_tokens, spec_process_logits_*, spec_kv_append_*,
+                                     spec_kv_commit: memory that the call writes overlaps memory that it
+                                     reads or another output, where the entry point does not allow it */
 
 /* Size of the fixed per-device scratch buffer of spec_verify_bf16_static_scratch. */
 #define SPEC_STATIC_SCRATCH_BYTES ((size_t)8 << 20)
@@ -444,7 +443,8 @@ int spec_token_state_words(int V);
  * Bad data: a length outside [0, stride] or a prompt length outside [0,
  * length] adds nothing to that row and sets SPEC_FLAG_BAD_DATA.  Counts are
  * exact.  Returns SPEC_OK, SPEC_ERR_NULL, SPEC_ERR_SHAPE (B < 0, a stride
- * outside [0, 2^30], V, a state off a 16-byte boundary) or SPEC_ERR_CUDA.  Asynchronous on `stream`; no scratch.
+ * outside [0, 2^30], V, a state off a 16-byte boundary), SPEC_ERR_OVERLAP (the
+ * state and an input share memory) or SPEC_ERR_CUDA.  Asynchronous on `stream`; no scratch.
  */
 int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32_t *prompt_lengths, int B,
                       int stride, int V, int reset, int32_t *state, cudaStream_t stream);
@@ -470,7 +470,8 @@ int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32
  *                 v / 32 set = token v allowed.  mask_rows is R, or 1 for one
  *                 mask per sequence.  Bits at V and above are not read as tokens.
  *   out_logits    [B, R, V]: `logits` itself (in place: only what changes is
- *                 read and written), or memory apart from it.
+ *                 read and written), or memory apart from it; apart from
+ *                 every other input (SPEC_ERR_OVERLAP).
  * With c the occurrences of v among the output tokens and the drafts above the
  * row, and seen = (v in the prompt or c > 0):
  *   z1 = seen ? (z > 0 ? z / repetition : z * repetition) : z
@@ -512,8 +513,8 @@ int spec_process_logits_bf16(const uint16_t *logits, const int32_t *draft_tokens
  *                 values contiguous (a slice of a joint projection fits).
  *   q, out_q      the same with Hq heads and q_stride; out_q is [B, T, Hq, D],
  *                 or q itself when q_stride == Hq * D (or there is one token);
- *                 it lies apart from the rest of q, from k, v and the caches
- *                 (SPEC_ERR_OVERLAP).  NULL when Hq == 0.
+ *                 it lies apart from the rest of q, every other input and
+ *                 the caches (SPEC_ERR_OVERLAP).  NULL when Hq == 0.
  *   parent_idx    [B, T-1] int32 as for spec_tree_verify_*, or NULL.
  *   n_new         [B] int32 or NULL (T): tokens i >= n_new[b] are padding;
  *                 nothing is written for them.
@@ -528,7 +529,9 @@ int spec_process_logits_bf16(const uint16_t *logits, const int32_t *draft_tokens
  *                 position, that is radians / (2 pi) * 2^64.  The fraction of
  *                 a turn is exact for every position.
  *   key_cache, value_cache  [pages, page_size, Hkv, D], apart from each other
- *                 (SPEC_ERR_OVERLAP).
+ *                 and from every input (SPEC_ERR_OVERLAP).  Only k may lie in
+ *                 key_cache, and v in value_cache, each token at its own slot:
+ *                 the pages are not looked up to check that.
  * Values are copied as they are; keys and queries are turned in fp32 and
  * rounded once.  Two tokens of a call that share a slot (sequences that share
  * a page they write to) are the caller's mistake: either may stay.
@@ -575,9 +578,8 @@ int spec_kv_append_bf16(const uint16_t *k, const uint16_t *v, int64_t kv_stride,
  * (SPEC_FLAG_BAD_DATA): an out_len outside [1, N + 1], tokens that no path of
  * the tree carries, a parent outside [-1, i), slots past the page table or a
  * page outside [0, pages).
- * The two caches may not share memory (their layers may lie by turns), nor
- * out_nodes and out_lengths with each other or with lengths, out_len,
- * out_path, tree_tokens, parent_idx or page_table (SPEC_ERR_OVERLAP).
+ * The two caches (whose layers may lie by turns), out_nodes and out_lengths
+ * share no memory with each other or with an input (SPEC_ERR_OVERLAP).
  * 0 <= N <= 1024, 1 <= layers <= 32767, entry_bytes <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,
  * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`;
  * no scratch.

@@ -539,7 +539,19 @@ constexpr int kMaxListed = 1 << 30;  // of a kernel's loop: its counter steps pa
 // Do [p, p + n) and [q, q + m) share a byte?
 bool overlaps(const void* p, size_t n, const void* q, size_t m) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + m && b < a + n;
+  return n > 0 && m > 0 && a < b + m && b < a + n;
+}
+
+// An input of a call, and whether one of several shares a byte with [p, p + n).
+struct Span {
+  const void* p;
+  size_t n;
+};
+template <size_t N>
+bool any_overlaps(const Span (&s)[N], const void* p, size_t n) {
+  for (const Span& x : s)
+    if (overlaps(x.p, x.n, p, n)) return true;
+  return false;
 }
 
 // Does a cache of `layers` parts of `size` bytes, `step` bytes apart, share memory
@@ -573,6 +585,13 @@ int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int
   const size_t esz = bf16 ? 2 : 4;
   const size_t bytes = (size_t)B * R * V * esz;
   if (logits != out && overlaps(logits, bytes, out, bytes)) return SPEC_ERR_OVERLAP;
+  // CTAs that still have rows to do read these while others write
+  const size_t row = (size_t)B * 4, W = ((size_t)V + 31) / 32;
+  const Span read[] = {{drafts, drafts ? row * (R - 1) : 0}, {parents, parents ? row * (R - 1) : 0},
+                       {state, state ? row * state_words(V) : 0}, {rep, rep ? row : 0}, {freq, freq ? row : 0},
+                       {pres, pres ? row : 0}, {bias_tokens, row * n_bias}, {bias_values, row * n_bias},
+                       {mask, mask ? row * mask_rows * W : 0}};
+  if (any_overlaps(read, out, bytes)) return SPEC_ERR_OVERLAP;
   sv::ProcessArgs a;
   memset(&a, 0, sizeof a);
   a.in = logits;
@@ -590,7 +609,7 @@ int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int
   a.bias_values = bias_values;
   a.mask = mask;
   a.mask_rows = mask_rows;
-  a.W = (int)(((long long)V + 31) / 32);
+  a.W = (int)W;
   a.B = B;
   a.R = R;
   a.V = V;
@@ -633,15 +652,24 @@ int kv_append_impl(bool bf16, const void* k, const void* v, int64_t kv_stride, c
   if (__builtin_mul_overflow((uint64_t)pages * page_size, (uint64_t)Hkv * D * (bf16 ? 2 : 4), &size))
     return SPEC_ERR_SHAPE;
   if (caches_overlap(k_cache, v_cache, size, size, 1)) return SPEC_ERR_OVERLAP;
+  // The warps of other tokens still read: turned queries go onto the same
+  // token's queries or where nothing of the call lies, and a cache lies apart from
+  // all but its own new values, which may be at their slots.
+  const uint64_t esz = bf16 ? 2 : 4, rows = (uint64_t)B * T, kv = (uint64_t)Hkv * D * esz;
+  const uint64_t qn = (uint64_t)Hq * D * esz, n = rows * qn;
+  const size_t row = (size_t)B * 4;
+  const Span read[] = {{parents, parents ? row * (T - 1) : 0}, {n_new, n_new ? row : 0}, {lengths, row},
+                       {page_table, row * max_pages}, {turns, (size_t)(rot / 2) * 8}};
+  if (any_overlaps(read, k_cache, size) || any_overlaps(read, v_cache, size) ||
+      rows_overlap(k, kv, kv_stride * esz, rows, v_cache, size) ||
+      rows_overlap(v, kv, kv_stride * esz, rows, k_cache, size))
+    return SPEC_ERR_OVERLAP;
   if (Hq > 0) {
-    // the warps of other tokens still read: turned queries go onto the same
-    // token's queries or where nothing of the call lies
-    const uint64_t esz = bf16 ? 2 : 4, rows = (uint64_t)B * T, kv = (uint64_t)Hkv * D * esz;
-    const uint64_t qn = (uint64_t)Hq * D * esz, n = rows * qn;
     const bool own = out_q == q && (q_stride == (long long)Hq * D || rows == 1);
     if ((!own && rows_overlap(q, qn, q_stride * esz, rows, out_q, n)) ||
         rows_overlap(k, kv, kv_stride * esz, rows, out_q, n) || rows_overlap(v, kv, kv_stride * esz, rows, out_q, n) ||
-        overlaps(out_q, n, k_cache, size) || overlaps(out_q, n, v_cache, size))
+        rows_overlap(q, qn, q_stride * esz, rows, k_cache, size) || rows_overlap(q, qn, q_stride * esz, rows, v_cache, size) ||
+        any_overlaps(read, out_q, n) || overlaps(out_q, n, k_cache, size) || overlaps(out_q, n, v_cache, size))
       return SPEC_ERR_OVERLAP;
   }
   sv::KvAppendArgs a;
@@ -916,6 +944,9 @@ int spec_count_tokens(const int32_t* tokens, const int32_t* lengths, const int32
   if (B == 0) return SPEC_OK;
   if (!state || (stride > 0 && !tokens)) return SPEC_ERR_NULL;
   if (!aligned16(state)) return SPEC_ERR_SHAPE;
+  const size_t row = (size_t)B * 4;
+  const Span read[] = {{tokens, row * stride}, {lengths, lengths ? row : 0}, {prompt_lengths, prompt_lengths ? row : 0}};
+  if (any_overlaps(read, state, row * state_words(V))) return SPEC_ERR_OVERLAP;
   DeviceState* d = nullptr;
   const int rc = get_device_state(&d);
   if (rc) return rc;
@@ -991,13 +1022,20 @@ int spec_kv_commit(void* key_cache, void* value_cache, int layers, int64_t layer
   // every CTA of a sequence reads its data while one writes the answers, and the
   // two caches move side by side: what is written lies elsewhere
   const size_t row = (size_t)B * 4, tree = row * N, path = row * (N + 1);
-  const struct { const void* p; size_t n; } read[] = {{lengths, row}, {out_len, row}, {out_path, path},
-                                                      {tree_tokens, tree}, {parent_idx, tree}, {page_table, row * max_pages}};
-  for (const auto& r : read)
-    if (overlaps(r.p, r.n, out_lengths, row) || overlaps(r.p, r.n, out_nodes, path)) return SPEC_ERR_OVERLAP;
-  if (overlaps(out_lengths, row, out_nodes, path)) return SPEC_ERR_OVERLAP;
-  if (caches_overlap(key_cache, value_cache, (uint64_t)pages * page_size * entry_bytes, layer_bytes, layers))
+  const Span read[] = {{lengths, row}, {out_len, row}, {out_path, path}, {tree_tokens, tree}, {parent_idx, tree},
+                       {page_table, row * max_pages}};
+  if (any_overlaps(read, out_lengths, row) || any_overlaps(read, out_nodes, path) ||
+      overlaps(out_lengths, row, out_nodes, path))
     return SPEC_ERR_OVERLAP;
+  const uint64_t size = (uint64_t)pages * page_size * entry_bytes;
+  if (caches_overlap(key_cache, value_cache, size, layer_bytes, layers)) return SPEC_ERR_OVERLAP;
+  for (const void* cache : {key_cache, value_cache}) {
+    for (const Span& x : read)
+      if (rows_overlap(cache, size, layer_bytes, layers, x.p, x.n)) return SPEC_ERR_OVERLAP;
+    if (rows_overlap(cache, size, layer_bytes, layers, out_lengths, row) ||
+        rows_overlap(cache, size, layer_bytes, layers, out_nodes, path))
+      return SPEC_ERR_OVERLAP;
+  }
   sv::KvCommitArgs a;
   memset(&a, 0, sizeof a);
   a.k_cache = key_cache;

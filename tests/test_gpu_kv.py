@@ -433,3 +433,18 @@ def test_appends_on_two_streams():
         torch.cuda.synchronize()
         for x, q, (a, b, c) in zip(xs, qs, alone):
             assert torch.equal(q, a) and torch.equal(x["kc"], b) and torch.equal(x["vc"], c)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_keys_and_values_at_their_own_slots(dtype, interleaved):
+    """A projection that wrote into consecutive pages is turned where it lies."""
+    rng = np.random.default_rng(11)
+    T, H, D, page, length = 37, 3, 32, 8, 13
+    x = make(rng, 1, T, 0, H, D, 24, dtype, page, 0, joint=False)
+    x["lengths"][:] = length
+    x["table"] = np.arange(7, dtype=np.int32)[None]
+    x["kc"], x["vc"] = (torch.randn((7, page, H, D), device=DEV).to(dtype) for _ in range(2))
+    x["k"], x["v"] = (x[c].view(1, -1, H, D)[:, length:length + T] for c in ("kc", "vc"))
+    run_and_check(x, interleaved)
+    assert sv.spec_get_status() == 0

@@ -229,3 +229,97 @@ def test_commit_answers_over_the_page_table_are_refused(lib):
         for at, n in ((FAR + 8192, 2 * 4 * 4), (FAR + 4096, 2 * 4)):
             for d in (-2 * 5 * 4, n):
                 assert commit(at + d) == _lib.SPEC_ERR_CUDA
+
+
+def expect(lib, call, where, written):
+    """`call(**{name: address})` is refused where an input of n bytes shares its
+    first or last word with what is written, and goes on next to it."""
+    for name, n in where.items():
+        for w, m in written:
+            for at in (w, w - n + 4, w + m - 4):
+                assert call(**{name: at}) == _lib.SPEC_ERR_OVERLAP, (name, at - w)
+    if not torch.cuda.is_available():
+        assert call() == _lib.SPEC_ERR_CUDA
+        for name, n in where.items():
+            for w, m in written:
+                for at in (w - n, w + m):
+                    assert call(**{name: at}) == _lib.SPEC_ERR_CUDA, (name, at - w)
+
+
+# What a call writes lies apart from the lists, tables and states that its CTAs read meanwhile.
+@pytest.mark.parametrize("e", [4, 2])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_process_output_over_what_it_reads_is_refused(lib, e, in_place):
+    B, R, V, nb, W = 2, 3, 64, 6, 2
+    z, out, words = FAR, FAR + (1 << 20), plain_ops.state_words(V)[1]
+    if in_place:
+        out = z
+    f = lib.spec_process_logits_f32 if e == 4 else lib.spec_process_logits_bf16
+    other = {n: FAR + (2 << 20) + i * 65536 for i, n in enumerate(("d", "p", "st", "rep", "fr", "pr", "bt", "bv", "mask"))}
+
+    def call(**at):
+        x = other | at
+        return f(z, x["d"], x["p"], x["st"], x["rep"], x["fr"], x["pr"], nb, x["bt"], x["bv"], x["mask"], R, B, R, V, out, None)
+
+    sizes = dict(d=B * (R - 1) * 4, p=B * (R - 1) * 4, rep=B * 4, fr=B * 4, pr=B * 4, bt=B * nb * 4, bv=B * nb * 4,
+                 mask=B * R * W * 4)
+    expect(lib, call, sizes, [(out, B * R * V * e)])
+    for at in (out, out - B * words * 4 + 16, out + B * R * V * e - 16):  # a state lies on 16 bytes
+        assert call(st=at) == _lib.SPEC_ERR_OVERLAP
+
+
+def test_counted_state_over_what_it_reads_is_refused(lib):
+    B, S, V = 2, 5, 64
+    n = B * plain_ops.state_words(V)[1] * 4
+
+    def call(tok=FAR, ln=FAR + 65536, pl=FAR + 2 * 65536):
+        return lib.spec_count_tokens(tok, ln, pl, B, S, V, 0, FAR + (1 << 20), None)
+
+    expect(lib, call, dict(tok=B * S * 4, ln=B * 4, pl=B * 4), [(FAR + (1 << 20), n)])
+
+
+@pytest.mark.parametrize("e", [4, 2])
+def test_append_writes_over_what_it_reads_are_refused(lib, e):
+    B, T, Hq, Hkv, D, pages, page, most = 2, 3, 4, 2, 16, 4, 16, 2
+    size, nq = pages * page * Hkv * D * e, B * T * Hq * D * e
+    kc, vc, oq = FAR + (4 << 20), FAR + (5 << 20), FAR + (6 << 20)
+    f = lib.spec_kv_append_f32 if e == 4 else lib.spec_kv_append_bf16
+    other = {n: FAR + i * 65536 for i, n in enumerate(("k", "v", "q", "par", "new", "ln", "tab", "turns"))}
+
+    def call(**at):
+        x = other | at
+        return f(x["k"], x["v"], Hkv * D, x["q"], Hq * D, oq, x["par"], x["new"], x["ln"], x["tab"], B, T, Hq, Hkv, D, D, 0,
+                 x["turns"], kc, vc, pages, page, most, None)
+
+    expect(lib, call, dict(par=B * (T - 1) * 4, new=B * 4, ln=B * 4, tab=B * most * 4, turns=D // 2 * 8),
+           [(kc, size), (vc, size), (oq, nq)])
+    expect(lib, call, dict(q=nq), [(kc, size), (vc, size)])
+    expect(lib, call, dict(k=B * T * Hkv * D * e), [(vc, size)])  # in its own cache a token may lie at its slot
+    expect(lib, call, dict(v=B * T * Hkv * D * e), [(kc, size)])
+    if not torch.cuda.is_available():
+        assert call(k=kc) == _lib.SPEC_ERR_CUDA
+        assert call(v=vc) == _lib.SPEC_ERR_CUDA
+
+
+def test_commit_writes_over_what_it_reads_are_refused(lib):
+    B, N, layers, most = 2, 3, 3, 5
+    size, step = 4 * 16 * 64, 3 * 4 * 16 * 64
+    kc, vc = FAR + (4 << 20), FAR + (4 << 20) + size  # layers by turns, with room between them
+    other = {n: FAR + i * 65536 for i, n in enumerate(("tab", "ln", "tok", "par", "path", "plen", "nodes", "oln"))}
+
+    def call(**at):
+        x = other | at
+        return lib.spec_kv_commit(kc, vc, layers, step, 4, 16, 64, x["tab"], most, x["ln"], x["tok"], x["par"], x["path"],
+                                  x["plen"], B, N, x["nodes"], x["oln"], None)
+
+    both = [(kc + l * step, 2 * size) for l in range(layers)]
+    expect(lib, call, dict(tab=B * most * 4, ln=B * 4, tok=B * N * 4, par=B * N * 4, path=B * (N + 1) * 4, plen=B * 4,
+                           nodes=B * (N + 1) * 4, oln=B * 4), both)
+
+
+def test_empty_inputs_share_no_memory(lib):
+    """A tree without nodes has no tokens, wherever its pointers point."""
+    if not torch.cuda.is_available():
+        nodes = FAR + 4096
+        assert lib.spec_kv_commit(FAR + (1 << 20), FAR + (2 << 20), 1, 4096, 4, 16, 64, FAR, 2, FAR + 64, nodes + 4, nodes + 4,
+                                  FAR + 128, FAR + 192, 2, 0, nodes, FAR + 256, None) == _lib.SPEC_ERR_CUDA
