@@ -92,11 +92,20 @@ def _out(t, shape, dtype, device, name):
     return t
 
 
+def _c_ints(*sizes):
+    """Refuses what the C entry points' ints do not carry (ctypes would drop the
+    upper bits)."""
+    for n in sizes:
+        if not -2 ** 31 <= n < 2 ** 31:
+            _lib.check(_lib.SPEC_ERR_SHAPE)
+
+
 def _chain_args(target_logits, draft_logits, draft_tokens, temperature):
     bf16 = _is_bf16(target_logits, "target_logits")
     if target_logits.dim() != 3:
         raise ValueError("target_logits must be [B, K+1, V]")
     B, K1, V = target_logits.shape
+    _c_ints(B, K1, V)
     K = K1 - 1
     if temperature > 0 and K > 0:
         if draft_logits is None:
@@ -210,6 +219,7 @@ def spec_verify_khint(target_logits, draft_logits, draft_tokens, temperature: fl
     k_max], -1 for a bad sequence.  Returns (tokens [B,K+1], n [B], k_next [B]
     int32, mean_entropy [B] float32)."""
     bf16, B, K, V = _chain_args(target_logits, draft_logits, draft_tokens, temperature)
+    _c_ints(int(k_min), int(k_max))
     dev = target_logits.device
     tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens")
     n = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted")
@@ -254,6 +264,7 @@ def spec_tree_verify_greedy(target_logits, tree_tokens, parent_idx, out_path=Non
     if target_logits.dim() != 3:
         raise ValueError("target_logits must be [B, N+1, V]")
     B, N1, V = target_logits.shape
+    _c_ints(B, N1, V)
     N = N1 - 1
     W = (N + 31) // 32
     dev = target_logits.device
@@ -294,6 +305,7 @@ def spec_tree_verify_sampling(target_logits, draft_logits, tree_tokens, parent_i
         raise ValueError(f"draft_logits has shape {tuple(draft_logits.shape)}, expected "
                          f"{tuple(target_logits.shape)}")
     B, N1, V = target_logits.shape
+    _c_ints(B, N1, V)
     N = N1 - 1
     dev = target_logits.device
     _same_device(draft_logits, dev, "draft_logits")
@@ -321,6 +333,7 @@ def spec_acceptance_stats(n_accepted, K: int, stream=None):
         raise TypeError("n_accepted must be a contiguous 1-D int32 CUDA tensor")
     dev = n_accepted.device
     B = n_accepted.shape[0]
+    _c_ints(B, int(K))
     hist = torch.empty((K + 2,), dtype=torch.int64, device=dev)
     alpha = torch.empty((max(K, 0),), dtype=torch.float64, device=dev)
     mean = torch.empty((1,), dtype=torch.float64, device=dev)
@@ -342,6 +355,7 @@ def spec_ngram_draft(tokens, lengths, n_min: int, n_max: int, K: int, out_drafts
     if tokens.dim() != 2:
         raise ValueError("tokens must be [B, Lmax]")
     B, Lmax = tokens.shape
+    _c_ints(B, Lmax, int(n_min), int(n_max), int(K))
     _i32(tokens, (B, Lmax), "tokens")
     dev = tokens.device
     _i32(lengths, (B,), "lengths", dev)
@@ -391,6 +405,12 @@ def _invoke(fn, device, stream, *args):
         _lib.check(code)
 
 
+# Sizes that the C entry points' ints do not carry are refused: `_too_large if
+# (a | b | ...) >> 31`, for sizes that are not negative (a third of the time of _c_ints).
+def _too_large():
+    _lib.check(_lib.SPEC_ERR_SHAPE)
+
+
 def _words(V: int) -> int:
     """spec_token_state_words(V), worked out here (the layout is the header's)."""
     if not 1 <= V <= 2 ** 30:
@@ -416,6 +436,8 @@ def spec_count_tokens(state, tokens, V: int, lengths=None, prompt_lengths=None, 
     if not isinstance(tokens, torch.Tensor) or not tokens.is_cuda or tokens.dim() != 2:
         raise ValueError("tokens must be a CUDA tensor [B, S]")
     B, S = tokens.shape
+    if (B | S) >> 31:
+        _too_large()
     dev, i32, V = tokens.device, torch.int32, int(V)
     _invoke(_lib.load().spec_count_tokens, dev, stream, _arg(tokens, i32, (B, S), dev, "tokens"),
             _arg(lengths, i32, (B,), dev, "lengths"), _arg(prompt_lengths, i32, (B,), dev, "prompt_lengths"), B, S, V,
@@ -450,6 +472,8 @@ def spec_process_logits(logits, draft_tokens=None, parent_idx=None, token_state=
         if bias_tokens.dim() != 2:
             raise ValueError("bias_tokens must be [B, n]")
         n_bias = bias_tokens.shape[1]
+    if (B | R | V | n_bias) >> 31:
+        _too_large()
     mask = None
     if allowed_mask is not None:
         W = (V + 31) // 32
@@ -532,12 +556,16 @@ def spec_kv_append(k, v, key_cache, value_cache, page_table, lengths, turns=None
     rot = 0
     if turns is not None:
         rot = 2 * turns.numel()
+    if (B | T | Hkv | D | rot | pages | page_size | max_pages) >> 31:
+        _too_large()
     qp = oq = None
     Hq = qs = 0
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError("q must be a CUDA tensor [B, T, Hq, D]")
         Hq = q.shape[2]
+        if Hq >> 31:
+            _too_large()
         qs = _token_stride(q, "q", dt, (B, T, Hq, D), dev)
         if out_q is None:
             out_q = torch.empty((B, T, Hq, D), dtype=dt, device=dev)
@@ -571,14 +599,14 @@ def spec_kv_commit(key_cache, value_cache, page_table, lengths, tree_tokens, par
     pages, page_size, H, D = shape[-4:]
     layers = shape[0] if len(shape) == 5 else 1
     entry = H * D * key_cache.element_size()
-    if max(shape) >= 2 ** 31 or entry > 2 ** 30:  # more than the C entry point's ints carry
-        _lib.check(_lib.SPEC_ERR_SHAPE)
     if not isinstance(tree_tokens, torch.Tensor) or tree_tokens.dim() != 2:
         raise ValueError("tree_tokens must be [B, N]")
     B, N = tree_tokens.shape
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     max_pages = page_table.shape[1]
+    if (layers | pages | page_size | entry | max_pages | B | N) >> 31:
+        _too_large()
     if out_nodes is None:
         out_nodes = torch.empty((B, N + 1), dtype=i32, device=dev)
     if out_lengths is None:

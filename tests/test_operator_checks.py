@@ -323,3 +323,58 @@ def test_empty_inputs_share_no_memory(lib):
         nodes = FAR + 4096
         assert lib.spec_kv_commit(FAR + (1 << 20), FAR + (2 << 20), 1, 4096, 4, 16, 64, FAR, 2, FAR + 64, nodes + 4, nodes + 4,
                                   FAR + 128, FAR + 192, 2, 0, nodes, FAR + 256, None) == _lib.SPEC_ERR_CUDA
+
+
+class Huge(torch.Tensor):
+    """A tensor of any size, without memory, that passes for one on a GPU."""
+    is_cuda = True
+
+
+def huge(*shape, dtype=torch.int32):
+    return torch.empty(shape, dtype=dtype, device="meta").as_subclass(Huge)
+
+
+BIG = 2 ** 32 + 8  # 8 in a C int
+
+
+@pytest.mark.parametrize("call", [
+    lambda i, f: sv.spec_process_logits(f(1, 1, BIG)),
+    lambda i, f: sv.spec_process_logits(f(1, BIG, 8)),
+    lambda i, f: sv.spec_process_logits(f(BIG, 1, 8)),
+    lambda i, f: sv.spec_process_logits(f(1, 1, 8), bias_tokens=i(1, BIG), bias_values=f(1, BIG)),
+    lambda i, f: sv.spec_count_tokens(i(1, 40), i(1, BIG), 8),
+    lambda i, f: sv.spec_count_tokens(i(BIG, 40), i(BIG, 1), 8),
+    lambda i, f: sv.spec_kv_append(f(1, 2, 1, 8), f(1, 2, 1, 8), f(BIG, 4, 1, 8), f(BIG, 4, 1, 8), i(1, 2), i(1)),
+    lambda i, f: sv.spec_kv_append(f(1, 2, 1, 8), f(1, 2, 1, 8), f(4, BIG, 1, 8), f(4, BIG, 1, 8), i(1, 2), i(1)),
+    lambda i, f: sv.spec_kv_append(f(1, 2, 1, 8), f(1, 2, 1, 8), f(4, 4, 1, 8), f(4, 4, 1, 8), i(1, BIG), i(1)),
+    lambda i, f: sv.spec_kv_append(f(1, BIG, 1, 8), f(1, BIG, 1, 8), f(4, 4, 1, 8), f(4, 4, 1, 8), i(1, 2), i(1)),
+    lambda i, f: sv.spec_kv_append(f(BIG, 1, 1, 8), f(BIG, 1, 1, 8), f(4, 4, 1, 8), f(4, 4, 1, 8), i(BIG, 2), i(BIG)),
+    lambda i, f: sv.spec_kv_append(f(1, 2, BIG, 8), f(1, 2, BIG, 8), f(4, 4, BIG, 8), f(4, 4, BIG, 8), i(1, 2), i(1)),
+    lambda i, f: sv.spec_kv_append(f(1, 2, 1, BIG), f(1, 2, 1, BIG), f(4, 4, 1, BIG), f(4, 4, 1, BIG), i(1, 2), i(1)),
+    lambda i, f: sv.spec_kv_append(f(1, 2, 1, 8), f(1, 2, 1, 8), f(4, 4, 1, 8), f(4, 4, 1, 8), i(1, 2), i(1), q=f(1, 2, BIG, 8)),
+    lambda i, f: sv.spec_kv_append(f(1, 2, 1, 8), f(1, 2, 1, 8), f(4, 4, 1, 8), f(4, 4, 1, 8), i(1, 2), i(1),
+                                   turns=i(2 ** 31 + 4).to(torch.int64)),
+    lambda i, f: sv.spec_kv_commit(f(BIG, 4, 1, 8), f(BIG, 4, 1, 8), i(1, 2), i(1), i(1, 3), i(1, 3), i(1, 4), i(1)),
+    lambda i, f: sv.spec_kv_commit(f(4, 4, 1, 8), f(4, 4, 1, 8), i(1, BIG), i(1), i(1, 3), i(1, 3), i(1, 4), i(1)),
+    lambda i, f: sv.spec_kv_commit(f(4, 4, 1, 8), f(4, 4, 1, 8), i(1, 2), i(1), i(1, BIG), i(1, BIG), i(1, BIG + 1), i(1)),
+    lambda i, f: sv.spec_kv_commit(f(4, 4, 1, 8), f(4, 4, 1, 8), i(BIG, 2), i(BIG), i(BIG, 3), i(BIG, 3), i(BIG, 4), i(BIG)),
+    lambda i, f: sv.spec_verify(f(1, 2, BIG), None, i(1, 1), 0.0, 0),
+    lambda i, f: sv.spec_verify(f(BIG, 2, 8), f(BIG, 1, 8), i(BIG, 1), 1.0, 0),
+    lambda i, f: sv.spec_verify_early_exit(f(1, 2, BIG), f(1, 1, BIG), i(1, 1), 1.0, 0),
+    lambda i, f: sv.spec_verify_khint(f(1, 2, 8), f(1, 1, 8), i(1, 1), 1.0, 0, 0.5, 1.0, 2 ** 32, 4),
+    lambda i, f: sv.spec_verify_khint(f(1, 2, 8), f(1, 1, 8), i(1, 1), 1.0, 0, 0.5, 1.0, 1, 2 ** 32 + 4),
+    lambda i, f: sv.spec_verify_greedy_argmax(f(1, 2, BIG), i(1, 1)),
+    lambda i, f: sv.spec_tree_verify_greedy(f(1, 2, BIG), i(1, 1), i(1, 1)),
+    lambda i, f: sv.spec_tree_verify_sampling(f(1, 2, BIG), f(1, 2, BIG), i(1, 1), i(1, 1), 1.0, 0),
+    lambda i, f: sv.spec_acceptance_stats(i(BIG), 4),
+    lambda i, f: sv.spec_acceptance_stats(i(2), -2 ** 32 + 4),
+    lambda i, f: sv.spec_ngram_draft(i(2, BIG), i(2), 1, 4, 8),
+    lambda i, f: sv.spec_ngram_draft(i(BIG, 9), i(BIG), 1, 4, 8),
+    lambda i, f: sv.spec_ngram_draft(i(2, 9), i(2), 2 ** 32 + 1, 4, 8),
+    lambda i, f: sv.spec_ngram_draft(i(2, 9), i(2), 1, 2 ** 32 + 4, 8),
+    lambda i, f: sv.spec_ngram_draft(i(2, 9), i(2), 1, 4, -2 ** 32 + 8),
+])
+def test_binding_refuses_sizes_past_a_c_int(lib, call):
+    with pytest.raises(sv.SpecError) as e:
+        call(huge, lambda *s: huge(*s, dtype=torch.bfloat16))
+    assert e.value.code == _lib.SPEC_ERR_SHAPE
