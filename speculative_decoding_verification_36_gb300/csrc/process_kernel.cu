@@ -211,8 +211,9 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
     }
     return cudaSuccess;
   }
-  if (a.stride == 0) return cudaSuccess;
-  const int per_row = (int)((a.stride + kCountThreads - 1) / kCountThreads);
+  if (a.stride == 0 && !a.lengths && !a.prompt_lengths) return cudaSuccess;
+  // (rows without entries: one CTA each, to judge their lengths)
+  const int per_row = a.stride ? (int)((a.stride + kCountThreads - 1) / kCountThreads) : 1;
   const int x = per_row < 4 * sms ? per_row : 4 * sms;
   for (int b0 = 0; b0 < a.B; b0 += 65535) {  // the grid's y extent
     c.B = a.B - b0 < 65535 ? a.B - b0 : 65535;

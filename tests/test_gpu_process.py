@@ -666,3 +666,17 @@ def test_smallest_and_largest_repetitions(value, good, in_place):
     else:
         assert bool(torch.isnan(got[1]).all())
     assert sv.spec_get_status() == (0 if good else sv.SPEC_FLAG_BAD_DATA)
+
+
+@pytest.mark.parametrize("reset", [False, True])
+@pytest.mark.parametrize("lengths,prompts,bad", [([0, 3], None, True), ([0, -1], None, True), ([0, 0], [0, 0], False),
+                                                 ([0, 0], [0, 1], True), (None, [-1, 0], True), (None, None, False)])
+def test_lengths_of_rows_without_entries_are_judged(lengths, prompts, bad, reset):
+    V = 40
+    state = sv.spec_count_tokens(sv.spec_token_state(2, V, DEV), dev(np.arange(6, dtype=np.int32).reshape(2, 3)), V)
+    want = torch.zeros_like(state) if reset else state.clone()
+    i32 = lambda x: None if x is None else dev(np.array(x, np.int32))  # noqa: E731
+    none = torch.empty((2, 0), dtype=torch.int32, device=DEV)
+    sv.spec_count_tokens(state, none, V, lengths=i32(lengths), prompt_lengths=i32(prompts), reset=reset)
+    assert torch.equal(state, want)
+    assert sv.spec_get_status() == (sv.SPEC_FLAG_BAD_DATA if bad else 0)
