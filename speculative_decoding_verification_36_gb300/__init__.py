@@ -6,6 +6,10 @@ shapes), allocates outputs that were not given, and calls the C entry point of
 the same name on the current stream; every step of the verify path runs in the
 library's CUDA kernels.  There is no CPU fallback.
 
+stream= (a torch stream or a cudaStream_t as an int) runs a call on another
+stream: its inputs have to be ready there and to stay until it is done, and its
+outputs are complete there.  Outputs that it allocates are that stream's memory.
+
     spec_verify(target_logits, draft_logits, draft_tokens, temperature, seed)
     spec_verify_early_exit(...)       # reads only the rows the result depends on
     spec_verify_static_scratch(...)   # no allocation: a fixed per-device scratch buffer
@@ -50,6 +54,12 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+# the handle of a device's current stream without a Stream object around it
+# (0.1 us, where torch.cuda.current_stream().cuda_stream takes 2.8)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _is_bf16(t: torch.Tensor, name: str) -> bool:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -84,9 +94,25 @@ def _i32(t: torch.Tensor, shape, name: str, device=None):
     return t
 
 
-def _out(t, shape, dtype, device, name):
-    if t is None:
+def _new(shape, dtype, device, stream):
+    """An output of a call on `stream`.  On another stream than the current one
+    it is that stream's memory, which no pending work of the current stream still
+    uses and which does not go back to the current stream while the call runs;
+    the current stream is noted as a user."""
+    handle = None if stream is None else _stream(stream)
+    if handle is None or handle == _raw_stream(device.index):
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _out(t, shape, dtype, device, name, stream):
+    if t is None:
+        return _new(shape, dtype, device, stream)
     if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape) or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
@@ -125,8 +151,8 @@ def spec_verify(target_logits, draft_logits, draft_tokens, temperature: float, s
     """Verify K drafted tokens per sequence; returns (out_tokens [B,K+1], n [B])."""
     bf16, B, K, V = _chain_args(target_logits, draft_logits, draft_tokens, temperature)
     dev = target_logits.device
-    out_tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens")
-    out_n_accepted = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted")
+    out_tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens", stream)
+    out_n_accepted = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted", stream)
     lib = _lib.load()
     fn = lib.spec_verify_bf16 if bf16 else lib.spec_verify_f32
     with torch.cuda.device(dev):
@@ -146,8 +172,8 @@ def spec_verify_early_exit(target_logits, draft_logits, draft_tokens, temperatur
     Returns (out_tokens [B,K+1], n [B])."""
     bf16, B, K, V = _chain_args(target_logits, draft_logits, draft_tokens, temperature)
     dev = target_logits.device
-    out_tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens")
-    out_n_accepted = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted")
+    out_tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens", stream)
+    out_n_accepted = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted", stream)
     lib = _lib.load()
     fn = lib.spec_verify_early_exit_bf16 if bf16 else lib.spec_verify_early_exit_f32
     with torch.cuda.device(dev):
@@ -168,8 +194,8 @@ def spec_verify_static_scratch(target_logits, draft_logits, draft_tokens, temper
     if not bf16:
         raise TypeError("spec_verify_static_scratch takes bf16 logits")
     dev = target_logits.device
-    out_tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens")
-    out_n_accepted = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted")
+    out_tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens", stream)
+    out_n_accepted = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted", stream)
     lib = _lib.load()
     with torch.cuda.device(dev):
         _lib.check(lib.spec_verify_bf16_static_scratch(
@@ -190,12 +216,12 @@ def spec_verify_stats(target_logits, draft_logits, draft_tokens, temperature: fl
         raise ValueError("spec_verify_stats needs temperature > 0")
     bf16, B, K, V = _chain_args(target_logits, draft_logits, draft_tokens, temperature)
     dev = target_logits.device
-    tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
-    n = torch.empty((B,), dtype=torch.int32, device=dev)
-    row_stats = torch.empty((B, 2 * K + 1, 2), dtype=torch.float32, device=dev)
-    pq = torch.empty((B, K, 2), dtype=torch.float32, device=dev)
-    resid = torch.empty((B,), dtype=torch.float32, device=dev)
-    ent = torch.empty((B, 2 * K + 1), dtype=torch.float32, device=dev) if entropy else None
+    tokens = _new((B, K + 1), torch.int32, dev, stream)
+    n = _new((B,), torch.int32, dev, stream)
+    row_stats = _new((B, 2 * K + 1, 2), torch.float32, dev, stream)
+    pq = _new((B, K, 2), torch.float32, dev, stream)
+    resid = _new((B,), torch.float32, dev, stream)
+    ent = _new((B, 2 * K + 1), torch.float32, dev, stream) if entropy else None
     lib = _lib.load()
     fn = lib.spec_verify_stats_bf16 if bf16 else lib.spec_verify_stats_f32
     with torch.cuda.device(dev):
@@ -221,10 +247,10 @@ def spec_verify_khint(target_logits, draft_logits, draft_tokens, temperature: fl
     bf16, B, K, V = _chain_args(target_logits, draft_logits, draft_tokens, temperature)
     _c_ints(int(k_min), int(k_max))
     dev = target_logits.device
-    tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens")
-    n = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted")
-    k_next = _out(out_k_next, (B,), torch.int32, dev, "out_k_next")
-    hmean = _out(out_mean_entropy, (B,), torch.float32, dev, "out_mean_entropy")
+    tokens = _out(out_tokens, (B, K + 1), torch.int32, dev, "out_tokens", stream)
+    n = _out(out_n_accepted, (B,), torch.int32, dev, "out_n_accepted", stream)
+    k_next = _out(out_k_next, (B,), torch.int32, dev, "out_k_next", stream)
+    hmean = _out(out_mean_entropy, (B,), torch.float32, dev, "out_mean_entropy", stream)
     lib = _lib.load()
     fn = lib.spec_verify_khint_bf16 if bf16 else lib.spec_verify_khint_f32
     with torch.cuda.device(dev):
@@ -241,9 +267,9 @@ def spec_verify_greedy_argmax(target_logits, draft_tokens, stream=None):
     Returns (out_tokens [B,K+1], n [B], row_argmax [B,K+1])."""
     bf16, B, K, V = _chain_args(target_logits, None, draft_tokens, 0.0)
     dev = target_logits.device
-    tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
-    n = torch.empty((B,), dtype=torch.int32, device=dev)
-    amax = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
+    tokens = _new((B, K + 1), torch.int32, dev, stream)
+    n = _new((B,), torch.int32, dev, stream)
+    amax = _new((B, K + 1), torch.int32, dev, stream)
     lib = _lib.load()
     fn = lib.spec_verify_greedy_argmax_bf16 if bf16 else lib.spec_verify_greedy_argmax_f32
     with torch.cuda.device(dev):
@@ -271,10 +297,10 @@ def spec_tree_verify_greedy(target_logits, tree_tokens, parent_idx, out_path=Non
     if N > 0:
         _i32(tree_tokens, (B, N), "tree_tokens", dev)
         _i32(parent_idx, (B, N), "parent_idx", dev)
-    out_path = _out(out_path, (B, N + 1), torch.int32, dev, "out_path")
-    out_len = _out(out_len, (B,), torch.int32, dev, "out_len")
+    out_path = _out(out_path, (B, N + 1), torch.int32, dev, "out_path", stream)
+    out_len = _out(out_len, (B,), torch.int32, dev, "out_len", stream)
     # torch has no uint32 arithmetic on every version: the mask words travel as int32 bits
-    out_mask = _out(out_mask, (B, N, W), torch.int32, dev, "out_mask")
+    out_mask = _out(out_mask, (B, N, W), torch.int32, dev, "out_mask", stream)
     lib = _lib.load()
     if early_exit:
         fn = lib.spec_tree_verify_greedy_early_exit_bf16 if bf16 else lib.spec_tree_verify_greedy_early_exit_f32
@@ -312,8 +338,8 @@ def spec_tree_verify_sampling(target_logits, draft_logits, tree_tokens, parent_i
     if N > 0:
         _i32(tree_tokens, (B, N), "tree_tokens", dev)
         _i32(parent_idx, (B, N), "parent_idx", dev)
-    out_path = _out(out_path, (B, N + 1), torch.int32, dev, "out_path")
-    out_len = _out(out_len, (B,), torch.int32, dev, "out_len")
+    out_path = _out(out_path, (B, N + 1), torch.int32, dev, "out_path", stream)
+    out_len = _out(out_len, (B,), torch.int32, dev, "out_len", stream)
     lib = _lib.load()
     fn = lib.spec_tree_verify_sampling_bf16 if bf16 else lib.spec_tree_verify_sampling_f32
     with torch.cuda.device(dev):
@@ -334,9 +360,9 @@ def spec_acceptance_stats(n_accepted, K: int, stream=None):
     dev = n_accepted.device
     B = n_accepted.shape[0]
     _c_ints(B, int(K))
-    hist = torch.empty((K + 2,), dtype=torch.int64, device=dev)
-    alpha = torch.empty((max(K, 0),), dtype=torch.float64, device=dev)
-    mean = torch.empty((1,), dtype=torch.float64, device=dev)
+    hist = _new((K + 2,), torch.int64, dev, stream)
+    alpha = _new((max(K, 0),), torch.float64, dev, stream)
+    mean = _new((1,), torch.float64, dev, stream)
     lib = _lib.load()
     with torch.cuda.device(dev):
         _lib.check(lib.spec_acceptance_stats(_ptr(n_accepted) if B > 0 else None, B, int(K),
@@ -359,9 +385,9 @@ def spec_ngram_draft(tokens, lengths, n_min: int, n_max: int, K: int, out_drafts
     _i32(tokens, (B, Lmax), "tokens")
     dev = tokens.device
     _i32(lengths, (B,), "lengths", dev)
-    drafts = _out(out_drafts, (B, max(int(K), 0)), torch.int32, dev, "out_drafts")  # K < 0: the C layer refuses
-    n_drafts = _out(out_n_drafts, (B,), torch.int32, dev, "out_n_drafts")
-    match_len = _out(out_match_len, (B,), torch.int32, dev, "out_match_len")
+    drafts = _out(out_drafts, (B, max(int(K), 0)), torch.int32, dev, "out_drafts", stream)  # K < 0: the C layer refuses
+    n_drafts = _out(out_n_drafts, (B,), torch.int32, dev, "out_n_drafts", stream)
+    match_len = _out(out_match_len, (B,), torch.int32, dev, "out_match_len", stream)
     lib = _lib.load()
     with torch.cuda.device(dev):
         _lib.check(lib.spec_ngram_draft(_ptr(tokens), _ptr(lengths), B, Lmax, int(n_min), int(n_max), int(K),
@@ -385,12 +411,6 @@ def _arg(t, dtype, shape, device, name):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     _same_device(t, device, name)
     raise ValueError(f"{name} cannot be used")
-
-
-# the handle of a device's current stream without a Stream object around it
-# (0.1 us, where torch.cuda.current_stream().cuda_stream takes 2.8)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _invoke(fn, device, stream, *args):
@@ -481,7 +501,7 @@ def spec_process_logits(logits, draft_tokens=None, parent_idx=None, token_state=
         mask = _arg(allowed_mask, i32, (B, W) if allowed_mask.dim() == 2 else (B, R, W), dev, "allowed_mask")
     state = None if token_state is None else _arg(token_state, i32, (B, _words(V)), dev, "token_state")
     if out is None:
-        out = torch.empty_like(logits)
+        out = _new((B, R, V), logits.dtype, dev, stream)
     lib = _lib.load()
     _invoke(lib.spec_process_logits_bf16 if bf16 else lib.spec_process_logits_f32, dev, stream, _ptr(logits),
             _arg(draft_tokens, i32, (B, R - 1), dev, "draft_tokens"), _arg(parent_idx, i32, (B, R - 1), dev, "parent_idx"),
@@ -568,7 +588,7 @@ def spec_kv_append(k, v, key_cache, value_cache, page_table, lengths, turns=None
             _too_large()
         qs = _token_stride(q, "q", dt, (B, T, Hq, D), dev)
         if out_q is None:
-            out_q = torch.empty((B, T, Hq, D), dtype=dt, device=dev)
+            out_q = _new((B, T, Hq, D), dt, dev, stream)
         qp, oq = q.data_ptr(), _arg(out_q, dt, (B, T, Hq, D), dev, "out_q")
     elif out_q is not None:
         raise ValueError("out_q needs q")
@@ -608,9 +628,9 @@ def spec_kv_commit(key_cache, value_cache, page_table, lengths, tree_tokens, par
     if (layers | pages | page_size | entry | max_pages | B | N) >> 31:
         _too_large()
     if out_nodes is None:
-        out_nodes = torch.empty((B, N + 1), dtype=i32, device=dev)
+        out_nodes = _new((B, N + 1), i32, dev, stream)
     if out_lengths is None:
-        out_lengths = torch.empty((B,), dtype=i32, device=dev)
+        out_lengths = _new((B,), i32, dev, stream)
     _invoke(_lib.load().spec_kv_commit, dev, stream, _arg(key_cache, dt, shape, dev, "key_cache"),
             _arg(value_cache, dt, shape, dev, "value_cache"), layers, pages * page_size * entry, pages, page_size, entry,
             _arg(page_table, i32, (B, max_pages), dev, "page_table"), max_pages,
