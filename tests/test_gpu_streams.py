@@ -76,25 +76,31 @@ def test_an_output_lets_the_current_streams_work_finish():
     given to that other stream while the use is pending; and a call does not
     write over memory that the current stream still reads."""
     z = torch.randn((1, 4, 1 << 18), device=DEV)
+    minus, side = -z, torch.cuda.Stream()
+    sv.spec_process_logits(z, out=torch.empty_like(z).copy_(z))  # kernels are loaded
+    torch.cuda._sleep(1)
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
-    side = torch.cuda.Stream()
     out = sv.spec_process_logits(z, stream=side)
     side.synchronize()
-    at, kept = out.data_ptr(), torch.empty_like(out)
-    torch.cuda._sleep(int(1e8))  # some 50 ms
+    at, kept, read = out.data_ptr(), torch.empty_like(out), torch.cuda.Event()
+    torch.cuda._sleep(int(2e8))  # some 100 ms
     kept.copy_(out)
+    read.record()
     del out
     with torch.cuda.stream(side):
-        again = sv.spec_process_logits(-z)
+        again = sv.spec_process_logits(minus)
+    assert not read.query()  # the use is still pending
     assert again.data_ptr() != at
+    torch.cuda.synchronize()
     old, seen = torch.full_like(z, 3.0), torch.empty_like(z)
-    torch.cuda._sleep(int(1e8))
+    torch.cuda.synchronize()
+    torch.cuda._sleep(int(2e8))
     seen.copy_(old)
     del old
     new = sv.spec_process_logits(z, stream=side)
     torch.cuda.synchronize()
-    assert torch.equal(kept, z) and torch.equal(again, -z) and torch.equal(new, z) and bool((seen == 3).all())
+    assert torch.equal(kept, z) and torch.equal(again, minus) and torch.equal(new, z) and bool((seen == 3).all())
 
 
 def test_default_stream_by_its_handle():
