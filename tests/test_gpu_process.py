@@ -680,3 +680,94 @@ def test_lengths_of_rows_without_entries_are_judged(lengths, prompts, bad, reset
     sv.spec_count_tokens(state, none, V, lengths=i32(lengths), prompt_lengths=i32(prompts), reset=reset)
     assert torch.equal(state, want)
     assert sv.spec_get_status() == (sv.SPEC_FLAG_BAD_DATA if bad else 0)
+
+
+# Launches of more units (chunks of 4096 tokens x groups of rows x sequences) than
+# start at once, 456 on 152 SMs: CTAs go on to further units, with the ring, the
+# masks, the counts and the gatherings of the next one under way.
+def take_over(seed, B, R, V, dtype, tree, mask, bias, shift=(0, 0)):
+    rng = np.random.default_rng(seed)
+    x = make(rng, B, R, V, dtype, tree, 400, bias=bias, mask=mask)
+    for b in range(1, B, 3):  # many in the first chunks; no token over three times
+        x["bias_tokens"][b, 3:] = rng.permutation(np.setdiff1d(np.arange(min(V, 5000)), x["bias_tokens"][b, :3]))[:bias - 3]
+    x["rep"][B // 3] = np.nan  # a bad sequence between good ones
+    if tree:
+        x["parents"][B // 2, 0] = 0
+    n = B * R * V
+    src = torch.zeros(n + 16, dtype=dtype, device=DEV)
+    z = src[shift[0]:shift[0] + n].view(B, R, V)
+    z.copy_(x["logits"])
+    buf = torch.full((n + 16,), 77.0, dtype=dtype, device=DEV)
+    out = buf[shift[1]:shift[1] + n].view(B, R, V)
+    check(x, call(x, logits=z, out=out))
+    assert bool((buf[:shift[1]] == 77).all()) and bool((buf[shift[1] + n:] == 77).all())
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    got = out.clone()
+    out.fill_(5)
+    call(x, logits=z, out=out)
+    assert torch.equal(out.view(bits), got.view(bits))
+    assert sv.spec_get_status() == sv.SPEC_FLAG_BAD_DATA
+
+
+@pytest.mark.parametrize("B,R,V,dtype,tree,mask,bias", [
+    (24, 4, 96001, torch.bfloat16, None, "shared", 20),     # rows off 16 bytes, 576 units
+    (24, 5, 96003, torch.float32, None, "rows", 600),       # ... in fp32, a long bias list
+    (16, 31, 40001, torch.bfloat16, "tree", "rows", 30),    # three groups of rows: 480 units
+    (16, 14, 60000, torch.float32, "tree", None, 6),        # two groups: 480 units
+    (40, 1, 96000, torch.float32, None, "shared", 6),       # single rows, 960 units
+    (48, 3, 50003, torch.float32, None, "rows", 40),        # 624 units
+    (1000, 3, 4000, torch.bfloat16, None, "rows", 12),      # a chunk a sequence
+    (7, 2, 300000, torch.bfloat16, None, None, 6),          # 518 units of a few long rows
+    (36, 40, 5000, torch.bfloat16, "tree", "shared", 9),    # many groups, two chunks
+])
+def test_units_taken_over_match_plain(B, R, V, dtype, tree, mask, bias):
+    take_over(V + R, B, R, V, dtype, tree, mask, bias)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [(1, 1), (3, 2)])
+def test_units_taken_over_off_16_bytes(dtype, shift):
+    take_over(7, 31, 3, 65536, dtype, None, "rows", 20, shift)
+
+
+def test_waits_that_run_out_write_nothing_wrong():
+    """With a limit of one poll some wait of a launch that is bound by memory
+    runs out: the call says so, and whatever it has written is right."""
+    B, R, V = 64, 9, 128251  # 0.3 GB in and out, rows off 16-byte boundaries
+    o = wl.make_settings(B, R, V, hist=2000, n_bias=40, seed=9, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(10)
+    state = sv.spec_count_tokens(sv.spec_token_state(B, V, DEV), o["tokens"], V, o["lengths"], o["prompt_lengths"], reset=True)
+    d = torch.randint(0, V, (B, R - 1), generator=g, device=DEV, dtype=torch.int32)
+    ran_out = 0
+    for dtype, bits in ((torch.bfloat16, torch.int16), (torch.float32, torch.int32)):
+        z = (torch.randn((B, R, V), generator=g, device=DEV) * 4).to(dtype)
+        buf = torch.full((B * R * V + 128,), 77.0, dtype=dtype, device=DEV)  # no logit is 77
+        out = buf[64:-64].view(B, R, V)
+
+        def one(out):
+            return sv.spec_process_logits(z, d, None, state, o["repetition"], o["frequency"], o["presence"], o["bias_tokens"],
+                                          o["bias_values"], o["allowed_mask"], out=out)
+
+        right = one(torch.empty_like(z))
+        assert sv.spec_get_status() == 0 and not bool((right == 77).any())
+        for _ in range(4):
+            buf.fill_(77.0)
+            torch.cuda.synchronize()
+            sv.spec_test_spin_limit(1)
+            try:
+                one(out)
+                torch.cuda.synchronize()
+            finally:
+                sv.spec_test_spin_limit(0)
+            status = sv.spec_get_status()
+            assert status in (0, sv.SPEC_FLAG_TIMEOUT)
+            same = out.view(bits) == right.view(bits)
+            assert bool((same | (out == 77)).all())
+            if status:
+                ran_out += 1
+            else:
+                assert bool(same.all())
+            assert bool((buf[:64] == 77).all()) and bool((buf[-64:] == 77).all())
+        one(out)
+        assert torch.equal(out.view(bits), right.view(bits)) and sv.spec_get_status() == 0
+    assert ran_out > 0
