@@ -604,7 +604,8 @@ int spec_test_fail_allocations(int n);
 /*
  * Test hook, for failure-detection tests: every bounded wait inside the
  * kernels of later calls on the current device gives up after `iterations`
- * polls (0 restores the default, about half a second).  A wait that gives up
+ * polls, where one that suspends the thread counts as 32 (0 restores the
+ * default, about half a second).  A wait that gives up
  * sets SPEC_FLAG_TIMEOUT, the kernel returns without faulting, and that call's
  * outputs are invalid; the device stays usable.  Synchronises the device
  * first.  Returns SPEC_OK or SPEC_ERR_CUDA.  The pages have no counterpart; it

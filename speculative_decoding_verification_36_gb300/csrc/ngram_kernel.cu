@@ -102,7 +102,7 @@ __device__ __forceinline__ NgramStage ngram_stage_of(const NgramArgs& a, int g, 
 // The producer's drain waits this long for its own copies whatever limit the
 // other waits have, so that no CTA leaves with a copy into its shared memory
 // still in flight.
-constexpr unsigned kNgramDrainLimit = kSpinLimit;
+constexpr unsigned kNgramDrainTries = mbar_tries(kSpinLimit);
 
 // One consumer warp's best key (m << 16) | r over its ends of the chunk in
 // `k` (0: none).  kVec: the tokens come from the stage (tok[x] = h[c0 + x]
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kNgramThreads) ngram_scan_kernel(const __grid_
       const int s = i % kNgramStages;
       if (i >= kNgramStages) {
         // the consumers have released the stage's previous round
-        ok = warp_wait(&s_empty[s], ((i / kNgramStages) & 1) ^ 1, spin_limit());
+        ok = warp_wait(&s_empty[s], ((i / kNgramStages) & 1) ^ 1, mbar_tries(spin_limit()));
         if (!ok) break;
         if (lane == 0) collect(s);
       }
@@ -253,13 +253,13 @@ __global__ void __launch_bounds__(kNgramThreads) ngram_scan_kernel(const __grid_
     // consumers release it.
     for (int r = i > kNgramStages ? i - kNgramStages : 0; r < i; ++r) {
       const int s = r % kNgramStages;
-      if (!warp_wait(&s_full[s], (r / kNgramStages) & 1, kNgramDrainLimit)) {
+      if (!warp_wait(&s_full[s], (r / kNgramStages) & 1, kNgramDrainTries)) {
         if (lane == 0) atomicOr(a.status, kStatusTimeout);
         continue;
       }
       // the closing round: no consumer releases it
       if (__shfl_sync(0xffffffffu, lane == 0 ? (int)(s_meta[s].g < 0) : 0, 0)) continue;
-      if (!warp_wait(&s_empty[s], (r / kNgramStages) & 1, spin_limit())) {
+      if (!warp_wait(&s_empty[s], (r / kNgramStages) & 1, mbar_tries(spin_limit()))) {
         if (lane == 0) atomicOr(a.status, kStatusTimeout);
         continue;
       }
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kNgramThreads) ngram_scan_kernel(const __grid_
   // ---------------- consumer warps ----------------
   for (int i = 0;; ++i) {
     const int s = i % kNgramStages;
-    if (!warp_wait(&s_full[s], (i / kNgramStages) & 1, spin_limit())) {
+    if (!warp_wait(&s_full[s], (i / kNgramStages) & 1, mbar_tries(spin_limit()))) {
       if (lane == 0) atomicOr(a.status, kStatusTimeout);
       break;
     }

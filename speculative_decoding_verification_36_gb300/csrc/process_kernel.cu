@@ -789,7 +789,8 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
   ProcShare c;
   c.paths = (ProcPaths*)(s_raw + sizeof(ProcCopyShared<T>));
   const unsigned short* list = sh.list + warp * kProcPiece;
-  const unsigned limit = spin_limit();
+  const unsigned tries = mbar_tries(spin_limit());
+  constexpr unsigned kMostTries = mbar_tries(kSpinLimit);
   bool dead = false;
   int g = 0;
   for (unsigned round = 0;; ++round) {
@@ -797,14 +798,14 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
       // the unit after this one, asked for a round ago; and the one after that
       const unsigned k = round & 1;
       int answer = -1;
-      bool came = false;
+      bool came = mbar_test(&sh.claimed[k], (round >> 1) & 1);
 #pragma unroll 1
-      for (unsigned it = 0; !came && it <= limit; ++it) came = mbar_try(&sh.claimed[k], (round >> 1) & 1);
+      for (unsigned it = 0; !came && it < tries; ++it) came = mbar_try(&sh.claimed[k], (round >> 1) & 1);
       if (!came) {
         // out of time; but the answer has to have come before the CTA leaves
         atomicOr(a.status, kStatusTimeout);
 #pragma unroll 1
-        for (unsigned it = 0; !came && it <= kSpinLimit; ++it) came = mbar_try(&sh.claimed[k], (round >> 1) & 1);
+        for (unsigned it = 0; !came && it < kMostTries; ++it) came = mbar_try(&sh.claimed[k], (round >> 1) & 1);
       }
       if (came) answer = cta_answer(&sh.claim[k]);
       sh.unit[k] = answer;
@@ -827,12 +828,12 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
         look(u, i0 / RB + 1);
       else if (next >= 0)
         look(proc_unit(a, (unsigned)next), 0);
-      if (!dead && !warp_wait(&sh.full[warp][g % NB], (g / NB) & 1, limit)) {
+      if (!dead && !warp_wait(&sh.full[warp][g % NB], (g / NB) & 1, tries)) {
         // a copy that never came: this warp hands out nothing more, and waits
         // for what is in flight, so that no copy outlives the CTA's memory
         if (lane == 0) atomicOr(a.status, kStatusTimeout);
 #pragma unroll 1
-        for (int q = g; q < load_g; ++q) warp_wait(&sh.full[warp][q % NB], (q / NB) & 1, kSpinLimit);
+        for (int q = g; q < load_g; ++q) warp_wait(&sh.full[warp][q % NB], (q / NB) & 1, kMostTries);
         dead = true;
       }
       if (dead) continue;

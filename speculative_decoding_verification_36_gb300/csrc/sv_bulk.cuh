@@ -22,10 +22,23 @@ __device__ __forceinline__ void mbar_arrive_tx(unsigned long long* bar, unsigned
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
                : "memory");
 }
-// Has the phase with this parity completed?  The thread may be suspended up
-// to about kSuspendNs while the phase is still open (no instructions
-// issue meanwhile).  Acquire: the completing arrivals and copies are visible
-// afterwards.
+// Has the phase with this parity completed?  Acquire: the completing arrivals
+// and copies are visible afterwards.
+__device__ __forceinline__ bool mbar_test(unsigned long long* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The same, but the thread is suspended while the phase is still open, until it
+// completes or for about 4 us (no instructions issue meanwhile; a GB300 takes
+// 3.9 to 4.0 us before it gives up on a phase that stays open, although the
+// hint says 128 ns).
 constexpr unsigned kSuspendNs = 128;
 __device__ __forceinline__ bool mbar_try(unsigned long long* bar, unsigned parity) {
   unsigned ok;
@@ -38,6 +51,9 @@ __device__ __forceinline__ bool mbar_try(unsigned long long* bar, unsigned parit
       : "memory");
   return ok != 0;
 }
+// Tries that last as long as `polls` polls of the other waits, which nap for
+// 128 ns each (4 us = 32 of them): the limit on polls bounds the time of both.
+__host__ __device__ constexpr unsigned mbar_tries(unsigned polls) { return polls / 32u; }
 // One bulk copy global -> shared, completing `bytes` on the mbarrier.  Both
 // addresses and the size are multiples of 16 bytes.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes, unsigned long long* bar) {
@@ -47,12 +63,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned b
       "l"(src), "r"(bytes), "r"(smem_addr(bar))
       : "memory");
 }
-// Warp-uniform bounded wait: every lane tries, and the warp leaves together
-// once all lanes have seen the phase; false after `limit` further tries
-// (each suspends for at most about kSuspendNs).
-__device__ __forceinline__ bool warp_wait(unsigned long long* bar, unsigned parity, unsigned limit) {
-  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-  for (unsigned it = 0; it < limit; ++it)
+// Warp-uniform bounded wait: every lane looks, and the warp leaves together
+// once all lanes have seen the phase; false after a look and `tries` tries
+// (each suspends for at most about 4 us).
+__device__ __forceinline__ bool warp_wait(unsigned long long* bar, unsigned parity, unsigned tries) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  for (unsigned it = 0; it < tries; ++it)
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
   return false;
 }

@@ -263,6 +263,34 @@ def test_ngram_lowered_wait_limit_returns_and_flags_only_timeouts():
     np.testing.assert_array_equal(drafts.cpu().numpy(), ref["drafts"])
 
 
+def test_ngram_waits_that_run_out_are_flagged():
+    """With a limit of one poll a consumer looks once at a stage whose copy has
+    just set out: waits run out, the call says so and returns, and every draft
+    is the right one or a shorter match of its own history."""
+    h = wl.make_ngram_histories(64, 40000, V=50, seed=13, copy_prob=0.6)
+    tok, ln = h["tokens"].to(DEV), h["lengths"].to(DEV)
+    right = sv.spec_ngram_draft(tok, ln, 1, 6, 9)
+    torch.cuda.synchronize()
+    assert sv.spec_get_status() == 0
+    ran_out = 0
+    try:
+        sv.spec_test_spin_limit(1)
+        for _ in range(4):
+            d, n, m = sv.spec_ngram_draft(tok, ln, 1, 6, 9)
+            torch.cuda.synchronize()
+            status = sv.spec_get_status()
+            assert status in (0, sv.SPEC_FLAG_TIMEOUT)
+            ran_out += status != 0
+            assert bool((m <= right[2]).all()) and bool((m >= 0).all()) and bool((n >= 0).all()) and bool((n <= 9).all())
+            if status == 0:
+                assert all(torch.equal(a, b) for a, b in zip((d, n, m), right))
+    finally:
+        sv.spec_test_spin_limit(0)
+    assert ran_out > 0
+    assert all(torch.equal(a, b) for a, b in zip(sv.spec_ngram_draft(tok, ln, 1, 6, 9), right))
+    assert sv.spec_get_status() == 0
+
+
 def test_two_full_capacity_launches_side_by_side():
     """Two full-size c3 verifies (B=256, grids sized to the whole device) on
     two streams at once: each launch starts with only part of its grid
