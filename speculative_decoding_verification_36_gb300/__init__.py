@@ -566,7 +566,9 @@ def spec_kv_append(k, v, key_cache, value_cache, page_table, lengths, turns=None
     B, T, Hkv, D = shape
     ks = _token_stride(k, "k", dt, shape, dev)
     if _token_stride(v, "v", dt, shape, dev) != ks:
-        raise ValueError("k and v must share a token stride")
+        if B != 1 or T != 1:  # (one token has none)
+            raise ValueError("k and v must share a token stride")
+        ks = Hkv * D
     if not isinstance(key_cache, torch.Tensor) or key_cache.dim() != 4:
         raise ValueError("key_cache must be [pages, page_size, Hkv, D]")
     pages, page_size = key_cache.shape[:2]

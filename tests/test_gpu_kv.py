@@ -448,3 +448,33 @@ def test_keys_and_values_at_their_own_slots(dtype, interleaved):
     x["k"], x["v"] = (x[c].view(1, -1, H, D)[:, length:length + T] for c in ("kc", "vc"))
     run_and_check(x, interleaved)
     assert sv.spec_get_status() == 0
+
+
+def test_one_token_from_two_projections():
+    rng = np.random.default_rng(12)
+    x = make(rng, 1, 1, 4, 2, 64, 64, torch.bfloat16, 16, 30)
+    x["v"] = x["v"].contiguous()
+    assert x["v"].stride() != x["k"].stride()
+    run_and_check(x)
+    x = make(rng, 1, 1, 4, 2, 64, 64, torch.bfloat16, 16, 30)
+    x["k"] = x["k"].contiguous()
+    run_and_check(x, interleaved=True)
+    # and a joint projection's queries turned where they lie: one token
+    x = make(rng, 1, 1, 4, 2, 64, 64, torch.float32, 16, 30)
+    want = sv.spec_kv_append(x["k"], x["v"], x["kc"].clone(), x["vc"].clone(), dev(x["table"]), dev(x["lengths"]),
+                             turns=sv.spec_rope_turns(x["inv"], DEV), q=x["q"])
+    got = sv.spec_kv_append(x["k"], x["v"], x["kc"], x["vc"], dev(x["table"]), dev(x["lengths"]),
+                            turns=sv.spec_rope_turns(x["inv"], DEV), q=x["q"], out_q=x["q"])
+    assert got is x["q"] and torch.equal(got, want)
+    assert sv.spec_get_status() == 0
+
+
+def test_queries_of_a_joint_projection_in_place_are_refused():
+    rng = np.random.default_rng(13)
+    x = make(rng, 1, 4, 2, 1, 64, 64, torch.float32, 16, 30, joint=False)
+    whole = torch.zeros((1, 16, 2, 64), device=DEV)
+    q = whole[:, ::4]  # four tokens of every fourth row
+    with pytest.raises(sv.SpecError) as e:  # its answer, next to each other, would lie over later tokens' queries
+        sv.spec_kv_append(x["k"], x["v"], x["kc"], x["vc"], dev(x["table"]), dev(x["lengths"]),
+                          turns=sv.spec_rope_turns(x["inv"], DEV), q=q, out_q=whole[:, :4])
+    assert e.value.code == sv._lib.SPEC_ERR_OVERLAP

@@ -378,3 +378,24 @@ def test_binding_refuses_sizes_past_a_c_int(lib, call):
     with pytest.raises(sv.SpecError) as e:
         call(huge, lambda *s: huge(*s, dtype=torch.bfloat16))
     assert e.value.code == _lib.SPEC_ERR_SHAPE
+
+
+def test_one_token_has_no_stride(lib, monkeypatch):
+    """Keys from a joint projection and values of their own: with one token
+    there is no distance between tokens that they could differ in."""
+    calls = []
+    monkeypatch.setattr(sv, "_invoke", lambda fn, device, stream, *args: calls.append(args))
+    i, f = huge, lambda *s: huge(*s, dtype=torch.bfloat16)
+
+    def call(B, T, k, v):
+        sv.spec_kv_append(k, v, f(4, 4, 2, 8), f(4, 4, 2, 8), i(B, 2), i(B))
+        return calls.pop()[2]
+
+    joint, own = f(1, 1, 6, 8), f(1, 1, 2, 8)
+    assert joint[:, :, :2].stride() != own.stride()
+    for k, v in ((joint[:, :, :2], own), (own, joint[:, :, 4:]), (joint[:, :, :2], joint[:, :, 2:4]), (own, own)):
+        assert call(1, 1, k, v) >= 16  # the C entry point wants room for a token
+    assert call(2, 1, f(2, 1, 6, 8)[:, :, :2], f(2, 1, 6, 8)[:, :, 2:4]) == 48
+    for B, T in ((2, 1), (1, 2)):
+        with pytest.raises(ValueError, match="share a token stride"):
+            call(B, T, f(B, T, 6, 8)[:, :, :2], f(B, T, 2, 8))
