@@ -453,11 +453,11 @@ def test_keys_and_values_at_their_own_slots(dtype, interleaved):
 def test_one_token_from_two_projections():
     rng = np.random.default_rng(12)
     x = make(rng, 1, 1, 4, 2, 64, 64, torch.bfloat16, 16, 30)
-    x["v"] = x["v"].contiguous()
+    x["v"] = x["v"].clone(memory_format=torch.contiguous_format)
     assert x["v"].stride() != x["k"].stride()
     run_and_check(x)
     x = make(rng, 1, 1, 4, 2, 64, 64, torch.bfloat16, 16, 30)
-    x["k"] = x["k"].contiguous()
+    x["k"] = x["k"].clone(memory_format=torch.contiguous_format)
     run_and_check(x, interleaved=True)
     # and a joint projection's queries turned where they lie: one token
     x = make(rng, 1, 1, 4, 2, 64, 64, torch.float32, 16, 30)

@@ -771,3 +771,29 @@ def test_waits_that_run_out_write_nothing_wrong():
         one(out)
         assert torch.equal(out.view(bits), right.view(bits)) and sv.spec_get_status() == 0
     assert ran_out > 0
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rows_past_32_bit_offsets(in_place):
+    """Over 2^32 logits: the last sequences against the same call on them alone."""
+    B, R, V, last = 3200, 9, 152063, 3  # rows off 16-byte boundaries
+    assert B * R * V > 2 ** 32
+    o = wl.make_settings(B, R, V, hist=64, n_bias=8, mask=False, seed=11, device=DEV)
+    mask = torch.full((B, (V + 31) // 32), -2, dtype=torch.int32, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(12)
+    z = torch.empty((B, R, V), dtype=torch.bfloat16, device=DEV)
+    z[:-last] = 1.0
+    z[-last:] = (torch.randn((last, R, V), generator=g, device=DEV) * 4).to(torch.bfloat16)
+    d = torch.randint(0, V, (B, R - 1), generator=g, device=DEV, dtype=torch.int32)
+    state = sv.spec_count_tokens(sv.spec_token_state(B, V, DEV), o["tokens"], V, o["lengths"], o["prompt_lengths"], reset=True)
+
+    def call(s, z, out):
+        return sv.spec_process_logits(z, d[s], None, state[s], o["repetition"][s], o["frequency"][s], o["presence"][s],
+                                      o["bias_tokens"][s], o["bias_values"][s], mask[s], out=out)
+
+    tail = slice(B - last, B)
+    want = call(tail, z[tail].clone(), None)
+    got = call(slice(0, B), z, z if in_place else None)
+    assert torch.equal(got[tail].view(torch.int16), want.view(torch.int16))
+    assert bool((got[:, :, ::32] == float("-inf"))[::101].all())
+    assert sv.spec_get_status() == 0
