@@ -469,9 +469,12 @@ int spec_count_tokens(const int32_t *tokens, const int32_t *lengths, const int32
  *   allowed_mask  [B, mask_rows, ceil(V/32)] uint32 or NULL: bit v % 32 of word
  *                 v / 32 set = token v allowed.  mask_rows is R, or 1 for one
  *                 mask per sequence.  Bits at V and above are not read as tokens.
- *   out_logits    [B, R, V]: `logits` itself (in place: only what changes is
- *                 read and written), or memory apart from it; apart from
- *                 every other input (SPEC_ERR_OVERLAP).
+ *   out_logits    [B, R, V]: `logits` itself (in place: only tokens with a
+ *                 penalty or a bias, and the 16 bytes around a token that is not
+ *                 allowed, are read and written, others among them as they
+ *                 were; slower than a copy where much of a row is touched and
+ *                 masked), or memory apart from it; apart from every other
+ *                 input (SPEC_ERR_OVERLAP).
  * With c the occurrences of v among the output tokens and the drafts above the
  * row, and seen = (v in the prompt or c > 0):
  *   z1 = seen ? (z > 0 ? z / repetition : z * repetition) : z
@@ -576,8 +579,9 @@ int spec_kv_append_bf16(const uint16_t *k, const uint16_t *v, int64_t kv_stride,
  * A sequence with out_len -1 (bad data of the verify) is left as it is:
  * out_nodes -1, out_lengths = lengths.  So is one whose own data are bad
  * (SPEC_FLAG_BAD_DATA): an out_len outside [1, N + 1], tokens that no path of
- * the tree carries, a parent outside [-1, i), slots past the page table or a
- * page outside [0, pages).
+ * the tree carries, a parent outside [-1, i), a page table without room for
+ * all N + 1 entries of the step (whichever of them were appended and kept) or
+ * a page of the path outside [0, pages).
  * The two caches (whose layers may lie by turns), out_nodes and out_lengths
  * share no memory with each other or with an input (SPEC_ERR_OVERLAP).
  * 0 <= N <= 1024, 1 <= layers <= 32767, entry_bytes <= 2^30.  Returns SPEC_OK, SPEC_ERR_NULL,

@@ -477,7 +477,9 @@ def spec_process_logits(logits, draft_tokens=None, parent_idx=None, token_state=
     bias_tokens int32 / bias_values float32 [B, n]; tokens outside [0, V) are
     padding.  allowed_mask int32 [B, R, ceil(V/32)], or [B, ceil(V/32)] for
     all rows: a set bit allows the token.  out=logits works in place and
-    touches only what changes; out=None allocates.  Returns out."""
+    touches only what changes and the 16 bytes around a token that is not
+    allowed (slower than a copy where that is much of a row); out=None
+    allocates.  Returns out."""
     bf16 = _is_bf16(logits, "logits")
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")

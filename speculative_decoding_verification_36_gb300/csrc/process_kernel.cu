@@ -241,7 +241,7 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
 // Apart from its input (process_kernel): a warp's parts of kBatch rows at a time
 // come to shared memory by bulk copies, with further batches behind them; the
 // list is applied to them there, and they go out through registers, masked.
-// The bound is one reading and one writing of the logits: 242 us for B = 256,
+// The bound is one reading and one writing of the logits: 241 us for B = 256,
 // R = 9, V = 152064 in bf16 with histories of up to 8192 tokens, 300 biases and
 // a mask for every row (1.46 GB, 6.0 TB/s; without any of them 207 us, as fast
 // as a plain copy).  What else was measured on that workload: the terms worked
@@ -253,7 +253,12 @@ cudaError_t launch_count(const CountArgs& a, int sms, cudaStream_t s) {
 //
 // In place (process_mask_kernel, process_in_place_kernel): only the vectors that
 // hold a forbidden token and the listed tokens are read and written, where they
-// lie.
+// lie.  That is the caller's choice, by out == in, and gains where little is
+// touched.  B = 256, R = 9, V = 152064 in bf16, us in place and apart: histories
+// of up to 512 tokens 92 and 211, of up to 8192 tokens 178 and 223; with a mask
+// for every row beside them, which makes a second pass over the same rows, 253
+// and 221 (512 tokens), 300 and 241 (8192 tokens and 300 biases).  Masks alone,
+// R = 5, V = 128256: 61 and 107.
 constexpr int kProcThreads = 256;
 constexpr int kProcWarps = kProcThreads / 32;
 constexpr int kProcPiece = 512;                        // tokens of a warp
@@ -370,7 +375,7 @@ struct ProcUnit {
 // first chunks, where a tokenizer puts what is frequent and the lists are long,
 // are dealt out evenly over the first half, so that none of them is still under
 // way when the others end.  (B = 256, R = 9, V = 152064, everything on: 266 us
-// without this, 242 with it.)
+// without this, 241 with it.)
 __device__ __forceinline__ ProcUnit proc_unit(const ProcessArgs& a, unsigned unit) {
   ProcUnit u;
   int pair = 0, chunk = 0, x = (int)unit;
@@ -950,7 +955,8 @@ __global__ void __launch_bounds__(kProcThreads, 3) process_kernel(const __grid_c
 // In place, the forbidden tokens: a warp takes 1024 tokens of one row, a lane
 // their mask word; a vector that holds a forbidden token is read (unless all
 // of it is forbidden) and written, no other is touched.  The bound is the
-// traffic of the sectors that hold one: 61 us for B = 256, R = 5, V = 128256
+// traffic of the sectors that hold one (the other tokens of a vector are written
+// as they were): 61 us for B = 256, R = 5, V = 128256
 // in bf16 where a quarter of the rows is free and the others allow 0.2, 10 or
 // 95 % (about 0.35 GB by that count; 104 us as a part of process_kernel).
 constexpr int kMaskThreads = 128;
@@ -1002,7 +1008,8 @@ __global__ void __launch_bounds__(kMaskThreads) process_mask_kernel(const __grid
 // left alone).  A lane has an entry, for kProcRows rows at a time.  Each token
 // costs the reading and writing of a sector, whatever else is in it: 178 us
 // for B = 256, R = 9, V = 152064 in bf16 and histories of up to 8192 tokens
-// (3 % of the tokens in 37 % of the sectors), 92 us with up to 512 tokens.
+// (3 % of the tokens in 37 % of the sectors, 76 us by their bytes), 92 us with
+// up to 512 tokens.
 template <class T>
 __global__ void __launch_bounds__(kProcThreads, 5) process_in_place_kernel(const __grid_constant__ ProcessArgs a) {
   using Ty = ProcType<T>;
