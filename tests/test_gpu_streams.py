@@ -111,3 +111,26 @@ def test_default_stream_by_its_handle():
         out = sv.spec_process_logits(z, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(out, z)
+
+
+def test_outputs_of_a_forked_stream_in_a_graph():
+    """A captured step whose call runs on a stream that was forked from the
+    capturing one: the output is the graph's memory, and a replay fills it."""
+    z, side, cap = torch.randn((2, 3, 5000), device=DEV), torch.cuda.Stream(), torch.cuda.Stream()
+    sv.spec_process_logits(z)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=cap):
+        side.wait_stream(cap)
+        out = sv.spec_process_logits(z, stream=side)
+        cap.wait_stream(side)
+        twice = out * 2
+        del out
+        again = sv.spec_process_logits(twice)
+    for _ in range(3):
+        z.normal_()
+        again.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, z * 2)
+    assert sv.spec_get_status() == 0
