@@ -1128,7 +1128,7 @@ const char* spec_status_string(int code) {
     case SPEC_ERR_HINT:
       return "bad draft-length parameters: need 0 <= k_min <= k_max <= 255 and h_lo <= h_hi (no NaN)";
     case SPEC_ERR_OVERLAP:
-      return "an output shares memory with an input that it may not share memory with";
+      return "memory that the call writes overlaps an input or another output";
     case SPEC_ERR_SCRATCH:
       return "the problem needs more scratch than the static buffer holds "
              "(SPEC_STATIC_SCRATCH_BYTES)";
