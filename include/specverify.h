@@ -595,6 +595,131 @@ int spec_kv_commit(void *key_cache, void *value_cache, int layers, int64_t layer
                    int32_t *out_lengths, cudaStream_t stream);
 
 /*
+ * The paged cache in 8 bits.  A sequence's committed tokens move, whole blocks at
+ * a time, from the plain cache (spec_kv_append_*, spec_kv_commit) into codes; the
+ * tokens behind the last whole block and a step's drafts stay plain.  A block is
+ * written once, from entries that no longer change, so a code is never rounded
+ * twice and never depends on a rejected draft.  The pages of plain entries whose
+ * tokens are codes may be given to later tokens.
+ *
+ *   format        SPEC_KV_INT8 (codes -127 .. 127) or SPEC_KV_E4M3 (fp8 of 4
+ *                 exponent and 3 mantissa bits, at most 448, no infinities).
+ *   key_codes, value_codes    layer l at element l * code_stride: [code_pages,
+ *                 block, Hkv, D] of one byte; a page is a block.
+ *   key_scales, value_scales  layer l at element l * scale_stride:
+ *                 [code_pages, Hkv] float32; an entry is code * scale.
+ *   code_table    [B, max_code_pages] int32: block i of sequence b lies in page
+ *                 code_table[b, i].
+ *   key_cache, value_cache    layer l at element l * layer_stride: [pages,
+ *                 page_size, Hkv, D], with page_table [B, max_pages].
+ * Strides are read when layers > 1.
+ * D is a multiple of 16 up to 256, Hkv * D up to 2^24, 1 <= block <= 65536,
+ * pages * page_size and code_pages * block below 2^31, max_code_pages <= 2^23 and
+ * max_code_pages * block <= 2^26, 1 <= layers <= 32767; the pools of entries and
+ * codes (and every layer of them) start on 16-byte boundaries.
+ *
+ * spec_kv_quantize_* makes codes of the whole blocks among the tokens [stored[b],
+ * lengths[b]) of every sequence, in all layers.  With top the largest magnitude of
+ * a block's values in one head and m = 127 or 448: scale = top * (1 / m) and code =
+ * round(x * (m / top)), in fp32, to the nearest and ties to even.  top below
+ * 2^-100: scale and codes are 0.  A value that is not finite: the scale is NaN and
+ * the codes are 0.
+ *   stored        [B] int32: tokens that are codes already, a multiple of block.
+ *   lengths       [B] int32: committed tokens.
+ *   out_stored    [B] int32: tokens that are codes afterwards.
+ * Bad data (SPEC_FLAG_BAD_DATA, out_stored = stored): stored negative, above
+ * lengths or no multiple of block, lengths above max_pages * page_size, more blocks
+ * than max_code_pages, or a page outside its pool (a block that such a page is
+ * not of may have been written to its place all the same).  Sequences that share
+ * a code page which a call writes are the caller's mistake.
+ *
+ * spec_kv_dequantize_* writes the entries [starts[b], ends[b]) of every sequence,
+ * code * scale rounded once, to their slots of the plain cache, in all layers: to
+ * go on from the middle of a block, or to hand a sequence on.
+ * Bad data: starts negative or above ends, ends above either table (nothing of that
+ * sequence is written), or a page outside its pool (its tokens are not written).
+ *
+ * What a call writes shares no memory with what it reads or with another output
+ * (SPEC_ERR_OVERLAP).  Returns SPEC_OK, SPEC_ERR_NULL, SPEC_ERR_SHAPE,
+ * SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  One launch on `stream`; no scratch.
+ */
+#define SPEC_KV_INT8 0
+#define SPEC_KV_E4M3 1
+int spec_kv_quantize_f32(const float *key_cache, const float *value_cache, int layers, int64_t layer_stride, int pages,
+                    int page_size, const int32_t *page_table, int max_pages, const int32_t *stored,
+                    const int32_t *lengths, int B, int Hkv, int D, int format, void *key_codes, void *value_codes,
+                    int64_t code_stride, float *key_scales, float *value_scales, int64_t scale_stride,
+                    int code_pages, int block, const int32_t *code_table, int max_code_pages, int32_t *out_stored,
+                    cudaStream_t stream);
+int spec_kv_quantize_bf16(const uint16_t *key_cache, const uint16_t *value_cache, int layers, int64_t layer_stride, int pages,
+                    int page_size, const int32_t *page_table, int max_pages, const int32_t *stored,
+                    const int32_t *lengths, int B, int Hkv, int D, int format, void *key_codes, void *value_codes,
+                    int64_t code_stride, float *key_scales, float *value_scales, int64_t scale_stride,
+                    int code_pages, int block, const int32_t *code_table, int max_code_pages, int32_t *out_stored,
+                    cudaStream_t stream);
+int spec_kv_dequantize_f32(const void *key_codes, const void *value_codes, int layers, int64_t code_stride,
+                    const float *key_scales, const float *value_scales, int64_t scale_stride, int code_pages,
+                    int block, const int32_t *code_table, int max_code_pages, const int32_t *starts,
+                    const int32_t *ends, int B, int Hkv, int D, int format, float *key_cache, float *value_cache,
+                    int64_t layer_stride, int pages, int page_size, const int32_t *page_table, int max_pages,
+                    cudaStream_t stream);
+int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int layers, int64_t code_stride,
+                    const float *key_scales, const float *value_scales, int64_t scale_stride, int code_pages,
+                    int block, const int32_t *code_table, int max_code_pages, const int32_t *starts,
+                    const int32_t *ends, int B, int Hkv, int D, int format, uint16_t *key_cache, uint16_t *value_cache,
+                    int64_t layer_stride, int pages, int page_size, const int32_t *page_table, int max_pages,
+                    cudaStream_t stream);
+
+/*
+ * Attention of a step's tokens to that cache:
+ *   out = softmax(scale * q K^T) V
+ * over the keys and values that a token sees, those in slots below stored[b] as
+ * code * scale and the others from the plain cache.
+ *
+ *   q, out        token t = b T + i of q at element t * q_stride, its Hq x D values
+ *                 contiguous, turned to its position (spec_kv_append_*); out is [B,
+ *                 T, Hq, D] on a 16-byte boundary.  Query head h reads head
+ *                 h / (Hq / Hkv) of the cache.
+ *   lengths       [B] int32: entries of the sequence before the step, as given to
+ *                 spec_kv_append_*, which has put the step's own behind them.
+ *   n_new         [B] int32 or NULL (T): tokens i >= n_new[b] are padding; their
+ *                 rows of out are left as they were.
+ *   parent_idx    [B, T-1] int32 or NULL.  NULL: token i sees the slots up to
+ *                 lengths[b] + i.  Otherwise a tree (token 0 the root, token j + 1
+ *                 node j): it sees the slots below lengths[b], the root's, its own
+ *                 and those of the nodes above it.
+ *   stored        [B] int32: tokens that are codes (spec_kv_quantize_*), a multiple
+ *                 of block, at most lengths[b] + n_new[b].
+ * Sums are held in fp32.  Queries, weights and plain entries enter the products
+ * in fp16 times powers of two (bf16 call: at least 11 bits of each; fp32 call: two
+ * fp16 parts, 22 bits).
+ * A query row that is not finite makes its row of out NaN; so does a key or value
+ * that is not finite (all the rows that see it), and a block whose scale is NaN
+ * (rows that see one of its tokens).  What a row does not see has no part in it.
+ * Bad data (SPEC_FLAG_BAD_DATA): a length, n_new or stored out of range, more tokens
+ * than max_pages * page_size or 2^31 - 2^16, or a parent index outside [-1, i): all
+ * T rows of that sequence are NaN.  A page outside its pool: the rows that see one
+ * of its tokens are NaN.
+ * T >= 0 (<= 1025 with parent_idx), Hq a multiple of Hkv, Hq * D up to 2^24, T * Hq
+ * up to 2^30, B * T < 2^31, scale finite; the rest as above.  out shares no
+ * memory with an input (SPEC_ERR_OVERLAP).  Returns SPEC_OK, SPEC_ERR_NULL,
+ * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  Two launches on `stream`;
+ * scratch of some MB.
+ */
+int spec_kv_attention_f32(const float *q, int64_t q_stride, const float *key_cache, const float *value_cache, int pages,
+                    int page_size, const int32_t *page_table, int max_pages, const int32_t *lengths,
+                    const int32_t *n_new, const int32_t *parent_idx, const void *key_codes,
+                    const void *value_codes, const float *key_scales, const float *value_scales, int code_pages,
+                    int block, const int32_t *code_table, int max_code_pages, const int32_t *stored, int format,
+                    int B, int T, int Hq, int Hkv, int D, float scale, float *out, cudaStream_t stream);
+int spec_kv_attention_bf16(const uint16_t *q, int64_t q_stride, const uint16_t *key_cache, const uint16_t *value_cache, int pages,
+                    int page_size, const int32_t *page_table, int max_pages, const int32_t *lengths,
+                    const int32_t *n_new, const int32_t *parent_idx, const void *key_codes,
+                    const void *value_codes, const float *key_scales, const float *value_scales, int code_pages,
+                    int block, const int32_t *code_table, int max_code_pages, const int32_t *stored, int format,
+                    int B, int T, int Hq, int Hkv, int D, float scale, uint16_t *out, cudaStream_t stream);
+
+/*
  * Test hook, for fault-injection tests: the next n scratch allocations from
  * the library's pool (any device, any entry point that allocates) fail as if
  * the pool were exhausted.  The call then returns SPEC_ERR_CUDA before

@@ -24,6 +24,9 @@ outputs are complete there.  Outputs that it allocates are that stream's memory.
     spec_process_logits(logits, draft_tokens, ...)  # penalties, biases and grammar masks on a verify's rows
     spec_kv_append(k, v, key_cache, value_cache, page_table, lengths, ...)  # rotated, into a paged cache
     spec_kv_commit(key_cache, value_cache, page_table, lengths, ...)  # a tree's accepted path stays
+    spec_kv_quantize(key_cache, ..., stored, lengths, key_codes, ...)  # whole blocks become 8-bit codes
+    spec_kv_dequantize(key_codes, ..., starts, ends, key_cache, ...)   # and plain entries again
+    spec_kv_attention(q, key_cache, ..., lengths, key_codes, ..., stored)  # a step's tokens to codes and plain entries
     spec_get_status()                 # device status word (bad data, timeouts)
 """
 from __future__ import annotations
@@ -40,7 +43,7 @@ __all__ = [
     "spec_verify_greedy_argmax",
     "spec_tree_verify_greedy", "spec_tree_verify_sampling", "spec_acceptance_stats", "spec_ngram_draft",
     "spec_token_state", "spec_count_tokens", "spec_process_logits", "spec_rope_turns", "spec_kv_append",
-    "spec_kv_commit",
+    "spec_kv_commit", "spec_kv_quantize", "spec_kv_dequantize", "spec_kv_attention",
     "spec_get_status", "spec_test_spin_limit", "spec_test_wait_probe", "SpecError",
     "SPEC_FLAG_BAD_DATA", "SPEC_FLAG_TIMEOUT",
 ]
@@ -643,6 +646,115 @@ def spec_kv_commit(key_cache, value_cache, page_table, lengths, tree_tokens, par
             _arg(out_len, i32, (B,), dev, "out_len"), B, N, _arg(out_nodes, i32, (B, N + 1), dev, "out_nodes"),
             _arg(out_lengths, i32, (B,), dev, "out_lengths"))
     return out_nodes, out_lengths
+
+
+_FORMATS = {torch.int8: _lib.SPEC_KV_INT8, torch.float8_e4m3fn: _lib.SPEC_KV_E4M3}
+
+
+def _kv8(key_cache, value_cache, page_table, key_codes, value_codes, key_scales, value_scales, code_table, B, layered):
+    """The checked sizes and addresses of an 8-bit cache and the plain one next to it."""
+    if not isinstance(key_cache, torch.Tensor) or not key_cache.is_cuda or key_cache.dim() not in ((4, 5) if layered else (4,)):
+        raise ValueError(f"key_cache must be a CUDA tensor [{'(layers,) ' if layered else ''}pages, page_size, Hkv, D]")
+    dt, dev, shape = key_cache.dtype, key_cache.device, key_cache.shape
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError(f"key_cache must be float32 or bfloat16, got {dt}")
+    if not isinstance(key_codes, torch.Tensor) or key_codes.dim() != len(shape):
+        raise ValueError("key_codes must have key_cache's dimensions")
+    ct, cs = key_codes.dtype, key_codes.shape
+    if ct not in _FORMATS:
+        raise TypeError(f"key_codes must be int8 or float8_e4m3fn, got {ct}")
+    lead, (pages, page_size, Hkv, D), (code_pages, block) = shape[:-4], shape[-4:], cs[-4:-2]
+    layers = lead[0] if lead else 1
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    if not isinstance(code_table, torch.Tensor) or code_table.dim() != 2:
+        raise ValueError("code_table must be [B, max_code_pages]")
+    max_pages, max_code = page_table.shape[1], code_table.shape[1]
+    if (layers | pages | page_size | Hkv | D | code_pages | block | max_pages | max_code | B) >> 31:
+        _too_large()
+    codes, scales, f32, i32 = (*lead, code_pages, block, Hkv, D), (*lead, code_pages, Hkv), torch.float32, torch.int32
+    at = (_arg(key_cache, dt, shape, dev, "key_cache"), _arg(value_cache, dt, shape, dev, "value_cache"),
+          _arg(page_table, i32, (B, max_pages), dev, "page_table"), _arg(key_codes, ct, codes, dev, "key_codes"),
+          _arg(value_codes, ct, codes, dev, "value_codes"), _arg(key_scales, f32, scales, dev, "key_scales"),
+          _arg(value_scales, f32, scales, dev, "value_scales"), _arg(code_table, i32, (B, max_code), dev, "code_table"))
+    return dt, dev, layers, (pages, page_size, max_pages), (code_pages, block, max_code), Hkv, D, _FORMATS[ct], at
+
+
+def spec_kv_quantize(key_cache, value_cache, page_table, stored, lengths, key_codes, value_codes, key_scales, value_scales,
+                     code_table, out_stored=None, stream=None):
+    """Makes 8-bit codes of the whole blocks among each sequence's tokens
+    [stored[b], lengths[b]); returns the tokens that are codes afterwards [B].
+
+    key_cache, value_cache: [pages, page_size, Hkv, D], or [layers, pages, ...] for
+    all layers at once.  key_codes, value_codes: int8 or float8_e4m3fn [(layers,)
+    code_pages, block, Hkv, D], key_scales and value_scales float32 [(layers,)
+    code_pages, Hkv]; block i of sequence b is page code_table[b, i].  An entry is
+    code * scale.  Pages whose tokens are all codes may be used for later tokens."""
+    if not isinstance(stored, torch.Tensor) or stored.dim() != 1:
+        raise ValueError("stored must be [B]")
+    B = stored.shape[0]
+    dt, dev, layers, (pages, page_size, max_pages), (code_pages, block, max_code), Hkv, D, fmt, at = _kv8(
+        key_cache, value_cache, page_table, key_codes, value_codes, key_scales, value_scales, code_table, B, True)
+    i32 = torch.int32
+    if out_stored is None:
+        out_stored = _new((B,), i32, dev, stream)
+    lib = _lib.load()
+    entry = Hkv * D
+    _invoke(lib.spec_kv_quantize_bf16 if dt is torch.bfloat16 else lib.spec_kv_quantize_f32, dev, stream, at[0], at[1], layers,
+            pages * page_size * entry, pages, page_size, at[2], max_pages, _arg(stored, i32, (B,), dev, "stored"),
+            _arg(lengths, i32, (B,), dev, "lengths"), B, Hkv, D, fmt, at[3], at[4], code_pages * block * entry, at[5], at[6],
+            code_pages * Hkv, code_pages, block, at[7], max_code, _arg(out_stored, i32, (B,), dev, "out_stored"))
+    return out_stored
+
+
+def spec_kv_dequantize(key_codes, value_codes, key_scales, value_scales, code_table, starts, ends, key_cache, value_cache,
+                       page_table, stream=None):
+    """Writes each sequence's entries [starts[b], ends[b]), code * scale, to their
+    slots of the plain cache; shapes as for spec_kv_quantize."""
+    if not isinstance(starts, torch.Tensor) or starts.dim() != 1:
+        raise ValueError("starts must be [B]")
+    B = starts.shape[0]
+    dt, dev, layers, (pages, page_size, max_pages), (code_pages, block, max_code), Hkv, D, fmt, at = _kv8(
+        key_cache, value_cache, page_table, key_codes, value_codes, key_scales, value_scales, code_table, B, True)
+    lib = _lib.load()
+    entry, i32 = Hkv * D, torch.int32
+    _invoke(lib.spec_kv_dequantize_bf16 if dt is torch.bfloat16 else lib.spec_kv_dequantize_f32, dev, stream, at[3], at[4],
+            layers, code_pages * block * entry, at[5], at[6], code_pages * Hkv, code_pages, block, at[7], max_code,
+            _arg(starts, i32, (B,), dev, "starts"), _arg(ends, i32, (B,), dev, "ends"), B, Hkv, D, fmt, at[0], at[1],
+            pages * page_size * entry, pages, page_size, at[2], max_pages)
+
+
+def spec_kv_attention(q, key_cache, value_cache, page_table, lengths, key_codes, value_codes, key_scales, value_scales,
+                      code_table, stored, parent_idx=None, n_new=None, scale=None, out=None, stream=None):
+    """softmax(scale q K^T) V of a step's queries q [B, T, Hq, D] (one token, a chain, a
+    tree or a prompt), after spec_kv_append has put the step's entries behind
+    lengths[b]: the slots below stored[b] are read from the codes (shapes as for
+    spec_kv_quantize, one layer), the others from the plain cache.
+
+    Token i sees the slots up to lengths[b] + i or, with parent_idx [B, T-1], those
+    below lengths[b], the root's, its own and its ancestors'.  n_new [B]: tokens
+    from there on are padding, whose rows of out are not written.  scale: D ** -0.5
+    by default.  q may be a slice of a joint projection.  Returns out [B, T, Hq, D]."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, T, Hq, D]")
+    B, T, Hq, D = q.shape
+    dt, dev, layers, (pages, page_size, max_pages), (code_pages, block, max_code), Hkv, Dc, fmt, at = _kv8(
+        key_cache, value_cache, page_table, key_codes, value_codes, key_scales, value_scales, code_table, B, False)
+    if Dc != D:
+        raise ValueError(f"q has heads of {D} values, key_cache of {Dc}")
+    if (T | Hq) >> 31:
+        _too_large()
+    qs = _token_stride(q, "q", dt, (B, T, Hq, D), dev)
+    if out is None:
+        out = _new((B, T, Hq, D), dt, dev, stream)
+    lib = _lib.load()
+    i32 = torch.int32
+    _invoke(lib.spec_kv_attention_bf16 if dt is torch.bfloat16 else lib.spec_kv_attention_f32, dev, stream, _ptr(q), qs, at[0],
+            at[1], pages, page_size, at[2], max_pages, _arg(lengths, i32, (B,), dev, "lengths"), _arg(n_new, i32, (B,), dev, "n_new"),
+            _arg(parent_idx, i32, (B, T - 1), dev, "parent_idx"), at[3], at[4], at[5], at[6], code_pages, block, at[7], max_code,
+            _arg(stored, i32, (B,), dev, "stored"), fmt, B, T, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale),
+            _arg(out, dt, (B, T, Hq, D), dev, "out"))
+    return out
 
 
 def spec_get_status(stream=None, device=None) -> int:

@@ -26,6 +26,8 @@ SPEC_ERR_OVERLAP = -7
 SPEC_STATIC_SCRATCH_BYTES = 8 << 20
 SPEC_FLAG_BAD_DATA = 1
 SPEC_FLAG_TIMEOUT = 2
+SPEC_KV_INT8 = 0
+SPEC_KV_E4M3 = 1
 
 _lock = threading.Lock()
 _lib = None
@@ -67,6 +69,12 @@ SIGNATURES = {
     "spec_kv_append_bf16": [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P,
                             _I, _I, _I, _P],
     "spec_kv_commit": [_P, _P, _I, _I64, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P],
+    **{f"spec_kv_quantize_{t}": [_P, _P, _I, _I64, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _I64, _P, _P, _I64,
+                                 _I, _I, _P, _I, _P, _P] for t in ("f32", "bf16")},
+    **{f"spec_kv_dequantize_{t}": [_P, _P, _I, _I64, _P, _P, _I64, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _I64,
+                                   _I, _I, _P, _I, _P] for t in ("f32", "bf16")},
+    **{f"spec_kv_attention_{t}": [_P, _I64, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _I,
+                                  _I, _I, _I, _I, _I, _F, _P, _P] for t in ("f32", "bf16")},
     "spec_test_fail_allocations": [_I],
     "spec_test_spin_limit": [ctypes.c_uint32],
     "spec_test_wait_probe": [ctypes.c_void_p],

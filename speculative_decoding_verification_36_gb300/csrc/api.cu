@@ -711,6 +711,193 @@ int kv_append_impl(bool bf16, const void* k, const void* v, int64_t kv_stride, c
   return SPEC_OK;
 }
 
+// Do the layers of two caches, of sizes n and m and `a` and `b` bytes apart, share a byte?
+bool layers_overlap(const void* p, uint64_t n, uint64_t a, const void* q, uint64_t m, uint64_t b, int layers) {
+  for (int l = 0; l < layers; ++l)
+    if (rows_overlap(p, n, layers > 1 ? a : n + 1, layers, (const char*)q + l * b, m)) return true;
+  return false;
+}
+
+// The pools of the 8-bit cache and the plain one, as three entry points take them.
+struct Kv8Sizes {
+  int layers, pages, page_size, max_pages, code_pages, block, max_code_pages, B, Hkv, D, format;
+};
+constexpr int kMaxCodePages = 1 << 23;          // of a sequence, and its tokens: a round of
+constexpr long long kMaxCodeTokens = 1LL << 26; // sequences is counted in 32 bits
+bool kv8_sizes_ok(const Kv8Sizes& z) {
+  return z.layers >= 1 && z.layers <= 32767 && z.B >= 0 && z.Hkv >= 1 && z.D >= 16 && z.D <= 256 && z.D % 16 == 0 &&
+         (long long)z.Hkv * z.D <= (1 << 24) && z.pages >= 1 && z.page_size >= 1 && z.max_pages >= 1 &&
+         (long long)z.pages * z.page_size <= INT_MAX && z.code_pages >= 1 && z.block >= 1 && z.block <= 65536 &&
+         (long long)z.code_pages * z.block <= INT_MAX && z.max_code_pages >= 1 && z.max_code_pages <= kMaxCodePages &&
+         (long long)z.max_code_pages * z.block <= kMaxCodeTokens &&
+         (z.format == SPEC_KV_INT8 || z.format == SPEC_KV_E4M3);
+}
+// A pool of one cache: [layers] of `size` bytes, `step` bytes apart.
+struct Pool {
+  const void* p;
+  uint64_t size, step;
+};
+
+// Quantising (out_stored) or reading back: the pools in `to` are written, those in `from` read.
+int kv8_impl(bool bf16, bool quantize, const Kv8Sizes& z, const void* k_cache, const void* v_cache, int64_t layer_stride,
+             const int32_t* page_table, const void* k_codes, const void* v_codes, int64_t code_stride, const float* k_scales,
+             const float* v_scales, int64_t scale_stride, const int32_t* code_table, const int32_t* first, const int32_t* last,
+             int32_t* out_stored, cudaStream_t stream) {
+  const uint64_t esz = bf16 ? 2 : 4, entry = (uint64_t)z.Hkv * z.D;
+  if (!kv8_sizes_ok(z)) return SPEC_ERR_SHAPE;
+  const uint64_t plain = (uint64_t)z.pages * z.page_size * entry, codes = (uint64_t)z.code_pages * z.block * entry,
+                 scales = (uint64_t)z.code_pages * z.Hkv;
+  constexpr uint64_t kFar = 1ull << 44;  // offsets of 32767 layers stay below 2^63 bytes
+  if (z.layers > 1 &&
+      (layer_stride < 0 || code_stride < 0 || scale_stride < 0 || (uint64_t)layer_stride < plain || (uint64_t)layer_stride > kFar ||
+       (uint64_t)code_stride < codes || (uint64_t)code_stride > kFar || (uint64_t)scale_stride < scales ||
+       (uint64_t)scale_stride > kFar || layer_stride * esz % 16 || code_stride % 16))
+    return SPEC_ERR_SHAPE;
+  if (z.B == 0) return SPEC_OK;
+  if (!k_cache || !v_cache || !page_table || !k_codes || !v_codes || !k_scales || !v_scales || !code_table || !first || !last ||
+      (quantize && !out_stored))
+    return SPEC_ERR_NULL;
+  for (const void* p : {k_cache, v_cache, k_codes, v_codes})
+    if (!aligned16(p)) return SPEC_ERR_SHAPE;
+  if (z.layers == 1) layer_stride = plain, code_stride = codes, scale_stride = scales;
+  const size_t row = (size_t)z.B * 4;
+  const Span read[] = {{page_table, row * z.max_pages}, {code_table, row * z.max_code_pages}, {first, row}, {last, row}};
+  const Pool caches[] = {{k_cache, plain * esz, layer_stride * esz}, {v_cache, plain * esz, layer_stride * esz}};
+  const Pool coded[] = {{k_codes, codes, (uint64_t)code_stride}, {v_codes, codes, (uint64_t)code_stride},
+                        {k_scales, scales * 4, (uint64_t)scale_stride * 4}, {v_scales, scales * 4, (uint64_t)scale_stride * 4}};
+  const Pool* to = quantize ? coded : caches;
+  const Pool* from = quantize ? caches : coded;
+  const int n_to = quantize ? 4 : 2, n_from = quantize ? 2 : 4;
+  for (int i = 0; i < n_to; ++i) {
+    for (int j = 0; j < n_from; ++j)
+      if (layers_overlap(to[i].p, to[i].size, to[i].step, from[j].p, from[j].size, from[j].step, z.layers)) return SPEC_ERR_OVERLAP;
+    for (int j = 0; j < i; ++j)
+      if (layers_overlap(to[i].p, to[i].size, to[i].step, to[j].p, to[j].size, to[j].step, z.layers)) return SPEC_ERR_OVERLAP;
+    for (const Span& x : read)
+      if (rows_overlap(to[i].p, to[i].size, to[i].step, z.layers, x.p, x.n)) return SPEC_ERR_OVERLAP;
+  }
+  if (quantize) {
+    if (any_overlaps(read, out_stored, row)) return SPEC_ERR_OVERLAP;
+    for (const Pool& x : caches)
+      if (rows_overlap(x.p, x.size, x.step, z.layers, out_stored, row)) return SPEC_ERR_OVERLAP;
+    for (const Pool& x : coded)
+      if (rows_overlap(x.p, x.size, x.step, z.layers, out_stored, row)) return SPEC_ERR_OVERLAP;
+  }
+  sv::Kv8Args a;
+  memset(&a, 0, sizeof a);
+  a.k_cache = (void*)k_cache;
+  a.v_cache = (void*)v_cache;
+  a.k_codes = (void*)k_codes;
+  a.v_codes = (void*)v_codes;
+  a.k_scales = (float*)k_scales;
+  a.v_scales = (float*)v_scales;
+  a.layer_stride = layer_stride;
+  a.code_stride = code_stride;
+  a.scale_stride = scale_stride;
+  a.page_table = page_table;
+  a.code_table = code_table;
+  a.pages = z.pages;
+  a.page_size = z.page_size;
+  a.max_pages = z.max_pages;
+  a.code_pages = z.code_pages;
+  a.block = z.block;
+  a.max_code_pages = z.max_code_pages;
+  a.first = first;
+  a.last = last;
+  a.out_stored = out_stored;
+  a.layers = z.layers;
+  a.B = z.B;
+  a.Hkv = z.Hkv;
+  a.D = z.D;
+  DeviceState* d = nullptr;
+  const int rc = get_device_state(&d);
+  if (rc) return rc;
+  a.status = d->status;
+  const bool e4m3 = z.format == SPEC_KV_E4M3;
+  const cudaError_t e = quantize ? sv::launch_kv_quantize(a, bf16, e4m3, d->sms, stream)
+                                 : sv::launch_kv_dequantize(a, bf16, e4m3, d->sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, quantize ? "cache quantising launch" : "cache reading launch");
+  return SPEC_OK;
+}
+
+int attention_impl(bool bf16, const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int pages, int page_size,
+                   const int32_t* page_table, int max_pages, const int32_t* lengths, const int32_t* n_new, const int32_t* parents,
+                   const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales, int code_pages, int block,
+                   const int32_t* code_table, int max_code_pages, const int32_t* stored, int format, int B, int T, int Hq, int Hkv,
+                   int D, float scale, void* out, cudaStream_t stream) {
+  const Kv8Sizes z = {1, pages, page_size, max_pages, code_pages, block, max_code_pages, B, Hkv, D, format};
+  if (!kv8_sizes_ok(z) || T < 0 || Hq < 1 || Hq % Hkv || (long long)Hq * D > (1 << 24) || (long long)B * T > INT_MAX ||
+      (long long)T * Hq > (1 << 30) || q_stride < (long long)Hq * D || (parents && T > sv::kMaxTreeNodes + 1) || !isfinite(scale))
+    return SPEC_ERR_SHAPE;
+  if (B == 0 || T == 0) return SPEC_OK;
+  if (!q || !k_cache || !v_cache || !page_table || !lengths || !k_codes || !v_codes || !k_scales || !v_scales || !code_table ||
+      !stored || !out)
+    return SPEC_ERR_NULL;
+  for (const void* p : {k_cache, v_cache, k_codes, v_codes, (const void*)out})
+    if (!aligned16(p)) return SPEC_ERR_SHAPE;
+  const uint64_t esz = bf16 ? 2 : 4, entry = (uint64_t)Hkv * D, rows = (uint64_t)B * T, qn = (uint64_t)Hq * D * esz;
+  const size_t row = (size_t)B * 4;
+  const uint64_t plain = (uint64_t)pages * page_size * entry * esz, codes = (uint64_t)code_pages * block * entry,
+                 scales = (uint64_t)code_pages * Hkv * 4;
+  const Span read[] = {{page_table, row * max_pages}, {code_table, row * max_code_pages}, {lengths, row}, {stored, row},
+                       {n_new, n_new ? row : 0}, {parents, parents ? row * (T - 1) : 0}, {k_cache, plain}, {v_cache, plain},
+                       {k_codes, codes}, {v_codes, codes}, {k_scales, scales}, {v_scales, scales}};
+  if (any_overlaps(read, out, rows * qn) || rows_overlap(q, qn, q_stride * esz, rows, out, rows * qn)) return SPEC_ERR_OVERLAP;
+  sv::KvAttendArgs a;
+  memset(&a, 0, sizeof a);
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_codes = (const uint8_t*)k_codes;
+  a.v_codes = (const uint8_t*)v_codes;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.page_table = page_table;
+  a.code_table = code_table;
+  a.pages = pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.code_pages = code_pages;
+  a.block = block;
+  a.max_code_pages = max_code_pages;
+  a.lengths = lengths;
+  a.stored = stored;
+  a.n_new = n_new;
+  a.parents = T > 1 ? parents : nullptr;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.G = Hq / Hkv;
+  a.scale = scale * 1.4426950408889634f;
+  a.div_block = sv::make_fastdiv((uint32_t)block);
+  a.div_page = sv::make_fastdiv((uint32_t)page_size);
+  a.div_g = sv::make_fastdiv((uint32_t)a.G);
+  DeviceState* d = nullptr;
+  int rc = get_device_state(&d);
+  if (rc) return rc;
+  a.status = d->status;
+  const bool e4m3 = format == SPEC_KV_E4M3;
+  const auto launch = bf16 ? (e4m3 ? sv::launch_attend_rows_bf16_e4m3 : sv::launch_attend_rows_bf16_int8)
+                           : (e4m3 ? sv::launch_attend_rows_f32_e4m3 : sv::launch_attend_rows_f32_int8);
+  sv::WsLayout l;
+  memset(&l, 0, sizeof l);
+  cudaError_t e = launch(a, d->sms, &l.total, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "attention workspace");
+  void* ws = nullptr;
+  rc = get_scratch(d, false, l, stream, &ws);
+  if (rc) return rc;
+  a.part = (float*)ws;
+  e = launch(a, d->sms, nullptr, stream);
+  const cudaError_t e2 = put_scratch(false, ws, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  if (e2 != cudaSuccess) return cuda_fail(e2, "cudaFreeAsync");
+  return SPEC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1068,6 +1255,72 @@ int spec_kv_commit(void* key_cache, void* value_cache, int layers, int64_t layer
   const cudaError_t e = sv::launch_kv_commit(a, vb, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cache commit launch");
   return SPEC_OK;
+}
+
+int spec_kv_quantize_f32(const float* key_cache, const float* value_cache, int layers, int64_t layer_stride, int pages,
+                         int page_size, const int32_t* page_table, int max_pages, const int32_t* stored,
+                         const int32_t* lengths, int B, int Hkv, int D, int format, void* key_codes, void* value_codes,
+                         int64_t code_stride, float* key_scales, float* value_scales, int64_t scale_stride,
+                         int code_pages, int block, const int32_t* code_table, int max_code_pages, int32_t* out_stored,
+                         cudaStream_t stream) {
+  const Kv8Sizes z = {layers, pages, page_size, max_pages, code_pages, block, max_code_pages, B, Hkv, D, format};
+  return kv8_impl(false, true, z, key_cache, value_cache, layer_stride, page_table, key_codes, value_codes, code_stride,
+                  key_scales, value_scales, scale_stride, code_table, stored, lengths, out_stored, stream);
+}
+
+int spec_kv_dequantize_f32(const void* key_codes, const void* value_codes, int layers, int64_t code_stride,
+                           const float* key_scales, const float* value_scales, int64_t scale_stride, int code_pages,
+                           int block, const int32_t* code_table, int max_code_pages, const int32_t* starts,
+                           const int32_t* ends, int B, int Hkv, int D, int format, float* key_cache, float* value_cache,
+                           int64_t layer_stride, int pages, int page_size, const int32_t* page_table, int max_pages,
+                           cudaStream_t stream) {
+  const Kv8Sizes z = {layers, pages, page_size, max_pages, code_pages, block, max_code_pages, B, Hkv, D, format};
+  return kv8_impl(false, false, z, key_cache, value_cache, layer_stride, page_table, key_codes, value_codes, code_stride,
+                  key_scales, value_scales, scale_stride, code_table, starts, ends, nullptr, stream);
+}
+
+int spec_kv_attention_f32(const float* q, int64_t q_stride, const float* key_cache, const float* value_cache, int pages,
+                          int page_size, const int32_t* page_table, int max_pages, const int32_t* lengths,
+                          const int32_t* n_new, const int32_t* parent_idx, const void* key_codes,
+                          const void* value_codes, const float* key_scales, const float* value_scales, int code_pages,
+                          int block, const int32_t* code_table, int max_code_pages, const int32_t* stored, int format,
+                          int B, int T, int Hq, int Hkv, int D, float scale, float* out, cudaStream_t stream) {
+  return attention_impl(false, q, q_stride, key_cache, value_cache, pages, page_size, page_table, max_pages, lengths, n_new,
+                        parent_idx, key_codes, value_codes, key_scales, value_scales, code_pages, block, code_table,
+                        max_code_pages, stored, format, B, T, Hq, Hkv, D, scale, out, stream);
+}
+
+int spec_kv_quantize_bf16(const uint16_t* key_cache, const uint16_t* value_cache, int layers, int64_t layer_stride, int pages,
+                         int page_size, const int32_t* page_table, int max_pages, const int32_t* stored,
+                         const int32_t* lengths, int B, int Hkv, int D, int format, void* key_codes, void* value_codes,
+                         int64_t code_stride, float* key_scales, float* value_scales, int64_t scale_stride,
+                         int code_pages, int block, const int32_t* code_table, int max_code_pages, int32_t* out_stored,
+                         cudaStream_t stream) {
+  const Kv8Sizes z = {layers, pages, page_size, max_pages, code_pages, block, max_code_pages, B, Hkv, D, format};
+  return kv8_impl(true, true, z, key_cache, value_cache, layer_stride, page_table, key_codes, value_codes, code_stride,
+                  key_scales, value_scales, scale_stride, code_table, stored, lengths, out_stored, stream);
+}
+
+int spec_kv_dequantize_bf16(const void* key_codes, const void* value_codes, int layers, int64_t code_stride,
+                           const float* key_scales, const float* value_scales, int64_t scale_stride, int code_pages,
+                           int block, const int32_t* code_table, int max_code_pages, const int32_t* starts,
+                           const int32_t* ends, int B, int Hkv, int D, int format, uint16_t* key_cache, uint16_t* value_cache,
+                           int64_t layer_stride, int pages, int page_size, const int32_t* page_table, int max_pages,
+                           cudaStream_t stream) {
+  const Kv8Sizes z = {layers, pages, page_size, max_pages, code_pages, block, max_code_pages, B, Hkv, D, format};
+  return kv8_impl(true, false, z, key_cache, value_cache, layer_stride, page_table, key_codes, value_codes, code_stride,
+                  key_scales, value_scales, scale_stride, code_table, starts, ends, nullptr, stream);
+}
+
+int spec_kv_attention_bf16(const uint16_t* q, int64_t q_stride, const uint16_t* key_cache, const uint16_t* value_cache, int pages,
+                          int page_size, const int32_t* page_table, int max_pages, const int32_t* lengths,
+                          const int32_t* n_new, const int32_t* parent_idx, const void* key_codes,
+                          const void* value_codes, const float* key_scales, const float* value_scales, int code_pages,
+                          int block, const int32_t* code_table, int max_code_pages, const int32_t* stored, int format,
+                          int B, int T, int Hq, int Hkv, int D, float scale, uint16_t* out, cudaStream_t stream) {
+  return attention_impl(true, q, q_stride, key_cache, value_cache, pages, page_size, page_table, max_pages, lengths, n_new,
+                        parent_idx, key_codes, value_codes, key_scales, value_scales, code_pages, block, code_table,
+                        max_code_pages, stored, format, B, T, Hq, Hkv, D, scale, out, stream);
 }
 
 int spec_test_fail_allocations(int n) { return g_fail_allocs.exchange(n < 0 ? 0 : n); }

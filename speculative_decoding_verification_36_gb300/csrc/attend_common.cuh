@@ -1,0 +1,182 @@
+// attend_common.cuh -- what the attention kernels share: which keys a row sees, how
+// the work is cut into equal shares, and how the shares' results are joined.
+//
+// A segment is a (sequence, head of keys, tile of rows); its rows are the queries
+// of the tile's tokens in the heads that share the keys, row = token * G + head.
+// A segment's keys come in units of kKeys: first the codes, then the plain entries.
+// All segments' units in a row are cut into as many equal shares as there are CTAs,
+// whatever the sequences' lengths; where a segment falls into several shares, each
+// leaves its sums (running maximum, sum, weighted values) in the workspace, and a
+// second launch adds them in the order of the shares: no atomics, the same bits
+// on every run.
+#pragma once
+#include "sv_common.cuh"
+#include "sv_kernels.h"
+
+namespace sv {
+
+constexpr long long kAttendMaxKeys = (1LL << 31) - (1 << 16);  // positions and ends of units stay below 2^31
+
+struct Sequence {
+  int len, stored, n_new;  // entries before the step, of which codes; the step's tokens
+  bool bad;
+};
+
+__device__ __forceinline__ Sequence attend_sequence(const KvAttendArgs& a, int b) {
+  Sequence s;
+  s.len = __ldg(a.lengths + b);
+  s.stored = __ldg(a.stored + b);
+  s.n_new = a.n_new ? __ldg(a.n_new + b) : a.T;
+  const long long end = (long long)s.len + s.n_new;
+  s.bad = s.len < 0 || s.n_new < 0 || s.n_new > a.T || end > (long long)a.max_pages * a.page_size || end > kAttendMaxKeys || s.stored < 0 ||
+          s.stored > end || s.stored > (long long)a.max_code_pages * a.block ||
+          fdiv(max(s.stored, 0), a.div_block) * a.block != s.stored;
+  if (s.bad) s.len = s.stored = 0, s.n_new = a.T;
+  return s;
+}
+
+// The keys [0, codes) and [stored, end) that a tile's rows may see.
+struct Keys {
+  int codes, stored, end;
+};
+template <int kRows>
+__device__ __forceinline__ Keys attend_keys(const KvAttendArgs& a, const Sequence& s, int tile) {
+  Keys k;
+  const int t1 = min(s.n_new, fdiv((tile + 1) * kRows - 1, a.div_g) + 1);  // behind the tile's last token
+  k.end = a.parents ? s.len + s.n_new : s.len + t1;
+  k.codes = min(s.stored, k.end);
+  k.stored = s.stored;
+  return k;
+}
+// Units of a segment: none where the tile has no tokens, one (which reads nothing)
+// for a bad sequence.
+template <int kRows, int kKeys>
+__device__ __forceinline__ int attend_units(const KvAttendArgs& a, const Sequence& s, int tile) {
+  if (fdiv(tile * kRows, a.div_g) >= s.n_new) return 0;
+  if (s.bad) return 1;
+  const Keys k = attend_keys<kRows>(a, s, tile);
+  return (k.codes + kKeys - 1) / kKeys + (k.end - k.codes + kKeys - 1) / kKeys;
+}
+
+// The share of one CTA, as a place among the segments and a number of units.
+struct Share {
+  long long all, from, left;  // units of the launch, those before the place, those of this share from there on
+  int shares;                 // CTAs with a share
+  int b, h, tile, u;          // the place: unit u of its segment
+  Sequence s;
+};
+
+// All threads of the CTA.  s_scan: kThreads + 1 words of 8 bytes.
+template <int kThreads, int kRows, int kKeys>
+__device__ __forceinline__ Share attend_share(const KvAttendArgs& a, unsigned long long* s_scan) {
+  __shared__ unsigned long long s_warp[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Share w;
+  auto count = [&](int b) -> unsigned long long {
+    if (b >= a.B) return 0;
+    const Sequence s = attend_sequence(a, b);
+    unsigned long long n = 0;
+    for (int t = 0; t < a.tiles; ++t) n += attend_units<kRows, kKeys>(a, s, t);
+    return n * a.Hkv;
+  };
+  // sums of a round of kThreads sequences: s_scan[i] before sequence i, s_scan[kThreads] of all
+  auto scan = [&](int b0) {
+    const unsigned long long n = count(b0 + threadIdx.x);
+    unsigned long long x = n;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    unsigned long long before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before += s_warp[i];
+      all += s_warp[i];
+    }
+    s_scan[threadIdx.x] = before + x - n;
+    if (threadIdx.x == 0) s_scan[kThreads] = all;
+    __syncthreads();
+  };
+  w.all = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    scan(b0);
+    w.all += s_scan[kThreads];
+  }
+  w.shares = (int)min((long long)gridDim.x, w.all);
+  if ((int)blockIdx.x >= w.shares) {
+    w.left = 0;
+    return w;
+  }
+  w.from = (long long)((unsigned long long)blockIdx.x * w.all / w.shares);
+  w.left = (long long)((unsigned long long)(blockIdx.x + 1) * w.all / w.shares) - w.from;
+  unsigned long long before = 0;
+  int b0 = 0;
+  if (a.B > kThreads) {
+    for (;; b0 += kThreads) {
+      scan(b0);
+      if (before + s_scan[kThreads] > (unsigned long long)w.from) break;
+      before += s_scan[kThreads];
+    }
+  }
+  int i = 0;  // the last sequence that begins at the place or before
+#pragma unroll
+  for (int d = kThreads / 2; d >= 1; d /= 2)
+    if (before + s_scan[i + d] <= (unsigned long long)w.from) i += d;
+  w.b = b0 + i;
+  long long rest = w.from - (long long)(before + s_scan[i]);
+  const long long head = (long long)((s_scan[i + 1] - s_scan[i]) / (unsigned)a.Hkv);  // units of each of its heads
+  w.s = attend_sequence(a, w.b);
+  w.h = (int)(rest / head);
+  rest -= (long long)w.h * head;
+  w.tile = 0;
+  for (;;) {
+    const int n = attend_units<kRows, kKeys>(a, w.s, w.tile);
+    if (rest < n) break;
+    rest -= n;
+    ++w.tile;
+  }
+  w.u = (int)rest;
+  return w;
+}
+// The next segment with units, once `done` of the place's have been taken.
+template <int kRows, int kKeys>
+__device__ __forceinline__ void attend_advance(const KvAttendArgs& a, Share& w, int done) {
+  w.left -= done;
+  w.from += done;
+  w.u = 0;
+  if (w.left <= 0) return;
+  do {
+    if (++w.tile == a.tiles) {
+      w.tile = 0;
+      if (++w.h == a.Hkv) {
+        w.h = 0;
+        w.s = attend_sequence(a, ++w.b);
+      }
+    }
+  } while (attend_units<kRows, kKeys>(a, w.s, w.tile) == 0);
+}
+// The share that unit `u` falls into.
+__device__ __forceinline__ int attend_share_of(const Share& w, long long u) {
+  return (int)(((unsigned long long)(u + 1) * w.shares - 1) / (unsigned long long)w.all);
+}
+
+// Ancestors of a token as bits: token 0 is the root, token j + 1 node j.
+__device__ __forceinline__ void attend_bits(const int* parents, int token, int words, uint32_t* bits) {
+  for (int w = 0; w < words; ++w) bits[w] = 0;
+  bits[0] = 1u;  // the root
+  for (int node = token - 1; node >= 0; node = parents[node]) bits[(node + 1) >> 5] |= 1u << ((node + 1) & 31);
+}
+
+// The power of two that brings a magnitude (its bits) into [2^7, 2^8), and the one back.
+__device__ __forceinline__ float scale_up(unsigned bits) {
+  return __uint_as_float((261u - max(min(bits >> 23, 254u), 8u)) << 23);
+}
+__device__ __forceinline__ float scale_down(unsigned bits) {
+  return __uint_as_float((max(min(bits >> 23, 254u), 8u) - 7u) << 23);
+}
+
+}  // namespace sv

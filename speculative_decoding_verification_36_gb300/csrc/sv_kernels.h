@@ -339,6 +339,51 @@ struct KvCommitArgs {
 };
 cudaError_t launch_kv_commit(const KvCommitArgs& a, int vec_bytes, cudaStream_t s);
 
+// The cache in 8 bits (kv8_kernel.cu): codes [layers] of [code_pages, block, Hkv, D],
+// scales [layers] of [code_pages, Hkv]; strides in elements.
+struct Kv8Args {
+  void *k_cache, *v_cache;  // [layers] of [pages, page_size, Hkv, D]
+  void *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+  long long layer_stride, code_stride, scale_stride;
+  const int32_t *page_table, *code_table;  // [B, max_pages], [B, max_code_pages]
+  int pages, page_size, max_pages, code_pages, block, max_code_pages;
+  const int32_t *first, *last;  // [B]
+  int32_t* out_stored;          // [B] (quantising)
+  int layers, B, Hkv, D;
+  unsigned* status;
+  FastDiv div_block, div_page, div_per, div_head;  // set by the launch
+};
+cudaError_t launch_kv_quantize(const Kv8Args& a, bool bf16, bool e4m3, int sms, cudaStream_t s);
+cudaError_t launch_kv_dequantize(const Kv8Args& a, bool bf16, bool e4m3, int sms, cudaStream_t s);
+
+// Attention of a step's tokens to the codes and the plain entries (attend_*.cu).
+struct KvAttendArgs {
+  const void* q;       // token stride q_stride, heads contiguous
+  void* out;           // [B, T, Hq, D]
+  long long q_stride;  // elements
+  const void *k_cache, *v_cache;  // [pages, page_size, Hkv, D]
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scales, *v_scales;
+  const int32_t *page_table, *code_table;
+  int pages, page_size, max_pages, code_pages, block, max_code_pages;
+  const int32_t *lengths, *stored;
+  const int32_t* n_new;    // [B] or NULL: T
+  const int32_t* parents;  // [B, T - 1] or NULL: a chain
+  int B, T, Hq, Hkv, D, G;  // G = Hq / Hkv
+  float scale;              // times log2(e)
+  FastDiv div_block, div_page, div_g;
+  unsigned* status;
+  float* part;  // workspace: the shares' sums
+  int tiles;    // set by the launch: row tiles of a sequence and head
+  int4* meta;   // ... per share the segment that it begins and others end
+};
+// With `bytes`, only the size of the workspace is asked for.
+cudaError_t launch_attend_rows_bf16_int8(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
+cudaError_t launch_attend_rows_bf16_e4m3(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
+cudaError_t launch_attend_rows_f32_int8(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
+cudaError_t launch_attend_rows_f32_e4m3(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
+
 // Resident CTAs per SM for each kernel (occupancy calculator).
 int sample_blocks_per_sm(bool bf16, bool vec);
 int greedy_blocks_per_sm(bool bf16, bool vec);
