@@ -20,8 +20,10 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["api.cu", "sample_kernel.cu", "greedy_kernel.cu", "acceptance_kernel.cu",
            "tree_sample_kernel.cu", "ngram_kernel.cu", "process_kernel.cu", "kv_kernel.cu", "kv8_kernel.cu",
-           "attend_rows_bf16_int8.cu", "attend_rows_bf16_e4m3.cu", "attend_rows_f32_int8.cu", "attend_rows_f32_e4m3.cu"]
-HEADERS = ["sv_common.cuh", "sv_bulk.cuh", "sv_kernels.h", "attend_common.cuh", "attend_rows.cuh"]
+           "attend_rows_bf16_int8.cu", "attend_rows_bf16_e4m3.cu", "attend_rows_f32_int8.cu", "attend_rows_f32_e4m3.cu",
+           "attend_tiles_int8.cu", "attend_tiles_e4m3.cu"]
+HEADERS = ["sv_common.cuh", "sv_bulk.cuh", "sv_kernels.h", "attend_common.cuh", "attend_rows.cuh",
+           "attend_tiles.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

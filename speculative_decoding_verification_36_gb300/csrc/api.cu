@@ -881,7 +881,9 @@ int attention_impl(bool bf16, const void* q, int64_t q_stride, const void* k_cac
   if (rc) return rc;
   a.status = d->status;
   const bool e4m3 = format == SPEC_KV_E4M3;
-  const auto launch = bf16 ? (e4m3 ? sv::launch_attend_rows_bf16_e4m3 : sv::launch_attend_rows_bf16_int8)
+  const bool tiles = bf16 && D <= sv::kAttendTilesMaxD && (!a.parents || T <= sv::kAttendTilesMaxTree) && (long long)T * a.G > 16;
+  const auto launch = tiles ? (e4m3 ? sv::launch_attend_tiles_e4m3 : sv::launch_attend_tiles_int8)
+                      : bf16 ? (e4m3 ? sv::launch_attend_rows_bf16_e4m3 : sv::launch_attend_rows_bf16_int8)
                            : (e4m3 ? sv::launch_attend_rows_f32_e4m3 : sv::launch_attend_rows_f32_int8);
   sv::WsLayout l;
   memset(&l, 0, sizeof l);
@@ -1336,6 +1338,8 @@ int spec_test_spin_limit(uint32_t iterations) {
   if (e == cudaSuccess) e = sv::tree_sample_set_spin_limit(n);
   if (e == cudaSuccess) e = sv::ngram_set_spin_limit(n);
   if (e == cudaSuccess) e = sv::process_set_spin_limit(n);
+  if (e == cudaSuccess) e = sv::attend_tiles_int8_set_spin_limit(n);
+  if (e == cudaSuccess) e = sv::attend_tiles_e4m3_set_spin_limit(n);
   if (e != cudaSuccess) return cuda_fail(e, "spin limit");
   return SPEC_OK;
 }

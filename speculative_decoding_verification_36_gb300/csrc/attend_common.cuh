@@ -13,6 +13,9 @@
 #include "sv_common.cuh"
 #include "sv_kernels.h"
 
+#include <cuda_fp16.h>
+#include <string.h>
+
 namespace sv {
 
 constexpr long long kAttendMaxKeys = (1LL << 31) - (1 << 16);  // positions and ends of units stay below 2^31
@@ -66,7 +69,8 @@ struct Share {
   Sequence s;
 };
 
-// All threads of the CTA.  s_scan: kThreads + 1 words of 8 bytes.
+// All threads of the CTA, of which the first kThreads (a power of two) count.  s_scan:
+// kThreads + 1 words of 8 bytes.
 template <int kThreads, int kRows, int kKeys>
 __device__ __forceinline__ Share attend_share(const KvAttendArgs& a, unsigned long long* s_scan) {
   __shared__ unsigned long long s_warp[kThreads / 32];
@@ -81,7 +85,8 @@ __device__ __forceinline__ Share attend_share(const KvAttendArgs& a, unsigned lo
   };
   // sums of a round of kThreads sequences: s_scan[i] before sequence i, s_scan[kThreads] of all
   auto scan = [&](int b0) {
-    const unsigned long long n = count(b0 + threadIdx.x);
+    const bool counts = threadIdx.x < kThreads;
+    const unsigned long long n = counts ? count(b0 + threadIdx.x) : 0;
     unsigned long long x = n;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -89,7 +94,7 @@ __device__ __forceinline__ Share attend_share(const KvAttendArgs& a, unsigned lo
       if (lane >= d) x += y;
     }
     __syncthreads();
-    if (lane == 31) s_warp[warp] = x;
+    if (counts && lane == 31) s_warp[warp] = x;
     __syncthreads();
     unsigned long long before = 0, all = 0;
 #pragma unroll
@@ -97,7 +102,7 @@ __device__ __forceinline__ Share attend_share(const KvAttendArgs& a, unsigned lo
       if (i < warp) before += s_warp[i];
       all += s_warp[i];
     }
-    s_scan[threadIdx.x] = before + x - n;
+    if (counts) s_scan[threadIdx.x] = before + x - n;
     if (threadIdx.x == 0) s_scan[kThreads] = all;
     __syncthreads();
   };
@@ -164,6 +169,9 @@ __device__ __forceinline__ int attend_share_of(const Share& w, long long u) {
   return (int)(((unsigned long long)(u + 1) * w.shares - 1) / (unsigned long long)w.all);
 }
 
+constexpr float kLow = -3.402823466e38f;  // a running maximum before any key
+constexpr float kSlack = 4.f;  // weights grow to 2^4 before the maximum moves (log2)
+
 // Ancestors of a token as bits: token 0 is the root, token j + 1 node j.
 __device__ __forceinline__ void attend_bits(const int* parents, int token, int words, uint32_t* bits) {
   for (int w = 0; w < words; ++w) bits[w] = 0;
@@ -177,6 +185,60 @@ __device__ __forceinline__ float scale_up(unsigned bits) {
 }
 __device__ __forceinline__ float scale_down(unsigned bits) {
   return __uint_as_float((max(min(bits >> 23, 254u), 8u) - 7u) << 23);
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
+// Codes to fp16.  int8: with its sign bit turned, a code is the low byte of an fp16
+// between 1024 and 1279, and 1152 is taken off exactly.
+template <bool kE4m3>
+struct Code {
+  // the four codes of a word as two pairs
+  static __device__ __forceinline__ void word(uint32_t w, uint32_t& p0, uint32_t& p1) {
+    if constexpr (kE4m3) {
+      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+          : "=r"(p0), "=r"(p1)
+          : "r"(w));
+    } else {
+      const uint32_t x = w ^ 0x80808080u;
+      p0 = less(__byte_perm(x, 0x64646464u, 0x4140));
+      p1 = less(__byte_perm(x, 0x64646464u, 0x4342));
+    }
+  }
+  static __device__ __forceinline__ uint32_t less(uint32_t h) {
+    uint32_t y;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(h), "r"(0x64806480u));
+    return y;
+  }
+};
+
+__device__ __forceinline__ uint4 stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// Eight values in a row, rounded once.
+template <class S>
+__device__ __forceinline__ void attend_store8(S* to, const float (&f)[8]) {
+  if constexpr (sizeof(S) == 4) {
+    ((float4*)to)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    ((float4*)to)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    *(uint4*)to = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 }  // namespace sv

@@ -12,16 +12,12 @@
 #pragma once
 #include "attend_common.cuh"
 
-#include <cuda_fp16.h>
-#include <string.h>
 
 namespace sv {
 
 constexpr int kARThreads = 128;
 constexpr int kARWarps = kARThreads / 32;
 constexpr int kARKeys = 16 * kARWarps;  // keys of a unit: 16 to a warp
-constexpr float kLow = -3.402823466e38f;  // a running maximum before any key
-constexpr float kSlack = 4.f;  // weights grow to 2^4 before the maximum moves (log2)
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -29,50 +25,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-  uint32_t w;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  return w;
-}
 __device__ __forceinline__ float2 floats_of(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 // What is left of two values behind their fp16 parts `w`.
 __device__ __forceinline__ uint32_t rest_of(float lo, float hi, uint32_t w) {
   const float2 f = floats_of(w);
   return half2_of(lo - f.x, hi - f.y);
-}
-
-// Codes to fp16.  int8: with its sign bit turned, a code is the low byte of an fp16
-// between 1024 and 1279, and 1152 is taken off exactly.
-template <bool kE4m3>
-struct Code {
-  // the four codes of a word as two pairs
-  static __device__ __forceinline__ void word(uint32_t w, uint32_t& p0, uint32_t& p1) {
-    if constexpr (kE4m3) {
-      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-          : "=r"(p0), "=r"(p1)
-          : "r"(w));
-    } else {
-      const uint32_t x = w ^ 0x80808080u;
-      p0 = less(__byte_perm(x, 0x64646464u, 0x4140));
-      p1 = less(__byte_perm(x, 0x64646464u, 0x4342));
-    }
-  }
-  static __device__ __forceinline__ uint32_t less(uint32_t h) {
-    uint32_t y;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(h), "r"(0x64806480u));
-    return y;
-  }
-};
-
-__device__ __forceinline__ uint4 stream16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 stream8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
 }
 
 // A lane's place in the products (g = lane / 4, t = lane % 4).  The order in which a
@@ -94,20 +51,6 @@ struct Rows {
            (tree ? (size_t)T * 4 + (size_t)16 * MT * ((T + 31) / 32) * 4 : 0);
   }
 };
-
-// Eight values in a row, rounded once.
-template <class S>
-__device__ __forceinline__ void attend_store8(S* to, const float (&f)[8]) {
-  if constexpr (sizeof(S) == 4) {
-    ((float4*)to)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    ((float4*)to)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-    *(uint4*)to = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
 
 template <class S>
 __device__ __forceinline__ float value_of(S x);
