@@ -5,7 +5,7 @@
 //   S = Q K^T      128 x 128 x D, both operands in shared memory as fp16
 //   P = weights    fp16, over S's columns in tensor memory
 //   O += P V       128 x D x 128, P from tensor memory, V from shared memory
-// Eight warps bring keys and values: codes go from global memory to registers two
+// Eight warps bring keys and eight values: codes go from global memory to registers two
 // units ahead, become fp16 (exactly) and are written to shared memory in the 128-byte
 // swizzle; plain entries become fp16 times a power of two for each key.  Eight warps make weights of
 // scores: a thread has one row and half of the unit's keys, so that rows need no
@@ -24,9 +24,13 @@
 namespace sv {
 
 constexpr int kATRows = 128, kATKeys = 128;
-constexpr int kATSoft = 8, kATLoad = 8;                    // warps of each kind
-constexpr int kATThreads = 32 * (kATSoft + kATLoad + 1);   // and one that issues
-constexpr int kATRing = 4;                                 // units whose scales are held
+constexpr int kATSoft = 8, kATLoad = 8;                        // warps that make weights; that bring keys, and as many values
+constexpr int kATThreads = 32 * (kATSoft + 2 * kATLoad + 4);   // and a group of one that issues and three that look up places
+// Registers of a thread: 72 at the launch, then by kind (896 * 72 = 256 * 96 + 512 * 64 + 128 * 56).
+constexpr int kATSoftRegs = 96, kATLoadRegs = 64, kATIssueRegs = 56;
+static_assert(kATThreads * 72 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * kATLoad * kATLoadRegs + 128 * kATIssueRegs <= kATThreads * 72, "registers");
+constexpr int kATRing = 8;    // units whose places and scales are held
+constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
 constexpr unsigned kATLeastRef = 64;  // values below 2^-82 lose bits, which keeps a row's sum below 2^128
 
 // Shared memory; each operand begins on a 1024-byte boundary, as the swizzle wants.
@@ -38,17 +42,21 @@ struct Tiles {
   static constexpr int kSlot = 128 * DP + 2 * 128;  // floats that a share leaves
   struct Rest {
     float sk[kATRing][kATKeys], sv[kATRing][kATKeys];
+    int at[kATRing][kATKeys];      // a key's entry in its pool, -1: a page outside; the keys of a loading thread side by side
     float qs[kATRows];
     float most[2][2][kATRows];     // [turn][half]
     unsigned top[2][2][kATRows];
     float sum[2][kATRows];
     uint32_t bits[kATRows][4];
     int parents[128];
-    unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], q_full, drain;
+    unsigned long long at_full[kATRing], at_empty[kATRing], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], q_full, drain;
     uint32_t tmem;
     int wrong;
     int meta[4];
   };
+  // Keys that eight loading warps take at once, and where a key's place is held.
+  static constexpr int kAtOnce = 32 * kATLoad / (DP / 16);
+  static __device__ __forceinline__ int place(int key) { return key % kAtOnce * (kATKeys / kAtOnce) + key / kAtOnce; }
   static constexpr size_t smem = kRest + sizeof(Rest) + 1024;
 };
 
@@ -99,11 +107,9 @@ __device__ __forceinline__ void tc_store16(uint32_t at, const uint32_t* r) {
 __device__ __forceinline__ void tc_loaded16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_M8(r, 0), SV_M8(r, 8)::"memory");
 }
-__device__ __forceinline__ void tc_loaded64(uint32_t (&r)[64]) {
+__device__ __forceinline__ void tc_loaded32(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_M8(r, 0), SV_M8(r, 8)::"memory");
   asm volatile("" : SV_M8(r, 16), SV_M8(r, 24));
-  asm volatile("" : SV_M8(r, 32), SV_M8(r, 40));
-  asm volatile("" : SV_M8(r, 48), SV_M8(r, 56));
 }
 __device__ __forceinline__ void tc_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -132,6 +138,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
   typename L::Rest& r = *(typename L::Rest*)(base + L::kRest);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned tries = mbar_tries(spin_limit());
+  constexpr int kIssue = kATSoft + 2 * kATLoad;  // the warp that issues
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
@@ -144,13 +151,17 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
       mbar_init(&r.pv_done[i], 1);
       mbar_init(&r.p_ready[i], kATSoft);
     }
+    for (int i = 0; i < kATRing; ++i) {
+      mbar_init(&r.at_full[i], 1);
+      mbar_init(&r.at_empty[i], 1);
+    }
     mbar_init(&r.q_full, kATSoft);
     mbar_init(&r.drain, 1);
     r.wrong = 0;
     r.meta[0] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kATSoft + kATLoad) {
+  if (warp == kIssue) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&r.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -168,6 +179,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
   };
 
   if (warp < kATSoft) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kATSoftRegs));
     // =====================================================================
     // weights
     // =====================================================================
@@ -260,53 +272,61 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
           const float* sk = r.sk[i & (kATRing - 1)] + 64 * half;
           const float* sv = r.sv[i & (kATRing - 1)] + 64 * half;
           const uint32_t t_s = tmem + 128 * s + 64 * half + lanes;
-          uint32_t x[64];
-          tc_load32(t_s, x);
-          tc_load32(t_s + 32, x + 32);
           const bool codes = u < n_codes;
-          const int first = (codes ? u * kATKeys : keys.stored + (u - n_codes) * kATKeys) + 64 * half;  // the thread's first key
-          const int end = codes ? keys.codes : keys.end;
-          const int unit = first - 64 * half;
+          if (!codes) wait(&r.v_full[s], i >> 1);  // the plain values' scales
+          const int unit = codes ? u * kATKeys : keys.stored + (u - n_codes) * kATKeys, end = codes ? keys.codes : keys.end;
           const bool masked = unit + kATKeys > end || (a.parents ? unit + kATKeys > w.s.len : unit + kATKeys - 1 > first_seen);
           const bool groups = codes && !masked && a.block % 16 == 0;  // 16 keys in a row share their scales
-          float most = -INFINITY;
-          unsigned top = kATLeastRef;
-          tc_loaded64(x);
-          if (groups) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              float y = __uint_as_float(x[16 * g]);
-#pragma unroll
-              for (int k = 1; k < 16; ++k) y = fmaxf(y, __uint_as_float(x[16 * g + k]));
-              most = fmaxf(most, y * sk[16 * g]);
-              const unsigned b = __float_as_uint(sv[16 * g]);
-              if (b < 0x7f800000u) top = max(top, (b >> 23) + 1u);
-            }
-          } else {
-            // the keys that the row sees, as bits
-            uint32_t vis[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int f = first + 32 * k, behind = min(end - f, a.parents ? 32 : last_seen - f + 1);
-              vis[k] = behind <= 0 ? 0u : behind >= 32 ? 0xffffffffu : (1u << behind) - 1u;
-              if (a.parents) {
-                const int at = f - w.s.len;  // the first key as a token of the step
-                if (at > -32) {
-                  const int word = at >> 5;  // -1 .. 3
-                  const uint32_t lo = word < 0 ? 0xffffffffu : word < 4 ? r.bits[row][word] : 0u;
-                  const uint32_t hi = word + 1 < 4 ? r.bits[row][word + 1] : 0u;
-                  vis[k] &= __funnelshift_r(lo, hi, at & 31);
-                }
+          // of 32 keys, those that the row sees
+          auto seen = [&](int c) {
+            if (!masked) return 0xffffffffu;
+            const int f = unit + 64 * half + 32 * c, behind = min(end - f, a.parents ? 32 : last_seen - f + 1);
+            uint32_t vis = behind <= 0 ? 0u : behind >= 32 ? 0xffffffffu : (1u << behind) - 1u;
+            if (a.parents) {
+              const int at = f - w.s.len;  // the first key as a token of the step
+              if (at > -32) {
+                const int word = at >> 5;  // -1 .. 3
+                const uint32_t lo = word < 0 ? 0xffffffffu : word < 4 ? r.bits[row][word] : 0u;
+                const uint32_t hi = word + 1 < 4 ? r.bits[row][word + 1] : 0u;
+                vis &= __funnelshift_r(lo, hi, at & 31);
               }
             }
+            return vis;
+          };
+          // Twice over the thread's 64 scores, 32 in registers at a time (those that came last
+          // stay): the maximum, then the weights.
+          uint32_t x[32];
+          float most = -INFINITY;
+          unsigned top = kATLeastRef;
+          auto exponent = [&](float v) {
+            const unsigned b = __float_as_uint(v);
+            return b < 0x7f800000u ? (b >> 23) + 1u : 0u;  // one that is not finite makes its weights NaN whatever the reference
+          };
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
-              const bool see = (vis[k >> 5] >> (k & 31)) & 1u;
-              const float y = __uint_as_float(x[k]) * sk[k];
-              x[k] = __float_as_uint(see ? y : -INFINITY);
-              most = fmaxf(most, __uint_as_float(x[k]));
-              const unsigned b = __float_as_uint(sv[k]);
-              if (see && b < 0x7f800000u) top = max(top, (b >> 23) + 1u);
+          for (int c = 1; c >= 0; --c) {
+            tc_load32(t_s + 32 * c, x);
+            tc_loaded32(x);
+            if (groups) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                float y = __uint_as_float(x[16 * g]);
+#pragma unroll
+                for (int k = 1; k < 16; ++k) y = fmaxf(y, __uint_as_float(x[16 * g + k]));
+                most = fmaxf(most, y * sk[32 * c + 16 * g]);
+                top = max(top, exponent(sv[32 * c + 16 * g]));
+              }
+            } else {
+              const uint32_t vis = seen(c);
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const float4 y = *(const float4*)(sk + 32 * c + k), v = *(const float4*)(sv + 32 * c + k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (vis >> (k + e) & 1u) {
+                    most = fmaxf(most, __uint_as_float(x[k + e]) * (e == 0 ? y.x : e == 1 ? y.y : e == 2 ? y.z : y.w));
+                    top = max(top, exponent(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w));
+                  }
+              }
             }
           }
           most *= qs;  // (a scale of 0: -inf becomes NaN, which no maximum takes)
@@ -339,33 +359,50 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
               }
             }
           }
+          f2_t sum = 0;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
+            if (c == 1) {
+              tc_load32(t_s + 32, x);
+              tc_loaded32(x);
+            }
             uint32_t p[16];
             if (groups) {
 #pragma unroll
               for (int g = 0; g < 2; ++g) {
                 const float by = sk[32 * c + 16 * g] * qs, v = sv[32 * c + 16 * g];
+                const f2_t by2 = f2(by, by), v2 = f2(v, v), less = f2(-M, -M);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                  const float p0 = ex2(fmaf(__uint_as_float(x[32 * c + 16 * g + 2 * k]), by, -M));
-                  const float p1 = ex2(fmaf(__uint_as_float(x[32 * c + 16 * g + 2 * k + 1]), by, -M));
-                  l += p0 + p1;
-                  p[8 * g + k] = half2_of(p0 * v, p1 * v);
+                  const f2_t y = f2fma(f2(__uint_as_float(x[16 * g + 2 * k]), __uint_as_float(x[16 * g + 2 * k + 1])), by2, less);
+                  const f2_t e = f2(ex2(f2lo(y)), ex2(f2hi(y)));
+                  sum = f2add(sum, e);
+                  const f2_t z = f2mul(e, v2);
+                  p[8 * g + k] = half2_of(f2lo(z), f2hi(z));
                 }
               }
             } else {
+              const uint32_t vis = seen(c);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float x0 = __uint_as_float(x[32 * c + 2 * k]), x1 = __uint_as_float(x[32 * c + 2 * k + 1]);
-                // what is not seen has no part, whatever its scales are
-                const float p0 = x0 == -INFINITY ? 0.f : ex2(fmaf(x0, qs, -M)), p1 = x1 == -INFINITY ? 0.f : ex2(fmaf(x1, qs, -M));
-                l += p0 + p1;
-                p[k] = half2_of(x0 == -INFINITY ? 0.f : p0 * sv[32 * c + 2 * k], x1 == -INFINITY ? 0.f : p1 * sv[32 * c + 2 * k + 1]);
+              for (int k = 0; k < 32; k += 4) {
+                const float4 y = *(const float4*)(sk + 32 * c + k), v = *(const float4*)(sv + 32 * c + k);
+                float z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float by = (e == 0 ? y.x : e == 1 ? y.y : e == 2 ? y.z : y.w) * qs;
+                  // what is not seen has no part, whatever its scales are
+                  const bool see = vis >> (k + e) & 1u;
+                  const float q = see ? ex2(fmaf(__uint_as_float(x[k + e]), by, -M)) : 0.f;
+                  l += q;
+                  z[e] = see ? q * (e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w) : 0.f;
+                }
+                p[k / 2] = half2_of(z[0], z[1]);
+                p[k / 2 + 1] = half2_of(z[2], z[3]);
               }
             }
             tc_store16(t_s + 16 * c, p);
           }
+          l += f2lo(sum) + f2hi(sum);
           tc_stored();
         }
         tc_before();
@@ -418,22 +455,31 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
       }
       attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
     }
-  } else if (warp < kATSoft + kATLoad) {
+  } else if (warp < kIssue) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATLoadRegs));
     // =====================================================================
     // keys and values
     // =====================================================================
-    constexpr int kPer = DP / 16, kAtOnce = 32 * kATLoad / kPer, kRounds = kATKeys / kAtOnce;  // lanes a key, keys at once
-    const int x = threadIdx.x - 32 * kATSoft, part = x % kPer, mine = x / kPer;
+    const bool values = warp >= kATSoft + kATLoad;
+    const int wx = warp - (values ? kATSoft + kATLoad : kATSoft), x = 32 * wx + lane;
+    // Eight lanes in a row write four units of two keys, which the swizzle puts on all
+    // banks; a warp reads whole heads.
+    constexpr int kPer = DP / 16, kAtOnce = L::kAtOnce, kRounds = kATKeys / kAtOnce;  // lanes a key, keys at once
+    const int part = (lane & 3) | (kPer == 8 ? (lane >> 1) & 4 : 0);
+    const int mine = wx * (32 / kPer) + (((lane >> 2) & 1) | (kPer == 8 ? (lane >> 3) & 2 : (lane >> 2) & 6));
     const bool on = 16 * part < a.D;
     const long long entry = (long long)a.Hkv * a.D;
+    unsigned char* operand = base + (values ? L::kV : L::kK);
+    unsigned long long *is_full = values ? r.v_full : r.k_full, *is_empty = values ? r.v_empty : r.k_empty;
+    const int put0 = (part >> 2) * L::kChunk + swizzled(mine, 2 * (part & 3)), put1 = (part >> 2) * L::kChunk + swizzled(mine, 2 * (part & 3) + 1);
     int i = 0;
-    auto wait_empty = [&](unsigned long long* bar) {  // the operand of two units ago has been read
-      if (i >= 2) wait(&bar[i & 1], (i >> 1) + 1);
+    auto wait_empty = [&]() {  // the operand of two units ago has been read
+      if (i >= 2) wait(&is_empty[i & 1], (i >> 1) + 1);
     };
-    auto full = [&](unsigned long long* bar) {
+    auto full = [&]() {
       fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[i & 1]);
+      if (lane == 0) mbar_arrive(&is_full[i & 1]);
     };
     while (w.left > 0) {
       const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
@@ -441,158 +487,123 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
       const Keys keys = attend_keys<kATRows>(a, w.s, w.tile);
       const int n_codes = w.s.bad ? 0 : (keys.codes + kATKeys - 1) / kATKeys, uc = min(u1, n_codes);
       if (u0 < uc) {
-        const int32_t* table = a.code_table + (long long)w.b * a.max_code_pages;
-        const uint8_t* kc = a.k_codes + (long long)w.h * a.D + 16 * part;
-        const uint8_t* vc = a.v_codes + (long long)w.h * a.D + 16 * part;
-        uint4 k[2][kRounds], v[2][kRounds];
-        float scale[2];  // lane `part` has one of the scales of its keys: K's of key part % kRounds, or V's
-        int page[kRounds], at[2][kRounds];
-        auto look = [&](int u) {
-#pragma unroll
-          for (int q = 0; q < kRounds; ++q) page[q] = __ldg(table + fdiv(min(u * kATKeys + mine + q * kAtOnce, keys.codes - 1), a.div_block));
-        };
-        auto place = [&](int u, int b) {  // of the unit that was looked up
-          int p = page[0];
-#pragma unroll
-          for (int q = 0; q < kRounds; ++q) {
-            const int key = min(u * kATKeys + mine + q * kAtOnce, keys.codes - 1), in = key - fdiv(key, a.div_block) * a.block;
-            if (part % kRounds == q) p = page[q];
-            at[b][q] = page[q] >= 0 && page[q] < a.code_pages ? page[q] * a.block + in : 0;
+        const uint8_t* from = (values ? a.v_codes : a.k_codes) + (long long)w.h * a.D + 16 * part;
+        uint4 c[2][kRounds];
+        auto load = [&](int j, int b) {  // unit j of the CTA's
+          wait(&r.at_full[j & (kATRing - 1)], j / kATRing);
+          const int* p = &r.at[j & (kATRing - 1)][mine * kRounds];
+          int at[kRounds];
+          if constexpr (kRounds == 4) {
+            const int4 v = *(const int4*)p;
+            at[0] = v.x, at[1] = v.y, at[2] = v.z, at[3] = v.w;
+          } else {
+            const int2 v = *(const int2*)p;
+            at[0] = v.x, at[1] = v.y;
           }
-          scale[b] = __uint_as_float(0x7fffffffu);
-          if (part < 2 * kRounds) {
-            if (p >= 0 && p < a.code_pages)
-              scale[b] = __ldg((part < kRounds ? a.k_scales : a.v_scales) + (long long)p * a.Hkv + w.h);
-            else
-              atomicOr(a.status, kStatusBadData);
-          }
-        };
-        auto load = [&](const uint8_t* from, const int (&e)[kRounds], uint4 (&to)[kRounds]) {
 #pragma unroll
-          for (int q = 0; q < kRounds; ++q) to[q] = on ? stream16(from + (long long)e[q] * entry) : make_uint4(0, 0, 0, 0);
+          for (int q = 0; q < kRounds; ++q) c[b][q] = on ? stream16(from + max(at[q], 0) * entry) : make_uint4(0, 0, 0, 0);
         };
-        auto put = [&](const uint4 (&from)[kRounds], unsigned char* to) {
-          if (!on) return;
-#pragma unroll
-          for (int q = 0; q < kRounds; ++q) {
-            const int key = mine + q * kAtOnce;
-            uint4 y[2];
-            Code<kE4m3>::word(from[q].x, y[0].x, y[0].y);
-            Code<kE4m3>::word(from[q].y, y[0].z, y[0].w);
-            Code<kE4m3>::word(from[q].z, y[1].x, y[1].y);
-            Code<kE4m3>::word(from[q].w, y[1].z, y[1].w);
-            // eight lanes write eight different units: those of the second chunk their upper one first
-            unsigned char* c = to + (part >> 2) * L::kChunk;
-            const int unit = 2 * (part & 3), up = part >> 2;
-            *(uint4*)(c + swizzled(key, unit + up)) = up ? y[1] : y[0];
-            *(uint4*)(c + swizzled(key, unit + 1 - up)) = up ? y[0] : y[1];
-          }
-        };
-        look(u0);
-        place(u0, 0);
-        load(kc, at[0], k[0]);
-        load(vc, at[0], v[0]);
-        if (u0 + 1 < uc) {
-          look(u0 + 1);
-          place(u0 + 1, 1);
-          load(kc, at[1], k[1]);
-          load(vc, at[1], v[1]);
-          if (u0 + 2 < uc) look(u0 + 2);
-        }
+        load(i, 0);
+        if (u0 + 1 < uc) load(i + 1, 1);
         for (int u = u0; u < uc; u += 2) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             if (u + b >= uc) break;
-            const bool more = u + b + 2 < uc;
-            wait_empty(r.k_empty);
-            put(k[b], base + L::kK + (i & 1) * L::kTile);
-            if (part < 2 * kRounds)
-              (part < kRounds ? r.sk : r.sv)[i & (kATRing - 1)][mine + (part % kRounds) * kAtOnce] = scale[b];
-            if (more) {
-              place(u + b + 2, b);
-              load(kc, at[b], k[b]);
+            wait_empty();
+            unsigned char* to = operand + (i & 1) * L::kTile;
+            if (on) {
+#pragma unroll
+              for (int q = 0; q < kRounds; ++q) {
+                uint4 z[2];
+                Code<kE4m3>::word(c[b][q].x, z[0].x, z[0].y);
+                Code<kE4m3>::word(c[b][q].y, z[0].z, z[0].w);
+                Code<kE4m3>::word(c[b][q].z, z[1].x, z[1].y);
+                Code<kE4m3>::word(c[b][q].w, z[1].z, z[1].w);
+                *(uint4*)(to + put0 + q * kAtOnce * 128) = z[0];
+                *(uint4*)(to + put1 + q * kAtOnce * 128) = z[1];
+              }
             }
-            full(r.k_full);
-            wait_empty(r.v_empty);
-            put(v[b], base + L::kV + (i & 1) * L::kTile);
-            if (more) load(vc, at[b], v[b]);
-            if (u + b + 3 < uc) look(u + b + 3);
-            full(r.v_full);
+            full();
+            if (u + b + 2 < uc) load(i + 2, b);
             ++i;
           }
         }
       }
       // plain entries: twice as many lanes a key, eight values each
       for (int u = max(u0, uc); u < u1; ++u) {
-        constexpr int kPer2 = DP / 8, kAtOnce2 = 32 * kATLoad / kPer2, kRounds2 = kATKeys / kAtOnce2;
+        constexpr int kPer2 = DP / 8, kAtOnce2 = 32 * kATLoad / kPer2, kRounds2 = kATKeys / kAtOnce2, kBatch = 4;
         const int part2 = x % kPer2, mine2 = x / kPer2;
         const bool on2 = 8 * part2 < a.D;
-        int at[kRounds2];
+        wait_empty();
         if (!w.s.bad) {
+          wait(&r.at_full[i & (kATRing - 1)], i / kATRing);
+          const uint16_t* from = (const uint16_t*)(values ? a.v_cache : a.k_cache) + w.h * a.D + 8 * part2;
+          unsigned char* to = operand + (i & 1) * L::kTile + (part2 >> 3) * L::kChunk;
+          float* scales = (values ? r.sv : r.sk)[i & (kATRing - 1)];
+#pragma unroll 1
+          for (int q0 = 0; q0 < kRounds2; q0 += kBatch) {
+            uint4 y[kBatch];
+            bool ok[kBatch];
 #pragma unroll
-          for (int q = 0; q < kRounds2; ++q) {
-            const int key = min(keys.stored + (u - n_codes) * kATKeys + mine2 + q * kAtOnce2, keys.end - 1), p = fdiv(key, a.div_page);
-            const int page = __ldg(a.page_table + (long long)w.b * a.max_pages + p);
-            const bool ok = page >= 0 && page < a.pages;
-            if (!ok) atomicOr(a.status, kStatusBadData);
-            at[q] = ok ? page * a.page_size + (key - p * a.page_size) : -1;
+            for (int q = 0; q < kBatch; ++q) {
+              const int row = mine2 + (q0 + q) * kAtOnce2, at = r.at[i & (kATRing - 1)][L::place(row)];
+              ok[q] = at >= 0;
+              y[q] = on2 && ok[q] ? *(const uint4*)(from + at * entry) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+              const int row = mine2 + (q0 + q) * kAtOnce2;
+              const unsigned lo = max(max(y[q].x & 0x7fffu, y[q].y & 0x7fffu), max(y[q].z & 0x7fffu, y[q].w & 0x7fffu));
+              const unsigned hi = max(max(y[q].x & 0x7fff0000u, y[q].y & 0x7fff0000u), max(y[q].z & 0x7fff0000u, y[q].w & 0x7fff0000u));
+              unsigned top = max(lo << 16, hi);
+#pragma unroll
+              for (int d = 1; d < kPer2; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+              const bool finite = top < 0x7f800000u;
+              const float up = finite ? scale_up(top) : 0.f;
+              if (part2 == 0) scales[row] = ok[q] && finite ? scale_down(top) : __uint_as_float(0x7fffffffu);
+              uint4 z = make_uint4(0, 0, 0, 0);
+              if (finite)
+                z = make_uint4(half2_of(bf16_lo(y[q].x) * up, bf16_hi(y[q].x) * up), half2_of(bf16_lo(y[q].y) * up, bf16_hi(y[q].y) * up),
+                               half2_of(bf16_lo(y[q].z) * up, bf16_hi(y[q].z) * up), half2_of(bf16_lo(y[q].w) * up, bf16_hi(y[q].w) * up));
+              if (on2) *(uint4*)(to + swizzled(row, part2 & 7)) = z;
+            }
           }
         }
-        auto fetch = [&](const void* cache, unsigned char* to, float* scales) {
-          uint4 y[kRounds2];
-#pragma unroll
-          for (int q = 0; q < kRounds2; ++q)
-            y[q] = on2 && at[q] >= 0 ? *(const uint4*)((const uint16_t*)cache + (long long)at[q] * entry + w.h * a.D + 8 * part2)
-                                     : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int q = 0; q < kRounds2; ++q) {
-            const unsigned lo = max(max(y[q].x & 0x7fffu, y[q].y & 0x7fffu), max(y[q].z & 0x7fffu, y[q].w & 0x7fffu));
-            const unsigned hi = max(max(y[q].x & 0x7fff0000u, y[q].y & 0x7fff0000u), max(y[q].z & 0x7fff0000u, y[q].w & 0x7fff0000u));
-            unsigned top = max(lo << 16, hi);
-#pragma unroll
-            for (int d = 1; d < kPer2; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const bool finite = top < 0x7f800000u;
-            const float up = finite ? scale_up(top) : 0.f;
-            if (part2 == 0) scales[mine2 + q * kAtOnce2] = at[q] >= 0 && finite ? scale_down(top) : __uint_as_float(0x7fffffffu);
-            uint4 z = make_uint4(0, 0, 0, 0);
-            if (finite)
-              z = make_uint4(half2_of(bf16_lo(y[q].x) * up, bf16_hi(y[q].x) * up), half2_of(bf16_lo(y[q].y) * up, bf16_hi(y[q].y) * up),
-                             half2_of(bf16_lo(y[q].z) * up, bf16_hi(y[q].z) * up), half2_of(bf16_lo(y[q].w) * up, bf16_hi(y[q].w) * up));
-            if (on2) *(uint4*)(to + (part2 >> 3) * L::kChunk + swizzled(mine2 + q * kAtOnce2, part2 & 7)) = z;
-          }
-        };
-        // the values' scales have to be there with the scores: both are fetched first
-        wait_empty(r.k_empty);
-        if (!w.s.bad) fetch(a.k_cache, base + L::kK + (i & 1) * L::kTile, r.sk[i & (kATRing - 1)]);
-        wait_empty(r.v_empty);
-        if (!w.s.bad) fetch(a.v_cache, base + L::kV + (i & 1) * L::kTile, r.sv[i & (kATRing - 1)]);
-        full(r.k_full);
-        full(r.v_full);
+        full();
         ++i;
       }
       attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATIssueRegs));
+    if (warp == kIssue) {
     // =====================================================================
     // products
     // =====================================================================
-    const uint32_t s_q = smem_addr(base + L::kQ), s_k = smem_addr(base + L::kK), s_v = smem_addr(base + L::kV);
+    // what the products take is the same in all lanes and nearly constant: an issue is
+    // a few instructions (worked out anew for each product it took 100 clocks)
+    const uint32_t t = __shfl_sync(0xffffffffu, tmem, 0);
+    const unsigned long long d_q = tc_operand(__shfl_sync(0xffffffffu, smem_addr(base + L::kQ), 0), 16);
+    const unsigned long long d_k = d_q + ((L::kK - L::kQ) >> 4);
+    const unsigned long long d_v = tc_operand(__shfl_sync(0xffffffffu, smem_addr(base + L::kV), 0), L::kChunk);
+    const int steps = a.D / 16;
     const uint32_t kind_s = tc_kind(128, false), kind_o = tc_kind(a.D, true);
     int i = 0, segments = 0;
     bool open = false;  // unit i - 1 has no P V yet
     bool fresh = false; // ... and begins its segment
     auto pv = [&]() {   // of unit i - 1
-      const int j = i - 1, s = j & 1;
+      const int j = i - 1, s = __shfl_sync(0xffffffffu, j & 1, 0);
       wait(&r.p_ready[s], j >> 1);
       wait(&r.v_full[s], j >> 1);
       tc_after();
       if (lane == 0 && !dead) {
+        const bool add = !fresh;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc_mma_t(t_o, tmem + 128 * s + 64 * (k >> 2) + 8 * (k & 3), tc_operand(s_v + s * L::kTile + k * 2048, L::kChunk), kind_o,
-                   k > 0 || !fresh);
+          tc_mma_t(t + 256, t + 128 * s + 64 * (k >> 2) + 8 * (k & 3), d_v + s * (L::kTile >> 4) + k * (2048 >> 4), kind_o, k > 0 || add);
         tc_commit(&r.v_empty[s]);
         tc_commit(&r.pv_done[s]);
+        tc_commit(&r.at_empty[j & (kATRing - 1)]);  // its places and scales have been used
       }
       __syncwarp();
       open = false;
@@ -601,7 +612,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
       const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
       const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
       for (int u = u0; u < u1; ++u, ++i) {
-        const int s = i & 1;
+        const int s = __shfl_sync(0xffffffffu, i & 1, 0);
         if (u == u0) {  // the last segment's products come to their end, then its queries go
           if (open) pv();
           wait(&r.q_full, segments++);
@@ -611,9 +622,10 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
         if (i >= 2) wait(&r.pv_done[s], (i >> 1) + 1);
         tc_after();
         if (lane == 0 && !dead) {
-          for (int k = 0; k < a.D / 16; ++k) {
-            const uint32_t off = (k >> 2) * L::kChunk + (k & 3) * 32;
-            tc_mma(tmem + 128 * s, tc_operand(s_q + off, 16), tc_operand(s_k + s * L::kTile + off, 16), kind_s, k > 0);
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t off = ((k >> 2) * L::kChunk + (k & 3) * 32) >> 4;
+            if (k < steps) tc_mma(t + 128 * s, d_q + off, d_k + s * (L::kTile >> 4) + off, kind_s, k > 0);
           }
           tc_commit(&r.k_empty[s]);
           tc_commit(&r.s_full[s]);
@@ -631,11 +643,64 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
     if (lane == 0) tc_commit(&r.drain);
     __syncwarp();
     if (!warp_wait(&r.drain, 0, mbar_tries(kSpinLimit))) dead = true;
+    } else {
+      // ===================================================================
+      // places and scales: this warp's units
+      // ===================================================================
+      int i = 0, turn = warp - kIssue - 1;  // units so far; until this warp's next one
+      while (w.left > 0) {
+        const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
+        const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
+        const Keys keys = attend_keys<kATRows>(a, w.s, w.tile);
+        const int n_codes = w.s.bad ? 0 : (keys.codes + kATKeys - 1) / kATKeys;
+        for (int u = u0; u < u1; ++u, ++i) {
+          if (turn-- != 0) continue;
+          turn = kATLook - 1;
+          const int slot = i & (kATRing - 1);
+          const bool codes = u < n_codes;
+          int at[4], page[4];
+          if (!w.s.bad) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // (keys past the end stand for the last one: they are read and not seen)
+              const int k = 32 * q + lane;
+              const int key = codes ? min(u * kATKeys + k, keys.codes - 1) : min(keys.stored + (u - n_codes) * kATKeys + k, keys.end - 1);
+              const int p = fdiv(key, codes ? a.div_block : a.div_page);
+              at[q] = key - p * (codes ? a.block : a.page_size);
+              page[q] = codes ? __ldg(a.code_table + (long long)w.b * a.max_code_pages + p) : __ldg(a.page_table + (long long)w.b * a.max_pages + p);
+            }
+          }
+          if (i >= kATRing) wait(&r.at_empty[slot], i / kATRing + 1);
+          if (!w.s.bad) {
+            float sk[4], sv[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const bool ok = page[q] >= 0 && page[q] < (codes ? a.code_pages : a.pages);
+              if (!ok) atomicOr(a.status, kStatusBadData);
+              at[q] = ok ? page[q] * (codes ? a.block : a.page_size) + at[q] : -1;
+              sk[q] = sv[q] = __uint_as_float(0x7fffffffu);
+              if (codes && ok) {
+                sk[q] = __ldg(a.k_scales + (long long)page[q] * a.Hkv + w.h);
+                sv[q] = __ldg(a.v_scales + (long long)page[q] * a.Hkv + w.h);
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int k = 32 * q + lane;
+              r.at[slot][L::place(k)] = at[q];
+              if (codes) r.sk[slot][k] = sk[q], r.sv[slot][k] = sv[q];
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&r.at_full[slot]);
+        }
+        attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
+      }
+    }
   }
   if (dead && lane == 0) atomicOr(a.status, kStatusTimeout);
   tc_before();
   __syncthreads();
-  if (warp == kATSoft + kATLoad) {
+  if (warp == kIssue) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
