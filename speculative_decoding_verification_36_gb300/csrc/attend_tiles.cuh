@@ -1,17 +1,17 @@
 // attend_tiles.cuh -- attention of a step's tokens to a cache whose older blocks are
 // 8-bit codes: many rows a head of keys, on the tensor cores of the SM (tcgen05).
 //
-// One CTA an SM takes tiles of 128 rows and units of 128 keys:
-//   S = Q K^T      128 x 128 x D, both operands in shared memory as fp16
+// A CTA takes tiles of 128 rows and units of 64 keys:
+//   S = Q K^T      128 x 64 x D, both operands in shared memory as fp16
 //   P = weights    fp16, over S's columns in tensor memory
-//   O += P V       128 x D x 128, P from tensor memory, V from shared memory
-// Eight warps bring keys and eight values: codes go from global memory to registers two
+//   O += P V       128 x D x 64, P from tensor memory, V from shared memory
+// Four warps bring keys and four values: codes go from global memory to registers two
 // units ahead, become fp16 (exactly) and are written to shared memory in the 128-byte
-// swizzle; plain entries become fp16 times a power of two for each key.  Eight warps make weights of
-// scores: a thread has one row and half of the unit's keys, so that rows need no
-// shuffles and two threads agree on a row's maximum through shared memory.  One thread
-// issues the products; S is double-buffered, so that the next scores are computed
-// while the weights of the last ones are made.
+// swizzle; plain entries become fp16 times a power of two for each key.  Three warps look the
+// entries' places and scales up further ahead.  Four warps make weights of scores: a
+// thread has one row, so that rows need no shuffles.  One thread issues the products; S
+// is double-buffered, so that the next scores are computed while the weights of the
+// last ones are made.  Two CTAs share an SM: what one waits for, the other uses.
 //
 // The scales never touch the codes: a key's scale multiplies its scores, a value's its
 // weight.  With M = m + ref - 138 (m the running maximum in log2, ref exponent bits above every
@@ -23,12 +23,14 @@
 
 namespace sv {
 
-constexpr int kATRows = 128, kATKeys = 128;
-constexpr int kATSoft = 8, kATLoad = 8;                        // warps that make weights; that bring keys, and as many values
+constexpr int kATRows = 128, kATKeys = 64;
+constexpr int kATSoft = 4, kATLoad = 4;                        // warps that make weights; that bring keys, and as many values
 constexpr int kATThreads = 32 * (kATSoft + 2 * kATLoad + 4);   // and a group of one that issues and three that look up places
-// Registers of a thread: 72 at the launch, then by kind (896 * 72 = 256 * 96 + 512 * 64 + 128 * 56).
-constexpr int kATSoftRegs = 96, kATLoadRegs = 64, kATIssueRegs = 56;
-static_assert(kATThreads * 72 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * kATLoad * kATLoadRegs + 128 * kATIssueRegs <= kATThreads * 72, "registers");
+constexpr int kATCtas = 2;                                     // of an SM
+// Registers of a thread: 64 at the launch, then by kind (512 * 64 = 128 * 96 + 256 * 56 + 128 * 48).
+constexpr int kATSoftRegs = 96, kATLoadRegs = 56, kATIssueRegs = 48;
+static_assert(kATCtas * kATThreads * 64 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * kATLoad * kATLoadRegs + 128 * kATIssueRegs <= kATThreads * 64,
+              "registers");
 constexpr int kATRing = 8;    // units whose places and scales are held
 constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
 constexpr unsigned kATLeastRef = 64;  // values below 2^-82 lose bits, which keeps a row's sum below 2^128
@@ -36,17 +38,15 @@ constexpr unsigned kATLeastRef = 64;  // values below 2^-82 lose bits, which kee
 // Shared memory; each operand begins on a 1024-byte boundary, as the swizzle wants.
 template <int DP>
 struct Tiles {
-  static constexpr int kTile = 128 * DP * 2;  // bytes of an operand
-  static constexpr int kChunk = 128 * 128;    // 128 rows of 64 fp16
-  static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kRest = 5 * kTile;
+  static constexpr int kTile = kATKeys * DP * 2;    // bytes of a unit's keys or values
+  static constexpr int kChunk = kATKeys * 128;      // its rows of 64 fp16
+  static constexpr int kQChunk = kATRows * 128;     // the queries'
+  static constexpr int kQ = 0, kK = kATRows * DP * 2, kV = kK + 2 * kTile, kRest = kV + 2 * kTile;
   static constexpr int kSlot = 128 * DP + 2 * 128;  // floats that a share leaves
   struct Rest {
     float sk[kATRing][kATKeys], sv[kATRing][kATKeys];
     int at[kATRing][kATKeys];      // a key's entry in its pool, -1: a page outside; the keys of a loading thread side by side
     float qs[kATRows];
-    float most[2][2][kATRows];     // [turn][half]
-    unsigned top[2][2][kATRows];
-    float sum[2][kATRows];
     uint32_t bits[kATRows][4];
     int parents[128];
     unsigned long long at_full[kATRing], at_empty[kATRing], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], q_full, drain;
@@ -63,6 +63,11 @@ struct Tiles {
 // ---- tcgen05 ----
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
 __device__ __forceinline__ void tc_commit(unsigned long long* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -130,13 +135,13 @@ __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("ba
 __device__ __forceinline__ int swizzled(int row, int u) { return row * 128 + ((u ^ (row & 7)) << 4); }
 
 template <bool kE4m3, int DP>
-__global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __grid_constant__ KvAttendArgs a) {
+__global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const __grid_constant__ KvAttendArgs a) {
   using L = Tiles<DP>;
   extern __shared__ unsigned char s_raw[];
   __shared__ unsigned long long s_scan[512 + 1];
   unsigned char* base = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
   typename L::Rest& r = *(typename L::Rest*)(base + L::kRest);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const unsigned tries = mbar_tries(spin_limit());
   constexpr int kIssue = kATSoft + 2 * kATLoad;  // the warp that issues
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssue) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&r.tmem)) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_addr(&r.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   Share w = attend_share<512, kATRows, kATKeys>(a, s_scan);
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
   __syncthreads();
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&r.tmem;
-  const uint32_t t_o = tmem + 256;  // S at 0 and 128, O at 256
+  const uint32_t t_o = tmem + 128;  // S at 0 and 64, O at 128
   // Once a wait has run out the warp goes on without waiting and takes part in every
   // barrier that is left: no warp waits for one that is gone.
   bool dead = false;
@@ -183,12 +188,11 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
     // =====================================================================
     // weights
     // =====================================================================
-    const int half = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
-    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    int i = 0, turn = 0;  // units so far; exchanges so far
+    const int row = 32 * warp + lane;
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    int i = 0;  // units so far
     int loaded_b = -1, loaded_tile = -1;
     bool bad = false;
-    auto both = [&]() { bar_sync(1 + quarter, 64); };  // the two warps of these rows
     while (w.left > 0) {
       const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
       const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
               if (finite)
                 y = make_uint2(half2_of(bf16_lo(x[k].x) * up, bf16_hi(x[k].x) * up), half2_of(bf16_lo(x[k].y) * up, bf16_hi(x[k].y) * up));
               const int d = 4 * lane;
-              *(uint2*)(base + L::kQ + (d >> 6) * L::kChunk + swizzled(q, (d & 63) >> 3) + (d & 4) * 2) = y;
+              *(uint2*)(base + L::kQ + (d >> 6) * L::kQChunk + swizzled(q, (d & 63) >> 3) + (d & 4) * 2) = y;
             }
           }
         }
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
         if (lane == 0) mbar_arrive(&r.q_full);
       }
       const float qs = r.qs[row];
-      const bool active = 32 * quarter < rows - row0;
+      const bool active = 32 * warp < rows - row0;
       const int last_seen = w.s.len + fdiv(row0 + row, a.div_g), first_seen = w.s.len + fdiv(row0, a.div_g);
       float m = kLow, M = kLow, l = 0.f;
       unsigned ref = kATLeastRef;
@@ -269,9 +273,8 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
         wait(&r.s_full[s], i >> 1);
         tc_after();
         if (active && !w.s.bad) {
-          const float* sk = r.sk[i & (kATRing - 1)] + 64 * half;
-          const float* sv = r.sv[i & (kATRing - 1)] + 64 * half;
-          const uint32_t t_s = tmem + 128 * s + 64 * half + lanes;
+          const float *sk = r.sk[i & (kATRing - 1)], *sv = r.sv[i & (kATRing - 1)];
+          const uint32_t t_s = tmem + 64 * s + lanes;
           const bool codes = u < n_codes;
           if (!codes) wait(&r.v_full[s], i >> 1);  // the plain values' scales
           const int unit = codes ? u * kATKeys : keys.stored + (u - n_codes) * kATKeys, end = codes ? keys.codes : keys.end;
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
           // of 32 keys, those that the row sees
           auto seen = [&](int c) {
             if (!masked) return 0xffffffffu;
-            const int f = unit + 64 * half + 32 * c, behind = min(end - f, a.parents ? 32 : last_seen - f + 1);
+            const int f = unit + 32 * c, behind = min(end - f, a.parents ? 32 : last_seen - f + 1);
             uint32_t vis = behind <= 0 ? 0u : behind >= 32 ? 0xffffffffu : (1u << behind) - 1u;
             if (a.parents) {
               const int at = f - w.s.len;  // the first key as a token of the step
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
             }
             return vis;
           };
-          // Twice over the thread's 64 scores, 32 in registers at a time (those that came last
+          // Twice over the row's 64 scores, 32 in registers at a time (those that came last
           // stay): the maximum, then the weights.
           uint32_t x[32];
           float most = -INFINITY;
@@ -331,12 +334,6 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
           }
           most *= qs;  // (a scale of 0: -inf becomes NaN, which no maximum takes)
           top = min(top, 254u);
-          r.most[turn & 1][half][row] = most;
-          r.top[turn & 1][half][row] = top;
-          both();
-          most = fmaxf(most, r.most[turn & 1][half ^ 1][row]);
-          top = max(top, r.top[turn & 1][half ^ 1][row]);
-          ++turn;
           if (__any_sync(0xffffffffu, most > m + kSlack || top > ref)) {
             m = fmaxf(m, most);
             ref = max(ref, top);
@@ -348,9 +345,9 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
               wait(&r.pv_done[j & 1], j >> 1);
               tc_after();
 #pragma unroll 1
-              for (int c = 0; c < DP / 2; c += 16) {
+              for (int c = 0; c < DP; c += 16) {
                 uint32_t o[16];
-                const uint32_t at = t_o + lanes + half * (DP / 2) + c;
+                const uint32_t at = t_o + lanes + c;
                 tc_load16(at, o);
                 tc_loaded16(o);
 #pragma unroll
@@ -415,17 +412,13 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
       tc_after();
       if (active) {
         if (lost) l = __uint_as_float(0x7fffffffu);
-        both();
-        r.sum[half][row] = l;
-        both();
-        l += r.sum[half ^ 1][row];
         const bool whole = u0 == 0 && u1 == n, mine = row0 + row < rows;
         const float by = l == 0.f ? 0.f : 1.f / l;
         const int token = fdiv(row0 + row, a.div_g);
         uint16_t* out = (uint16_t*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + row - token * a.G) * a.D;
         float* part = a.part + (2LL * blockIdx.x + (u0 == 0)) * L::kSlot;
 #pragma unroll 1
-        for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 16) {
+        for (int c = 0; c < DP; c += 16) {
           uint32_t o[16];
           tc_load16(t_o + lanes + c, o);
           tc_loaded16(o);
@@ -446,7 +439,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
           }
           __syncwarp();
         }
-        if (!whole && half == 0 && mine) part[128 * DP + row] = M, part[128 * DP + 128 + row] = l;
+        if (!whole && mine) part[128 * DP + row] = M, part[128 * DP + 128 + row] = l;
       }
       tc_before();
       if (u0 == 0 && u1 < n && threadIdx.x == 0) {
@@ -577,72 +570,73 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATIssueRegs));
     if (warp == kIssue) {
-    // =====================================================================
-    // products
-    // =====================================================================
-    // what the products take is the same in all lanes and nearly constant: an issue is
-    // a few instructions (worked out anew for each product it took 100 clocks)
-    const uint32_t t = __shfl_sync(0xffffffffu, tmem, 0);
-    const unsigned long long d_q = tc_operand(__shfl_sync(0xffffffffu, smem_addr(base + L::kQ), 0), 16);
-    const unsigned long long d_k = d_q + ((L::kK - L::kQ) >> 4);
-    const unsigned long long d_v = tc_operand(__shfl_sync(0xffffffffu, smem_addr(base + L::kV), 0), L::kChunk);
-    const int steps = a.D / 16;
-    const uint32_t kind_s = tc_kind(128, false), kind_o = tc_kind(a.D, true);
-    int i = 0, segments = 0;
-    bool open = false;  // unit i - 1 has no P V yet
-    bool fresh = false; // ... and begins its segment
-    auto pv = [&]() {   // of unit i - 1
-      const int j = i - 1, s = __shfl_sync(0xffffffffu, j & 1, 0);
-      wait(&r.p_ready[s], j >> 1);
-      wait(&r.v_full[s], j >> 1);
-      tc_after();
-      if (lane == 0 && !dead) {
-        const bool add = !fresh;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_t(t + 256, t + 128 * s + 64 * (k >> 2) + 8 * (k & 3), d_v + s * (L::kTile >> 4) + k * (2048 >> 4), kind_o, k > 0 || add);
-        tc_commit(&r.v_empty[s]);
-        tc_commit(&r.pv_done[s]);
-        tc_commit(&r.at_empty[j & (kATRing - 1)]);  // its places and scales have been used
-      }
-      __syncwarp();
-      open = false;
-    };
-    while (w.left > 0) {
-      const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
-      const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
-      for (int u = u0; u < u1; ++u, ++i) {
-        const int s = __shfl_sync(0xffffffffu, i & 1, 0);
-        if (u == u0) {  // the last segment's products come to their end, then its queries go
-          if (open) pv();
-          wait(&r.q_full, segments++);
-        }
-        // S's columns hold the weights of unit i - 2 until P V has read them
-        wait(&r.k_full[s], i >> 1);
-        if (i >= 2) wait(&r.pv_done[s], (i >> 1) + 1);
+      // ===================================================================
+      // products
+      // ===================================================================
+      // The warp walks along together and its elected lane issues: what the products take is
+      // then known to be the same in all lanes (an issue under `lane == 0` took 100 clocks,
+      // 64 being the product's own time).
+      const bool leader = tc_elect();
+      const unsigned long long d_q = tc_operand(smem_addr(base + L::kQ), 16), d_k = tc_operand(smem_addr(base + L::kK), 16);
+      const unsigned long long d_v = tc_operand(smem_addr(base + L::kV), L::kChunk);
+      const uint32_t kind_s = tc_kind(kATKeys, false), kind_o = tc_kind(a.D, true);
+      const int steps = a.D / 16;
+      int i = 0, segments = 0;
+      bool open = false;   // unit i - 1 has no P V yet
+      bool fresh = false;  // ... and begins its segment
+      auto pv = [&]() {    // of unit i - 1
+        const int j = i - 1, s = j & 1;
+        wait(&r.p_ready[s], j >> 1);
+        wait(&r.v_full[s], j >> 1);
         tc_after();
-        if (lane == 0 && !dead) {
+        if (leader && !dead) {
+          const unsigned long long d = d_v + s * (L::kTile >> 4);
+          const bool add = !fresh;
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint32_t off = ((k >> 2) * L::kChunk + (k & 3) * 32) >> 4;
-            if (k < steps) tc_mma(t + 128 * s, d_q + off, d_k + s * (L::kTile >> 4) + off, kind_s, k > 0);
-          }
-          tc_commit(&r.k_empty[s]);
-          tc_commit(&r.s_full[s]);
-          mbar_arrive(&r.s_full[s]);  // with what k_full brought: the scales
+          for (int k = 0; k < kATKeys / 16; ++k) tc_mma_t(t_o, tmem + 64 * s + 8 * k, d + k * (2048 >> 4), kind_o, k > 0 || add);
+          tc_commit(&r.v_empty[s]);
+          tc_commit(&r.pv_done[s]);
+          tc_commit(&r.at_empty[j & (kATRing - 1)]);  // its places and scales have been used
         }
         __syncwarp();
-        if (open) pv();
-        open = true;
-        fresh = u == u0;
+        open = false;
+      };
+      while (w.left > 0) {
+        const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
+        const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
+        for (int u = u0; u < u1; ++u, ++i) {
+          const int s = i & 1;
+          if (u == u0) {  // the last segment's products come to their end, then its queries go
+            if (open) pv();
+            wait(&r.q_full, segments++);
+          }
+          // S's columns hold the weights of unit i - 2 until P V has read them
+          wait(&r.k_full[s], i >> 1);
+          if (i >= 2) wait(&r.pv_done[s], (i >> 1) + 1);
+          tc_after();
+          if (leader && !dead) {
+            const unsigned long long d = d_k + s * (L::kTile >> 4);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+              if (k < steps)
+                tc_mma(tmem + 64 * s, d_q + (((k >> 2) * L::kQChunk + (k & 3) * 32) >> 4), d + (((k >> 2) * L::kChunk + (k & 3) * 32) >> 4), kind_s,
+                       k > 0);
+            tc_commit(&r.k_empty[s]);
+            tc_commit(&r.s_full[s]);
+            mbar_arrive(&r.s_full[s]);  // with what k_full brought: the scales
+          }
+          __syncwarp();
+          if (open) pv();
+          open = true;
+          fresh = u == u0;
+        }
+        attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
       }
-      attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
-    }
-    if (open) pv();
-    // nothing of the tensor cores is in flight when the tensor memory goes back
-    if (lane == 0) tc_commit(&r.drain);
-    __syncwarp();
-    if (!warp_wait(&r.drain, 0, mbar_tries(kSpinLimit))) dead = true;
+      if (open) pv();
+      // nothing of the tensor cores is in flight when the tensor memory goes back
+      if (leader) tc_commit(&r.drain);
+      __syncwarp();
+      if (!warp_wait(&r.drain, 0, mbar_tries(kSpinLimit))) dead = true;
     } else {
       // ===================================================================
       // places and scales: this warp's units
@@ -658,10 +652,11 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
           turn = kATLook - 1;
           const int slot = i & (kATRing - 1);
           const bool codes = u < n_codes;
-          int at[4], page[4];
+          constexpr int kQ = kATKeys / 32;
+          int at[kQ], page[kQ];
           if (!w.s.bad) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // (keys past the end stand for the last one: they are read and not seen)
+            for (int q = 0; q < kQ; ++q) {  // (keys past the end stand for the last one: they are read and not seen)
               const int k = 32 * q + lane;
               const int key = codes ? min(u * kATKeys + k, keys.codes - 1) : min(keys.stored + (u - n_codes) * kATKeys + k, keys.end - 1);
               const int p = fdiv(key, codes ? a.div_block : a.div_page);
@@ -671,9 +666,9 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
           }
           if (i >= kATRing) wait(&r.at_empty[slot], i / kATRing + 1);
           if (!w.s.bad) {
-            float sk[4], sv[4];
+            float sk[kQ], sv[kQ];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kQ; ++q) {
               const bool ok = page[q] >= 0 && page[q] < (codes ? a.code_pages : a.pages);
               if (!ok) atomicOr(a.status, kStatusBadData);
               at[q] = ok ? page[q] * (codes ? a.block : a.page_size) + at[q] : -1;
@@ -684,7 +679,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
               }
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kQ; ++q) {
               const int k = 32 * q + lane;
               r.at[slot][L::place(k)] = at[q];
               if (codes) r.sk[slot][k] = sk[q], r.sv[slot][k] = sv[q];
@@ -702,7 +697,7 @@ __global__ void __launch_bounds__(kATThreads, 1) attend_tiles_kernel(const __gri
   __syncthreads();
   if (warp == kIssue) {
     tc_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");
   }
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(r.meta[0], r.meta[1], r.meta[2], r.meta[3]);
 }
@@ -751,7 +746,7 @@ static cudaError_t launch_tiles(KvAttendArgs a, int sms, size_t* bytes, cudaStre
   a.tiles = (int)(((long long)a.T * a.G + kATRows - 1) / kATRows);
   const long long keys = (long long)a.max_code_pages * a.block + (long long)a.max_pages * a.page_size;
   const double most = (double)a.B * a.Hkv * a.tiles * (double)(keys / kATKeys + 2);
-  const int grid = (int)fmin((double)sms, most);
+  const int grid = (int)fmin((double)sms * kATCtas, most);
   const size_t slots = ((size_t)grid * 2 * L::kSlot * 4 + 255) / 256 * 256;
   if (bytes) {
     *bytes = slots + (size_t)grid * sizeof(int4);
