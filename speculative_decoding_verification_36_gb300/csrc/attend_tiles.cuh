@@ -27,11 +27,12 @@ constexpr int kATRows = 128, kATKeys = 64;
 constexpr int kATSoft = 4, kATLoad = 4;                        // warps that make weights; that bring keys, and as many values
 constexpr int kATThreads = 32 * (kATSoft + 2 * kATLoad + 4);   // and a group of one that issues and three that look up places
 constexpr int kATCtas = 2;                                     // of an SM
-// Registers of a thread: 64 at the launch, then by kind (512 * 64 = 128 * 96 + 256 * 56 + 128 * 48).
-constexpr int kATSoftRegs = 96, kATLoadRegs = 56, kATIssueRegs = 48;
+// Registers of a thread: 64 at the launch, then by kind (512 * 64 = 128 * 80 + 256 * 64 + 128 * 48).
+constexpr int kATSoftRegs = 80, kATLoadRegs = 64, kATIssueRegs = 48;
 static_assert(kATCtas * kATThreads * 64 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * kATLoad * kATLoadRegs + 128 * kATIssueRegs <= kATThreads * 64,
               "registers");
 constexpr int kATRing = 8;    // units whose places and scales are held
+constexpr int kATCodes = 0, kATPlain = 1, kATNone = 2;  // kinds of units (log2 of a value's bytes); the last: a bad sequence's
 constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
 constexpr unsigned kATLeastRef = 64;  // values below 2^-82 lose bits, which keeps a row's sum below 2^128
 
@@ -45,13 +46,17 @@ struct Tiles {
   static constexpr int kSlot = 128 * DP + 2 * 128;  // floats that a share leaves
   struct Rest {
     float sk[kATRing][kATKeys], sv[kATRing][kATKeys];
-    int at[kATRing][kATKeys];      // a key's entry in its pool, -1: a page outside; the keys of a loading thread side by side
+    int kind[kATRing];
+    unsigned at[kATRing][kATKeys];   // where a key's head lies in its pool, in 16 bytes (0: a page outside); the keys of a loading thread side by side
+    unsigned outside[kATRing][kATKeys / 32];  // keys whose page is outside, as bits
+    unsigned top[kATRing];         // exponent bits above a unit's scales of V
     float qs[kATRows];
     uint32_t bits[kATRows][4];
     int parents[128];
     unsigned long long at_full[kATRing], at_empty[kATRing], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], q_full, drain;
     uint32_t tmem;
     int wrong;
+    volatile unsigned tries;  // of a wait, 0 once one has run out
     int meta[4];
   };
   // Keys that eight loading warps take at once, and where a key's place is held.
@@ -112,10 +117,6 @@ __device__ __forceinline__ void tc_store16(uint32_t at, const uint32_t* r) {
 __device__ __forceinline__ void tc_loaded16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_M8(r, 0), SV_M8(r, 8)::"memory");
 }
-__device__ __forceinline__ void tc_loaded32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_M8(r, 0), SV_M8(r, 8)::"memory");
-  asm volatile("" : SV_M8(r, 16), SV_M8(r, 24));
-}
 __device__ __forceinline__ void tc_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // An operand of 128-byte rows in the 128-byte swizzle: groups of 8 rows 1024 bytes
@@ -129,7 +130,15 @@ __device__ __forceinline__ constexpr uint32_t tc_kind(int n, bool by_rows) {
   return 1u << 4 | (by_rows ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
 }
 
+__device__ __forceinline__ void mbar_arrive_n(unsigned long long* bar, unsigned n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+}
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+template <int k>
+struct Kind {
+  static constexpr int value = k;
+};
 
 // Where 16 bytes (unit u of 8 in a 128-byte row) of a row lie.
 __device__ __forceinline__ int swizzled(int row, int u) { return row * 128 + ((u ^ (row & 7)) << 4); }
@@ -142,7 +151,6 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   unsigned char* base = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
   typename L::Rest& r = *(typename L::Rest*)(base + L::kRest);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-  const unsigned tries = mbar_tries(spin_limit());
   constexpr int kIssue = kATSoft + 2 * kATLoad;  // the warp that issues
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -163,6 +171,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     mbar_init(&r.q_full, kATSoft);
     mbar_init(&r.drain, 1);
     r.wrong = 0;
+    r.tries = mbar_tries(spin_limit());
     r.meta[0] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -176,11 +185,13 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&r.tmem;
   const uint32_t t_o = tmem + 128;  // S at 0 and 64, O at 128
-  // Once a wait has run out the warp goes on without waiting and takes part in every
+  // Once a wait has run out all warps go on without waiting and take part in every
   // barrier that is left: no warp waits for one that is gone.
-  bool dead = false;
   auto wait = [&](unsigned long long* bar, unsigned parity) {
-    if (!dead && !warp_wait(bar, parity & 1, tries)) dead = true;
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return;
+    for (unsigned n = __reduce_min_sync(0xffffffffu, r.tries); n > 0; --n)
+      if (__all_sync(0xffffffffu, mbar_try(bar, parity & 1))) return;
+    r.tries = 0;
   };
 
   if (warp < kATSoft) {
@@ -220,42 +231,42 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
       const bool lost = w.s.bad || (a.parents && bad);
       if (lost && threadIdx.x == 0) atomicOr(a.status, kStatusBadData);
       {
-        // a warp a row, a lane four values in a row; eight rows in flight
-        const bool fast = ((uintptr_t)a.q & 7) == 0 && a.q_stride % 4 == 0;
-        const int live = min(kATRows, rows - row0);
-        for (int r0 = warp; r0 < live; r0 += 8 * kATSoft) {
-          uint2 x[8];
+        // 16 lanes a row, eight values a lane; 16 rows of a warp in flight
+        const bool fast = ((uintptr_t)a.q & 15) == 0 && a.q_stride % 8 == 0;
+        const int live = min(kATRows, rows - row0), d = 8 * (lane & 15);
+        for (int r0 = 2 * warp; r0 < live; r0 += 16 * kATSoft) {
+          uint4 x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int q = r0 + k * kATSoft;
-            x[k] = make_uint2(0, 0);
-            if (q < live && 4 * lane < a.D && !lost) {
+            const int q = r0 + 2 * kATSoft * k + (lane >> 4);
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (q < live && d < a.D && !lost) {
               const int token = fdiv(row0 + q, a.div_g);
               const uint16_t* p = (const uint16_t*)a.q + ((long long)w.b * a.T + token) * a.q_stride +
-                                  ((long long)w.h * a.G + row0 + q - token * a.G) * a.D + 4 * lane;
+                                  ((long long)w.h * a.G + row0 + q - token * a.G) * a.D + d;
               if (fast)
-                x[k] = *(const uint2*)p;
+                x[k] = __ldg((const uint4*)p);
               else
-                x[k] = make_uint2(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16);
+                x[k] = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
             }
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int q = r0 + k * kATSoft;
-            if (q >= live) break;
-            unsigned top = max(max(x[k].x << 16 & 0x7fff0000u, x[k].x & 0x7fff0000u), max(x[k].y << 16 & 0x7fff0000u, x[k].y & 0x7fff0000u));
-            top = __reduce_max_sync(0xffffffffu, top);
+            const int q = r0 + 2 * kATSoft * k + (lane >> 4);
+            const unsigned lo = max(max(x[k].x & 0x7fffu, x[k].y & 0x7fffu), max(x[k].z & 0x7fffu, x[k].w & 0x7fffu));
+            const unsigned hi = max(max(x[k].x & 0x7fff0000u, x[k].y & 0x7fff0000u), max(x[k].z & 0x7fff0000u, x[k].w & 0x7fff0000u));
+            unsigned top = max(lo << 16, hi);
+#pragma unroll
+            for (int e = 1; e < 16; e *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, e));
+            if (q >= live) continue;
             const bool finite = top < 0x7f800000u;
             // the scale's sign goes with the query: what multiplies the scores is positive
-            const float up = !finite ? 0.f : a.scale < 0.f ? -scale_up(top) : scale_up(top);
-            if (lane == 0) r.qs[q] = lost || !finite ? __uint_as_float(0x7fffffffu) : scale_down(top) * fabsf(a.scale);
-            if (4 * lane < a.D) {
-              uint2 y = make_uint2(0, 0);
-              if (finite)
-                y = make_uint2(half2_of(bf16_lo(x[k].x) * up, bf16_hi(x[k].x) * up), half2_of(bf16_lo(x[k].y) * up, bf16_hi(x[k].y) * up));
-              const int d = 4 * lane;
-              *(uint2*)(base + L::kQ + (d >> 6) * L::kQChunk + swizzled(q, (d & 63) >> 3) + (d & 4) * 2) = y;
-            }
+            const float up = a.scale < 0.f ? -scale_up(top) : scale_up(top);
+            if ((lane & 15) == 0) r.qs[q] = lost || !finite ? __uint_as_float(0x7fffffffu) : scale_down(top) * fabsf(a.scale);
+            auto two = [&](uint32_t v) { return finite ? half2_of(bf16_lo(v) * up, bf16_hi(v) * up) : 0u; };
+            if (d < a.D)
+              *(uint4*)(base + L::kQ + (d >> 6) * L::kQChunk + swizzled(q, (d & 63) >> 3)) =
+                  make_uint4(two(x[k].x), two(x[k].y), two(x[k].z), two(x[k].w));
           }
         }
         fence_async();
@@ -263,80 +274,28 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         if (lane == 0) mbar_arrive(&r.q_full);
       }
       const float qs = r.qs[row];
-      const bool active = 32 * warp < rows - row0;
+      const bool active = 32 * warp < rows - row0, mine = row0 + row < rows;
       const int last_seen = w.s.len + fdiv(row0 + row, a.div_g), first_seen = w.s.len + fdiv(row0, a.div_g);
       float m = kLow, M = kLow, l = 0.f;
       unsigned ref = kATLeastRef;
       const int n_codes = w.s.bad ? 0 : (keys.codes + kATKeys - 1) / kATKeys;
-      for (int u = u0; u < u1; ++u, ++i) {
+      // units of codes that every row sees whole and whose keys share their scales by 16
+      const int u_groups = w.s.bad || a.block % 16 ? 0 : min(keys.codes, a.parents ? w.s.len : first_seen + 1) / kATKeys;
+      // warps without rows stay away: the first arrives for them
+      const unsigned arrivals = warp ? 1u : 1u + kATSoft - min(kATSoft, (rows - row0 + 31) / 32);
+      if (!active) i += u1 - u0;
+      for (int u = active ? u0 : u1; u < u1; ++u, ++i) {
         const int s = i & 1;
         wait(&r.s_full[s], i >> 1);
         tc_after();
-        if (active && !w.s.bad) {
-          const float *sk = r.sk[i & (kATRing - 1)], *sv = r.sv[i & (kATRing - 1)];
+        if (!w.s.bad) {
+          const int slot = i & (kATRing - 1);
+          const float *sk = r.sk[slot], *sv = r.sv[slot];
           const uint32_t t_s = tmem + 64 * s + lanes;
-          const bool codes = u < n_codes;
-          if (!codes) wait(&r.v_full[s], i >> 1);  // the plain values' scales
-          const int unit = codes ? u * kATKeys : keys.stored + (u - n_codes) * kATKeys, end = codes ? keys.codes : keys.end;
-          const bool masked = unit + kATKeys > end || (a.parents ? unit + kATKeys > w.s.len : unit + kATKeys - 1 > first_seen);
-          const bool groups = codes && !masked && a.block % 16 == 0;  // 16 keys in a row share their scales
-          // of 32 keys, those that the row sees
-          auto seen = [&](int c) {
-            if (!masked) return 0xffffffffu;
-            const int f = unit + 32 * c, behind = min(end - f, a.parents ? 32 : last_seen - f + 1);
-            uint32_t vis = behind <= 0 ? 0u : behind >= 32 ? 0xffffffffu : (1u << behind) - 1u;
-            if (a.parents) {
-              const int at = f - w.s.len;  // the first key as a token of the step
-              if (at > -32) {
-                const int word = at >> 5;  // -1 .. 3
-                const uint32_t lo = word < 0 ? 0xffffffffu : word < 4 ? r.bits[row][word] : 0u;
-                const uint32_t hi = word + 1 < 4 ? r.bits[row][word + 1] : 0u;
-                vis &= __funnelshift_r(lo, hi, at & 31);
-              }
-            }
-            return vis;
-          };
-          // Twice over the row's 64 scores, 32 in registers at a time (those that came last
-          // stay): the maximum, then the weights.
-          uint32_t x[32];
-          float most = -INFINITY;
-          unsigned top = kATLeastRef;
-          auto exponent = [&](float v) {
-            const unsigned b = __float_as_uint(v);
-            return b < 0x7f800000u ? (b >> 23) + 1u : 0u;  // one that is not finite makes its weights NaN whatever the reference
-          };
-#pragma unroll
-          for (int c = 1; c >= 0; --c) {
-            tc_load32(t_s + 32 * c, x);
-            tc_loaded32(x);
-            if (groups) {
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                float y = __uint_as_float(x[16 * g]);
-#pragma unroll
-                for (int k = 1; k < 16; ++k) y = fmaxf(y, __uint_as_float(x[16 * g + k]));
-                most = fmaxf(most, y * sk[32 * c + 16 * g]);
-                top = max(top, exponent(sv[32 * c + 16 * g]));
-              }
-            } else {
-              const uint32_t vis = seen(c);
-#pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const float4 y = *(const float4*)(sk + 32 * c + k), v = *(const float4*)(sv + 32 * c + k);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (vis >> (k + e) & 1u) {
-                    most = fmaxf(most, __uint_as_float(x[k + e]) * (e == 0 ? y.x : e == 1 ? y.y : e == 2 ? y.z : y.w));
-                    top = max(top, exponent(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w));
-                  }
-              }
-            }
-          }
-          most *= qs;  // (a scale of 0: -inf becomes NaN, which no maximum takes)
-          top = min(top, 254u);
-          if (__any_sync(0xffffffffu, most > m + kSlack || top > ref)) {
+          // the maximum moves, and with it the sums: to a score of at least `most` (log2) and exponent bits `top`
+          auto move = [&](float most, unsigned top) {
             m = fmaxf(m, most);
-            ref = max(ref, top);
+            ref = max(ref, min(top, 254u));
             const float M2 = m + ((float)ref - 138.f), f = ex2(M - M2);
             M = M2;
             l *= f;
@@ -355,64 +314,117 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
                 tc_store16(at, o);
               }
             }
-          }
-          f2_t sum = 0;
+          };
+          // Scores to weights under the maximum as it is; where one of the warp's rows has
+          // outgrown it, it moves and the scores, which are still there, are taken again.
+          // Kind 0: 16 keys share their scales; 1: each key has its own; 2: and some rows do not see some.
+          auto weigh = [&](auto kind_, uint32_t vis0, uint32_t vis1) {
+            constexpr int kKind = decltype(kind_)::value;
+            uint32_t p[32];
+            f2_t sum0, sum1;
+            for (bool again = false;; again = true) {
+              uint32_t x[2][16];  // the next 16 come while these are taken
+              tc_load16(t_s, x[0]);
+              unsigned top = kKind < 2 ? r.top[slot] : 0u;
+              float most0 = -INFINITY, most1 = -INFINITY;  // of the exponents
+              sum0 = sum1 = 0;
+              const f2_t less = f2(-M, -M);
+              tc_loaded16(x[0]);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (c == 1) {
-              tc_load32(t_s + 32, x);
-              tc_loaded32(x);
-            }
-            uint32_t p[16];
-            if (groups) {
+              for (int g = 0; g < 4; ++g) {
+                if (g < 3) tc_load16(t_s + 16 * (g + 1), x[(g + 1) & 1]);
+                float b = 0.f, v = 0.f;
+                if constexpr (kKind == 0) b = sk[16 * g] * qs, v = sv[16 * g];
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const float by = sk[32 * c + 16 * g] * qs, v = sv[32 * c + 16 * g];
-                const f2_t by2 = f2(by, by), v2 = f2(v, v), less = f2(-M, -M);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const f2_t y = f2fma(f2(__uint_as_float(x[16 * g + 2 * k]), __uint_as_float(x[16 * g + 2 * k + 1])), by2, less);
-                  const f2_t e = f2(ex2(f2lo(y)), ex2(f2hi(y)));
-                  sum = f2add(sum, e);
-                  const f2_t z = f2mul(e, v2);
-                  p[8 * g + k] = half2_of(f2lo(z), f2hi(z));
+                for (int k = 0; k < 16; k += 4) {
+                  const uint32_t(&z)[16] = x[g & 1];
+                  float4 b4 = make_float4(b, b, b, b), v4 = make_float4(v, v, v, v);
+                  if constexpr (kKind > 0) {
+                    b4 = *(const float4*)(sk + 16 * g + k), v4 = *(const float4*)(sv + 16 * g + k);
+                    b4 = make_float4(b4.x * qs, b4.y * qs, b4.z * qs, b4.w * qs);
+                  }
+                  f2_t y0 = f2fma(f2(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), f2(b4.x, b4.y), less);
+                  f2_t y1 = f2fma(f2(__uint_as_float(z[k + 2]), __uint_as_float(z[k + 3])), f2(b4.z, b4.w), less);
+                  if constexpr (kKind == 2) {
+                    const uint32_t vis = g < 2 ? vis0 : vis1;
+                    const int e = 16 * (g & 1) + k;
+                    const bool s0 = vis >> e & 1u, s1 = vis >> (e + 1) & 1u, s2 = vis >> (e + 2) & 1u, s3 = vis >> (e + 3) & 1u;
+                    y0 = f2(s0 ? f2lo(y0) : -INFINITY, s1 ? f2hi(y0) : -INFINITY);
+                    y1 = f2(s2 ? f2lo(y1) : -INFINITY, s3 ? f2hi(y1) : -INFINITY);
+                    // what is not seen has no part, whatever its scales are
+                    v4 = make_float4(s0 ? v4.x : 0.f, s1 ? v4.y : 0.f, s2 ? v4.z : 0.f, s3 ? v4.w : 0.f);
+                    top = max(max(max(top, __float_as_uint(v4.x)), max(__float_as_uint(v4.y), __float_as_uint(v4.z))), __float_as_uint(v4.w));
+                  }
+                  most0 = fmaxf(most0, fmaxf(f2lo(y0), f2hi(y0)));
+                  most1 = fmaxf(most1, fmaxf(f2lo(y1), f2hi(y1)));
+                  const f2_t e0 = f2(ex2(f2lo(y0)), ex2(f2hi(y0))), e1 = f2(ex2(f2lo(y1)), ex2(f2hi(y1)));
+                  sum0 = f2add(sum0, e0);
+                  sum1 = f2add(sum1, e1);
+                  const f2_t z0 = f2mul(e0, f2(v4.x, v4.y)), z1 = f2mul(e1, f2(v4.z, v4.w));
+                  p[8 * g + k / 2] = half2_of(f2lo(z0), f2hi(z0));
+                  p[8 * g + k / 2 + 1] = half2_of(f2lo(z1), f2hi(z1));
                 }
+                if (g < 3) tc_loaded16(x[(g + 1) & 1]);
               }
+              // (a scale that is not finite makes its weights NaN whatever the reference)
+              if constexpr (kKind == 2) top = top < 0x7f800000u ? (top >> 23) + 1u : 0u;
+              // (rows past the last hold anything; a score that is infinite outgrows every maximum)
+              if (again || !__any_sync(0xffffffffu, mine && (fmaxf(most0, most1) > kSlack + 138.f - (float)ref || top > ref))) break;
+              float most = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t z[16];
+                tc_load16(t_s + 16 * c, z);
+                tc_loaded16(z);
+                const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1));
+#pragma unroll
+                for (int k = 0; k < 16; ++k) most = fmaxf(most, vis >> k & 1u ? __uint_as_float(z[k]) * sk[16 * c + k] : -INFINITY);
+              }
+              move(most * qs, top);  // (a scale of 0: -inf becomes NaN, which no maximum takes)
+            }
+            sum0 = f2add(sum0, sum1);
+            l += f2lo(sum0) + f2hi(sum0);
+            tc_store16(t_s, p);
+            tc_store16(t_s + 16, p + 16);
+          };
+          if (u < u_groups) {
+            weigh(Kind<0>(), 0xffffffffu, 0xffffffffu);
+          } else {
+            const bool codes = u < n_codes;
+            if (!codes) wait(&r.v_full[s], i >> 1);  // the plain values' scales
+            const int unit = codes ? u * kATKeys : keys.stored + (u - n_codes) * kATKeys, end = codes ? keys.codes : keys.end;
+            if (unit + kATKeys > end || (a.parents ? unit + kATKeys > w.s.len : unit + kATKeys - 1 > first_seen)) {
+              // of 32 keys, those that the row sees
+              auto seen = [&](int f) {
+                const int behind = min(end - f, a.parents ? 32 : last_seen - f + 1);
+                uint32_t vis = behind <= 0 ? 0u : behind >= 32 ? 0xffffffffu : (1u << behind) - 1u;
+                const int at = f - w.s.len;  // the first key as a token of the step
+                if (a.parents && at > -32) {
+                  const int word = at >> 5;  // -1 .. 3
+                  const uint32_t lo = word < 0 ? 0xffffffffu : word < 4 ? r.bits[row][word] : 0u;
+                  const uint32_t hi = word + 1 < 4 ? r.bits[row][word + 1] : 0u;
+                  vis &= __funnelshift_r(lo, hi, at & 31);
+                }
+                return vis;
+              };
+              weigh(Kind<2>(), seen(unit), seen(unit + 32));
             } else {
-              const uint32_t vis = seen(c);
-#pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const float4 y = *(const float4*)(sk + 32 * c + k), v = *(const float4*)(sv + 32 * c + k);
-                float z[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float by = (e == 0 ? y.x : e == 1 ? y.y : e == 2 ? y.z : y.w) * qs;
-                  // what is not seen has no part, whatever its scales are
-                  const bool see = vis >> (k + e) & 1u;
-                  const float q = see ? ex2(fmaf(__uint_as_float(x[k + e]), by, -M)) : 0.f;
-                  l += q;
-                  z[e] = see ? q * (e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w) : 0.f;
-                }
-                p[k / 2] = half2_of(z[0], z[1]);
-                p[k / 2 + 1] = half2_of(z[2], z[3]);
-              }
+              weigh(Kind<1>(), 0xffffffffu, 0xffffffffu);
             }
-            tc_store16(t_s + 16 * c, p);
           }
-          l += f2lo(sum) + f2hi(sum);
           tc_stored();
         }
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&r.p_ready[s]);
+        if (lane == 0) mbar_arrive_n(&r.p_ready[s], arrivals);
       }
       // ---- out, or to the workspace ----
-      const int j = i - 1;
-      wait(&r.pv_done[j & 1], j >> 1);
-      tc_after();
       if (active) {
+        const int j = i - 1;
+        wait(&r.pv_done[j & 1], j >> 1);
+        tc_after();
         if (lost) l = __uint_as_float(0x7fffffffu);
-        const bool whole = u0 == 0 && u1 == n, mine = row0 + row < rows;
+        const bool whole = u0 == 0 && u1 == n;
         const float by = l == 0.f ? 0.f : 1.f / l;
         const int token = fdiv(row0 + row, a.div_g);
         uint16_t* out = (uint16_t*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + row - token * a.G) * a.D;
@@ -454,118 +466,109 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     // keys and values
     // =====================================================================
     const bool values = warp >= kATSoft + kATLoad;
-    const int wx = warp - (values ? kATSoft + kATLoad : kATSoft), x = 32 * wx + lane;
+    const int wx = warp - (values ? kATSoft + kATLoad : kATSoft);
     // Eight lanes in a row write four units of two keys, which the swizzle puts on all
     // banks; a warp reads whole heads.
     constexpr int kPer = DP / 16, kAtOnce = L::kAtOnce, kRounds = kATKeys / kAtOnce;  // lanes a key, keys at once
     const int part = (lane & 3) | (kPer == 8 ? (lane >> 1) & 4 : 0);
     const int mine = wx * (32 / kPer) + (((lane >> 2) & 1) | (kPer == 8 ? (lane >> 3) & 2 : (lane >> 2) & 6));
     const bool on = 16 * part < a.D;
-    const long long entry = (long long)a.Hkv * a.D;
     unsigned char* operand = base + (values ? L::kV : L::kK);
     unsigned long long *is_full = values ? r.v_full : r.k_full, *is_empty = values ? r.v_empty : r.k_empty;
     const int put0 = (part >> 2) * L::kChunk + swizzled(mine, 2 * (part & 3)), put1 = (part >> 2) * L::kChunk + swizzled(mine, 2 * (part & 3) + 1);
-    int i = 0;
-    auto wait_empty = [&]() {  // the operand of two units ago has been read
-      if (i >= 2) wait(&is_empty[i & 1], (i >> 1) + 1);
+    const int units = (int)w.left;
+    uint4 c[2][kRounds];  // of the next two units: 16 codes of each key, or the first 8 of 16 plain values
+    // (Registers are scarce here: a spilled one would come back from L2, for L1 is small beside
+    // this much shared memory.)
+    auto places = [&](int slot, unsigned (&at)[kRounds]) {
+      const unsigned* p = &r.at[slot][mine * kRounds];
+      if constexpr (kRounds == 4) {
+        const uint4 v = *(const uint4*)p;
+        at[0] = v.x, at[1] = v.y, at[2] = v.z, at[3] = v.w;
+      } else {
+        const uint2 v = *(const uint2*)p;
+        at[0] = v.x, at[1] = v.y;
+      }
     };
-    auto full = [&]() {
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&is_full[i & 1]);
+    const unsigned part_of = on ? 16 * part : 0;  // (lanes past the head read its first values again)
+    auto pool = [&](int kind) {
+      return (kind == kATPlain ? (const char*)(values ? a.v_cache : a.k_cache) : (const char*)(values ? a.v_codes : a.k_codes)) + (part_of << kind);
     };
-    while (w.left > 0) {
-      const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
-      const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
-      const Keys keys = attend_keys<kATRows>(a, w.s, w.tile);
-      const int n_codes = w.s.bad ? 0 : (keys.codes + kATKeys - 1) / kATKeys, uc = min(u1, n_codes);
-      if (u0 < uc) {
-        const uint8_t* from = (values ? a.v_codes : a.k_codes) + (long long)w.h * a.D + 16 * part;
-        uint4 c[2][kRounds];
-        auto load = [&](int j, int b) {  // unit j of the CTA's
-          wait(&r.at_full[j & (kATRing - 1)], j / kATRing);
-          const int* p = &r.at[j & (kATRing - 1)][mine * kRounds];
-          int at[kRounds];
-          if constexpr (kRounds == 4) {
-            const int4 v = *(const int4*)p;
-            at[0] = v.x, at[1] = v.y, at[2] = v.z, at[3] = v.w;
-          } else {
-            const int2 v = *(const int2*)p;
-            at[0] = v.x, at[1] = v.y;
+    auto load = [&](int j, uint4 (&to)[kRounds]) {
+      const int slot = j & (kATRing - 1);
+      wait(&r.at_full[slot], j / kATRing);
+      const int kind = r.kind[slot];
+      // one load whatever the kind: where two paths met, their values would have to be there
+      const char* from = pool(kind == kATPlain ? kATPlain : kATCodes);
+      unsigned at[kRounds];
+      places(slot, at);
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q) to[q] = stream16(from + at[q] * 16ull);
+    };
+    if (units > 0) load(0, c[0]);
+    if (units > 1) load(1, c[1]);
+    for (int i0 = 0; i0 < units; i0 += 2) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int i = i0 + b, slot = i & (kATRing - 1);
+        if (i >= units) break;
+        const int kind = r.kind[slot];
+        unsigned char* to = operand + b * L::kTile;
+        if (i >= 2) wait(&is_empty[b], (i >> 1) + 1);  // the operand of two units ago has been read
+        if (kind == kATCodes) {
+          if (on) {
+#pragma unroll
+            for (int q = 0; q < kRounds; ++q) {
+              uint4 z[2];
+              Code<kE4m3>::word(c[b][q].x, z[0].x, z[0].y);
+              Code<kE4m3>::word(c[b][q].y, z[0].z, z[0].w);
+              Code<kE4m3>::word(c[b][q].z, z[1].x, z[1].y);
+              Code<kE4m3>::word(c[b][q].w, z[1].z, z[1].w);
+              *(uint4*)(to + put0 + q * kAtOnce * 128) = z[0];
+              *(uint4*)(to + put1 + q * kAtOnce * 128) = z[1];
+            }
           }
+        } else if (kind == kATPlain) {
+          float* scales = (values ? r.sv : r.sk)[slot];
+          const char* from = pool(kATPlain) + 16;
+          unsigned at[kRounds];
+          places(slot, at);
 #pragma unroll
-          for (int q = 0; q < kRounds; ++q) c[b][q] = on ? stream16(from + max(at[q], 0) * entry) : make_uint4(0, 0, 0, 0);
-        };
-        load(i, 0);
-        if (u0 + 1 < uc) load(i + 1, 1);
-        for (int u = u0; u < uc; u += 2) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (u + b >= uc) break;
-            wait_empty();
-            unsigned char* to = operand + (i & 1) * L::kTile;
+          for (int q = 0; q < kRounds; ++q) {
+            // the other 8 values came into L2 with the first: they share a sector
+            const int key = mine + q * kAtOnce;
+            const bool in = !(r.outside[slot][key >> 5] >> (key & 31) & 1u);
+            const uint4 other = stream16(from + at[q] * 16ull);
+            const uint4 y = on && in ? c[b][q] : make_uint4(0, 0, 0, 0), z = on && in ? other : make_uint4(0, 0, 0, 0);
+            const unsigned lo = max(max(max(y.x & 0x7fffu, y.y & 0x7fffu), max(y.z & 0x7fffu, y.w & 0x7fffu)),
+                                    max(max(z.x & 0x7fffu, z.y & 0x7fffu), max(z.z & 0x7fffu, z.w & 0x7fffu)));
+            const unsigned hi = max(max(max(y.x & 0x7fff0000u, y.y & 0x7fff0000u), max(y.z & 0x7fff0000u, y.w & 0x7fff0000u)),
+                                    max(max(z.x & 0x7fff0000u, z.y & 0x7fff0000u), max(z.z & 0x7fff0000u, z.w & 0x7fff0000u)));
+            unsigned top = max(lo << 16, hi);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (kPer == 8) top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            const bool finite = top < 0x7f800000u;
+            const float down = in && finite ? scale_down(top) : __uint_as_float(0x7fffffffu);
+            if (part == 0) scales[key] = down;
+            if (values) {
+              const unsigned above = __reduce_max_sync(0xffffffffu, in && finite ? (__float_as_uint(down) >> 23) + 1u : 0u);
+              if (lane == 0) atomicMax(&r.top[slot], above);
+            }
+            const float up = finite ? scale_up(top) : 0.f;
+            auto two = [&](uint32_t v) { return finite ? half2_of(bf16_lo(v) * up, bf16_hi(v) * up) : 0u; };
             if (on) {
-#pragma unroll
-              for (int q = 0; q < kRounds; ++q) {
-                uint4 z[2];
-                Code<kE4m3>::word(c[b][q].x, z[0].x, z[0].y);
-                Code<kE4m3>::word(c[b][q].y, z[0].z, z[0].w);
-                Code<kE4m3>::word(c[b][q].z, z[1].x, z[1].y);
-                Code<kE4m3>::word(c[b][q].w, z[1].z, z[1].w);
-                *(uint4*)(to + put0 + q * kAtOnce * 128) = z[0];
-                *(uint4*)(to + put1 + q * kAtOnce * 128) = z[1];
-              }
+              *(uint4*)(to + put0 + q * kAtOnce * 128) = make_uint4(two(y.x), two(y.y), two(y.z), two(y.w));
+              *(uint4*)(to + put1 + q * kAtOnce * 128) = make_uint4(two(z.x), two(z.y), two(z.z), two(z.w));
             }
-            full();
-            if (u + b + 2 < uc) load(i + 2, b);
-            ++i;
+            if (q % 2) asm volatile("" ::: "memory");  // two keys at a time
           }
         }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&is_full[b]);
+        if (i + 2 < units) load(i + 2, c[b]);
       }
-      // plain entries: twice as many lanes a key, eight values each
-      for (int u = max(u0, uc); u < u1; ++u) {
-        constexpr int kPer2 = DP / 8, kAtOnce2 = 32 * kATLoad / kPer2, kRounds2 = kATKeys / kAtOnce2, kBatch = 4;
-        const int part2 = x % kPer2, mine2 = x / kPer2;
-        const bool on2 = 8 * part2 < a.D;
-        wait_empty();
-        if (!w.s.bad) {
-          wait(&r.at_full[i & (kATRing - 1)], i / kATRing);
-          const uint16_t* from = (const uint16_t*)(values ? a.v_cache : a.k_cache) + w.h * a.D + 8 * part2;
-          unsigned char* to = operand + (i & 1) * L::kTile + (part2 >> 3) * L::kChunk;
-          float* scales = (values ? r.sv : r.sk)[i & (kATRing - 1)];
-#pragma unroll 1
-          for (int q0 = 0; q0 < kRounds2; q0 += kBatch) {
-            uint4 y[kBatch];
-            bool ok[kBatch];
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-              const int row = mine2 + (q0 + q) * kAtOnce2, at = r.at[i & (kATRing - 1)][L::place(row)];
-              ok[q] = at >= 0;
-              y[q] = on2 && ok[q] ? *(const uint4*)(from + at * entry) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-              const int row = mine2 + (q0 + q) * kAtOnce2;
-              const unsigned lo = max(max(y[q].x & 0x7fffu, y[q].y & 0x7fffu), max(y[q].z & 0x7fffu, y[q].w & 0x7fffu));
-              const unsigned hi = max(max(y[q].x & 0x7fff0000u, y[q].y & 0x7fff0000u), max(y[q].z & 0x7fff0000u, y[q].w & 0x7fff0000u));
-              unsigned top = max(lo << 16, hi);
-#pragma unroll
-              for (int d = 1; d < kPer2; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-              const bool finite = top < 0x7f800000u;
-              const float up = finite ? scale_up(top) : 0.f;
-              if (part2 == 0) scales[row] = ok[q] && finite ? scale_down(top) : __uint_as_float(0x7fffffffu);
-              uint4 z = make_uint4(0, 0, 0, 0);
-              if (finite)
-                z = make_uint4(half2_of(bf16_lo(y[q].x) * up, bf16_hi(y[q].x) * up), half2_of(bf16_lo(y[q].y) * up, bf16_hi(y[q].y) * up),
-                               half2_of(bf16_lo(y[q].z) * up, bf16_hi(y[q].z) * up), half2_of(bf16_lo(y[q].w) * up, bf16_hi(y[q].w) * up));
-              if (on2) *(uint4*)(to + swizzled(row, part2 & 7)) = z;
-            }
-          }
-        }
-        full();
-        ++i;
-      }
-      attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATIssueRegs));
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         wait(&r.p_ready[s], j >> 1);
         wait(&r.v_full[s], j >> 1);
         tc_after();
-        if (leader && !dead) {
+        if (leader) {
           const unsigned long long d = d_v + s * (L::kTile >> 4);
           const bool add = !fresh;
 #pragma unroll
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
           wait(&r.k_full[s], i >> 1);
           if (i >= 2) wait(&r.pv_done[s], (i >> 1) + 1);
           tc_after();
-          if (leader && !dead) {
+          if (leader) {
             const unsigned long long d = d_k + s * (L::kTile >> 4);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k)
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
       // nothing of the tensor cores is in flight when the tensor memory goes back
       if (leader) tc_commit(&r.drain);
       __syncwarp();
-      if (!warp_wait(&r.drain, 0, mbar_tries(kSpinLimit))) dead = true;
+      if (!warp_wait(&r.drain, 0, mbar_tries(kSpinLimit))) r.tries = 0;
     } else {
       // ===================================================================
       // places and scales: this warp's units
@@ -667,6 +670,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
           if (i >= kATRing) wait(&r.at_empty[slot], i / kATRing + 1);
           if (!w.s.bad) {
             float sk[kQ], sv[kQ];
+            unsigned top = 0;
 #pragma unroll
             for (int q = 0; q < kQ; ++q) {
               const bool ok = page[q] >= 0 && page[q] < (codes ? a.code_pages : a.pages);
@@ -679,12 +683,23 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
               }
             }
 #pragma unroll
+            for (int q = 0; q < kQ; ++q)
+              if (__float_as_uint(sv[q]) < 0x7f800000u) top = max(top, (__float_as_uint(sv[q]) >> 23) + 1u);
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) r.top[slot] = top;
+#pragma unroll
             for (int q = 0; q < kQ; ++q) {
               const int k = 32 * q + lane;
-              r.at[slot][L::place(k)] = at[q];
+              r.at[slot][L::place(k)] = at[q] < 0 ? 0u : (unsigned)((((long long)at[q] * a.Hkv + w.h) * a.D >> 4) << (codes ? 0 : 1));
+              const unsigned out = __ballot_sync(0xffffffffu, at[q] < 0);
+              if (lane == 0) r.outside[slot][q] = out;
               if (codes) r.sk[slot][k] = sk[q], r.sv[slot][k] = sv[q];
             }
           }
+          if (w.s.bad)
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) r.at[slot][32 * q + lane] = 0;
+          if (lane == 0) r.kind[slot] = w.s.bad ? kATNone : codes ? kATCodes : kATPlain;
           __syncwarp();
           if (lane == 0) mbar_arrive(&r.at_full[slot]);
         }
@@ -692,9 +707,9 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
       }
     }
   }
-  if (dead && lane == 0) atomicOr(a.status, kStatusTimeout);
   tc_before();
   __syncthreads();
+  if (threadIdx.x == 0 && r.tries == 0) atomicOr(a.status, kStatusTimeout);
   if (warp == kIssue) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");

@@ -385,6 +385,7 @@ cudaError_t launch_attend_rows_f32_int8(const KvAttendArgs& a, int sms, size_t* 
 cudaError_t launch_attend_rows_f32_e4m3(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
 // Tiles of 128 rows on the tensor cores: bf16, D <= 128, trees of up to 128 tokens.
 constexpr int kAttendTilesMaxD = 128, kAttendTilesMaxTree = 128;
+constexpr unsigned long long kAttendTilesMaxPool = 1ull << 36;  // bytes: places are 32 bits of 16
 cudaError_t launch_attend_tiles_int8(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
 cudaError_t launch_attend_tiles_e4m3(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
 cudaError_t attend_tiles_int8_set_spin_limit(unsigned n);
