@@ -2,16 +2,16 @@
 // 8-bit codes: many rows a head of keys, on the tensor cores of the SM (tcgen05).
 //
 // A CTA takes tiles of 128 rows and units of 64 keys:
-//   S = Q K^T      128 x 64 x D, both operands in shared memory as fp16
+//   S = Q K^T      128 x 64 x D, Q from tensor memory, K from shared memory, both fp16
 //   P = weights    fp16, over S's columns in tensor memory
 //   O += P V       128 x D x 64, P from tensor memory, V from shared memory
 // Four warps bring keys and four values: codes go from global memory to registers two
 // units ahead, become fp16 (exactly) and are written to shared memory in the 128-byte
 // swizzle; plain entries become fp16 times a power of two for each key.  Three warps look the
 // entries' places and scales up further ahead.  Four warps make weights of scores: a
-// thread has one row, so that rows need no shuffles.  One thread issues the products; S
-// is double-buffered, so that the next scores are computed while the weights of the
-// last ones are made.  Two CTAs share an SM: what one waits for, the other uses.
+// thread has one row, so that rows need no shuffles.  One thread issues the products.
+// Two CTAs share an SM: while one waits for its weights, the other's products run, and what
+// is left to be shared is shared memory's bandwidth: 512 bytes a key and head written, 512 read.
 //
 // The scales never touch the codes: a key's scale multiplies its scores, a value's its
 // weight.  With M = m + ref - 138 (m the running maximum in log2, ref exponent bits above every
@@ -31,6 +31,7 @@ constexpr int kATCtas = 2;                                     // of an SM
 constexpr int kATSoftRegs = 80, kATLoadRegs = 64, kATIssueRegs = 48;
 static_assert(kATCtas * kATThreads * 64 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * kATLoad * kATLoadRegs + 128 * kATIssueRegs <= kATThreads * 64,
               "registers");
+constexpr int kATStages = 2;  // units whose keys and values are in shared memory
 constexpr int kATRing = 8;    // units whose places and scales are held
 constexpr int kATCodes = 0, kATPlain = 1, kATNone = 2;  // kinds of units (log2 of a value's bytes); the last: a bad sequence's
 constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
@@ -41,8 +42,7 @@ template <int DP>
 struct Tiles {
   static constexpr int kTile = kATKeys * DP * 2;    // bytes of a unit's keys or values
   static constexpr int kChunk = kATKeys * 128;      // its rows of 64 fp16
-  static constexpr int kQChunk = kATRows * 128;     // the queries'
-  static constexpr int kQ = 0, kK = kATRows * DP * 2, kV = kK + 2 * kTile, kRest = kV + 2 * kTile;
+  static constexpr int kK = 0, kV = kATStages * kTile, kRest = 2 * kATStages * kTile;
   static constexpr int kSlot = 128 * DP + 2 * 128;  // floats that a share leaves
   struct Rest {
     float sk[kATRing][kATKeys], sv[kATRing][kATKeys];
@@ -50,10 +50,10 @@ struct Tiles {
     unsigned at[kATRing][kATKeys];   // where a key's head lies in its pool, in 16 bytes (0: a page outside); the keys of a loading thread side by side
     unsigned outside[kATRing][kATKeys / 32];  // keys whose page is outside, as bits
     unsigned top[kATRing];         // exponent bits above a unit's scales of V
-    float qs[kATRows];
     uint32_t bits[kATRows][4];
     int parents[128];
-    unsigned long long at_full[kATRing], at_empty[kATRing], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], q_full, drain;
+    unsigned long long at_full[kATRing], at_empty[kATRing], k_full[kATStages], k_empty[kATStages], v_full[kATStages],
+        v_empty[kATStages], s_full, p_ready, pv_done, q_full, drain;
     uint32_t tmem;
     int wrong;
     volatile unsigned tries;  // of a wait, 0 once one has run out
@@ -76,15 +76,7 @@ __device__ __forceinline__ bool tc_elect() {
 __device__ __forceinline__ void tc_commit(unsigned long long* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// D = A B (+ D), A in shared memory
-__device__ __forceinline__ void tc_mma(uint32_t d, unsigned long long a, unsigned long long b, uint32_t kind, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
-      : "memory");
-}
-// ... A in tensor memory
+// D = A B (+ D), A in tensor memory
 __device__ __forceinline__ void tc_mma_t(uint32_t d, uint32_t a, unsigned long long b, uint32_t kind, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
@@ -117,6 +109,9 @@ __device__ __forceinline__ void tc_store16(uint32_t at, const uint32_t* r) {
 __device__ __forceinline__ void tc_loaded16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_M8(r, 0), SV_M8(r, 8)::"memory");
 }
+__device__ __forceinline__ void tc_store8(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::SV_W8(r, 0), "r"(at) : "memory");
+}
 __device__ __forceinline__ void tc_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // An operand of 128-byte rows in the 128-byte swizzle: groups of 8 rows 1024 bytes
@@ -135,11 +130,6 @@ __device__ __forceinline__ void mbar_arrive_n(unsigned long long* bar, unsigned 
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-template <int k>
-struct Kind {
-  static constexpr int value = k;
-};
-
 // Where 16 bytes (unit u of 8 in a 128-byte row) of a row lie.
 __device__ __forceinline__ int swizzled(int row, int u) { return row * 128 + ((u ^ (row & 7)) << 4); }
 
@@ -155,15 +145,15 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kATStages; ++i) {
       mbar_init(&r.k_full[i], kATLoad);
       mbar_init(&r.v_full[i], kATLoad);
       mbar_init(&r.k_empty[i], 1);
       mbar_init(&r.v_empty[i], 1);
-      mbar_init(&r.s_full[i], 2);
-      mbar_init(&r.pv_done[i], 1);
-      mbar_init(&r.p_ready[i], kATSoft);
     }
+    mbar_init(&r.s_full, 2);
+    mbar_init(&r.pv_done, 1);
+    mbar_init(&r.p_ready, kATSoft);
     for (int i = 0; i < kATRing; ++i) {
       mbar_init(&r.at_full[i], 1);
       mbar_init(&r.at_empty[i], 1);
@@ -184,7 +174,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   __syncthreads();
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&r.tmem;
-  const uint32_t t_o = tmem + 128;  // S at 0 and 64, O at 128
+  const uint32_t t_q = tmem + 64, t_o = tmem + 128;  // S, then its weights, at 0
   // Once a wait has run out all warps go on without waiting and take part in every
   // barrier that is left: no warp waits for one that is gone.
   auto wait = [&](unsigned long long* bar, unsigned parity) {
@@ -224,57 +214,59 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         bad = r.wrong != 0;
         if (!bad && threadIdx.x < kATRows) {
           const int token = fdiv(row0 + threadIdx.x, a.div_g);
-          if (token < a.T) attend_bits(r.parents, token, 4, r.bits[threadIdx.x]);
+          if (token < a.T) attend_bits(r.parents, token, 4, r.bits[threadIdx.x]);  // (its own row's)
         }
       }
       loaded_b = w.b, loaded_tile = w.tile;
       const bool lost = w.s.bad || (a.parents && bad);
       if (lost && threadIdx.x == 0) atomicOr(a.status, kStatusBadData);
-      {
-        // 16 lanes a row, eight values a lane; 16 rows of a warp in flight
+      const bool active = 32 * warp < rows - row0, mine = row0 + row < rows;
+      float qs = __uint_as_float(0x7fffffffu);
+      if (active) {
+        // A thread has its row, and lays it down in tensor memory: the products read it from there,
+        // which leaves shared memory to the keys and values.
+        const int token = fdiv(row0 + row, a.div_g);
+        const uint16_t* q = (const uint16_t*)a.q + ((long long)w.b * a.T + token) * a.q_stride + ((long long)w.h * a.G + row0 + row - token * a.G) * a.D;
         const bool fast = ((uintptr_t)a.q & 15) == 0 && a.q_stride % 8 == 0;
-        const int live = min(kATRows, rows - row0), d = 8 * (lane & 15);
-        for (int r0 = 2 * warp; r0 < live; r0 += 16 * kATSoft) {
-          uint4 x[8];
+        auto eight = [&](int d) {
+          if (!mine || lost || d >= a.D) return make_uint4(0, 0, 0, 0);
+          const uint16_t* p = q + d;
+          if (fast) return __ldg((const uint4*)p);
+          return make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+        };
+        unsigned lo = 0, hi = 0;
+#pragma unroll 2
+        for (int d = 0; d < DP; d += 32) {
+          uint4 x[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int q = r0 + 2 * kATSoft * k + (lane >> 4);
-            x[k] = make_uint4(0, 0, 0, 0);
-            if (q < live && d < a.D && !lost) {
-              const int token = fdiv(row0 + q, a.div_g);
-              const uint16_t* p = (const uint16_t*)a.q + ((long long)w.b * a.T + token) * a.q_stride +
-                                  ((long long)w.h * a.G + row0 + q - token * a.G) * a.D + d;
-              if (fast)
-                x[k] = __ldg((const uint4*)p);
-              else
-                x[k] = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
-            }
-          }
+          for (int e = 0; e < 4; ++e) x[e] = eight(d + 8 * e);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int q = r0 + 2 * kATSoft * k + (lane >> 4);
-            const unsigned lo = max(max(x[k].x & 0x7fffu, x[k].y & 0x7fffu), max(x[k].z & 0x7fffu, x[k].w & 0x7fffu));
-            const unsigned hi = max(max(x[k].x & 0x7fff0000u, x[k].y & 0x7fff0000u), max(x[k].z & 0x7fff0000u, x[k].w & 0x7fff0000u));
-            unsigned top = max(lo << 16, hi);
-#pragma unroll
-            for (int e = 1; e < 16; e *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, e));
-            if (q >= live) continue;
-            const bool finite = top < 0x7f800000u;
-            // the scale's sign goes with the query: what multiplies the scores is positive
-            const float up = a.scale < 0.f ? -scale_up(top) : scale_up(top);
-            if ((lane & 15) == 0) r.qs[q] = lost || !finite ? __uint_as_float(0x7fffffffu) : scale_down(top) * fabsf(a.scale);
-            auto two = [&](uint32_t v) { return finite ? half2_of(bf16_lo(v) * up, bf16_hi(v) * up) : 0u; };
-            if (d < a.D)
-              *(uint4*)(base + L::kQ + (d >> 6) * L::kQChunk + swizzled(q, (d & 63) >> 3)) =
-                  make_uint4(two(x[k].x), two(x[k].y), two(x[k].z), two(x[k].w));
+          for (int e = 0; e < 4; ++e) {
+            lo = max(lo, max(max(x[e].x & 0x7fffu, x[e].y & 0x7fffu), max(x[e].z & 0x7fffu, x[e].w & 0x7fffu)));
+            hi = max(hi, max(max(x[e].x & 0x7fff0000u, x[e].y & 0x7fff0000u), max(x[e].z & 0x7fff0000u, x[e].w & 0x7fff0000u)));
           }
         }
-        fence_async();
-        bar_sync(5, 32 * kATSoft);  // also: r.qs and the tree's bits
-        if (lane == 0) mbar_arrive(&r.q_full);
+        const unsigned top = max(lo << 16, hi);
+        const bool finite = top < 0x7f800000u;
+        // the scale's sign goes with the query: what multiplies the scores is positive
+        const float up = a.scale < 0.f ? -scale_up(top) : scale_up(top);
+        if (!lost && finite) qs = scale_down(top) * fabsf(a.scale);
+        auto two = [&](uint32_t v) { return finite ? half2_of(bf16_lo(v) * up, bf16_hi(v) * up) : 0u; };
+#pragma unroll 2
+        for (int d = 0; d < DP; d += 32) {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4 x = eight(d + 8 * e);
+            y[4 * e] = two(x.x), y[4 * e + 1] = two(x.y), y[4 * e + 2] = two(x.z), y[4 * e + 3] = two(x.w);
+          }
+          tc_store16(t_q + lanes + d / 2, y);
+        }
+        tc_stored();
       }
-      const float qs = r.qs[row];
-      const bool active = 32 * warp < rows - row0, mine = row0 + row < rows;
+      tc_before();
+      bar_sync(5, 32 * kATSoft);  // no warp is more than a segment ahead
+      if (lane == 0) mbar_arrive(&r.q_full);
       const int last_seen = w.s.len + fdiv(row0 + row, a.div_g), first_seen = w.s.len + fdiv(row0, a.div_g);
       float m = kLow, M = kLow, l = 0.f;
       unsigned ref = kATLeastRef;
@@ -285,13 +277,12 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
       const unsigned arrivals = warp ? 1u : 1u + kATSoft - min(kATSoft, (rows - row0 + 31) / 32);
       if (!active) i += u1 - u0;
       for (int u = active ? u0 : u1; u < u1; ++u, ++i) {
-        const int s = i & 1;
-        wait(&r.s_full[s], i >> 1);
+        wait(&r.s_full, i);
         tc_after();
         if (!w.s.bad) {
           const int slot = i & (kATRing - 1);
           const float *sk = r.sk[slot], *sv = r.sv[slot];
-          const uint32_t t_s = tmem + 64 * s + lanes;
+          const uint32_t t_s = tmem + lanes;
           // the maximum moves, and with it the sums: to a score of at least `most` (log2) and exponent bits `top`
           auto move = [&](float most, unsigned top) {
             m = fmaxf(m, most);
@@ -300,11 +291,8 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
             M = M2;
             l *= f;
             if (u > u0) {
-              const int j = i - 1;
-              wait(&r.pv_done[j & 1], j >> 1);
-              tc_after();
 #pragma unroll 1
-              for (int c = 0; c < DP; c += 16) {
+              for (int c = 0; c < DP; c += 16) {  // (no product is under way: the scores came after the last one)
                 uint32_t o[16];
                 const uint32_t at = t_o + lanes + c;
                 tc_load16(at, o);
@@ -315,17 +303,15 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
               }
             }
           };
-          // Scores to weights under the maximum as it is; where one of the warp's rows has
-          // outgrown it, it moves and the scores, which are still there, are taken again.
-          // Kind 0: 16 keys share their scales; 1: each key has its own; 2: and some rows do not see some.
-          auto weigh = [&](auto kind_, uint32_t vis0, uint32_t vis1) {
-            constexpr int kKind = decltype(kind_)::value;
+          if (u < u_groups) {
+            // Scores to weights under the maximum as it is; where one of the warp's rows has
+            // outgrown it, it moves and the scores, which are still there, are taken again.
+            const unsigned top = r.top[slot];
             uint32_t p[32];
             f2_t sum0, sum1;
             for (bool again = false;; again = true) {
               uint32_t x[2][16];  // the next 16 come while these are taken
               tc_load16(t_s, x[0]);
-              unsigned top = kKind < 2 ? r.top[slot] : 0u;
               float most0 = -INFINITY, most1 = -INFINITY;  // of the exponents
               sum0 = sum1 = 0;
               const f2_t less = f2(-M, -M);
@@ -333,52 +319,36 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
                 if (g < 3) tc_load16(t_s + 16 * (g + 1), x[(g + 1) & 1]);
-                float b = 0.f, v = 0.f;
-                if constexpr (kKind == 0) b = sk[16 * g] * qs, v = sv[16 * g];
+                const float b = sk[16 * g] * qs, v = sv[16 * g];
+                const f2_t by = f2(b, b), of = f2(v, v);
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
                   const uint32_t(&z)[16] = x[g & 1];
-                  float4 b4 = make_float4(b, b, b, b), v4 = make_float4(v, v, v, v);
-                  if constexpr (kKind > 0) {
-                    b4 = *(const float4*)(sk + 16 * g + k), v4 = *(const float4*)(sv + 16 * g + k);
-                    b4 = make_float4(b4.x * qs, b4.y * qs, b4.z * qs, b4.w * qs);
-                  }
-                  f2_t y0 = f2fma(f2(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), f2(b4.x, b4.y), less);
-                  f2_t y1 = f2fma(f2(__uint_as_float(z[k + 2]), __uint_as_float(z[k + 3])), f2(b4.z, b4.w), less);
-                  if constexpr (kKind == 2) {
-                    const uint32_t vis = g < 2 ? vis0 : vis1;
-                    const int e = 16 * (g & 1) + k;
-                    const bool s0 = vis >> e & 1u, s1 = vis >> (e + 1) & 1u, s2 = vis >> (e + 2) & 1u, s3 = vis >> (e + 3) & 1u;
-                    y0 = f2(s0 ? f2lo(y0) : -INFINITY, s1 ? f2hi(y0) : -INFINITY);
-                    y1 = f2(s2 ? f2lo(y1) : -INFINITY, s3 ? f2hi(y1) : -INFINITY);
-                    // what is not seen has no part, whatever its scales are
-                    v4 = make_float4(s0 ? v4.x : 0.f, s1 ? v4.y : 0.f, s2 ? v4.z : 0.f, s3 ? v4.w : 0.f);
-                    top = max(max(max(top, __float_as_uint(v4.x)), max(__float_as_uint(v4.y), __float_as_uint(v4.z))), __float_as_uint(v4.w));
-                  }
+                  const f2_t y0 = f2fma(f2(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), by, less);
+                  const f2_t y1 = f2fma(f2(__uint_as_float(z[k + 2]), __uint_as_float(z[k + 3])), by, less);
                   most0 = fmaxf(most0, fmaxf(f2lo(y0), f2hi(y0)));
                   most1 = fmaxf(most1, fmaxf(f2lo(y1), f2hi(y1)));
                   const f2_t e0 = f2(ex2(f2lo(y0)), ex2(f2hi(y0))), e1 = f2(ex2(f2lo(y1)), ex2(f2hi(y1)));
                   sum0 = f2add(sum0, e0);
                   sum1 = f2add(sum1, e1);
-                  const f2_t z0 = f2mul(e0, f2(v4.x, v4.y)), z1 = f2mul(e1, f2(v4.z, v4.w));
+                  const f2_t z0 = f2mul(e0, of), z1 = f2mul(e1, of);
                   p[8 * g + k / 2] = half2_of(f2lo(z0), f2hi(z0));
                   p[8 * g + k / 2 + 1] = half2_of(f2lo(z1), f2hi(z1));
                 }
                 if (g < 3) tc_loaded16(x[(g + 1) & 1]);
               }
-              // (a scale that is not finite makes its weights NaN whatever the reference)
-              if constexpr (kKind == 2) top = top < 0x7f800000u ? (top >> 23) + 1u : 0u;
               // (rows past the last hold anything; a score that is infinite outgrows every maximum)
               if (again || !__any_sync(0xffffffffu, mine && (fmaxf(most0, most1) > kSlack + 138.f - (float)ref || top > ref))) break;
               float most = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
+              for (int g = 0; g < 4; ++g) {
                 uint32_t z[16];
-                tc_load16(t_s + 16 * c, z);
+                tc_load16(t_s + 16 * g, z);
                 tc_loaded16(z);
-                const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1));
+                float y = __uint_as_float(z[0]);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) most = fmaxf(most, vis >> k & 1u ? __uint_as_float(z[k]) * sk[16 * c + k] : -INFINITY);
+                for (int k = 1; k < 16; ++k) y = fmaxf(y, __uint_as_float(z[k]));
+                most = fmaxf(most, y * sk[16 * g]);
               }
               move(most * qs, top);  // (a scale of 0: -inf becomes NaN, which no maximum takes)
             }
@@ -386,42 +356,92 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
             l += f2lo(sum0) + f2hi(sum0);
             tc_store16(t_s, p);
             tc_store16(t_s + 16, p + 16);
-          };
-          if (u < u_groups) {
-            weigh(Kind<0>(), 0xffffffffu, 0xffffffffu);
           } else {
+            // A scale for each key, and keys that some rows do not see: twice over the scores, 16
+            // at a time.  What is not seen has no part, whatever its scales are.
             const bool codes = u < n_codes;
-            if (!codes) wait(&r.v_full[s], i >> 1);  // the plain values' scales
+            if (!codes) wait(&r.v_full[i % kATStages], i / kATStages);  // the plain values' scales
             const int unit = codes ? u * kATKeys : keys.stored + (u - n_codes) * kATKeys, end = codes ? keys.codes : keys.end;
-            if (unit + kATKeys > end || (a.parents ? unit + kATKeys > w.s.len : unit + kATKeys - 1 > first_seen)) {
-              // of 32 keys, those that the row sees
-              auto seen = [&](int f) {
-                const int behind = min(end - f, a.parents ? 32 : last_seen - f + 1);
-                uint32_t vis = behind <= 0 ? 0u : behind >= 32 ? 0xffffffffu : (1u << behind) - 1u;
-                const int at = f - w.s.len;  // the first key as a token of the step
-                if (a.parents && at > -32) {
-                  const int word = at >> 5;  // -1 .. 3
-                  const uint32_t lo = word < 0 ? 0xffffffffu : word < 4 ? r.bits[row][word] : 0u;
-                  const uint32_t hi = word + 1 < 4 ? r.bits[row][word + 1] : 0u;
-                  vis &= __funnelshift_r(lo, hi, at & 31);
+            const bool masked = unit + kATKeys > end || (a.parents ? unit + kATKeys > w.s.len : unit + kATKeys - 1 > first_seen);
+            // of 32 keys, those that the row sees
+            auto seen = [&](int f) {
+              if (!masked) return 0xffffffffu;
+              const int behind = min(end - f, a.parents ? 32 : last_seen - f + 1);
+              uint32_t vis = behind <= 0 ? 0u : behind >= 32 ? 0xffffffffu : (1u << behind) - 1u;
+              const int at = f - w.s.len;  // the first key as a token of the step
+              if (a.parents && at > -32) {
+                const int word = at >> 5;  // -1 .. 3
+                const uint32_t lo = word < 0 ? 0xffffffffu : word < 4 ? r.bits[row][word] : 0u;
+                const uint32_t hi = word + 1 < 4 ? r.bits[row][word + 1] : 0u;
+                vis &= __funnelshift_r(lo, hi, at & 31);
+              }
+              return vis;
+            };
+            const uint32_t vis0 = seen(unit), vis1 = seen(unit + 32);
+            float most = -INFINITY;
+            unsigned top = masked ? 0u : r.top[slot];
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[16];
+              tc_load16(t_s + 16 * c, x);
+              tc_loaded16(x);
+              const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1));
+              unsigned bits = 0;  // of the largest scale; one that is not finite makes its weights NaN whatever the reference
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) {
+                const float4 y = *(const float4*)(sk + 16 * c + k);
+                const float z0 = __uint_as_float(x[k]) * y.x, z1 = __uint_as_float(x[k + 1]) * y.y, z2 = __uint_as_float(x[k + 2]) * y.z,
+                            z3 = __uint_as_float(x[k + 3]) * y.w;
+                if (masked) {
+                  const uint4 v = *(const uint4*)(sv + 16 * c + k);
+                  most = fmaxf(fmaxf(most, vis >> k & 1u ? z0 : -INFINITY), vis >> (k + 1) & 1u ? z1 : -INFINITY);
+                  most = fmaxf(fmaxf(most, vis >> (k + 2) & 1u ? z2 : -INFINITY), vis >> (k + 3) & 1u ? z3 : -INFINITY);
+                  bits = max(bits, max(max(vis >> k & 1u ? v.x : 0u, vis >> (k + 1) & 1u ? v.y : 0u),
+                                       max(vis >> (k + 2) & 1u ? v.z : 0u, vis >> (k + 3) & 1u ? v.w : 0u)));
+                } else {
+                  most = fmaxf(most, fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)));
                 }
-                return vis;
-              };
-              weigh(Kind<2>(), seen(unit), seen(unit + 32));
-            } else {
-              weigh(Kind<1>(), 0xffffffffu, 0xffffffffu);
+              }
+              if (masked) top = max(top, bits < 0x7f800000u ? (bits >> 23) + 1u : 0u);
             }
+            most *= qs;
+            if (__any_sync(0xffffffffu, mine && (most > m + kSlack || top > ref))) move(most, top);
+            f2_t sum = 0;
+            const f2_t less = f2(-M, -M), by = f2(qs, qs);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[16], p[8];
+              tc_load16(t_s + 16 * c, x);
+              tc_loaded16(x);
+              const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1));
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float2 y = *(const float2*)(sk + 16 * c + k), v = *(const float2*)(sv + 16 * c + k);
+                const f2_t t = f2fma(f2mul(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2(y.x, y.y)), by, less);
+                f2_t e = f2(ex2(f2lo(t)), ex2(f2hi(t))), z;
+                if (masked) {
+                  const bool s0 = vis >> k & 1u, s1 = vis >> (k + 1) & 1u;
+                  e = f2(s0 ? f2lo(e) : 0.f, s1 ? f2hi(e) : 0.f);
+                  z = f2mul(e, f2(s0 ? v.x : 0.f, s1 ? v.y : 0.f));
+                } else {
+                  z = f2mul(e, f2(v.x, v.y));
+                }
+                sum = f2add(sum, e);
+                p[k / 2] = half2_of(f2lo(z), f2hi(z));
+              }
+              tc_store8(t_s + 8 * c, p);  // over scores that have been taken
+            }
+            l += f2lo(sum) + f2hi(sum);
           }
           tc_stored();
         }
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_n(&r.p_ready[s], arrivals);
+        if (lane == 0) mbar_arrive_n(&r.p_ready, arrivals);
       }
       // ---- out, or to the workspace ----
       if (active) {
-        const int j = i - 1;
-        wait(&r.pv_done[j & 1], j >> 1);
+        wait(&r.pv_done, i - 1);
         tc_after();
         if (lost) l = __uint_as_float(0x7fffffffu);
         const bool whole = u0 == 0 && u1 == n;
@@ -507,14 +527,15 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     };
     if (units > 0) load(0, c[0]);
     if (units > 1) load(1, c[1]);
+    int stage = 0, lap = 0;
     for (int i0 = 0; i0 < units; i0 += 2) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int i = i0 + b, slot = i & (kATRing - 1);
         if (i >= units) break;
         const int kind = r.kind[slot];
-        unsigned char* to = operand + b * L::kTile;
-        if (i >= 2) wait(&is_empty[b], (i >> 1) + 1);  // the operand of two units ago has been read
+        unsigned char* to = operand + stage * L::kTile;
+        if (lap) wait(&is_empty[stage], lap + 1);  // what lay there has been read
         if (kind == kATCodes) {
           if (on) {
 #pragma unroll
@@ -566,7 +587,8 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&is_full[b]);
+        if (lane == 0) mbar_arrive(&is_full[stage]);
+        if (++stage == kATStages) stage = 0, ++lap;
         if (i + 2 < units) load(i + 2, c[b]);
       }
     }
@@ -580,62 +602,45 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
       // then known to be the same in all lanes (an issue under `lane == 0` took 100 clocks,
       // 64 being the product's own time).
       const bool leader = tc_elect();
-      const unsigned long long d_q = tc_operand(smem_addr(base + L::kQ), 16), d_k = tc_operand(smem_addr(base + L::kK), 16);
-      const unsigned long long d_v = tc_operand(smem_addr(base + L::kV), L::kChunk);
+      const unsigned long long d_k = tc_operand(smem_addr(base + L::kK), 16), d_v = tc_operand(smem_addr(base + L::kV), L::kChunk);
       const uint32_t kind_s = tc_kind(kATKeys, false), kind_o = tc_kind(a.D, true);
       const int steps = a.D / 16;
-      int i = 0, segments = 0;
-      bool open = false;   // unit i - 1 has no P V yet
-      bool fresh = false;  // ... and begins its segment
-      auto pv = [&]() {    // of unit i - 1
-        const int j = i - 1, s = j & 1;
-        wait(&r.p_ready[s], j >> 1);
-        wait(&r.v_full[s], j >> 1);
-        tc_after();
-        if (leader) {
-          const unsigned long long d = d_v + s * (L::kTile >> 4);
-          const bool add = !fresh;
-#pragma unroll
-          for (int k = 0; k < kATKeys / 16; ++k) tc_mma_t(t_o, tmem + 64 * s + 8 * k, d + k * (2048 >> 4), kind_o, k > 0 || add);
-          tc_commit(&r.v_empty[s]);
-          tc_commit(&r.pv_done[s]);
-          tc_commit(&r.at_empty[j & (kATRing - 1)]);  // its places and scales have been used
-        }
-        __syncwarp();
-        open = false;
-      };
+      int i = 0, stage = 0, lap = 0, segments = 0;
       while (w.left > 0) {
         const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
         const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
+        wait(&r.q_full, segments++);
         for (int u = u0; u < u1; ++u, ++i) {
-          const int s = i & 1;
-          if (u == u0) {  // the last segment's products come to their end, then its queries go
-            if (open) pv();
-            wait(&r.q_full, segments++);
-          }
-          // S's columns hold the weights of unit i - 2 until P V has read them
-          wait(&r.k_full[s], i >> 1);
-          if (i >= 2) wait(&r.pv_done[s], (i >> 1) + 1);
+          wait(&r.k_full[stage], lap);
+          if (i > 0) wait(&r.pv_done, i - 1);  // S's columns hold the weights of the last unit until P V has read them
           tc_after();
           if (leader) {
-            const unsigned long long d = d_k + s * (L::kTile >> 4);
+            const unsigned long long d = d_k + stage * (L::kTile >> 4);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k)
-              if (k < steps)
-                tc_mma(tmem + 64 * s, d_q + (((k >> 2) * L::kQChunk + (k & 3) * 32) >> 4), d + (((k >> 2) * L::kChunk + (k & 3) * 32) >> 4), kind_s,
-                       k > 0);
-            tc_commit(&r.k_empty[s]);
-            tc_commit(&r.s_full[s]);
-            mbar_arrive(&r.s_full[s]);  // with what k_full brought: the scales
+              if (k < steps) tc_mma_t(tmem, t_q + 8 * k, d + (((k >> 2) * L::kChunk + (k & 3) * 32) >> 4), kind_s, k > 0);
+            tc_commit(&r.k_empty[stage]);
+            tc_commit(&r.s_full);
+            mbar_arrive(&r.s_full);  // with what k_full brought: the scales
           }
           __syncwarp();
-          if (open) pv();
-          open = true;
-          fresh = u == u0;
+          wait(&r.v_full[stage], lap);
+          wait(&r.p_ready, i);
+          tc_after();
+          if (leader) {
+            const unsigned long long d = d_v + stage * (L::kTile >> 4);
+            const bool add = u > u0;
+#pragma unroll
+            for (int k = 0; k < kATKeys / 16; ++k) tc_mma_t(t_o, tmem + 8 * k, d + k * (2048 >> 4), kind_o, k > 0 || add);
+            tc_commit(&r.v_empty[stage]);
+            tc_commit(&r.pv_done);
+            tc_commit(&r.at_empty[i & (kATRing - 1)]);  // its places and scales have been used
+          }
+          __syncwarp();
+          if (++stage == kATStages) stage = 0, ++lap;
         }
         attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
       }
-      if (open) pv();
       // nothing of the tensor cores is in flight when the tensor memory goes back
       if (leader) tc_commit(&r.drain);
       __syncwarp();
