@@ -241,4 +241,84 @@ __device__ __forceinline__ void attend_store8(S* to, const float (&f)[8]) {
   }
 }
 
+// What a share leaves of a tile: floats [rows][DP], then the rows' maxima and sums.
+__host__ __device__ constexpr int attend_slot(int rows, int DP) { return rows * DP + 2 * rows; }
+
+// Joins a segment that fell into several shares, in their order: CTAs x join the one that
+// begins in share x and goes on, a warp to a row.  The shares' maxima and sums come at
+// once, a lane each; their values eight shares at a time.
+template <class S, int DP, int kRows>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ KvAttendArgs a) {
+  constexpr int kSlot = attend_slot(kRows, DP), kN = DP / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 meta = a.meta[blockIdx.x];
+  const int first = blockIdx.x, n = meta.x - first + 1;
+  if (meta.x < 0) return;
+  const Sequence q = attend_sequence(a, meta.y);
+  const int lane = threadIdx.x & 31, row0 = meta.w * kRows, live = min(kRows, q.n_new * a.G - row0);
+  auto slot = [&](int s) { return a.part + (2LL * (first + s) + (s == 0)) * kSlot; };
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < live; r += gridDim.y * 4) {
+    float most = kLow;
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      const float m = s0 + lane < n ? slot(s0 + lane)[kRows * DP + r] : kLow;
+      most = fmaxf(most, m);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    float sum = 0.f, f[kN] = {};
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      const bool on = s0 + lane < n;
+      const float* p = slot(on ? s0 + lane : 0) + kRows * DP;
+      const float by = on ? ex2(p[r] - most) : 0.f, l = on ? p[kRows + r] * by : 0.f;
+      const int count = min(32, n - s0);
+      for (int s = 0; s < count; s += 8) {
+        float x[8][kN];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float* from = slot(s0 + min(s + e, count - 1)) + r * DP + kN * lane;
+#pragma unroll
+          for (int k = 0; k < kN; k += 2) *(float2*)&x[e][k] = *(const float2*)(from + k);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (s + e >= count) break;
+          const float w = __shfl_sync(0xffffffffu, by, s + e);
+          sum += __shfl_sync(0xffffffffu, l, s + e);
+#pragma unroll
+          for (int k = 0; k < kN; ++k) f[k] += x[e][k] * w;
+        }
+      }
+    }
+    if (kN * lane >= a.D) continue;
+    const float by = sum == 0.f ? 0.f : 1.f / sum;
+    const int token = fdiv(row0 + r, a.div_g);
+    S* out = (S*)a.out + (((long long)meta.y * a.T + token) * a.Hq + (long long)meta.z * a.G + row0 + r - token * a.G) * a.D + kN * lane;
+#pragma unroll
+    for (int k = 0; k < kN; k += 2) {
+      if constexpr (sizeof(S) == 4) {
+        *(float2*)(out + k) = make_float2(f[k] * by, f[k + 1] * by);
+      } else {
+        uint32_t y;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(f[k + 1] * by), "f"(f[k] * by));
+        *(uint32_t*)(out + k) = y;
+      }
+    }
+  }
+}
+
+template <class S, int DP, int kRows>
+static cudaError_t launch_join(const KvAttendArgs& a, int grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3((unsigned)grid, kRows < 32 ? kRows / 4 : 8);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<S, DP, kRows>, a);
+}
+
 }  // namespace sv

@@ -45,7 +45,6 @@ struct Rows {
   static constexpr bool kTwo = sizeof(S) == 4;  // two fp16 parts
   static constexpr int kSteps = DP / 16, kChunks = DP / 64, NT = DP / 8, kParts = kTwo ? 2 : 1;
   static constexpr int kFrag = kSteps * 32;                  // uint4's of one row tile's queries
-  static constexpr int kSlot = MT * (NT * 4 * 32 + 2 * 16);  // floats that a share leaves
   static constexpr size_t smem(int T, bool tree) {
     return (size_t)MT * kParts * kFrag * 16 + (size_t)MT * NT * 4 * 32 * 4 + 2 * kARWarps * 16 * MT * 4 + 16 * MT * 4 +
            (tree ? (size_t)T * 4 + (size_t)16 * MT * ((T + 31) / 32) * 4 : 0);
@@ -88,7 +87,8 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
   constexpr int NT = R::NT, kChunks = R::kChunks, kRows = 16 * MT;
   constexpr bool kTwo = R::kTwo;
   constexpr int VW = DP / 32;               // words of V's codes per key and lane
-  constexpr bool kAhead = DP * MT <= 128;   // V's codes of the next unit are in flight too
+  constexpr bool kAhead = DP <= 128;        // the next unit's K is in flight
+  constexpr bool kAheadV = DP * MT <= 128;  // ... and its V
   extern __shared__ __align__(16) unsigned char s_attend[];
   uint4* s_q = (uint4*)s_attend;                                   // [MT][parts][steps][32]
   float* s_acc = (float*)(s_q + MT * R::kParts * R::kFrag);        // [MT][NT][4][32]
@@ -324,17 +324,23 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) at_v[k] = __shfl_sync(0xffffffffu, e, 2 * t + (k & 1) + 8 * (k >> 1));
-        if constexpr (kAhead) load_v(x);
+        if constexpr (kAheadV) load_v(x);
       };
       Tile now;
       look(u0);
-      load(now);
-      if (u0 + 1 < uc) look(u0 + 1);
+      if constexpr (kAhead) {
+        load(now);
+        if (u0 + 1 < uc) look(u0 + 1);
+      }
 #pragma unroll 2
       for (int u = u0; u < uc; ++u) {
         Tile next;
-        if constexpr (!kAhead) load_v(now);
-        if (u + 1 < uc) {
+        if constexpr (!kAhead) {
+          load(now);
+          if (u + 1 < uc) look(u + 1);
+        }
+        if constexpr (!kAheadV) load_v(now);
+        if (kAhead && u + 1 < uc) {
           load(next);
           if (u + 2 < uc) look(u + 2);
         }
@@ -387,7 +393,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
 #pragma unroll
               for (int part = 0; part < R::kParts; ++part) mma16816(o[i][4 * x + y], wt[i][part], b0[y], b1[y]);
         }
-        now = next;
+        if constexpr (kAhead) now = next;
       }
     }
 
@@ -541,34 +547,35 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
     }
 
     // ---- out, or to the workspace ----
-    if (u0 == 0 && u1 == n) {
-      // item: a row's half c and eight of its values in a row
-      for (int x = warp; x < MT * 4 * (NT / 8); x += kARWarps) {
-        const int oct = x % (NT / 8), c = x / (NT / 8) % 4, i = x / (NT / 8) / 4;
-        const int r = row0 + 16 * i + 8 * (c >> 1) + g, d = (2 * t + (c & 1)) * NT + 8 * oct;
-        float sum = 0.f;
+    const bool whole = u0 == 0 && u1 == n;
+    float* part = a.part + (2LL * blockIdx.x + (u0 == 0)) * attend_slot(kRows, DP);
+    // item: a row's half c and eight of its values in a row
+    for (int x = warp; x < MT * 4 * (NT / 8); x += kARWarps) {
+      const int oct = x % (NT / 8), c = x / (NT / 8) % 4, i = x / (NT / 8) / 4;
+      const int r = 16 * i + 8 * (c >> 1) + g, d = (2 * t + (c & 1)) * NT + 8 * oct;
+      if (row0 + r >= rows || d >= a.D) continue;
+      float sum = 0.f, f[8];
 #pragma unroll
-        for (int y = 0; y < MT; ++y)
-          if (i == y) sum = c >> 1 ? l[y][1] : l[y][0];
-        const float by = sum == 0.f ? 0.f : 1.f / sum;
-        float f[8];
+      for (int y = 0; y < MT; ++y)
+        if (i == y) sum = c >> 1 ? l[y][1] : l[y][0];
+      const float by = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int y = 0; y < 8; ++y) f[y] = s_acc[((i * NT + 8 * oct + y) * 4 + c) * 32 + lane] * by;
-        if (r >= rows || d >= a.D) continue;
-        const int token = fdiv(r, a.div_g);
-        S* to = (S*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + r - token * a.G) * a.D + d;
-        attend_store8<S>(to, f);
+      for (int y = 0; y < 8; ++y) f[y] = s_acc[((i * NT + 8 * oct + y) * 4 + c) * 32 + lane] * by;
+      if (whole) {
+        const int token = fdiv(row0 + r, a.div_g);
+        attend_store8<S>((S*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + r - token * a.G) * a.D + d, f);
+      } else {
+        attend_store8<uint32_t>((uint32_t*)part + r * DP + d, f);
       }
-    } else {
-      float* to = a.part + (2LL * blockIdx.x + (u0 == 0)) * R::kSlot;
-      for (int x = threadIdx.x; x < MT * NT * 4 * 32; x += kARThreads) to[x] = s_acc[x];
+    }
+    if (!whole) {
       if (warp == 0 && t == 0)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            to[MT * NT * 4 * 32 + 16 * i + 8 * e + g] = m[i][e];
-            to[MT * NT * 4 * 32 + kRows + 16 * i + 8 * e + g] = l[i][e];
+            part[kRows * DP + 16 * i + 8 * e + g] = m[i][e];
+            part[kRows * DP + kRows + 16 * i + 8 * e + g] = l[i][e];
           }
       if (u0 == 0) {
         meta_last = attend_share_of(w, w.from + n - 1);
@@ -578,43 +585,6 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
     attend_advance<kRows, kARKeys>(a, w, u1 - u0);
   }
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(meta_last, meta_b, meta_h, meta_tile);
-}
-
-// Joins a segment that fell into several shares: CTA x takes the one that begins in
-// share x and goes on.  In the order of the shares; one warp to eight values of 32
-// (row, place) pairs.
-template <class S, int NT, int MT>
-__global__ void __launch_bounds__(kARThreads) attend_rows_join_kernel(const __grid_constant__ KvAttendArgs a) {
-  constexpr int kRows = 16 * MT, kSums = MT * NT * 4 * 32, kSlot = kSums + 2 * kRows;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 meta = a.meta[blockIdx.x];
-  const int last = meta.x;
-  if (last < 0) return;
-  const int lane = threadIdx.x & 31, x = blockIdx.y * (kARThreads / 32) + (threadIdx.x >> 5), g = lane >> 2, t = lane & 3;
-  if (x >= MT * 4 * (NT / 8)) return;
-  const int oct = x % (NT / 8), c = x / (NT / 8) % 4, i = x / (NT / 8) / 4, r = 16 * i + 8 * (c >> 1) + g;
-  const int first = blockIdx.x;
-  auto slot = [&](int s) { return a.part + (2LL * s + (s == first)) * kSlot; };
-  float most = kLow;
-#pragma unroll 4
-  for (int s = first; s <= last; ++s) most = fmaxf(most, slot(s)[kSums + r]);
-  float sum = 0.f, f[8] = {};
-#pragma unroll 2
-  for (int s = first; s <= last; ++s) {
-    const float* p = slot(s);
-    const float by = ex2(p[kSums + r] - most);
-    sum += p[kSums + kRows + r] * by;
-#pragma unroll
-    for (int y = 0; y < 8; ++y) f[y] += p[((i * NT + 8 * oct + y) * 4 + c) * 32 + lane] * by;
-  }
-  const Sequence q = attend_sequence(a, meta.y);
-  const int row = meta.w * kRows + r, d = (2 * t + (c & 1)) * NT + 8 * oct;
-  if (row >= q.n_new * a.G || d >= a.D) return;
-  const float by = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int y = 0; y < 8; ++y) f[y] *= by;
-  const int token = fdiv(row, a.div_g);
-  attend_store8<S>((S*)a.out + (((long long)meta.y * a.T + token) * a.Hq + (long long)meta.z * a.G + row - token * a.G) * a.D + d, f);
 }
 
 // ---------------------------------------------------------------------------
@@ -632,7 +602,7 @@ static cudaError_t launch_rows(KvAttendArgs a, int sms, size_t* bytes, cudaStrea
   const long long keys = (long long)a.max_code_pages * a.block + (long long)a.max_pages * a.page_size;
   const double most = (double)a.B * a.Hkv * a.tiles * (double)(keys / kARKeys + 2);
   const int grid = (int)fmin((double)sms * kCtas, most);
-  const size_t slots = ((size_t)grid * 2 * R::kSlot * 4 + 255) / 256 * 256;
+  const size_t slots = ((size_t)grid * 2 * attend_slot(kRows, DP) * 4 + 255) / 256 * 256;
   if (bytes) {
     *bytes = slots + (size_t)grid * sizeof(int4);
     return cudaSuccess;
@@ -644,32 +614,14 @@ static cudaError_t launch_rows(KvAttendArgs a, int sms, size_t* bytes, cudaStrea
   }
   kernel<<<grid, kARThreads, smem, s>>>(a);
   const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3((unsigned)grid, (MT * 4 * (R::NT / 8) + kARWarps - 1) / kARWarps);
-  cfg.blockDim = dim3(kARThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_rows_join_kernel<S, R::NT, MT>, a);
+  return e != cudaSuccess ? e : launch_join<S, DP, kRows>(a, grid, s);
 }
 
-// A tile of 16 rows, or of 32 where there are more rows and the sums of 32 fit the
-// registers: a code is then read and made fp16 once for twice as many rows.
+// CTAs of an SM by what a thread needs: three of 168 registers spill at 128 values a head.
 template <class S, bool kE4m3>
 static cudaError_t launch_rows_of(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s) {
-  const bool more = (long long)a.T * a.G > 16;
-  if constexpr (sizeof(S) == 2) {
-    if (a.D <= 64) return more ? launch_rows<S, kE4m3, 64, 2, 3>(a, sms, bytes, s) : launch_rows<S, kE4m3, 64, 1, 4>(a, sms, bytes, s);
-    if (a.D <= 128) return more ? launch_rows<S, kE4m3, 128, 2, 2>(a, sms, bytes, s) : launch_rows<S, kE4m3, 128, 1, 3>(a, sms, bytes, s);
-  } else {
-    if (a.D <= 64) return launch_rows<S, kE4m3, 64, 1, 4>(a, sms, bytes, s);
-    if (a.D <= 128) return launch_rows<S, kE4m3, 128, 1, 3>(a, sms, bytes, s);
-  }
+  if (a.D <= 64) return launch_rows<S, kE4m3, 64, 1, sizeof(S) == 2 ? 4 : 3>(a, sms, bytes, s);
+  if (a.D <= 128) return launch_rows<S, kE4m3, 128, 1, 2>(a, sms, bytes, s);
   return launch_rows<S, kE4m3, 256, 1, 2>(a, sms, bytes, s);
 }
 

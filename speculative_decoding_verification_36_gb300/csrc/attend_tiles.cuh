@@ -43,7 +43,6 @@ struct Tiles {
   static constexpr int kTile = kATKeys * DP * 2;    // bytes of a unit's keys or values
   static constexpr int kChunk = kATKeys * 128;      // its rows of 64 fp16
   static constexpr int kK = 0, kV = kATStages * kTile, kRest = 2 * kATStages * kTile;
-  static constexpr int kSlot = 128 * DP + 2 * 128;  // floats that a share leaves
   struct Rest {
     float sk[kATRing][kATKeys], sv[kATRing][kATKeys];
     int kind[kATRing];
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         const float by = l == 0.f ? 0.f : 1.f / l;
         const int token = fdiv(row0 + row, a.div_g);
         uint16_t* out = (uint16_t*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + row - token * a.G) * a.D;
-        float* part = a.part + (2LL * blockIdx.x + (u0 == 0)) * L::kSlot;
+        float* part = a.part + (2LL * blockIdx.x + (u0 == 0)) * attend_slot(kATRows, DP);
 #pragma unroll 1
         for (int c = 0; c < DP; c += 16) {
           uint32_t o[16];
@@ -722,44 +721,6 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(r.meta[0], r.meta[1], r.meta[2], r.meta[3]);
 }
 
-// Joins a segment that fell into several shares, in their order: a warp to a row.
-template <int DP>
-__global__ void __launch_bounds__(128) attend_tiles_join_kernel(const __grid_constant__ KvAttendArgs a) {
-  constexpr int kSlot = Tiles<DP>::kSlot, kN = DP / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 meta = a.meta[blockIdx.x];
-  const int first = blockIdx.x, last = meta.x;
-  if (last < 0) return;
-  const Sequence q = attend_sequence(a, meta.y);
-  const int lane = threadIdx.x & 31, row0 = meta.w * kATRows, live = min(kATRows, q.n_new * a.G - row0);
-  auto slot = [&](int s) { return a.part + (2LL * s + (s == first)) * kSlot; };
-  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < live; r += gridDim.y * 4) {
-    float most = kLow;
-#pragma unroll 4
-    for (int s = first; s <= last; ++s) most = fmaxf(most, slot(s)[128 * DP + r]);
-    float sum = 0.f, f[kN] = {};
-#pragma unroll 4
-    for (int s = first; s <= last; ++s) {
-      const float* p = slot(s);
-      const float by = ex2(p[128 * DP + r] - most);
-      sum += p[128 * DP + 128 + r] * by;
-#pragma unroll
-      for (int k = 0; k < kN; ++k) f[k] += p[r * DP + kN * lane + k] * by;
-    }
-    if (kN * lane >= a.D) continue;
-    const float by = sum == 0.f ? 0.f : 1.f / sum;
-    const int token = fdiv(row0 + r, a.div_g);
-    uint16_t* out = (uint16_t*)a.out + (((long long)meta.y * a.T + token) * a.Hq + (long long)meta.z * a.G + row0 + r - token * a.G) * a.D +
-                    kN * lane;
-#pragma unroll
-    for (int k = 0; k < kN; k += 2) {
-      uint32_t y;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(f[k + 1] * by), "f"(f[k] * by));
-      *(uint32_t*)(out + k) = y;
-    }
-  }
-}
-
 template <bool kE4m3, int DP>
 static cudaError_t launch_tiles(KvAttendArgs a, int sms, size_t* bytes, cudaStream_t s) {
   using L = Tiles<DP>;
@@ -767,7 +728,7 @@ static cudaError_t launch_tiles(KvAttendArgs a, int sms, size_t* bytes, cudaStre
   const long long keys = (long long)a.max_code_pages * a.block + (long long)a.max_pages * a.page_size;
   const double most = (double)a.B * a.Hkv * a.tiles * (double)(keys / kATKeys + 2);
   const int grid = (int)fmin((double)sms * kATCtas, most);
-  const size_t slots = ((size_t)grid * 2 * L::kSlot * 4 + 255) / 256 * 256;
+  const size_t slots = ((size_t)grid * 2 * attend_slot(kATRows, DP) * 4 + 255) / 256 * 256;
   if (bytes) {
     *bytes = slots + (size_t)grid * sizeof(int4);
     return cudaSuccess;
@@ -779,17 +740,7 @@ static cudaError_t launch_tiles(KvAttendArgs a, int sms, size_t* bytes, cudaStre
   kernel<<<grid, kATThreads, L::smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3((unsigned)grid, 8);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_tiles_join_kernel<DP>, a);
+  return launch_join<uint16_t, DP, kATRows>(a, grid, s);
 }
 
 }  // namespace sv

@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t four_codes(float x0, float x1, float x2, flo
 // values are read once into registers (a block of more than 8 vectors a thread
 // reads the rest a second time), the largest magnitude found, and the codes written.
 template <class S, bool kE4m3, int kThreads>
-__global__ void __launch_bounds__(kQThreads) kv_quantize_kernel(const __grid_constant__ Kv8Args a) {
+__global__ void __launch_bounds__(kQThreads, 8) kv_quantize_kernel(const __grid_constant__ Kv8Args a) {
   __shared__ int s_sum[kQThreads], s_warp[kQThreads / 32];
   __shared__ unsigned s_top[2][kQThreads / 32];
   constexpr int kGroups = kQThreads / kThreads, kN = Bits<S>::n;
@@ -212,10 +212,10 @@ __global__ void __launch_bounds__(kQThreads) kv_quantize_kernel(const __grid_con
   }
 }
 
-// Codes to plain entries: a warp takes a run of tokens of one sequence, so that its
-// place is looked up once for the run, a lane 16 codes at a time.
+// Codes to plain entries: a CTA takes a run of tokens of one sequence, so that its
+// place is looked up once for the run, a thread 16 codes at a time.
 constexpr int kRun = 8;     // tokens
-constexpr int kRFlight = 4; // vectors in flight per lane
+constexpr int kRFlight = 4; // vectors in flight per thread
 
 __device__ __forceinline__ int runs_to_read(const Kv8Args& a, int b, bool* bad) {
   const int from = __ldg(a.first + b), to = __ldg(a.last + b);
@@ -226,7 +226,7 @@ __device__ __forceinline__ int runs_to_read(const Kv8Args& a, int b, bool* bad) 
 template <class S, bool kE4m3>
 __global__ void __launch_bounds__(kQThreads) kv_dequantize_kernel(const __grid_constant__ Kv8Args a) {
   __shared__ int s_sum[kQThreads], s_warp[kQThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int layer = blockIdx.y >> 1, which = blockIdx.y & 1;
   S* cache = (S*)(which ? a.v_cache : a.k_cache) + layer * a.layer_stride;
   const uint8_t* codes = (const uint8_t*)(which ? a.v_codes : a.k_codes) + layer * a.code_stride;
@@ -238,10 +238,10 @@ __global__ void __launch_bounds__(kQThreads) kv_dequantize_kernel(const __grid_c
     if (b0 + (int)threadIdx.x < a.B) n = runs_to_read(a, b0 + threadIdx.x, &bad);
     if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusBadData);
     const int all = sum_up(n, s_sum, s_warp);
-    for (int at = blockIdx.x * (kQThreads / 32) + warp; at < all; at += gridDim.x * (kQThreads / 32)) {
+    for (int at = blockIdx.x; at < all; at += gridDim.x) {
       const int i = sequence_of(at, s_sum), b = b0 + i;
       const int s0 = __ldg(a.first + b) + (at - s_sum[i]) * kRun, count = min(kRun, __ldg(a.last + b) - s0);
-      // lane x looks up token x
+      // lane x of every warp looks up token x
       int code_page = -1, from = -1, to = -1;
       if (lane < count) {
         const int s = s0 + lane, c = fdiv(s, a.div_block), p = fdiv(s, a.div_page);
@@ -255,13 +255,13 @@ __global__ void __launch_bounds__(kQThreads) kv_dequantize_kernel(const __grid_c
         }
       }
       const int total = count * per;
-      for (int v0 = lane; v0 - lane < total; v0 += 32 * kRFlight) {
+      for (int v0 = threadIdx.x; v0 - lane < total; v0 += kQThreads * kRFlight) {
         uint4 x[kRFlight];
         float scale[kRFlight];
         long long out[kRFlight];
 #pragma unroll
         for (int q = 0; q < kRFlight; ++q) {
-          const int v = v0 + 32 * q, tok = v < total ? fdiv(v, a.div_per) : 0, r = v - tok * per;
+          const int v = v0 + kQThreads * q, tok = v < total ? fdiv(v, a.div_per) : 0, r = v - tok * per;
           const int f = __shfl_sync(0xffffffffu, from, tok), t = __shfl_sync(0xffffffffu, to, tok);
           const int cp = __shfl_sync(0xffffffffu, code_page, tok);
           out[q] = v < total && f >= 0 ? (long long)t * entry + r * 16 : -1;
@@ -358,7 +358,7 @@ cudaError_t launch_kv_dequantize(const Kv8Args& args, bool bf16, bool e4m3, int 
   Kv8Args a = args;
   set_divisions(a, a.Hkv * a.D / 16);
   const long long most = min((long long)a.max_pages * a.page_size, (long long)a.max_code_pages * a.block);
-  const dim3 grid(ctas(a, (a.B * ((most + kRun - 1) / kRun) + 3) / 4, sms), 2 * a.layers);
+  const dim3 grid(ctas(a, a.B * ((most + kRun - 1) / kRun), sms), 2 * a.layers);
   if (bf16 && e4m3)
     kv_dequantize_kernel<uint16_t, true><<<grid, kQThreads, 0, s>>>(a);
   else if (bf16)
