@@ -189,7 +189,8 @@ int run_scratch(DeviceState* d, const sv::WsLayout& l, cudaStream_t stream, void
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(stream, &cap);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-  if (cap == cudaStreamCaptureStatusNone) {
+  // (what needs no preparation is allocated on the caller's stream)
+  if (cap == cudaStreamCaptureStatusNone && (l.zero_bytes || l.marker_bytes)) {
     std::lock_guard<std::mutex> lock(g_mu);
     if (!d->side) {
       e = cudaStreamCreateWithFlags(&d->side, cudaStreamNonBlocking);

@@ -45,11 +45,27 @@ struct Rows {
   static constexpr bool kTwo = sizeof(S) == 4;  // two fp16 parts
   static constexpr int kSteps = DP / 16, kChunks = DP / 64, NT = DP / 8, kParts = kTwo ? 2 : 1;
   static constexpr int kFrag = kSteps * 32;                  // uint4's of one row tile's queries
+  // A warp's ring: 16 keys' codes, their values' and both scales a stage.
+  static constexpr int kStages = DP < 256 ? 4 : kTwo ? 2 : 3, kStage = 2 * 16 * DP + 2 * 16 * 4;
+  static_assert(MT * NT * 4 * 32 * 4 <= kARWarps * kStages * kStage, "the warps' sums go over the rings");
+  // Where 16 bytes (unit u) of a row lie: both products' reads fall on all banks.
+  static __device__ __forceinline__ int at(int row, int u) {
+    const int turn = DP == 64 ? (row & 2) : ((row ^ (row >> 2)) & 1) << 2 | (row & 2);
+    return row * DP + ((u ^ turn) << 4);
+  }
   static constexpr size_t smem(int T, bool tree) {
-    return (size_t)MT * kParts * kFrag * 16 + (size_t)MT * NT * 4 * 32 * 4 + 2 * kARWarps * 16 * MT * 4 + 16 * MT * 4 +
+    return (size_t)MT * kParts * kFrag * 16 + (size_t)kARWarps * kStages * kStage + 2 * kARWarps * 16 * MT * 4 + 16 * MT * 4 +
            (tree ? (size_t)T * 4 + (size_t)16 * MT * ((T + 31) / 32) * 4 : 0);
   }
 };
+
+// 16 bytes (zeros where !in) or 4 from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
 
 template <class S>
 __device__ __forceinline__ float value_of(S x);
@@ -73,6 +89,16 @@ __device__ __forceinline__ void plain_values(const S* p, float (&f)[N]) {
     }
   }
 }
+template <class S>
+__device__ __forceinline__ void four_values(const S* p, float (&f)[4]) {
+  if constexpr (sizeof(S) == 4) {
+    const uint4 v = *(const uint4*)p;
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  } else {
+    const uint2 v = *(const uint2*)p;
+    f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+  }
+}
 template <int N>
 __device__ __forceinline__ unsigned top_bits(const float (&f)[N]) {
   unsigned m = 0;
@@ -87,12 +113,11 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
   constexpr int NT = R::NT, kChunks = R::kChunks, kRows = 16 * MT;
   constexpr bool kTwo = R::kTwo;
   constexpr int VW = DP / 32;               // words of V's codes per key and lane
-  constexpr bool kAhead = DP <= 128;        // the next unit's K is in flight
-  constexpr bool kAheadV = DP * MT <= 128;  // ... and its V
   extern __shared__ __align__(16) unsigned char s_attend[];
   uint4* s_q = (uint4*)s_attend;                                   // [MT][parts][steps][32]
-  float* s_acc = (float*)(s_q + MT * R::kParts * R::kFrag);        // [MT][NT][4][32]
-  float* s_m = s_acc + MT * NT * 4 * 32;                           // [warps][rows], then sums
+  unsigned char* s_ring = (unsigned char*)(s_q + MT * R::kParts * R::kFrag);  // the warps' rings, then
+  float* s_acc = (float*)s_ring;                                              // [MT][NT][4][32]
+  float* s_m = (float*)(s_ring + kARWarps * R::kStages * R::kStage);          // [warps][rows], then sums
   float* s_l = s_m + kARWarps * kRows;
   float* s_qs = s_l + kARWarps * kRows;                            // [rows]
   int* s_par = (int*)(s_qs + kRows);                               // [T]
@@ -282,73 +307,51 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
         within = key - block * a.block;
         page = __ldg(table + block);
       };
-      struct Tile {
-        uint4 k[2][kChunks];
-        uint32_t v[4][VW];
-        float sk, sv;
-      };
-      long long at_v[4];
-      auto load_v = [&](Tile& x) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint8_t* p = vc + at_v[k] * entry + g * (DP / 8);
-          const bool on = g * (DP / 8) < a.D;
-          if constexpr (VW == 2) {
-            const uint2 y = on ? stream8(p) : make_uint2(0, 0);
-            x.v[k][0] = y.x, x.v[k][1] = y.y;
+      unsigned char* ring = s_ring + warp * R::kStages * R::kStage;
+      // Keys, values and scales of the tile that was looked up go to a stage of the warp's ring.
+      auto fetch = [&](int stage, bool some) {
+        if (some) {
+          const bool on = page >= 0 && page < a.code_pages;
+          const int e = on ? page * a.block + within : 0;
+          unsigned char* to = ring + stage * R::kStage;
+          float* scales = (float*)(to + 2 * 16 * DP);
+          if (on) {
+            copy4(scales + lane, (lane < 16 ? a.k_scales : a.v_scales) + (long long)page * a.Hkv + w.h);
           } else {
+            scales[lane] = __uint_as_float(0x7fffffffu);
+            atomicOr(a.status, kStatusBadData);
+          }
 #pragma unroll
-            for (int i = 0; i < VW / 4; ++i) {
-              const uint4 y = on && g * (DP / 8) + 16 * i < a.D ? stream16(p + 16 * i) : make_uint4(0, 0, 0, 0);
-              x.v[k][4 * i] = y.x, x.v[k][4 * i + 1] = y.y, x.v[k][4 * i + 2] = y.z, x.v[k][4 * i + 3] = y.w;
-            }
+          for (int j = 0; j < DP / 32; ++j) {
+            const int x = lane + 32 * j, row = x / (DP / 16), u = x % (DP / 16);
+            const long long from = __shfl_sync(0xffffffffu, e, row) * entry + 16 * u;
+            const bool in = 16 * u < a.D;  // (zeros behind the head)
+            copy16(to + R::at(row, u), kc + (in ? from : 0), in);
+            copy16(to + 16 * DP + R::at(row, u), vc + (in ? from : 0), in);
           }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      auto load = [&](Tile& x) {  // the tile that was looked up
-        const bool on = page >= 0 && page < a.code_pages;
-        const int e = on ? page * a.block + within : 0;
-        x.sk = x.sv = __uint_as_float(0x7fffffffu);
-        if (on) {
-          x.sk = __ldg(a.k_scales + (long long)page * a.Hkv + w.h);
-          x.sv = __ldg(a.v_scales + (long long)page * a.Hkv + w.h);
-        } else {
-          atomicOr(a.status, kStatusBadData);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const long long at = __shfl_sync(0xffffffffu, e, g + 8 * k);
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            x.k[k][c] = 64 * c + 16 * t < a.D ? stream16(kc + at * entry + 64 * c + 16 * t) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) at_v[k] = __shfl_sync(0xffffffffu, e, 2 * t + (k & 1) + 8 * (k >> 1));
-        if constexpr (kAheadV) load_v(x);
-      };
-      Tile now;
+      constexpr int kAhead = R::kStages - 1;
       look(u0);
-      if constexpr (kAhead) {
-        load(now);
-        if (u0 + 1 < uc) look(u0 + 1);
+      for (int j = 0; j < kAhead; ++j) {
+        fetch(j, u0 + j < uc);
+        if (u0 + j + 1 < uc) look(u0 + j + 1);
       }
-#pragma unroll 2
+      int stage = 0;
       for (int u = u0; u < uc; ++u) {
-        Tile next;
-        if constexpr (!kAhead) {
-          load(now);
-          if (u + 1 < uc) look(u + 1);
-        }
-        if constexpr (!kAheadV) load_v(now);
-        if (kAhead && u + 1 < uc) {
-          load(next);
-          if (u + 2 < uc) look(u + 2);
-        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        __syncwarp();  // the tile is there, and all lanes are done with the last one
+        fetch(stage ? stage - 1 : kAhead, u + kAhead < uc);
+        if (u + kAhead + 1 < uc) look(u + kAhead + 1);
+        const unsigned char* from = ring + stage * R::kStage;
+        const float* scales = (const float*)(from + 2 * 16 * DP);
+        if (++stage == R::kStages) stage = 0;
         float c[MT][2][4] = {};
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
-          const uint32_t w0[4] = {now.k[0][ch].x, now.k[0][ch].y, now.k[0][ch].z, now.k[0][ch].w};
-          const uint32_t w1[4] = {now.k[1][ch].x, now.k[1][ch].y, now.k[1][ch].z, now.k[1][ch].w};
+          const uint4 k0 = *(const uint4*)(from + R::at(g, 4 * ch + t)), k1 = *(const uint4*)(from + R::at(g + 8, 4 * ch + t));
+          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             uint32_t b0, b1, b2, b3;
@@ -365,36 +368,47 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
           }
         }
         float sk[4], sv[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sk[k] = __shfl_sync(0xffffffffu, now.sk, 2 * t + (k & 1) + 8 * (k >> 1));
-          sv[k] = __shfl_sync(0xffffffffu, now.sv, 2 * t + (k & 1) + 8 * (k >> 1));
-        }
+        *(float2*)sk = *(const float2*)(scales + 2 * t), *(float2*)(sk + 2) = *(const float2*)(scales + 2 * t + 8);
+        *(float2*)sv = *(const float2*)(scales + 16 + 2 * t), *(float2*)(sv + 2) = *(const float2*)(scales + 24 + 2 * t);
         const int base = u * kARKeys + 16 * warp;
         uint4 wt[MT][R::kParts];
-        if (base + 16 > keys.codes || (a.parents ? base + 16 > w.s.len : base + 15 > first_seen))
-          weights(c, sk, sv, base, keys.codes, true, wt);
-        else
-          weights(c, sk, sv, base, keys.codes, false, wt);
+        weights(c, sk, sv, base, keys.codes, base + 16 > keys.codes || (a.parents ? base + 16 > w.s.len : base + 15 > first_seen), wt);
+        const unsigned char* values = from + 16 * DP;
+        constexpr int kWords = VW < 4 ? VW : 4;  // of a place, 16 bytes at most at a time
 #pragma unroll
-        for (int x = 0; x < VW; ++x) {
-          // codes of one place in the head, of the keys 2 t and 2 t + 1, side by side
-          const uint32_t lo0 = __byte_perm(now.v[0][x], now.v[1][x], 0x5140), hi0 = __byte_perm(now.v[0][x], now.v[1][x], 0x7362);
-          const uint32_t lo1 = __byte_perm(now.v[2][x], now.v[3][x], 0x5140), hi1 = __byte_perm(now.v[2][x], now.v[3][x], 0x7362);
-          uint32_t b0[4], b1[4];
-          Code<kE4m3>::word(lo0, b0[0], b0[1]);
-          Code<kE4m3>::word(hi0, b0[2], b0[3]);
-          Code<kE4m3>::word(lo1, b1[0], b1[1]);
-          Code<kE4m3>::word(hi1, b1[2], b1[3]);
+        for (int x0 = 0; x0 < VW; x0 += kWords) {
+          uint32_t v[4][kWords];
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
+          for (int k = 0; k < 4; ++k) {
+            const int row = 2 * t + (k & 1) + 8 * (k >> 1), byte = g * (DP / 8) + 4 * x0;
+            if constexpr (kWords == 2) {
+              const uint2 y = *(const uint2*)(values + R::at(row, byte >> 4) + (byte & 15));
+              v[k][0] = y.x, v[k][1] = y.y;
+            } else {
+              const uint4 y = *(const uint4*)(values + R::at(row, byte >> 4));
+              v[k][0] = y.x, v[k][1] = y.y, v[k][2] = y.z, v[k][3] = y.w;
+            }
+          }
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+          for (int x = 0; x < kWords; ++x) {
+            // codes of one place in the head, of the keys 2 t and 2 t + 1, side by side
+            const uint32_t lo0 = __byte_perm(v[0][x], v[1][x], 0x5140), hi0 = __byte_perm(v[0][x], v[1][x], 0x7362);
+            const uint32_t lo1 = __byte_perm(v[2][x], v[3][x], 0x5140), hi1 = __byte_perm(v[2][x], v[3][x], 0x7362);
+            uint32_t b0[4], b1[4];
+            Code<kE4m3>::word(lo0, b0[0], b0[1]);
+            Code<kE4m3>::word(hi0, b0[2], b0[3]);
+            Code<kE4m3>::word(lo1, b1[0], b1[1]);
+            Code<kE4m3>::word(hi1, b1[2], b1[3]);
 #pragma unroll
-              for (int part = 0; part < R::kParts; ++part) mma16816(o[i][4 * x + y], wt[i][part], b0[y], b1[y]);
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int part = 0; part < R::kParts; ++part) mma16816(o[i][4 * (x0 + x) + y], wt[i][part], b0[y], b1[y]);
+          }
         }
-        if constexpr (kAhead) now = next;
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 
     // ---- plain entries ----
@@ -475,28 +489,28 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       uint4 wt[MT][R::kParts];
       weights(c, sk, sv, base, keys.end, true, wt);
 #pragma unroll
-      for (int x = 0; x < NT / 8; ++x) {
-        float f[4][8];
+      for (int x = 0; x < NT / 4; ++x) {  // four values at a time: registers are scarce
+        float f[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-#pragma unroll
-          for (int y = 0; y < 8; ++y) f[k][y] = 0.f;
-          if (g * (DP / 8) + 8 * x < a.D && up[k] > 0.f) plain_values<S, 8>(from[k] + 8 * x, f[k]);
+          f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0.f;
+          if (g * (DP / 8) + 4 * x < a.D && up[k] > 0.f) four_values<S>(from[k] + 4 * x, f[k]);
         }
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
+        for (int y = 0; y < 4; ++y) {
           const float y0 = f[0][y] * up[0], y1 = f[1][y] * up[1], y2 = f[2][y] * up[2], y3 = f[3][y] * up[3];
           const uint32_t b0 = half2_of(y0, y1), b1 = half2_of(y2, y3);
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int part = 0; part < R::kParts; ++part) mma16816(o[i][8 * x + y], wt[i][part], b0, b1);
+            for (int part = 0; part < R::kParts; ++part) mma16816(o[i][4 * x + y], wt[i][part], b0, b1);
           if constexpr (kTwo) {
             const uint32_t r0 = rest_of(y0, y1, b0), r1 = rest_of(y2, y3, b1);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) mma16816(o[i][8 * x + y], wt[i][0], r0, r1);
+            for (int i = 0; i < MT; ++i) mma16816(o[i][4 * x + y], wt[i][0], r0, r1);
           }
         }
+        asm volatile("" ::: "memory");
       }
     }
 
@@ -617,11 +631,11 @@ static cudaError_t launch_rows(KvAttendArgs a, int sms, size_t* bytes, cudaStrea
   return e != cudaSuccess ? e : launch_join<S, DP, kRows>(a, grid, s);
 }
 
-// CTAs of an SM by what a thread needs: three of 168 registers spill at 128 values a head.
+// CTAs of an SM by the registers that a thread needs and by the rings.
 template <class S, bool kE4m3>
 static cudaError_t launch_rows_of(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s) {
   if (a.D <= 64) return launch_rows<S, kE4m3, 64, 1, sizeof(S) == 2 ? 4 : 3>(a, sms, bytes, s);
-  if (a.D <= 128) return launch_rows<S, kE4m3, 128, 1, 2>(a, sms, bytes, s);
+  if (a.D <= 128) return launch_rows<S, kE4m3, 128, 1, sizeof(S) == 2 ? 3 : 2>(a, sms, bytes, s);
   return launch_rows<S, kE4m3, 256, 1, 2>(a, sms, bytes, s);
 }
 

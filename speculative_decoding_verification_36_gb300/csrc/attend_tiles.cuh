@@ -381,10 +381,11 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
             unsigned top = masked ? 0u : r.top[slot];
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
+              const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1)) & 0xffffu;
+              if (!__any_sync(0xffffffffu, vis)) continue;
               uint32_t x[16];
               tc_load16(t_s + 16 * c, x);
               tc_loaded16(x);
-              const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1));
               unsigned bits = 0;  // of the largest scale; one that is not finite makes its weights NaN whatever the reference
 #pragma unroll
               for (int k = 0; k < 16; k += 4) {
@@ -409,10 +410,14 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
             const f2_t less = f2(-M, -M), by = f2(qs, qs);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              uint32_t x[16], p[8];
+              const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1)) & 0xffffu;
+              uint32_t x[16], p[8] = {};
+              if (!__any_sync(0xffffffffu, vis)) {
+                tc_store8(t_s + 8 * c, p);
+                continue;
+              }
               tc_load16(t_s + 16 * c, x);
               tc_loaded16(x);
-              const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1));
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
                 const float2 y = *(const float2*)(sk + 16 * c + k), v = *(const float2*)(sv + 16 * c + k);
