@@ -17,13 +17,20 @@ namespace sv {
 
 constexpr int kARThreads = 128;
 constexpr int kARWarps = kARThreads / 32;
+constexpr int kARRows = 8;              // of a tile
 constexpr int kARKeys = 16 * kARWarps;  // keys of a unit: 16 to a warp
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint2& b) {
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+// An 8 x 8 matrix of 16-bit values (row lane / 4, columns 2 (lane % 4) and the next) turned over.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ float2 floats_of(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 // What is left of two values behind their fp16 parts `w`.
@@ -32,30 +39,33 @@ __device__ __forceinline__ uint32_t rest_of(float lo, float hi, uint32_t w) {
   return half2_of(lo - f.x, hi - f.y);
 }
 
+// The keys are the products' 16 rows and the queries their 8 columns (an mma.sync takes
+// 8 clocks of an SM here, so half-empty sides cost as much as memory does):
+//   S^T = K Q^T, O^T = V^T P^T, and P^T turns between them by movmatrix.
 // A lane's place in the products (g = lane / 4, t = lane % 4).  The order in which a
 // product runs over its inner index is free, so a lane's operands are bytes that lie
-// together in memory and go from global memory to registers without a shuffle:
-//   q K^T, chunk c of 64 values: the lane's 16 codes of key g at 64 c + 16 t feed
+// together:
+//   K, chunk c of 64 values: the lane's 16 codes of the keys g and g + 8 at 64 c + 16 t feed
 //     four steps of 16 (step 4 c + s: its codes 4 s .. 4 s + 3);
-//   P V: the lane's DP / 8 codes of its keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 at g DP / 8
-//     are the columns n = g of the DP / 8 products, so that a row's sums of product j
-//     are the values 2 t DP / 8 + j and (2 t + 1) DP / 8 + j: DP / 4 in a row.
-template <class S, bool kE4m3, int DP, int MT>
+//   V: the lane's DP / 8 codes of its keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 at g DP / 8 are
+//     the rows g and g + 8 of the DP / 16 products, so that a lane's sums of the query rows
+//     2 t and 2 t + 1 are DP / 8 values in a row.
+template <class S, int DP>
 struct Rows {
   static constexpr bool kTwo = sizeof(S) == 4;  // two fp16 parts
-  static constexpr int kSteps = DP / 16, kChunks = DP / 64, NT = DP / 8, kParts = kTwo ? 2 : 1;
-  static constexpr int kFrag = kSteps * 32;                  // uint4's of one row tile's queries
+  static constexpr int kSteps = DP / 16, kChunks = DP / 64, NT = DP / 16, kParts = kTwo ? 2 : 1;
+  static constexpr int kFrag = kSteps * 32;  // uint2's of the queries
   // A warp's ring: 16 keys' codes, their values' and both scales a stage.
-  static constexpr int kStages = DP < 256 ? 4 : kTwo ? 2 : 3, kStage = 2 * 16 * DP + 2 * 16 * 4;
-  static_assert(MT * NT * 4 * 32 * 4 <= kARWarps * kStages * kStage, "the warps' sums go over the rings");
+  static constexpr int kStages = DP == 256 ? 3 : 4, kStage = 2 * 16 * DP + 2 * 16 * 4;
+  static_assert(NT * 4 * 32 * 4 <= kARWarps * kStages * kStage, "the warps' sums go over the rings");
   // Where 16 bytes (unit u) of a row lie: both products' reads fall on all banks.
   static __device__ __forceinline__ int at(int row, int u) {
     const int turn = DP == 64 ? (row & 2) : ((row ^ (row >> 2)) & 1) << 2 | (row & 2);
     return row * DP + ((u ^ turn) << 4);
   }
   static constexpr size_t smem(int T, bool tree) {
-    return (size_t)MT * kParts * kFrag * 16 + (size_t)kARWarps * kStages * kStage + 2 * kARWarps * 16 * MT * 4 + 16 * MT * 4 +
-           (tree ? (size_t)T * 4 + (size_t)16 * MT * ((T + 31) / 32) * 4 : 0);
+    return (size_t)kParts * kFrag * 8 + (size_t)kARWarps * kStages * kStage + 2 * kARWarps * kARRows * 4 + kARRows * 4 +
+           (tree ? (size_t)T * 4 + (size_t)kARRows * ((T + 31) / 32) * 4 : 0);
   }
 };
 
@@ -107,21 +117,21 @@ __device__ __forceinline__ unsigned top_bits(const float (&f)[N]) {
   return m;
 }
 
-template <class S, bool kE4m3, int DP, int MT, int kCtas>
+template <class S, bool kE4m3, int DP, int kCtas>
 __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __grid_constant__ KvAttendArgs a) {
-  using R = Rows<S, kE4m3, DP, MT>;
-  constexpr int NT = R::NT, kChunks = R::kChunks, kRows = 16 * MT;
+  using R = Rows<S, DP>;
+  constexpr int NT = R::NT, kChunks = R::kChunks, kRows = kARRows;
   constexpr bool kTwo = R::kTwo;
-  constexpr int VW = DP / 32;               // words of V's codes per key and lane
+  constexpr int VW = DP / 32;  // words of V's codes per key and lane
   extern __shared__ __align__(16) unsigned char s_attend[];
-  uint4* s_q = (uint4*)s_attend;                                   // [MT][parts][steps][32]
-  unsigned char* s_ring = (unsigned char*)(s_q + MT * R::kParts * R::kFrag);  // the warps' rings, then
-  float* s_acc = (float*)s_ring;                                              // [MT][NT][4][32]
-  float* s_m = (float*)(s_ring + kARWarps * R::kStages * R::kStage);          // [warps][rows], then sums
+  uint2* s_q = (uint2*)s_attend;                                      // [parts][steps][32]
+  unsigned char* s_ring = (unsigned char*)(s_q + R::kParts * R::kFrag);  // the warps' rings, then
+  float* s_acc = (float*)s_ring;                                      // [NT][4][32]
+  float* s_m = (float*)(s_ring + kARWarps * R::kStages * R::kStage);  // [warps][rows], then sums
   float* s_l = s_m + kARWarps * kRows;
-  float* s_qs = s_l + kARWarps * kRows;                            // [rows]
-  int* s_par = (int*)(s_qs + kRows);                               // [T]
-  uint32_t* s_bits = (uint32_t*)(s_par + a.T);                     // [rows][words]
+  float* s_qs = s_l + kARWarps * kRows;                               // [rows]
+  int* s_par = (int*)(s_qs + kRows);                                  // [T]
+  uint32_t* s_bits = (uint32_t*)(s_par + a.T);                        // [rows][words]
   __shared__ unsigned long long s_scan[kARThreads + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int words = (a.T + 31) / 32;
@@ -176,121 +186,97 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
 #pragma unroll
       for (int i = 0; i < DP / 32; ++i) {
         const int d = lane + 32 * i;
-        // value d: chunk d / 64, lane t = d % 64 / 16, step d % 16 / 4, register pair by d % 4 / 2
-        const int step = 4 * (d >> 6) + ((d & 15) >> 2), at = (r & 7) * 4 + ((d & 63) >> 4), reg = ((r >> 3) & 1) + 2 * ((d & 3) >> 1);
+        // value d: chunk d / 64, lane t = d % 64 / 16, step d % 16 / 4, register d % 4 / 2
+        const int step = 4 * (d >> 6) + ((d & 15) >> 2), at = r * 4 + ((d & 63) >> 4);
         const float y = finite ? x[i] * up : 0.f;
         const __half hi = __float2half_rn(y);
-        __half* to = (__half*)(s_q + ((r >> 4) * R::kParts * R::kSteps + step) * 32 + at) + reg * 2 + (d & 1);
+        __half* to = (__half*)(s_q + step * 32 + at) + (d & 3);
         *to = hi;
-        if (kTwo) to[R::kFrag * 8] = __float2half_rn(y - __half2float(hi));
+        if (kTwo) to[R::kFrag * 4] = __float2half_rn(y - __half2float(hi));
       }
     }
     __syncthreads();
 
-    // ---- the lane's rows ----
-    float qs[MT][2], m[MT][2], l[MT][2];
-    int seen[MT][2];  // a chain's last key
+    // ---- the lane's rows, 2 t and the next ----
+    float qs[2], m[2], l[2];
+    int seen[2];       // a chain's last key
+    unsigned ref[2];   // exponent bits above every scale of V that the row has seen
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 16 * i + 8 * e + g;
-        qs[i][e] = s_qs[r];
-        m[i][e] = kLow;
-        l[i][e] = 0.f;
-        seen[i][e] = w.s.len + fdiv(row0 + r, a.div_g);
-      }
+    for (int e = 0; e < 2; ++e) {
+      qs[e] = s_qs[2 * t + e];
+      m[e] = kLow;
+      l[e] = 0.f;
+      ref[e] = 11u;
+      seen[e] = w.s.len + fdiv(row0 + 2 * t + e, a.div_g);
+    }
     const int first_seen = w.s.len + fdiv(row0, a.div_g);
-    float o[MT][NT][4];
+    float o[NT][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
-    unsigned ref[MT][2];  // exponent bits above every scale of V that the row has seen
-#pragma unroll
-    for (int i = 0; i < MT; ++i) ref[i][0] = ref[i][1] = 11u;
+    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-    auto visible = [&](int i, int e, int key, int end) {
+    auto visible = [&](int e, int key, int end) {
       if (key >= end) return false;
-      if (!a.parents) return key <= seen[i][e];
+      if (!a.parents) return key <= seen[e];
       const int at = key - w.s.len;
-      return at < 0 || (lost ? false : ((s_bits[(16 * i + 8 * e + g) * words + (at >> 5)] >> (at & 31)) & 1u) != 0);
+      return at < 0 || (lost ? false : ((s_bits[(2 * t + e) * words + (at >> 5)] >> (at & 31)) & 1u) != 0);
     };
 
-    // Scores of 16 keys to weights; the lane's keys are base + 2 t + {0, 1, 8, 9}.
-    // sk, sv: their scales.  wt: the weights as products' left sides.
-    auto weights = [&](float (&c)[MT][2][4], const float (&sk)[4], const float (&sv)[4], int base, int end, bool masked,
-                       uint4 (&wt)[MT][R::kParts]) {
-      float x[MT][2][4];
-      unsigned top[4], all = 11u;  // exponents above the keys' scales of V; a scale that is not finite makes its weights NaN whatever the reference
+    // Scores of the keys base + g and base + g + 8 (c[0], c[1] and c[2], c[3]) to weights.
+    // sk, sv: the keys' scales.  wt: the weights as the products' right sides.
+    auto weights = [&](const float (&c)[4], const float (&sk)[2], const float (&sv)[2], int base, int end, bool masked, uint2 (&wt)[R::kParts]) {
+      float x[2][2];  // [row][key]
+      unsigned top[2];  // exponents above the keys' scales of V; a scale that is not finite makes its weights NaN whatever the reference
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        top[k] = __float_as_uint(sv[k]) < 0x7f800000u ? max((__float_as_uint(sv[k]) >> 23) + 1u, 11u) : 11u;
-        all = max(all, top[k]);
-      }
+      for (int k = 0; k < 2; ++k) top[k] = __float_as_uint(sv[k]) < 0x7f800000u ? (__float_as_uint(sv[k]) >> 23) + 1u : 0u;
       bool grow = false;
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          unsigned mine = masked ? 11u : all;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[i][e][k] = c[i][k >> 1][2 * e + (k & 1)] * sk[k] * qs[i][e];
-            if (masked) {
-              if (visible(i, e, base + 2 * t + (k & 1) + 8 * (k >> 1), end))
-                mine = max(mine, top[k]);
-              else
-                x[i][e][k] = -INFINITY;
-            }
-            grow |= x[i][e][k] > m[i][e] + kSlack;
-          }
-          grow |= mine > ref[i][e];
+        for (int k = 0; k < 2; ++k) {
+          x[e][k] = c[2 * k + e] * (sk[k] * qs[e]);
+          const bool see = !masked || visible(e, base + g + 8 * k, end);
+          if (!see) x[e][k] = -INFINITY;
+          grow |= x[e][k] > m[e] + kSlack || (see && top[k] > ref[e]);
         }
+      }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y = fmaxf(fmaxf(x[i][e][0], x[i][e][1]), fmaxf(x[i][e][2], x[i][e][3]));
-            unsigned to = ref[i][e];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (!masked || x[i][e][k] != -INFINITY) to = max(to, top[k]);
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-            y = fmaxf(y, m[i][e]);
-            to = max(to, __shfl_xor_sync(0xffffffffu, to, 1));
-            to = max(to, __shfl_xor_sync(0xffffffffu, to, 2));
-            const float f = ex2(m[i][e] - y), both = f * ex2((float)((int)ref[i][e] - (int)to));
-            m[i][e] = y;
-            ref[i][e] = to;
-            l[i][e] *= f;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) o[i][j][2 * e] *= both, o[i][j][2 * e + 1] *= both;
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        float y[2][4];
-#pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // 2^11 over the reference: weights stay below 2^15 and keep fp16's full precision 2^25 below it
-          const float over = __uint_as_float((265u - ref[i][e]) << 23);
+          float y = fmaxf(fmaxf(x[e][0], x[e][1]), m[e]);
+          unsigned to = ref[e];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float p = ex2(x[i][e][k] - m[i][e]);
-            l[i][e] += p;
-            y[e][k] = masked && x[i][e][k] == -INFINITY ? 0.f : p * (sv[k] * over);
+          for (int k = 0; k < 2; ++k)
+            if (!masked || x[e][k] != -INFINITY) to = max(to, top[k]);
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) {
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+            to = max(to, __shfl_xor_sync(0xffffffffu, to, d));
           }
+          const float f = ex2(m[e] - y), both = f * ex2((float)((int)ref[e] - (int)to));
+          m[e] = y;
+          ref[e] = to;
+          l[e] *= f;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) o[j][e] *= both, o[j][2 + e] *= both;
         }
-        wt[i][0] = make_uint4(half2_of(y[0][0], y[0][1]), half2_of(y[1][0], y[1][1]), half2_of(y[0][2], y[0][3]), half2_of(y[1][2], y[1][3]));
-        if constexpr (kTwo)
-          wt[i][1] = make_uint4(rest_of(y[0][0], y[0][1], wt[i][0].x), rest_of(y[1][0], y[1][1], wt[i][0].y),
-                                rest_of(y[0][2], y[0][3], wt[i][0].z), rest_of(y[1][2], y[1][3], wt[i][0].w));
       }
+      float y[2][2];  // [key][row]
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // 2^11 over the reference: weights stay below 2^15 and keep fp16's full precision 2^25 below it
+        const float over = __uint_as_float((265u - ref[e]) << 23);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float p = ex2(x[e][k] - m[e]);
+          l[e] += p;
+          y[k][e] = masked && x[e][k] == -INFINITY ? 0.f : p * (sv[k] * over);
+        }
+      }
+      const uint32_t w0 = half2_of(y[0][0], y[0][1]), w1 = half2_of(y[1][0], y[1][1]);
+      wt[0] = make_uint2(turned(w0), turned(w1));
+      if constexpr (kTwo) wt[1] = make_uint2(turned(rest_of(y[0][0], y[0][1], w0)), turned(rest_of(y[1][0], y[1][1], w1)));
     };
-    auto query = [&](int i, int part, int step) { return s_q[((i * R::kParts + part) * R::kSteps + step) * 32 + lane]; };
+    auto query = [&](int part, int step) { return s_q[(part * R::kSteps + step) * 32 + lane]; };
 
     // ---- codes ----
     const int n_codes = w.s.bad ? 0 : (keys.codes + kARKeys - 1) / kARKeys;
@@ -347,7 +333,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
         const unsigned char* from = ring + stage * R::kStage;
         const float* scales = (const float*)(from + 2 * 16 * DP);
         if (++stage == R::kStages) stage = 0;
-        float c[MT][2][4] = {};
+        float c[4] = {};
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
           const uint4 k0 = *(const uint4*)(from + R::at(g, 4 * ch + t)), k1 = *(const uint4*)(from + R::at(g + 8, 4 * ch + t));
@@ -358,20 +344,12 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
             Code<kE4m3>::word(w0[s], b0, b1);
             Code<kE4m3>::word(w1[s], b2, b3);
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int part = 0; part < R::kParts; ++part) {
-                const uint4 q = query(i, part, 4 * ch + s);
-                mma16816(c[i][0], q, b0, b1);
-                mma16816(c[i][1], q, b2, b3);
-              }
+            for (int part = 0; part < R::kParts; ++part) mma16816(c, b0, b2, b1, b3, query(part, 4 * ch + s));
           }
         }
-        float sk[4], sv[4];
-        *(float2*)sk = *(const float2*)(scales + 2 * t), *(float2*)(sk + 2) = *(const float2*)(scales + 2 * t + 8);
-        *(float2*)sv = *(const float2*)(scales + 16 + 2 * t), *(float2*)(sv + 2) = *(const float2*)(scales + 24 + 2 * t);
+        const float sk[2] = {scales[g], scales[g + 8]}, sv[2] = {scales[16 + g], scales[24 + g]};
         const int base = u * kARKeys + 16 * warp;
-        uint4 wt[MT][R::kParts];
+        uint2 wt[R::kParts];
         weights(c, sk, sv, base, keys.codes, base + 16 > keys.codes || (a.parents ? base + 16 > w.s.len : base + 15 > first_seen), wt);
         const unsigned char* values = from + 16 * DP;
         constexpr int kWords = VW < 4 ? VW : 4;  // of a place, 16 bytes at most at a time
@@ -400,11 +378,9 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
             Code<kE4m3>::word(lo1, b1[0], b1[1]);
             Code<kE4m3>::word(hi1, b1[2], b1[3]);
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
+            for (int y = 0; y < 4; y += 2)
 #pragma unroll
-              for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int part = 0; part < R::kParts; ++part) mma16816(o[i][4 * (x0 + x) + y], wt[i][part], b0[y], b1[y]);
+              for (int part = 0; part < R::kParts; ++part) mma16816(o[2 * (x0 + x) + y / 2], b0[y], b0[y + 1], b1[y], b1[y + 1], wt[part]);
           }
         }
       }
@@ -423,92 +399,93 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       const S* kc = (const S*)a.k_cache + (long long)w.h * a.D;
       const S* vc = (const S*)a.v_cache + (long long)w.h * a.D;
       const long long entry = (long long)a.Hkv * a.D;
-      float c[MT][2][4] = {};
-      float sk_own[2];
+      // K: the keys g and g + 8; their largest magnitudes first, then their parts
+      float c[4] = {}, sk[2], sv[2], up[2];
+      const S* from[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {  // key g + 8 k: its largest magnitude first, then its parts
+      for (int k = 0; k < 2; ++k) {
         const int at = __shfl_sync(0xffffffffu, e, g + 8 * k);
-        const S* from = kc + (long long)max(at, 0) * entry + 16 * t;
+        from[k] = kc + (long long)max(at, 0) * entry + 16 * t;
         unsigned top = 0;
 #pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch)
-          if (64 * ch + 16 * t < a.D) {
-            float f[16];
-            plain_values<S, 16>(from + 64 * ch, f);
+        for (int x = 0; x < DP / 16; ++x)
+          if (64 * (x / 4) + 16 * t < a.D) {
+            float f[4];
+            four_values<S>(from[k] + 64 * (x / 4) + 4 * (x & 3), f);
             top = max(top, top_bits(f));
           }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const bool finite = top < 0x7f800000u;
-        sk_own[k] = at < 0 || !finite ? __uint_as_float(0x7fffffffu) : scale_down(top);
-        const float up = scale_up(top);
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          float f[16] = {};
-          if (64 * ch + 16 * t < a.D && finite) plain_values<S, 16>(from + 64 * ch, f);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const float y0 = f[4 * s] * up, y1 = f[4 * s + 1] * up, y2 = f[4 * s + 2] * up, y3 = f[4 * s + 3] * up;
-            const uint32_t b0 = half2_of(y0, y1), b1 = half2_of(y2, y3);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int part = 0; part < R::kParts; ++part) mma16816(c[i][k], query(i, part, 4 * ch + s), b0, b1);
-            if constexpr (kTwo) {
-              const uint32_t r0 = rest_of(y0, y1, b0), r1 = rest_of(y2, y3, b1);
-#pragma unroll
-              for (int i = 0; i < MT; ++i) mma16816(c[i][k], query(i, 0, 4 * ch + s), r0, r1);
-            }
-          }
-        }
+        sk[k] = at < 0 || !finite ? __uint_as_float(0x7fffffffu) : scale_down(top);
+        up[k] = finite ? scale_up(top) : 0.f;
       }
-      // V: the lane's four keys
-      float sk[4], sv[4], up[4];
-      const S* from[4];
+#pragma unroll
+      for (int x = 0; x < DP / 16; ++x) {
+        float f[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (64 * (x / 4) + 16 * t < a.D && up[k] > 0.f) four_values<S>(from[k] + 64 * (x / 4) + 4 * (x & 3), f[k]);
+        uint32_t p[4], r[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            p[k + 2 * y] = half2_of(f[k][2 * y] * up[k], f[k][2 * y + 1] * up[k]);
+            if (kTwo) r[k + 2 * y] = rest_of(f[k][2 * y] * up[k], f[k][2 * y + 1] * up[k], p[k + 2 * y]);
+          }
+#pragma unroll
+        for (int part = 0; part < R::kParts; ++part) mma16816(c, p[0], p[1], p[2], p[3], query(part, x));
+        if constexpr (kTwo) mma16816(c, r[0], r[1], r[2], r[3], query(0, x));
+      }
+      // V: the scales of the keys 2 t, 2 t + 1, 2 t + 8 and 2 t + 9, then of g and g + 8
+      float of[4], raise[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int x = 2 * t + (k & 1);
-        sk[k] = __shfl_sync(0xffffffffu, sk_own[k >> 1], 4 * x);
-        const int at = __shfl_sync(0xffffffffu, e, x + 8 * (k >> 1));
+        const int at = __shfl_sync(0xffffffffu, e, 2 * t + (k & 1) + 8 * (k >> 1));
         from[k] = vc + (long long)max(at, 0) * entry + g * (DP / 8);
         unsigned top = 0;
 #pragma unroll
-        for (int i = 0; i < DP / 64; ++i)
-          if (g * (DP / 8) + 8 * i < a.D) {
-            float f[8];
-            plain_values<S, 8>(from[k] + 8 * i, f);
+        for (int x = 0; x < DP / 32; ++x)
+          if (g * (DP / 8) + 4 * x < a.D) {
+            float f[4];
+            four_values<S>(from[k] + 4 * x, f);
             top = max(top, top_bits(f));
           }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
         const bool finite = top < 0x7f800000u;
-        sv[k] = at < 0 || !finite ? __uint_as_float(0x7fffffffu) : scale_down(top);
-        up[k] = finite ? scale_up(top) : 0.f;
+        of[k] = at < 0 || !finite ? __uint_as_float(0x7fffffffu) : scale_down(top);
+        raise[k] = finite ? scale_up(top) : 0.f;
       }
-      uint4 wt[MT][R::kParts];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float even = __shfl_sync(0xffffffffu, of[2 * k], g >> 1), odd = __shfl_sync(0xffffffffu, of[2 * k + 1], g >> 1);
+        sv[k] = g & 1 ? odd : even;
+      }
+      uint2 wt[R::kParts];
       weights(c, sk, sv, base, keys.end, true, wt);
 #pragma unroll
-      for (int x = 0; x < NT / 4; ++x) {  // four values at a time: registers are scarce
-        float f[4][4];
+      for (int x = 0; x < DP / 32; ++x) {  // four values of a place at a time
+        float f[4][4] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0.f;
-          if (g * (DP / 8) + 4 * x < a.D && up[k] > 0.f) four_values<S>(from[k] + 4 * x, f[k]);
-        }
+        for (int k = 0; k < 4; ++k)
+          if (g * (DP / 8) + 4 * x < a.D && raise[k] > 0.f) four_values<S>(from[k] + 4 * x, f[k]);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float y0 = f[0][y] * up[0], y1 = f[1][y] * up[1], y2 = f[2][y] * up[2], y3 = f[3][y] * up[3];
-          const uint32_t b0 = half2_of(y0, y1), b1 = half2_of(y2, y3);
+        for (int y = 0; y < 4; y += 2) {
+          uint32_t p[4], r[4];
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int d = 0; d < 2; ++d)
 #pragma unroll
-            for (int part = 0; part < R::kParts; ++part) mma16816(o[i][4 * x + y], wt[i][part], b0, b1);
-          if constexpr (kTwo) {
-            const uint32_t r0 = rest_of(y0, y1, b0), r1 = rest_of(y2, y3, b1);
+            for (int k = 0; k < 2; ++k) {
+              const float y0 = f[2 * k][y + d] * raise[2 * k], y1 = f[2 * k + 1][y + d] * raise[2 * k + 1];
+              p[d + 2 * k] = half2_of(y0, y1);
+              if (kTwo) r[d + 2 * k] = rest_of(y0, y1, p[d + 2 * k]);
+            }
 #pragma unroll
-            for (int i = 0; i < MT; ++i) mma16816(o[i][4 * x + y], wt[i][0], r0, r1);
-          }
+          for (int part = 0; part < R::kParts; ++part) mma16816(o[2 * x + y / 2], p[0], p[1], p[2], p[3], wt[part]);
+          if constexpr (kTwo) mma16816(o[2 * x + y / 2], r[0], r[1], r[2], r[3], wt[0]);
         }
         asm volatile("" ::: "memory");
       }
@@ -516,46 +493,40 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
 
     // ---- the warps' sums become one ----
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 1);
-        l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 2);
-        if (lost) l[i][e] = __uint_as_float(0x7fffffffu);
-        if (t == 0) s_m[warp * kRows + 16 * i + 8 * e + g] = m[i][e], s_l[warp * kRows + 16 * i + 8 * e + g] = l[i][e];
-      }
+      for (int d = 4; d < 32; d *= 2) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+      if (lost) l[e] = __uint_as_float(0x7fffffffu);
+      if (g == 0) s_m[warp * kRows + 2 * t + e] = m[e], s_l[warp * kRows + 2 * t + e] = l[e];
+    }
     __syncthreads();
-    float factor[MT][2], back[MT][2];
+    float factor[2], back[2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * t + e;
+      float most = s_m[r];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 16 * i + 8 * e + g;
-        float most = s_m[r];
+      for (int x = 1; x < kARWarps; ++x) most = fmaxf(most, s_m[x * kRows + r]);
+      float sum = 0.f;
 #pragma unroll
-        for (int x = 1; x < kARWarps; ++x) most = fmaxf(most, s_m[x * kRows + r]);
-        float sum = 0.f;
-#pragma unroll
-        for (int x = 0; x < kARWarps; ++x) sum += s_l[x * kRows + r] * ex2(s_m[x * kRows + r] - most);
-        // 2^(ref - 138) in two steps: it may lie below fp32's normal values
-        const int half = ((int)ref[i][e] - 138) / 2;
-        factor[i][e] = ex2(m[i][e] - most) * __uint_as_float((unsigned)(127 + half) << 23);
-        back[i][e] = __uint_as_float((unsigned)((int)ref[i][e] - 11 - half) << 23);
-        m[i][e] = most;
-        l[i][e] = sum;
-      }
+      for (int x = 0; x < kARWarps; ++x) sum += s_l[x * kRows + r] * ex2(s_m[x * kRows + r] - most);
+      // 2^(ref - 138) in two steps: it may lie below fp32's normal values
+      const int half = ((int)ref[e] - 138) / 2;
+      factor[e] = ex2(m[e] - most) * __uint_as_float((unsigned)(127 + half) << 23);
+      back[e] = __uint_as_float((unsigned)((int)ref[e] - 11 - half) << 23);
+      m[e] = most;
+      l[e] = sum;
+    }
     for (int x = 0; x < kARWarps; ++x) {
       if (warp == x) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float* to = s_acc + ((i * NT + j) * 4 + e) * 32 + lane;
-              const float y = o[i][j][e] * factor[i][e >> 1] * back[i][e >> 1];
-              *to = x ? *to + y : y;
-            }
+          for (int e = 0; e < 4; ++e) {
+            float* to = s_acc + (j * 4 + e) * 32 + lane;
+            const float y = o[j][e] * factor[e & 1] * back[e & 1];
+            *to = x ? *to + y : y;
+          }
       }
       __syncthreads();
     }
@@ -563,18 +534,14 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
     // ---- out, or to the workspace ----
     const bool whole = u0 == 0 && u1 == n;
     float* part = a.part + (2LL * blockIdx.x + (u0 == 0)) * attend_slot(kRows, DP);
-    // item: a row's half c and eight of its values in a row
-    for (int x = warp; x < MT * 4 * (NT / 8); x += kARWarps) {
-      const int oct = x % (NT / 8), c = x / (NT / 8) % 4, i = x / (NT / 8) / 4;
-      const int r = 16 * i + 8 * (c >> 1) + g, d = (2 * t + (c & 1)) * NT + 8 * oct;
+    // item: row 2 t + e of a lane, eight of its values in a row
+    for (int x = warp; x < 2 * (NT / 4); x += kARWarps) {
+      const int e = x & 1, oct = x >> 1, r = 2 * t + e, d = g * (DP / 8) + 8 * oct;
       if (row0 + r >= rows || d >= a.D) continue;
-      float sum = 0.f, f[8];
+      const float by = !whole ? 1.f : l[0] == 0.f && !e || l[1] == 0.f && e ? 0.f : 1.f / (e ? l[1] : l[0]);
+      float f[8];
 #pragma unroll
-      for (int y = 0; y < MT; ++y)
-        if (i == y) sum = c >> 1 ? l[y][1] : l[y][0];
-      const float by = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-      for (int y = 0; y < 8; ++y) f[y] = s_acc[((i * NT + 8 * oct + y) * 4 + c) * 32 + lane] * by;
+      for (int y = 0; y < 8; ++y) f[y] = s_acc[((4 * oct + y / 2) * 4 + 2 * (y & 1) + e) * 32 + lane] * by;
       if (whole) {
         const int token = fdiv(row0 + r, a.div_g);
         attend_store8<S>((S*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + r - token * a.G) * a.D + d, f);
@@ -583,14 +550,12 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       }
     }
     if (!whole) {
-      if (warp == 0 && t == 0)
+      if (warp == 0 && g == 0)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            part[kRows * DP + 16 * i + 8 * e + g] = m[i][e];
-            part[kRows * DP + kRows + 16 * i + 8 * e + g] = l[i][e];
-          }
+        for (int e = 0; e < 2; ++e) {
+          part[kRows * DP + 2 * t + e] = m[e];
+          part[kRows * DP + kRows + 2 * t + e] = l[e];
+        }
       if (u0 == 0) {
         meta_last = attend_share_of(w, w.from + n - 1);
         meta_b = w.b, meta_h = w.h, meta_tile = w.tile;
@@ -605,11 +570,11 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
 // launch
 // ---------------------------------------------------------------------------
 // With `bytes`, only says how much workspace (a.part) the launch takes.
-template <class S, bool kE4m3, int DP, int MT, int kCtas>
+template <class S, bool kE4m3, int DP, int kCtas>
 static cudaError_t launch_rows(KvAttendArgs a, int sms, size_t* bytes, cudaStream_t s) {
-  using R = Rows<S, kE4m3, DP, MT>;
-  constexpr int kRows = 16 * MT;
-  auto kernel = attend_rows_kernel<S, kE4m3, DP, MT, kCtas>;
+  using R = Rows<S, DP>;
+  constexpr int kRows = kARRows;
+  auto kernel = attend_rows_kernel<S, kE4m3, DP, kCtas>;
   a.tiles = (int)(((long long)a.T * a.G + kRows - 1) / kRows);
   const size_t smem = R::smem(a.T, a.parents != nullptr);
   // no more CTAs than units can be
@@ -634,9 +599,9 @@ static cudaError_t launch_rows(KvAttendArgs a, int sms, size_t* bytes, cudaStrea
 // CTAs of an SM by the registers that a thread needs and by the rings.
 template <class S, bool kE4m3>
 static cudaError_t launch_rows_of(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s) {
-  if (a.D <= 64) return launch_rows<S, kE4m3, 64, 1, sizeof(S) == 2 ? 4 : 3>(a, sms, bytes, s);
-  if (a.D <= 128) return launch_rows<S, kE4m3, 128, 1, sizeof(S) == 2 ? 3 : 2>(a, sms, bytes, s);
-  return launch_rows<S, kE4m3, 256, 1, 2>(a, sms, bytes, s);
+  if (a.D <= 64) return launch_rows<S, kE4m3, 64, 5>(a, sms, bytes, s);
+  if (a.D <= 128) return launch_rows<S, kE4m3, 128, 3>(a, sms, bytes, s);
+  return launch_rows<S, kE4m3, 256, 2>(a, sms, bytes, s);
 }
 
 }  // namespace sv
