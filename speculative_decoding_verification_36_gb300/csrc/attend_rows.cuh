@@ -84,21 +84,7 @@ __device__ __forceinline__ float value_of<uint32_t>(uint32_t x) { return __uint_
 template <>
 __device__ __forceinline__ float value_of<uint16_t>(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
 
-// N values from memory (N * sizeof(S) a multiple of 16 bytes), in fp32.
-template <class S, int N>
-__device__ __forceinline__ void plain_values(const S* p, float (&f)[N]) {
-#pragma unroll
-  for (int i = 0; i < N * (int)sizeof(S) / 16; ++i) {
-    const uint4 v = ((const uint4*)p)[i];
-    if constexpr (sizeof(S) == 4) {
-      f[4 * i] = __uint_as_float(v.x), f[4 * i + 1] = __uint_as_float(v.y), f[4 * i + 2] = __uint_as_float(v.z),
-                                  f[4 * i + 3] = __uint_as_float(v.w);
-    } else {
-      f[8 * i] = bf16_lo(v.x), f[8 * i + 1] = bf16_hi(v.x), f[8 * i + 2] = bf16_lo(v.y), f[8 * i + 3] = bf16_hi(v.y);
-      f[8 * i + 4] = bf16_lo(v.z), f[8 * i + 5] = bf16_hi(v.z), f[8 * i + 6] = bf16_lo(v.w), f[8 * i + 7] = bf16_hi(v.w);
-    }
-  }
-}
+// Four values in fp32.
 template <class S>
 __device__ __forceinline__ void four_values(const S* p, float (&f)[4]) {
   if constexpr (sizeof(S) == 4) {
@@ -298,7 +284,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       auto fetch = [&](int stage, bool some) {
         if (some) {
           const bool on = page >= 0 && page < a.code_pages;
-          const int e = on ? page * a.block + within : 0;
+          const int e = on ? page * a.block + within : -1;
           unsigned char* to = ring + stage * R::kStage;
           float* scales = (float*)(to + 2 * 16 * DP);
           if (on) {
@@ -310,8 +296,10 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
 #pragma unroll
           for (int j = 0; j < DP / 32; ++j) {
             const int x = lane + 32 * j, row = x / (DP / 16), u = x % (DP / 16);
-            const long long from = __shfl_sync(0xffffffffu, e, row) * entry + 16 * u;
-            const bool in = 16 * u < a.D;  // (zeros behind the head)
+            const int of = __shfl_sync(0xffffffffu, e, row);
+            const long long from = of * entry + 16 * u;
+            // zeros behind the head, and for a page outside: a row that does not see it would get 0 * NaN
+            const bool in = of >= 0 && 16 * u < a.D;
             copy16(to + R::at(row, u), kc + (in ? from : 0), in);
             copy16(to + 16 * DP + R::at(row, u), vc + (in ? from : 0), in);
           }

@@ -47,7 +47,7 @@ struct Tiles {
     float sk[kATRing][kATKeys], sv[kATRing][kATKeys];
     int kind[kATRing];
     unsigned at[kATRing][kATKeys];   // where a key's head lies in its pool, in 16 bytes (0: a page outside); the keys of a loading thread side by side
-    unsigned outside[kATRing][kATKeys / 32];  // keys whose page is outside, as bits
+    alignas(8) unsigned outside[kATRing][kATKeys / 32];  // keys whose page is outside, as bits
     unsigned top[kATRing];         // exponent bits above a unit's scales of V
     uint32_t bits[kATRows][4];
     int parents[128];
@@ -85,14 +85,7 @@ __device__ __forceinline__ void tc_mma_t(uint32_t d, uint32_t a, unsigned long l
 }
 #define SV_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define SV_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
-// 32 columns of the warp's 32 lanes (a register a column)
-__device__ __forceinline__ void tc_load32(uint32_t at, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24)
-      : "r"(at));
-}
+// 16 columns of the warp's 32 lanes (a register a column)
 __device__ __forceinline__ void tc_load16(uint32_t at, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                : SV_R8(r, 0), SV_R8(r, 8)
@@ -174,13 +167,16 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&r.tmem;
   const uint32_t t_q = tmem + 64, t_o = tmem + 128;  // S, then its weights, at 0
-  // Once a wait has run out all warps go on without waiting and take part in every
-  // barrier that is left: no warp waits for one that is gone.
+  // Whether the phase has come.  Once a wait has run out (`tries` is 0) all warps go on without
+  // waiting and take part in every barrier that is left: no warp waits for one that is gone.
+  // Phases then say nothing any more: no place is used, none is written over, and nothing
+  // arrives for more than one.
   auto wait = [&](unsigned long long* bar, unsigned parity) {
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return;
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return true;
     for (unsigned n = __reduce_min_sync(0xffffffffu, r.tries); n > 0; --n)
-      if (__all_sync(0xffffffffu, mbar_try(bar, parity & 1))) return;
+      if (__all_sync(0xffffffffu, mbar_try(bar, parity & 1))) return true;
     r.tries = 0;
+    return false;
   };
 
   if (warp < kATSoft) {
@@ -278,6 +274,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
       for (int u = active ? u0 : u1; u < u1; ++u, ++i) {
         wait(&r.s_full, i);
         tc_after();
+        const bool alive = r.tries != 0;
         if (!w.s.bad) {
           const int slot = i & (kATRing - 1);
           const float *sk = r.sk[slot], *sv = r.sv[slot];
@@ -441,7 +438,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         }
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_n(&r.p_ready, arrivals);
+        if (lane == 0 && alive) mbar_arrive_n(&r.p_ready, arrivals);
       }
       // ---- out, or to the workspace ----
       if (active) {
@@ -518,29 +515,39 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     auto pool = [&](int kind) {
       return (kind == kATPlain ? (const char*)(values ? a.v_cache : a.k_cache) : (const char*)(values ? a.v_codes : a.k_codes)) + (part_of << kind);
     };
-    auto load = [&](int j, uint4 (&to)[kRounds]) {
+    auto load = [&](int j, uint4 (&to)[kRounds], int& kind) {
       const int slot = j & (kATRing - 1);
       wait(&r.at_full[slot], j / kATRing);
-      const int kind = r.kind[slot];
+      const bool come = r.tries != 0;
+      kind = come ? r.kind[slot] : kATNone;
       // one load whatever the kind: where two paths met, their values would have to be there
       const char* from = pool(kind == kATPlain ? kATPlain : kATCodes);
       unsigned at[kRounds];
       places(slot, at);
 #pragma unroll
-      for (int q = 0; q < kRounds; ++q) to[q] = stream16(from + at[q] * 16ull);
+      for (int q = 0; q < kRounds; ++q) to[q] = stream16(from + (come ? at[q] : 0u) * 16ull);
     };
-    if (units > 0) load(0, c[0]);
-    if (units > 1) load(1, c[1]);
+    int kinds[2];
+    if (units > 0) load(0, c[0], kinds[0]);
+    if (units > 1) load(1, c[1], kinds[1]);
     int stage = 0, lap = 0;
     for (int i0 = 0; i0 < units; i0 += 2) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int i = i0 + b, slot = i & (kATRing - 1);
         if (i >= units) break;
-        const int kind = r.kind[slot];
+        const int kind = kinds[b];
         unsigned char* to = operand + stage * L::kTile;
         if (lap) wait(&is_empty[stage], lap + 1);  // what lay there has been read
         if (kind == kATCodes) {
+          // what stands for a page outside may hold anything: a row that does not see it would get 0 * NaN
+          if (*(const unsigned long long*)r.outside[slot]) {
+#pragma unroll
+            for (int q = 0; q < kRounds; ++q) {
+              const int key = mine + q * kAtOnce;
+              if (r.outside[slot][key >> 5] >> (key & 31) & 1u) c[b][q] = make_uint4(0, 0, 0, 0);
+            }
+          }
           if (on) {
 #pragma unroll
             for (int q = 0; q < kRounds; ++q) {
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         __syncwarp();
         if (lane == 0) mbar_arrive(&is_full[stage]);
         if (++stage == kATStages) stage = 0, ++lap;
-        if (i + 2 < units) load(i + 2, c[b]);
+        if (i + 2 < units) load(i + 2, c[b], kinds[b]);
       }
     }
   } else {
@@ -677,6 +684,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
             }
           }
           if (i >= kATRing) wait(&r.at_empty[slot], i / kATRing + 1);
+          if (r.tries == 0) continue;  // nothing is looked up any more
           if (!w.s.bad) {
             float sk[kQ], sv[kQ];
             unsigned top = 0;
