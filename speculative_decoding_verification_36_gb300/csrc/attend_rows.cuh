@@ -26,6 +26,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
+// The products' own sums drop bits instead of rounding, which adds up over a long sequence: in fp32
+// calls a product's sum starts at zero, its smaller parts first, and is added here.
+__device__ __forceinline__ void add4(float (&c)[4], const float (&d)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] += d[i];
+}
 // An 8 x 8 matrix of 16-bit values (row lane / 4, columns 2 (lane % 4) and the next) turned over.
 __device__ __forceinline__ uint32_t turned(uint32_t x) {
   uint32_t y;
@@ -321,9 +327,10 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
         const unsigned char* from = ring + stage * R::kStage;
         const float* scales = (const float*)(from + 2 * 16 * DP);
         if (++stage == R::kStages) stage = 0;
-        float c[4] = {};
+        float c[4] = {}, low[4] = {};
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
+          float part_of[4] = {};
           const uint4 k0 = *(const uint4*)(from + R::at(g, 4 * ch + t)), k1 = *(const uint4*)(from + R::at(g + 8, 4 * ch + t));
           const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -331,10 +338,16 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
             uint32_t b0, b1, b2, b3;
             Code<kE4m3>::word(w0[s], b0, b1);
             Code<kE4m3>::word(w1[s], b2, b3);
-#pragma unroll
-            for (int part = 0; part < R::kParts; ++part) mma16816(c, b0, b2, b1, b3, query(part, 4 * ch + s));
+            if constexpr (kTwo) {
+              mma16816(part_of, b0, b2, b1, b3, query(0, 4 * ch + s));
+              mma16816(low, b0, b2, b1, b3, query(1, 4 * ch + s));
+            } else {
+              mma16816(c, b0, b2, b1, b3, query(0, 4 * ch + s));
+            }
           }
+          if constexpr (kTwo) add4(c, part_of);
         }
+        if constexpr (kTwo) add4(c, low);
         const float sk[2] = {scales[g], scales[g + 8]}, sv[2] = {scales[16 + g], scales[24 + g]};
         const int base = u * kARKeys + 16 * warp;
         uint2 wt[R::kParts];
@@ -366,9 +379,16 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
             Code<kE4m3>::word(lo1, b1[0], b1[1]);
             Code<kE4m3>::word(hi1, b1[2], b1[3]);
 #pragma unroll
-            for (int y = 0; y < 4; y += 2)
-#pragma unroll
-              for (int part = 0; part < R::kParts; ++part) mma16816(o[2 * (x0 + x) + y / 2], b0[y], b0[y + 1], b1[y], b1[y + 1], wt[part]);
+            for (int y = 0; y < 4; y += 2) {
+              if constexpr (kTwo) {
+                float part_of[4] = {};
+                mma16816(part_of, b0[y], b0[y + 1], b1[y], b1[y + 1], wt[1]);
+                mma16816(part_of, b0[y], b0[y + 1], b1[y], b1[y + 1], wt[0]);
+                add4(o[2 * (x0 + x) + y / 2], part_of);
+              } else {
+                mma16816(o[2 * (x0 + x) + y / 2], b0[y], b0[y + 1], b1[y], b1[y + 1], wt[0]);
+              }
+            }
           }
         }
       }
@@ -388,7 +408,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       const S* vc = (const S*)a.v_cache + (long long)w.h * a.D;
       const long long entry = (long long)a.Hkv * a.D;
       // K: the keys g and g + 8; their largest magnitudes first, then their parts
-      float c[4] = {}, sk[2], sv[2], up[2];
+      float c[4] = {}, low[4] = {}, sk[2], sv[2], up[2];
       const S* from[4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -422,10 +442,17 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
             p[k + 2 * y] = half2_of(f[k][2 * y] * up[k], f[k][2 * y + 1] * up[k]);
             if (kTwo) r[k + 2 * y] = rest_of(f[k][2 * y] * up[k], f[k][2 * y + 1] * up[k], p[k + 2 * y]);
           }
-#pragma unroll
-        for (int part = 0; part < R::kParts; ++part) mma16816(c, p[0], p[1], p[2], p[3], query(part, x));
-        if constexpr (kTwo) mma16816(c, r[0], r[1], r[2], r[3], query(0, x));
+        if constexpr (kTwo) {
+          float part_of[4] = {};
+          mma16816(part_of, p[0], p[1], p[2], p[3], query(0, x));
+          add4(c, part_of);
+          mma16816(low, p[0], p[1], p[2], p[3], query(1, x));
+          mma16816(low, r[0], r[1], r[2], r[3], query(0, x));
+        } else {
+          mma16816(c, p[0], p[1], p[2], p[3], query(0, x));
+        }
       }
+      if constexpr (kTwo) add4(c, low);
       // V: the scales of the keys 2 t, 2 t + 1, 2 t + 8 and 2 t + 9, then of g and g + 8
       float of[4], raise[4];
 #pragma unroll
@@ -471,9 +498,15 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
               p[d + 2 * k] = half2_of(y0, y1);
               if (kTwo) r[d + 2 * k] = rest_of(y0, y1, p[d + 2 * k]);
             }
-#pragma unroll
-          for (int part = 0; part < R::kParts; ++part) mma16816(o[2 * x + y / 2], p[0], p[1], p[2], p[3], wt[part]);
-          if constexpr (kTwo) mma16816(o[2 * x + y / 2], r[0], r[1], r[2], r[3], wt[0]);
+          if constexpr (kTwo) {
+            float part_of[4] = {};
+            mma16816(part_of, p[0], p[1], p[2], p[3], wt[1]);
+            mma16816(part_of, r[0], r[1], r[2], r[3], wt[0]);
+            mma16816(part_of, p[0], p[1], p[2], p[3], wt[0]);
+            add4(o[2 * x + y / 2], part_of);
+          } else {
+            mma16816(o[2 * x + y / 2], p[0], p[1], p[2], p[3], wt[0]);
+          }
         }
         asm volatile("" ::: "memory");
       }
@@ -584,11 +617,12 @@ static cudaError_t launch_rows(KvAttendArgs a, int sms, size_t* bytes, cudaStrea
   return e != cudaSuccess ? e : launch_join<S, DP, kRows>(a, grid, s);
 }
 
-// CTAs of an SM by the registers that a thread needs and by the rings.
+// CTAs of an SM by the registers that a thread needs without spilling (fp32 calls hold two
+// parts of everything) and by the rings.
 template <class S, bool kE4m3>
 static cudaError_t launch_rows_of(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s) {
-  if (a.D <= 64) return launch_rows<S, kE4m3, 64, 5>(a, sms, bytes, s);
-  if (a.D <= 128) return launch_rows<S, kE4m3, 128, 3>(a, sms, bytes, s);
+  if (a.D <= 64) return launch_rows<S, kE4m3, 64, sizeof(S) == 4 ? 4 : 5>(a, sms, bytes, s);
+  if (a.D <= 128) return launch_rows<S, kE4m3, 128, sizeof(S) == 4 ? 2 : 3>(a, sms, bytes, s);
   return launch_rows<S, kE4m3, 256, 2>(a, sms, bytes, s);
 }
 
