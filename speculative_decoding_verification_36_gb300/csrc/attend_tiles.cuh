@@ -33,7 +33,7 @@ static_assert(kATCtas * kATThreads * 64 <= 65536 && 32 * kATSoft * kATSoftRegs +
               "registers");
 constexpr int kATStages = 2;  // units whose keys and values are in shared memory
 constexpr int kATRing = 8;    // units whose places and scales are held
-constexpr int kATCodes = 0, kATPlain = 1, kATNone = 2;  // kinds of units (log2 of a value's bytes); the last: a bad sequence's
+constexpr int kATCodes = 0, kATPlain = 1, kATNone = 2;  // kinds of units (log2 of a value's bytes); the last: a bad sequence's, or one without pages
 constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
 constexpr unsigned kATLeastRef = 64;  // values below 2^-82 lose bits, which keeps a row's sum below 2^128
 
@@ -46,8 +46,10 @@ struct Tiles {
   struct Rest {
     float sk[kATRing][kATKeys], sv[kATRing][kATKeys];
     int kind[kATRing];
-    unsigned at[kATRing][kATKeys];   // where a key's head lies in its pool, in 16 bytes (0: a page outside); the keys of a loading thread side by side
-    alignas(8) unsigned outside[kATRing][kATKeys / 32];  // keys whose page is outside, as bits
+    // where a key's head lies in the pool of codes and in that of plain entries, in 16 bytes (0: a page
+    // outside, or none yet); the keys of a loading thread side by side
+    unsigned at[2][kATRing][kATKeys];
+    unsigned outside[kATRing][kATKeys / 32];  // keys whose page is outside, as bits
     unsigned top[kATRing];         // exponent bits above a unit's scales of V
     uint32_t bits[kATRows][4];
     int parents[128];
@@ -117,9 +119,6 @@ __device__ __forceinline__ constexpr uint32_t tc_kind(int n, bool by_rows) {
   return 1u << 4 | (by_rows ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
 }
 
-__device__ __forceinline__ void mbar_arrive_n(unsigned long long* bar, unsigned n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
-}
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // Where 16 bytes (unit u of 8 in a 128-byte row) of a row lie.
@@ -161,22 +160,24 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_addr(&r.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  for (int i = threadIdx.x; i < 2 * kATRing * kATKeys; i += kATThreads) (&r.at[0][0][0])[i] = 0;
+  if (threadIdx.x < kATRing) r.kind[threadIdx.x] = kATNone;
+  for (int i = threadIdx.x; i < kATStages * L::kTile / 16; i += kATThreads) ((uint4*)(base + L::kV))[i] = make_uint4(0, 0, 0, 0);
+  fence_async();
   Share w = attend_share<512, kATRows, kATKeys>(a, s_scan);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&r.tmem;
   const uint32_t t_q = tmem + 64, t_o = tmem + 128;  // S, then its weights, at 0
-  // Whether the phase has come.  Once a wait has run out (`tries` is 0) all warps go on without
-  // waiting and take part in every barrier that is left: no warp waits for one that is gone.
-  // Phases then say nothing any more: no place is used, none is written over, and nothing
-  // arrives for more than one.
+  // Once a wait has run out all warps go on without waiting and take part in every
+  // barrier that is left: no warp waits for one that is gone.  What they then read may be another
+  // unit's, and the places in shared memory are at any time ones inside their pools.
   auto wait = [&](unsigned long long* bar, unsigned parity) {
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return true;
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return;
     for (unsigned n = __reduce_min_sync(0xffffffffu, r.tries); n > 0; --n)
-      if (__all_sync(0xffffffffu, mbar_try(bar, parity & 1))) return true;
+      if (__all_sync(0xffffffffu, mbar_try(bar, parity & 1))) return;
     r.tries = 0;
-    return false;
   };
 
   if (warp < kATSoft) {
@@ -274,7 +275,6 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
       for (int u = active ? u0 : u1; u < u1; ++u, ++i) {
         wait(&r.s_full, i);
         tc_after();
-        const bool alive = r.tries != 0;
         if (!w.s.bad) {
           const int slot = i & (kATRing - 1);
           const float *sk = r.sk[slot], *sv = r.sv[slot];
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         }
         tc_before();
         __syncwarp();
-        if (lane == 0 && alive) mbar_arrive_n(&r.p_ready, arrivals);
+        if (lane < arrivals) mbar_arrive(&r.p_ready);
       }
       // ---- out, or to the workspace ----
       if (active) {
@@ -501,8 +501,8 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     uint4 c[2][kRounds];  // of the next two units: 16 codes of each key, or the first 8 of 16 plain values
     // (Registers are scarce here: a spilled one would come back from L2, for L1 is small beside
     // this much shared memory.)
-    auto places = [&](int slot, unsigned (&at)[kRounds]) {
-      const unsigned* p = &r.at[slot][mine * kRounds];
+    auto places = [&](int kind, int slot, unsigned (&at)[kRounds]) {
+      const unsigned* p = &r.at[kind == kATPlain][slot][mine * kRounds];
       if constexpr (kRounds == 4) {
         const uint4 v = *(const uint4*)p;
         at[0] = v.x, at[1] = v.y, at[2] = v.z, at[3] = v.w;
@@ -515,39 +515,29 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     auto pool = [&](int kind) {
       return (kind == kATPlain ? (const char*)(values ? a.v_cache : a.k_cache) : (const char*)(values ? a.v_codes : a.k_codes)) + (part_of << kind);
     };
-    auto load = [&](int j, uint4 (&to)[kRounds], int& kind) {
+    auto load = [&](int j, uint4 (&to)[kRounds]) {
       const int slot = j & (kATRing - 1);
       wait(&r.at_full[slot], j / kATRing);
-      const bool come = r.tries != 0;
-      kind = come ? r.kind[slot] : kATNone;
+      const int kind = r.kind[slot];
       // one load whatever the kind: where two paths met, their values would have to be there
       const char* from = pool(kind == kATPlain ? kATPlain : kATCodes);
       unsigned at[kRounds];
-      places(slot, at);
+      places(kind, slot, at);
 #pragma unroll
-      for (int q = 0; q < kRounds; ++q) to[q] = stream16(from + (come ? at[q] : 0u) * 16ull);
+      for (int q = 0; q < kRounds; ++q) to[q] = stream16(from + at[q] * 16ull);
     };
-    int kinds[2];
-    if (units > 0) load(0, c[0], kinds[0]);
-    if (units > 1) load(1, c[1], kinds[1]);
+    if (units > 0) load(0, c[0]);
+    if (units > 1) load(1, c[1]);
     int stage = 0, lap = 0;
     for (int i0 = 0; i0 < units; i0 += 2) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int i = i0 + b, slot = i & (kATRing - 1);
         if (i >= units) break;
-        const int kind = kinds[b];
+        const int kind = r.kind[slot];
         unsigned char* to = operand + stage * L::kTile;
         if (lap) wait(&is_empty[stage], lap + 1);  // what lay there has been read
         if (kind == kATCodes) {
-          // what stands for a page outside may hold anything: a row that does not see it would get 0 * NaN
-          if (*(const unsigned long long*)r.outside[slot]) {
-#pragma unroll
-            for (int q = 0; q < kRounds; ++q) {
-              const int key = mine + q * kAtOnce;
-              if (r.outside[slot][key >> 5] >> (key & 31) & 1u) c[b][q] = make_uint4(0, 0, 0, 0);
-            }
-          }
           if (on) {
 #pragma unroll
             for (int q = 0; q < kRounds; ++q) {
@@ -564,7 +554,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
           float* scales = (values ? r.sv : r.sk)[slot];
           const char* from = pool(kATPlain) + 16;
           unsigned at[kRounds];
-          places(slot, at);
+          places(kATPlain, slot, at);
 #pragma unroll
           for (int q = 0; q < kRounds; ++q) {
             // the other 8 values came into L2 with the first: they share a sector
@@ -600,7 +590,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         __syncwarp();
         if (lane == 0) mbar_arrive(&is_full[stage]);
         if (++stage == kATStages) stage = 0, ++lap;
-        if (i + 2 < units) load(i + 2, c[b], kinds[b]);
+        if (i + 2 < units) load(i + 2, c[b]);
       }
     }
   } else {
@@ -684,7 +674,6 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
             }
           }
           if (i >= kATRing) wait(&r.at_empty[slot], i / kATRing + 1);
-          if (r.tries == 0) continue;  // nothing is looked up any more
           if (!w.s.bad) {
             float sk[kQ], sv[kQ];
             unsigned top = 0;
@@ -704,19 +693,20 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
               if (__float_as_uint(sv[q]) < 0x7f800000u) top = max(top, (__float_as_uint(sv[q]) >> 23) + 1u);
             top = __reduce_max_sync(0xffffffffu, top);
             if (lane == 0) r.top[slot] = top;
+            // Codes of a page outside may be seen by some rows alone, and a product with a weight of 0 has to
+            // be 0: another key of the unit stands for them or, if there is none, what lies in shared memory.
+            const int some = __reduce_max_sync(0xffffffffu, max(at[0], at[kQ - 1]));
 #pragma unroll
             for (int q = 0; q < kQ; ++q) {
               const int k = 32 * q + lane;
-              r.at[slot][L::place(k)] = at[q] < 0 ? 0u : (unsigned)((((long long)at[q] * a.Hkv + w.h) * a.D >> 4) << (codes ? 0 : 1));
+              r.at[!codes][slot][L::place(k)] = some < 0 ? 0u : (unsigned)((((long long)(at[q] < 0 ? some : at[q]) * a.Hkv + w.h) * a.D >> 4) << (codes ? 0 : 1));
               const unsigned out = __ballot_sync(0xffffffffu, at[q] < 0);
               if (lane == 0) r.outside[slot][q] = out;
               if (codes) r.sk[slot][k] = sk[q], r.sv[slot][k] = sv[q];
             }
+            if (lane == 0) r.kind[slot] = !codes ? kATPlain : some < 0 ? kATNone : kATCodes;
           }
-          if (w.s.bad)
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) r.at[slot][32 * q + lane] = 0;
-          if (lane == 0) r.kind[slot] = w.s.bad ? kATNone : codes ? kATCodes : kATPlain;
+          if (w.s.bad && lane == 0) r.kind[slot] = kATNone;
           __syncwarp();
           if (lane == 0) mbar_arrive(&r.at_full[slot]);
         }
