@@ -693,6 +693,9 @@ int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int 
  * Sums are held in fp32.  Queries, weights and plain entries enter the products
  * in fp16 times powers of two (bf16 call: at least 11 bits of each; fp32 call: two
  * fp16 parts, 22 bits).
+ * Codes and scales are taken as spec_kv_quantize_* writes them: scales are not
+ * negative, and an e4m3 code is no NaN (one that is reaches rows that do not see it,
+ * too).  bf16 call: values of blocks whose scale is below 2^-64 may lose bits.
  * A query row that is not finite makes its row of out NaN; so does a key or value
  * that is not finite (all the rows that see it), and a block whose scale is NaN
  * (rows that see one of its tokens).  What a row does not see has no part in it.
@@ -703,8 +706,11 @@ int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int 
  * T >= 0 (<= 1025 with parent_idx), Hq a multiple of Hkv, Hq * D up to 2^24, T * Hq
  * up to 2^30, B * T < 2^31, scale finite; the rest as above.  out shares no
  * memory with an input (SPEC_ERR_OVERLAP).  Returns SPEC_OK, SPEC_ERR_NULL,
- * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  Two launches on `stream`;
- * scratch of some MB.
+ * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  Two launches on `stream`.
+ * Scratch: for each share of the work (up to 5 CTAs an SM) the sums of two tiles of 8
+ * rows, or for more than 8 rows a head of keys (2 an SM) of two tiles of 128 rows: 10 to
+ * 80 MB.  The latter's waits are bounded: one that runs out sets SPEC_FLAG_TIMEOUT, and the
+ * call's out is invalid.  The same call gives the same bits on every run.
  */
 int spec_kv_attention_f32(const float *q, int64_t q_stride, const float *key_cache, const float *value_cache, int pages,
                     int page_size, const int32_t *page_table, int max_pages, const int32_t *lengths,

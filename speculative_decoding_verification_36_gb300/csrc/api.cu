@@ -882,7 +882,7 @@ int attention_impl(bool bf16, const void* q, int64_t q_stride, const void* k_cac
   if (rc) return rc;
   a.status = d->status;
   const bool e4m3 = format == SPEC_KV_E4M3;
-  const bool tiles = bf16 && D <= sv::kAttendTilesMaxD && (!a.parents || T <= sv::kAttendTilesMaxTree) && (long long)T * a.G > sv::kAttendFewRows &&
+  const bool tiles = bf16 && (!a.parents || T <= sv::kAttendTilesMaxTree) && (long long)T * a.G > sv::kAttendFewRows &&
                      plain <= sv::kAttendTilesMaxPool && codes <= sv::kAttendTilesMaxPool;
   const auto launch = tiles ? (e4m3 ? sv::launch_attend_tiles_e4m3 : sv::launch_attend_tiles_int8)
                       : bf16 ? (e4m3 ? sv::launch_attend_rows_bf16_e4m3 : sv::launch_attend_rows_bf16_int8)

@@ -13,6 +13,21 @@
 // Two CTAs share an SM: while one waits for its weights, the other's products run, and what
 // is left to be shared is shared memory's bandwidth: 512 bytes a key and head written, 512 read.
 //
+// Measured (GB300, 32 heads to 8 of keys of 128; the floor by bytes, or by products at 1.95
+// PFLOP/s, beside it): chains of 9, 64 sequences of 4096 to 8192 entries, int8: 317 us (121);
+// trees of 31 tokens, 32 such sequences, e4m3: 188 us (63); 5 tokens, two sequences of 131072 to
+// 262144, e4m3: 165 us (119); prompts of up to 2048 tokens behind 16384, int8: 1110 us (244).
+// A unit takes a CTA 2000 to 3900 clocks, of which 800 to 1000 are its products and 1200 to
+// 1600 its weights, which take 450 with nothing else on the SM: the two CTAs' 32 warps issue
+// in half of all clocks (the int8 codes' five instructions for four take their part: e4m3's two
+// make it an eighth shorter), so a warp waits for its turn at each step, and S, weights and P V
+// follow on one another.  A segment costs a CTA about 20 000 clocks at its ends.
+// Steps before: units of 128 keys with one CTA an SM 440 us (chains), queries in shared
+// memory 203 (trees), three stages or spilled registers slower (L1 is small beside this much
+// shared memory); tiles of up to 64 rows taken twice or four times, each copy with its part of the keys:
+// no faster (chains 380 of 380), the weights' own instructions are not what is waited for.
+// A check for each unit in the loading warps costs a tenth.
+//
 // The scales never touch the codes: a key's scale multiplies its scores, a value's its
 // weight.  With M = m + ref - 138 (m the running maximum in log2, ref exponent bits above every
 // scale of V that the row has seen) a weight is 2^(x - M) sv, below 2^15, and the row's sum is
@@ -26,10 +41,9 @@ namespace sv {
 constexpr int kATRows = 128, kATKeys = 64;
 constexpr int kATSoft = 4, kATLoad = 4;                        // warps that make weights; that bring keys, and as many values
 constexpr int kATThreads = 32 * (kATSoft + 2 * kATLoad + 4);   // and a group of one that issues and three that look up places
-constexpr int kATCtas = 2;                                     // of an SM
-// Registers of a thread: 64 at the launch, then by kind (512 * 64 = 128 * 80 + 256 * 64 + 128 * 48).
+// Registers of a thread with two CTAs an SM: 64 at the launch, then by kind (512 * 64 = 128 * 80 + 256 * 64 + 128 * 48).
 constexpr int kATSoftRegs = 80, kATLoadRegs = 64, kATIssueRegs = 48;
-static_assert(kATCtas * kATThreads * 64 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * kATLoad * kATLoadRegs + 128 * kATIssueRegs <= kATThreads * 64,
+static_assert(2 * kATThreads * 64 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * kATLoad * kATLoadRegs + 128 * kATIssueRegs <= kATThreads * 64,
               "registers");
 constexpr int kATStages = 2;  // units whose keys and values are in shared memory
 constexpr int kATRing = 8;    // units whose places and scales are held
@@ -41,6 +55,10 @@ constexpr unsigned kATLeastRef = 64;  // values below 2^-82 lose bits, which kee
 template <int DP>
 struct Tiles {
   static constexpr int kTile = kATKeys * DP * 2;    // bytes of a unit's keys or values
+  static constexpr int kCtas = DP == 256 ? 1 : 2;   // of an SM
+  // Columns of tensor memory: S and its weights from 0 on, the queries from 64 on, then O.
+  static constexpr int kColumns = 512 / kCtas, kO = kColumns / 2;
+  static constexpr int kAhead = DP == 256 ? 1 : 2;  // units that a loading warp holds in registers
   static constexpr int kChunk = kATKeys * 128;      // its rows of 64 fp16
   static constexpr int kK = 0, kV = kATStages * kTile, kRest = 2 * kATStages * kTile;
   struct Rest {
@@ -125,7 +143,7 @@ __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("ba
 __device__ __forceinline__ int swizzled(int row, int u) { return row * 128 + ((u ^ (row & 7)) << 4); }
 
 template <bool kE4m3, int DP>
-__global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const __grid_constant__ KvAttendArgs a) {
+__global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_kernel(const __grid_constant__ KvAttendArgs a) {
   using L = Tiles<DP>;
   extern __shared__ unsigned char s_raw[];
   __shared__ unsigned long long s_scan[512 + 1];
@@ -157,7 +175,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssue) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_addr(&r.tmem)) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&r.tmem)), "n"(L::kColumns) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   for (int i = threadIdx.x; i < 2 * kATRing * kATKeys; i += kATThreads) (&r.at[0][0][0])[i] = 0;
@@ -169,7 +187,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   __syncthreads();
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&r.tmem;
-  const uint32_t t_q = tmem + 64, t_o = tmem + 128;  // S, then its weights, at 0
+  const uint32_t t_q = tmem + 64, t_o = tmem + L::kO;  // S, then its weights, at 0
   // Once a wait has run out all warps go on without waiting and take part in every
   // barrier that is left: no warp waits for one that is gone.  What they then read may be another
   // unit's, and the places in shared memory are at any time ones inside their pools.
@@ -181,7 +199,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   };
 
   if (warp < kATSoft) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kATSoftRegs));
+    if constexpr (L::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kATSoftRegs));
     // =====================================================================
     // weights
     // =====================================================================
@@ -472,7 +490,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
           }
           __syncwarp();
         }
-        if (!whole && mine) part[128 * DP + row] = M, part[128 * DP + 128 + row] = l;
+        if (!whole && mine) part[kATRows * DP + row] = M, part[kATRows * DP + kATRows + row] = l;
       }
       tc_before();
       if (u0 == 0 && u1 < n && threadIdx.x == 0) {
@@ -482,7 +500,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
       attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
     }
   } else if (warp < kIssue) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATLoadRegs));
+    if constexpr (L::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATLoadRegs));
     // =====================================================================
     // keys and values
     // =====================================================================
@@ -491,21 +509,25 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
     // Eight lanes in a row write four units of two keys, which the swizzle puts on all
     // banks; a warp reads whole heads.
     constexpr int kPer = DP / 16, kAtOnce = L::kAtOnce, kRounds = kATKeys / kAtOnce;  // lanes a key, keys at once
-    const int part = (lane & 3) | (kPer == 8 ? (lane >> 1) & 4 : 0);
-    const int mine = wx * (32 / kPer) + (((lane >> 2) & 1) | (kPer == 8 ? (lane >> 3) & 2 : (lane >> 2) & 6));
+    const int part = (lane & 3) | (kPer == 4 ? 0 : (lane >> 1) & (kPer == 8 ? 4 : 12));
+    const int mine = wx * (32 / kPer) + (((lane >> 2) & 1) | (kPer == 4 ? (lane >> 2) & 6 : kPer == 8 ? (lane >> 3) & 2 : 0));
     const bool on = 16 * part < a.D;
     unsigned char* operand = base + (values ? L::kV : L::kK);
     unsigned long long *is_full = values ? r.v_full : r.k_full, *is_empty = values ? r.v_empty : r.k_empty;
     const int put0 = (part >> 2) * L::kChunk + swizzled(mine, 2 * (part & 3)), put1 = (part >> 2) * L::kChunk + swizzled(mine, 2 * (part & 3) + 1);
     const int units = (int)w.left;
-    uint4 c[2][kRounds];  // of the next two units: 16 codes of each key, or the first 8 of 16 plain values
+    constexpr int kAhead = L::kAhead;
+    uint4 c[kAhead][kRounds];  // of the next units: 16 codes of each key, or the first 8 of 16 plain values
     // (Registers are scarce here: a spilled one would come back from L2, for L1 is small beside
     // this much shared memory.)
     auto places = [&](int kind, int slot, unsigned (&at)[kRounds]) {
       const unsigned* p = &r.at[kind == kATPlain][slot][mine * kRounds];
-      if constexpr (kRounds == 4) {
-        const uint4 v = *(const uint4*)p;
-        at[0] = v.x, at[1] = v.y, at[2] = v.z, at[3] = v.w;
+      if constexpr (kRounds % 4 == 0) {
+#pragma unroll
+        for (int q = 0; q < kRounds; q += 4) {
+          const uint4 v = *(const uint4*)(p + q);
+          at[q] = v.x, at[q + 1] = v.y, at[q + 2] = v.z, at[q + 3] = v.w;
+        }
       } else {
         const uint2 v = *(const uint2*)p;
         at[0] = v.x, at[1] = v.y;
@@ -526,12 +548,13 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
 #pragma unroll
       for (int q = 0; q < kRounds; ++q) to[q] = stream16(from + at[q] * 16ull);
     };
-    if (units > 0) load(0, c[0]);
-    if (units > 1) load(1, c[1]);
-    int stage = 0, lap = 0;
-    for (int i0 = 0; i0 < units; i0 += 2) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAhead; ++b)
+      if (b < units) load(b, c[b]);
+    int stage = 0, lap = 0;
+    for (int i0 = 0; i0 < units; i0 += kAhead) {
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
         const int i = i0 + b, slot = i & (kATRing - 1);
         if (i >= units) break;
         const int kind = r.kind[slot];
@@ -569,7 +592,8 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
             unsigned top = max(lo << 16, hi);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (kPer == 8) top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            if (kPer >= 8) top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            if (kPer == 16) top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
             const bool finite = top < 0x7f800000u;
             const float down = in && finite ? scale_down(top) : __uint_as_float(0x7fffffffu);
             if (part == 0) scales[key] = down;
@@ -590,11 +614,11 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
         __syncwarp();
         if (lane == 0) mbar_arrive(&is_full[stage]);
         if (++stage == kATStages) stage = 0, ++lap;
-        if (i + 2 < units) load(i + 2, c[b]);
+        if (i + kAhead < units) load(i + kAhead, c[b]);
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATIssueRegs));
+    if constexpr (L::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATIssueRegs));
     if (warp == kIssue) {
       // ===================================================================
       // products
@@ -719,7 +743,7 @@ __global__ void __launch_bounds__(kATThreads, kATCtas) attend_tiles_kernel(const
   if (threadIdx.x == 0 && r.tries == 0) atomicOr(a.status, kStatusTimeout);
   if (warp == kIssue) {
     tc_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kColumns) : "memory");
   }
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(r.meta[0], r.meta[1], r.meta[2], r.meta[3]);
 }
@@ -730,7 +754,7 @@ static cudaError_t launch_tiles(KvAttendArgs a, int sms, size_t* bytes, cudaStre
   a.tiles = (int)(((long long)a.T * a.G + kATRows - 1) / kATRows);
   const long long keys = (long long)a.max_code_pages * a.block + (long long)a.max_pages * a.page_size;
   const double most = (double)a.B * a.Hkv * a.tiles * (double)(keys / kATKeys + 2);
-  const int grid = (int)fmin((double)sms * kATCtas, most);
+  const int grid = (int)fmin((double)sms * L::kCtas, most);
   const size_t slots = ((size_t)grid * 2 * attend_slot(kATRows, DP) * 4 + 255) / 256 * 256;
   if (bytes) {
     *bytes = slots + (size_t)grid * sizeof(int4);

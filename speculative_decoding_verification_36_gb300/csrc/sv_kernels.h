@@ -383,12 +383,12 @@ cudaError_t launch_attend_rows_bf16_int8(const KvAttendArgs& a, int sms, size_t*
 cudaError_t launch_attend_rows_bf16_e4m3(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
 cudaError_t launch_attend_rows_f32_int8(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
 cudaError_t launch_attend_rows_f32_e4m3(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
-// Tiles of 128 rows on the tensor cores: bf16, D <= 128, trees of up to 128 tokens, and more
+// Tiles of 128 rows on the tensor cores: bf16, trees of up to 128 tokens, and more
 // rows a head of keys than the other kernel's tile has (which reads the cache once
 // for each tile: 64 sequences of 6144 entries and 4 query heads to one of keys take 178 us with one token
 // there, 288 us here; with three tokens 323 us there in two tiles, 292 us here).
 constexpr int kAttendFewRows = 8;
-constexpr int kAttendTilesMaxD = 128, kAttendTilesMaxTree = 128;
+constexpr int kAttendTilesMaxTree = 128;
 constexpr unsigned long long kAttendTilesMaxPool = 1ull << 36;  // bytes: places are 32 bits of 16
 cudaError_t launch_attend_tiles_int8(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
 cudaError_t launch_attend_tiles_e4m3(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);

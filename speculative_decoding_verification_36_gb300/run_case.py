@@ -12,7 +12,9 @@ histories of up to 131072 tokens for ngram; spec_count_tokens and
 spec_process_logits on the c3 target rows (process) or the c5 tree's
 (process-tree), then the greedy verify of what comes out; spec_kv_append, the
 greedy tree verify and spec_kv_commit on the c5 tree with 4 layers of 8 heads
-of 128 (cache)), then synchronises.
+of 128 (cache); the same step with spec_kv_attention in each layer over a cache
+whose whole blocks are int8 codes, which spec_kv_quantize makes before the step
+and after its commit (cache8)), then synchronises.
 """
 from __future__ import annotations
 
@@ -22,7 +24,7 @@ import sys
 
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
-    ap.add_argument("preset", choices=["c1", "c2", "c3", "c4", "c5", "c5s", "ngram", "process", "process-tree", "cache"])
+    ap.add_argument("preset", choices=["c1", "c2", "c3", "c4", "c5", "c5s", "ngram", "process", "process-tree", "cache", "cache8"])
     ap.add_argument("--early-exit", action="store_true", help="c1-c5: the early-exit verify")
     ap.add_argument("--batch", type=int, default=0, help="sequences (default: the preset's B)")
     ap.add_argument("--calls", type=int, default=3)
@@ -32,7 +34,8 @@ def main(argv=None) -> int:
 
     from . import build, spec_get_status, spec_ngram_draft, spec_tree_verify_greedy, spec_tree_verify_sampling
     from . import spec_verify, spec_verify_early_exit
-    from . import spec_count_tokens, spec_kv_append, spec_kv_commit, spec_process_logits, spec_rope_turns, spec_token_state
+    from . import spec_count_tokens, spec_kv_append, spec_kv_attention, spec_kv_commit, spec_kv_quantize
+    from . import spec_process_logits, spec_rope_turns, spec_token_state
     from . import workloads as wl
 
     build.build()
@@ -69,20 +72,30 @@ def main(argv=None) -> int:
         flags = spec_get_status()
         print(f"{args.preset} B={B}: {args.calls} calls, status flags {flags}")
         return 0 if flags == 0 else 1
-    if args.preset == "cache":
+    if args.preset in ("cache", "cache8"):
         x = wl.make_tree(wl.preset("c5", **({"B": args.batch} if args.batch else {})), device=dev, seed=0)
         B, N = x["tokens"].shape
         c = wl.make_cache_step(B, N + 1, 32, 8, 128, layers=4, device=dev)
         turns, lengths = spec_rope_turns(c["inv_freq"], dev), c["lengths"]
+        pools = c["key_cache"], c["value_cache"], c["page_table"]
+        if args.preset == "cache8":  # a block to a page
+            codes = [torch.empty(c["key_cache"].shape, dtype=torch.int8, device=dev) for _ in range(2)]
+            scales = [torch.empty((*codes[0].shape[:2], 8), device=dev) for _ in range(2)]
+            stored = spec_kv_quantize(*pools, torch.zeros_like(lengths), lengths, *codes, *scales, c["page_table"])
         for _ in range(args.calls):
             for i in range(4):
-                spec_kv_append(c["k"][i], c["v"][i], c["key_cache"][i], c["value_cache"][i], c["page_table"], lengths,
-                               turns=turns, q=c["q"][i], parent_idx=x["parents"])
+                q = spec_kv_append(c["k"][i], c["v"][i], c["key_cache"][i], c["value_cache"][i], c["page_table"], lengths,
+                                   turns=turns, q=c["q"][i], parent_idx=x["parents"])
+                if args.preset == "cache8":
+                    spec_kv_attention(q, c["key_cache"][i], c["value_cache"][i], c["page_table"], lengths, *(t[i] for t in codes + scales),
+                                      c["page_table"], stored, parent_idx=x["parents"])
             path, n, _ = spec_tree_verify_greedy(x["target"], x["tokens"], x["parents"])
-            spec_kv_commit(c["key_cache"], c["value_cache"], c["page_table"], lengths, x["tokens"], x["parents"], path, n)
+            _, after = spec_kv_commit(*pools, lengths, x["tokens"], x["parents"], path, n)
+            if args.preset == "cache8":
+                spec_kv_quantize(*pools, stored, after, *codes, *scales, c["page_table"])
         torch.cuda.synchronize()
         flags = spec_get_status()
-        print(f"cache B={B}: {args.calls} calls, status flags {flags}")
+        print(f"{args.preset} B={B}: {args.calls} calls, status flags {flags}")
         return 0 if flags == 0 else 1
     name = "c5" if args.preset == "c5s" else args.preset
     p = wl.preset(name, B=args.batch) if args.batch else wl.preset(name)
