@@ -238,52 +238,62 @@ __device__ __forceinline__ void attend_store8(S* to, const float (&f)[8]) {
 // What a share leaves of a tile: floats [rows][DP], then the rows' maxima and sums.
 __host__ __device__ constexpr int attend_slot(int rows, int DP) { return rows * DP + 2 * rows; }
 
+// What a share leaves for the joining: the last share of the segment that begins in it and goes
+// on, and its rows.
+__device__ __forceinline__ int attend_joint(int last, int rows) { return last | rows << 16; }
+
 // Joins a segment that fell into several shares, in their order: CTAs x join the one that
-// begins in share x and goes on, a warp to a row.  The shares' maxima and sums come at
-// once, a lane each; their values eight shares at a time.
+// begins in share x and goes on.  A warp asks for the maxima, sums and values of 8 shares at once.  Either each warp
+// has rows of its own or the four take a quarter of a row's shares each, whichever waits for
+// memory less often (one token with 2048 entries in 32 shares: the call took 23 us where a
+// warp had all of a row's shares, 17 so).
 template <class S, int DP, int kRows>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ KvAttendArgs a) {
   constexpr int kSlot = attend_slot(kRows, DP), kN = DP / 32;
+  __shared__ float s_f[4][DP], s_m[4], s_l[4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 meta = a.meta[blockIdx.x];
-  const int first = blockIdx.x, n = meta.x - first + 1;
   if (meta.x < 0) return;
-  const Sequence q = attend_sequence(a, meta.y);
-  const int lane = threadIdx.x & 31, row0 = meta.w * kRows, live = min(kRows, q.n_new * a.G - row0);
+  const int first = blockIdx.x, n = (meta.x & 0xffff) - first + 1, live = meta.x >> 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row0 = meta.w * kRows;
   auto slot = [&](int s) { return a.part + (2LL * (first + s) + (s == 0)) * kSlot; };
-  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < live; r += gridDim.y * 4) {
-    float most = kLow;
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      const float m = s0 + lane < n ? slot(s0 + lane)[kRows * DP + r] : kLow;
-      most = fmaxf(most, m);
-    }
+  float most, sum, f[kN];
+  // the shares from `from` to `to` of row r
+  auto take = [&](int r, int from, int to) {
+    most = kLow, sum = 0.f;
 #pragma unroll
-    for (int d = 16; d >= 1; d /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-    float sum = 0.f, f[kN] = {};
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      const bool on = s0 + lane < n;
-      const float* p = slot(on ? s0 + lane : 0) + kRows * DP;
-      const float by = on ? ex2(p[r] - most) : 0.f, l = on ? p[kRows + r] * by : 0.f;
-      const int count = min(32, n - s0);
-      for (int s = 0; s < count; s += 8) {
-        float x[8][kN];
+    for (int k = 0; k < kN; ++k) f[k] = 0.f;
+    for (int s = from; s < to; s += 8) {
+      const int count = min(8, to - s);
+      const float* p = slot(s + min(lane, count - 1)) + kRows * DP + r;
+      const float m = p[0], l = p[kRows];
+      float x[8][kN];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float* from = slot(s0 + min(s + e, count - 1)) + r * DP + kN * lane;
+      for (int e = 0; e < 8; ++e) {
+        const float* at = slot(s + min(e, count - 1)) + r * DP + kN * lane;
 #pragma unroll
-          for (int k = 0; k < kN; k += 2) *(float2*)&x[e][k] = *(const float2*)(from + k);
-        }
+        for (int k = 0; k < kN; k += 2) *(float2*)&x[e][k] = *(const float2*)(at + k);
+      }
+      float top = fmaxf(m, most);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (s + e >= count) break;
-          const float w = __shfl_sync(0xffffffffu, by, s + e);
-          sum += __shfl_sync(0xffffffffu, l, s + e);
+      for (int d = 16; d >= 1; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float by = ex2(m - top), old = ex2(most - top), part = l * by;
+      most = top;
+      sum *= old;
 #pragma unroll
-          for (int k = 0; k < kN; ++k) f[k] += x[e][k] * w;
-        }
+      for (int k = 0; k < kN; ++k) f[k] *= old;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e >= count) break;
+        const float w = __shfl_sync(0xffffffffu, by, e);
+        sum += __shfl_sync(0xffffffffu, part, e);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) f[k] += x[e][k] * w;
       }
     }
-    if (kN * lane >= a.D) continue;
+  };
+  auto put = [&](int r) {
+    if (kN * lane >= a.D) return;
     const float by = sum == 0.f ? 0.f : 1.f / sum;
     const int token = fdiv(row0 + r, a.div_g);
     S* out = (S*)a.out + (((long long)meta.y * a.T + token) * a.Hq + (long long)meta.z * a.G + row0 + r - token * a.G) * a.D + kN * lane;
@@ -297,6 +307,37 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
         *(uint32_t*)(out + k) = y;
       }
     }
+  };
+  const int alone = (live + 4 * gridDim.y - 1) / (4 * gridDim.y) * ((n + 7) / 8), together = (live + gridDim.y - 1) / gridDim.y * ((n + 31) / 32);
+  if (alone <= together) {
+    for (int r = blockIdx.y * 4 + warp; r < live; r += gridDim.y * 4) {
+      take(r, 0, n);
+      put(r);
+    }
+    return;
+  }
+  const int each = (n + 3) / 4;
+  for (int r = blockIdx.y; r < live; r += gridDim.y) {
+    take(r, min(n, warp * each), min(n, (warp + 1) * each));
+    if (lane == 0) s_m[warp] = most, s_l[warp] = sum;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) s_f[warp][32 * k + lane] = f[k];
+    __syncthreads();
+    if (warp == 0) {
+      most = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+      sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) f[k] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float by = ex2(s_m[w] - most);
+        sum += s_l[w] * by;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) f[k] += s_f[w][32 * k + lane] * by;
+      }
+      put(r);
+    }
+    __syncthreads();
   }
 }
 
@@ -304,7 +345,7 @@ template <class S, int DP, int kRows>
 static cudaError_t launch_join(const KvAttendArgs& a, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3((unsigned)grid, kRows < 32 ? kRows / 4 : 8);
+  cfg.gridDim = dim3((unsigned)grid, 8);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

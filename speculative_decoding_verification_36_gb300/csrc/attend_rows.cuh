@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
           part[kRows * DP + kRows + 2 * t + e] = l[e];
         }
       if (u0 == 0) {
-        meta_last = attend_share_of(w, w.from + n - 1);
+        meta_last = attend_joint(attend_share_of(w, w.from + n - 1), min(kRows, rows - row0));
         meta_b = w.b, meta_h = w.h, meta_tile = w.tile;
       }
     }

@@ -77,6 +77,7 @@ struct Tiles {
     int wrong;
     volatile unsigned tries;  // of a wait, 0 once one has run out
     int meta[4];
+    int live;  // rows of the segment
   };
   // Keys that eight loading warps take at once, and where a key's place is held.
   static constexpr int kAtOnce = 32 * kATLoad / (DP / 16);
@@ -123,6 +124,9 @@ __device__ __forceinline__ void tc_loaded16(uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tc_store8(uint32_t at, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::SV_W8(r, 0), "r"(at) : "memory");
+}
+__device__ __forceinline__ void tc_store1(uint32_t at, uint32_t x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(x), "r"(at) : "memory");
 }
 __device__ __forceinline__ void tc_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -232,6 +236,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
         }
       }
       loaded_b = w.b, loaded_tile = w.tile;
+      if (threadIdx.x == 0) r.live = min(kATRows, rows - row0);
       const bool lost = w.s.bad || (a.parents && bad);
       if (lost && threadIdx.x == 0) atomicOr(a.status, kStatusBadData);
       const bool active = 32 * warp < rows - row0, mine = row0 + row < rows;
@@ -241,39 +246,47 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
         // which leaves shared memory to the keys and values.
         const int token = fdiv(row0 + row, a.div_g);
         const uint16_t* q = (const uint16_t*)a.q + ((long long)w.b * a.T + token) * a.q_stride + ((long long)w.h * a.G + row0 + row - token * a.G) * a.D;
-        const bool fast = ((uintptr_t)a.q & 15) == 0 && a.q_stride % 8 == 0;
-        auto eight = [&](int d) {
-          if (!mine || lost || d >= a.D) return make_uint4(0, 0, 0, 0);
-          const uint16_t* p = q + d;
-          if (fast) return __ldg((const uint4*)p);
-          return make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
-        };
+        const bool fast = ((uintptr_t)a.q & 15) == 0 && a.q_stride % 8 == 0, there = mine && !lost;
+        auto eight = [&](int d) { return there && d < a.D ? __ldg((const uint4*)(q + d)) : make_uint4(0, 0, 0, 0); };
+        // once from memory (the first trip brings the whole row to L2), then from tensor memory
+        if (there)
+          for (int d = 0; d < a.D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
         unsigned lo = 0, hi = 0;
+        if (fast) {
 #pragma unroll 2
-        for (int d = 0; d < DP; d += 32) {
-          uint4 x[4];
+          for (int d = 0; d < DP; d += 32) {
+            uint4 x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = eight(d + 8 * e);
+            for (int e = 0; e < 4; ++e) x[e] = eight(d + 8 * e);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            lo = max(lo, max(max(x[e].x & 0x7fffu, x[e].y & 0x7fffu), max(x[e].z & 0x7fffu, x[e].w & 0x7fffu)));
-            hi = max(hi, max(max(x[e].x & 0x7fff0000u, x[e].y & 0x7fff0000u), max(x[e].z & 0x7fff0000u, x[e].w & 0x7fff0000u)));
+            for (int e = 0; e < 4; ++e) {
+              lo = max(lo, max(max(x[e].x & 0x7fffu, x[e].y & 0x7fffu), max(x[e].z & 0x7fffu, x[e].w & 0x7fffu)));
+              hi = max(hi, max(max(x[e].x & 0x7fff0000u, x[e].y & 0x7fff0000u), max(x[e].z & 0x7fff0000u, x[e].w & 0x7fff0000u)));
+            }
+            tc_store16(t_q + lanes + d / 2, (const uint32_t*)x);
+          }
+        } else {
+#pragma unroll 1
+          for (int d = 0; d < DP; d += 2) {
+            const uint32_t x = there && d < a.D ? q[d] | (uint32_t)q[d + 1] << 16 : 0u;
+            lo = max(lo, x & 0x7fffu), hi = max(hi, x & 0x7fff0000u);
+            tc_store1(t_q + lanes + d / 2, x);
           }
         }
+        tc_stored();
         const unsigned top = max(lo << 16, hi);
         const bool finite = top < 0x7f800000u;
         // the scale's sign goes with the query: what multiplies the scores is positive
         const float up = a.scale < 0.f ? -scale_up(top) : scale_up(top);
         if (!lost && finite) qs = scale_down(top) * fabsf(a.scale);
         auto two = [&](uint32_t v) { return finite ? half2_of(bf16_lo(v) * up, bf16_hi(v) * up) : 0u; };
-#pragma unroll 2
+#pragma unroll 1
         for (int d = 0; d < DP; d += 32) {
           uint32_t y[16];
+          tc_load16(t_q + lanes + d / 2, y);
+          tc_loaded16(y);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 x = eight(d + 8 * e);
-            y[4 * e] = two(x.x), y[4 * e + 1] = two(x.y), y[4 * e + 2] = two(x.z), y[4 * e + 3] = two(x.w);
-          }
+          for (int e = 0; e < 16; ++e) y[e] = two(y[e]);
           tc_store16(t_q + lanes + d / 2, y);
         }
         tc_stored();
@@ -494,7 +507,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
       }
       tc_before();
       if (u0 == 0 && u1 < n && threadIdx.x == 0) {
-        r.meta[0] = attend_share_of(w, w.from + n - 1);
+        r.meta[0] = attend_joint(attend_share_of(w, w.from + n - 1), r.live);
         r.meta[1] = w.b, r.meta[2] = w.h, r.meta[3] = w.tile;
       }
       attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
