@@ -9,12 +9,12 @@
 // read once for each tile of 8.
 //
 // Measured (GB300; the codes' bytes at 6.77 TB/s beside it): single tokens, 64 sequences of
-// 4096 to 8192 entries, 32 heads to 8 of keys of 128, int8: 169 us (119); chains of 5 in
-// fp32, 8 sequences of up to 4000, 8 heads of 80: 33 us (4.6); three tokens with 8 heads to
-// one of 256, 16 sequences of up to 10000: 59 us (9.1).  The first is bound by what a warp
-// issues for 16 keys (turning codes to fp16, 16 mma.sync of 8 clocks of the SM each) beside
-// the memory's latency; the others by the chain of a CTA's few units, the prologue (lengths, shares,
-// tables: about three trips to memory) and the joining launch.  From steps before: fragments
+// 4096 to 8192 entries, 32 heads to 8 of keys of 128, int8: 169 to 177 us (121); chains of 5 in
+// fp32, 8 sequences of up to 4000, 8 heads of 80: 31 us (4.4).  The first is bound by what a
+// warp does for 16 keys, turning codes to fp16 before all (the integer pipe is busy in 53 % of
+// the clocks, DRAM at 61 % of its peak, 168 registers leave 12 warps an SM); the second by the chain
+// of a CTA's few units, the prologue (lengths, shares, tables: about three trips to memory)
+// and the joining launch.  From steps before: fragments
 // from global memory to registers 212 us, with the ring 197, with the keys as the products'
 // rows instead of the queries 169.
 //

@@ -10,18 +10,21 @@
 // swizzle; plain entries become fp16 times a power of two for each key.  Three warps look the
 // entries' places and scales up further ahead.  Four warps make weights of scores: a
 // thread has one row, so that rows need no shuffles.  One thread issues the products.
-// Two CTAs share an SM: while one waits for its weights, the other's products run, and what
+// Two CTAs share an SM (heads of more than 128: one, which has all the tensor memory): while one
+// waits for its weights, the other's products run, and what
 // is left to be shared is shared memory's bandwidth: 512 bytes a key and head written, 512 read.
 //
 // Measured (GB300, 32 heads to 8 of keys of 128; the floor by bytes, or by products at 1.95
-// PFLOP/s, beside it): chains of 9, 64 sequences of 4096 to 8192 entries, int8: 317 us (121);
-// trees of 31 tokens, 32 such sequences, e4m3: 188 us (63); 5 tokens, two sequences of 131072 to
-// 262144, e4m3: 165 us (119); prompts of up to 2048 tokens behind 16384, int8: 1110 us (244).
+// PFLOP/s, beside it): chains of 9, 64 sequences of 4096 to 8192 entries, int8: 307 us (123);
+// trees of 31 tokens, 32 such sequences, e4m3: 176 us (65); 5 tokens, two sequences of 131072 to
+// 262144, e4m3: 163 us (81); prompts of up to 2048 tokens behind 16384, int8: 1106 us (298); three
+// tokens with 8 heads to one of 256, 16 sequences of 5000 to 10000: 46 us (9.4).
 // A unit takes a CTA 2000 to 3900 clocks, of which 800 to 1000 are its products and 1200 to
 // 1600 its weights, which take 450 with nothing else on the SM: the two CTAs' 32 warps issue
 // in half of all clocks (the int8 codes' five instructions for four take their part: e4m3's two
 // make it an eighth shorter), so a warp waits for its turn at each step, and S, weights and P V
-// follow on one another.  A segment costs a CTA about 20 000 clocks at its ends.
+// follow on one another.  A segment costs a CTA some 15 000 clocks at its ends, most of them for
+// its queries: code that is run once comes to the SM from L2, too.
 // Steps before: units of 128 keys with one CTA an SM 440 us (chains), queries in shared
 // memory 203 (trees), three stages or spilled registers slower (L1 is small beside this much
 // shared memory); tiles of up to 64 rows taken twice or four times, each copy with its part of the keys:

@@ -11,7 +11,7 @@
 // Both are bound by HBM where there is much.  Measured (GB300, the bytes at 6.77 TB/s beside it):
 // 8 prompts of up to 8192 tokens, 8 heads of 128, bf16 to int8: quantised in 90 us (59), read
 // back in 70 (59); 2 layers of 8 sequences of up to 16384 read back in 194 us (179); the few blocks
-// of a commit, 64 sequences in 16 layers: 23 us for both calls (9.3), two launches and
+// of a commit, 64 sequences in 16 layers: 23 us for both calls (8.8), two launches and
 // three trips to memory each.
 #include "sv_common.cuh"
 #include "sv_kernels.h"
