@@ -708,8 +708,8 @@ int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int 
  * memory with an input (SPEC_ERR_OVERLAP).  Returns SPEC_OK, SPEC_ERR_NULL,
  * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  Two launches on `stream`.
  * Scratch: for each share of the work (up to 5 CTAs an SM) the sums of two tiles of 8
- * rows, or for more than 8 rows a head of keys (2 an SM) of two tiles of 128 rows: 10 to
- * 80 MB.  The latter's waits are bounded: one that runs out sets SPEC_FLAG_TIMEOUT, and the
+ * rows, up to 5 MB; in bf16 calls with more than 8 rows a head of keys of two tiles of 128
+ * rows, up to 40 MB.  The latter's waits are bounded: one that runs out sets SPEC_FLAG_TIMEOUT, and the
  * call's out is invalid.  The same call gives the same bits on every run.
  */
 int spec_kv_attention_f32(const float *q, int64_t q_stride, const float *key_cache, const float *value_cache, int pages,

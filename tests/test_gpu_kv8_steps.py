@@ -109,6 +109,23 @@ def test_attention_of_more_shapes(B, T, Hq, Hkv, D):
     assert sv.spec_get_status() == 0
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,block,page,lengths,tree,ragged,stored", [
+    (2, 31, 8, 1, 256, 16, 16, [700, 33], True, False, "blocks"),
+    (1, 200, 2, 1, 160, 24, 7, [333], False, False, "step"),
+    (3, 9, 4, 2, 144, 64, 16, [1000, 63, 0], False, True, "some"),
+    (2, 128, 2, 2, 192, 16, 5, [50, 400], True, True, "blocks"),   # the largest tree of the tiles
+    (1, 129, 1, 1, 208, 16, 16, [90], True, False, "blocks"),      # a larger one
+    (1, 16, 1, 1, 256, 16, 16, [20000], False, False, "blocks"),   # one segment over all CTAs: a quarter of its shares to a warp
+])
+def test_attention_of_wide_heads(B, T, Hq, Hkv, D, block, page, lengths, tree, ragged, stored, fmt):
+    rng = np.random.default_rng(T + D + B)
+    x = attend_case(rng, B, T, Hq, Hkv, D, BF16, fmt, block, page, lengths, tree, ragged, stored)
+    out = torch.full(x["q"].shape, 5.0, dtype=BF16, device=DEV)
+    check(x, attend(x, out=out))
+    assert sv.spec_get_status() == 0
+
+
 @pytest.mark.parametrize("T,Hkv,D,dtype,tree", [(1, 2, 128, BF16, False), (5, 1, 80, BF16, True), (5, 1, 80, F32, True), (37, 3, 48, BF16, False), (3, 1, 240, BF16, False)])
 def test_outputs_are_guarded(T, Hkv, D, dtype, tree):
     rng = np.random.default_rng(T)
