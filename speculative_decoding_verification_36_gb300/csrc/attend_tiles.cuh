@@ -5,8 +5,8 @@
 //   S = Q K^T      128 x 64 x D, Q from tensor memory, K from shared memory, both fp16
 //   P = weights    fp16, over S's columns in tensor memory
 //   O += P V       128 x D x 64, P from tensor memory, V from shared memory
-// Four warps bring keys and four values: codes go from global memory to registers two
-// units ahead, become fp16 (exactly) and are written to shared memory in the 128-byte
+// Four warps bring keys and four values: codes go from global memory to registers a
+// unit ahead (two ahead: chains 306 us instead of 266, prompts 1096 instead of 845), become fp16 (exactly) and are written to shared memory in the 128-byte
 // swizzle; plain entries become fp16 times a power of two for each key.  Three warps look the
 // entries' places and scales up further ahead.  Four warps make weights of scores: a
 // thread has one row, so that rows need no shuffles.  One thread issues the products.
@@ -44,8 +44,8 @@ namespace sv {
 constexpr int kATRows = 128, kATKeys = 64;
 constexpr int kATSoft = 4, kATLoad = 4;                        // warps that make weights; that bring keys, and as many values
 constexpr int kATThreads = 32 * (kATSoft + 2 * kATLoad + 4);   // and a group of one that issues and three that look up places
-// Registers of a thread with two CTAs an SM: 64 at the launch, then by kind (512 * 64 = 128 * 80 + 256 * 64 + 128 * 48).
-constexpr int kATSoftRegs = 80, kATLoadRegs = 64, kATIssueRegs = 48;
+// Registers of a thread with two CTAs an SM: 64 at the launch, then by kind (512 * 64 = 128 * 88 + 256 * 56 + 128 * 56).
+constexpr int kATSoftRegs = 88, kATLoadRegs = 56, kATIssueRegs = 56;
 static_assert(2 * kATThreads * 64 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * kATLoad * kATLoadRegs + 128 * kATIssueRegs <= kATThreads * 64,
               "registers");
 constexpr int kATStages = 2;  // units whose keys and values are in shared memory
@@ -61,7 +61,6 @@ struct Tiles {
   static constexpr int kCtas = DP == 256 ? 1 : 2;   // of an SM
   // Columns of tensor memory: S and its weights from 0 on, the queries from 64 on, then O.
   static constexpr int kColumns = 512 / kCtas, kO = kColumns / 2;
-  static constexpr int kAhead = DP == 256 ? 1 : 2;  // units that a loading warp holds in registers
   static constexpr int kChunk = kATKeys * 128;      // its rows of 64 fp16
   static constexpr int kK = 0, kV = kATStages * kTile, kRest = 2 * kATStages * kTile;
   struct Rest {
@@ -532,8 +531,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
     unsigned long long *is_full = values ? r.v_full : r.k_full, *is_empty = values ? r.v_empty : r.k_empty;
     const int put0 = (part >> 2) * L::kChunk + swizzled(mine, 2 * (part & 3)), put1 = (part >> 2) * L::kChunk + swizzled(mine, 2 * (part & 3) + 1);
     const int units = (int)w.left;
-    constexpr int kAhead = L::kAhead;
-    uint4 c[kAhead][kRounds];  // of the next units: 16 codes of each key, or the first 8 of 16 plain values
+    uint4 c[kRounds];  // of the next unit: 16 codes of each key, or the first 8 of 16 plain values
     // (Registers are scarce here: a spilled one would come back from L2, for L1 is small beside
     // this much shared memory.)
     auto places = [&](int kind, int slot, unsigned (&at)[kRounds]) {
@@ -564,74 +562,68 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
 #pragma unroll
       for (int q = 0; q < kRounds; ++q) to[q] = stream16(from + at[q] * 16ull);
     };
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b)
-      if (b < units) load(b, c[b]);
+    if (units > 0) load(0, c);
     int stage = 0, lap = 0;
-    for (int i0 = 0; i0 < units; i0 += kAhead) {
-#pragma unroll
-      for (int b = 0; b < kAhead; ++b) {
-        const int i = i0 + b, slot = i & (kATRing - 1);
-        if (i >= units) break;
-        const int kind = r.kind[slot];
-        unsigned char* to = operand + stage * L::kTile;
-        if (lap) wait(&is_empty[stage], lap + 1);  // what lay there has been read
-        if (kind == kATCodes) {
-          if (on) {
-#pragma unroll
-            for (int q = 0; q < kRounds; ++q) {
-              uint4 z[2];
-              Code<kE4m3>::word(c[b][q].x, z[0].x, z[0].y);
-              Code<kE4m3>::word(c[b][q].y, z[0].z, z[0].w);
-              Code<kE4m3>::word(c[b][q].z, z[1].x, z[1].y);
-              Code<kE4m3>::word(c[b][q].w, z[1].z, z[1].w);
-              *(uint4*)(to + put0 + q * kAtOnce * 128) = z[0];
-              *(uint4*)(to + put1 + q * kAtOnce * 128) = z[1];
-            }
-          }
-        } else if (kind == kATPlain) {
-          float* scales = (values ? r.sv : r.sk)[slot];
-          const char* from = pool(kATPlain) + 16;
-          unsigned at[kRounds];
-          places(kATPlain, slot, at);
+    for (int i = 0; i < units; ++i) {
+      const int slot = i & (kATRing - 1);
+      const int kind = r.kind[slot];
+      unsigned char* to = operand + stage * L::kTile;
+      if (lap) wait(&is_empty[stage], lap + 1);  // what lay there has been read
+      if (kind == kATCodes) {
+        if (on) {
 #pragma unroll
           for (int q = 0; q < kRounds; ++q) {
-            // the other 8 values came into L2 with the first: they share a sector
-            const int key = mine + q * kAtOnce;
-            const bool in = !(r.outside[slot][key >> 5] >> (key & 31) & 1u);
-            const uint4 other = stream16(from + at[q] * 16ull);
-            const uint4 y = on && in ? c[b][q] : make_uint4(0, 0, 0, 0), z = on && in ? other : make_uint4(0, 0, 0, 0);
-            const unsigned lo = max(max(max(y.x & 0x7fffu, y.y & 0x7fffu), max(y.z & 0x7fffu, y.w & 0x7fffu)),
-                                    max(max(z.x & 0x7fffu, z.y & 0x7fffu), max(z.z & 0x7fffu, z.w & 0x7fffu)));
-            const unsigned hi = max(max(max(y.x & 0x7fff0000u, y.y & 0x7fff0000u), max(y.z & 0x7fff0000u, y.w & 0x7fff0000u)),
-                                    max(max(z.x & 0x7fff0000u, z.y & 0x7fff0000u), max(z.z & 0x7fff0000u, z.w & 0x7fff0000u)));
-            unsigned top = max(lo << 16, hi);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (kPer >= 8) top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            if (kPer == 16) top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const bool finite = top < 0x7f800000u;
-            const float down = in && finite ? scale_down(top) : __uint_as_float(0x7fffffffu);
-            if (part == 0) scales[key] = down;
-            if (values) {
-              const unsigned above = __reduce_max_sync(0xffffffffu, in && finite ? (__float_as_uint(down) >> 23) + 1u : 0u);
-              if (lane == 0) atomicMax(&r.top[slot], above);
-            }
-            const float up = finite ? scale_up(top) : 0.f;
-            auto two = [&](uint32_t v) { return finite ? half2_of(bf16_lo(v) * up, bf16_hi(v) * up) : 0u; };
-            if (on) {
-              *(uint4*)(to + put0 + q * kAtOnce * 128) = make_uint4(two(y.x), two(y.y), two(y.z), two(y.w));
-              *(uint4*)(to + put1 + q * kAtOnce * 128) = make_uint4(two(z.x), two(z.y), two(z.z), two(z.w));
-            }
-            if (q % 2) asm volatile("" ::: "memory");  // two keys at a time
+            uint4 z[2];
+            Code<kE4m3>::word(c[q].x, z[0].x, z[0].y);
+            Code<kE4m3>::word(c[q].y, z[0].z, z[0].w);
+            Code<kE4m3>::word(c[q].z, z[1].x, z[1].y);
+            Code<kE4m3>::word(c[q].w, z[1].z, z[1].w);
+            *(uint4*)(to + put0 + q * kAtOnce * 128) = z[0];
+            *(uint4*)(to + put1 + q * kAtOnce * 128) = z[1];
           }
         }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&is_full[stage]);
-        if (++stage == kATStages) stage = 0, ++lap;
-        if (i + kAhead < units) load(i + kAhead, c[b]);
+      } else if (kind == kATPlain) {
+        float* scales = (values ? r.sv : r.sk)[slot];
+        const char* from = pool(kATPlain) + 16;
+        unsigned at[kRounds];
+        places(kATPlain, slot, at);
+#pragma unroll
+        for (int q = 0; q < kRounds; ++q) {
+          // the other 8 values came into L2 with the first: they share a sector
+          const int key = mine + q * kAtOnce;
+          const bool in = !(r.outside[slot][key >> 5] >> (key & 31) & 1u);
+          const uint4 other = stream16(from + at[q] * 16ull);
+          const uint4 y = on && in ? c[q] : make_uint4(0, 0, 0, 0), z = on && in ? other : make_uint4(0, 0, 0, 0);
+          const unsigned lo = max(max(max(y.x & 0x7fffu, y.y & 0x7fffu), max(y.z & 0x7fffu, y.w & 0x7fffu)),
+                                  max(max(z.x & 0x7fffu, z.y & 0x7fffu), max(z.z & 0x7fffu, z.w & 0x7fffu)));
+          const unsigned hi = max(max(max(y.x & 0x7fff0000u, y.y & 0x7fff0000u), max(y.z & 0x7fff0000u, y.w & 0x7fff0000u)),
+                                  max(max(z.x & 0x7fff0000u, z.y & 0x7fff0000u), max(z.z & 0x7fff0000u, z.w & 0x7fff0000u)));
+          unsigned top = max(lo << 16, hi);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          if (kPer >= 8) top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          if (kPer == 16) top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const bool finite = top < 0x7f800000u;
+          const float down = in && finite ? scale_down(top) : __uint_as_float(0x7fffffffu);
+          if (part == 0) scales[key] = down;
+          if (values) {
+            const unsigned above = __reduce_max_sync(0xffffffffu, in && finite ? (__float_as_uint(down) >> 23) + 1u : 0u);
+            if (lane == 0) atomicMax(&r.top[slot], above);
+          }
+          const float up = finite ? scale_up(top) : 0.f;
+          auto two = [&](uint32_t v) { return finite ? half2_of(bf16_lo(v) * up, bf16_hi(v) * up) : 0u; };
+          if (on) {
+            *(uint4*)(to + put0 + q * kAtOnce * 128) = make_uint4(two(y.x), two(y.y), two(y.z), two(y.w));
+            *(uint4*)(to + put1 + q * kAtOnce * 128) = make_uint4(two(z.x), two(z.y), two(z.z), two(z.w));
+          }
+          if (q % 2) asm volatile("" ::: "memory");  // two keys at a time
+        }
       }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&is_full[stage]);
+      if (++stage == kATStages) stage = 0, ++lap;
+      if (i + 1 < units) load(i + 1, c);
     }
   } else {
     if constexpr (L::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATIssueRegs));
