@@ -9,7 +9,7 @@
 // read once for each tile of 8.
 //
 // Measured (GB300; the codes' bytes at 6.77 TB/s beside it): single tokens, 64 sequences of
-// 4096 to 8192 entries, 32 heads to 8 of keys of 128, int8: 169 to 177 us (121); chains of 5 in
+// 4096 to 8192 entries, 32 heads to 8 of keys of 128, int8: 169 to 180 us (121); chains of 5 in
 // fp32, 8 sequences of up to 4000, 8 heads of 80: 31 us (4.4).  The first is bound by what a
 // warp does for 16 keys, turning codes to fp16 before all (the integer pipe is busy in 53 % of
 // the clocks, DRAM at 61 % of its peak, 168 registers leave 12 warps an SM); the second by the chain

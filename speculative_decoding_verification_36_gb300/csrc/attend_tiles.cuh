@@ -6,25 +6,25 @@
 //   P = weights    fp16, over S's columns in tensor memory
 //   O += P V       128 x D x 64, P from tensor memory, V from shared memory
 // Four warps bring keys and four values: codes go from global memory to registers a
-// unit ahead (two ahead: chains 306 us instead of 266, prompts 1096 instead of 845), become fp16 (exactly) and are written to shared memory in the 128-byte
-// swizzle; plain entries become fp16 times a power of two for each key.  Three warps look the
+// unit ahead (two ahead: chains 306 us instead of 266, prompts 1096 instead of 845; two warps for
+// each: chains 253, prompts 915), become fp16 (exactly) and are written to shared memory
+// in the 128-byte swizzle; plain entries become fp16 times a power of two for each key.  Three warps look the
 // entries' places and scales up further ahead.  Four warps make weights of scores: a
 // thread has one row, so that rows need no shuffles.  One thread issues the products.
 // Two CTAs share an SM (heads of more than 128: one, which has all the tensor memory): while one
-// waits for its weights, the other's products run, and what
-// is left to be shared is shared memory's bandwidth: 512 bytes a key and head written, 512 read.
+// waits for its weights, the other's products run.  They share shared memory's bandwidth: 512
+// bytes a key and head of 128 written, 512 read.
 //
 // Measured (GB300, 32 heads to 8 of keys of 128; the floor by bytes, or by products at 1.95
-// PFLOP/s, beside it): chains of 9, 64 sequences of 4096 to 8192 entries, int8: 307 us (123);
-// trees of 31 tokens, 32 such sequences, e4m3: 176 us (65); 5 tokens, two sequences of 131072 to
-// 262144, e4m3: 163 us (81); prompts of up to 2048 tokens behind 16384, int8: 1106 us (298); three
+// PFLOP/s, beside it): chains of 9, 64 sequences of 4096 to 8192 entries, int8: 266 us (123);
+// trees of 31 tokens, 32 such sequences, e4m3: 170 us (65); 5 tokens, two sequences of 131072 to
+// 262144, e4m3: 163 us (81); prompts of up to 2048 tokens behind 16384, int8: 846 us (298); three
 // tokens with 8 heads to one of 256, 16 sequences of 5000 to 10000: 46 us (9.4).
-// A unit takes a CTA 2000 to 3900 clocks, of which 800 to 1000 are its products and 1200 to
-// 1600 its weights, which take 450 with nothing else on the SM: the two CTAs' 32 warps issue
-// in half of all clocks (the int8 codes' five instructions for four take their part: e4m3's two
-// make it an eighth shorter), so a warp waits for its turn at each step, and S, weights and P V
-// follow on one another.  A segment costs a CTA some 15 000 clocks at its ends, most of them for
-// its queries: code that is run once comes to the SM from L2, too.
+// A unit takes a CTA 2000 to 3300 clocks.  800 to 1000 are its products.  Its weights took 1200 to
+// 1600 when last counted (with two units ahead), 450 with nothing else on the SM: the two CTAs' 32
+// warps issued in half of all clocks, so a warp waits for its turn at each step, and S, weights and
+// P V follow on one another.  A segment cost a CTA 15 000 to 20 000 clocks at its ends, most of
+// them for its queries.
 // Steps before: units of 128 keys with one CTA an SM 440 us (chains), queries in shared
 // memory 203 (trees), three stages or spilled registers slower (L1 is small beside this much
 // shared memory); tiles of up to 64 rows taken twice or four times, each copy with its part of the keys:
