@@ -203,6 +203,21 @@ def test_what_lies_on_other_pages_does_not_matter(T, Hq, D, dtype):
     assert torch.isnan(got[0, 16:]).all() and torch.equal(got[0, :16], good[0, :16]) and torch.equal(got[1], good[1])
 
 
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (256, BF16), (64, F32)])
+def test_a_whole_unit_without_a_page(D, dtype):
+    """The step's own second block of 64 has no page: tokens before it are as they were, the rest NaN."""
+    rng = np.random.default_rng(D)
+    x = attend_case(rng, 3, 140, 2, 1, D, dtype, "e4m3", 64, 16, [0, 64, 5], stored="step")
+    good = attend(x)
+    check(x, good)
+    lost = x["code_table"].copy()
+    lost[:, 1] = -1
+    got = attend(dict(x, code_table=lost))
+    assert sv.spec_get_status() == sv.SPEC_FLAG_BAD_DATA
+    for b, first in enumerate((64, 0, 59)):
+        assert torch.equal(got[b, :first], good[b, :first]) and torch.isnan(got[b, first:]).all()
+
+
 @pytest.mark.parametrize("T,dtype", [(2, BF16), (30, BF16), (4, F32)])
 def test_queries_off_16_byte_boundaries(T, dtype):
     rng = np.random.default_rng(T)
@@ -212,6 +227,24 @@ def test_queries_off_16_byte_boundaries(T, dtype):
     wide[..., 1:257] = x["q"].reshape(2, T, 256)
     x["q"] = wide[..., 1:257].view(2, T, 4, 64)
     assert torch.equal(attend(x), want)
+
+
+def test_calls_side_by_side():
+    """Calls of different head sizes on three streams share the SMs and their tensor memory."""
+    rng = np.random.default_rng(4)
+    xs = [attend_case(rng, 3, T, 8, 2, D, BF16, "int8", 16, 16, [3000, 10, 500]) for T, D in ((9, 256), (20, 128), (7, 64))]
+    args = [[x["q"], x["k"], x["v"], dev(x["table"]), dev(x["lengths"]), x["k_codes"], x["v_codes"], x["k_scales"], x["v_scales"],
+             dev(x["code_table"]), dev(x["stored"])] for x in xs]
+    want = [sv.spec_kv_attention(*a) for a in args]
+    outs = [[torch.empty_like(w) for _ in range(8)] for w in want]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for a, o, s in zip(args, outs, streams):
+            sv.spec_kv_attention(*a, out=o[i], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for w, many in zip(want, outs) for o in many)
+    assert sv.spec_get_status() == 0
 
 
 def test_nothing_to_do():
