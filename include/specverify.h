@@ -695,7 +695,7 @@ int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int 
  * fp16 parts, 22 bits).
  * Codes and scales are taken as spec_kv_quantize_* writes them: scales are not
  * negative, and an e4m3 code is no NaN (one that is reaches rows that do not see it,
- * too).  bf16 call: values of blocks whose scale is below 2^-64 may lose bits.
+ * too).  Values of blocks whose scale is below 2^-116 may lose bits.
  * A query row that is not finite makes its row of out NaN; so does a key or value
  * that is not finite (all the rows that see it), and a block whose scale is NaN
  * (rows that see one of its tokens).  What a row does not see has no part in it.

@@ -187,6 +187,9 @@ __device__ __forceinline__ float scale_down(unsigned bits) {
   return __uint_as_float((max(min(bits >> 23, 254u), 8u) - 7u) << 23);
 }
 
+// 2^k, 0 below fp32's normal values, 2^127 above.
+__device__ __forceinline__ float two_to(int k) { return __uint_as_float((unsigned)(max(min(k, 127), -127) + 127) << 23); }
+
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   uint32_t w;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
@@ -235,8 +238,16 @@ __device__ __forceinline__ void attend_store8(S* to, const float (&f)[8]) {
   }
 }
 
-// What a share leaves of a tile: floats [rows][DP], then the rows' maxima and sums.
-__host__ __device__ constexpr int attend_slot(int rows, int DP) { return rows * DP + 2 * rows; }
+// What a share leaves of a tile: floats [rows][DP], then the rows' maxima, sums and units: the
+// floats are in units of 2^unit, the sums are not.
+__host__ __device__ constexpr int attend_slot(int rows, int DP) { return rows * DP + 3 * rows; }
+__device__ __forceinline__ void attend_leave(float* part, int rows, int DP, int row, float m, float l, int unit) {
+  part += rows * DP + row;
+  part[0] = m, part[rows] = l, part[2 * rows] = __int_as_float(unit);
+}
+// The unit of values that come together under the maximum `most`: no weighted unit, 2^(m - most + unit),
+// is above it by more than a half.  (high: the largest m + unit, -infinity where there is none.)
+__device__ __forceinline__ int attend_unit(float high, float most) { return (int)fminf(fmaxf(rintf(high - most), -126.f), 126.f); }
 
 // What a share leaves for the joining: the last share of the segment that begins in it and goes
 // on, and its rows.
@@ -251,6 +262,7 @@ template <class S, int DP, int kRows>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ KvAttendArgs a) {
   constexpr int kSlot = attend_slot(kRows, DP), kN = DP / 32;
   __shared__ float s_f[4][DP], s_m[4], s_l[4];
+  __shared__ int s_unit[4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 meta = a.meta[blockIdx.x];
   if (meta.x < 0) return;
@@ -258,15 +270,17 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row0 = meta.w * kRows;
   auto slot = [&](int s) { return a.part + (2LL * (first + s) + (s == 0)) * kSlot; };
   float most, sum, f[kN];
+  int unit;  // f is in units of 2^unit
   // the shares from `from` to `to` of row r
   auto take = [&](int r, int from, int to) {
-    most = kLow, sum = 0.f;
+    most = kLow, sum = 0.f, unit = 0;
 #pragma unroll
     for (int k = 0; k < kN; ++k) f[k] = 0.f;
     for (int s = from; s < to; s += 8) {
       const int count = min(8, to - s);
-      const float* p = slot(s + min(lane, count - 1)) + kRows * DP + r;
+      const float* p = slot(s + min(lane & 7, count - 1)) + kRows * DP + r;
       const float m = p[0], l = p[kRows];
+      const int its = __float_as_int(p[2 * kRows]);
       float x[8][kN];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -276,16 +290,21 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
       }
       float top = fmaxf(m, most);
 #pragma unroll
-      for (int d = 16; d >= 1; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      for (int d = 4; d >= 1; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       const float by = ex2(m - top), old = ex2(most - top), part = l * by;
-      most = top;
+      float high = fmaxf(by > 0.f ? m + (float)its : -INFINITY, old > 0.f ? most + (float)unit : -INFINITY);
+#pragma unroll
+      for (int d = 4; d >= 1; d /= 2) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+      const int to_unit = attend_unit(high, top);
+      const float of = by * two_to(its - to_unit), old_of = old * two_to(unit - to_unit);
+      most = top, unit = to_unit;
       sum *= old;
 #pragma unroll
-      for (int k = 0; k < kN; ++k) f[k] *= old;
+      for (int k = 0; k < kN; ++k) f[k] *= old_of;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (e >= count) break;
-        const float w = __shfl_sync(0xffffffffu, by, e);
+        const float w = __shfl_sync(0xffffffffu, of, e);
         sum += __shfl_sync(0xffffffffu, part, e);
 #pragma unroll
         for (int k = 0; k < kN; ++k) f[k] += x[e][k] * w;
@@ -294,16 +313,17 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   };
   auto put = [&](int r) {
     if (kN * lane >= a.D) return;
-    const float by = sum == 0.f ? 0.f : 1.f / sum;
+    const int half = unit / 2;
+    const float by = sum == 0.f ? 0.f : 1.f / sum * two_to(half), rest = two_to(unit - half);
     const int token = fdiv(row0 + r, a.div_g);
     S* out = (S*)a.out + (((long long)meta.y * a.T + token) * a.Hq + (long long)meta.z * a.G + row0 + r - token * a.G) * a.D + kN * lane;
 #pragma unroll
     for (int k = 0; k < kN; k += 2) {
       if constexpr (sizeof(S) == 4) {
-        *(float2*)(out + k) = make_float2(f[k] * by, f[k + 1] * by);
+        *(float2*)(out + k) = make_float2(f[k] * by * rest, f[k + 1] * by * rest);
       } else {
         uint32_t y;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(f[k + 1] * by), "f"(f[k] * by));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(f[k + 1] * by * rest), "f"(f[k] * by * rest));
         *(uint32_t*)(out + k) = y;
       }
     }
@@ -319,21 +339,26 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const int each = (n + 3) / 4;
   for (int r = blockIdx.y; r < live; r += gridDim.y) {
     take(r, min(n, warp * each), min(n, (warp + 1) * each));
-    if (lane == 0) s_m[warp] = most, s_l[warp] = sum;
+    if (lane == 0) s_m[warp] = most, s_l[warp] = sum, s_unit[warp] = unit;
 #pragma unroll
     for (int k = 0; k < kN; ++k) s_f[warp][32 * k + lane] = f[k];
     __syncthreads();
     if (warp == 0) {
       most = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
       sum = 0.f;
+      float high = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (ex2(s_m[w] - most) > 0.f) high = fmaxf(high, s_m[w] + (float)s_unit[w]);
+      unit = attend_unit(high, most);
 #pragma unroll
       for (int k = 0; k < kN; ++k) f[k] = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float by = ex2(s_m[w] - most);
+        const float by = ex2(s_m[w] - most), of = by * two_to(s_unit[w] - unit);
         sum += s_l[w] * by;
 #pragma unroll
-        for (int k = 0; k < kN; ++k) f[k] += s_f[w][32 * k + lane] * by;
+        for (int k = 0; k < kN; ++k) f[k] += s_f[w][32 * k + lane] * of;
       }
       put(r);
     }

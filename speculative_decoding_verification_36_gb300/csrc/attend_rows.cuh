@@ -588,10 +588,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
     if (!whole) {
       if (warp == 0 && g == 0)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          part[kRows * DP + 2 * t + e] = m[e];
-          part[kRows * DP + kRows + 2 * t + e] = l[e];
-        }
+        for (int e = 0; e < 2; ++e) attend_leave(part, kRows, DP, 2 * t + e, m[e], l[e], 0);
       if (u0 == 0) {
         meta_last = attend_joint(attend_share_of(w, w.from + n - 1), min(kRows, rows - row0));
         meta_b = w.b, meta_h = w.h, meta_tile = w.tile;

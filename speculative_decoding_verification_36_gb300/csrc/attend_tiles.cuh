@@ -32,9 +32,9 @@
 // A check for each unit in the loading warps costs a tenth.
 //
 // The scales never touch the codes: a key's scale multiplies its scores, a value's its
-// weight.  With M = m + ref - 138 (m the running maximum in log2, ref exponent bits above every
-// scale of V that the row has seen) a weight is 2^(x - M) sv, below 2^15, and the row's sum is
-// that of 2^(x - M): the powers of two cancel in the quotient.
+// weight.  With m the running maximum (log2) and ref exponent bits above every scale of V that
+// the row has seen, a weight is 2^(x - m) sv 2^(138 - ref), below 2^15; the row's sum is that of
+// 2^(x - m) alone, so that no size of the values rescales it.
 #pragma once
 #include "attend_common.cuh"
 #include "sv_bulk.cuh"
@@ -52,7 +52,7 @@ constexpr int kATStages = 2;  // units whose keys and values are in shared memor
 constexpr int kATRing = 8;    // units whose places and scales are held
 constexpr int kATCodes = 0, kATPlain = 1, kATNone = 2;  // kinds of units (log2 of a value's bytes); the last: a bad sequence's, or one without pages
 constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
-constexpr unsigned kATLeastRef = 64;  // values below 2^-82 lose bits, which keeps a row's sum below 2^128
+constexpr unsigned kATLeastRef = 11;  // 2^(138 - ref) is finite
 
 // Shared memory; each operand begins on a 1024-byte boundary, as the swizzle wants.
 template <int DP>
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
       bar_sync(5, 32 * kATSoft);  // no warp is more than a segment ahead
       if (lane == 0) mbar_arrive(&r.q_full);
       const int last_seen = w.s.len + fdiv(row0 + row, a.div_g), first_seen = w.s.len + fdiv(row0, a.div_g);
-      float m = kLow, M = kLow, l = 0.f;
+      float m = kLow, l = 0.f, over = 0.f;
       unsigned ref = kATLeastRef;
       const int n_codes = w.s.bad ? 0 : (keys.codes + kATKeys - 1) / kATKeys;
       // units of codes that every row sees whole and whose keys share their scales by 16
@@ -314,11 +314,11 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
           const uint32_t t_s = tmem + lanes;
           // the maximum moves, and with it the sums: to a score of at least `most` (log2) and exponent bits `top`
           auto move = [&](float most, unsigned top) {
-            m = fmaxf(m, most);
-            ref = max(ref, min(top, 254u));
-            const float M2 = m + ((float)ref - 138.f), f = ex2(M - M2);
-            M = M2;
-            l *= f;
+            const float m2 = fmaxf(m, most), by = ex2(m - m2);
+            const unsigned ref2 = max(ref, min(top, 254u));
+            const float f = by * two_to((int)ref - (int)ref2);
+            m = m2, ref = ref2, over = two_to(138 - (int)ref);
+            l *= by;
             if (u > u0) {
 #pragma unroll 1
               for (int c = 0; c < DP; c += 16) {  // (no product is under way: the scores came after the last one)
@@ -343,12 +343,12 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
               tc_load16(t_s, x[0]);
               float most0 = -INFINITY, most1 = -INFINITY;  // of the exponents
               sum0 = sum1 = 0;
-              const f2_t less = f2(-M, -M);
+              const f2_t less = f2(-m, -m);
               tc_loaded16(x[0]);
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
                 if (g < 3) tc_load16(t_s + 16 * (g + 1), x[(g + 1) & 1]);
-                const float b = sk[16 * g] * qs, v = sv[16 * g];
+                const float b = sk[16 * g] * qs, v = sv[16 * g] * over;
                 const f2_t by = f2(b, b), of = f2(v, v);
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
                 if (g < 3) tc_loaded16(x[(g + 1) & 1]);
               }
               // (rows past the last hold anything; a score that is infinite outgrows every maximum)
-              if (again || !__any_sync(0xffffffffu, mine && (fmaxf(most0, most1) > kSlack + 138.f - (float)ref || top > ref))) break;
+              if (again || !__any_sync(0xffffffffu, mine && (fmaxf(most0, most1) > kSlack || top > ref))) break;
               float most = -INFINITY;
 #pragma unroll 1
               for (int g = 0; g < 4; ++g) {
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
             most *= qs;
             if (__any_sync(0xffffffffu, mine && (most > m + kSlack || top > ref))) move(most, top);
             f2_t sum = 0;
-            const f2_t less = f2(-M, -M), by = f2(qs, qs);
+            const f2_t less = f2(-m, -m), by = f2(qs, qs), of = f2(over, over);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1)) & 0xffffu;
@@ -456,9 +456,9 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
                 if (masked) {
                   const bool s0 = vis >> k & 1u, s1 = vis >> (k + 1) & 1u;
                   e = f2(s0 ? f2lo(e) : 0.f, s1 ? f2hi(e) : 0.f);
-                  z = f2mul(e, f2(s0 ? v.x : 0.f, s1 ? v.y : 0.f));
+                  z = f2mul(e, f2mul(f2(s0 ? v.x : 0.f, s1 ? v.y : 0.f), of));
                 } else {
-                  z = f2mul(e, f2(v.x, v.y));
+                  z = f2mul(e, f2mul(f2(v.x, v.y), of));
                 }
                 sum = f2add(sum, e);
                 p[k / 2] = half2_of(f2lo(z), f2hi(z));
@@ -479,7 +479,9 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
         tc_after();
         if (lost) l = __uint_as_float(0x7fffffffu);
         const bool whole = u0 == 0 && u1 == n;
-        const float by = l == 0.f ? 0.f : 1.f / l;
+        // the products' unit, 2^(ref - 138), in two steps: it may lie below fp32's normal values
+        const int unit = (int)ref - 138, half = unit / 2;
+        const float by = l == 0.f ? 0.f : 1.f / l * two_to(half), rest = two_to(unit - half);
         const int token = fdiv(row0 + row, a.div_g);
         uint16_t* out = (uint16_t*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + row - token * a.G) * a.D;
         float* part = a.part + (2LL * blockIdx.x + (u0 == 0)) * attend_slot(kATRows, DP);
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
               for (int e = 0; e < 2; ++e) {
                 float f[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = lost ? l : __uint_as_float(o[8 * e + k]) * by;
+                for (int k = 0; k < 8; ++k) f[k] = lost ? l : __uint_as_float(o[8 * e + k]) * by * rest;
                 attend_store8<uint16_t>(out + c + 8 * e, f);
               }
             } else {
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
           }
           __syncwarp();
         }
-        if (!whole && mine) part[kATRows * DP + row] = M, part[kATRows * DP + kATRows + row] = l;
+        if (!whole && mine) attend_leave(part, kATRows, DP, row, m, l, unit);
       }
       tc_before();
       if (u0 == 0 && u1 < n && threadIdx.x == 0) {
