@@ -690,9 +690,12 @@ int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int 
  *                 and those of the nodes above it.
  *   stored        [B] int32: tokens that are codes (spec_kv_quantize_*), a multiple
  *                 of block, at most lengths[b] + n_new[b].
- * Sums are held in fp32.  Queries, weights and plain entries enter the products
- * in fp16 times powers of two (bf16 call: at least 11 bits of each; fp32 call: two
- * fp16 parts, 22 bits).
+ * Sums are held in fp32.  Queries, weights and plain entries enter the products in
+ * fp16 times powers of two, in a bf16 call with 11 bits, in an fp32 call as two parts with 22.
+ * Of a query or an entry these count from its head's largest value, of a weight (exp of a
+ * score less the row's largest one, times the scale of the key's values) from the row's
+ * largest: what lies more than 2^-21 (fp32: 2^-10) below that has fewer bits, with an error
+ * of up to 2^-32 of the largest.  exp below 2^-126 counts as 0.
  * Codes and scales are taken as spec_kv_quantize_* writes them: scales are not
  * negative, and an e4m3 code is no NaN (one that is reaches rows that do not see it,
  * too).  Values of blocks whose scale is below 2^-116 may lose bits.

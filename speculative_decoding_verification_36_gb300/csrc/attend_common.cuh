@@ -170,8 +170,16 @@ __device__ __forceinline__ int attend_share_of(const Share& w, long long u) {
 }
 
 constexpr float kLow = -3.402823466e38f;  // a running maximum before any key
-constexpr float kSlack = 4.f;  // weights grow to 2^4 before the maximum moves (log2)
+constexpr float kSlack = 4.f;  // p grows to 2^4 before the maximum moves (log2)
+constexpr float kMostWeight = 32768.f;  // a weight grows to this before its unit moves
 
+// Weights go into the second product in fp16, as p sv 2^-unit: p = 2^(x - m) of a score x under the
+// running maximum m, sv the scale of the key's values.  2^unit follows the largest p sv of the row, which
+// becomes 2^7 to 2^10: weights stay below 2^15 until the unit moves again, have 11 bits down to 2^-21
+// of the largest and are off by 2^-32 of it below.  p below 2^-126 is 0.  (A unit of the largest sv
+// alone, whatever its p, lost all weights beside one key with values 2^36 times theirs, though it
+// counted for nothing.  2^9 to 2^12 has two bits more and moves more often: 31 tokens of 32
+// sequences of 8192 170 us instead of 167, prompts 793 instead of 781.)
 // Ancestors of a token as bits: token 0 is the root, token j + 1 node j.
 __device__ __forceinline__ void attend_bits(const int* parents, int token, int words, uint32_t* bits) {
   for (int w = 0; w < words; ++w) bits[w] = 0;
@@ -238,6 +246,17 @@ __device__ __forceinline__ void attend_store8(S* to, const float (&f)[8]) {
   }
 }
 
+// The unit of values that come together under the maximum `most`: no weighted unit, 2^(m - most + unit),
+// is above it by more than a half.  (high: the largest m + unit, -infinity where there is none.)
+__device__ __forceinline__ int attend_unit(float high, float most) { return (int)fminf(fmaxf(rintf(high - most), -126.f), 126.f); }
+// The unit of weights under the maximum `most`, where the largest x + log_above(sv) is `high`.
+__device__ __forceinline__ int attend_weight_unit(float high, float most) { return max(attend_unit(high, most) - 9, -126); }
+// The exponent of the power of two above a scale; -infinity of one that is not finite: it makes its weights NaN whatever the unit.
+__device__ __forceinline__ float log_above(float scale) {
+  const unsigned bits = __float_as_uint(scale);
+  return bits < 0x7f800000u ? (float)((int)(bits >> 23) - 126) : -INFINITY;
+}
+
 // What a share leaves of a tile: floats [rows][DP], then the rows' maxima, sums and units: the
 // floats are in units of 2^unit, the sums are not.
 __host__ __device__ constexpr int attend_slot(int rows, int DP) { return rows * DP + 3 * rows; }
@@ -245,9 +264,6 @@ __device__ __forceinline__ void attend_leave(float* part, int rows, int DP, int 
   part += rows * DP + row;
   part[0] = m, part[rows] = l, part[2 * rows] = __int_as_float(unit);
 }
-// The unit of values that come together under the maximum `most`: no weighted unit, 2^(m - most + unit),
-// is above it by more than a half.  (high: the largest m + unit, -infinity where there is none.)
-__device__ __forceinline__ int attend_unit(float high, float most) { return (int)fminf(fmaxf(rintf(high - most), -126.f), 126.f); }
 
 // What a share leaves for the joining: the last share of the segment that begins in it and goes
 // on, and its rows.

@@ -22,7 +22,7 @@
 // scale multiplies the score or the weight, never the code.  Queries come as fp16
 // times a power of two for each row (bf16 queries exactly, fp32 ones as a sum of two
 // fp16 parts), weights as fp16 (fp32: two parts) times a power of two that follows the
-// values' scales.  Plain entries become fp16 (two parts) times a power of two for each
+// weighted scales of the values.  Plain entries become fp16 (two parts) times a power of two for each
 // key.  The softmax runs in the log2 domain with one pass over the keys.
 #pragma once
 #include "attend_common.cuh"
@@ -85,7 +85,7 @@ struct Rows {
     return row * DP + ((u ^ turn) << 4);
   }
   static constexpr size_t smem(int T, bool tree) {
-    return (size_t)kParts * kFrag * 8 + (size_t)kARWarps * kStages * kStage + 2 * kARWarps * kARRows * 4 + kARRows * 4 +
+    return (size_t)kParts * kFrag * 8 + (size_t)kARWarps * kStages * kStage + 3 * kARWarps * kARRows * 4 + kARRows * 4 +
            (tree ? (size_t)T * 4 + (size_t)kARRows * ((T + 31) / 32) * 4 : 0);
   }
 };
@@ -134,9 +134,10 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
   uint2* s_q = (uint2*)s_attend;                                      // [parts][steps][32]
   unsigned char* s_ring = (unsigned char*)(s_q + R::kParts * R::kFrag);  // the warps' rings, then
   float* s_acc = (float*)s_ring;                                      // [NT][4][32]
-  float* s_m = (float*)(s_ring + kARWarps * R::kStages * R::kStage);  // [warps][rows], then sums
+  float* s_m = (float*)(s_ring + kARWarps * R::kStages * R::kStage);  // [warps][rows], then sums and units
   float* s_l = s_m + kARWarps * kRows;
-  float* s_qs = s_l + kARWarps * kRows;                               // [rows]
+  int* s_unit = (int*)(s_l + kARWarps * kRows);
+  float* s_qs = (float*)(s_unit + kARWarps * kRows);                  // [rows]
   int* s_par = (int*)(s_qs + kRows);                                  // [T]
   uint32_t* s_bits = (uint32_t*)(s_par + a.T);                        // [rows][words]
   __shared__ unsigned long long s_scan[kARThreads + 1];
@@ -206,14 +207,15 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
 
     // ---- the lane's rows, 2 t and the next ----
     float qs[2], m[2], l[2];
-    int seen[2];       // a chain's last key
-    unsigned ref[2];   // exponent bits above every scale of V that the row has seen
+    int seen[2];                // a chain's last key
+    float high[2], over[2];     // the largest x + log_above(sv), and 2^-unit
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       qs[e] = s_qs[2 * t + e];
       m[e] = kLow;
       l[e] = 0.f;
-      ref[e] = 11u;
+      high[e] = kLow;
+      over[e] = 1.f;
       seen[e] = w.s.len + fdiv(row0 + 2 * t + e, a.div_g);
     }
     const int first_seen = w.s.len + fdiv(row0, a.div_g);
@@ -228,57 +230,55 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       return at < 0 || (lost ? false : ((s_bits[(2 * t + e) * words + (at >> 5)] >> (at & 31)) & 1u) != 0);
     };
 
+    auto unit_of = [](float over) { return 127 - (int)(__float_as_uint(over) >> 23); };
+
     // Scores of the keys base + g and base + g + 8 (c[0], c[1] and c[2], c[3]) to weights.
     // sk, sv: the keys' scales.  wt: the weights as the products' right sides.
     auto weights = [&](const float (&c)[4], const float (&sk)[2], const float (&sv)[2], int base, int end, bool masked, uint2 (&wt)[R::kParts]) {
       float x[2][2];  // [row][key]
-      unsigned top[2];  // exponents above the keys' scales of V; a scale that is not finite makes its weights NaN whatever the reference
-#pragma unroll
-      for (int k = 0; k < 2; ++k) top[k] = __float_as_uint(sv[k]) < 0x7f800000u ? (__float_as_uint(sv[k]) >> 23) + 1u : 0u;
-      bool grow = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           x[e][k] = c[2 * k + e] * (sk[k] * qs[e]);
-          const bool see = !masked || visible(e, base + g + 8 * k, end);
-          if (!see) x[e][k] = -INFINITY;
-          grow |= x[e][k] > m[e] + kSlack || (see && top[k] > ref[e]);
+          if (masked && !visible(e, base + g + 8 * k, end)) x[e][k] = -INFINITY;
         }
       }
-      if (__any_sync(0xffffffffu, grow)) {
+      // Weights under the maximum and the unit as they are; where a row has outgrown them, they move
+      // and the weights are taken again.
+      float y[2][2], p[2][2];  // [key][row]
+      for (bool again = false;; again = true) {
+        bool grow = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float y = fmaxf(fmaxf(x[e][0], x[e][1]), m[e]);
-          unsigned to = ref[e];
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (!masked || x[e][k] != -INFINITY) to = max(to, top[k]);
+          for (int k = 0; k < 2; ++k) {
+            p[k][e] = ex2(x[e][k] - m[e]);
+            y[k][e] = masked && x[e][k] == -INFINITY ? 0.f : p[k][e] * sv[k] * over[e];
+            grow |= x[e][k] > m[e] + kSlack || y[k][e] > kMostWeight;
+          }
+        }
+        if (again || !__any_sync(0xffffffffu, grow)) break;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float most = fmaxf(fmaxf(x[e][0], x[e][1]), m[e]);
+          high[e] = fmaxf(high[e], fmaxf(x[e][0] + log_above(sv[0]), x[e][1] + log_above(sv[1])));
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) {
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-            to = max(to, __shfl_xor_sync(0xffffffffu, to, d));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+            high[e] = fmaxf(high[e], __shfl_xor_sync(0xffffffffu, high[e], d));
           }
-          const float f = ex2(m[e] - y), both = f * ex2((float)((int)ref[e] - (int)to));
-          m[e] = y;
-          ref[e] = to;
+          const int unit = attend_weight_unit(high[e], most);
+          const float f = ex2(m[e] - most), both = f * two_to(unit_of(over[e]) - unit);
+          m[e] = most;
+          over[e] = two_to(-unit);
           l[e] *= f;
 #pragma unroll
           for (int j = 0; j < NT; ++j) o[j][e] *= both, o[j][2 + e] *= both;
         }
       }
-      float y[2][2];  // [key][row]
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // 2^11 over the reference: weights stay below 2^15 and keep fp16's full precision 2^25 below it
-        const float over = __uint_as_float((265u - ref[e]) << 23);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float p = ex2(x[e][k] - m[e]);
-          l[e] += p;
-          y[k][e] = masked && x[e][k] == -INFINITY ? 0.f : p * (sv[k] * over);
-        }
-      }
+      for (int e = 0; e < 2; ++e) l[e] += p[0][e] + p[1][e];
       const uint32_t w0 = half2_of(y[0][0], y[0][1]), w1 = half2_of(y[1][0], y[1][1]);
       wt[0] = make_uint2(turned(w0), turned(w1));
       if constexpr (kTwo) wt[1] = make_uint2(turned(rest_of(y[0][0], y[0][1], w0)), turned(rest_of(y[1][0], y[1][1], w1)));
@@ -533,23 +533,29 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
 #pragma unroll
       for (int d = 4; d < 32; d *= 2) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
       if (lost) l[e] = __uint_as_float(0x7fffffffu);
-      if (g == 0) s_m[warp * kRows + 2 * t + e] = m[e], s_l[warp * kRows + 2 * t + e] = l[e];
+      if (g == 0) {
+        const int at = warp * kRows + 2 * t + e;
+        s_m[at] = m[e], s_l[at] = l[e], s_unit[at] = unit_of(over[e]);
+      }
     }
     __syncthreads();
-    float factor[2], back[2];
+    float factor[2];
+    int unit[2];  // of the sums
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 2 * t + e;
       float most = s_m[r];
 #pragma unroll
       for (int x = 1; x < kARWarps; ++x) most = fmaxf(most, s_m[x * kRows + r]);
-      float sum = 0.f;
+      float sum = 0.f, top = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < kARWarps; ++x) sum += s_l[x * kRows + r] * ex2(s_m[x * kRows + r] - most);
-      // 2^(ref - 138) in two steps: it may lie below fp32's normal values
-      const int half = ((int)ref[e] - 138) / 2;
-      factor[e] = ex2(m[e] - most) * __uint_as_float((unsigned)(127 + half) << 23);
-      back[e] = __uint_as_float((unsigned)((int)ref[e] - 11 - half) << 23);
+      for (int x = 0; x < kARWarps; ++x) {
+        const float by = ex2(s_m[x * kRows + r] - most);
+        sum += s_l[x * kRows + r] * by;
+        if (by > 0.f) top = fmaxf(top, s_m[x * kRows + r] + (float)s_unit[x * kRows + r]);
+      }
+      unit[e] = attend_unit(top, most);
+      factor[e] = ex2(m[e] - most) * two_to(unit_of(over[e]) - unit[e]);
       m[e] = most;
       l[e] = sum;
     }
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float* to = s_acc + (j * 4 + e) * 32 + lane;
-            const float y = o[j][e] * factor[e & 1] * back[e & 1];
+            const float y = o[j][e] * factor[e & 1];
             *to = x ? *to + y : y;
           }
       }
@@ -574,10 +580,13 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
     for (int x = warp; x < 2 * (NT / 4); x += kARWarps) {
       const int e = x & 1, oct = x >> 1, r = 2 * t + e, d = g * (DP / 8) + 8 * oct;
       if (row0 + r >= rows || d >= a.D) continue;
-      const float by = !whole ? 1.f : l[0] == 0.f && !e || l[1] == 0.f && e ? 0.f : 1.f / (e ? l[1] : l[0]);
+      // 2^unit in two steps: their product may lie outside fp32's normal values
+      const int its = e ? unit[1] : unit[0], half = its / 2;
+      const float by = !whole ? 1.f : l[0] == 0.f && !e || l[1] == 0.f && e ? 0.f : 1.f / (e ? l[1] : l[0]) * two_to(half);
+      const float rest = whole ? two_to(its - half) : 1.f;
       float f[8];
 #pragma unroll
-      for (int y = 0; y < 8; ++y) f[y] = s_acc[((4 * oct + y / 2) * 4 + 2 * (y & 1) + e) * 32 + lane] * by;
+      for (int y = 0; y < 8; ++y) f[y] = s_acc[((4 * oct + y / 2) * 4 + 2 * (y & 1) + e) * 32 + lane] * by * rest;
       if (whole) {
         const int token = fdiv(row0 + r, a.div_g);
         attend_store8<S>((S*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + r - token * a.G) * a.D + d, f);
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
     if (!whole) {
       if (warp == 0 && g == 0)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) attend_leave(part, kRows, DP, 2 * t + e, m[e], l[e], 0);
+        for (int e = 0; e < 2; ++e) attend_leave(part, kRows, DP, 2 * t + e, m[e], l[e], unit[e]);
       if (u0 == 0) {
         meta_last = attend_joint(attend_share_of(w, w.from + n - 1), min(kRows, rows - row0));
         meta_b = w.b, meta_h = w.h, meta_tile = w.tile;

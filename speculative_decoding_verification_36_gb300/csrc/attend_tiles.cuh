@@ -32,9 +32,10 @@
 // A check for each unit in the loading warps costs a tenth.
 //
 // The scales never touch the codes: a key's scale multiplies its scores, a value's its
-// weight.  With m the running maximum (log2) and ref exponent bits above every scale of V that
-// the row has seen, a weight is 2^(x - m) sv 2^(138 - ref), below 2^15; the row's sum is that of
-// 2^(x - m) alone, so that no size of the values rescales it.
+// weight.  With m the running maximum (log2) a weight is 2^(x - m) sv 2^-unit, below 2^15, where
+// 2^unit follows the largest 2^(x - m) sv that the row has seen: a key with large values and
+// little weight takes no bits from the others.  The row's sum is that of 2^(x - m) alone, so that no
+// size of the values rescales it.
 #pragma once
 #include "attend_common.cuh"
 #include "sv_bulk.cuh"
@@ -52,7 +53,6 @@ constexpr int kATStages = 2;  // units whose keys and values are in shared memor
 constexpr int kATRing = 8;    // units whose places and scales are held
 constexpr int kATCodes = 0, kATPlain = 1, kATNone = 2;  // kinds of units (log2 of a value's bytes); the last: a bad sequence's, or one without pages
 constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
-constexpr unsigned kATLeastRef = 11;  // 2^(138 - ref) is finite
 
 // Shared memory; each operand begins on a 1024-byte boundary, as the swizzle wants.
 template <int DP>
@@ -70,7 +70,7 @@ struct Tiles {
     // outside, or none yet); the keys of a loading thread side by side
     unsigned at[2][kATRing][kATKeys];
     unsigned outside[kATRing][kATKeys / 32];  // keys whose page is outside, as bits
-    unsigned top[kATRing];         // exponent bits above a unit's scales of V
+    float top[kATRing];            // exponent bits above a unit's scales of V
     uint32_t bits[kATRows][4];
     int parents[128];
     unsigned long long at_full[kATRing], at_empty[kATRing], k_full[kATStages], k_empty[kATStages], v_full[kATStages],
@@ -297,8 +297,9 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
       bar_sync(5, 32 * kATSoft);  // no warp is more than a segment ahead
       if (lane == 0) mbar_arrive(&r.q_full);
       const int last_seen = w.s.len + fdiv(row0 + row, a.div_g), first_seen = w.s.len + fdiv(row0, a.div_g);
-      float m = kLow, l = 0.f, over = 0.f;
-      unsigned ref = kATLeastRef;
+      float m = kLow, high = kLow, l = 0.f, over = 1.f;  // high: the largest x + log_above(sv)
+      float room = 142.f;  // 15 + 127 + unit
+      int unit = 0;        // over = 2^-unit
       const int n_codes = w.s.bad ? 0 : (keys.codes + kATKeys - 1) / kATKeys;
       // units of codes that every row sees whole and whose keys share their scales by 16
       const int u_groups = w.s.bad || a.block % 16 ? 0 : min(keys.codes, a.parents ? w.s.len : first_seen + 1) / kATKeys;
@@ -312,14 +313,15 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
           const int slot = i & (kATRing - 1);
           const float *sk = r.sk[slot], *sv = r.sv[slot];
           const uint32_t t_s = tmem + lanes;
-          // the maximum moves, and with it the sums: to a score of at least `most` (log2) and exponent bits `top`
-          auto move = [&](float most, unsigned top) {
+          // the maximum and the unit move, and with them the sums: to scores up to `most` and weighted scales up to `weighted` (log2)
+          auto move = [&](float most, float weighted) {
             const float m2 = fmaxf(m, most), by = ex2(m - m2);
-            const unsigned ref2 = max(ref, min(top, 254u));
-            const float f = by * two_to((int)ref - (int)ref2);
-            m = m2, ref = ref2, over = two_to(138 - (int)ref);
+            high = fmaxf(high, weighted);
+            const int unit2 = attend_weight_unit(high, m2);
+            const float f = by * two_to(unit - unit2);
+            m = m2, unit = unit2, over = two_to(-unit), room = (float)(142 + unit);
             l *= by;
-            if (u > u0) {
+            if (u > u0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
               for (int c = 0; c < DP; c += 16) {  // (no product is under way: the scores came after the last one)
                 uint32_t o[16];
@@ -332,10 +334,13 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
               }
             }
           };
-          if (u < u_groups) {
-            // Scores to weights under the maximum as it is; where one of the warp's rows has
+          // how far above the maximum a score of a unit may be, its exponent bits being up to `top`, for weights below 2^15
+          auto limit = [&](float top) { return fminf(kSlack, room - top); };
+          bool grouped = u < u_groups;
+          if (grouped) {
+            const float top = r.top[slot];
+            // Scores to weights under the maximum as it is; where one of the warp's rows may have
             // outgrown it, it moves and the scores, which are still there, are taken again.
-            const unsigned top = r.top[slot];
             uint32_t p[32];
             f2_t sum0, sum1;
             for (bool again = false;; again = true) {
@@ -367,8 +372,13 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
                 if (g < 3) tc_loaded16(x[(g + 1) & 1]);
               }
               // (rows past the last hold anything; a score that is infinite outgrows every maximum)
-              if (again || !__any_sync(0xffffffffu, mine && (fmaxf(most0, most1) > kSlack || top > ref))) break;
-              float most = -INFINITY;
+              const float lim = limit(top);
+              if (!__any_sync(0xffffffffu, mine && (fmaxf(most0, most1) > lim || lim < -96.f))) break;
+              if (again) {
+                grouped = !__any_sync(0xffffffffu, mine && lim < -96.f);  // sv over may not be finite
+                break;
+              }
+              float most = -INFINITY, weighted = -INFINITY;
 #pragma unroll 1
               for (int g = 0; g < 4; ++g) {
                 uint32_t z[16];
@@ -377,15 +387,20 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
                 float y = __uint_as_float(z[0]);
 #pragma unroll
                 for (int k = 1; k < 16; ++k) y = fmaxf(y, __uint_as_float(z[k]));
-                most = fmaxf(most, y * sk[16 * g]);
+                y *= sk[16 * g] * qs;  // (a maximum takes no NaN)
+                most = fmaxf(most, y);
+                weighted = fmaxf(weighted, y + log_above(sv[16 * g]));
               }
-              move(most * qs, top);  // (a scale of 0: -inf becomes NaN, which no maximum takes)
+              move(most, weighted);
             }
-            sum0 = f2add(sum0, sum1);
-            l += f2lo(sum0) + f2hi(sum0);
-            tc_store16(t_s, p);
-            tc_store16(t_s + 16, p + 16);
-          } else {
+            if (grouped) {
+              sum0 = f2add(sum0, sum1);
+              l += f2lo(sum0) + f2hi(sum0);
+              tc_store16(t_s, p);
+              tc_store16(t_s + 16, p + 16);
+            }
+          }
+          if (!grouped) {
             // A scale for each key, and keys that some rows do not see: twice over the scores, 16
             // at a time.  What is not seen has no part, whatever its scales are.
             const bool codes = u < n_codes;
@@ -408,7 +423,8 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
             };
             const uint32_t vis0 = seen(unit), vis1 = seen(unit + 32);
             float most = -INFINITY;
-            unsigned top = masked ? 0u : r.top[slot];
+            const f2_t by = f2(qs, qs);
+            float top = masked ? 0.f : r.top[slot];
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1)) & 0xffffu;
@@ -420,8 +436,9 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
 #pragma unroll
               for (int k = 0; k < 16; k += 4) {
                 const float4 y = *(const float4*)(sk + 16 * c + k);
-                const float z0 = __uint_as_float(x[k]) * y.x, z1 = __uint_as_float(x[k + 1]) * y.y, z2 = __uint_as_float(x[k + 2]) * y.z,
-                            z3 = __uint_as_float(x[k + 3]) * y.w;
+                const f2_t y0 = f2mul(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2mul(f2(y.x, y.y), by));
+                const f2_t y1 = f2mul(f2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), f2mul(f2(y.z, y.w), by));
+                const float z0 = f2lo(y0), z1 = f2hi(y0), z2 = f2lo(y1), z3 = f2hi(y1);
                 if (masked) {
                   const uint4 v = *(const uint4*)(sv + 16 * c + k);
                   most = fmaxf(fmaxf(most, vis >> k & 1u ? z0 : -INFINITY), vis >> (k + 1) & 1u ? z1 : -INFINITY);
@@ -432,12 +449,24 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
                   most = fmaxf(most, fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)));
                 }
               }
-              if (masked) top = max(top, bits < 0x7f800000u ? (bits >> 23) + 1u : 0u);
+              if (masked) top = fmaxf(top, bits < 0x7f800000u ? (float)((bits >> 23) + 1u) : 0.f);
             }
-            most *= qs;
-            if (__any_sync(0xffffffffu, mine && (most > m + kSlack || top > ref))) move(most, top);
+            if (__any_sync(0xffffffffu, mine && most - m > limit(top))) {
+              float weighted = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1)) & 0xffffu;
+                uint32_t x[16];
+                tc_load16(t_s + 16 * c, x);
+                tc_loaded16(x);
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  if (vis >> k & 1u) weighted = fmaxf(weighted, __uint_as_float(x[k]) * (sk[16 * c + k] * qs) + log_above(sv[16 * c + k]));
+              }
+              move(most, weighted);
+            }
             f2_t sum = 0;
-            const f2_t less = f2(-m, -m), by = f2(qs, qs), of = f2(over, over);
+            const f2_t less = f2(-m, -m), of = f2(over, over);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1)) & 0xffffu;
@@ -451,14 +480,14 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
                 const float2 y = *(const float2*)(sk + 16 * c + k), v = *(const float2*)(sv + 16 * c + k);
-                const f2_t t = f2fma(f2mul(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2(y.x, y.y)), by, less);
+                const f2_t t = f2fma(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2mul(f2(y.x, y.y), by), less);
                 f2_t e = f2(ex2(f2lo(t)), ex2(f2hi(t))), z;
                 if (masked) {
                   const bool s0 = vis >> k & 1u, s1 = vis >> (k + 1) & 1u;
                   e = f2(s0 ? f2lo(e) : 0.f, s1 ? f2hi(e) : 0.f);
-                  z = f2mul(e, f2mul(f2(s0 ? v.x : 0.f, s1 ? v.y : 0.f), of));
+                  z = f2mul(f2mul(e, f2(s0 ? v.x : 0.f, s1 ? v.y : 0.f)), of);
                 } else {
-                  z = f2mul(e, f2mul(f2(v.x, v.y), of));
+                  z = f2mul(f2mul(e, f2(v.x, v.y)), of);
                 }
                 sum = f2add(sum, e);
                 p[k / 2] = half2_of(f2lo(z), f2hi(z));
@@ -479,8 +508,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
         tc_after();
         if (lost) l = __uint_as_float(0x7fffffffu);
         const bool whole = u0 == 0 && u1 == n;
-        // the products' unit, 2^(ref - 138), in two steps: it may lie below fp32's normal values
-        const int unit = (int)ref - 138, half = unit / 2;
+        const int half = unit / 2;  // 2^unit in two steps: their product may lie outside fp32's normal values
         const float by = l == 0.f ? 0.f : 1.f / l * two_to(half), rest = two_to(unit - half);
         const int token = fdiv(row0 + row, a.div_g);
         uint16_t* out = (uint16_t*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + row - token * a.G) * a.D;
@@ -610,7 +638,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
           if (part == 0) scales[key] = down;
           if (values) {
             const unsigned above = __reduce_max_sync(0xffffffffu, in && finite ? (__float_as_uint(down) >> 23) + 1u : 0u);
-            if (lane == 0) atomicMax(&r.top[slot], above);
+            if (lane == 0) atomicMax((unsigned*)&r.top[slot], __float_as_uint((float)above));
           }
           const float up = finite ? scale_up(top) : 0.f;
           auto two = [&](uint32_t v) { return finite ? half2_of(bf16_lo(v) * up, bf16_hi(v) * up) : 0u; };
@@ -726,7 +754,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
             for (int q = 0; q < kQ; ++q)
               if (__float_as_uint(sv[q]) < 0x7f800000u) top = max(top, (__float_as_uint(sv[q]) >> 23) + 1u);
             top = __reduce_max_sync(0xffffffffu, top);
-            if (lane == 0) r.top[slot] = top;
+            if (lane == 0) r.top[slot] = (float)top;
             // Codes of a page outside may be seen by some rows alone, and a product with a weight of 0 has to
             // be 0: another key of the unit stands for them or, if there is none, what lies in shared memory.
             const int some = __reduce_max_sync(0xffffffffu, max(at[0], at[kQ - 1]));

@@ -25,9 +25,9 @@ def check_weighted(x, got, only=None):
 
     A weight p (the largest p of a row is at least 1, l is their sum) enters the second product as
     w = p s / 2^unit in fp16, s its key's scale.  2^unit follows the largest p s that the row has
-    seen: that one is at least 2^9 in these units.  fp16 is off by its relative step (counted with
-    the weight) or by 2^-25, which is 2^-34 of the largest p s.  A code is at most 448, a plain
-    entry below 256: a key may add 2^-34 * 448 max(p s) / l.
+    seen: that one is at least 2^7 in these units.  fp16 is off by its relative step (counted with
+    the weight) or by 2^-25, which is 2^-32 of the largest p s.  A code is at most 448, a plain
+    entry below 256: a key may add 2^-32 * 448 max(p s) / l.
     p below 2^-126 counts as 0: at most 2^-126 * 448 s a key, as l is at least 1."""
     B, T, Hq, D = x["q"].shape
     q, got = x["q"].double().cpu().numpy(), got.double().cpu().numpy()
@@ -46,7 +46,7 @@ def check_weighted(x, got, only=None):
             z = np.where(see, z.T, -np.inf)
             p = np.exp(z - z.max(1, keepdims=True))
             size = s[:, h // (Hq // k.shape[1])]
-            tol[:, h] += 448 * ((2.0 ** -34 * keys * (p * size).max(1) / p.sum(1)) + 2.0 ** -126 * np.where(see, size, 0).sum(1))[:, None]
+            tol[:, h] += 448 * ((2.0 ** -32 * keys * (p * size).max(1) / p.sum(1)) + 2.0 ** -126 * np.where(see, size, 0).sum(1))[:, None]
         tol += (2.0 ** -24 if two else 2.0 ** -8) * (np.abs(out) + tol)
         assert np.isfinite(got[b, :n]).all() and np.isfinite(out).all()
         off = np.abs(got[b, :n] - out)
@@ -88,4 +88,29 @@ def test_the_sum_of_weights_does_not_go_by_the_values(T, Hq, D, dtype, first, la
     rng = np.random.default_rng(D)
     x = sized_case(rng, 1, T, Hq, D, dtype, "int8", 16, ctx, lambda s: 0.0, lambda s: first if s < ctx // 2 else later)
     check_weighted(x, attend(x))
+    assert sv.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("B,ctx", [(1, 1024), (1, 6400), (200, 1024)])  # shares of a unit, of a few, of many
+@pytest.mark.parametrize("block", [4, 16])  # others beside it in a unit, in a product
+@pytest.mark.parametrize("fmt,outlier", [("int8", 2.0 ** 25), ("e4m3", 2.0 ** 36), ("int8", 2.0 ** 60), ("int8", 2.0 ** 120)])
+@pytest.mark.parametrize("T,Hq,D,dtype", KINDS)
+def test_large_values_of_little_weight(T, Hq, D, dtype, fmt, outlier, block, B, ctx):
+    """A block whose values are far larger than all others and whose weight is e^-100 of theirs."""
+    rng = np.random.default_rng(D)
+    at = 16 * (ctx // 48)
+    x = sized_case(rng, B, T, Hq, D, dtype, fmt, block, ctx, lambda s: -100.0 if s == at else 0.0, lambda s: outlier if s == at else 1.0, tail=1.0)
+    check_weighted(x, attend(x), only=range(0, B, 67))
+    assert sv.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("down", [80.0, 120.0])
+@pytest.mark.parametrize("T,Hq,D,dtype", KINDS)
+def test_large_values_whose_weight_falls(T, Hq, D, dtype, down):
+    """The first values are the largest and their scores the lowest: what they add in the end goes down
+    with the scores that come after, in small steps and in one."""
+    rng = np.random.default_rng(D)
+    for steps in (1, 4, 60):
+        x = sized_case(rng, 200, T, Hq, D, dtype, "int8", 16, 1024, lambda s: down * (s // 16 * steps // 64 / steps - 1), lambda s: 2.0 ** 80 if s < 32 else 1.0)
+        check_weighted(x, attend(x), only=(0, 77, 199))
     assert sv.spec_get_status() == 0
