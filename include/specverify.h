@@ -615,7 +615,7 @@ int spec_kv_commit(void *key_cache, void *value_cache, int layers, int64_t layer
  * Strides are read when layers > 1.
  * D is a multiple of 16 up to 256, Hkv * D up to 2^24, 1 <= block <= 65536,
  * pages * page_size and code_pages * block below 2^31, max_code_pages <= 2^23 and
- * max_code_pages * block <= 2^26, 1 <= layers <= 32767; the pools of entries and
+ * max_code_pages * block <= 2^26, 1 <= layers <= 32767, 0 <= B <= 2^30; the pools of entries and
  * codes (and every layer of them) start on 16-byte boundaries.
  *
  * spec_kv_quantize_* makes codes of the whole blocks among the tokens [stored[b],

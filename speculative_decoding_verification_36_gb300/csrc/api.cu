@@ -726,7 +726,7 @@ struct Kv8Sizes {
 constexpr int kMaxCodePages = 1 << 23;          // of a sequence, and its tokens: a round of
 constexpr long long kMaxCodeTokens = 1LL << 26; // sequences is counted in 32 bits
 bool kv8_sizes_ok(const Kv8Sizes& z) {
-  return z.layers >= 1 && z.layers <= 32767 && z.B >= 0 && z.Hkv >= 1 && z.D >= 16 && z.D <= 256 && z.D % 16 == 0 &&
+  return z.layers >= 1 && z.layers <= 32767 && z.B >= 0 && z.B <= kMaxListed && z.Hkv >= 1 && z.D >= 16 && z.D <= 256 && z.D % 16 == 0 &&
          (long long)z.Hkv * z.D <= (1 << 24) && z.pages >= 1 && z.page_size >= 1 && z.max_pages >= 1 &&
          (long long)z.pages * z.page_size <= INT_MAX && z.code_pages >= 1 && z.block >= 1 && z.block <= 65536 &&
          (long long)z.code_pages * z.block <= INT_MAX && z.max_code_pages >= 1 && z.max_code_pages <= kMaxCodePages &&
