@@ -707,7 +707,8 @@ int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int 
  * T rows of that sequence are NaN.  A page outside its pool: the rows that see one
  * of its tokens are NaN.
  * T >= 0 (<= 1025 with parent_idx), Hq a multiple of Hkv, Hq * D up to 2^24, T * Hq
- * up to 2^30, B * T < 2^31, scale finite; the rest as above.  out shares no
+ * up to 2^30, B * T < 2^31, |scale| up to 2^127 (a query's largest value times scale, too, or
+ * its row may be NaN); the rest as above.  out shares no
  * memory with an input (SPEC_ERR_OVERLAP).  Returns SPEC_OK, SPEC_ERR_NULL,
  * SPEC_ERR_SHAPE, SPEC_ERR_OVERLAP or SPEC_ERR_CUDA.  Two launches on `stream`.
  * Scratch: for each share of the work (up to 5 CTAs an SM) the sums of two tiles of 8

@@ -821,6 +821,8 @@ int kv8_impl(bool bf16, bool quantize, const Kv8Sizes& z, const void* k_cache, c
   return SPEC_OK;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 int attention_impl(bool bf16, const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int pages, int page_size,
                    const int32_t* page_table, int max_pages, const int32_t* lengths, const int32_t* n_new, const int32_t* parents,
                    const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales, int code_pages, int block,
@@ -828,7 +830,7 @@ int attention_impl(bool bf16, const void* q, int64_t q_stride, const void* k_cac
                    int D, float scale, void* out, cudaStream_t stream) {
   const Kv8Sizes z = {1, pages, page_size, max_pages, code_pages, block, max_code_pages, B, Hkv, D, format};
   if (!kv8_sizes_ok(z) || T < 0 || Hq < 1 || Hq % Hkv || (long long)Hq * D > (1 << 24) || (long long)B * T > INT_MAX ||
-      (long long)T * Hq > (1 << 30) || q_stride < (long long)Hq * D || (parents && T > sv::kMaxTreeNodes + 1) || !isfinite(scale))
+      (long long)T * Hq > (1 << 30) || q_stride < (long long)Hq * D || (parents && T > sv::kMaxTreeNodes + 1) || !isfinite(scale * kLog2e))
     return SPEC_ERR_SHAPE;
   if (B == 0 || T == 0) return SPEC_OK;
   if (!q || !k_cache || !v_cache || !page_table || !lengths || !k_codes || !v_codes || !k_scales || !v_scales || !code_table ||
@@ -873,7 +875,7 @@ int attention_impl(bool bf16, const void* q, int64_t q_stride, const void* k_cac
   a.Hkv = Hkv;
   a.D = D;
   a.G = Hq / Hkv;
-  a.scale = scale * 1.4426950408889634f;
+  a.scale = scale * kLog2e;
   a.div_block = sv::make_fastdiv((uint32_t)block);
   a.div_page = sv::make_fastdiv((uint32_t)page_size);
   a.div_g = sv::make_fastdiv((uint32_t)a.G);

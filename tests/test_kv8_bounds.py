@@ -21,3 +21,10 @@ def test_batches(lib, t, B):
     assert quantize(lib, "spec_kv_quantize_" + t, B=B, **far) == _lib.SPEC_ERR_SHAPE
     assert dequantize(lib, "spec_kv_dequantize_" + t, B=B, **far) == _lib.SPEC_ERR_SHAPE
     assert attention(lib, t, B=B, T=1, out=0x600000000000) == _lib.SPEC_ERR_SHAPE
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.4e38, -3.0e38])
+def test_scales_past_the_exponent_s_range(lib, t, scale):
+    """The scale is taken times log2(e), which has to be finite in fp32 too."""
+    assert attention(lib, t, scale=scale) == _lib.SPEC_ERR_SHAPE
