@@ -269,6 +269,27 @@ __device__ __forceinline__ void attend_leave(float* part, int rows, int DP, int 
 // on, and its rows.
 __device__ __forceinline__ int attend_joint(int last, int rows) { return last | rows << 16; }
 
+// All T rows of a sequence with a bad parent are NaN.  The rows below n_new[b] are the other kernel's, which
+// meets the tree with them; padding is written here, and a tree without tokens is looked at here alone.
+template <class S>
+__device__ __forceinline__ void attend_padding(const KvAttendArgs& a) {
+  const int N = a.T - 1;
+  for (int b = blockIdx.y * gridDim.x + blockIdx.x; b < a.B; b += gridDim.x * gridDim.y) {
+    const Sequence s = attend_sequence(a, b);
+    if (s.n_new == a.T) continue;
+    bool wrong = false;
+    for (int j = threadIdx.x; j < N; j += blockDim.x) {
+      const int p = __ldg(a.parents + (long long)b * N + j);
+      wrong |= p < -1 || p >= j;
+    }
+    if (!__syncthreads_or(wrong)) continue;
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusBadData);
+    const long long row = (long long)a.Hq * a.D, end = (a.T - s.n_new) * row;
+    S* out = (S*)a.out + ((long long)b * a.T + s.n_new) * row;
+    for (long long i = threadIdx.x; i < end; i += blockDim.x) out[i] = (S)0x7fffffffu;  // NaN in either type
+  }
+}
+
 // Joins a segment that fell into several shares, in their order: CTAs x join the one that
 // begins in share x and goes on.  A warp asks for the maxima, sums and values of 8 shares at once.  Either each warp
 // has rows of its own or the four take a quarter of a row's shares each, whichever waits for
@@ -279,6 +300,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   constexpr int kSlot = attend_slot(kRows, DP), kN = DP / 32;
   __shared__ float s_f[4][DP], s_m[4], s_l[4];
   __shared__ int s_unit[4];
+  if (a.parents && a.n_new) attend_padding<S>(a);  // (beside the other kernel, which writes other rows)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 meta = a.meta[blockIdx.x];
   if (meta.x < 0) return;

@@ -1,0 +1,26 @@
+"""Attention to the 8-bit cache at the edges of what its documentation allows."""
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verification_36_gb300 as sv
+from test_gpu_kv8 import BF16, F32, attend, attend_case, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,dtype", [(4, BF16), (40, BF16), (200, BF16), (5, F32)])
+def test_bad_parents_of_a_padded_sequence(T, dtype):
+    """A parent outside [-1, i) makes all T rows of its sequence NaN, those of padding too, wherever it lies and
+    however few tokens there are; padding of the other sequences stays."""
+    rng = np.random.default_rng(T)
+    for n_new in (0, 1, T - 1, T):
+        for node, parent in ((T - 2, T - 2), (0, -2)):
+            x = attend_case(rng, 4, T, 4, 2, 64, dtype, "int8", 16, 16, [64, 300, 5, 40], tree=True)
+            x["n_new"] = np.array([n_new, 0, T, T // 2], np.int32)
+            x["parents"][0, node] = parent
+            out = torch.full(x["q"].shape, 5.0, dtype=dtype, device=x["q"].device)
+            got = attend(x, out=out)
+            assert sv.spec_get_status() == sv.SPEC_FLAG_BAD_DATA
+            assert torch.isnan(got[0]).all()
+            check(x, got, skip=[0])
