@@ -766,6 +766,14 @@ int spec_test_spin_limit(uint32_t iterations);
 int spec_test_wait_probe(uint32_t* out_flags);
 
 /*
+ * The same for the waits of spec_kv_attention_bf16 with more than 8 rows a head of
+ * keys.  out_flags (host, 3 words): [0] whether a wait on a complete phase counted as
+ * run out, [1] whether one on a phase that stays open did, [2] how often later
+ * waits may look again: {0, 1, 0} for a correct library.
+ */
+int spec_test_attend_wait_probe(uint32_t* out_flags);
+
+/*
  * Synchronises `stream`, then returns in *flags_out (may be NULL) the device
  * status word of the current device (an OR of SPEC_FLAG_* set by every call
  * since the last read) and clears it.  Returns SPEC_OK or SPEC_ERR_CUDA.

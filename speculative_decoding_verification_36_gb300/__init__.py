@@ -44,7 +44,7 @@ __all__ = [
     "spec_tree_verify_greedy", "spec_tree_verify_sampling", "spec_acceptance_stats", "spec_ngram_draft",
     "spec_token_state", "spec_count_tokens", "spec_process_logits", "spec_rope_turns", "spec_kv_append",
     "spec_kv_commit", "spec_kv_quantize", "spec_kv_dequantize", "spec_kv_attention",
-    "spec_get_status", "spec_test_spin_limit", "spec_test_wait_probe", "SpecError",
+    "spec_get_status", "spec_test_spin_limit", "spec_test_wait_probe", "spec_test_attend_wait_probe", "SpecError",
     "SPEC_FLAG_BAD_DATA", "SPEC_FLAG_TIMEOUT",
 ]
 
@@ -789,3 +789,16 @@ def spec_test_wait_probe(device=None) -> tuple:
     with torch.cuda.device(dev):
         _lib.check(_lib.load().spec_test_wait_probe(ctypes.addressof(flags)))
     return int(flags[0]), int(flags[1])
+
+
+def spec_test_attend_wait_probe(device=None) -> tuple:
+    """Test hook: runs the wait of the attention's kernel for many rows on a complete
+    phase and on one that stays open, under the current limit.  Returns (the first
+    counted as run out, the second did, looks left to later waits); a correct library
+    gives (0, 1, 0)."""
+    import ctypes
+    flags = (ctypes.c_uint32 * 3)()
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(dev):
+        _lib.check(_lib.load().spec_test_attend_wait_probe(ctypes.addressof(flags)))
+    return tuple(int(x) for x in flags)

@@ -78,6 +78,7 @@ SIGNATURES = {
     "spec_test_fail_allocations": [_I],
     "spec_test_spin_limit": [ctypes.c_uint32],
     "spec_test_wait_probe": [ctypes.c_void_p],
+    "spec_test_attend_wait_probe": [ctypes.c_void_p],
     "spec_get_status": [_P, _P],
     "spec_status_string": [_I],
 }

@@ -1358,6 +1358,16 @@ int spec_test_wait_probe(uint32_t* out_flags) {
   return SPEC_OK;
 }
 
+int spec_test_attend_wait_probe(uint32_t* out_flags) {
+  if (!out_flags) return SPEC_ERR_NULL;
+  DeviceState* d = nullptr;
+  const int rc = get_device_state(&d);
+  if (rc) return rc;
+  const cudaError_t e = sv::attend_wait_probe(out_flags);
+  if (e != cudaSuccess) return cuda_fail(e, "attention wait probe");
+  return SPEC_OK;
+}
+
 int spec_get_status(cudaStream_t stream, uint32_t* flags_out) {
   DeviceState* d = nullptr;
   int rc = get_device_state(&d);

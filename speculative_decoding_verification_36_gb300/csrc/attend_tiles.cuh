@@ -54,6 +54,20 @@ constexpr int kATRing = 8;    // units whose places and scales are held
 constexpr int kATCodes = 0, kATPlain = 1, kATNone = 2;  // kinds of units (log2 of a value's bytes); the last: a bad sequence's, or one without pages
 constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
 
+// A CTA's waits.  Once one has run out all warps go on without waiting and take part in every
+// barrier that is left: no warp waits for one that is gone.
+struct Waits {
+  volatile unsigned tries;  // of a wait after its first look, 0 once one has run out
+  volatile unsigned out;    // one has
+};
+__device__ __forceinline__ void bounded_wait(Waits& w, unsigned long long* bar, unsigned parity) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return;
+  for (unsigned n = __reduce_min_sync(0xffffffffu, w.tries); n > 0; --n)
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity & 1))) return;
+  w.tries = 0;
+  w.out = 1;
+}
+
 // Shared memory; each operand begins on a 1024-byte boundary, as the swizzle wants.
 template <int DP>
 struct Tiles {
@@ -77,7 +91,7 @@ struct Tiles {
         v_empty[kATStages], s_full, p_ready, pv_done, q_full, drain;
     uint32_t tmem;
     int wrong;
-    volatile unsigned tries;  // of a wait, 0 once one has run out
+    Waits waits;
     int meta[4];
     int live;  // rows of the segment
   };
@@ -176,7 +190,8 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
     mbar_init(&r.q_full, kATSoft);
     mbar_init(&r.drain, 1);
     r.wrong = 0;
-    r.tries = mbar_tries(spin_limit());
+    r.waits.tries = mbar_tries(spin_limit());
+    r.waits.out = 0;
     r.meta[0] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -194,15 +209,9 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&r.tmem;
   const uint32_t t_q = tmem + 64, t_o = tmem + L::kO;  // S, then its weights, at 0
-  // Once a wait has run out all warps go on without waiting and take part in every
-  // barrier that is left: no warp waits for one that is gone.  What they then read may be another
-  // unit's, and the places in shared memory are at any time ones inside their pools.
-  auto wait = [&](unsigned long long* bar, unsigned parity) {
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return;
-    for (unsigned n = __reduce_min_sync(0xffffffffu, r.tries); n > 0; --n)
-      if (__all_sync(0xffffffffu, mbar_try(bar, parity & 1))) return;
-    r.tries = 0;
-  };
+  // After a wait that ran out, what the warps read may be another unit's, and the places in shared
+  // memory are at any time ones inside their pools.
+  auto wait = [&](unsigned long long* bar, unsigned parity) { bounded_wait(r.waits, bar, parity); };
 
   if (warp < kATSoft) {
     if constexpr (L::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kATSoftRegs));
@@ -707,7 +716,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
       // nothing of the tensor cores is in flight when the tensor memory goes back
       if (leader) tc_commit(&r.drain);
       __syncwarp();
-      if (!warp_wait(&r.drain, 0, mbar_tries(kSpinLimit))) r.tries = 0;
+      if (!warp_wait(&r.drain, 0, mbar_tries(kSpinLimit))) r.waits.out = 1;
     } else {
       // ===================================================================
       // places and scales: this warp's units
@@ -778,7 +787,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
   }
   tc_before();
   __syncthreads();
-  if (threadIdx.x == 0 && r.tries == 0) atomicOr(a.status, kStatusTimeout);
+  if (threadIdx.x == 0 && r.waits.out) atomicOr(a.status, kStatusTimeout);
   if (warp == kIssue) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kColumns) : "memory");

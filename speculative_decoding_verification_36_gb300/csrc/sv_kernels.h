@@ -395,6 +395,8 @@ constexpr unsigned long long kAttendTilesMaxPool = 1ull << 36;  // bytes: places
 cudaError_t launch_attend_tiles_int8(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
 cudaError_t launch_attend_tiles_e4m3(const KvAttendArgs& a, int sms, size_t* bytes, cudaStream_t s);
 cudaError_t attend_tiles_int8_set_spin_limit(unsigned n);
+// Runs that kernel's wait on a phase that is complete and on one that stays open (test hook; synchronous).
+cudaError_t attend_wait_probe(uint32_t* flags_host);
 cudaError_t attend_tiles_e4m3_set_spin_limit(unsigned n);
 
 // Resident CTAs per SM for each kernel (occupancy calculator).

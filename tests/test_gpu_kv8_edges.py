@@ -24,3 +24,15 @@ def test_bad_parents_of_a_padded_sequence(T, dtype):
             assert sv.spec_get_status() == sv.SPEC_FLAG_BAD_DATA
             assert torch.isnan(got[0]).all()
             check(x, got, skip=[0])
+
+
+@pytest.mark.parametrize("limit", [1, 31, 64, 2000])
+def test_a_wait_that_ran_out_is_told_from_one_that_did_not(limit):
+    """Also under limits that leave a wait one look: a complete phase is no timeout, one that stays open is, and
+    later waits do not wait."""
+    try:
+        sv.spec_test_spin_limit(limit)
+        assert sv.spec_test_attend_wait_probe() == (0, 1, 0)
+    finally:
+        sv.spec_test_spin_limit(0)
+    assert sv.spec_get_status() == 0
