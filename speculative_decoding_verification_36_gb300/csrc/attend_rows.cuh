@@ -629,8 +629,10 @@ static cudaError_t launch_rows(KvAttendArgs a, int sms, size_t* bytes, cudaStrea
     return cudaSuccess;
   }
   a.meta = (int4*)((char*)a.part + slots);
-  if (smem > 47 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The attribute is the largest tree's, always: another host thread's call may set it between this one's and the launch.
+  constexpr size_t most_smem = R::smem(kMaxTreeNodes + 1, true);
+  if (most_smem > 47 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem);
     if (e != cudaSuccess) return e;
   }
   kernel<<<grid, kARThreads, smem, s>>>(a);

@@ -1,9 +1,14 @@
 """Attention to the 8-bit cache at the edges of what its documentation allows."""
+import os
+import shutil
+import subprocess
+
 import numpy as np
 import pytest
 import torch
 
 import speculative_decoding_verification_36_gb300 as sv
+from speculative_decoding_verification_36_gb300 import _lib
 from test_gpu_kv8 import BF16, F32, attend, attend_case, check
 
 pytestmark = pytest.mark.gpu
@@ -36,3 +41,21 @@ def test_a_wait_that_ran_out_is_told_from_one_that_did_not(limit):
     finally:
         sv.spec_test_spin_limit(0)
     assert sv.spec_get_status() == 0
+
+
+def test_two_threads_whose_trees_differ(tmp_path):
+    """Launches of one kernel with shared memory of different sizes, from two host threads."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    _lib.load()  # the library is built
+    here = os.path.dirname(os.path.abspath(__file__))
+    cuda, libdir = os.environ.get("CUDA_HOME", "/usr/local/cuda"), os.path.dirname(_lib.LIB_PATH)
+    exe = str(tmp_path / "c_abi_threads")
+    res = subprocess.run([cc, "-O2", "-std=c99", "-I", os.path.join(os.path.dirname(here), "include"), "-I", os.path.join(cuda, "include"),
+                          os.path.join(here, "c_abi_threads.c"), "-o", exe, "-L", libdir, "-l:libspecverify.so", f"-Wl,-rpath,{libdir}",
+                          "-L", os.path.join(cuda, "lib64"), "-lcudart", f"-Wl,-rpath,{os.path.join(cuda, 'lib64')}", "-lpthread"],
+                         capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    res = subprocess.run([exe], capture_output=True, text=True, timeout=100)
+    assert res.returncode == 0, (res.returncode, res.stderr)
