@@ -690,7 +690,8 @@ int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int 
  *                 and those of the nodes above it.
  *   stored        [B] int32: tokens that are codes (spec_kv_quantize_*), a multiple
  *                 of block, at most lengths[b] + n_new[b].
- * Sums are held in fp32.  Queries, weights and plain entries enter the products in
+ * Sums are held in fp32; those of the products over the keys come out up to 2^-12 small in a
+ * bf16 call (the tensor cores drop bits; 2^-14 in the mean), whatever the length.  Queries, weights and plain entries enter the products in
  * fp16 times powers of two, in a bf16 call with 11 bits, in an fp32 call as two parts with 22.
  * Of a query or an entry these count from its head's largest value, of a weight (exp of a
  * score less the row's largest one, times the scale of the key's values) from the row's

@@ -34,6 +34,9 @@ constexpr int kARThreads = 128;
 constexpr int kARWarps = kARThreads / 32;
 constexpr int kARRows = 8;              // of a tile
 constexpr int kARKeys = 16 * kARWarps;  // keys of a unit: 16 to a warp
+// Units whose products a warp adds up.  The products' sums drop bits, up to 2^-23 of the sum for each 16
+// keys, always downwards: 2^-12 in as many units.  Longer runs are taken in pieces and added up in the workspace.
+constexpr int kARPiece = 2048;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint2& b) {
   asm(
@@ -149,9 +152,11 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
   int meta_last = -1, meta_b = 0, meta_h = 0, meta_tile = 0;
   int loaded_b = -1, loaded_tile = -1;
   bool bad = false;
+  int done = 0;  // of the share's units of the segment
   while (w.left > 0) {
     const int n = attend_units<kRows, kARKeys>(a, w.s, w.tile);
-    const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
+    const int last = (int)min((long long)n, w.u + w.left);
+    const int u0 = w.u + done, u1 = min(last, u0 + kARPiece);
     const Keys keys = attend_keys<kRows>(a, w.s, w.tile);
     const int row0 = w.tile * kRows, rows = w.s.n_new * a.G;
 
@@ -539,7 +544,9 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       }
     }
     __syncthreads();
-    float factor[2];
+    const bool more = done > 0;  // to sums that are in the workspace
+    float* part = a.part + (2LL * blockIdx.x + (w.u == 0)) * attend_slot(kRows, DP);
+    float factor[2], of[2];
     int unit[2];  // of the sums
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -547,7 +554,15 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       float most = s_m[r];
 #pragma unroll
       for (int x = 1; x < kARWarps; ++x) most = fmaxf(most, s_m[x * kRows + r]);
-      float sum = 0.f, top = -INFINITY;
+      float sum = 0.f, top = -INFINITY, old = 0.f;
+      int its = 0;
+      if (more) {
+        const float* there = part + kRows * DP + r;
+        most = fmaxf(most, there[0]);
+        old = ex2(there[0] - most), its = __float_as_int(there[2 * kRows]);
+        sum = there[kRows] * old;
+        if (old > 0.f) top = there[0] + (float)its;
+      }
 #pragma unroll
       for (int x = 0; x < kARWarps; ++x) {
         const float by = ex2(s_m[x * kRows + r] - most);
@@ -556,6 +571,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       }
       unit[e] = attend_unit(top, most);
       factor[e] = ex2(m[e] - most) * two_to(unit_of(over[e]) - unit[e]);
+      of[e] = old * two_to(its - unit[e]);
       m[e] = most;
       l[e] = sum;
     }
@@ -574,8 +590,7 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
     }
 
     // ---- out, or to the workspace ----
-    const bool whole = u0 == 0 && u1 == n;
-    float* part = a.part + (2LL * blockIdx.x + (u0 == 0)) * attend_slot(kRows, DP);
+    const bool whole = w.u == 0 && u1 == n;
     // item: row 2 t + e of a lane, eight of its values in a row
     for (int x = warp; x < 2 * (NT / 4); x += kARWarps) {
       const int e = x & 1, oct = x >> 1, r = 2 * t + e, d = g * (DP / 8) + 8 * oct;
@@ -586,7 +601,11 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       const float rest = whole ? two_to(its - half) : 1.f;
       float f[8];
 #pragma unroll
-      for (int y = 0; y < 8; ++y) f[y] = s_acc[((4 * oct + y / 2) * 4 + 2 * (y & 1) + e) * 32 + lane] * by * rest;
+      for (int y = 0; y < 8; ++y) {
+        f[y] = s_acc[((4 * oct + y / 2) * 4 + 2 * (y & 1) + e) * 32 + lane];
+        if (more) f[y] += part[r * DP + d + y] * (e ? of[1] : of[0]);
+        f[y] = f[y] * by * rest;
+      }
       if (whole) {
         const int token = fdiv(row0 + r, a.div_g);
         attend_store8<S>((S*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + r - token * a.G) * a.D + d, f);
@@ -598,12 +617,15 @@ __global__ void __launch_bounds__(kARThreads, kCtas) attend_rows_kernel(const __
       if (warp == 0 && g == 0)
 #pragma unroll
         for (int e = 0; e < 2; ++e) attend_leave(part, kRows, DP, 2 * t + e, m[e], l[e], unit[e]);
-      if (u0 == 0) {
+      if (w.u == 0 && last < n) {
         meta_last = attend_joint(attend_share_of(w, w.from + n - 1), min(kRows, rows - row0));
         meta_b = w.b, meta_h = w.h, meta_tile = w.tile;
       }
     }
-    attend_advance<kRows, kARKeys>(a, w, u1 - u0);
+    done += u1 - u0;
+    if (u1 < last) continue;  // (the slot is read behind the next barrier)
+    attend_advance<kRows, kARKeys>(a, w, done);
+    done = 0;
   }
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(meta_last, meta_b, meta_h, meta_tile);
 }

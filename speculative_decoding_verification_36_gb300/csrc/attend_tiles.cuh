@@ -52,6 +52,10 @@ static_assert(2 * kATThreads * 64 <= 65536 && 32 * kATSoft * kATSoftRegs + 64 * 
 constexpr int kATStages = 2;  // units whose keys and values are in shared memory
 constexpr int kATRing = 8;    // units whose places and scales are held
 constexpr int kATCodes = 0, kATPlain = 1, kATNone = 2;  // kinds of units (log2 of a value's bytes); the last: a bad sequence's, or one without pages
+// Units whose products are added up in tensor memory.  The products' sums drop bits, up to 2^-23 of the sum for each 16
+// keys, always downwards: 2^-12 in as many units.  (Without an end to it 262144 keys in one CTA came out
+// 0.1 to 0.2 % small.)  Longer runs are taken in pieces and added up in the workspace, in fp32.
+constexpr int kATPiece = 512;
 constexpr int kATLook = 3;    // warps that look them up, by turns: two trips to memory a unit
 
 // A CTA's waits.  Once one has run out all warps go on without waiting and take part in every
@@ -220,15 +224,16 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
     // =====================================================================
     const int row = 32 * warp + lane;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    int i = 0;  // units so far
+    int i = 0;     // units so far
+    int done = 0;  // of the share's units of the segment
     int loaded_b = -1, loaded_tile = -1;
     bool bad = false;
     while (w.left > 0) {
-      const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
-      const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
+      const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile), last = (int)min((long long)n, w.u + w.left);
+      const int u0 = w.u + done, u1 = min(last, u0 + kATPiece);
       const Keys keys = attend_keys<kATRows>(a, w.s, w.tile);
       const int row0 = w.tile * kATRows, rows = w.s.n_new * a.G;
-      // ---- queries to shared memory: all scores of the last segment are there ----
+      // ---- queries to shared memory: all scores of the last piece are there ----
       if (a.parents && (w.b != loaded_b || w.tile != loaded_tile)) {
         bar_sync(5, 32 * kATSoft);  // nobody reads the last tree
         if (threadIdx.x == 0) r.wrong = 0;
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
         tc_stored();
       }
       tc_before();
-      bar_sync(5, 32 * kATSoft);  // no warp is more than a segment ahead
+      bar_sync(5, 32 * kATSoft);  // no warp is more than a piece ahead
       if (lane == 0) mbar_arrive(&r.q_full);
       const int last_seen = w.s.len + fdiv(row0 + row, a.div_g), first_seen = w.s.len + fdiv(row0, a.div_g);
       float m = kLow, high = kLow, l = 0.f, over = 1.f;  // high: the largest x + log_above(sv)
@@ -516,12 +521,32 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
         wait(&r.pv_done, i - 1);
         tc_after();
         if (lost) l = __uint_as_float(0x7fffffffu);
-        const bool whole = u0 == 0 && u1 == n;
+        const bool whole = w.u == 0 && u1 == n;
+        float* part = a.part + (2LL * blockIdx.x + (w.u == 0)) * attend_slot(kATRows, DP);
+        if (done > 0) {  // with the sums that are in the workspace
+          const float* there = part + kATRows * DP + (mine ? row : 0);
+          const float most = fmaxf(m, there[0]), f = ex2(m - most), old = ex2(there[0] - most);
+          const int its = __float_as_int(there[2 * kATRows]);
+          const int to = attend_unit(fmaxf(f > 0.f ? m + (float)unit : -INFINITY, old > 0.f ? there[0] + (float)its : -INFINITY), most);
+          const float of = old * two_to(its - to), now = f * two_to(unit - to);
+          l = l * f + there[kATRows] * old;
+          m = most, unit = to;
+#pragma unroll 1
+          for (int c = 0; c < a.D; c += 16) {
+            uint32_t o[16];
+            tc_load16(t_o + lanes + c, o);
+            tc_loaded16(o);
+            const float* x = part + (mine ? row : 0) * DP + c;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * now + x[e] * of);
+            tc_store16(t_o + lanes + c, o);
+          }
+          tc_stored();
+        }
         const int half = unit / 2;  // 2^unit in two steps: their product may lie outside fp32's normal values
         const float by = l == 0.f ? 0.f : 1.f / l * two_to(half), rest = two_to(unit - half);
         const int token = fdiv(row0 + row, a.div_g);
         uint16_t* out = (uint16_t*)a.out + (((long long)w.b * a.T + token) * a.Hq + (long long)w.h * a.G + row0 + row - token * a.G) * a.D;
-        float* part = a.part + (2LL * blockIdx.x + (u0 == 0)) * attend_slot(kATRows, DP);
 #pragma unroll 1
         for (int c = 0; c < DP; c += 16) {
           uint32_t o[16];
@@ -547,11 +572,14 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
         if (!whole && mine) attend_leave(part, kATRows, DP, row, m, l, unit);
       }
       tc_before();
-      if (u0 == 0 && u1 < n && threadIdx.x == 0) {
+      done += u1 - u0;
+      if (u1 < last) continue;
+      if (w.u == 0 && last < n && threadIdx.x == 0) {
         r.meta[0] = attend_joint(attend_share_of(w, w.from + n - 1), r.live);
         r.meta[1] = w.b, r.meta[2] = w.h, r.meta[3] = w.tile;
       }
-      attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
+      attend_advance<kATRows, kATKeys>(a, w, done);
+      done = 0;
     }
   } else if (warp < kIssue) {
     if constexpr (L::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kATLoadRegs));
@@ -677,11 +705,11 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
       const unsigned long long d_k = tc_operand(smem_addr(base + L::kK), 16), d_v = tc_operand(smem_addr(base + L::kV), L::kChunk);
       const uint32_t kind_s = tc_kind(kATKeys, false), kind_o = tc_kind(a.D, true);
       const int steps = a.D / 16;
-      int i = 0, stage = 0, lap = 0, segments = 0;
+      int i = 0, stage = 0, lap = 0, pieces = 0, done = 0;
       while (w.left > 0) {
-        const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile);
-        const int u0 = w.u, u1 = (int)min((long long)n, u0 + w.left);
-        wait(&r.q_full, segments++);
+        const int n = attend_units<kATRows, kATKeys>(a, w.s, w.tile), last = (int)min((long long)n, w.u + w.left);
+        const int u0 = w.u + done, u1 = min(last, u0 + kATPiece);
+        wait(&r.q_full, pieces++);
         for (int u = u0; u < u1; ++u, ++i) {
           wait(&r.k_full[stage], lap);
           if (i > 0) wait(&r.pv_done, i - 1);  // S's columns hold the weights of the last unit until P V has read them
@@ -711,7 +739,10 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
           __syncwarp();
           if (++stage == kATStages) stage = 0, ++lap;
         }
-        attend_advance<kATRows, kATKeys>(a, w, u1 - u0);
+        done += u1 - u0;
+        if (u1 < last) continue;
+        attend_advance<kATRows, kATKeys>(a, w, done);
+        done = 0;
       }
       // nothing of the tensor cores is in flight when the tensor memory goes back
       if (leader) tc_commit(&r.drain);

@@ -114,3 +114,31 @@ def test_large_values_whose_weight_falls(T, Hq, D, dtype, down):
         x = sized_case(rng, 200, T, Hq, D, dtype, "int8", 16, 1024, lambda s: down * (s // 16 * steps // 64 / steps - 1), lambda s: 2.0 ** 80 if s < 32 else 1.0)
         check_weighted(x, attend(x), only=(0, 77, 199))
     assert sv.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("T,D,dtype,B,blocks", [(9, 64, BF16, 310, 8192), (9, 256, BF16, 155, 8192), (40, 128, BF16, 305, 8192), (1, 128, BF16, 460, 16384),
+                                                (1, 64, F32, 620, 16384)])
+def test_sums_of_many_keys_do_not_drift(T, D, dtype, B, blocks):
+    """Many sequences of the same 2^19 or 2^20 entries with equal weights: a CTA has a whole sequence or most of one.
+
+    An entry is c * 1027 * 2^-10, exact in the products, and its sum takes more than 24 bits.  These c lie 2^-12 to
+    2^-11 above the middle of two bf16 numbers.  A sum may drop 2^-23 for each 16 keys (there are no more
+    than 2048 such steps in a row: 2^-12), so that the upper one has to come out.  fp32: 2048 sums of 64 keys in a
+    row, each rounded by 2^-24, and the sum of the up to 8 such sums: 2^-13 + 2^-21."""
+    block = 64
+    code = torch.tensor([47, 48, 49, 50, 51, 94, 95, 96, 97, 98, 99, 100, 101, 102])[torch.arange(D) % 14]
+    want = code.double() * 1027 * 2.0 ** -10
+    dev_ = "cuda"
+    codes = code.to(torch.int8).to(dev_).expand(blocks, block, 1, D).contiguous()
+    scales = torch.full((blocks, 1), 1027 * 2.0 ** -10, device=dev_)
+    cache = want.to(torch.bfloat16).to(dtype).to(dev_).expand(1, block, 1, D).contiguous()
+    code_table = torch.arange(blocks, dtype=torch.int32, device=dev_).expand(B, blocks).contiguous()
+    lengths = torch.full((B,), blocks * block, dtype=torch.int32, device=dev_)
+    table = torch.zeros((B, blocks + 1), dtype=torch.int32, device=dev_)
+    q = torch.zeros((B, T, 1, D), dtype=dtype, device=dev_)
+    got = sv.spec_kv_attention(q, cache, cache, table, lengths, codes, codes, scales, scales, code_table, lengths)
+    assert sv.spec_get_status() == 0
+    if dtype == BF16:
+        assert torch.equal(got, want.to(BF16).to(dev_).expand_as(got))
+    else:
+        assert float((got.double() / want.to(dev_) - 1).abs().max()) <= 2.0 ** -13 + 2.0 ** -21 + 2.0 ** -24
