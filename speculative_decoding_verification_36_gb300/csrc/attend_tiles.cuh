@@ -82,7 +82,7 @@ struct Tiles {
   static constexpr int kChunk = kATKeys * 128;      // its rows of 64 fp16
   static constexpr int kK = 0, kV = kATStages * kTile, kRest = 2 * kATStages * kTile;
   struct Rest {
-    float sk[kATRing][kATKeys], sv[kATRing][kATKeys];
+    float sk[kATRing][kATKeys], sv[kATRing][kATKeys], above[kATRing][kATKeys];  // above: log_above(sv)
     int kind[kATRing];
     // where a key's head lies in the pool of codes and in that of plain entries, in 16 bytes (0: a page
     // outside, or none yet); the keys of a loading thread side by side
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
       if (lane == 0) mbar_arrive(&r.q_full);
       const int last_seen = w.s.len + fdiv(row0 + row, a.div_g), first_seen = w.s.len + fdiv(row0, a.div_g);
       float m = kLow, high = kLow, l = 0.f, over = 1.f;  // high: the largest x + log_above(sv)
-      float room = 142.f;  // 15 + 127 + unit
+      float room = 142.f;  // 15 + unit + 127: how far a score with its scale's exponent bits may be above the maximum, for weights below 2^15
       int unit = 0;        // over = 2^-unit
       const int n_codes = w.s.bad ? 0 : (keys.codes + kATKeys - 1) / kATKeys;
       // units of codes that every row sees whole and whose keys share their scales by 16
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
         tc_after();
         if (!w.s.bad) {
           const int slot = i & (kATRing - 1);
-          const float *sk = r.sk[slot], *sv = r.sv[slot];
+          const float *sk = r.sk[slot], *sv = r.sv[slot], *above = r.above[slot];
           const uint32_t t_s = tmem + lanes;
           // the maximum and the unit move, and with them the sums: to scores up to `most` and weighted scales up to `weighted` (log2)
           auto move = [&](float most, float weighted) {
@@ -348,8 +348,6 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
               }
             }
           };
-          // how far above the maximum a score of a unit may be, its exponent bits being up to `top`, for weights below 2^15
-          auto limit = [&](float top) { return fminf(kSlack, room - top); };
           bool grouped = u < u_groups;
           if (grouped) {
             const float top = r.top[slot];
@@ -386,7 +384,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
                 if (g < 3) tc_loaded16(x[(g + 1) & 1]);
               }
               // (rows past the last hold anything; a score that is infinite outgrows every maximum)
-              const float lim = limit(top);
+              const float lim = fminf(kSlack, room - top);  // where the largest score and the largest scale are one key's
               if (!__any_sync(0xffffffffu, mine && (fmaxf(most0, most1) > lim || lim < -96.f))) break;
               if (again) {
                 grouped = !__any_sync(0xffffffffu, mine && lim < -96.f);  // sv over may not be finite
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
                 for (int k = 1; k < 16; ++k) y = fmaxf(y, __uint_as_float(z[k]));
                 y *= sk[16 * g] * qs;  // (a maximum takes no NaN)
                 most = fmaxf(most, y);
-                weighted = fmaxf(weighted, y + log_above(sv[16 * g]));
+                weighted = fmaxf(weighted, y + above[16 * g]);
               }
               move(most, weighted);
             }
@@ -436,9 +434,9 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
               return vis;
             };
             const uint32_t vis0 = seen(unit), vis1 = seen(unit + 32);
-            float most = -INFINITY;
+            // the largest score, and the largest with its key's scale of V
+            float most = -INFINITY, weighted = -INFINITY;
             const f2_t by = f2(qs, qs);
-            float top = masked ? 0.f : r.top[slot];
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1)) & 0xffffu;
@@ -446,37 +444,18 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
               uint32_t x[16];
               tc_load16(t_s + 16 * c, x);
               tc_loaded16(x);
-              unsigned bits = 0;  // of the largest scale; one that is not finite makes its weights NaN whatever the reference
 #pragma unroll
               for (int k = 0; k < 16; k += 4) {
-                const float4 y = *(const float4*)(sk + 16 * c + k);
+                const float4 y = *(const float4*)(sk + 16 * c + k), v = *(const float4*)(above + 16 * c + k);
                 const f2_t y0 = f2mul(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2mul(f2(y.x, y.y), by));
                 const f2_t y1 = f2mul(f2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), f2mul(f2(y.z, y.w), by));
-                const float z0 = f2lo(y0), z1 = f2hi(y0), z2 = f2lo(y1), z3 = f2hi(y1);
-                if (masked) {
-                  const uint4 v = *(const uint4*)(sv + 16 * c + k);
-                  most = fmaxf(fmaxf(most, vis >> k & 1u ? z0 : -INFINITY), vis >> (k + 1) & 1u ? z1 : -INFINITY);
-                  most = fmaxf(fmaxf(most, vis >> (k + 2) & 1u ? z2 : -INFINITY), vis >> (k + 3) & 1u ? z3 : -INFINITY);
-                  bits = max(bits, max(max(vis >> k & 1u ? v.x : 0u, vis >> (k + 1) & 1u ? v.y : 0u),
-                                       max(vis >> (k + 2) & 1u ? v.z : 0u, vis >> (k + 3) & 1u ? v.w : 0u)));
-                } else {
-                  most = fmaxf(most, fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)));
-                }
+                const float z0 = vis >> k & 1u ? f2lo(y0) : -INFINITY, z1 = vis >> (k + 1) & 1u ? f2hi(y0) : -INFINITY,
+                            z2 = vis >> (k + 2) & 1u ? f2lo(y1) : -INFINITY, z3 = vis >> (k + 3) & 1u ? f2hi(y1) : -INFINITY;
+                most = fmaxf(most, fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)));
+                weighted = fmaxf(weighted, fmaxf(fmaxf(z0 + v.x, z1 + v.y), fmaxf(z2 + v.z, z3 + v.w)));
               }
-              if (masked) top = fmaxf(top, bits < 0x7f800000u ? (float)((bits >> 23) + 1u) : 0.f);
             }
-            if (__any_sync(0xffffffffu, mine && most - m > limit(top))) {
-              float weighted = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t vis = (c < 2 ? vis0 : vis1) >> (16 * (c & 1)) & 0xffffu;
-                uint32_t x[16];
-                tc_load16(t_s + 16 * c, x);
-                tc_loaded16(x);
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  if (vis >> k & 1u) weighted = fmaxf(weighted, __uint_as_float(x[k]) * (sk[16 * c + k] * qs) + log_above(sv[16 * c + k]));
-              }
+            if (__any_sync(0xffffffffu, mine && (most - m > kSlack || weighted - m > room - 127.f))) {
               move(most, weighted);
             }
             f2_t sum = 0;
@@ -672,7 +651,10 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
           if (kPer == 16) top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
           const bool finite = top < 0x7f800000u;
           const float down = in && finite ? scale_down(top) : __uint_as_float(0x7fffffffu);
-          if (part == 0) scales[key] = down;
+          if (part == 0) {
+            scales[key] = down;
+            if (values) r.above[slot][key] = log_above(down);
+          }
           if (values) {
             const unsigned above = __reduce_max_sync(0xffffffffu, in && finite ? (__float_as_uint(down) >> 23) + 1u : 0u);
             if (lane == 0) atomicMax((unsigned*)&r.top[slot], __float_as_uint((float)above));
@@ -804,7 +786,7 @@ __global__ void __launch_bounds__(kATThreads, DP == 256 ? 1 : 2) attend_tiles_ke
               r.at[!codes][slot][L::place(k)] = some < 0 ? 0u : (unsigned)((((long long)(at[q] < 0 ? some : at[q]) * a.Hkv + w.h) * a.D >> 4) << (codes ? 0 : 1));
               const unsigned out = __ballot_sync(0xffffffffu, at[q] < 0);
               if (lane == 0) r.outside[slot][q] = out;
-              if (codes) r.sk[slot][k] = sk[q], r.sv[slot][k] = sv[q];
+              if (codes) r.sk[slot][k] = sk[q], r.sv[slot][k] = sv[q], r.above[slot][k] = log_above(sv[q]);
             }
             if (lane == 0) r.kind[slot] = !codes ? kATPlain : some < 0 ? kATNone : kATCodes;
           }
