@@ -513,7 +513,8 @@ int spec_process_logits_bf16(const uint16_t *logits, const int32_t *draft_tokens
  * token 0 and the node's level for the others (a child of the root: 1).
  *
  *   k, v          token t = b T + i at element t * kv_stride, its Hkv x D
- *                 values contiguous (a slice of a joint projection fits).
+ *                 values contiguous (a slice of a joint projection fits); a
+ *                 stride is at most 2^44, and not read for a single token.
  *   q, out_q      the same with Hq heads and q_stride; out_q is [B, T, Hq, D],
  *                 or q itself when q_stride == Hq * D (or there is one token);
  *                 it lies apart from the rest of q, every other input and
@@ -677,8 +678,8 @@ int spec_kv_dequantize_bf16(const void *key_codes, const void *value_codes, int 
  * code * scale and the others from the plain cache.
  *
  *   q, out        token t = b T + i of q at element t * q_stride, its Hq x D values
- *                 contiguous, turned to its position (spec_kv_append_*); out is [B,
- *                 T, Hq, D] on a 16-byte boundary.  Query head h reads head
+ *                 contiguous, turned to its position (spec_kv_append_*; its limit on
+ *                 the stride, too); out is [B, T, Hq, D] on a 16-byte boundary.  Query head h reads head
  *                 h / (Hq / Hkv) of the cache.
  *   lengths       [B] int32: entries of the sequence before the step, as given to
  *                 spec_kv_append_*, which has put the step's own behind them.

@@ -571,6 +571,11 @@ bool rows_overlap(const void* p, uint64_t n, uint64_t step, uint64_t rows, const
   return k < rows && a + (unsigned __int128)step * k < (unsigned __int128)b + m;
 }
 
+// A step's tokens lie `stride` elements apart: a single one nowhere apart, whatever is passed, and the byte
+// offsets of many stay below 2^63.
+constexpr long long kMostStride = 1LL << 44;
+bool stride_ok(int64_t stride, long long row, int B, int T) { return stride >= row && (stride <= kMostStride || (long long)B * T <= 1); }
+
 int process_impl(bool bf16, const void* logits, const int32_t* drafts, const int32_t* parents,
                  const int32_t* state, const float* rep, const float* freq, const float* pres,
                  int n_bias, const int32_t* bias_tokens, const float* bias_values,
@@ -642,10 +647,11 @@ int kv_append_impl(bool bf16, const void* k, const void* v, int64_t kv_stride, c
   if (B < 0 || T < 0 || Hq < 0 || Hkv < 1 || D < 1 || D > sv::kv_max_rot() || rot < 0 || rot > D ||
       rot % 2 || pages < 1 || page_size < 1 || max_pages < 1 ||
       (parents && T > sv::kMaxTreeNodes + 1) || (long long)Hkv * D > (1 << 24) ||
-      (long long)Hq * D > (1 << 24) || kv_stride < (long long)Hkv * D ||
-      (Hq > 0 && q_stride < (long long)Hq * D) || (long long)B * T > INT_MAX)
+      (long long)Hq * D > (1 << 24) || !stride_ok(kv_stride, (long long)Hkv * D, B, T) ||
+      (Hq > 0 && !stride_ok(q_stride, (long long)Hq * D, B, T)) || (long long)B * T > INT_MAX)
     return SPEC_ERR_SHAPE;
   if (B == 0 || T == 0) return SPEC_OK;
+  if ((long long)B * T == 1) kv_stride = (long long)Hkv * D, q_stride = (long long)Hq * D;
   if (!k || !v || !lengths || !page_table || !k_cache || !v_cache || (rot > 0 && !turns) ||
       (Hq > 0 && (!q || !out_q)))
     return SPEC_ERR_NULL;
@@ -748,7 +754,7 @@ int kv8_impl(bool bf16, bool quantize, const Kv8Sizes& z, const void* k_cache, c
   if (!kv8_sizes_ok(z)) return SPEC_ERR_SHAPE;
   const uint64_t plain = (uint64_t)z.pages * z.page_size * entry, codes = (uint64_t)z.code_pages * z.block * entry,
                  scales = (uint64_t)z.code_pages * z.Hkv;
-  constexpr uint64_t kFar = 1ull << 44;  // offsets of 32767 layers stay below 2^63 bytes
+  constexpr uint64_t kFar = kMostStride;  // offsets of 32767 layers stay below 2^63 bytes
   if (z.layers > 1 &&
       (layer_stride < 0 || code_stride < 0 || scale_stride < 0 || (uint64_t)layer_stride < plain || (uint64_t)layer_stride > kFar ||
        (uint64_t)code_stride < codes || (uint64_t)code_stride > kFar || (uint64_t)scale_stride < scales ||
@@ -830,9 +836,10 @@ int attention_impl(bool bf16, const void* q, int64_t q_stride, const void* k_cac
                    int D, float scale, void* out, cudaStream_t stream) {
   const Kv8Sizes z = {1, pages, page_size, max_pages, code_pages, block, max_code_pages, B, Hkv, D, format};
   if (!kv8_sizes_ok(z) || T < 0 || Hq < 1 || Hq % Hkv || (long long)Hq * D > (1 << 24) || (long long)B * T > INT_MAX ||
-      (long long)T * Hq > (1 << 30) || q_stride < (long long)Hq * D || (parents && T > sv::kMaxTreeNodes + 1) || !isfinite(scale * kLog2e))
+      (long long)T * Hq > (1 << 30) || !stride_ok(q_stride, (long long)Hq * D, B, T) || (parents && T > sv::kMaxTreeNodes + 1) || !isfinite(scale * kLog2e))
     return SPEC_ERR_SHAPE;
   if (B == 0 || T == 0) return SPEC_OK;
+  if ((long long)B * T == 1) q_stride = (long long)Hq * D;
   if (!q || !k_cache || !v_cache || !page_table || !lengths || !k_codes || !v_codes || !k_scales || !v_scales || !code_table ||
       !stored || !out)
     return SPEC_ERR_NULL;

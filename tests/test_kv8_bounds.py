@@ -28,3 +28,20 @@ def test_batches(lib, t, B):
 def test_scales_past_the_exponent_s_range(lib, t, scale):
     """The scale is taken times log2(e), which has to be finite in fp32 too."""
     assert attention(lib, t, scale=scale) == _lib.SPEC_ERR_SHAPE
+
+
+@pytest.mark.parametrize("t,e", [("f32", 4), ("bf16", 2)])
+def test_token_strides_past_the_address_range(lib, t, e):
+    """A stride whose bytes wrap around 2^64 to 0 ended the process in the look for shared memory.  Between tokens
+    such strides are refused; a single token has none, and its queries may lie anywhere."""
+    for stride in (2 ** 44 + 1, 2 ** 61, 2 ** 62, 2 ** 63 - 1):
+        assert attention(lib, t, qs=stride) == _lib.SPEC_ERR_SHAPE
+        assert attention(lib, t, qs=stride, B=1, T=1, out=ROWS) == _lib.SPEC_ERR_OVERLAP
+        append = getattr(lib, "spec_kv_append_" + t)
+        far, n = 1 << 45, 1 << 40
+
+        def call(ks, qs, B, out=far + 6 * n):
+            return append(far, far + n, ks, far + 2 * n, qs, out, None, None, ROWS, TAB, B, 1, 4, 2, 32, 0, 0, None, far + 3 * n, far + 4 * n, 4, 16, 4, None)
+
+        assert call(stride, 128, 2) == _lib.SPEC_ERR_SHAPE and call(64, stride, 2) == _lib.SPEC_ERR_SHAPE
+        assert call(stride, stride, 1, out=ROWS) == _lib.SPEC_ERR_OVERLAP
