@@ -66,9 +66,9 @@ extern "C" {
                                      SPEC_STATIC_SCRATCH_BYTES of scratch */
 #define SPEC_ERR_HINT (-6)        /* spec_verify_khint_*: k_min < 0, k_max > 255, k_min > k_max,
                                      a NaN threshold or h_lo > h_hi */
-#define SPEC_ERR_OVERLAP (-7)     /* spec_count_tokens, spec_process_logits_*, spec_kv_append_*,
-                                     spec_kv_commit: memory that the call writes overlaps memory that it
-                                     reads or another output, where the entry point does not allow it */
+#define SPEC_ERR_OVERLAP (-7)     /* spec_count_tokens, spec_process_logits_*, spec_kv_*: memory that
+                                     the call writes overlaps memory that it reads or another output,
+                                     where the entry point does not allow it */
 
 /* Size of the fixed per-device scratch buffer of spec_verify_bf16_static_scratch. */
 #define SPEC_STATIC_SCRATCH_BYTES ((size_t)8 << 20)

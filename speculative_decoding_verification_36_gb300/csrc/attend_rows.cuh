@@ -9,10 +9,10 @@
 // read once for each tile of 8.
 //
 // Measured (GB300; the codes' bytes at 6.77 TB/s beside it): single tokens, 64 sequences of
-// 4096 to 8192 entries, 32 heads to 8 of keys of 128, int8: 169 to 180 us (121); chains of 5 in
-// fp32, 8 sequences of up to 4000, 8 heads of 80: 31 us (4.4).  The first is bound by what a
-// warp does for 16 keys, turning codes to fp16 before all (the integer pipe is busy in 53 % of
-// the clocks, DRAM at 61 % of its peak, 168 registers leave 12 warps an SM); the second by the chain
+// 4096 to 8192 entries, 32 heads to 8 of keys of 128, int8: 174 to 182 us (121); chains of 5 in
+// fp32, 8 sequences of up to 4000, 8 heads of 80: 31 us (4.4).  In the first nothing is at its limit
+// (issue slots 54 %, the integer pipe, which turns codes to fp16, 48 %, DRAM 59 % of its peak): 168 registers
+// leave 12 warps an SM, and a warp's steps for 16 keys follow on one another.  The second is the chain
 // of a CTA's few units, the prologue (lengths, shares, tables: about three trips to memory)
 // and the joining launch.  From steps before: fragments
 // from global memory to registers 212 us, with the ring 197, with the keys as the products'
@@ -23,7 +23,8 @@
 // times a power of two for each row (bf16 queries exactly, fp32 ones as a sum of two
 // fp16 parts), weights as fp16 (fp32: two parts) times a power of two that follows the
 // weighted scales of the values.  Plain entries become fp16 (two parts) times a power of two for each
-// key.  The softmax runs in the log2 domain with one pass over the keys.
+// key.  In bf16 calls one part is enough: weights off by 2^-12 in the mean leave a result's error
+// against 64 bits at that of its rounding to bf16 (0.0017 of it, as with weights in fp32).  The softmax runs in the log2 domain with one pass over the keys.
 #pragma once
 #include "attend_common.cuh"
 

@@ -3,7 +3,8 @@
 //
 // A CTA takes tiles of 128 rows and units of 64 keys:
 //   S = Q K^T      128 x 64 x D, Q from tensor memory, K from shared memory, both fp16
-//   P = weights    fp16, over S's columns in tensor memory
+//   P = weights    fp16, over S's columns in tensor memory (as attend_rows.cuh says, the rounding does
+//                  not show in a bf16 result)
 //   O += P V       128 x D x 64, P from tensor memory, V from shared memory
 // Four warps bring keys and four values: codes go from global memory to registers a
 // unit ahead (two ahead: chains 306 us instead of 266, prompts 1096 instead of 845; two warps for
@@ -17,12 +18,13 @@
 //
 // Measured (GB300, 32 heads to 8 of keys of 128; the floor by bytes, or by products at 1.95
 // PFLOP/s, beside it): chains of 9, 64 sequences of 4096 to 8192 entries, int8: 266 us (123);
-// trees of 31 tokens, 32 such sequences, e4m3: 170 us (65); 5 tokens, two sequences of 131072 to
-// 262144, e4m3: 163 us (81); prompts of up to 2048 tokens behind 16384, int8: 846 us (298); three
+// trees of 31 tokens, 32 such sequences, e4m3: 171 us (65); 5 tokens, two sequences of 131072 to
+// 262144, e4m3: 159 us (81); prompts of up to 2048 tokens behind 16384, int8: 846 us (298); three
 // tokens with 8 heads to one of 256, 16 sequences of 5000 to 10000: 46 us (9.4).
-// A unit takes a CTA 2000 to 3300 clocks.  800 to 1000 are its products.  Its weights took 1200 to
-// 1600 when last counted (with two units ahead), 450 with nothing else on the SM: the two CTAs' 32
-// warps issued in half of all clocks, so a warp waits for its turn at each step, and S, weights and
+// A unit takes a CTA 2000 to 3300 clocks.  800 to 1000 are its products (chains: the tensor pipe is busy
+// in 35 % of the clocks).  Its weights took 1200 to 1600 when last counted (with two units ahead, and a
+// reference by scales alone), 450 with nothing else on the SM: the two CTAs' 32
+// warps issue in half of all clocks, so a warp waits for its turn at each step, and S, weights and
 // P V follow on one another.  A segment cost a CTA 15 000 to 20 000 clocks at its ends, most of
 // them for its queries.
 // Steps before: units of 128 keys with one CTA an SM 440 us (chains), queries in shared
