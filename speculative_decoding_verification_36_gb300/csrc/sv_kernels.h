@@ -386,9 +386,9 @@ cudaError_t launch_attend_rows_f32_e4m3(const KvAttendArgs& a, int sms, size_t* 
 // Tiles of 128 rows on the tensor cores: bf16, trees of up to 128 tokens, and more
 // rows a head of keys than the other kernel's tile has (which reads the cache once
 // for each tile: 64 sequences of 4096 to 8192 entries, 4 query heads to one of 8 heads of keys of 128: with
-// two tokens 179 to 188 us there, 232 here; with three 315 there in two tiles, 234 here; 2 heads of
-// 256: 121 and 139, 193 and 141; 32 sequences of up to 1024 and 8 heads: 33 and 44, 49 and 45.  One
-// sequence of up to 2048 goes the other way, by less: three tokens 21 us there, 24 here).
+// two tokens 189 us there, 229 here; with three 337 there in two tiles, 230 here; 2 heads of
+// 256: 121 and 139, 195 and 142; 32 sequences of up to 1024 and 8 heads: 33 and 45, 50 and 45.  One
+// sequence of up to 2048 goes the other way, by less: three tokens 21 us there, 25 here).
 constexpr int kAttendFewRows = 8;
 constexpr int kAttendTilesMaxTree = 128;
 constexpr unsigned long long kAttendTilesMaxPool = 1ull << 36;  // bytes: places are 32 bits of 16
